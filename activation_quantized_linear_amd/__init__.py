@@ -38,6 +38,10 @@ AQL_OP_Q8TA_Q8CSW = 1
 AQL_OP_DQ8CA = 2
 AQL_OP_GPTQ_INT8 = 3
 AQL_OP_W8A16 = 4
+AQL_OP_W8A16_DGRAD = 5
+AQL_LORA_MAX_RANK = 128
+AQL_LORA_MAX_ADAPTERS = 1024
+AQL_CKPT_GROUP = 128
 AQL_MAX_K_INT8 = 65536
 AQL_NOALLOC_SCRATCH_BYTES = 8 << 20
 
@@ -82,6 +86,16 @@ _SIGS = {
     "aql_w8a16_group_table_bytes": ([_int], _sz),
     "aql_w8a16_group_plan": ([_p, _int, _p, _sz], _int),
     "aql_linear_w8a16_grouped": ([_p, _p, _p], _int),
+    "aql_lora_plan_bytes": ([_i64, _i64], _sz),
+    "aql_lora_plan": ([_p, _i64, _i64, _p, _sz, _p], _int),
+    "aql_linear_w8a16_lora": ([_p, _i64, _i64, _p, _p, _p, _i64, _p, _p, _p, _i64, _i64, _p, _p,
+                               _p, _p, _sz, _p], _int),
+    "aql_linear_w8a16_dgrad": ([_p, _i64, _i64, _p, _p, _i64, _p, _p, _sz, _p], _int),
+    "aql_lora_backward_bytes": ([_i64, _i64, _i64, _i64], _sz),
+    "aql_linear_w8a16_lora_backward": ([_p, _i64, _i64, _p, _p, _i64, _p, _p, _p, _i64, _i64, _p,
+                                        _p, _p, _p, _int, _p, _p, _p, _p, _sz, _p], _int),
+    "aql_act_checkpoint": ([_p, _int, _i64, _i64, _p, _p, _p], _int),
+    "aql_act_restore": ([_p, _p, _i64, _i64, _p, _int, _p], _int),
 }
 for _name, (_args, _res) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -522,3 +536,192 @@ def aql_linear_w8a16_grouped(host_table, dev_table):
     _check("aql_linear_w8a16_grouped",
            _lib.aql_linear_w8a16_grouped(_ptr(host_table), _ptr(dev_table),
                                          _stream(dev_table.device)))
+
+
+# -------------------------------------------------------- low-rank adapters
+
+
+def _call(name, dev, *args):
+    """The C entry on the current stream of dev, with dev the current device."""
+    fn = getattr(_lib, name)
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(dev))
+    _check(name, rc)
+
+
+class LoraPlan:
+    """A batch's rows sorted by adapter (aql_lora_plan). Holds the sizes it was
+    made for and its device buffer; every layer and both directions of a batch
+    share one."""
+
+    __slots__ = ("M", "L", "buffer")
+
+    def __init__(self, M, L, buffer):
+        self.M, self.L, self.buffer = M, L, buffer
+
+
+def aql_lora_plan_bytes(M, L):
+    return _lib.aql_lora_plan_bytes(M, L)
+
+
+def aql_lora_plan(idx, L, plan=None):
+    """idx int32 [M]: each row's adapter in [0, L), any other value: none -> LoraPlan.
+    plan: a LoraPlan of the same M and L on idx's device to write again (its
+    buffer keeps its address, so a captured graph sees the new batch)."""
+    _need(idx, "idx", torch.int32, 1)
+    M, L = idx.shape[0], int(L)
+    nbytes = aql_lora_plan_bytes(M, L)
+    if plan is None:
+        plan = LoraPlan(M, L, torch.empty(max(nbytes, 16), dtype=torch.uint8, device=idx.device))
+    else:
+        _lora_plan(plan, M, L, idx.device)
+    _call("aql_lora_plan", idx.device, _ptr(idx), M, L, _ptr(plan.buffer), plan.buffer.numel())
+    return plan
+
+
+def _lora_plan(plan, M, L, dev):
+    if not isinstance(plan, LoraPlan):
+        raise TypeError("plan must be a LoraPlan (aql_lora_plan)")
+    if (plan.M, plan.L) != (M, L):
+        raise ValueError(f"plan is for M={plan.M}, L={plan.L}; the call has M={M}, L={L}")
+    _need(plan.buffer, "plan.buffer", torch.uint8, 1, dev)
+    if plan.buffer.numel() < aql_lora_plan_bytes(M, L):
+        raise ValueError("plan.buffer is too small")
+
+
+def _lora_args(A, B, alpha, N, K, dev):
+    _need(A, "A", torch.bfloat16, 3, dev)
+    L, R = A.shape[0], A.shape[1]
+    _shape(A, "A", (L, R, K))
+    _need(B, "B", torch.bfloat16, 3, dev)
+    _shape(B, "B", (L, N, R))
+    _need(alpha, "alpha", torch.float32, 1, dev)
+    _shape(alpha, "alpha", (L,))
+    return L, R
+
+
+def aql_linear_w8a16_lora(x, q, scale, A, B, alpha, plan, bias=None, y=None, h=None,
+                          workspace=None):
+    """W8A16 linear with every row's low-rank adapter. x bfloat16 [M, K], q int8 [N, K],
+    scale float32 [N], A bfloat16 [L, R, K], B bfloat16 [L, N, R], alpha float32 [L],
+    plan of aql_lora_plan, bias bfloat16 [N] -> (y bfloat16 [M, N], h float32 [M, R]),
+    h = alpha A x, which the backward pass takes. workspace: as aql_linear_w8a16."""
+    _need(x, "x", torch.bfloat16, 2)
+    dev = x.device
+    M, K = x.shape
+    _need(q, "q", torch.int8, 2, dev)
+    N = q.shape[0]
+    _shape(q, "q", (N, K))
+    _need(scale, "scale", torch.float32, 1, dev)
+    _shape(scale, "scale", (N,))
+    L, R = _lora_args(A, B, alpha, N, K, dev)
+    _lora_plan(plan, M, L, dev)
+    if bias is not None:
+        _need(bias, "bias", torch.bfloat16, 1, dev)
+        _shape(bias, "bias", (N,))
+    y = _out(y, "y", (M, N), torch.bfloat16, dev)
+    h = _out(h, "h", (M, R), torch.float32, dev)
+    nbytes = aql_workspace_bytes(AQL_OP_W8A16, M, N, K)
+    ws = _workspace(workspace, nbytes, dev) if workspace is not None or nbytes > 0 else None
+    _call("aql_linear_w8a16_lora", dev, _ptr(x), M, K, _ptr(q), _ptr(scale), _ptr(bias), N,
+          _ptr(A), _ptr(B), _ptr(alpha), L, R, _ptr(plan.buffer), _ptr(y), _ptr(h), _ptr(ws), 0
+          if ws is None else ws.numel())
+    return y, h
+
+
+def aql_linear_w8a16_dgrad(dy, q, scale, dx=None, workspace=None):
+    """Gradient of aql_linear_w8a16 to x: dy bfloat16 [M, N], q int8 [N, K], scale
+    float32 [N] -> dx bfloat16 [M, K] = (dy * scale) @ q."""
+    _need(dy, "dy", torch.bfloat16, 2)
+    dev = dy.device
+    M, N = dy.shape
+    _need(q, "q", torch.int8, 2, dev)
+    K = q.shape[1]
+    _shape(q, "q", (N, K))
+    _need(scale, "scale", torch.float32, 1, dev)
+    _shape(scale, "scale", (N,))
+    dx = _out(dx, "dx", (M, K), torch.bfloat16, dev)
+    nbytes = aql_workspace_bytes(AQL_OP_W8A16_DGRAD, M, N, K)
+    ws = _workspace(workspace, nbytes, dev) if workspace is not None or nbytes > 0 else None
+    _call("aql_linear_w8a16_dgrad", dev, _ptr(dy), M, N, _ptr(q), _ptr(scale), K, _ptr(dx),
+          _ptr(ws), 0 if ws is None else ws.numel())
+    return dx
+
+
+def aql_lora_backward_bytes(M, N, K, R):
+    return _lib.aql_lora_backward_bytes(M, N, K, R)
+
+
+def aql_linear_w8a16_lora_backward(dy, q, scale, A, B, alpha, plan, h, xq, xs, dx=None, dA=None,
+                                   dB=None, accumulate=False, need_dx=True, workspace=None):
+    """Backward pass of aql_linear_w8a16_lora. dy bfloat16 [M, N]; h float32 [M, R] of the
+    forward pass; xq int8 [M, K], xs float32 [M, ceil(K / 128)]: the checkpoint of x
+    (aql_act_checkpoint) -> (dx bfloat16 [M, K] or None, dA float32 [L, R, K],
+    dB float32 [L, N, R]). accumulate=True adds to the given dA and dB.
+    need_dx=False leaves dx out."""
+    _need(dy, "dy", torch.bfloat16, 2)
+    dev = dy.device
+    M, N = dy.shape
+    _need(q, "q", torch.int8, 2, dev)
+    K = q.shape[1]
+    _shape(q, "q", (N, K))
+    _need(scale, "scale", torch.float32, 1, dev)
+    _shape(scale, "scale", (N,))
+    L, R = _lora_args(A, B, alpha, N, K, dev)
+    _lora_plan(plan, M, L, dev)
+    _need(h, "h", torch.float32, 2, dev)
+    _shape(h, "h", (M, R))
+    _need(xq, "xq", torch.int8, 2, dev)
+    _shape(xq, "xq", (M, K))
+    _need(xs, "xs", torch.float32, 2, dev)
+    _shape(xs, "xs", (M, (K + AQL_CKPT_GROUP - 1) // AQL_CKPT_GROUP))
+    if accumulate and (dA is None or dB is None):
+        raise ValueError("accumulate needs the dA and dB to add to")
+    if dx is not None and not need_dx:
+        raise ValueError("dx is given but need_dx is False")
+    dx = _out(dx, "dx", (M, K), torch.bfloat16, dev) if need_dx else None
+    dA = _out(dA, "dA", (L, R, K), torch.float32, dev)
+    dB = _out(dB, "dB", (L, N, R), torch.float32, dev)
+    ws = _workspace(workspace, aql_lora_backward_bytes(M, N, K, R), dev)
+    _call("aql_linear_w8a16_lora_backward", dev, _ptr(dy), M, N, _ptr(q), _ptr(scale), K,
+          _ptr(A), _ptr(B), _ptr(alpha), L, R, _ptr(plan.buffer), _ptr(h), _ptr(xq), _ptr(xs),
+          int(bool(accumulate)), _ptr(dx), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel())
+    return dx, dA, dB
+
+
+# ------------------------------------------------ 8-bit activation checkpoints
+
+
+def _act_dtype(dtype, name):
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    return AQL_F32 if dtype == torch.float32 else AQL_BF16
+
+
+def aql_act_checkpoint(x, xq=None, xs=None):
+    """x float32 or bfloat16 [M, K] -> (xq int8 [M, K], xs float32 [M, ceil(K / 128)]):
+    8-bit codes with one scale per 128 values of a row."""
+    dt = _act_dtype(x.dtype, "x")
+    _need(x, "x", x.dtype, 2)
+    M, K = x.shape
+    dev = x.device
+    xq = _out(xq, "xq", (M, K), torch.int8, dev)
+    xs = _out(xs, "xs", (M, (K + AQL_CKPT_GROUP - 1) // AQL_CKPT_GROUP), torch.float32, dev)
+    _call("aql_act_checkpoint", dev, _ptr(x), dt, M, K, _ptr(xq), _ptr(xs))
+    return xq, xs
+
+
+def aql_act_restore(xq, xs, dtype=torch.bfloat16, x=None):
+    """xq int8 [M, K], xs float32 [M, ceil(K / 128)] -> x [M, K] of dtype: code * scale."""
+    dt = _act_dtype(dtype, "dtype")
+    _need(xq, "xq", torch.int8, 2)
+    M, K = xq.shape
+    dev = xq.device
+    _need(xs, "xs", torch.float32, 2, dev)
+    _shape(xs, "xs", (M, (K + AQL_CKPT_GROUP - 1) // AQL_CKPT_GROUP))
+    x = _out(x, "x", (M, K), dtype, dev)
+    _call("aql_act_restore", dev, _ptr(xq), _ptr(xs), M, K, _ptr(x), dt)
+    return x

@@ -15,12 +15,15 @@
 
 #include "aql.h"
 #include "calib.h"
+#include "ckpt.h"
 #include "dq8ca_q4.h"
 #include "gemm_i8.h"
 #include "gptq.h"
+#include "lora.h"
 #include "quant.h"
 #include "w8a16.h"
 #include "measure.h"
+#include "w8a16_dgrad.h"
 #include "w8a16_gemm.h"
 
 // Rows of x from which aql_linear_w8a16 uses the tiled GEMM.
@@ -133,6 +136,57 @@ int check_w8a16(const char *fn, const uint16_t *x, int64_t M, int64_t K, const i
   return AQL_OK;
 }
 
+// Rows a 16-row tile grid of the W8A16 kernels can index.
+constexpr int64_t kMaxRows = 0xffff * 16LL;
+
+// Validation of the adapters shared by the forward and backward entry points.
+int check_lora(const char *fn, const uint16_t *A, const uint16_t *B, const float *alpha, int64_t L,
+               int64_t R, const void *plan, const float *h) {
+  REQUIRE(R >= 8 && R <= AQL_LORA_MAX_RANK && R % 8 == 0 && L >= 1 && L <= AQL_LORA_MAX_ADAPTERS,
+          AQL_ERR_SHAPE, "%s: need R a multiple of 8 in [8, %d] and L in [1, %d] (R=%lld L=%lld)",
+          fn, AQL_LORA_MAX_RANK, AQL_LORA_MAX_ADAPTERS, (long long)R, (long long)L);
+  REQUIRE(aligned16(A) && aligned16(B) && aligned16(alpha) && aligned16(plan) && aligned16(h),
+          AQL_ERR_ALIGN, "%s: pointers must be 16-byte aligned", fn);
+  return AQL_OK;
+}
+
+int check_dgrad(const char *fn, const uint16_t *dy, int64_t M, int64_t N, const int8_t *q,
+                const float *scale, int64_t K, const uint16_t *dx) {
+  REQUIRE(M >= 0 && M <= kMaxRows, AQL_ERR_SHAPE, "%s: need 0 <= M <= %lld (M=%lld)", fn,
+          (long long)kMaxRows, (long long)M);
+  REQUIRE(K >= 16 && K % 16 == 0 && K <= kMaxKW8A16 && N >= 0 && N % 8 == 0 && N <= (1LL << 22),
+          AQL_ERR_SHAPE,
+          "%s: need K a multiple of 16 in [16, %lld] and N a multiple of 8 in [0, %lld] (N=%lld "
+          "K=%lld)",
+          fn, (long long)kMaxKW8A16, 1LL << 22, (long long)N, (long long)K);
+  REQUIRE(aligned16(dy) && aligned16(q) && aligned16(scale) && aligned16(dx), AQL_ERR_ALIGN,
+          "%s: pointers must be 16-byte aligned", fn);
+  return AQL_OK;
+}
+
+int check_ckpt(const char *fn, const void *x, int64_t M, int64_t K, const int8_t *xq,
+               const float *xs) {
+  REQUIRE(M >= 0 && K >= 1 && K % 4 == 0 && K <= (1LL << 40), AQL_ERR_SHAPE,
+          "%s: need M >= 0, K >= 1 and K %% 4 == 0 (M=%lld K=%lld)", fn, (long long)M,
+          (long long)K);
+  const int64_t G = (K + AQL_CKPT_GROUP - 1) / AQL_CKPT_GROUP;
+  REQUIRE(M <= (1LL << 36) / G, AQL_ERR_SHAPE, "%s: too many groups (M=%lld K=%lld)", fn,
+          (long long)M, (long long)K);
+  REQUIRE(aligned16(x) && aligned16(xq) && aligned16(xs), AQL_ERR_ALIGN,
+          "%s: pointers must be 16-byte aligned", fn);
+  return AQL_OK;
+}
+
+bool plan_sizes_ok(int64_t M, int64_t L) {
+  return M >= 0 && M <= kMaxRows && L >= 1 && L <= AQL_LORA_MAX_ADAPTERS;
+}
+static_assert(AQL_LORA_MAX_ADAPTERS == aql::kLoraMaxAdapters &&
+                  AQL_LORA_MAX_RANK == aql::kLoraMaxRank && AQL_CKPT_GROUP == aql::kCkptGroup,
+              "adapter bounds");
+
+// u [M, R], then the partial sums of dx.
+size_t lora_bwd_u_bytes(int64_t M, int64_t R) { return align256((size_t)M * (size_t)R * 4); }
+
 // Validation shared by both static W8A8 entry points (all before any HIP call).
 int check_q8ta(const char *fn, const float *x, int64_t M, int64_t K, float s1, int32_t z1,
                int two_pass, float s2, int32_t z2, const int8_t *q, const int32_t *wsum,
@@ -235,6 +289,10 @@ size_t aql_workspace_bytes(int op, int64_t M, int64_t N, int64_t K) {
     if (M < kW8A16GemmMinM) return aql::w8a16_skinny_part_bytes(M, N, K);
     if (K > (1LL << 22)) return 0;
     return aql::w8a16_gemm_part_bytes(M, N, K);
+  }
+  if (op == AQL_OP_W8A16_DGRAD) {
+    if (M == 0 || K == 0 || K > kMaxKW8A16) return 0;
+    return aql::w8a16_dgrad_part_bytes(M, N, K);
   }
   return 0;
 }
@@ -560,6 +618,158 @@ int aql_linear_dq8ca(const float *x, int64_t M, int64_t K, int wfmt, const void 
   a.xs = xs;
   a.xz = xz;
   return launched(aql::launch_gemm_i8(a, aql::EPI_DQ8, false, st), fn);
+}
+
+size_t aql_lora_plan_bytes(int64_t M, int64_t L) {
+  if (!plan_sizes_ok(M, L)) return 0;
+  return (size_t)aql::lora_plan_layout(M, L).total * 4;
+}
+
+int aql_lora_plan(const int32_t *idx, int64_t M, int64_t L, void *plan, size_t plan_bytes,
+                  void *stream) {
+  const char *fn = "aql_lora_plan";
+  REQUIRE(plan_sizes_ok(M, L), AQL_ERR_SHAPE,
+          "%s: need 0 <= M <= %lld and L in [1, %d] (M=%lld L=%lld)", fn, (long long)kMaxRows,
+          AQL_LORA_MAX_ADAPTERS, (long long)M, (long long)L);
+  REQUIRE(aligned16(idx) && aligned16(plan), AQL_ERR_ALIGN,
+          "%s: pointers must be 16-byte aligned", fn);
+  REQUIRE(plan && (idx || M == 0), AQL_ERR_NULL, "%s: idx and plan must not be NULL", fn);
+  REQUIRE(plan_bytes >= aql_lora_plan_bytes(M, L), AQL_ERR_WORKSPACE, "%s: plan needs %zu bytes",
+          fn, aql_lora_plan_bytes(M, L));
+  if (int e = check_device(fn)) return e;
+  return launched(aql::launch_lora_plan(idx, M, L, static_cast<int32_t *>(plan),
+                                        (hipStream_t)stream),
+                  fn);
+}
+
+int aql_linear_w8a16_lora(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
+                          const float *scale, const uint16_t *bias, int64_t N, const uint16_t *A,
+                          const uint16_t *B, const float *alpha, int64_t L, int64_t R,
+                          const void *plan, uint16_t *y, float *h, void *ws, size_t ws_bytes,
+                          void *stream) {
+  const char *fn = "aql_linear_w8a16_lora";
+  if (int e = check_w8a16(fn, x, M, K, q, scale, bias, N, y)) return e;
+  if (int e = check_lora(fn, A, B, alpha, L, R, plan, h)) return e;
+  REQUIRE(aligned16(ws), AQL_ERR_ALIGN, "%s: ws must be 16-byte aligned", fn);
+  if (M == 0 || N == 0) return ok();
+  REQUIRE(A && B && alpha && plan && h, AQL_ERR_NULL,
+          "%s: A, B, alpha, plan and h must not be NULL", fn);
+  if (int e = check_device(fn)) return e;
+  hipStream_t st = (hipStream_t)stream;
+  const int32_t *p = static_cast<const int32_t *>(plan);
+  hipError_t e = aql::launch_lora_shrink(x, M, K, A, alpha, L, R, p, h, st);
+  if (e != hipSuccess) return launched(e, fn);
+  const aql::LoraTerm lt{h, B, p + aql::lora_plan_layout(M, L).idx, (int32_t)R, N};
+  float *part = static_cast<float *>(ws);
+  const size_t pb = ws ? ws_bytes : 0;
+  // the same M-dispatch as aql_linear_w8a16
+  if (M >= kW8A16GemmMinM && K <= (1LL << 22))
+    return launched(aql::launch_w8a16_gemm(x, M, K, q, scale, bias, N, y, part, pb, st, lt), fn);
+  return launched(aql::launch_w8a16(x, M, K, q, scale, bias, N, y, part, pb, st, lt), fn);
+}
+
+int aql_linear_w8a16_dgrad(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q,
+                           const float *scale, int64_t K, uint16_t *dx, void *ws, size_t ws_bytes,
+                           void *stream) {
+  const char *fn = "aql_linear_w8a16_dgrad";
+  if (int e = check_dgrad(fn, dy, M, N, q, scale, K, dx)) return e;
+  REQUIRE(aligned16(ws), AQL_ERR_ALIGN, "%s: ws must be 16-byte aligned", fn);
+  if (M == 0) return ok();
+  REQUIRE(dx && (N == 0 || (dy && q && scale)), AQL_ERR_NULL,
+          "%s: dy, q, scale and dx must not be NULL", fn);
+  if (int e = check_device(fn)) return e;
+  return launched(aql::launch_w8a16_dgrad(dy, M, N, q, scale, K, dx, static_cast<float *>(ws),
+                                          ws ? ws_bytes : 0, (hipStream_t)stream),
+                  fn);
+}
+
+size_t aql_lora_backward_bytes(int64_t M, int64_t N, int64_t K, int64_t R) {
+  if (M <= 0 || M > kMaxRows || N < 0 || K < 16 || K > kMaxKW8A16 || R < 8 ||
+      R > AQL_LORA_MAX_RANK)
+    return 0;
+  return lora_bwd_u_bytes(M, R) + aql::w8a16_dgrad_part_bytes(M, N, K);
+}
+
+int aql_linear_w8a16_lora_backward(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q,
+                                   const float *scale, int64_t K, const uint16_t *A,
+                                   const uint16_t *B, const float *alpha, int64_t L, int64_t R,
+                                   const void *plan, const float *h, const int8_t *xq,
+                                   const float *xs, int accumulate, uint16_t *dx, float *dA,
+                                   float *dB, void *ws, size_t ws_bytes, void *stream) {
+  const char *fn = "aql_linear_w8a16_lora_backward";
+  if (int e = check_dgrad(fn, dy, M, N, q, scale, K, dx)) return e;
+  if (int e = check_lora(fn, A, B, alpha, L, R, plan, h)) return e;
+  REQUIRE(aligned16(xq) && aligned16(xs) && aligned16(dA) && aligned16(dB) && aligned16(ws),
+          AQL_ERR_ALIGN, "%s: pointers must be 16-byte aligned", fn);
+  REQUIRE(plan, AQL_ERR_NULL, "%s: plan must not be NULL", fn);
+  REQUIRE(M == 0 || (A && alpha && h && (!dA || (xq && xs))), AQL_ERR_NULL,
+          "%s: A, alpha and h (xq and xs with dA) must not be NULL", fn);
+  REQUIRE(M == 0 || N == 0 || (dy && q && scale && B), AQL_ERR_NULL,
+          "%s: dy, q, scale and B must not be NULL", fn);
+  const size_t need = aql_lora_backward_bytes(M, N, K, R);
+  REQUIRE(M == 0 || (ws && ws_bytes >= need), AQL_ERR_WORKSPACE,
+          "%s: workspace needs %zu bytes (got %zu)", fn, need, ws ? ws_bytes : (size_t)0);
+  if (!dx && !dA && !dB) return ok();
+  if (int e = check_device(fn)) return e;
+  hipStream_t st = (hipStream_t)stream;
+  const int32_t *p = static_cast<const int32_t *>(plan);
+  float *u = static_cast<float *>(ws);
+  hipError_t e = hipSuccess;
+  if (M > 0 && (dx || dA)) {
+    e = aql::launch_lora_shrink_t(dy, M, N, B, alpha, L, R, p, u, st);
+    if (e != hipSuccess) return launched(e, fn);
+  }
+  if (dA || (dB && N > 0)) {
+    aql::LoraWgradArgs w{};
+    w.dy = dy;
+    w.xq = xq;
+    w.xs = xs;
+    w.h = h;
+    w.u = u;
+    w.plan = p;
+    w.dA = dA;
+    w.dB = N > 0 ? dB : nullptr;
+    w.M = M;
+    w.N = N;
+    w.K = K;
+    w.L = L;
+    w.R = R;
+    w.accumulate = accumulate != 0;
+    e = aql::launch_lora_wgrad(w, st);
+    if (e != hipSuccess) return launched(e, fn);
+  }
+  if (dx && M > 0) {
+    const aql::LoraTerm lt{u, A, p + aql::lora_plan_layout(M, L).idx, (int32_t)R, K};
+    const size_t ub = lora_bwd_u_bytes(M, R);
+    float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + ub);
+    e = aql::launch_w8a16_dgrad(dy, M, N, q, scale, K, dx, part, ws_bytes - ub, st, lt);
+  }
+  return launched(e, fn);
+}
+
+int aql_act_checkpoint(const void *x, int dtype, int64_t M, int64_t K, int8_t *xq, float *xs,
+                       void *stream) {
+  const char *fn = "aql_act_checkpoint";
+  REQUIRE(dtype == AQL_F32 || dtype == AQL_BF16, AQL_ERR_PARAM, "%s: unknown dtype %d", fn, dtype);
+  if (int e = check_ckpt(fn, x, M, K, xq, xs)) return e;
+  if (M == 0) return ok();
+  REQUIRE(x && xq && xs, AQL_ERR_NULL, "%s: x, xq and xs must not be NULL", fn);
+  if (int e = check_device(fn)) return e;
+  return launched(aql::launch_act_checkpoint(x, dtype == AQL_BF16, M, K, xq, xs,
+                                             (hipStream_t)stream),
+                  fn);
+}
+
+int aql_act_restore(const int8_t *xq, const float *xs, int64_t M, int64_t K, void *x, int dtype,
+                    void *stream) {
+  const char *fn = "aql_act_restore";
+  REQUIRE(dtype == AQL_F32 || dtype == AQL_BF16, AQL_ERR_PARAM, "%s: unknown dtype %d", fn, dtype);
+  if (int e = check_ckpt(fn, x, M, K, xq, xs)) return e;
+  if (M == 0) return ok();
+  REQUIRE(x && xq && xs, AQL_ERR_NULL, "%s: x, xq and xs must not be NULL", fn);
+  if (int e = check_device(fn)) return e;
+  return launched(aql::launch_act_restore(xq, xs, M, K, x, dtype == AQL_BF16, (hipStream_t)stream),
+                  fn);
 }
 
 int aql_gemm_i8_i32(const int8_t *a, const int8_t *b, int32_t *c, int64_t M, int64_t N,

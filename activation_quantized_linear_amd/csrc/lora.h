@@ -1,0 +1,231 @@
+// Low-rank adapters beside the int8 linear (internal to libaql.so): the batch
+// plan, the adapter term that the W8A16 kernels add in their epilogues, and the
+// launchers of the adapter kernels. Arguments are validated by the C ABI layer.
+#pragma once
+
+#include "common.h"
+
+namespace aql {
+
+// ------------------------------------------------------------------ the plan
+//
+// Device buffer of int32 that orders a batch's rows by adapter: a header, the
+// rows' adapters (-1: none), then tiles of 16 positions. A tile holds rows of
+// one adapter, adapters ascending, rows ascending within one; the rows without
+// an adapter come last as adapter -1. A segment's last tile is padded with -1.
+constexpr int kLoraTile = 16;
+constexpr int kLoraMaxAdapters = 1024;
+constexpr int kLoraHeader = 16;  // [0] tiles in use
+constexpr int kLoraMaxRank = 128;
+
+struct LoraPlanLayout {
+  int64_t tiles;     // tiles a batch of M rows over L adapters can need
+  int64_t idx;       // [M] adapter of each row
+  int64_t perm;      // [16 tiles] row at each sorted position, -1: padding
+  int64_t owner;     // [tiles] adapter of a tile, -1: rows without one, -2: unused
+  int64_t first;     // [L + 1] first tile of adapter a; [L]: of the rows without one
+  int64_t total;     // int32 elements in all
+};
+constexpr LoraPlanLayout lora_plan_layout(int64_t M, int64_t L) {
+  LoraPlanLayout p{};
+  p.tiles = M / kLoraTile + (M < L + 1 ? M : L + 1);
+  p.idx = kLoraHeader;
+  p.perm = p.idx + (M + 15) / 16 * 16;
+  p.owner = p.perm + p.tiles * kLoraTile;
+  p.first = p.owner + (p.tiles + 15) / 16 * 16;
+  p.total = p.first + (L + 1 + 15) / 16 * 16;
+  return p;
+}
+
+hipError_t launch_lora_plan(const int32_t *idx, int64_t M, int64_t L, int32_t *plan,
+                            hipStream_t st);
+
+// --------------------------------------------------- the term in an epilogue
+
+// No adapters: the epilogues compile to what they are without this parameter.
+struct NoLora {
+  static constexpr bool on = false;
+  __device__ __forceinline__ float add(int64_t, int64_t, float v) const { return v; }
+};
+
+// v + sum_j h[m, j] W[a][n, j], a = idx[m]: the low-rank product of one output.
+// h is float32 and the sum is taken in float32, so the output is rounded to
+// bf16 once, with the projection's sum in it. Rows without an adapter read
+// neither h nor W.
+struct LoraTerm {
+  static constexpr bool on = true;
+  const float *h;        // [M, R]
+  const uint16_t *W;     // [L, N, R] bf16
+  const int32_t *idx;    // [M]
+  int32_t R;             // a multiple of 8
+  int64_t N;
+  __device__ __forceinline__ float add(int64_t m, int64_t n, float v) const {
+    const int a = idx[m];
+    if (a < 0) return v;
+    const uint16_t *w = W + ((int64_t)a * N + n) * R;
+    const float *hm = h + m * R;
+    float s0 = 0.0f, s1 = 0.0f;
+    for (int j = 0; j < R; j += 8) {
+      const i32x4 wv = *reinterpret_cast<const i32x4 *>(w + j);
+      const f32x4 h0 = *reinterpret_cast<const f32x4 *>(hm + j);
+      const f32x4 h1 = *reinterpret_cast<const f32x4 *>(hm + j + 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t d = (uint32_t)wv[e];
+        const float a0 = e < 2 ? h0[2 * e] : h1[2 * e - 4];
+        const float a1 = e < 2 ? h0[2 * e + 1] : h1[2 * e - 3];
+        s0 = fmaf(__uint_as_float(d << 16), a0, s0);
+        s1 = fmaf(__uint_as_float(d & 0xffff0000u), a1, s1);
+      }
+    }
+    return v + (s0 + s1);
+  }
+};
+
+// Eight floats -> bf16 parts with v = hi + lo up to 2^-16 |v| (both rounded to
+// nearest, 2^-8 each): products with bf16 operands then cost two matrix instructions and
+// keep the float32 operand's precision well below the output's rounding.
+__device__ __forceinline__ void split_bf16(const float (&v)[8], bf16x8 &hi, bf16x8 &lo) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    hi[e] = (__bf16)v[e];
+    lo[e] = (__bf16)(v[e] - (float)hi[e]);
+  }
+}
+
+// The same in three parts (v = hi + mid + lo up to 2^-24 |v|, float32's own
+// rounding), for the weight gradients, whose outputs are float32.
+__device__ __forceinline__ void split_bf16(const float (&v)[8], bf16x8 &hi, bf16x8 &mid,
+                                           bf16x8 &lo) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    hi[e] = (__bf16)v[e];
+    const float r = v[e] - (float)hi[e];
+    mid[e] = (__bf16)r;
+    lo[e] = (__bf16)(r - (float)mid[e]);
+  }
+}
+
+// acc[i][j] += h . W_a^T over a wave's tile of MFMA blocks: 16 TI rows from m0
+// by 16 TJ columns from n0, accumulators in the 16x16x32 layout (lane 16 g + r
+// holds rows 4 g + v of column r). The wave walks the distinct adapters of its
+// rows in ascending order; a block that holds none of an adapter's rows is
+// skipped, and in a block of several adapters the products of the other rows
+// are computed and dropped by a select, so no value of one adapter (an
+// infinity or a NaN in it among them) reaches a row of another. All 64 lanes
+// must be active. KMAJOR: W is [L, R, N] (contraction rows), else [L, N, R].
+template <bool KMAJOR, int TI, int TJ>
+__device__ __forceinline__ void lora_add_tile(f32x4 (&acc)[TI][TJ], const LoraTerm &t, int64_t m0,
+                                              int64_t M, int64_t n0) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  int id[TI];
+#pragma unroll
+  for (int i = 0; i < TI; ++i) {
+    const int64_t m = m0 + 16 * i + r;
+    id[i] = m < M ? t.idx[m] : -1;
+  }
+  int prev = -1;
+  for (;;) {
+    int next = 0x7fffffff;
+#pragma unroll
+    for (int i = 0; i < TI; ++i) next = id[i] > prev && id[i] < next ? id[i] : next;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+      const int other = __shfl_xor(next, o);
+      next = other < next ? other : next;
+    }
+    const int a = __builtin_amdgcn_readfirstlane(next);
+    if (a == 0x7fffffff) return;
+    prev = a;
+    for (int c = 0; c < t.R; c += 32) {
+      const int j0 = c + 8 * g;
+      const bool in = j0 < t.R;  // whole chunks of 8: R is a multiple of 8
+      bf16x8 w[TJ];
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        const int64_t n = n0 + 16 * j + r;
+        i32x4 v = {0, 0, 0, 0};
+        if (in && n < t.N) {
+          if constexpr (KMAJOR) {
+            const uint16_t *p = t.W + ((int64_t)a * t.R + j0) * t.N + n;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = (int)((uint32_t)p[(int64_t)(2 * e) * t.N] |
+                           ((uint32_t)p[(int64_t)(2 * e + 1) * t.N] << 16));
+          } else {
+            v = *reinterpret_cast<const i32x4 *>(t.W + ((int64_t)a * t.N + n) * t.R + j0);
+          }
+        }
+        w[j] = __builtin_bit_cast(bf16x8, v);
+      }
+#pragma unroll
+      for (int i = 0; i < TI; ++i) {
+        const uint64_t has = __ballot(id[i] == a);
+        if (has == 0) continue;
+        // bit v: output row 4 g + v is the adapter's. Kept opaque, so that the
+        // masks of all blocks are not hoisted out of the loop into registers.
+        uint32_t own = (uint32_t)(has >> (4 * g));
+        asm volatile("" : "+v"(own));
+        float hv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (in && id[i] == a) {
+          // opaque for the same reason (a lane offset, not TI hoisted addresses)
+          uint32_t ho = (uint32_t)(r * t.R + j0);
+          asm volatile("" : "+v"(ho));
+          const float *hm = t.h + (m0 + 16 * i) * t.R + ho;
+          const f32x4 h0 = *reinterpret_cast<const f32x4 *>(hm);
+          const f32x4 h1 = *reinterpret_cast<const f32x4 *>(hm + 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            hv[e] = h0[e];
+            hv[4 + e] = h1[e];
+          }
+        }
+        bf16x8 hi, lo;
+        split_bf16(hv, hi, lo);
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+          f32x4 d = {0.f, 0.f, 0.f, 0.f};
+          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[j], d, 0, 0, 0);
+          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[j], d, 0, 0, 0);
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            acc[i][j][v] += own & (1u << v) ? d[v] : 0.0f;
+        }
+        // one block's operands at a time: hoisting the loads of all TI blocks
+        // would cost the registers that hold the accumulators
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- launchers
+
+// h[m, :] = alpha[a] A_a x[m] (float32 [M, R]); rows without an adapter get
+// zeros. x [M, K] bf16, A [L, R, K] bf16.
+hipError_t launch_lora_shrink(const uint16_t *x, int64_t M, int64_t K, const uint16_t *A,
+                              const float *alpha, int64_t L, int64_t R, const int32_t *plan,
+                              float *h, hipStream_t st);
+
+// u[m, :] = alpha[a] B_a^T dy[m] (float32 [M, R]); rows without an adapter get
+// zeros. dy [M, N] bf16, B [L, N, R] bf16, N % 8 == 0.
+hipError_t launch_lora_shrink_t(const uint16_t *dy, int64_t M, int64_t N, const uint16_t *B,
+                                const float *alpha, int64_t L, int64_t R, const int32_t *plan,
+                                float *u, hipStream_t st);
+
+// dB[a][n, j] = sum_{m in a} dy[m, n] h[m, j] and
+// dA[a][j, k] = sum_{m in a} u[m, j] xq[m, k] xs[m, k / 128], both float32;
+// accumulate adds to what the outputs hold. Either output may be NULL.
+struct LoraWgradArgs {
+  const uint16_t *dy;
+  const int8_t *xq;
+  const float *xs;
+  const float *h, *u;
+  const int32_t *plan;
+  float *dA, *dB;
+  int64_t M, N, K, L, R;
+  bool accumulate;
+};
+hipError_t launch_lora_wgrad(const LoraWgradArgs &a, hipStream_t st);
+
+}  // namespace aql

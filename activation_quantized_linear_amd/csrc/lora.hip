@@ -1,0 +1,541 @@
+// Low-rank adapters beside the int8 linear: the batch plan, the shrink
+// products (x onto an adapter's A, dy onto its B) and the weight gradients.
+//
+//   h[m, j]     = alpha[a] sum_k x[m, k] A_a[j, k]            a = idx[m]
+//   u[m, j]     = alpha[a] sum_n dy[m, n] B_a[n, j]
+//   dB_a[n, j]  = sum_{m in a} dy[m, n] h[m, j]
+//   dA_a[j, k]  = sum_{m in a} u[m, j] xq[m, k] xs[m, k / 128]
+//
+// h and u are float32 [M, R]; the expanding products h B^T and u A are added in
+// the epilogues of the projection's own kernels (lora.h), so neither y nor dx
+// makes a second trip through memory. All products run on the bf16 matrix
+// cores with float32 accumulation (or as float32 FMAs of exact bf16 products);
+// float32 operands are split into bf16 parts that add up to them.
+// Every sum has one order, so results repeat bit for bit.
+#include "lora.h"
+
+namespace aql {
+namespace {
+
+constexpr int kGroup = 128;  // columns of a checkpoint scale
+
+// ------------------------------------------------------------------ the plan
+
+// A counting sort of the rows by adapter, by one workgroup: LDS histogram (its
+// atomics count, so their order does not matter), tile offsets by a scan over
+// the adapters, then chunks of 1024 rows in order. Inside a chunk a row's rank
+// is the number of equal rows before it in its wave (ballots) plus the counts
+// of the waves before (a byte table), so rows keep their order in a segment.
+__global__ __launch_bounds__(1024) void k_lora_plan(const int32_t *__restrict__ idx, int64_t M,
+                                                    int64_t L, int32_t *__restrict__ plan) {
+  constexpr int NB = kLoraMaxAdapters + 1;  // the last bin: rows without an adapter
+  __shared__ int next[NB];                  // counts, then the next free position of a bin
+  __shared__ int scan[1024];
+  __shared__ int total;
+  __shared__ uint8_t cnt[16][NB + 3];
+  const LoraPlanLayout p = lora_plan_layout(M, L);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int nb = (int)L + 1;
+  for (int b = tid; b < nb; b += 1024) next[b] = 0;
+  for (int b = tid; b < 16 * (NB + 3); b += 1024) (&cnt[0][0])[b] = 0;
+  __syncthreads();
+  auto bin_of = [&](int64_t m) {
+    const int a = idx[m];
+    return a >= 0 && a < L ? a : (int)L;
+  };
+  for (int64_t m = tid; m < M; m += 1024) {
+    const int b = bin_of(m);
+    plan[p.idx + m] = b < L ? b : -1;
+    atomicAdd(&next[b], 1);
+  }
+  __syncthreads();
+  // tiles of bins 0 .. L - 1, scanned; bin L (at most 1025 bins) comes last
+  const int mine = tid < nb && tid < 1024 ? (next[tid] + kLoraTile - 1) / kLoraTile : 0;
+  scan[tid] = mine;
+  __syncthreads();
+  for (int o = 1; o < 1024; o <<= 1) {
+    const int v = tid >= o ? scan[tid - o] : 0;
+    __syncthreads();
+    scan[tid] += v;
+    __syncthreads();
+  }
+  const int before = scan[tid] - mine;
+  if (tid == 0) {
+    const int all = scan[1023];
+    total = nb > 1024 ? all + (next[1024] + kLoraTile - 1) / kLoraTile : all;
+    if (nb > 1024) {  // L = 1024: the bin past the scan
+      plan[p.first + 1024] = all;
+      next[1024] = all * kLoraTile;
+    }
+  }
+  __syncthreads();
+  if (tid < nb && tid < 1024) {
+    plan[p.first + tid] = before;
+    next[tid] = before * kLoraTile;
+  }
+  for (int64_t t = total + tid; t < p.tiles; t += 1024) plan[p.owner + t] = -2;
+  for (int64_t i = tid; i < p.tiles * kLoraTile; i += 1024) plan[p.perm + i] = -1;
+  if (tid == 0) plan[0] = total;
+  __threadfence_block();
+  __syncthreads();
+  for (int64_t m0 = 0; m0 < M; m0 += 1024) {
+    const int64_t m = m0 + tid;
+    const bool live = m < M;
+    const int b = live ? bin_of(m) : -1;
+    uint64_t left = __ballot(live);
+    int rank = 0;
+    while (left) {
+      const int lead = __ffsll((unsigned long long)left) - 1;
+      const int bb = __shfl(b, lead);
+      const uint64_t same = __ballot(b == bb);
+      if (b == bb) rank = __popcll(same & ((1ull << lane) - 1));
+      if (lane == lead) cnt[wave][bb] = (uint8_t)__popcll(same);
+      left &= ~same;
+    }
+    __syncthreads();
+    if (live) {
+      int pos = next[b] + rank;
+      for (int w = 0; w < wave; ++w) pos += cnt[w][b];
+      plan[p.perm + pos] = (int32_t)m;
+      if (pos % kLoraTile == 0) plan[p.owner + pos / kLoraTile] = b < L ? b : -1;
+    }
+    __syncthreads();
+    for (int c = tid; c < nb; c += 1024) {
+      int sum = 0;
+      for (int w = 0; w < 16; ++w) {
+        sum += cnt[w][c];
+        cnt[w][c] = 0;
+      }
+      next[c] += sum;
+    }
+    __syncthreads();
+  }
+}
+
+// --------------------------------------------------- shrink, streaming form
+
+__device__ __forceinline__ float bf16_lo(int d) { return __uint_as_float((uint32_t)d << 16); }
+__device__ __forceinline__ float bf16_hi(int d) {
+  return __uint_as_float((uint32_t)d & 0xffff0000u);
+}
+
+// Few rows: a workgroup of 4 waves takes J ranks of one row and reads J rows
+// of its adapter's A once, the waves taking 512-element steps of K in turn.
+// Bound by latency and, with many adapters, by reading them (2 R K bytes each).
+template <int J>
+__global__ __launch_bounds__(256) void k_lora_shrink_rows(
+    const uint16_t *__restrict__ x, int64_t K, const uint16_t *__restrict__ A,
+    const float *__restrict__ alpha, int R, const int32_t *__restrict__ idx,
+    float *__restrict__ h) {
+  __shared__ float red[4][J];
+  const int64_t m = blockIdx.y;
+  const int j0 = blockIdx.x * J;
+  const int a = idx[m];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (a < 0) {  // uniform over the workgroup
+    if (threadIdx.x < J) h[m * R + j0 + threadIdx.x] = 0.0f;
+    return;
+  }
+  const uint16_t *xr = x + m * K, *ar = A + ((int64_t)a * R + j0) * K;
+  float acc[J][2];
+#pragma unroll
+  for (int j = 0; j < J; ++j) acc[j][0] = acc[j][1] = 0.0f;
+  constexpr int U = J == 1 ? 4 : 2;
+  for (int64_t k0 = 8 * (int64_t)threadIdx.x; k0 < K; k0 += 2048 * U) {
+    i32x4 xv[U], av[U][J];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t k = k0 + 2048 * u;
+      xv[u] = i32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < J; ++j) av[u][j] = i32x4{0, 0, 0, 0};
+      if (k < K) {
+        xv[u] = *reinterpret_cast<const i32x4 *>(xr + k);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          av[u][j] = *reinterpret_cast<const i32x4 *>(ar + j * K + k);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x0 = bf16_lo(xv[u][e]), x1 = bf16_hi(xv[u][e]);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          acc[j][0] = fmaf(x0, bf16_lo(av[u][j][e]), acc[j][0]);
+          acc[j][1] = fmaf(x1, bf16_hi(av[u][j][e]), acc[j][1]);
+        }
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    float s = acc[j][0] + acc[j][1];
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    if (lane == 0) red[wave][j] = s;
+  }
+  __syncthreads();
+  if (threadIdx.x < J) {
+    const int j = threadIdx.x;
+    h[m * R + j0 + j] = alpha[a] * ((red[0][j] + red[1][j]) + (red[2][j] + red[3][j]));
+  }
+}
+
+// ------------------------------------------------------- shrink, tiled form
+
+// A workgroup of W waves takes one tile of the plan (16 rows of one adapter)
+// and all 16 RT ranks; the waves split the contraction in steps of 32 U and
+// meet in LDS. Operands go from memory to the MFMA registers as they lie: both
+// x and A have the contraction contiguous. KMAJOR: the adapter matrix is
+// [C, R] (dy onto B); each wave then copies its step's 32 x 16 blocks into LDS
+// with loads that write it directly and reads them back transposed.
+typedef __attribute__((address_space(3))) void lds_void;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+template <int W, int RT, bool KMAJOR>
+struct ShrinkLds {
+  static constexpr int U = RT <= 2 ? 4 : (RT <= 4 ? 2 : 1);
+  static constexpr int STEP = KMAJOR ? U * RT * 1024 : 0;  // bytes a wave stages per step
+  static constexpr int RED = W * RT * 64 * 16;
+  static constexpr int BYTES = W * STEP > RED ? W * STEP : RED;
+};
+
+template <int W, int RT, bool KMAJOR>
+__global__ __launch_bounds__(64 * W) void k_lora_shrink(
+    const uint16_t *__restrict__ x, int64_t C, const uint16_t *__restrict__ A,
+    const float *__restrict__ alpha, int R, int64_t M, int64_t L,
+    const int32_t *__restrict__ plan, float *__restrict__ h) {
+  using S = ShrinkLds<W, RT, KMAJOR>;
+  constexpr int U = S::U;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const LoraPlanLayout p = lora_plan_layout(M, L);
+  const int tile = blockIdx.x;
+  const int a = plan[p.owner + tile];
+  if (a == -2) return;
+  const int32_t *perm = plan + p.perm + (int64_t)tile * kLoraTile;
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (a < 0) {
+    for (int i = threadIdx.x; i < kLoraTile * R; i += 64 * W) {
+      const int m = perm[i / R];
+      if (m >= 0) h[(int64_t)m * R + i % R] = 0.0f;
+    }
+    return;
+  }
+  // a padding position computes the tile's first row again; its results are dropped
+  const int mrow = perm[r] >= 0 ? perm[r] : perm[0];
+  const uint16_t *xr = x + (int64_t)mrow * C;
+  const uint16_t *ab = A + (int64_t)a * R * C;
+  const i32x4 zero = {0, 0, 0, 0};
+  f32x4 acc[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  char *stage = smem + wave * S::STEP;
+  for (int64_t c0 = (int64_t)wave * (32 * U); c0 < C; c0 += (int64_t)W * 32 * U) {
+    i32x4 xv[U], av[U][RT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = c0 + 32 * u + 8 * g;
+      xv[u] = c < C ? *reinterpret_cast<const i32x4 *>(xr + c) : zero;
+      if constexpr (!KMAJOR) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          const int j = 16 * t + r < R ? 16 * t + r : R - 1;  // past R: dropped columns
+          av[u][t] = c < C ? *reinterpret_cast<const i32x4 *>(ab + (int64_t)j * C + c) : zero;
+        }
+      } else {
+        // lane l: row c0 + 32 u + l / 2 of A, ranks 16 t + 8 (l % 2) .. + 7
+        const int64_t cr = c0 + 32 * u + (lane >> 1);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          const int j = 16 * t + 8 * (lane & 1);
+          av[u][t] = cr < C && j < R ? *reinterpret_cast<const i32x4 *>(ab + cr * R + j) : zero;
+        }
+      }
+    }
+    if constexpr (KMAJOR) {
+      // a wave's own LDS slot: its stores and loads complete in order
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+          *reinterpret_cast<i32x4 *>(stage + (u * RT + t) * 1024 + 16 * lane) = av[u][t];
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          // 16 lanes read 4 rows x 16 ranks and get column r of them
+          const uint32_t at = (uint32_t)(uintptr_t)(stage + (u * RT + t) * 1024 +
+                                                    (8 * g + (r >> 2)) * 32 + 8 * (r & 3));
+          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)at);
+          const s16x4 hi =
+              __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)(at + 128));
+          const i32x2 l2 = __builtin_bit_cast(i32x2, lo), h2 = __builtin_bit_cast(i32x2, hi);
+          av[u][t] = i32x4{l2[0], l2[1], h2[0], h2[1]};
+        }
+      __builtin_amdgcn_wave_barrier();
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv[u]),
+                                                         __builtin_bit_cast(bf16x8, av[u][t]),
+                                                         acc[t], 0, 0, 0);
+  }
+  __syncthreads();
+  f32x4 *red = reinterpret_cast<f32x4 *>(smem);
+#pragma unroll
+  for (int t = 0; t < RT; ++t) red[(wave * RT + t) * 64 + lane] = acc[t];
+  __syncthreads();
+  const float al = alpha[a];
+  for (int t = wave; t < RT; t += W) {
+    f32x4 s = red[t * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < W; ++w) s += red[(w * RT + t) * 64 + lane];
+    const int j = 16 * t + r;
+    if (j >= R) continue;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int m = perm[4 * g + v];
+      if (m >= 0) h[(int64_t)m * R + j] = al * s[v];
+    }
+  }
+}
+
+// ----------------------------------------------------------- weight gradients
+
+// One workgroup of W waves: adapter a, 128 columns of dy (dB) or of the
+// checkpoint (dA; they share one scale per row) and 16 RT ranks. The
+// contraction runs over the adapter's rows in sorted order, 32 at a step, the
+// waves taking steps in turn and meeting in LDS at the end. Both operands have
+// the contraction as their slow axis: lane (r, g) reads 8 columns of the 8 rows
+// 8 g .. 8 g + 7 and turns the 8 x 8 block in registers into the operands of 8
+// MFMAs, MFMA c covering columns 8 r + c. The float32 operand (h, or u times
+// the row's scale) is split into three bf16 parts.
+// a.lo16 | b.lo16 << 16 and the high halves
+__device__ __forceinline__ int pack_lo(int a, int b) {
+  return (int)__builtin_amdgcn_perm((uint32_t)b, (uint32_t)a, 0x05040100u);
+}
+__device__ __forceinline__ int pack_hi(int a, int b) {
+  return (int)__builtin_amdgcn_perm((uint32_t)b, (uint32_t)a, 0x07060302u);
+}
+
+template <int W, int RT, bool CODES>
+__device__ __forceinline__ void lora_wgrad(const LoraWgradArgs &p, const LoraPlanLayout &pl,
+                                           int64_t a, int64_t c0, int j0, char *smem) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t C = CODES ? p.K : p.N;
+  const int R = (int)p.R;
+  const int64_t G = (p.K + kGroup - 1) / kGroup;
+  const int32_t *perm = p.plan + pl.perm;
+  const int first = p.plan[pl.first + a] * kLoraTile, last = p.plan[pl.first + a + 1] * kLoraTile;
+  const float *left = CODES ? p.u : p.h;
+  const int64_t col = c0 + 8 * r;
+  const bool cin = col < C;  // whole chunks of 8: C is a multiple of 8
+
+  f32x4 acc[RT][8];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  for (int p0 = first + 32 * wave; p0 < last; p0 += 32 * W) {
+    int row[8];
+    const int q0 = p0 + 8 * g;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) row[e] = q0 + e < last ? perm[q0 + e] : -1;
+    // 8 rows x 8 columns; rows of padding are zero on both sides
+    i32x4 d[8];
+    float s[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      d[e] = i32x4{0, 0, 0, 0};
+      s[e] = 1.0f;
+      if (row[e] >= 0 && cin) {
+        if constexpr (CODES) {
+          const i32x2 v = *reinterpret_cast<const i32x2 *>(p.xq + (int64_t)row[e] * C + col);
+          d[e][0] = v[0];
+          d[e][1] = v[1];
+        } else {
+          d[e] = *reinterpret_cast<const i32x4 *>(p.dy + (int64_t)row[e] * C + col);
+        }
+      }
+      if constexpr (CODES) s[e] = row[e] >= 0 ? p.xs[(int64_t)row[e] * G + c0 / kGroup] : 0.0f;
+    }
+    bf16x8 hi[RT], mid[RT], lo[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      float v[8];
+      const int j = j0 + 16 * t + r;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = row[e] >= 0 && j < R ? left[(int64_t)row[e] * R + j] : 0.0f;
+        if constexpr (CODES) v[e] *= s[e];
+      }
+      split_bf16(v, hi[t], mid[t], lo[t]);
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      i32x4 b;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (CODES) {
+          const float f0 = (float)(int8_t)(d[2 * e][c >> 2] >> (8 * (c & 3)));
+          const float f1 = (float)(int8_t)(d[2 * e + 1][c >> 2] >> (8 * (c & 3)));
+          b[e] = pack_hi((int)__float_as_uint(f0), (int)__float_as_uint(f1));  // exact
+        } else {
+          b[e] = (c & 1) ? pack_hi(d[2 * e][c >> 1], d[2 * e + 1][c >> 1])
+                         : pack_lo(d[2 * e][c >> 1], d[2 * e + 1][c >> 1]);
+        }
+      }
+      const bf16x8 bv = __builtin_bit_cast(bf16x8, b);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[t], bv, acc[t][c], 0, 0, 0);
+        acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mid[t], bv, acc[t][c], 0, 0, 0);
+        acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[t], bv, acc[t][c], 0, 0, 0);
+      }
+    }
+  }
+  // the waves' sums meet pairwise
+  f32x4 *red = reinterpret_cast<f32x4 *>(smem);
+#pragma unroll
+  for (int half = W / 2; half > 0; half >>= 1) {
+    __syncthreads();
+    if (wave >= half && wave < 2 * half) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) red[(((wave - half) * RT + t) * 8 + c) * 64 + lane] = acc[t][c];
+    }
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[t][c] += red[((wave * RT + t) * 8 + c) * 64 + lane];
+    }
+  }
+  if (wave != 0 || !cin) return;
+  // acc[t][c] lane: ranks j0 + 16 t + 4 g + v of column col + c
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int j = j0 + 16 * t + 4 * g;
+    if (j >= R) continue;  // whole groups of 4
+    if constexpr (CODES) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        float *dst = p.dA + ((int64_t)a * R + j + v) * C + col;
+        f32x4 o0 = {acc[t][0][v], acc[t][1][v], acc[t][2][v], acc[t][3][v]};
+        f32x4 o1 = {acc[t][4][v], acc[t][5][v], acc[t][6][v], acc[t][7][v]};
+        if (p.accumulate) {
+          o0 += *reinterpret_cast<const f32x4 *>(dst);
+          o1 += *reinterpret_cast<const f32x4 *>(dst + 4);
+        }
+        *reinterpret_cast<f32x4 *>(dst) = o0;
+        *reinterpret_cast<f32x4 *>(dst + 4) = o1;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        float *dst = p.dB + ((int64_t)a * C + col + c) * R + j;
+        f32x4 o = acc[t][c];
+        if (p.accumulate) o += *reinterpret_cast<const f32x4 *>(dst);
+        *reinterpret_cast<f32x4 *>(dst) = o;
+      }
+    }
+  }
+}
+
+template <int W, int RT>
+__global__ __launch_bounds__(64 * W) void k_lora_wgrad(LoraWgradArgs p, int tiles_b) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const LoraPlanLayout pl = lora_plan_layout(p.M, p.L);
+  const int64_t a = blockIdx.y;
+  const int j0 = blockIdx.z * 16 * RT;
+  const int tile = blockIdx.x;
+  if (tile < tiles_b)
+    lora_wgrad<W, RT, false>(p, pl, a, (int64_t)tile * 128, j0, smem);
+  else
+    lora_wgrad<W, RT, true>(p, pl, a, (int64_t)(tile - tiles_b) * 128, j0, smem);
+}
+
+template <int W, int RT, bool KMAJOR>
+hipError_t go_shrink(const uint16_t *x, int64_t M, int64_t C, const uint16_t *A,
+                     const float *alpha, int64_t L, int64_t R, const int32_t *plan, float *h,
+                     hipStream_t st) {
+  constexpr int bytes = ShrinkLds<W, RT, KMAJOR>::BYTES;
+  if constexpr (bytes > 65536) {
+    (void)hipFuncSetAttribute((const void *)k_lora_shrink<W, RT, KMAJOR>,
+                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    (void)hipGetLastError();
+  }
+  hipLaunchKernelGGL((k_lora_shrink<W, RT, KMAJOR>), dim3((unsigned)lora_plan_layout(M, L).tiles),
+                     dim3(64 * W), bytes, st, x, C, A, alpha, (int)R, M, L, plan, h);
+  return hipGetLastError();
+}
+
+template <bool KMAJOR>
+hipError_t go_shrink_r(const uint16_t *x, int64_t M, int64_t C, const uint16_t *A,
+                       const float *alpha, int64_t L, int64_t R, const int32_t *plan, float *h,
+                       hipStream_t st) {
+  if (R <= 16) return go_shrink<8, 1, KMAJOR>(x, M, C, A, alpha, L, R, plan, h, st);
+  if (R <= 32) return go_shrink<8, 2, KMAJOR>(x, M, C, A, alpha, L, R, plan, h, st);
+  if (R <= 64) return go_shrink<8, 4, KMAJOR>(x, M, C, A, alpha, L, R, plan, h, st);
+  return go_shrink<8, 8, KMAJOR>(x, M, C, A, alpha, L, R, plan, h, st);
+}
+
+template <int W, int RT>
+hipError_t go_wgrad(const LoraWgradArgs &a, hipStream_t st) {
+  constexpr int bytes = W / 2 * RT * 8 * 64 * 16;
+  if constexpr (bytes > 65536) {
+    (void)hipFuncSetAttribute((const void *)k_lora_wgrad<W, RT>,
+                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    (void)hipGetLastError();
+  }
+  const int tb = a.dB ? (int)((a.N + 127) / 128) : 0, ta = a.dA ? (int)((a.K + 127) / 128) : 0;
+  const dim3 grid((unsigned)(tb + ta), (unsigned)a.L, (unsigned)((a.R + 16 * RT - 1) / (16 * RT)));
+  hipLaunchKernelGGL((k_lora_wgrad<W, RT>), grid, dim3(64 * W), bytes, st, a, tb);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_lora_plan(const int32_t *idx, int64_t M, int64_t L, int32_t *plan,
+                            hipStream_t st) {
+  hipLaunchKernelGGL(k_lora_plan, dim3(1), dim3(1024), 0, st, idx, M, L, plan);
+  return hipGetLastError();
+}
+
+hipError_t launch_lora_shrink(const uint16_t *x, int64_t M, int64_t K, const uint16_t *A,
+                              const float *alpha, int64_t L, int64_t R, const int32_t *plan,
+                              float *h, hipStream_t st) {
+  if (M >= 64) return go_shrink_r<false>(x, M, K, A, alpha, L, R, plan, h, st);
+  const int32_t *idx = plan + lora_plan_layout(M, L).idx;
+  if (M * R < 2048)
+    hipLaunchKernelGGL(k_lora_shrink_rows<1>, dim3((unsigned)R, (unsigned)M), dim3(256), 0, st, x,
+                       K, A, alpha, (int)R, idx, h);
+  else
+    hipLaunchKernelGGL(k_lora_shrink_rows<4>, dim3((unsigned)(R / 4), (unsigned)M), dim3(256), 0,
+                       st, x, K, A, alpha, (int)R, idx, h);
+  return hipGetLastError();
+}
+
+hipError_t launch_lora_shrink_t(const uint16_t *dy, int64_t M, int64_t N, const uint16_t *B,
+                                const float *alpha, int64_t L, int64_t R, const int32_t *plan,
+                                float *u, hipStream_t st) {
+  return go_shrink_r<true>(dy, M, N, B, alpha, L, R, plan, u, st);
+}
+
+hipError_t launch_lora_wgrad(const LoraWgradArgs &a, hipStream_t st) {
+  if (a.R <= 16) return go_wgrad<8, 1>(a, st);
+  if (a.R <= 32) return go_wgrad<8, 2>(a, st);
+  return go_wgrad<4, 4>(a, st);
+}
+
+}  // namespace aql

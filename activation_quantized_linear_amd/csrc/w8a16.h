@@ -4,6 +4,7 @@
 #pragma once
 
 #include "common.h"
+#include "lora.h"
 
 namespace aql {
 
@@ -12,6 +13,10 @@ namespace aql {
 hipError_t launch_w8a16(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
                         const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
                         float *part, size_t part_bytes, hipStream_t st);
+// The same with every row's adapter term added before the rounding.
+hipError_t launch_w8a16(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
+                        const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
+                        float *part, size_t part_bytes, hipStream_t st, const LoraTerm &lt);
 
 // K splits of the shared-x skinny tile below kW8A16ShareMinN channels (1: the
 // shape does not split): 12 <= M < 64, K >= 8192, 4 splits up to 128 tiles of

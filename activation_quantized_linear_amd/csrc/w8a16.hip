@@ -110,9 +110,9 @@ struct Red {
 // workgroup instead of once per wave tile, and each step reads its 8 bytes per
 // lane from LDS. The copy is issued before the first weight batch and waited
 // for after it, so its latency hides behind the weights'.
-template <int W, int CW, int TG, int U, bool XL>
+template <int W, int CW, int TG, int U, bool XL, class LT>
 __device__ __forceinline__ void w8a16_tile_m1(const Tile &t, Red<W * CW, TG, 0> &red,
-                                              uint8_t *xs) {
+                                              uint8_t *xs, const LT &lt) {
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cw = wid / W, wave = wid % W;
@@ -250,7 +250,7 @@ __device__ __forceinline__ void w8a16_tile_m1(const Tile &t, Red<W * CW, TG, 0> 
     for (int tg = 1; tg < TG; ++tg) sum = (lane >> 2) == tg ? v[tg] : sum;
   }
   const float bv = t.bias ? bf16_to_f32(t.bias[n]) : 0.0f;
-  t.y[t.m0 * t.N + n] = f32_to_bf16_rne(t.scale[n] * sum + bv);
+  t.y[t.m0 * t.N + n] = f32_to_bf16_rne(lt.add(t.m0, n, t.scale[n] * sum + bv));
 }
 
 // TG row groups of 4 output channels per tile (4 TG channels), MB blocks of 4
@@ -404,8 +404,8 @@ __device__ __forceinline__ void sk_wait_vm() {
   __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
 }
 
-template <int W, int NT>
-__device__ __forceinline__ void w8a16_tile_sk(const Tile &t, SkLds<W, NT> &sm) {
+template <int W, int NT, class LT>
+__device__ __forceinline__ void w8a16_tile_sk(const Tile &t, SkLds<W, NT> &sm, const LT &lt) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
@@ -514,7 +514,7 @@ __device__ __forceinline__ void w8a16_tile_sk(const Tile &t, SkLds<W, NT> &sm) {
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const int64_t mm = t.m0 + 4 * g + v;
-      if (mm < t.M) t.y[mm * t.N + n] = f32_to_bf16_rne(s * acc[c][v] + bv);
+      if (mm < t.M) t.y[mm * t.N + n] = f32_to_bf16_rne(lt.add(mm, n, s * acc[c][v] + bv));
     }
   }
 }
@@ -536,12 +536,12 @@ constexpr int batch_steps() {
 // next batch in flight while one is used. The 8 rows' lane partials are summed
 // by a transposing butterfly (3 exchange steps halve the values a lane carries,
 // 3 more finish the sum), the waves' sums meet in LDS.
-template <int W, int P, int B = 4>
+template <int W, int P, int B, class LT>
 __global__ __launch_bounds__(64 * W) void k_w8a16_m1c(const uint16_t *__restrict__ x, int64_t K,
                                                        const int8_t *__restrict__ q,
                                                        const float *__restrict__ scale,
                                                        const uint16_t *__restrict__ bias,
-                                                       int64_t N, uint16_t *__restrict__ y) {
+                                                       int64_t N, uint16_t *__restrict__ y, LT lt) {
   constexpr int R = 8;           // channels per workgroup
   constexpr int NL = R * P;      // weight loads per wave
   constexpr int NB = (NL + B - 1) / B;
@@ -655,7 +655,7 @@ __global__ __launch_bounds__(64 * W) void k_w8a16_m1c(const uint16_t *__restrict
   const int64_t n = n0 + row;
   if (n >= N) return;
   const float bv = bias ? bf16_to_f32(bias[n]) : 0.0f;
-  y[n] = f32_to_bf16_rne(scale[n] * sum + bv);
+  y[n] = f32_to_bf16_rne(lt.add(0, n, scale[n] * sum + bv));
 }
 
 // Grouped single-row GEMVs in the contiguous form of k_w8a16_m1c (1 KB row
@@ -814,12 +814,12 @@ __device__ __forceinline__ float dot2_bf16(int a, int b, float c) {
   asm volatile("v_dot2_f32_bf16 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
   return d;
 }
-template <int W, int P, int MR>
+template <int W, int P, int MR, class LT>
 __global__ __launch_bounds__(64 * W) void k_w8a16_mfew(const uint16_t *__restrict__ x, int64_t M,
                                                         int64_t K, const int8_t *__restrict__ q,
                                                         const float *__restrict__ scale,
                                                         const uint16_t *__restrict__ bias,
-                                                        int64_t N, uint16_t *__restrict__ y) {
+                                                        int64_t N, uint16_t *__restrict__ y, LT lt) {
   constexpr int R = 8;           // channels per workgroup
   constexpr int NL = R * P;      // weight loads per wave
   constexpr int B = 4;           // loads per batch
@@ -947,14 +947,14 @@ __global__ __launch_bounds__(64 * W) void k_w8a16_mfew(const uint16_t *__restric
     const int64_t n = n0 + r;
     if (m >= M || n >= N) return;
     const float bv = bias ? bf16_to_f32(bias[n]) : 0.0f;
-    y[m * N + n] = f32_to_bf16_rne(scale[n] * sum + bv);
+    y[m * N + n] = f32_to_bf16_rne(lt.add(m, n, scale[n] * sum + bv));
   } else {
     if (!lead) return;
     const int r = idx / MR, m = idx % MR;
     const int64_t n = n0 + r;
     if (m >= M || n >= N) return;
     const float bv = bias ? bf16_to_f32(bias[n]) : 0.0f;
-    y[m * N + n] = f32_to_bf16_rne(scale[n] * sum + bv);
+    y[m * N + n] = f32_to_bf16_rne(lt.add(m, n, scale[n] * sum + bv));
   }
 }
 
@@ -998,23 +998,23 @@ __global__ __launch_bounds__(64 * W) void k_w8a16_grouped(const W8A16GroupEntry 
 }
 
 // Skinny tile (M <= 16): 16 NT channels x 16 rows per workgroup of W waves.
-template <int W, int NT>
+template <int W, int NT, class LT>
 __global__ __launch_bounds__(64 * W) void k_w8a16_sk(const uint16_t *__restrict__ x, int64_t M,
                                                      int64_t K, const int8_t *__restrict__ q,
                                                      const float *__restrict__ scale,
                                                      const uint16_t *__restrict__ bias, int64_t N,
-                                                     uint16_t *__restrict__ y) {
+                                                     uint16_t *__restrict__ y, LT lt) {
   __shared__ __attribute__((aligned(16))) SkLds<W, NT> sm;
   const Tile t{x, q, scale, bias, y, M, N, K, (int64_t)blockIdx.x * 16 * NT,
                (int64_t)blockIdx.y * 16};
-  w8a16_tile_sk<W, NT>(t, sm);
+  w8a16_tile_sk<W, NT>(t, sm, lt);
 }
 
 template <int W, int NT>
 __global__ __launch_bounds__(64 * W) void k_w8a16_sk_grouped(const W8A16GroupEntry *__restrict__ tab,
                                                              int count) {
   __shared__ __attribute__((aligned(16))) SkLds<W, NT> sm;
-  w8a16_tile_sk<W, NT>(group_tile(tab, count, 16 * NT), sm);
+  w8a16_tile_sk<W, NT>(group_tile(tab, count, 16 * NT), sm, NoLora{});
 }
 
 // Skinny tile with x shared through LDS (row blocks of 16, N >= kW8A16ShareMinN).
@@ -1037,13 +1037,13 @@ struct ShLds {
 
 // part == nullptr: the whole K, y written. Else split blockIdx.z takes steps
 // [z spl, (z + 1) spl) and writes its unscaled sums to part[z][M][N] (fp32).
-template <int WC, int WK>
+template <int WC, int WK, class LT>
 __global__ __launch_bounds__(64 * WC * WK) void k_w8a16_sksh(const uint16_t *__restrict__ x, int64_t M,
                                                              int64_t K, const int8_t *__restrict__ q,
                                                              const float *__restrict__ scale,
                                                              const uint16_t *__restrict__ bias,
                                                              int64_t N, uint16_t *__restrict__ y,
-                                                             float *__restrict__ part, int spl) {
+                                                             float *__restrict__ part, int spl, LT lt) {
   static_assert(8 % WC == 0, "x pieces split over a range's waves");
   __shared__ __attribute__((aligned(16))) ShLds<WC, WK> sm;
   const int lane = threadIdx.x & 63;
@@ -1162,22 +1162,22 @@ __global__ __launch_bounds__(64 * WC * WK) void k_w8a16_sksh(const uint16_t *__r
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     const int64_t mm = m0 + 4 * g + v;
-    if (mm < M) y[mm * N + n] = f32_to_bf16_rne(s * acc[v] + bv);
+    if (mm < M) y[mm * N + n] = f32_to_bf16_rne(lt.add(mm, n, s * acc[v] + bv));
   }
 }
 
 // Single-row tile; dynamic LDS holds x when XL.
-template <int W, int CW, bool XL>
+template <int W, int CW, bool XL, class LT>
 __global__ __launch_bounds__(64 * W * CW, 4) void k_w8a16_m1(const uint16_t *__restrict__ x,
                                                           int64_t K,
                                                           const int8_t *__restrict__ q,
                                                           const float *__restrict__ scale,
                                                           const uint16_t *__restrict__ bias,
-                                                          int64_t N, uint16_t *__restrict__ y) {
+                                                          int64_t N, uint16_t *__restrict__ y, LT lt) {
   __shared__ Red<W * CW, M1_TG, 0> red;
   extern __shared__ __attribute__((aligned(16))) uint8_t xs[];
   const Tile t{x, q, scale, bias, y, 1, N, K, (int64_t)blockIdx.x * 4 * M1_TG * CW, 0};
-  w8a16_tile_m1<W, CW, M1_TG, M1_U, XL>(t, red, xs);
+  w8a16_tile_m1<W, CW, M1_TG, M1_U, XL>(t, red, xs, lt);
 }
 
 template <int W, int CW, bool XL>
@@ -1185,7 +1185,7 @@ __global__ __launch_bounds__(64 * W * CW, 4) void k_w8a16_m1_grouped(
     const W8A16GroupEntry *__restrict__ tab, int count) {
   __shared__ Red<W * CW, M1_TG, 0> red;
   extern __shared__ __attribute__((aligned(16))) uint8_t xs[];
-  w8a16_tile_m1<W, CW, M1_TG, M1_U, XL>(group_tile(tab, count, 4 * M1_TG * CW), red, xs);
+  w8a16_tile_m1<W, CW, M1_TG, M1_U, XL>(group_tile(tab, count, 4 * M1_TG * CW), red, xs, NoLora{});
 }
 
 template <int TG, int MB>
@@ -1216,21 +1216,21 @@ void launch_group(int W, int blocks, hipStream_t st, const W8A16GroupEntry *tab,
   }
 }
 
-template <int NT>
+template <int NT, class LT>
 void launch_sk_single(int W, dim3 grid, hipStream_t st, const uint16_t *x, int64_t M, int64_t K,
                       const int8_t *q, const float *scale, const uint16_t *bias, int64_t N,
-                      uint16_t *y) {
+                      uint16_t *y, const LT &lt) {
   switch (W) {
 #define AQL_W(w)                                                                              \
   case w:                                                                                     \
-    hipLaunchKernelGGL((k_w8a16_sk<w, NT>), grid, dim3(64 * w), 0, st, x, M, K, q, scale, bias, \
-                       N, y);                                                                 \
+    hipLaunchKernelGGL((k_w8a16_sk<w, NT, LT>), grid, dim3(64 * w), 0, st, x, M, K, q, scale, \
+                       bias, N, y, lt);                                                       \
     break;
     AQL_W(8) AQL_W(4) AQL_W(2) AQL_W(1)
 #undef AQL_W
     default:  // 16 waves (32 channels would not fit the registers of 1024 threads)
-      hipLaunchKernelGGL((k_w8a16_sk<NT == 1 ? 16 : 8, NT>), grid, dim3(NT == 1 ? 1024 : 512), 0,
-                         st, x, M, K, q, scale, bias, N, y);
+      hipLaunchKernelGGL((k_w8a16_sk<NT == 1 ? 16 : 8, NT, LT>), grid, dim3(NT == 1 ? 1024 : 512),
+                         0, st, x, M, K, q, scale, bias, N, y, lt);
       break;
   }
 }
@@ -1348,26 +1348,40 @@ int w8a16_xlds_bytes(int64_t K) {
   return b <= kW8A16MaxXlds ? (int)b : 0;
 }
 
-hipError_t launch_w8a16_shape(const W8A16Shape &sh, const uint16_t *x, int64_t M, int64_t K,
-                              const int8_t *q, const float *scale, const uint16_t *bias,
-                              int64_t N, uint16_t *y, hipStream_t st) {
+namespace {
+
+// The single-row tile and the skinny tile, with or without adapters.
+template <class LT>
+hipError_t launch_m1_or_sk(const W8A16Shape &sh, const uint16_t *x, int64_t M, int64_t K,
+                           const int8_t *q, const float *scale, const uint16_t *bias, int64_t N,
+                           uint16_t *y, hipStream_t st, const LT &lt) {
   if (sh.mblocks == 0) {
     if (M != 1 || !m1_shape_ok(sh) || (sh.xlds && sh.xlds < 2 * K)) return hipErrorInvalidValue;
     const int64_t rows = 4 * M1_TG * sh.cgroups;
     const dim3 grid((unsigned)((N + rows - 1) / rows)), block(64 * sh.waves * sh.cgroups);
     m1_dispatch(sh.waves, sh.cgroups, sh.xlds > 0, [&](auto w, auto c, auto xl) {
-      hipLaunchKernelGGL((k_w8a16_m1<decltype(w)::value, decltype(c)::value, decltype(xl)::value>),
-                         grid, block, sh.xlds, st, x, K, q, scale, bias, N, y);
+      hipLaunchKernelGGL(
+          (k_w8a16_m1<decltype(w)::value, decltype(c)::value, decltype(xl)::value, LT>), grid,
+          block, sh.xlds, st, x, K, q, scale, bias, N, y, lt);
     });
     return hipGetLastError();
   }
   const int64_t rows = 4 * sh.tgroups;
   const dim3 grid((unsigned)((N + rows - 1) / rows), (unsigned)((M + 15) / 16));
-  if (sh.mblocks == kW8A16Skinny) {
-    if (sh.tgroups == 8) launch_sk_single<2>(sh.waves, grid, st, x, M, K, q, scale, bias, N, y);
-    else launch_sk_single<1>(sh.waves, grid, st, x, M, K, q, scale, bias, N, y);
-    return hipGetLastError();
-  }
+  if (sh.tgroups == 8) launch_sk_single<2>(sh.waves, grid, st, x, M, K, q, scale, bias, N, y, lt);
+  else launch_sk_single<1>(sh.waves, grid, st, x, M, K, q, scale, bias, N, y, lt);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_w8a16_shape(const W8A16Shape &sh, const uint16_t *x, int64_t M, int64_t K,
+                              const int8_t *q, const float *scale, const uint16_t *bias,
+                              int64_t N, uint16_t *y, hipStream_t st) {
+  if (sh.mblocks == 0 || sh.mblocks == kW8A16Skinny)
+    return launch_m1_or_sk(sh, x, M, K, q, scale, bias, N, y, st, NoLora{});
+  const int64_t rows = 4 * sh.tgroups;
+  const dim3 grid((unsigned)((N + rows - 1) / rows), (unsigned)((M + 15) / 16));
   switch (sh.tgroups) {
     case 1: launch_single_tg<1>(sh.mblocks, sh.waves, grid, st, x, M, K, q, scale, bias, N, y); break;
     case 2: launch_single_tg<2>(sh.mblocks, sh.waves, grid, st, x, M, K, q, scale, bias, N, y); break;
@@ -1376,8 +1390,11 @@ hipError_t launch_w8a16_shape(const W8A16Shape &sh, const uint16_t *x, int64_t M
   return hipGetLastError();
 }
 
-hipError_t launch_w8a16_m1c(const uint16_t *x, int64_t K, const int8_t *q, const float *scale,
-                            const uint16_t *bias, int64_t N, uint16_t *y, hipStream_t st) {
+namespace {
+
+template <class LT>
+hipError_t launch_m1c(const uint16_t *x, int64_t K, const int8_t *q, const float *scale,
+                      const uint16_t *bias, int64_t N, uint16_t *y, hipStream_t st, const LT &lt) {
   if (K < kW8A16ContigMinK || K > kW8A16ContigMaxK || K % 16) return hipErrorInvalidValue;
   const dim3 grid((unsigned)((N + 7) / 8));
   // 4 waves split K, each with one or two pieces of 1 KB per row; one piece
@@ -1386,12 +1403,19 @@ hipError_t launch_w8a16_m1c(const uint16_t *x, int64_t K, const int8_t *q, const
   // over the same 58.7 MB takes 10.39 us). A grid of at most one workgroup a
   // CU is bound by latency, not by the stream: its 8 loads go out at once.
   if (K <= 4096 && grid.x <= 256)
-    hipLaunchKernelGGL((k_w8a16_m1c<4, 1, 8>), grid, dim3(256), 0, st, x, K, q, scale, bias, N, y);
+    hipLaunchKernelGGL((k_w8a16_m1c<4, 1, 8, LT>), grid, dim3(256), 0, st, x, K, q, scale, bias, N, y, lt);
   else if (K <= 4096)
-    hipLaunchKernelGGL((k_w8a16_m1c<4, 1, 2>), grid, dim3(256), 0, st, x, K, q, scale, bias, N, y);
+    hipLaunchKernelGGL((k_w8a16_m1c<4, 1, 2, LT>), grid, dim3(256), 0, st, x, K, q, scale, bias, N, y, lt);
   else
-    hipLaunchKernelGGL((k_w8a16_m1c<4, 2>), grid, dim3(256), 0, st, x, K, q, scale, bias, N, y);
+    hipLaunchKernelGGL((k_w8a16_m1c<4, 2, 4, LT>), grid, dim3(256), 0, st, x, K, q, scale, bias, N, y, lt);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_w8a16_m1c(const uint16_t *x, int64_t K, const int8_t *q, const float *scale,
+                            const uint16_t *bias, int64_t N, uint16_t *y, hipStream_t st) {
+  return launch_m1c(x, K, q, scale, bias, N, y, st, NoLora{});
 }
 
 hipError_t launch_w8a16_m1p_grouped(const W8A16GroupEntry *dev_tab, const W8A16GroupEntry *host_tab,
@@ -1412,26 +1436,37 @@ hipError_t launch_w8a16_m1p_grouped(const W8A16GroupEntry *dev_tab, const W8A16G
   return hipGetLastError();
 }
 
-hipError_t launch_w8a16_mfew(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
-                             const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
-                             hipStream_t st) {
+namespace {
+
+template <class LT>
+hipError_t launch_mfew(const uint16_t *x, int64_t M, int64_t K, const int8_t *q, const float *scale,
+                       const uint16_t *bias, int64_t N, uint16_t *y, hipStream_t st,
+                       const LT &lt) {
   if (M < 2 || M > kW8A16FewMaxM || K < kW8A16FewMinK || K > kW8A16FewMaxK || K % 16)
     return hipErrorInvalidValue;
   const dim3 grid((unsigned)((N + 7) / 8));
   auto go = [&](auto kern, int W) {
-    hipLaunchKernelGGL(kern, grid, dim3(64 * W), 0, st, x, M, K, q, scale, bias, N, y);
+    hipLaunchKernelGGL(kern, grid, dim3(64 * W), 0, st, x, M, K, q, scale, bias, N, y, lt);
   };
   // waves split K so that each keeps one or two pieces of 1 KB per row
   if (M == 2) {
-    if (K <= 4096) go(k_w8a16_mfew<4, 1, 2>, 4);
-    else if (K <= 8192) go(k_w8a16_mfew<4, 2, 2>, 4);
-    else go(k_w8a16_mfew<8, 2, 2>, 8);
+    if (K <= 4096) go(k_w8a16_mfew<4, 1, 2, LT>, 4);
+    else if (K <= 8192) go(k_w8a16_mfew<4, 2, 2, LT>, 4);
+    else go(k_w8a16_mfew<8, 2, 2, LT>, 8);
   } else {
-    if (K <= 4096) go(k_w8a16_mfew<4, 1, 4>, 4);
-    else if (K <= 8192) go(k_w8a16_mfew<4, 2, 4>, 4);
-    else go(k_w8a16_mfew<8, 2, 4>, 8);
+    if (K <= 4096) go(k_w8a16_mfew<4, 1, 4, LT>, 4);
+    else if (K <= 8192) go(k_w8a16_mfew<4, 2, 4, LT>, 4);
+    else go(k_w8a16_mfew<8, 2, 4, LT>, 8);
   }
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_w8a16_mfew(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
+                             const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
+                             hipStream_t st) {
+  return launch_mfew(x, M, K, q, scale, bias, N, y, st, NoLora{});
 }
 
 int w8a16_skinny_splits(int64_t M, int64_t N, int64_t K) {
@@ -1445,13 +1480,16 @@ size_t w8a16_skinny_part_bytes(int64_t M, int64_t N, int64_t K) {
   return S > 1 ? (size_t)S * (size_t)M * (size_t)N * 4 : 0;
 }
 
-hipError_t launch_w8a16(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
-                        const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
-                        float *part, size_t part_bytes, hipStream_t st) {
+namespace {
+
+template <class LT>
+hipError_t launch_stream(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
+                         const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
+                         float *part, size_t part_bytes, hipStream_t st, const LT &lt) {
   if (M == 1 && K >= kW8A16ContigMinK && K <= kW8A16ContigMaxK)
-    return launch_w8a16_m1c(x, K, q, scale, bias, N, y, st);
+    return launch_m1c(x, K, q, scale, bias, N, y, st, lt);
   if (M >= 2 && M <= kW8A16FewMaxM && K >= kW8A16FewMinK && K <= kW8A16FewMaxK)
-    return launch_w8a16_mfew(x, M, K, q, scale, bias, N, y, st);
+    return launch_mfew(x, M, K, q, scale, bias, N, y, st, lt);
   if (M >= kW8A16SkinnyMinM && N >= kW8A16ShareMinN) {
     // 64 channels a workgroup; one K range for rows of up to 4 KiB once there
     // are 192 workgroups a row block, else two (M = 16: K = 4096, N = 14336:
@@ -1459,9 +1497,9 @@ hipError_t launch_w8a16(const uint16_t *x, int64_t M, int64_t K, const int8_t *q
     // K = N = 8192: 20.0 vs 22.4)
     const dim3 grid((unsigned)((N + 63) / 64), (unsigned)((M + 15) / 16));
     if (N >= 12288 && K <= 4096)
-      hipLaunchKernelGGL((k_w8a16_sksh<4, 1>), grid, dim3(256), 0, st, x, M, K, q, scale, bias, N, y, nullptr, 0);
+      hipLaunchKernelGGL((k_w8a16_sksh<4, 1, LT>), grid, dim3(256), 0, st, x, M, K, q, scale, bias, N, y, nullptr, 0, lt);
     else
-      hipLaunchKernelGGL((k_w8a16_sksh<4, 2>), grid, dim3(512), 0, st, x, M, K, q, scale, bias, N, y, nullptr, 0);
+      hipLaunchKernelGGL((k_w8a16_sksh<4, 2, LT>), grid, dim3(512), 0, st, x, M, K, q, scale, bias, N, y, nullptr, 0, lt);
     return hipGetLastError();
   }
   const int S = w8a16_skinny_splits(M, N, K);
@@ -1473,13 +1511,32 @@ hipError_t launch_w8a16(const uint16_t *x, int64_t M, int64_t K, const int8_t *q
     const int spl = (nst + S - 1) / S;
     const int splits = (nst + spl - 1) / spl;
     const dim3 grid((unsigned)((N + 63) / 64), (unsigned)((M + 15) / 16), (unsigned)splits);
-    hipLaunchKernelGGL((k_w8a16_sksh<4, 1>), grid, dim3(256), 0, st, x, M, K, q, scale, bias, N, y,
-                       part, spl);
+    hipLaunchKernelGGL((k_w8a16_sksh<4, 1, LT>), grid, dim3(256), 0, st, x, M, K, q, scale, bias, N, y,
+                       part, spl, lt);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    return launch_w8a16_splitk_reduce(part, splits, M, N, scale, bias, y, st);
+    return launch_w8a16_splitk_reduce(part, splits, M, N, scale, bias, y, st, lt);
   }
-  return launch_w8a16_shape(w8a16_shape(M, N, K), x, M, K, q, scale, bias, N, y, st);
+  if constexpr (LT::on)
+    // two or three rows take the skinny tile too (the 4-row tile has no adapter form)
+    return launch_m1_or_sk(w8a16_shape(M > 1 && M < kW8A16SkinnyMinM ? kW8A16SkinnyMinM : M, N, K),
+                           x, M, K, q, scale, bias, N, y, st, lt);
+  else
+    return launch_w8a16_shape(w8a16_shape(M, N, K), x, M, K, q, scale, bias, N, y, st);
+}
+
+}  // namespace
+
+hipError_t launch_w8a16(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
+                        const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
+                        float *part, size_t part_bytes, hipStream_t st) {
+  return launch_stream(x, M, K, q, scale, bias, N, y, part, part_bytes, st, NoLora{});
+}
+
+hipError_t launch_w8a16(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
+                        const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
+                        float *part, size_t part_bytes, hipStream_t st, const LoraTerm &lt) {
+  return launch_stream(x, M, K, q, scale, bias, N, y, part, part_bytes, st, lt);
 }
 
 hipError_t launch_w8a16_grouped(const W8A16GroupEntry *dev_tab, int count, int total_blocks,

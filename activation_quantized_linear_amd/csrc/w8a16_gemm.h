@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "lora.h"
+
 namespace aql {
 
 // K splits of the wide tile this shape takes when a workspace is given (1:
@@ -18,7 +20,10 @@ size_t w8a16_gemm_part_bytes(int64_t M, int64_t N, int64_t K);
 // the partial sums (fp32, S x M x N) added in split order.
 hipError_t launch_w8a16_splitk_reduce(const float *part, int S, int64_t M, int64_t N,
                                       const float *scale, const uint16_t *bias, uint16_t *y,
-                                      hipStream_t st);
+                                      hipStream_t st, const NoLora &lt = NoLora{});
+hipError_t launch_w8a16_splitk_reduce(const float *part, int S, int64_t M, int64_t N,
+                                      const float *scale, const uint16_t *bias, uint16_t *y,
+                                      hipStream_t st, const LoraTerm &lt);
 
 // y[M, N] bf16 = scale[n] * x[M, K] bf16 . q[N, K]^T int8 (+ bias[n] bf16);
 // K <= 2^22 (32-bit buffer offsets of a 128-row tile of x). part (may be
@@ -27,5 +32,9 @@ hipError_t launch_w8a16_splitk_reduce(const float *part, int S, int64_t M, int64
 hipError_t launch_w8a16_gemm(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
                              const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
                              float *part, size_t part_bytes, hipStream_t st);
+// The same with every row's adapter term added before the rounding.
+hipError_t launch_w8a16_gemm(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
+                             const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
+                             float *part, size_t part_bytes, hipStream_t st, const LoraTerm &lt);
 
 }  // namespace aql

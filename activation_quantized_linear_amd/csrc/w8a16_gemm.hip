@@ -104,11 +104,11 @@ struct GemmLds {
 // RAG: K is not a multiple of 64, so the last stage is partial and every load
 // checks its chunk against the row end; otherwise the k advance of a load is a
 // uniform (scalar) offset and costs no vector instruction.
-template <int WM, int TI, int SG, int KP, bool RAG>
+template <int WM, int TI, int SG, int KP, bool RAG, class LT>
 __global__ __launch_bounds__((64 * GemmLds<WM, TI, SG, KP>::NW)) void k_w8a16_gemm(
     const uint16_t *__restrict__ x, const int8_t *__restrict__ q, const float *__restrict__ scale,
     const uint16_t *__restrict__ bias, uint16_t *__restrict__ y, int64_t M, int64_t N, int64_t K,
-    int tiles_m, int tiles_n) {
+    int tiles_m, int tiles_n, LT lt) {
   using L = GemmLds<WM, TI, SG, KP>;
   constexpr int BM = L::BM, NG = L::NG, NW = L::NW, PS = L::PS, NXL = L::NXL;
   constexpr int NL = L::NXL + L::NWL;
@@ -301,7 +301,34 @@ __global__ __launch_bounds__((64 * GemmLds<WM, TI, SG, KP>::NW)) void k_w8a16_ge
   }
   __syncthreads();
   uint16_t *tl = reinterpret_cast<uint16_t *>(smem + L::XCH);
-  if (part == 0) {
+  if constexpr (LT::on) {
+    if (part == 0) {  // the same sums in place, then the adapter terms
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t n = n0 + wn * 64 + j * 16 + r;
+        const float s = n < N ? scale[n] : 0.0f;
+        const float b = (n < N && bias) ? bf16_to_f32(bias[n]) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < TI; ++i) {
+          f32x4 v4 = acc[i][j];
+#pragma unroll
+          for (int pp = 1; pp < 2 * KP; ++pp)
+            v4 += xch[(((pp - 1) * 2 * L::WMW + blk) * 4 * TI + i * 4 + j) * 64 + lane];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[i][j][v] = s * v4[v] + b;
+        }
+      }
+      lora_add_tile<false>(acc, lt, m0 + wm * 16 * TI, M, n0 + wn * 64);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            tl[(wm * 16 * TI + i * 16 + 4 * g + v) * L::TLD + wn * 64 + j * 16 + r] =
+                f32_to_bf16_rne(acc[i][j][v]);
+    }
+  } else if (part == 0) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int col = wn * 64 + j * 16 + r;
@@ -374,7 +401,7 @@ struct WideLds {
 // of 4 x 3584 k instead of 256 tiles of 64 x 128 over the whole row), where
 // every CU otherwise streams the whole of K for a small tile: the operand
 // bytes per CU halve.
-template <int SG, bool SPLIT>
+template <int SG, bool SPLIT, class LT>
 __global__ __launch_bounds__(512, SG == 2 ? 4 : 2) void k_w8a16_gemm_wide(const uint16_t *__restrict__ x,
                                                          const int8_t *__restrict__ q,
                                                          const float *__restrict__ scale,
@@ -382,7 +409,7 @@ __global__ __launch_bounds__(512, SG == 2 ? 4 : 2) void k_w8a16_gemm_wide(const 
                                                          uint16_t *__restrict__ y, int64_t M,
                                                          int64_t N, int64_t K, int tiles_m,
                                                          int tiles_n, float *__restrict__ part,
-                                                         int ks) {
+                                                         int ks, LT lt) {
   using L = WideLds<SG>;
   constexpr int BM = L::BM, BNW = L::BNW, NL = 4;  // loads per wave per stage
   extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -557,17 +584,31 @@ __global__ __launch_bounds__(512, SG == 2 ? 4 : 2) void k_w8a16_gemm_wide(const 
   // scale + bias + bf16 into the LDS output tile; acc[i][j] lane holds
   // D[4g + v][r] of MFMA tile (i, j): row m, column n.
   uint16_t *tl = reinterpret_cast<uint16_t *>(smem);
+  if constexpr (LT::on) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t n = n0 + wn * 32 + j * 16 + r;
+      const float s = n < N ? scale[n] : 0.0f;
+      const float b = (n < N && bias) ? bf16_to_f32(bias[n]) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][j][v] = s * acc[i][j][v] + b;
+    }
+    lora_add_tile<false>(acc, lt, m0, M, n0 + wn * 32);
+  }
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int col = wn * 32 + j * 16 + r;
     const int64_t n = n0 + col;
-    const float s = n < N ? scale[n] : 0.0f;
-    const float b = (n < N && bias) ? bf16_to_f32(bias[n]) : 0.0f;
+    const float s = LT::on ? 1.0f : n < N ? scale[n] : 0.0f;
+    const float b = (!LT::on && n < N && bias) ? bf16_to_f32(bias[n]) : 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        tl[(i * 16 + 4 * g + v) * L::TLD + col] = f32_to_bf16_rne(s * acc[i][j][v] + b);
+        tl[(i * 16 + 4 * g + v) * L::TLD + col] =
+            f32_to_bf16_rne(LT::on ? acc[i][j][v] : s * acc[i][j][v] + b);
   }
   __syncthreads();
   // 32 lanes x 16 B per 512-byte row
@@ -593,11 +634,12 @@ __global__ __launch_bounds__(512, SG == 2 ? 4 : 2) void k_w8a16_gemm_wide(const 
 // the sum in split order; a thread takes 4 consecutive outputs of a row (one
 // 16-byte load per split: 4.4 us for S = 4 at M = 512, N = 4096, against 9.5
 // with 8 outputs a thread).
+template <class LT>
 __global__ __launch_bounds__(256) void k_w8a16_splitk_reduce(const float *__restrict__ part, int S,
                                                             int64_t M, int64_t N,
                                                             const float *__restrict__ scale,
                                                             const uint16_t *__restrict__ bias,
-                                                            uint16_t *__restrict__ y) {
+                                                            uint16_t *__restrict__ y, LT lt) {
   const int64_t ng = (N + 3) / 4;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= M * ng) return;
@@ -633,7 +675,7 @@ __global__ __launch_bounds__(256) void k_w8a16_splitk_reduce(const float *__rest
   for (int e = 0; e < 4; ++e) {
     const int64_t nn = n + (e < cnt ? e : 0);
     const float b = bias ? bf16_to_f32(bias[nn]) : 0.0f;
-    out[e] = f32_to_bf16_rne(scale[nn] * acc[e] + b);
+    out[e] = f32_to_bf16_rne(lt.add(m, nn, scale[nn] * acc[e] + b));
   }
   uint16_t *dst = y + m * N + n;
   if (vec) {
@@ -645,45 +687,58 @@ __global__ __launch_bounds__(256) void k_w8a16_splitk_reduce(const float *__rest
   }
 }
 
+template <class LT>
+hipError_t launch_reduce(const float *part, int S, int64_t M, int64_t N, const float *scale,
+                         const uint16_t *bias, uint16_t *y, hipStream_t st, const LT &lt) {
+  const int64_t groups = M * ((N + 3) / 4);
+  hipLaunchKernelGGL(k_w8a16_splitk_reduce<LT>, dim3((unsigned)((groups + 255) / 256)), dim3(256),
+                     0, st, part, S, M, N, scale, bias, y, lt);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_w8a16_splitk_reduce(const float *part, int S, int64_t M, int64_t N,
                                       const float *scale, const uint16_t *bias, uint16_t *y,
-                                      hipStream_t st) {
-  const int64_t groups = M * ((N + 3) / 4);
-  hipLaunchKernelGGL(k_w8a16_splitk_reduce, dim3((unsigned)((groups + 255) / 256)), dim3(256), 0,
-                     st, part, S, M, N, scale, bias, y);
-  return hipGetLastError();
+                                      hipStream_t st, const NoLora &lt) {
+  return launch_reduce(part, S, M, N, scale, bias, y, st, lt);
+}
+
+hipError_t launch_w8a16_splitk_reduce(const float *part, int S, int64_t M, int64_t N,
+                                      const float *scale, const uint16_t *bias, uint16_t *y,
+                                      hipStream_t st, const LoraTerm &lt) {
+  return launch_reduce(part, S, M, N, scale, bias, y, st, lt);
 }
 
 namespace {
 
-template <int SG>
+template <int SG, class LT>
 hipError_t launch_wide(const uint16_t *x, int64_t M, int64_t K, const int8_t *q, const float *scale,
-                       const uint16_t *bias, int64_t N, uint16_t *y, hipStream_t st) {
+                       const uint16_t *bias, int64_t N, uint16_t *y, hipStream_t st, const LT &lt) {
   using L = WideLds<SG>;
   static bool attr_set = false;
   if (!attr_set) {  // more than 64 KB of dynamic LDS; a launch the limit refuses reports itself
-    (void)hipFuncSetAttribute((const void *)k_w8a16_gemm_wide<SG, false>,
+    (void)hipFuncSetAttribute((const void *)k_w8a16_gemm_wide<SG, false, LT>,
                               hipFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
     (void)hipGetLastError();
     attr_set = true;
   }
   const int tiles_m = (int)((M + L::BM - 1) / L::BM), tiles_n = (int)((N + L::BNW - 1) / L::BNW);
-  hipLaunchKernelGGL((k_w8a16_gemm_wide<SG, false>), dim3((unsigned)(tiles_m * tiles_n)), dim3(512),
-                     L::BYTES, st, x, q, scale, bias, y, M, N, K, tiles_m, tiles_n, nullptr, 0);
+  hipLaunchKernelGGL((k_w8a16_gemm_wide<SG, false, LT>), dim3((unsigned)(tiles_m * tiles_n)), dim3(512),
+                     L::BYTES, st, x, q, scale, bias, y, M, N, K, tiles_m, tiles_n, nullptr, 0, lt);
   return hipGetLastError();
 }
 
 // The wide tile over S splits of K into part (S M N floats), then the sum.
+template <class LT>
 hipError_t launch_wide_split(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
                              const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
-                             float *part, int S, hipStream_t st) {
+                             float *part, int S, hipStream_t st, const LT &lt) {
   constexpr int SG = 4;
   using L = WideLds<SG>;
   static bool attr_set = false;
   if (!attr_set) {
-    (void)hipFuncSetAttribute((const void *)k_w8a16_gemm_wide<SG, true>,
+    (void)hipFuncSetAttribute((const void *)k_w8a16_gemm_wide<SG, true, NoLora>,
                               hipFuncAttributeMaxDynamicSharedMemorySize, L::BYTES_SPLIT);
     (void)hipGetLastError();
     attr_set = true;
@@ -693,35 +748,36 @@ hipError_t launch_wide_split(const uint16_t *x, int64_t M, int64_t K, const int8
   int ks = (nk + S - 1) / S;
   ks = (ks + SG - 1) / SG * SG;  // whole turns of the ring
   const int splits = (nk + ks - 1) / ks;
-  hipLaunchKernelGGL((k_w8a16_gemm_wide<SG, true>), dim3((unsigned)(tiles_m * tiles_n * splits)),
+  hipLaunchKernelGGL((k_w8a16_gemm_wide<SG, true, NoLora>), dim3((unsigned)(tiles_m * tiles_n * splits)),
                      dim3(512), L::BYTES_SPLIT, st, x, q, scale, bias, y, M, N, K, tiles_m,
-                     tiles_n, part, ks);
-  return launch_w8a16_splitk_reduce(part, splits, M, N, scale, bias, y, st);
+                     tiles_n, part, ks, NoLora{});
+  return launch_reduce(part, splits, M, N, scale, bias, y, st, lt);
 }
 
-template <int WM, int TI, int SG, int KP, bool RAG>
+template <int WM, int TI, int SG, int KP, bool RAG, class LT>
 hipError_t launch_wm_k(const uint16_t *x, int64_t M, int64_t K, const int8_t *q, const float *scale,
-                     const uint16_t *bias, int64_t N, uint16_t *y, hipStream_t st) {
+                       const uint16_t *bias, int64_t N, uint16_t *y, hipStream_t st, const LT &lt) {
   using L = GemmLds<WM, TI, SG, KP>;
   static bool attr_set = false;
   if (!attr_set) {  // more than 64 KB of dynamic LDS; a launch the limit refuses reports itself
-    (void)hipFuncSetAttribute((const void *)k_w8a16_gemm<WM, TI, SG, KP, RAG>,
+    (void)hipFuncSetAttribute((const void *)k_w8a16_gemm<WM, TI, SG, KP, RAG, LT>,
                               hipFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
     (void)hipGetLastError();
     attr_set = true;
   }
   const int tiles_m = (int)((M + L::BM - 1) / L::BM), tiles_n = (int)((N + BN - 1) / BN);
-  hipLaunchKernelGGL((k_w8a16_gemm<WM, TI, SG, KP, RAG>), dim3((unsigned)(tiles_m * tiles_n)),
+  hipLaunchKernelGGL((k_w8a16_gemm<WM, TI, SG, KP, RAG, LT>), dim3((unsigned)(tiles_m * tiles_n)),
                      dim3(64 * L::NW), L::BYTES, st, x, q, scale, bias, y, M, N, K, tiles_m,
-                     tiles_n);
+                     tiles_n, lt);
   return hipGetLastError();
 }
 
-template <int WM, int TI, int SG, int KP>
+template <int WM, int TI, int SG, int KP, class LT>
 hipError_t launch_wm(const uint16_t *x, int64_t M, int64_t K, const int8_t *q, const float *scale,
-                     const uint16_t *bias, int64_t N, uint16_t *y, hipStream_t st) {
-  if (K % BK == 0) return launch_wm_k<WM, TI, SG, KP, false>(x, M, K, q, scale, bias, N, y, st);
-  return launch_wm_k<WM, TI, SG, KP, true>(x, M, K, q, scale, bias, N, y, st);
+                     const uint16_t *bias, int64_t N, uint16_t *y, hipStream_t st, const LT &lt) {
+  if (K % BK == 0)
+    return launch_wm_k<WM, TI, SG, KP, false>(x, M, K, q, scale, bias, N, y, st, lt);
+  return launch_wm_k<WM, TI, SG, KP, true>(x, M, K, q, scale, bias, N, y, st, lt);
 }
 
 }  // namespace
@@ -740,6 +796,8 @@ size_t w8a16_gemm_part_bytes(int64_t M, int64_t N, int64_t K) {
   return S > 1 ? (size_t)S * (size_t)M * (size_t)N * 4 : 0;
 }
 
+namespace {
+
 // Few wide tiles and long rows (a workspace given): the wide tile over K
 // splits, then the sum (M = 512, N = 4096, K = 14336: 76 vs 89 us; M = 128:
 // 37 vs 82 us; rotated weights). Else 128 x 256 tiles from 160 of them on
@@ -747,18 +805,33 @@ size_t w8a16_gemm_part_bytes(int64_t M, int64_t N, int64_t K) {
 // workgroups a CU from 512 on; else 128 x 128 tiles when those fill the CUs,
 // else 64 x 128 tiles with two stage groups and an 8-stage ring (measured at
 // M = 512, K = 14336, N = 4096: 74 us against 95 us for one group of 4 waves).
+template <class LT>
+hipError_t launch_gemm(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
+                       const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
+                       float *part, size_t part_bytes, hipStream_t st, const LT &lt) {
+  const int S = w8a16_gemm_splits(M, N, K);
+  if (S > 1 && part && part_bytes >= w8a16_gemm_part_bytes(M, N, K))
+    return launch_wide_split(x, M, K, q, scale, bias, N, y, part, S, st, lt);
+  const int64_t twide = ((M + 127) / 128) * ((N + 255) / 256);
+  if (twide >= 512) return launch_wide<2>(x, M, K, q, scale, bias, N, y, st, lt);
+  if (twide >= 160) return launch_wide<4>(x, M, K, q, scale, bias, N, y, st, lt);
+  const int64_t t128 = ((M + 127) / 128) * ((N + BN - 1) / BN);
+  if (t128 >= 256) return launch_wm<2, 4, 4, 1>(x, M, K, q, scale, bias, N, y, st, lt);
+  return launch_wm<1, 4, 8, 2>(x, M, K, q, scale, bias, N, y, st, lt);
+}
+
+}  // namespace
+
 hipError_t launch_w8a16_gemm(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
                              const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
                              float *part, size_t part_bytes, hipStream_t st) {
-  const int S = w8a16_gemm_splits(M, N, K);
-  if (S > 1 && part && part_bytes >= w8a16_gemm_part_bytes(M, N, K))
-    return launch_wide_split(x, M, K, q, scale, bias, N, y, part, S, st);
-  const int64_t twide = ((M + 127) / 128) * ((N + 255) / 256);
-  if (twide >= 512) return launch_wide<2>(x, M, K, q, scale, bias, N, y, st);
-  if (twide >= 160) return launch_wide<4>(x, M, K, q, scale, bias, N, y, st);
-  const int64_t t128 = ((M + 127) / 128) * ((N + BN - 1) / BN);
-  if (t128 >= 256) return launch_wm<2, 4, 4, 1>(x, M, K, q, scale, bias, N, y, st);
-  return launch_wm<1, 4, 8, 2>(x, M, K, q, scale, bias, N, y, st);
+  return launch_gemm(x, M, K, q, scale, bias, N, y, part, part_bytes, st, NoLora{});
+}
+
+hipError_t launch_w8a16_gemm(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
+                             const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
+                             float *part, size_t part_bytes, hipStream_t st, const LoraTerm &lt) {
+  return launch_gemm(x, M, K, q, scale, bias, N, y, part, part_bytes, st, lt);
 }
 
 }  // namespace aql

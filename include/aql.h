@@ -72,6 +72,15 @@ extern "C" {
 #define AQL_OP_DQ8CA 2      /* workspace of aql_linear_dq8ca */
 #define AQL_OP_GPTQ_INT8 3  /* workspace of aql_gptq_int8 (M = the column block) */
 #define AQL_OP_W8A16 4      /* optional workspace of aql_linear_w8a16 (0: none used) */
+#define AQL_OP_W8A16_DGRAD 5 /* optional workspace of aql_linear_w8a16_dgrad (0: none used) */
+
+/* Bounds of the low-rank adapters: rank R a multiple of 8 up to
+ * AQL_LORA_MAX_RANK, at most AQL_LORA_MAX_ADAPTERS stacked adapters. */
+#define AQL_LORA_MAX_RANK 128
+#define AQL_LORA_MAX_ADAPTERS 1024
+
+/* Values of a row that share one scale in an 8-bit activation checkpoint. */
+#define AQL_CKPT_GROUP 128
 
 /* Largest K accepted by the int8 paths: keeps |sum_k (xq - z) q| below 2^31. */
 #define AQL_MAX_K_INT8 65536
@@ -328,6 +337,122 @@ int aql_w8a16_group_plan(const aql_w8a16_problem *problems, int count, void *tab
  * (they travel in the kernel arguments); larger groups read dev_table when
  * the kernel runs. Both tables must describe the same plan. */
 int aql_linear_w8a16_grouped(const void *table, const void *dev_table, void *stream);
+
+/* ------------------------------------------------------- low-rank adapters */
+
+/*
+ * Low-rank adapters beside the frozen W8A16 linear: many requests, each with
+ * its own adapter or none, in one call (serving), and the gradients of the
+ * adapters and of the input through the int8 weights (training).
+ *
+ * Adapters are stacked: A [L, R, K] bf16, B [L, N, R] bf16, alpha [L] float32;
+ * row m of a batch belongs to adapter a = idx[m], and a value of idx outside
+ * [0, L) means no adapter. Adapters of smaller rank are padded with zeros to R.
+ *   h[m, j] = alpha[a] sum_k x[m, k] A[a][j, k]          (0 without an adapter)
+ *   y[m, n] = scale[n] sum_k x[m, k] q[n, k] + bias[n] + sum_j h[m, j] B[a][n, j]
+ * and, for a gradient dy of y,
+ *   u[m, j]     = alpha[a] sum_n dy[m, n] B[a][n, j]     (0 without an adapter)
+ *   dx[m, k]    = sum_n dy[m, n] scale[n] q[n, k] + sum_j u[m, j] A[a][j, k]
+ *   dB[a][n, j] = sum_{m: idx[m] = a} dy[m, n] h[m, j]
+ *   dA[a][j, k] = sum_{m: idx[m] = a} u[m, j] x'[m, k]
+ * where x' is x as its 8-bit checkpoint holds it (below). alpha is not trained.
+ * A value of one adapter, or a row of one request, never reaches the rows and
+ * gradients of another, whatever it holds.
+ *
+ * The plan. aql_lora_plan sorts a batch's rows by adapter into
+ * aql_lora_plan_bytes(M, L) bytes of device memory. Every layer's linears and
+ * both directions use the same plan for as long as idx stands; it copies idx,
+ * which may change or go after the call. M and L must be those of the plan in
+ * every call that takes it.
+ *
+ *   idx   device, [M] int32
+ *   plan  device, aql_lora_plan_bytes(M, L) bytes (output)
+ * Errors: M < 0 or > 1048560; L outside 1..AQL_LORA_MAX_ADAPTERS; NULL (M > 0)
+ * or misaligned pointers; plan_bytes too small (AQL_ERR_WORKSPACE).
+ */
+size_t aql_lora_plan_bytes(int64_t M, int64_t L); /* 0 for invalid sizes */
+int aql_lora_plan(const int32_t *idx, int64_t M, int64_t L, void *plan, size_t plan_bytes,
+                  void *stream);
+
+/*
+ * The linear with adapters. The products with the adapters are float32 sums of
+ * exact products; y is rounded to bf16 once, with everything in the sum.
+ *
+ *   x, q, scale, bias, y, M, N, K, ws   as aql_linear_w8a16 (the workspace is
+ *           optional and sized by AQL_OP_W8A16)
+ *   A, B, alpha, L, R   the stacked adapters
+ *   plan    from aql_lora_plan for this batch (M, L)
+ *   h       device, [M, R] float32 (output; the backward pass takes it)
+ * Errors: as aql_linear_w8a16, plus R not a multiple of 8 in
+ * 8..AQL_LORA_MAX_RANK, L outside 1..AQL_LORA_MAX_ADAPTERS, NULL or misaligned
+ * A, B, alpha, plan or h. N == 0 launches nothing and leaves h as it was.
+ */
+int aql_linear_w8a16_lora(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
+                          const float *scale, const uint16_t *bias, int64_t N, const uint16_t *A,
+                          const uint16_t *B, const float *alpha, int64_t L, int64_t R,
+                          const void *plan, uint16_t *y, float *h, void *ws, size_t ws_bytes,
+                          void *stream);
+
+/*
+ * Gradient of aql_linear_w8a16 to its input: dx[m, k] = sum_n dy[m, n] scale[n]
+ * q[n, k], on the weights as they lie (no transposed copy). Each weight enters
+ * as bf16(scale[n] q[n, k]), one rounding; sums are float32.
+ *
+ *   dy  device, [M, N] bf16;  q, scale as aql_linear_w8a16
+ *   dx  device, [M, K] bf16 (output)
+ *   ws  optional device workspace of aql_workspace_bytes(AQL_OP_W8A16_DGRAD, M,
+ *       N, K) bytes: shapes of few output tiles split the sum over N with it.
+ * Errors: M < 0 or > 1048560; K < 16, K % 16 != 0 or K > 2^24; N < 0,
+ * N % 8 != 0 or N > 2^22; NULL (M, N > 0) or misaligned pointers. N == 0
+ * writes zeros.
+ */
+int aql_linear_w8a16_dgrad(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q,
+                           const float *scale, int64_t K, uint16_t *dx, void *ws, size_t ws_bytes,
+                           void *stream);
+
+/*
+ * Backward pass of aql_linear_w8a16_lora (formulas above).
+ *
+ *   dy      device, [M, N] bf16
+ *   h       device, [M, R] float32 from the forward pass
+ *   xq, xs  the 8-bit checkpoint of x: int8 [M, K], float32 [M, ceil(K / 128)]
+ *   accumulate  nonzero: dA and dB are added to (gradients over several
+ *           batches); else they are overwritten, with zeros for an adapter
+ *           that no row names
+ *   dx      device, [M, K] bf16 (output; may be NULL: not computed)
+ *   dA, dB  device, [L, R, K] and [L, N, R] float32 (outputs; either may be
+ *           NULL: not computed. xq and xs may be NULL without dA)
+ *   ws      device workspace of aql_lora_backward_bytes(M, N, K, R) bytes
+ * Errors: as aql_linear_w8a16_dgrad and aql_linear_w8a16_lora;
+ * AQL_ERR_WORKSPACE. M == 0 or N == 0 write what is left of the outputs
+ * (zeros, unless they accumulate).
+ */
+size_t aql_lora_backward_bytes(int64_t M, int64_t N, int64_t K, int64_t R);
+int aql_linear_w8a16_lora_backward(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q,
+                                   const float *scale, int64_t K, const uint16_t *A,
+                                   const uint16_t *B, const float *alpha, int64_t L, int64_t R,
+                                   const void *plan, const float *h, const int8_t *xq,
+                                   const float *xs, int accumulate, uint16_t *dx, float *dA,
+                                   float *dB, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------- 8-bit activation checkpoints */
+
+/*
+ * Activations kept for a backward pass in 8 bits, with one scale for each 128
+ * values of a row (a row's last group may be shorter): s = max |x| / 127 in
+ * binary32, 1 where that is not positive; code = clamp(round(x / s), -127, 127),
+ * the quotient in binary32. Restored values are code * s. A channel that runs
+ * hot costs its own group precision, not the row.
+ *
+ *   x   device, [M, K] float32 (dtype AQL_F32) or bf16 (AQL_BF16)
+ *   xq  device, [M, K] int8;  xs  device, [M, ceil(K / 128)] float32
+ * Errors: unknown dtype; M < 0; K < 1 or K % 4 != 0; M * ceil(K / 128) > 2^36;
+ * NULL (M > 0) or misaligned pointers.
+ */
+int aql_act_checkpoint(const void *x, int dtype, int64_t M, int64_t K, int8_t *xq, float *xs,
+                       void *stream);
+int aql_act_restore(const int8_t *xq, const float *xs, int64_t M, int64_t K, void *x, int dtype,
+                    void *stream);
 
 /* ------------------------------------------------------------ stage entry */
 

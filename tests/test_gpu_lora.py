@@ -1,0 +1,554 @@
+"""Low-rank adapters beside the W8A16 linear, their gradients, and 8-bit
+activation checkpoints, against plain 64-bit forms on the CPU.
+
+Tolerances. With u = 2^-24, a float32 sum of n terms in any order is off by at
+most (n + 1) u T, T the sum of the terms' magnitudes (products of bf16 or int8
+values are exact in float32; one rounding more for a scale). Then
+  h, u     (K + 3) u T                     (N for u; + alpha's rounding)
+  y        2^-8 |y| (rounding to bf16) + (K + R + 4) u T
+           + (|h|'s own error + 2^-16 |h|, its two-part split) . |B|
+  dx       2^-8 |dx| + (N + R + 4) u T + 2^-8 sum |dy scale q|  (the weights are
+           rounded to bf16) + (|u|'s own error + 2^-16 |u|) . |A|
+  dA, dB   (m + 4) u T + 2^-23 T (three-part split, the product with a scale)
+           + u's own error . |x'|,  m the adapter's rows
+and over the whole of a bf16 output the norm of the error is at most 4e-3 of
+the output's: two roundings of relative size 2^-8 / sqrt(3) at most each,
+3.2e-3 together."""
+import numpy as np
+import pytest
+import torch
+
+import activation_quantized_linear_amd as aql
+import workloads
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+U = 2.0 ** -24
+GROUP = 128
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+def make(M, K, N, L, R, mix="random", bias=False, seed=0):
+    g = workloads.gen(1000 + seed + 7 * M + 11 * K + 13 * N + L + R)
+    w = workloads.randn(g, N, K, std=0.02)
+    scale = w.abs().amax(1).clamp_min(1e-9) / 127.0 if N else torch.empty(0)
+    c = {
+        "q": torch.round(w / scale[:, None]).clamp(-127, 127).to(torch.int8),
+        "scale": scale,
+        "bias": workloads.randn(g, N, std=0.1).to(torch.bfloat16) if bias else None,
+        "x": workloads.randn(g, M, K).to(torch.bfloat16),
+        "dy": (workloads.randn(g, M, N, std=1e-3)
+               * torch.exp(workloads.randn(g, M, 1))).to(torch.bfloat16),
+        "A": workloads.randn(g, L, R, K, std=K ** -0.5).to(torch.bfloat16),
+        "B": workloads.randn(g, L, N, R, std=0.02).to(torch.bfloat16),
+        "alpha": 0.5 + torch.rand(L, generator=g),
+    }
+    if mix == "random":
+        idx = torch.randint(-1, L + 1, (M,), generator=g)  # -1 and L: none
+        idx[idx == L] = 2 ** 31 - 1
+    elif mix == "runs":
+        idx = (torch.arange(M) * L) // max(M, 1)
+    elif mix == "none":
+        idx = torch.full((M,), -5)
+    else:
+        idx = torch.full((M,), int(mix))
+    c["idx"] = idx.to(torch.int32)
+    return c
+
+
+def dev(c):
+    return {k: (v.contiguous().to(DEV) if isinstance(v, torch.Tensor) else v) for k, v in c.items()}
+
+
+def f64(t):
+    return t.double()
+
+
+def rows_of(c, a):
+    return (c["idx"] == a).nonzero()[:, 0]
+
+
+def ref_forward(c):
+    x, q, s = f64(c["x"]), f64(c["q"]), f64(c["scale"])
+    M, K = x.shape
+    N, (L, R) = q.shape[0], c["A"].shape[:2]
+    y, T = (x @ q.T) * s, (x.abs() @ q.abs().T) * s
+    h, hT = torch.zeros(M, R).double(), torch.zeros(M, R).double()
+    tol = torch.zeros(M, N).double()
+    for a in range(L):
+        r = rows_of(c, a)
+        if len(r) == 0:
+            continue
+        A, B, al = f64(c["A"][a]), f64(c["B"][a]), float(c["alpha"][a])
+        h[r] = al * (x[r] @ A.T)
+        hT[r] = al * (x[r].abs() @ A.abs().T)
+        y[r] += h[r] @ B.T
+        T[r] += h[r].abs() @ B.abs().T
+        tol[r] += ((K + 3) * U * hT[r] + 2.0 ** -16 * h[r].abs()) @ B.abs().T
+    if c["bias"] is not None:
+        y, T = y + f64(c["bias"]), T + f64(c["bias"]).abs()
+    tol += 2.0 ** -8 * y.abs() + (K + R + 4) * U * T
+    return y, tol, h, (K + 3) * U * hT
+
+
+def checkpoint_ref(x):
+    """Codes and scales in the definition's own float32 steps."""
+    x = x.float()
+    M, K = x.shape
+    G = (K + GROUP - 1) // GROUP
+    p = torch.zeros(M, G * GROUP)
+    p[:, :K] = x
+    p = p.view(M, G, GROUP)
+    s = p.abs().amax(2) / np.float32(127.0)
+    s = torch.where(s > 0, s, torch.ones_like(s))
+    codes = torch.round(p / s[:, :, None]).clamp(-127, 127)
+    return codes.view(M, -1)[:, :K].to(torch.int8), s
+
+
+def decoded(xq, xs):
+    K = xq.shape[1]
+    return f64(xq) * f64(xs).repeat_interleave(GROUP, 1)[:, :K]
+
+
+def ref_backward(c, h, xq, xs):
+    dy, q, s, x = f64(c["dy"]), f64(c["q"]), f64(c["scale"]), decoded(xq, xs)
+    N, K = q.shape
+    L, R = c["A"].shape[:2]
+    dx = (dy * s) @ q
+    T = (dy.abs() * s) @ q.abs()
+    tol = 2.0 ** -8 * T
+    dA, dB = torch.zeros(L, R, K).double(), torch.zeros(L, N, R).double()
+    tA, tB = torch.zeros_like(dA), torch.zeros_like(dB)
+    for a in range(L):
+        r = rows_of(c, a)
+        m = len(r)
+        if m == 0:
+            continue
+        A, B, al = f64(c["A"][a]), f64(c["B"][a]), float(c["alpha"][a])
+        u = al * (dy[r] @ B)
+        ue = (N + 3) * U * al * (dy[r].abs() @ B.abs())
+        dx[r] += u @ A
+        T[r] += u.abs() @ A.abs()
+        tol[r] += (ue + 2.0 ** -16 * u.abs()) @ A.abs()
+        dA[a] = u.T @ x[r]
+        tA[a] = ((m + 4) * U + 2.0 ** -23) * (u.abs().T @ x[r].abs()) + ue.T @ x[r].abs()
+        hr = f64(h[r])
+        dB[a] = dy[r].T @ hr
+        tB[a] = ((m + 4) * U + 2.0 ** -23) * (dy[r].abs().T @ hr.abs())
+    tol += 2.0 ** -8 * dx.abs() + (N + R + 4) * U * T
+    return (dx, tol), (dA, tA), (dB, tB)
+
+
+def close(got, ref, tol, what, norm=None):
+    got = got.double().cpu()
+    assert got.shape == ref.shape, what
+    assert torch.isfinite(got).all(), f"{what}: not finite"
+    err = (got - ref).abs()
+    bad = err > tol
+    if bad.any():
+        i = torch.argmax(err - tol)
+        at = np.unravel_index(int(i), tuple(err.shape))
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} outside; worst at {at}: got "
+                             f"{got[at].item()!r} want {ref[at].item()!r} tol {tol[at].item()!r}")
+    if norm is not None and ref.numel():
+        assert err.norm() <= norm * ref.norm() + 1e-300, f"{what}: norm {err.norm() / ref.norm()}"
+
+
+def forward(d, plan=None, **kw):
+    if plan is None:
+        plan = aql.aql_lora_plan(d["idx"], d["A"].shape[0])
+    y, h = aql.aql_linear_w8a16_lora(d["x"], d["q"], d["scale"], d["A"], d["B"], d["alpha"], plan,
+                                     d["bias"], **kw)
+    return y, h, plan
+
+
+def backward(d, plan, h, xq, xs, **kw):
+    return aql.aql_linear_w8a16_lora_backward(d["dy"], d["q"], d["scale"], d["A"], d["B"],
+                                              d["alpha"], plan, h, xq, xs, **kw)
+
+
+# ------------------------------------------------------------------- the plan
+
+
+@pytest.mark.parametrize("M,L", [(1, 1), (1, 7), (5, 2), (16, 3), (17, 1), (64, 64), (500, 3),
+                                 (1023, 9), (1024, 1), (1025, 33), (3000, 1024), (5000, 200)])
+@pytest.mark.parametrize("mix", ["random", "runs", "none"])
+def test_plan(M, L, mix):
+    say("plan", M, L, mix)
+    g = workloads.gen(M + L)
+    if mix == "random":
+        idx = torch.randint(-2, L + 2, (M,), generator=g).to(torch.int32)
+    elif mix == "runs":
+        idx = ((torch.arange(M) * L) // M).to(torch.int32)
+    else:
+        idx = torch.full((M,), -1, dtype=torch.int32)
+    p = aql.aql_lora_plan(idx.to(DEV), L)
+    torch.cuda.synchronize()
+    assert (p.M, p.L) == (M, L)
+    b = p.buffer.cpu().view(torch.int32)
+    tiles = M // 16 + min(M, L + 1)
+    up = lambda v: (v + 15) // 16 * 16
+    o_idx, o_perm = 16, 16 + up(M)
+    o_own = o_perm + 16 * tiles
+    o_first = o_own + up(tiles)
+    valid = torch.where((idx >= 0) & (idx < L), idx, torch.full_like(idx, -1))
+    assert torch.equal(b[o_idx:o_idx + M], valid)
+    perm, own, first = b[o_perm:o_own], b[o_own:o_own + tiles], b[o_first:o_first + L + 1]
+    t = 0
+    for a in list(range(L)) + [-1]:
+        rows = (valid == a).nonzero()[:, 0].to(torch.int32)
+        n = (len(rows) + 15) // 16
+        assert int(first[a if a >= 0 else L]) == t
+        want = torch.full((16 * n,), -1, dtype=torch.int32)
+        want[:len(rows)] = rows
+        assert torch.equal(perm[16 * t:16 * (t + n)], want), (a, rows)
+        assert (own[t:t + n] == a).all()
+        t += n
+    assert int(b[0]) == t and (own[t:] == -2).all() and (perm[16 * t:] == -1).all()
+
+
+# -------------------------------------------------------------------- forward
+
+FORWARD = [
+    # one row: single-row tile (K outside 2048..8192), contiguous form, x past the LDS budget
+    (1, 16, 1, 1, 8, "0"), (1, 960, 2560, 4, 8, "random"), (1, 2048, 40, 2, 16, "0"),
+    (1, 4096, 2056, 3, 64, "1"), (1, 8192, 24, 2, 128, "0"), (1, 17408, 24, 2, 16, "1"),
+    (1, 960, 77, 3, 24, "none"),
+    # two to four rows: skinny tile, few-row form
+    (2, 256, 50, 3, 16, "random"), (3, 2048, 33, 4, 40, "random"), (4, 4096, 64, 2, 8, "runs"),
+    (2, 16384, 9, 2, 16, "runs"), (3, 16400, 9, 2, 16, "runs"),
+    # skinny tile, shared-x tile, split K with the workspace
+    (5, 960, 2560, 8, 16, "random"), (16, 976, 65, 3, 32, "random"), (27, 512, 131, 27, 16, "runs"),
+    (63, 2560, 960, 5, 128, "random"), (33, 64, 8200, 4, 16, "random"),
+    (17, 4096, 12290, 2, 8, "random"), (16, 8192, 72, 3, 64, "random"), (63, 9232, 40, 1, 16, "0"),
+    # tiled GEMM: ragged and whole K, 64 x 128, 128 x 128, wide with 4 and 2 stages, split K
+    (64, 48, 130, 3, 8, "random"), (65, 64, 127, 64, 16, "random"), (200, 320, 257, 3, 64, "runs"),
+    (129, 1024, 264, 2, 128, "random"), (2048, 64, 2048, 5, 24, "runs"),
+    (70, 64, 40960, 3, 16, "random"), (1024, 80, 16384, 2, 40, "runs"),
+    (100, 8192, 72, 3, 16, "random"), (257, 8192, 1024, 1, 64, "0"), (150, 96, 64, 2, 16, "none"),
+]
+
+
+@pytest.mark.parametrize("M,K,N,L,R,mix", FORWARD)
+@pytest.mark.parametrize("bias", [False, True])
+def test_forward(M, K, N, L, R, mix, bias):
+    say("forward", M, K, N, L, R, mix, bias)
+    c = make(M, K, N, L, R, mix, bias)
+    y, h, _ = forward(dev(c))
+    torch.cuda.synchronize()
+    yr, ytol, hr, htol = ref_forward(c)
+    close(h, hr, htol, "h")
+    close(y, yr, ytol, "y", norm=4e-3)
+
+
+def test_forward_without_adapters_is_the_plain_linear():
+    for M, K, N in ((1, 960, 2560), (1, 4096, 520), (3, 4096, 40), (20, 512, 96), (40, 64, 8200),
+                    (128, 256, 512)):
+        say("plain", M, K, N)
+        d = dev(make(M, K, N, 2, 16, "none", True))
+        y, h, _ = forward(d)
+        assert torch.equal(h, torch.zeros_like(h))
+        if M in (1, 20, 40, 128):  # the same kernels serve both calls
+            assert torch.equal(y, aql.aql_linear_w8a16(d["x"], d["q"], d["scale"], d["bias"]))
+
+
+@pytest.mark.parametrize("M", [9, 27, 150, 300])
+def test_adapters_do_not_reach_each_other(M):
+    """NaN and infinities in one adapter's matrices, and in its rows, stay in its rows."""
+    say("isolation", M)
+    c = make(M, 512, 320, 3, 16, "random")
+    y0, h0, _ = forward(dev(c))
+    c["A"][1], c["B"][1, ::2], c["B"][1, 1::2] = float("nan"), float("inf"), float("nan")
+    c["x"][c["idx"] == 1] = float("inf")
+    y1, h1, plan = forward(dev(c))
+    torch.cuda.synchronize()
+    other = (c["idx"] != 1).to(DEV)
+    assert torch.equal(y0[other], y1[other]) and torch.equal(h0[other], h1[other])
+    assert not torch.isfinite(h1[~other]).any()
+    # the gradients too: rows of adapter 1, and rows without one, hold NaN
+    c = make(M, 512, 320, 3, 16, "random")
+    d = dev(c)
+    y, h, plan = forward(d)
+    xq, xs = aql.aql_act_checkpoint(d["x"])
+    dx0, dA0, dB0 = backward(d, plan, h, xq, xs)
+    for bad in (1, -1, 2 ** 31 - 1):
+        rows = (c["idx"] == bad).to(DEV)
+        d["dy"][rows], h[rows], xs[rows] = float("nan"), float("inf"), float("nan")
+    d["A"][1], d["B"][1] = float("nan"), float("inf")
+    dx1, dA1, dB1 = backward(d, plan, h, xq, xs)
+    torch.cuda.synchronize()
+    ok = ((c["idx"] == 0) | (c["idx"] == 2)).to(DEV)
+    assert torch.equal(dx0[ok], dx1[ok])
+    assert torch.equal(dA0[::2], dA1[::2]) and torch.equal(dB0[::2], dB1[::2])
+
+
+# ------------------------------------------------------------------- backward
+
+BACKWARD = [
+    (1, 16, 8, 1, 8, "0"), (1, 960, 2560, 2, 16, "1"), (2, 144, 24, 3, 24, "runs"),
+    (15, 128, 128, 2, 32, "random"), (16, 272, 136, 1, 40, "0"), (17, 256, 264, 4, 64, "random"),
+    (31, 2560, 960, 3, 128, "runs"), (63, 960, 2560, 2, 8, "runs"), (64, 64, 4096, 64, 16, "runs"),
+    (130, 4096, 72, 3, 16, "random"), (257, 304, 200, 5, 48, "runs"), (500, 1024, 520, 3, 64, "runs"),
+    (300, 80, 1048, 1, 16, "none"), (1000, 512, 640, 7, 128, "random"),
+    (2100, 2560, 192, 2, 16, "runs"), (1100, 16384, 64, 1, 8, "0"), (33, 12288, 1032, 33, 8, "runs"),
+]
+
+
+@pytest.mark.parametrize("M,K,N,L,R,mix", BACKWARD)
+def test_backward(M, K, N, L, R, mix):
+    say("backward", M, K, N, L, R, mix)
+    c = make(M, K, N, L, R, mix)
+    d = dev(c)
+    _, h, plan = forward(d)
+    xq, xs = aql.aql_act_checkpoint(d["x"])
+    dx, dA, dB = backward(d, plan, h, xq, xs)
+    torch.cuda.synchronize()
+    (rx, tx), (rA, tA), (rB, tB) = ref_backward(c, h.cpu(), xq.cpu(), xs.cpu())
+    close(dx, rx, tx, "dx", norm=4e-3)
+    close(dA, rA, tA, "dA")
+    close(dB, rB, tB, "dB")
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 8, 16), (1, 4096, 2048), (7, 72, 48), (64, 64, 128),
+                                   (65, 136, 400), (333, 2560, 960), (200, 200, 12304),
+                                   (128, 11008, 256), (2500, 128, 2064), (1300, 64, 16384),
+                                   (40, 0, 64)])
+def test_dgrad(M, N, K):
+    say("dgrad", M, N, K)
+    c = make(M, K, N, 1, 8, "0")
+    d = dev(c)
+    dx = aql.aql_linear_w8a16_dgrad(d["dy"], d["q"], d["scale"])
+    torch.cuda.synchronize()
+    dy, q, s = f64(c["dy"]), f64(c["q"]), f64(c["scale"])
+    ref, T = (dy * s) @ q, (dy.abs() * s) @ q.abs()
+    close(dx, ref, 2.0 ** -8 * ref.abs() + (2.0 ** -8 + (N + 4) * U) * T, "dx", norm=4e-3)
+    if aql.aql_workspace_bytes(aql.AQL_OP_W8A16_DGRAD, M, N, K):  # without the workspace: no split
+        dx = aql.aql_linear_w8a16_dgrad(d["dy"], d["q"], d["scale"],
+                                        workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+        close(dx, ref, 2.0 ** -8 * ref.abs() + (2.0 ** -8 + (N + 4) * U) * T, "dx", norm=4e-3)
+
+
+def test_backward_accumulates_and_leaves_out():
+    c = make(100, 256, 136, 4, 16, "runs")
+    c["idx"][c["idx"] == 2] = 1  # adapter 2: no rows
+    d = dev(c)
+    _, h, plan = forward(d)
+    xq, xs = aql.aql_act_checkpoint(d["x"])
+    dx, dA, dB = backward(d, plan, h, xq, xs)
+    assert torch.equal(dA[2], torch.zeros_like(dA[2])) and torch.equal(dB[2], torch.zeros_like(dB[2]))
+    a0, b0 = torch.randn_like(dA), torch.randn_like(dB)
+    a1, b1 = a0.clone(), b0.clone()
+    none, a2, b2 = backward(d, plan, h, xq, xs, dA=a1, dB=b1, accumulate=True, need_dx=False)
+    assert none is None and a2 is a1 and b2 is b1
+    assert torch.equal(a1, a0 + dA) and torch.equal(b1, b0 + dB)
+    with pytest.raises(ValueError):
+        backward(d, plan, h, xq, xs, accumulate=True)
+    with pytest.raises(ValueError):
+        backward(d, plan, h, xq, xs, dx=dx, need_dx=False)
+
+
+def test_gradients_against_differences():
+    """Central differences of sum(dy y) in 64 bits, x as its checkpoint holds it,
+    along random directions: the function is linear in A, in B and in x, so a
+    difference is exact up to rounding; the kernels' gradients agree within
+    their tolerances summed against the direction's magnitudes."""
+    c = make(48, 144, 72, 3, 16, "random")
+    d = dev(c)
+    xq, xs = aql.aql_act_checkpoint(d["x"])
+    c["x"] = decoded(xq.cpu(), xs.cpu())
+    plan = aql.aql_lora_plan(d["idx"], 3)
+    h = torch.zeros(48, 16)
+    al = [float(v) for v in c["alpha"]]
+
+    def loss(x, A, B):
+        y = (x @ f64(c["q"]).T) * f64(c["scale"])
+        for a in range(3):
+            r = rows_of(c, a)
+            y[r] += al[a] * (x[r] @ A[a].T) @ B[a].T
+        return float((y * f64(c["dy"])).sum())
+
+    p = {"x": c["x"], "A": f64(c["A"]), "B": f64(c["B"])}
+    for a in range(3):
+        r = rows_of(c, a)
+        h[r] = (al[a] * (p["x"][r] @ p["A"][a].T)).float()
+    dx, dA, dB = backward(d, plan, h.to(DEV), xq, xs)
+    (_, tx), (_, tA), (_, tB) = ref_backward(c, h, xq.cpu(), xs.cpu())
+    g = workloads.gen(5)
+    for name, got, tol in (("x", dx, tx), ("A", dA, tA), ("B", dB, tB)):
+        v = torch.randn(p[name].shape, generator=g).double()
+        up, down = dict(p), dict(p)
+        up[name], down[name] = p[name] + 1e-3 * v, p[name] - 1e-3 * v
+        diff = (loss(**up) - loss(**down)) / 2e-3
+        slack = float((tol * v.abs()).sum()) + 1e-9 * abs(diff)
+        # dB's reference h was rounded to float32 once
+        slack += 2.0 ** -24 * float((f64(got.cpu()).abs() * v.abs()).sum()) * 48
+        assert abs(float((got.double().cpu() * v).sum()) - diff) <= slack, name
+
+
+# ---------------------------------------------------------------- checkpoints
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,K", [(1, 4), (3, 128), (5, 132), (1, 260), (37, 960), (64, 1020),
+                                 (2, 14336), (1000, 512)])
+def test_checkpoint(M, K, dt):
+    say("checkpoint", M, K, dt)
+    g = workloads.gen(M + K)
+    x = workloads.randn(g, M, K)
+    x[:, K // 2] *= 100.0
+    x[M // 2, : min(K, 128)] = 0.0
+    if M > 4:
+        x[0] *= 1e-38   # subnormal scales
+        x[1] *= 1e-44   # scales that round to 0 or to the smallest subnormal
+        x[2] *= 1e36 if dt == torch.float32 else 1e34
+    x = x.to(dt)
+    xq, xs = aql.aql_act_checkpoint(x.to(DEV))
+    out = aql.aql_act_restore(xq, xs, dt)
+    other = aql.aql_act_restore(xq, xs, torch.bfloat16 if dt == torch.float32 else torch.float32)
+    torch.cuda.synchronize()
+    rq, rs = checkpoint_ref(x)
+    assert torch.equal(xs.cpu(), rs)
+    assert torch.equal(xq.cpu(), rq)
+    exact = decoded(rq, rs).float()  # a product of 8 and 24 bits: one float32 rounding
+    assert torch.equal((out if dt == torch.float32 else other).cpu(), exact)
+    assert torch.equal((other if dt == torch.float32 else out).cpu(), exact.to(torch.bfloat16))
+
+
+def test_checkpoint_past_32_bits():
+    M, K = 528000, 4096  # 2.16e9 values
+    x = torch.empty(M, K, dtype=torch.bfloat16, device=DEV)
+    x.normal_(generator=torch.Generator(device=DEV).manual_seed(3))
+    xq, xs = aql.aql_act_checkpoint(x)
+    back = aql.aql_act_restore(xq, xs)
+    for r in (0, 262143, 524287, 524289, M - 3):
+        q1, s1 = aql.aql_act_checkpoint(x[r:r + 3].clone())
+        assert torch.equal(xq[r:r + 3], q1) and torch.equal(xs[r:r + 3], s1)
+        assert torch.equal(back[r:r + 3], aql.aql_act_restore(q1, s1))
+
+
+# ------------------------------------------------------------------- together
+
+
+def test_training_step_of_an_mlp():
+    """Checkpoint, forward and backward of a SmolVLM-size up projection feeding a
+    down projection, three adapters in the batch, then one update of them: the
+    chain's gradients against 64 bits on the same intermediate values."""
+    M, L, R = 200, 3, 16
+    up = make(M, 960, 2560, L, R, "runs", seed=1)
+    down = make(M, 2560, 960, L, R, "runs", seed=2)
+    u, d = dev(up), dev(down)
+    plan = aql.aql_lora_plan(u["idx"], L)
+    ck1 = aql.aql_act_checkpoint(u["x"])
+    y1, h1, _ = forward(u, plan)
+    act = torch.relu(y1)
+    d["x"] = act
+    down["x"] = act.cpu()
+    ck2 = aql.aql_act_checkpoint(act)
+    y2, h2, _ = forward(d, plan)
+    d["dy"] = (y2.float() * 1e-3).to(torch.bfloat16)
+    down["dy"] = d["dy"].cpu()
+    da, dA2, dB2 = backward(d, plan, h2, *ck2)
+    u["dy"] = torch.where(act > 0, da, torch.zeros_like(da))
+    up["dy"] = u["dy"].cpu()
+    dx, dA1, dB1 = backward(u, plan, h1, *ck1)
+    new = [(p.float() - 0.1 * g).to(torch.bfloat16)
+           for p, g in ((u["A"], dA1), (u["B"], dB1), (d["A"], dA2), (d["B"], dB2))]
+    torch.cuda.synchronize()
+    y, ytol, h, htol = ref_forward(down)
+    close(y2, y, ytol, "y2", norm=4e-3)
+    for c, h, ck, got in ((down, h2, ck2, (da, dA2, dB2)), (up, h1, ck1, (dx, dA1, dB1))):
+        refs = ref_backward(c, h.cpu(), ck[0].cpu(), ck[1].cpu())
+        for name, g, (ref, tol) in zip(("dx", "dA", "dB"), got, refs):
+            close(g, ref, tol, name, norm=4e-3)
+    assert all(torch.isfinite(t).all() for t in new)
+
+
+@pytest.mark.parametrize("M", [1, 20, 200])
+def test_repeats_bit_for_bit_and_on_a_side_stream(M):
+    c = make(M, 2560, 960, 4, 32, "random")
+    d = dev(c)
+    y, h, plan = forward(d)
+    xq, xs = aql.aql_act_checkpoint(d["x"])
+    g = backward(d, plan, h, xq, xs)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        y2, h2, plan2 = forward(d)
+        xq2, xs2 = aql.aql_act_checkpoint(d["x"])
+        g2 = backward(d, plan2, h2, xq2, xs2)
+    s.synchronize()
+    for a, b in zip((y, h, xq, xs, *g), (y2, h2, xq2, xs2, *g2)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("M", [3, 150])
+def test_graph_replays_with_a_new_batch(M):
+    """One captured graph of plan, forward, checkpoint and backward, replayed with
+    new rows, adapters and gradients in its inputs, eager work between."""
+    L, R = 4, 16
+    c = make(M, 512, 264, L, R, "random")
+    d = dev(c)
+    plan = aql.aql_lora_plan(d["idx"], L)
+    kw = dict(y=torch.empty(M, 264, dtype=torch.bfloat16, device=DEV),
+              h=torch.empty(M, R, device=DEV))
+    out = dict(dx=torch.empty(M, 512, dtype=torch.bfloat16, device=DEV),
+               dA=torch.empty(L, R, 512, device=DEV), dB=torch.empty(L, 264, R, device=DEV),
+               workspace=torch.empty(aql.aql_lora_backward_bytes(M, 264, 512, R), dtype=torch.uint8,
+                                     device=DEV))
+    xq, xs = aql.aql_act_checkpoint(d["x"])
+
+    def step():
+        aql.aql_lora_plan(d["idx"], L, plan)
+        forward(d, plan, **kw)
+        aql.aql_act_checkpoint(d["x"], xq, xs)
+        backward(d, plan, kw["h"], xq, xs, **out)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(4):
+        n = dev(make(M, 512, 264, L, R, "random", seed=10 + i))
+        for k in ("x", "dy", "idx"):
+            d[k].copy_(n[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (kw["y"], kw["h"], xq, xs, out["dx"], out["dA"], out["dB"])]
+        y, h, p = forward(d)
+        eq, es = aql.aql_act_checkpoint(d["x"])
+        for a, b in zip(got, (y, h, eq, es, *backward(d, p, h, eq, es))):
+            assert torch.equal(a, b), i
+
+
+def test_a_plan_serves_only_its_batch():
+    d = dev(make(8, 64, 32, 2, 8, "runs"))
+    plan = aql.aql_lora_plan(d["idx"], 2)
+    d2 = dev(make(9, 64, 32, 2, 8, "runs"))
+    with pytest.raises(ValueError):
+        forward(d2, plan)
+    with pytest.raises(ValueError):
+        aql.aql_lora_plan(d2["idx"], 2, plan)
+    with pytest.raises(TypeError):
+        forward(d, plan.buffer)
+
+
+def test_empty_batches():
+    d = dev(make(0, 64, 32, 2, 8, "none"))
+    y, h, plan = forward(d)
+    assert y.shape == (0, 32) and h.shape == (0, 8)
+    xq, xs = aql.aql_act_checkpoint(d["x"])
+    dx, dA, dB = backward(d, plan, h, xq, xs)
+    assert dx.shape == (0, 64) and not dA.any() and not dB.any()
+    a, b = torch.ones_like(dA), torch.ones_like(dB)
+    backward(d, plan, h, xq, xs, dA=a, dB=b, accumulate=True)
+    assert (a == 1).all() and (b == 1).all()
+    # no output channels: the input's gradient is zero, dA too
+    d = dev(make(5, 64, 0, 2, 8, "runs"))
+    plan = aql.aql_lora_plan(d["idx"], 2)
+    xq, xs = aql.aql_act_checkpoint(d["x"])
+    dx, dA, dB = backward(d, plan, torch.zeros(5, 8, device=DEV), xq, xs)
+    assert not dx.any() and not dA.any() and dB.shape == (2, 0, 8)

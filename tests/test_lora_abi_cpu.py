@@ -1,0 +1,138 @@
+"""Refusals of the low-rank adapter and 8-bit checkpoint entry points without a
+GPU: every invalid argument gets the documented status before any HIP call
+(fake device addresses are never touched), and empty problems launch nothing."""
+import ctypes as C
+
+import pytest
+import torch
+
+import activation_quantized_linear_amd as aql
+
+P = C.c_void_p(0x10000)    # fake, 16-byte aligned, never dereferenced
+MIS = C.c_void_p(0x10004)  # misaligned
+L = aql._lib
+BIG = 1 << 40
+
+OK, NULL, SHAPE, ALIGN, PARAM, WS = (aql.AQL_OK, aql.AQL_ERR_NULL, aql.AQL_ERR_SHAPE,
+                                     aql.AQL_ERR_ALIGN, aql.AQL_ERR_PARAM, aql.AQL_ERR_WORKSPACE)
+
+
+def call(fn, defaults, **kw):
+    args = dict(defaults)
+    for k, v in kw.items():
+        assert k in args, k
+        args[k] = v
+    return fn(*args.values())
+
+
+def plan(**kw):
+    return call(L.aql_lora_plan, dict(idx=P, M=5, L=3, plan=P, plan_bytes=BIG, stream=None), **kw)
+
+
+def test_plan_bytes():
+    b = aql.aql_lora_plan_bytes
+    assert b(0, 1) > 0 and b(1, 1) > 0
+    # idx, 16 positions and an owner a tile: M / 16 + min(M, L + 1) tiles
+    assert b(1000, 7) >= 4 * (1000 + 17 * (1000 // 16 + 8) + 8)
+    for M, A in ((-1, 1), (1, 0), (1, 1025), (1048561, 1)):
+        assert b(M, A) == 0
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(M=-1), SHAPE), (dict(M=1048561), SHAPE), (dict(L=0), SHAPE), (dict(L=1025), SHAPE),
+    (dict(idx=None), NULL), (dict(plan=None), NULL), (dict(idx=MIS), ALIGN),
+    (dict(plan=MIS), ALIGN), (dict(plan_bytes=64), WS)])
+def test_plan_refusals(kw, code):
+    assert plan(**kw) == code
+    assert "aql_lora_plan" in aql.aql_last_error()
+
+
+FWD = dict(x=P, M=5, K=64, q=P, scale=P, bias=None, N=24, A=P, B=P, alpha=P, L=3, R=8, plan=P, y=P,
+           h=P, ws=None, ws_bytes=0, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(M=-1), SHAPE), (dict(N=-1), SHAPE), (dict(K=8), SHAPE), (dict(K=40), SHAPE),
+    (dict(R=0), SHAPE), (dict(R=12), SHAPE), (dict(R=136), SHAPE), (dict(L=0), SHAPE),
+    (dict(L=1025), SHAPE)]
+    + [({k: None}, NULL) for k in ("x", "q", "scale", "A", "B", "alpha", "plan", "y", "h")]
+    + [({k: MIS}, ALIGN) for k in ("x", "q", "scale", "bias", "A", "B", "alpha", "plan", "y", "h",
+                                   "ws")])
+def test_forward_refusals(kw, code):
+    assert call(L.aql_linear_w8a16_lora, FWD, **kw) == code
+
+
+def test_forward_empty():
+    none = {k: None for k in ("x", "y", "h")}
+    assert call(L.aql_linear_w8a16_lora, FWD, M=0, **none) == OK
+    assert call(L.aql_linear_w8a16_lora, FWD, N=0, q=None, scale=None, y=None, B=None) == OK
+
+
+DG = dict(dy=P, M=5, N=24, q=P, scale=P, K=64, dx=P, ws=None, ws_bytes=0, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(M=-1), SHAPE), (dict(M=1048561), SHAPE), (dict(N=-8), SHAPE), (dict(N=12), SHAPE),
+    (dict(N=(1 << 22) + 8), SHAPE), (dict(K=0), SHAPE), (dict(K=24), SHAPE),
+    (dict(K=(1 << 24) + 16), SHAPE)]
+    + [({k: None}, NULL) for k in ("dy", "q", "scale", "dx")]
+    + [({k: MIS}, ALIGN) for k in ("dy", "q", "scale", "dx", "ws")])
+def test_dgrad_refusals(kw, code):
+    assert call(L.aql_linear_w8a16_dgrad, DG, **kw) == code
+
+
+def test_dgrad_empty_and_workspace():
+    assert call(L.aql_linear_w8a16_dgrad, DG, M=0, dy=None, dx=None) == OK
+    wb = lambda M, N, K: L.aql_workspace_bytes(aql.AQL_OP_W8A16_DGRAD, M, N, K)
+    assert wb(2048, 11008, 4096) == 0                       # many tiles: no split
+    assert wb(64, 4096, 4096) > 0 and wb(64, 4096, 4096) % (64 * 4096 * 4) == 0
+    assert wb(-1, 16, 16) == 0 and wb(0, 16, 16) == 0
+
+
+BWD = dict(dy=P, M=5, N=24, q=P, scale=P, K=64, A=P, B=P, alpha=P, L=3, R=8, plan=P, h=P, xq=P,
+           xs=P, accumulate=0, dx=P, dA=P, dB=P, ws=P, ws_bytes=BIG, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(M=-1), SHAPE), (dict(N=12), SHAPE), (dict(K=24), SHAPE), (dict(R=4), SHAPE),
+    (dict(R=132), SHAPE), (dict(L=0), SHAPE), (dict(L=1025), SHAPE), (dict(ws=None), WS),
+    (dict(ws_bytes=16), WS)]
+    + [({k: None}, NULL) for k in ("dy", "q", "scale", "A", "B", "alpha", "plan", "h", "xq", "xs")]
+    + [({k: MIS}, ALIGN) for k in ("dy", "q", "scale", "A", "B", "alpha", "plan", "h", "xq", "xs",
+                                   "dx", "dA", "dB", "ws")])
+def test_backward_refusals(kw, code):
+    assert call(L.aql_linear_w8a16_lora_backward, BWD, **kw) == code
+
+
+def test_backward_nothing_asked_for():
+    assert call(L.aql_linear_w8a16_lora_backward, BWD, dx=None, dA=None, dB=None) == OK
+    assert aql.aql_lora_backward_bytes(0, 24, 64, 8) == 0
+    assert aql.aql_lora_backward_bytes(5, 24, 64, 8) >= 5 * 8 * 4
+
+
+CK = dict(x=P, dtype=0, M=5, K=64, xq=P, xs=P, stream=None)
+RS = dict(xq=P, xs=P, M=5, K=64, x=P, dtype=0, stream=None)
+
+
+@pytest.mark.parametrize("fn,base", [("aql_act_checkpoint", CK), ("aql_act_restore", RS)])
+def test_checkpoint_refusals(fn, base):
+    f = getattr(L, fn)
+    assert call(f, base, dtype=2) == PARAM
+    for kw in (dict(M=-1), dict(K=0), dict(K=6), dict(M=1 << 37)):
+        assert call(f, base, **kw) == SHAPE
+    for k in ("x", "xq", "xs"):
+        assert call(f, base, **{k: None}) == NULL
+        assert call(f, base, **{k: MIS}) == ALIGN
+    assert call(f, base, M=0, x=None, xq=None, xs=None) == OK
+
+
+def test_binding_refuses_host_tensors():
+    idx = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        aql.aql_lora_plan(idx, 2)
+    with pytest.raises(TypeError):
+        aql.aql_lora_plan(idx.long(), 2)
+    with pytest.raises(ValueError):
+        aql.aql_act_checkpoint(torch.zeros(4, 16))
+    with pytest.raises(TypeError):
+        aql.aql_act_checkpoint(torch.zeros(4, 16, dtype=torch.float16))
