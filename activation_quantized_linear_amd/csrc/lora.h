@@ -106,94 +106,110 @@ __device__ __forceinline__ void split_bf16(const float (&v)[8], bf16x8 &hi, bf16
   }
 }
 
+// The 16 x 32 contraction block of h that lane (r, g) holds for a matrix
+// instruction: row r of the block, ranks j0 .. j0 + 7, in two bf16 parts.
+__device__ __forceinline__ void lora_h_frag(const float *h, bool in, bf16x8 &hi, bf16x8 &lo) {
+  f32x4 h0 = {0.f, 0.f, 0.f, 0.f}, h1 = h0;
+  if (in) {
+    h0 = *reinterpret_cast<const f32x4 *>(h);
+    h1 = *reinterpret_cast<const f32x4 *>(h + 4);
+  }
+  const float v[8] = {h0[0], h0[1], h0[2], h0[3], h1[0], h1[1], h1[2], h1[3]};
+  split_bf16(v, hi, lo);
+}
+
+// Its other operand: column n of the output, ranks j0 .. j0 + 7 of adapter a.
+// KMAJOR: W is [L, R, N] (contraction rows), else [L, N, R].
+template <bool KMAJOR>
+__device__ __forceinline__ bf16x8 lora_w_frag(const LoraTerm &t, int a, int64_t n, int j0) {
+  i32x4 v = {0, 0, 0, 0};
+  if (j0 < t.R && n < t.N) {  // whole chunks of 8: R is a multiple of 8
+    if constexpr (KMAJOR) {
+      const uint16_t *p = t.W + ((int64_t)a * t.R + j0) * t.N + n;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[e] = (int)((uint32_t)p[(int64_t)(2 * e) * t.N] |
+                     ((uint32_t)p[(int64_t)(2 * e + 1) * t.N] << 16));
+    } else {
+      v = *reinterpret_cast<const i32x4 *>(t.W + ((int64_t)a * t.N + n) * t.R + j0);
+    }
+  }
+  return __builtin_bit_cast(bf16x8, v);
+}
+
 // acc[i][j] += h . W_a^T over a wave's tile of MFMA blocks: 16 TI rows from m0
 // by 16 TJ columns from n0, accumulators in the 16x16x32 layout (lane 16 g + r
-// holds rows 4 g + v of column r). The wave walks the distinct adapters of its
-// rows in ascending order; a block that holds none of an adapter's rows is
-// skipped, and in a block of several adapters the products of the other rows
-// are computed and dropped by a select, so no value of one adapter (an
-// infinity or a NaN in it among them) reaches a row of another. All 64 lanes
-// must be active. KMAJOR: W is [L, R, N] (contraction rows), else [L, N, R].
+// holds rows 4 g + v of one column: n0 + 16 j + r, or with KMAJOR n0 + TJ r + j).
+// All 64 lanes must be active.
+// Where all the tile's rows are of one adapter (a prefill, a training batch)
+// its operand is loaded once for the tile. Else each block of 16 rows walks its
+// distinct adapters in ascending order; in a block of several the products of
+// the other rows are computed and dropped by a select, so no value of one
+// adapter (an infinity or a NaN in it among them) reaches a row of another.
 template <bool KMAJOR, int TI, int TJ>
 __device__ __forceinline__ void lora_add_tile(f32x4 (&acc)[TI][TJ], const LoraTerm &t, int64_t m0,
                                               int64_t M, int64_t n0) {
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   int id[TI];
+  bool same = true;
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
     const int64_t m = m0 + 16 * i + r;
     id[i] = m < M ? t.idx[m] : -1;
   }
-  int prev = -1;
-  for (;;) {
-    int next = 0x7fffffff;
+  const int a0 = __builtin_amdgcn_readfirstlane(id[0]);
 #pragma unroll
-    for (int i = 0; i < TI; ++i) next = id[i] > prev && id[i] < next ? id[i] : next;
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) {
-      const int other = __shfl_xor(next, o);
-      next = other < next ? other : next;
-    }
-    const int a = __builtin_amdgcn_readfirstlane(next);
-    if (a == 0x7fffffff) return;
-    prev = a;
+  for (int i = 0; i < TI; ++i) same = same && (id[i] == a0 || m0 + 16 * i + r >= M);
+  if (__all(same)) {
+    if (a0 < 0) return;
     for (int c = 0; c < t.R; c += 32) {
       const int j0 = c + 8 * g;
-      const bool in = j0 < t.R;  // whole chunks of 8: R is a multiple of 8
       bf16x8 w[TJ];
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        const int64_t n = n0 + 16 * j + r;
-        i32x4 v = {0, 0, 0, 0};
-        if (in && n < t.N) {
-          if constexpr (KMAJOR) {
-            const uint16_t *p = t.W + ((int64_t)a * t.R + j0) * t.N + n;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[e] = (int)((uint32_t)p[(int64_t)(2 * e) * t.N] |
-                           ((uint32_t)p[(int64_t)(2 * e + 1) * t.N] << 16));
-          } else {
-            v = *reinterpret_cast<const i32x4 *>(t.W + ((int64_t)a * t.N + n) * t.R + j0);
-          }
-        }
-        w[j] = __builtin_bit_cast(bf16x8, v);
-      }
+      for (int j = 0; j < TJ; ++j) w[j] = lora_w_frag<KMAJOR>(t, a0, KMAJOR ? n0 + TJ * r + j : n0 + 16 * j + r, j0);
+      const float *h = t.h + m0 * t.R;
 #pragma unroll
       for (int i = 0; i < TI; ++i) {
-        const uint64_t has = __ballot(id[i] == a);
-        if (has == 0) continue;
-        // bit v: output row 4 g + v is the adapter's. Kept opaque, so that the
-        // masks of all blocks are not hoisted out of the loop into registers.
-        uint32_t own = (uint32_t)(has >> (4 * g));
-        asm volatile("" : "+v"(own));
-        float hv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (in && id[i] == a) {
-          // opaque for the same reason (a lane offset, not TI hoisted addresses)
-          uint32_t ho = (uint32_t)(r * t.R + j0);
-          asm volatile("" : "+v"(ho));
-          const float *hm = t.h + (m0 + 16 * i) * t.R + ho;
-          const f32x4 h0 = *reinterpret_cast<const f32x4 *>(hm);
-          const f32x4 h1 = *reinterpret_cast<const f32x4 *>(hm + 4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            hv[e] = h0[e];
-            hv[4 + e] = h1[e];
-          }
-        }
+        const int row = 16 * i + r;
         bf16x8 hi, lo;
-        split_bf16(hv, hi, lo);
+        lora_h_frag(h + row * t.R + j0, j0 < t.R && m0 + row < M, hi, lo);
 #pragma unroll
         for (int j = 0; j < TJ; ++j) {
-          f32x4 d = {0.f, 0.f, 0.f, 0.f};
-          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[j], d, 0, 0, 0);
-          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[j], d, 0, 0, 0);
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            acc[i][j][v] += own & (1u << v) ? d[v] : 0.0f;
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[j], acc[i][j], 0, 0, 0);
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[j], acc[i][j], 0, 0, 0);
         }
-        // one block's operands at a time: hoisting the loads of all TI blocks
-        // would cost the registers that hold the accumulators
-        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < TI; ++i) {
+    int prev = -1;
+    for (;;) {
+      int next = id[i] > prev ? id[i] : 0x7fffffff;
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) {
+        const int other = __shfl_xor(next, o);
+        next = other < next ? other : next;
+      }
+      const int a = __builtin_amdgcn_readfirstlane(next);
+      if (a == 0x7fffffff) break;
+      prev = a;
+      const uint32_t own = (uint32_t)(__ballot(id[i] == a) >> (4 * g));  // bit v: row 4 g + v
+      for (int c = 0; c < t.R; c += 32) {
+        const int j0 = c + 8 * g;
+        bf16x8 hi, lo;
+        lora_h_frag(t.h + (m0 + 16 * i + r) * t.R + j0, j0 < t.R && id[i] == a, hi, lo);
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+          const bf16x8 w =
+              lora_w_frag<KMAJOR>(t, a, KMAJOR ? n0 + TJ * r + j : n0 + 16 * j + r, j0);
+          f32x4 d = {0.f, 0.f, 0.f, 0.f};
+          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w, d, 0, 0, 0);
+          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w, d, 0, 0, 0);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[i][j][v] += own & (1u << v) ? d[v] : 0.0f;
+        }
       }
     }
   }

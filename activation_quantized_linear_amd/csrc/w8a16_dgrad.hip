@@ -5,25 +5,27 @@
 // rounding (at most 2^-8 relative) per weight, which is what a bf16 copy of the
 // dequantized weight would hold; products and sums are float32.
 //
-// Tile: 16 TI rows of dy x 32 NWV columns of dx per workgroup of NWV waves side
-// by side along K, each 16 TI x 32, over stages of 64 channels. Operands go
+// Tile: 16 TI rows of dy x 256 columns of dx per workgroup of 4 waves side by
+// side along K, each 16 TI x 64, over stages of 64 channels. Operands go
 // global -> LDS by buffer loads that write LDS directly: dy as rows of 128 B,
-// the weights as they lie, 64 channel rows of 32 NWV bytes, and each wave's own
-// copy of the stage's 64 scales. q has the contraction as its slow axis; the
-// byte-transposing LDS read (8 rows x 16 columns per 16 lanes) hands each lane
-// the 8 channels of one column that the matrix instruction wants, so no
-// transposed copy of the weights exists anywhere.
+// the weights as they lie, 64 channel rows of 256 B, and each wave's own copy
+// of the stage's 64 scales, one a lane. q has the contraction as its slow axis:
+// a lane reads one dword (4 columns) of each of the 8 channel rows it needs, and
+// byte j of the eight is its operand for columns 4 r + j, so the matrix
+// instructions take the columns in strides of 4 and nothing is transposed,
+// neither in memory nor in registers. The scales come to the multiplies by lane
+// broadcasts within a row of 16 (DPP), without an LDS read of their own.
 // A ring of SG stages keeps loads in flight behind exact vmcnt waits. dy rows
-// store their 16-byte chunks XOR-swizzled by (row / 2) mod 8 and weight rows by
-// the row (by row / 2 for 128-byte rows), which spreads each half wave's reads
-// over all banks.
+// store their 16-byte chunks XOR-swizzled by (row / 2) mod 8, and weight rows
+// theirs by 4 (row / 8 mod 4), which spreads each read over all banks.
 #include "w8a16_dgrad.h"
+
+#include <type_traits>
 
 namespace aql {
 namespace {
 
 typedef __attribute__((address_space(3))) void lds_void;
-typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
 
 constexpr int BC = 64;           // channels a stage
 constexpr int OOB = 0x40000000;  // past any range: loads give 0
@@ -45,11 +47,14 @@ __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t rr, uint32_t dst, 
 
 constexpr int vmcnt_imm(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
 
-template <int TI, int NWV, int SG>
+constexpr int NWV = 4, TJ = 4;  // waves of a workgroup, 16-column blocks of a wave
+
+template <int TI, int SG>
 struct DgradLds {
-  static constexpr int BM = 16 * TI, BK = 32 * NWV;
+  static constexpr int BM = 16 * TI, BK = 256;
   static constexpr int NX = BM / 8 / NWV;     // dy loads per wave and stage (8 rows x 128 B)
-  static constexpr int NL = NX + 2 + 1;       // + weights (1 KB each) + scales
+  static constexpr int NQ = BC * BK / 1024 / NWV;  // weight loads (1 KB each)
+  static constexpr int NL = NX + NQ + 1;      // + scales
   static constexpr int XS = BM * 128, QS = BC * BK, SS = NWV * 256;
   static constexpr int STAGE = XS + QS + SS;
   static constexpr int RING = SG * STAGE;
@@ -59,29 +64,43 @@ struct DgradLds {
   static constexpr int TILEF = BM * TLDF * 4;
   static constexpr int BYTES = RING > TILE ? RING : TILE;
   static constexpr int BYTES_SPLIT = RING > TILEF ? RING : TILEF;
-  static_assert(NX * NWV * 8 == BM, "dy loads split evenly");
+  static_assert(NX * NWV * 8 == BM && NQ * NWV * 1024 == BC * BK, "loads split evenly");
+  static_assert(NL * (SG - 1) < 64, "vmcnt");
 };
 
-// Eight codes (rows n .. n + 7 of a column) times their scales, as bf16.
-__device__ __forceinline__ bf16x8 widen_scaled(i32x2 w, const float (&s)[8]) {
+// The value of lane N of each row of 16 (a DPP operand of the multiply that takes it).
+template <int N>
+__device__ __forceinline__ float row_lane(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+      0, (int)__float_as_uint(v), 0x150 + N, 0xf, 0xf, false));
+}
+
+// Byte J of eight codes (channels n .. n + 7) times their scales, as bf16. Lane t
+// of a row of 16 holds the scale of channel 32 (t / 8) + 8 g + t % 8 of the
+// stage, so half KK's eight are lanes 8 KK .. 8 KK + 7 of the row.
+template <int KK, int J>
+__device__ __forceinline__ bf16x8 widen_scaled(const int (&w)[8], float s) {
   bf16x8 b;
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    b[e] = (__bf16)((float)(int8_t)(w[e >> 2] >> (8 * (e & 3))) * s[e]);
+  b[0] = (__bf16)((float)(int8_t)(w[0] >> (8 * J)) * row_lane<8 * KK>(s));
+  b[1] = (__bf16)((float)(int8_t)(w[1] >> (8 * J)) * row_lane<8 * KK + 1>(s));
+  b[2] = (__bf16)((float)(int8_t)(w[2] >> (8 * J)) * row_lane<8 * KK + 2>(s));
+  b[3] = (__bf16)((float)(int8_t)(w[3] >> (8 * J)) * row_lane<8 * KK + 3>(s));
+  b[4] = (__bf16)((float)(int8_t)(w[4] >> (8 * J)) * row_lane<8 * KK + 4>(s));
+  b[5] = (__bf16)((float)(int8_t)(w[5] >> (8 * J)) * row_lane<8 * KK + 5>(s));
+  b[6] = (__bf16)((float)(int8_t)(w[6] >> (8 * J)) * row_lane<8 * KK + 6>(s));
+  b[7] = (__bf16)((float)(int8_t)(w[7] >> (8 * J)) * row_lane<8 * KK + 7>(s));
   return b;
 }
 
 // SPLIT: unit (tile, sp) takes the ks stages from sp * ks and writes its fp32
 // sums to part[sp][M][K]; k_w8a16_dgrad_reduce adds them.
-template <int TI, int NWV, int SG, bool SPLIT, class LT>
-__global__ __launch_bounds__(64 * NWV, SG == 2 ? NWV / 2 : NWV / 4) void k_w8a16_dgrad(
+template <int TI, int SG, bool SPLIT, class LT>
+__global__ __launch_bounds__(64 * NWV, 2) void k_w8a16_dgrad(
     const uint16_t *__restrict__ dy, const int8_t *__restrict__ q,
     const float *__restrict__ scale, uint16_t *__restrict__ dx, int64_t M, int64_t N, int64_t K,
     int tiles_m, int tiles_k, float *__restrict__ part, int ks, LT lt) {
-  using L = DgradLds<TI, NWV, SG>;
-  constexpr int BM = L::BM, BK = L::BK, NX = L::NX, NL = L::NL;
-  constexpr int CH = BK / 16;      // 16-byte chunks of a weight row
-  constexpr int RPL = 1024 / BK;   // weight rows a load covers
+  using L = DgradLds<TI, SG>;
+  constexpr int BM = L::BM, BK = L::BK, NX = L::NX, NQ = L::NQ, NL = L::NL;
   extern __shared__ __attribute__((aligned(16))) char smem[];
 
   const int nt = tiles_m * tiles_k;
@@ -108,109 +127,125 @@ __global__ __launch_bounds__(64 * NWV, SG == 2 ? NWV / 2 : NWV / 4) void k_w8a16
     xoff[i] = (uint32_t)row * (uint32_t)(2 * N) + 16u * c;
     xlim[i] = row < mval ? (int)((N - 8 * c + BC - 1) / BC) : 0;
   }
-  auto qswz = [](int row) { return CH == 16 ? row & 15 : (row >> 1) & 7; };
-  int qrow[2];
-  uint32_t qoff[2];
-  bool qin[2];
+  int qrow[NQ];
+  uint32_t qoff[NQ];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    qrow[i] = RPL * (i * NWV + wave) + lane / CH;
-    const int c = (lane % CH) ^ qswz(qrow[i]);
+  for (int i = 0; i < NQ; ++i) {
+    qrow[i] = 4 * (i * NWV + wave) + (lane >> 4);
+    const int c = (lane & 15) ^ (4 * ((qrow[i] >> 3) & 3));
     qoff[i] = (uint32_t)qrow[i] * (uint32_t)K + 16u * c;
-    qin[i] = k0 + 16 * c < K;
+    if (k0 + 16 * c >= K) qrow[i] = OOB;  // a column past K: never loaded
   }
+  const int soff = 32 * ((lane >> 3) & 1) + 8 * g + (lane & 7);  // the lane's channel of a stage
   const uint32_t lds_base = (uint32_t)(uintptr_t)smem;
-  auto issue = [&](int kt) {
-    const uint32_t st = lds_base + (uint32_t)((kt % SG) * L::STAGE);
+  // stage kt into ring slot `slot`; past N everything reads as zero
+  auto issue = [&](int kt, int slot) {
+    const uint32_t st = lds_base + (uint32_t)(slot * L::STAGE);
 #pragma unroll
     for (int i = 0; i < NX; ++i)
       to_lds<16>(rx, st + 1024u * (i * NWV + wave),
                  kt < xlim[i] ? (int)(xoff[i] + 128u * (uint32_t)kt) : OOB);
     const int64_t n0 = (int64_t)BC * kt;
-    const __amdgpu_buffer_rsrc_t rq = rsrc(q + n0 * K + k0, 0x3fffffffu);
+    const int64_t left = N - n0;
+    const int rows = left < BC ? (int)left : BC;  // not positive past the end: none
+    const __amdgpu_buffer_rsrc_t rq = rsrc(q + (left > 0 ? n0 : 0) * K + k0, 0x3fffffffu);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      to_lds<16>(rq, st + L::XS + 1024u * (i * NWV + wave),
-                 qin[i] && n0 + qrow[i] < N ? (int)qoff[i] : OOB);
-    const int64_t ns = n0 + lane;
-    to_lds<4>(rs, st + L::XS + L::QS + 256u * wave, ns < N ? (int)(4 * ns) : OOB);
+    for (int i = 0; i < NQ; ++i)
+      to_lds<16>(rq, st + L::XS + 1024u * (i * NWV + wave), qrow[i] < rows ? (int)qoff[i] : OOB);
+    to_lds<4>(rs, st + L::XS + L::QS + 256u * wave, soff < rows ? (int)(4 * (n0 + soff)) : OOB);
   };
 
-  int fxo[2][TI], fqo[2][2];
-#pragma unroll
-  for (int kk = 0; kk < 2; ++kk) {
-#pragma unroll
-    for (int i = 0; i < TI; ++i) {
-      const int R = i * 16 + r;
-      fxo[kk][i] = R * 128 + 16 * ((4 * kk + g) ^ ((R >> 1) & 7));
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      // lanes 2 e and 2 e + 1 of 16 address row e's 16 columns
-      const int n = 32 * kk + 8 * g + (r >> 1);
-      fqo[kk][j] = L::XS + n * BK + 16 * ((2 * wave + j) ^ qswz(n)) + 8 * (r & 1);
-    }
-  }
+  // fragment offsets within a stage. dy: block i adds 2048 i, half kk flips bit
+  // 6 (chunk 4 kk + g under the swizzle); weights: half kk adds 32 rows, channel
+  // e of the lane's eight adds e rows
+  const int fx = r * 128 + 16 * (g ^ ((r >> 1) & 7));
+  const int fq = L::XS + 8 * g * BK + 16 * ((4 * wave + (r >> 2)) ^ (4 * g)) + 4 * (r & 3);
+  const int fs = L::XS + L::QS + 256 * wave + 4 * lane;
 
-  f32x4 acc[TI][2];
+  f32x4 acc[TI][TJ];
 #pragma unroll
   for (int i = 0; i < TI; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  auto compute = [&](int kt) {
-    const char *st = smem + (kt % SG) * L::STAGE;
+  // Software pipeline over the 32-channel halves of the stages. While the matrix
+  // core works on one half, the next half's weights come from LDS and are
+  // widened between the matrix instructions, and each block of dy is replaced by
+  // the next half's as soon as its products are issued, so only the widened
+  // weights are held twice.
+  bf16x8 fa[TI], b0[TJ], b1[TJ];
+  int raw[8];
+  float sv;
+  auto read_w = [&](const char *st, auto kk) {
+    constexpr int KK = decltype(kk)::value;
+    if constexpr (KK == 0) sv = *reinterpret_cast<const float *>(st + fs);
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      const float *sl = reinterpret_cast<const float *>(st + L::XS + L::QS + 256 * wave) + 32 * kk +
-                        8 * g;
-      const f32x4 s0 = *reinterpret_cast<const f32x4 *>(sl);
-      const f32x4 s1 = *reinterpret_cast<const f32x4 *>(sl + 4);
-      const float s[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
-      bf16x8 fa[TI], fb[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        fb[j] = widen_scaled(__builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                                 (lds_i32x2 *)(uintptr_t)((uint32_t)(uintptr_t)st + fqo[kk][j])),
-                             s);
-#pragma unroll
-      for (int i = 0; i < TI; ++i) fa[i] = *reinterpret_cast<const bf16x8 *>(st + fxo[kk][i]);
-      __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-      for (int i = 0; i < TI; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
-      __builtin_amdgcn_s_setprio(0);
-    }
+    for (int e = 0; e < 8; ++e)
+      raw[e] = *reinterpret_cast<const int *>(st + fq + (32 * KK + e) * BK);
   };
+  auto read_x = [&](const char *st, auto kk, int i) {
+    fa[i] = *reinterpret_cast<const bf16x8 *>(st + (fx ^ (64 * decltype(kk)::value)) + 2048 * i);
+  };
+  auto widen = [&](auto kk, bf16x8 (&b)[TJ]) {
+    constexpr int KK = decltype(kk)::value;
+    b[0] = widen_scaled<KK, 0>(raw, sv);
+    b[1] = widen_scaled<KK, 1>(raw, sv);
+    b[2] = widen_scaled<KK, 2>(raw, sv);
+    b[3] = widen_scaled<KK, 3>(raw, sv);
+  };
+  // the products of the half in fa and b; st and kk: the next half
+  auto half = [&](const char *st, auto kk, const bf16x8 (&b)[TJ], bf16x8 (&next)[TJ]) {
+    read_w(st, kk);
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], b[j], acc[i][j], 0, 0, 0);
+      read_x(st, kk, i);
+    }
+    widen(kk, next);
+    __builtin_amdgcn_sched_group_barrier(0x100, 9, 0);  // DS reads: the weights
+    __builtin_amdgcn_sched_group_barrier(0x008, TJ, 0);  // MFMA
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+#pragma unroll
+    for (int i = 1; i < TI; ++i) {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, TI == 8 ? 4 : 8, 0);  // VALU
+      }
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  std::integral_constant<int, 0> h0;
+  std::integral_constant<int, 1> h1;
 
   const int nk_all = (int)((N + BC - 1) / BC);
   const int kb = SPLIT ? sp * ks : 0;
-  const int nk = SPLIT ? (kb + ks < nk_all ? kb + ks : nk_all) : nk_all;
+  const int nk = (SPLIT ? (kb + ks < nk_all ? kb + ks : nk_all) : nk_all) - kb;  // stages
 #pragma unroll
-  for (int s = 0; s < SG - 1; ++s) issue(kb + s);
-  int kt = kb;
-  auto step = [&](int k) {
+  for (int s = 0; s < SG; ++s) issue(s < nk ? kb + s : nk_all, s);
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(NL * (SG - 1)));
+  __builtin_amdgcn_s_barrier();  // stage 0 complete everywhere
+  const char *st = smem;
+  read_w(st, h0);
+#pragma unroll
+  for (int i = 0; i < TI; ++i) read_x(st, h0, i);
+  widen(h0, b0);
+  // Stage t: its second half is read under the first half's products; then its
+  // slot is free and takes stage t + SG (zeros past the last), stage t + 1 must
+  // have landed, and its first half is read under the second half's products.
+  int slot = 0;
+  for (int t = 0; t < nk; ++t) {
+    half(st, h1, b0, b1);
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's reads of the slot are done
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(NL * (SG - 2)));
-    __builtin_amdgcn_s_barrier();  // stage k complete everywhere; slot of k - 1 free
-    issue(k + SG - 1);
-    compute(k);
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // this stage's fragment reads done
-  };
-  const int nmain = nk - (SG - 1);
-  for (; kt < nmain; ++kt) step(kt);
-#pragma unroll
-  for (int t = 0; t < SG - 1; ++t) {
-    if (kt < nk) {
-      if (t == 0) __builtin_amdgcn_s_waitcnt(vmcnt_imm(NL * (SG - 2)));
-      else if (t == 1) __builtin_amdgcn_s_waitcnt(vmcnt_imm(SG > 3 ? NL * (SG - 3) : 0));
-      else __builtin_amdgcn_s_waitcnt(0x0F70);
-      __builtin_amdgcn_s_barrier();
-      compute(kt);
-      __builtin_amdgcn_s_waitcnt(0xC07F);
-    }
-    ++kt;
+    __builtin_amdgcn_s_barrier();
+    issue(t + SG < nk ? kb + t + SG : nk_all, slot);
+    slot = slot + 1 == SG ? 0 : slot + 1;
+    st = smem + slot * L::STAGE;
+    half(st, h0, b1, b0);
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);
   __syncthreads();
@@ -218,12 +253,11 @@ __global__ __launch_bounds__(64 * NWV, SG == 2 ? NWV / 2 : NWV / 4) void k_w8a16
   if constexpr (SPLIT) {
     float *tf = reinterpret_cast<float *>(smem);
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int i = 0; i < TI; ++i)
 #pragma unroll
-      for (int i = 0; i < TI; ++i)
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          tf[(i * 16 + 4 * g + v) * L::TLDF + wave * 32 + j * 16 + r] = acc[i][j][v];
+      for (int v = 0; v < 4; ++v)
+        *reinterpret_cast<f32x4 *>(tf + (i * 16 + 4 * g + v) * L::TLDF + 64 * wave + 4 * r) =
+            f32x4{acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]};
     __syncthreads();
     float *pb = part + (int64_t)sp * M * K;
     for (int u = tid; u < BM * (BK / 4); u += 64 * NWV) {
@@ -235,15 +269,18 @@ __global__ __launch_bounds__(64 * NWV, SG == 2 ? NWV / 2 : NWV / 4) void k_w8a16
     }
     return;
   }
-  if constexpr (LT::on) lora_add_tile<true>(acc, lt, m0, M, k0 + 32 * wave);
+  // acc[i][j] lane (r, g): rows 16 i + 4 g + v, column 64 wave + 4 r + j
+  if constexpr (LT::on) lora_add_tile<true>(acc, lt, m0, M, k0 + 64 * wave);
   uint16_t *tl = reinterpret_cast<uint16_t *>(smem);
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
+  for (int i = 0; i < TI; ++i)
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        tl[(i * 16 + 4 * g + v) * L::TLD + wave * 32 + j * 16 + r] = f32_to_bf16_rne(acc[i][j][v]);
+    for (int v = 0; v < 4; ++v) {
+      const uint32_t lo = f32_to_bf16_rne(acc[i][0][v]) | ((uint32_t)f32_to_bf16_rne(acc[i][1][v]) << 16);
+      const uint32_t hi = f32_to_bf16_rne(acc[i][2][v]) | ((uint32_t)f32_to_bf16_rne(acc[i][3][v]) << 16);
+      *reinterpret_cast<i32x2 *>(tl + (i * 16 + 4 * g + v) * L::TLD + 64 * wave + 4 * r) =
+          i32x2{(int)lo, (int)hi};
+    }
   __syncthreads();
   for (int u = tid; u < BM * (BK / 8); u += 64 * NWV) {
     const int row = u / (BK / 8), c = u % (BK / 8);
@@ -289,12 +326,12 @@ __global__ __launch_bounds__(256) void k_w8a16_dgrad_reduce(const float *__restr
   *reinterpret_cast<i32x2 *>(dx + m * K + k) = i32x2{(int)lo, (int)hi};
 }
 
-template <int TI, int NWV, int SG, class LT>
+template <int TI, int SG, class LT>
 hipError_t go(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q, const float *scale,
               int64_t K, uint16_t *dx, hipStream_t st, const LT &lt) {
-  using L = DgradLds<TI, NWV, SG>;
+  using L = DgradLds<TI, SG>;
   void (*kern)(const uint16_t *, const int8_t *, const float *, uint16_t *, int64_t, int64_t, int64_t,
-               int, int, float *, int, LT) = k_w8a16_dgrad<TI, NWV, SG, false, LT>;
+               int, int, float *, int, LT) = k_w8a16_dgrad<TI, SG, false, LT>;
   (void)hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize,
                             L::BYTES);
   (void)hipGetLastError();
@@ -304,12 +341,12 @@ hipError_t go(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q, const f
   return hipGetLastError();
 }
 
-template <int TI, int NWV, int SG, class LT>
+template <int TI, int SG, class LT>
 hipError_t go_split(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q, const float *scale,
                     int64_t K, uint16_t *dx, float *part, int S, hipStream_t st, const LT &lt) {
-  using L = DgradLds<TI, NWV, SG>;
+  using L = DgradLds<TI, SG>;
   void (*kern)(const uint16_t *, const int8_t *, const float *, uint16_t *, int64_t, int64_t, int64_t,
-               int, int, float *, int, NoLora) = k_w8a16_dgrad<TI, NWV, SG, true, NoLora>;
+               int, int, float *, int, NoLora) = k_w8a16_dgrad<TI, SG, true, NoLora>;
   (void)hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize,
                             L::BYTES_SPLIT);
   (void)hipGetLastError();
@@ -331,22 +368,21 @@ hipError_t launch(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q, con
                   int64_t K, uint16_t *dx, float *part, size_t part_bytes, hipStream_t st,
                   const LT &lt) {
   const int64_t twide = ((M + 127) / 128) * ((K + 255) / 256);
-  if (twide >= 512) return go<8, 8, 2>(dy, M, N, q, scale, K, dx, st, lt);
-  if (twide >= 160) return go<8, 8, 4>(dy, M, N, q, scale, K, dx, st, lt);
+  if (twide >= 160) return go<8, 4>(dy, M, N, q, scale, K, dx, st, lt);
   const int S = w8a16_dgrad_splits(M, N, K);
   if (S > 1 && part && part_bytes >= w8a16_dgrad_part_bytes(M, N, K))
-    return go_split<4, 4, 4>(dy, M, N, q, scale, K, dx, part, S, st, lt);
-  return go<4, 4, 4>(dy, M, N, q, scale, K, dx, st, lt);
+    return go_split<4, 4>(dy, M, N, q, scale, K, dx, part, S, st, lt);
+  return go<4, 4>(dy, M, N, q, scale, K, dx, st, lt);
 }
 
 }  // namespace
 
-// 64 x 128 tiles split while the units stay within two a CU and each keeps at
+// 64 x 256 tiles split while the units stay within two a CU and each keeps at
 // least 8 stages of 64 channels.
 int w8a16_dgrad_splits(int64_t M, int64_t N, int64_t K) {
   const int64_t twide = ((M + 127) / 128) * ((K + 255) / 256);
   if (twide >= 160) return 1;
-  const int64_t tiles = ((M + 63) / 64) * ((K + 127) / 128), nk = (N + BC - 1) / BC;
+  const int64_t tiles = ((M + 63) / 64) * ((K + 255) / 256), nk = (N + BC - 1) / BC;
   int S = 1;
   while (S < 32 && tiles * 2 * S <= 512 && nk / (2 * S) >= 8) S *= 2;
   return S;
