@@ -644,10 +644,9 @@ def aql_linear_w8a16_dgrad(dy, q, scale, dx=None, workspace=None):
     _need(scale, "scale", torch.float32, 1, dev)
     _shape(scale, "scale", (N,))
     dx = _out(dx, "dx", (M, K), torch.bfloat16, dev)
-    nbytes = aql_workspace_bytes(AQL_OP_W8A16_DGRAD, M, N, K)
-    ws = _workspace(workspace, nbytes, dev) if workspace is not None or nbytes > 0 else None
+    ws = _workspace(workspace, aql_workspace_bytes(AQL_OP_W8A16_DGRAD, M, N, K), dev)
     _call("aql_linear_w8a16_dgrad", dev, _ptr(dy), M, N, _ptr(q), _ptr(scale), K, _ptr(dx),
-          _ptr(ws), 0 if ws is None else ws.numel())
+          _ptr(ws), ws.numel())
     return dx
 
 

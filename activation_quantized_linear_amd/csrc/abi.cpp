@@ -184,7 +184,7 @@ static_assert(AQL_LORA_MAX_ADAPTERS == aql::kLoraMaxAdapters &&
                   AQL_LORA_MAX_RANK == aql::kLoraMaxRank && AQL_CKPT_GROUP == aql::kCkptGroup,
               "adapter bounds");
 
-// u [M, R], then the partial sums of dx.
+// u [M, R], then the workspace of dx.
 size_t lora_bwd_u_bytes(int64_t M, int64_t R) { return align256((size_t)M * (size_t)R * 4); }
 
 // Validation shared by both static W8A8 entry points (all before any HIP call).
@@ -291,8 +291,8 @@ size_t aql_workspace_bytes(int op, int64_t M, int64_t N, int64_t K) {
     return aql::w8a16_gemm_part_bytes(M, N, K);
   }
   if (op == AQL_OP_W8A16_DGRAD) {
-    if (M == 0 || K == 0 || K > kMaxKW8A16) return 0;
-    return aql::w8a16_dgrad_part_bytes(M, N, K);
+    if (M == 0 || M > kMaxRows || K == 0 || K > kMaxKW8A16 || N > (1LL << 22)) return 0;
+    return aql::w8a16_dgrad_bytes(M, N, K);
   }
   return 0;
 }
@@ -677,17 +677,19 @@ int aql_linear_w8a16_dgrad(const uint16_t *dy, int64_t M, int64_t N, const int8_
   if (M == 0) return ok();
   REQUIRE(dx && (N == 0 || (dy && q && scale)), AQL_ERR_NULL,
           "%s: dy, q, scale and dx must not be NULL", fn);
+  const size_t need = aql::w8a16_dgrad_bytes(M, N, K);
+  REQUIRE(ws && ws_bytes >= need, AQL_ERR_WORKSPACE, "%s: workspace needs %zu bytes (got %zu)", fn,
+          need, ws ? ws_bytes : (size_t)0);
   if (int e = check_device(fn)) return e;
-  return launched(aql::launch_w8a16_dgrad(dy, M, N, q, scale, K, dx, static_cast<float *>(ws),
-                                          ws ? ws_bytes : 0, (hipStream_t)stream),
-                  fn);
+  return launched(
+      aql::launch_w8a16_dgrad(dy, M, N, q, scale, K, dx, ws, (hipStream_t)stream), fn);
 }
 
 size_t aql_lora_backward_bytes(int64_t M, int64_t N, int64_t K, int64_t R) {
-  if (M <= 0 || M > kMaxRows || N < 0 || K < 16 || K > kMaxKW8A16 || R < 8 ||
+  if (M <= 0 || M > kMaxRows || N < 0 || N > (1LL << 22) || K < 16 || K > kMaxKW8A16 || R < 8 ||
       R > AQL_LORA_MAX_RANK)
     return 0;
-  return lora_bwd_u_bytes(M, R) + aql::w8a16_dgrad_part_bytes(M, N, K);
+  return lora_bwd_u_bytes(M, R) + aql::w8a16_dgrad_bytes(M, N, K);
 }
 
 int aql_linear_w8a16_lora_backward(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q,
@@ -740,9 +742,8 @@ int aql_linear_w8a16_lora_backward(const uint16_t *dy, int64_t M, int64_t N, con
   }
   if (dx && M > 0) {
     const aql::LoraTerm lt{u, A, p + aql::lora_plan_layout(M, L).idx, (int32_t)R, K};
-    const size_t ub = lora_bwd_u_bytes(M, R);
-    float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + ub);
-    e = aql::launch_w8a16_dgrad(dy, M, N, q, scale, K, dx, part, ws_bytes - ub, st, lt);
+    e = aql::launch_w8a16_dgrad(dy, M, N, q, scale, K, dx,
+                                static_cast<char *>(ws) + lora_bwd_u_bytes(M, R), st, lt);
   }
   return launched(e, fn);
 }

@@ -118,23 +118,42 @@ __device__ __forceinline__ void lora_h_frag(const float *h, bool in, bf16x8 &hi,
   split_bf16(v, hi, lo);
 }
 
-// Its other operand: column n of the output, ranks j0 .. j0 + 7 of adapter a.
-// KMAJOR: W is [L, R, N] (contraction rows), else [L, N, R].
-template <bool KMAJOR>
-__device__ __forceinline__ bf16x8 lora_w_frag(const LoraTerm &t, int a, int64_t n, int j0) {
-  i32x4 v = {0, 0, 0, 0};
-  if (j0 < t.R && n < t.N) {  // whole chunks of 8: R is a multiple of 8
-    if constexpr (KMAJOR) {
-      const uint16_t *p = t.W + ((int64_t)a * t.R + j0) * t.N + n;
+// Its other operand, for a wave's TJ blocks of columns: ranks j0 .. j0 + 7 of
+// adapter a. W [L, N, R]: block j's column is n + 16 j, its ranks lie together.
+// KMAJOR, W [L, R, N] (contraction rows): block j's column is n + j, so the four
+// blocks' values of a rank are one 8-byte load, and pairs of ranks are packed.
+template <bool KMAJOR, int TJ>
+__device__ __forceinline__ void lora_w_frags(const LoraTerm &t, int a, int64_t n, int j0,
+                                             bf16x8 (&w)[TJ]) {
+  const bool jin = j0 < t.R;  // whole chunks of 8: R is a multiple of 8
+  if constexpr (KMAJOR) {
+    static_assert(TJ == 4, "four columns a lane");
+    i32x2 d[8];
+    const uint16_t *p = t.W + ((int64_t)a * t.R + j0) * t.N + n;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      d[e] = i32x2{0, 0};
+      if (jin && n < t.N) d[e] = *reinterpret_cast<const i32x2 *>(p + (int64_t)e * t.N);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      i32x4 v;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        v[e] = (int)((uint32_t)p[(int64_t)(2 * e) * t.N] |
-                     ((uint32_t)p[(int64_t)(2 * e + 1) * t.N] << 16));
-    } else {
-      v = *reinterpret_cast<const i32x4 *>(t.W + ((int64_t)a * t.N + n) * t.R + j0);
+        v[e] = (int)__builtin_amdgcn_perm((uint32_t)d[2 * e + 1][j >> 1], (uint32_t)d[2 * e][j >> 1],
+                                          j & 1 ? 0x07060302u : 0x05040100u);
+      w[j] = __builtin_bit_cast(bf16x8, v);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      const int64_t nj = n + 16 * j;
+      i32x4 v = {0, 0, 0, 0};
+      if (jin && nj < t.N)
+        v = *reinterpret_cast<const i32x4 *>(t.W + ((int64_t)a * t.N + nj) * t.R + j0);
+      w[j] = __builtin_bit_cast(bf16x8, v);
     }
   }
-  return __builtin_bit_cast(bf16x8, v);
 }
 
 // acc[i][j] += h . W_a^T over a wave's tile of MFMA blocks: 16 TI rows from m0
@@ -150,6 +169,7 @@ template <bool KMAJOR, int TI, int TJ>
 __device__ __forceinline__ void lora_add_tile(f32x4 (&acc)[TI][TJ], const LoraTerm &t, int64_t m0,
                                               int64_t M, int64_t n0) {
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int64_t n = KMAJOR ? n0 + TJ * r : n0 + r;
   int id[TI];
   bool same = true;
 #pragma unroll
@@ -165,8 +185,7 @@ __device__ __forceinline__ void lora_add_tile(f32x4 (&acc)[TI][TJ], const LoraTe
     for (int c = 0; c < t.R; c += 32) {
       const int j0 = c + 8 * g;
       bf16x8 w[TJ];
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) w[j] = lora_w_frag<KMAJOR>(t, a0, KMAJOR ? n0 + TJ * r + j : n0 + 16 * j + r, j0);
+      lora_w_frags<KMAJOR>(t, a0, n, j0, w);
       const float *h = t.h + m0 * t.R;
 #pragma unroll
       for (int i = 0; i < TI; ++i) {
@@ -200,13 +219,13 @@ __device__ __forceinline__ void lora_add_tile(f32x4 (&acc)[TI][TJ], const LoraTe
         const int j0 = c + 8 * g;
         bf16x8 hi, lo;
         lora_h_frag(t.h + (m0 + 16 * i + r) * t.R + j0, j0 < t.R && id[i] == a, hi, lo);
+        bf16x8 w[TJ];
+        lora_w_frags<KMAJOR>(t, a, n, j0, w);
 #pragma unroll
         for (int j = 0; j < TJ; ++j) {
-          const bf16x8 w =
-              lora_w_frag<KMAJOR>(t, a, KMAJOR ? n0 + TJ * r + j : n0 + 16 * j + r, j0);
           f32x4 d = {0.f, 0.f, 0.f, 0.f};
-          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w, d, 0, 0, 0);
-          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w, d, 0, 0, 0);
+          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[j], d, 0, 0, 0);
+          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[j], d, 0, 0, 0);
 #pragma unroll
           for (int v = 0; v < 4; ++v) acc[i][j][v] += own & (1u << v) ? d[v] : 0.0f;
         }

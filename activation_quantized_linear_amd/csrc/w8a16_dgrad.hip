@@ -1,21 +1,25 @@
 // Gradient of the W8A16 linear to its input: dx[m, k] = sum_n dy[m, n] scale[n] q[n, k].
 //
-// The contraction runs over the output channels, so the channel scale no longer
-// factors out of the sum: the weights are widened to bf16(scale[n] q[n, k]), one
-// rounding (at most 2^-8 relative) per weight, which is what a bf16 copy of the
-// dequantized weight would hold; products and sums are float32.
+// The contraction runs over the output channels, so the channel scale does not
+// factor out of the sum. It goes to dy's side, once per element instead of once
+// per use of a weight: a first kernel writes d[m, n] = dy[m, n] scale[n] 2^e[m]
+// as float16, the row's exponent e[m] bringing its largest product to
+// [2^13, 2^14). float16 holds 11 bits where bf16 holds 8, so this rounding
+// (2^-11 at most, and 2^-38 of the row's largest product for the tiny ones that
+// become subnormal) vanishes beside the output's, and the int8 codes are exact
+// in it. The product then runs on the float16 matrix cores with float32 sums,
+// and 2^-e comes back in the epilogue.
 //
-// Tile: 16 TI rows of dy x 256 columns of dx per workgroup of 4 waves side by
+// Tile: 16 TI rows of d x 256 columns of dx per workgroup of 4 waves side by
 // side along K, each 16 TI x 64, over stages of 64 channels. Operands go
-// global -> LDS by buffer loads that write LDS directly: dy as rows of 128 B,
-// the weights as they lie, 64 channel rows of 256 B, and each wave's own copy
-// of the stage's 64 scales, one a lane. q has the contraction as its slow axis:
-// a lane reads one dword (4 columns) of each of the 8 channel rows it needs, and
-// byte j of the eight is its operand for columns 4 r + j, so the matrix
-// instructions take the columns in strides of 4 and nothing is transposed,
-// neither in memory nor in registers. The scales come to the multiplies by lane
-// broadcasts within a row of 16 (DPP), without an LDS read of their own.
-// A ring of SG stages keeps loads in flight behind exact vmcnt waits. dy rows
+// global -> LDS by buffer loads that write LDS directly: d as rows of 128 B, the
+// weights as they lie, 64 channel rows of 256 B. q has the contraction as its
+// slow axis: a lane reads one dword (4 columns) of each of the 8 channel rows it
+// needs, and byte j of the eight is its operand for columns 4 r + j, so the
+// matrix instructions take the columns in strides of 4 and nothing is
+// transposed, in memory or in registers. d is padded with zeros to whole
+// stages, so what the last stage reads past N in q adds nothing.
+// A ring of SG stages keeps loads in flight behind exact vmcnt waits. d rows
 // store their 16-byte chunks XOR-swizzled by (row / 2) mod 8, and weight rows
 // theirs by 4 (row / 8 mod 4), which spreads each read over all banks.
 #include "w8a16_dgrad.h"
@@ -26,81 +30,153 @@ namespace aql {
 namespace {
 
 typedef __attribute__((address_space(3))) void lds_void;
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int BC = 64;           // channels a stage
-constexpr int OOB = 0x40000000;  // past any range: loads give 0
+constexpr int kTop = 14;         // exponent of a row's largest scaled product
+constexpr int kCode = 9;         // codes enter the matrix cores as q 2^-9
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *base, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes,
                                            0x00020000);
 }
 
-// SIZE bytes a lane from offset off into LDS at dst + SIZE lane.
-template <int SIZE>
-__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t rr, uint32_t dst, int off) {
-  lds_void *p = (lds_void *)(uintptr_t)__builtin_amdgcn_readfirstlane(dst);
-  if constexpr (SIZE == 16)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rr, p, 16, off, 0, 0, 0);
-  else
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rr, p, 4, off, 0, 0, 0);
+// ------------------------------------------------------------- scaling of dy
+
+// TPR threads a row, 8 values a thread and round; NI rounds are held in
+// registers between the maximum and the scaling, so dy is read once (NI = 0: any
+// N, read twice). Bound by memory: 4 bytes a value.
+template <int TPR, int NI>
+__global__ __launch_bounds__(256) void k_dgrad_scale(const uint16_t *__restrict__ dy,
+                                                     const float *__restrict__ scale, int64_t M,
+                                                     int64_t N, int64_t NP,
+                                                     uint16_t *__restrict__ d,
+                                                     int32_t *__restrict__ ex) {
+  __shared__ float red[8];
+  const int t = threadIdx.x % TPR;
+  const int64_t m = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
+  if (TPR == 64 && m >= M) return;  // whole waves (TPR 256: one row a workgroup)
+  const uint16_t *row = dy + m * N;
+  auto load = [&](int64_t n, float (&v)[8]) {
+    const i32x4 w = *reinterpret_cast<const i32x4 *>(row + n);
+    const f32x4 s0 = *reinterpret_cast<const f32x4 *>(scale + n);
+    const f32x4 s1 = *reinterpret_cast<const f32x4 *>(scale + n + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = (uint32_t)w[i];
+      v[2 * i] = __uint_as_float(u << 16) * (i < 2 ? s0[2 * i] : s1[2 * i - 4]);
+      v[2 * i + 1] = __uint_as_float(u & 0xffff0000u) * (i < 2 ? s0[2 * i + 1] : s1[2 * i - 3]);
+    }
+  };
+  float mx = 0.0f;
+  constexpr int NR = NI > 0 ? NI : 1;
+  float v[NR][8];
+  if constexpr (NI > 0) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int64_t n = 8 * (int64_t)(t + TPR * i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+      if (n < N) load(n, v[i]);  // whole chunks: N is a multiple of 8
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[i][e]));
+  } else {
+    for (int64_t n = 8 * (int64_t)t; n < N; n += 8 * TPR) {
+      load(n, v[0]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[0][e]));
+    }
+  }
+  mx = group_reduce_max<TPR>(mx, red);
+  const int e2 = kTop - __builtin_amdgcn_frexp_expf(mx);
+  if (t == 0) ex[m] = e2;
+  auto store = [&](int64_t n, const float (&x)[8]) {
+    f16x8 o;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = (_Float16)ldexpf(x[e], e2);
+    *reinterpret_cast<f16x8 *>(d + m * NP + n) = o;
+  };
+  if constexpr (NI > 0) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int64_t n = 8 * (int64_t)(t + TPR * i);
+      if (n < NP) store(n, v[i]);
+    }
+  } else {
+    for (int64_t n = 8 * (int64_t)t; n < NP; n += 8 * TPR) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[0][e] = 0.0f;
+      if (n < N) load(n, v[0]);
+      store(n, v[0]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------- product
+
+// 16 bytes a lane from offsets off + soff into LDS at dst + 16 lane.
+__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t rr, uint32_t dst, int off, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      rr, (lds_void *)(uintptr_t)__builtin_amdgcn_readfirstlane(dst), 16, off, soff, 0, 0);
 }
 
 constexpr int vmcnt_imm(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
+
+template <int I, int N, class F>
+__device__ __forceinline__ void static_for(F &&f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for<I + 1, N>(f);
+  }
+}
 
 constexpr int NWV = 4, TJ = 4;  // waves of a workgroup, 16-column blocks of a wave
 
 template <int TI, int SG>
 struct DgradLds {
   static constexpr int BM = 16 * TI, BK = 256;
-  static constexpr int NX = BM / 8 / NWV;     // dy loads per wave and stage (8 rows x 128 B)
+  static constexpr int NX = BM / 8 / NWV;  // d loads per wave and stage (8 rows x 128 B)
   static constexpr int NQ = BC * BK / 1024 / NWV;  // weight loads (1 KB each)
-  static constexpr int NL = NX + NQ + 1;      // + scales
-  static constexpr int XS = BM * 128, QS = BC * BK, SS = NWV * 256;
-  static constexpr int STAGE = XS + QS + SS;
+  static constexpr int NL = NX + NQ;
+  static constexpr int XS = BM * 128, QS = BC * BK;
+  static constexpr int STAGE = XS + QS;
   static constexpr int RING = SG * STAGE;
-  static constexpr int TLD = BK + 8;          // bf16 per staged output row
+  static constexpr int TLD = BK + 8;  // bf16 per staged output row
   static constexpr int TILE = BM * TLD * 2;
-  static constexpr int TLDF = BK + 4;         // fp32 per staged partial-sum row
+  static constexpr int TLDF = BK + 4;  // fp32 per staged partial-sum row
   static constexpr int TILEF = BM * TLDF * 4;
   static constexpr int BYTES = RING > TILE ? RING : TILE;
   static constexpr int BYTES_SPLIT = RING > TILEF ? RING : TILEF;
   static_assert(NX * NWV * 8 == BM && NQ * NWV * 1024 == BC * BK, "loads split evenly");
-  static_assert(NL * (SG - 1) < 64, "vmcnt");
+  static_assert(NL * (SG - 2) < 64, "vmcnt");
 };
 
-// The value of lane N of each row of 16 (a DPP operand of the multiply that takes it).
-template <int N>
-__device__ __forceinline__ float row_lane(float v) {
-  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
-      0, (int)__float_as_uint(v), 0x150 + N, 0xf, 0xf, false));
-}
-
-// Byte J of eight codes (channels n .. n + 7) times their scales, as bf16. Lane t
-// of a row of 16 holds the scale of channel 32 (t / 8) + 8 g + t % 8 of the
-// stage, so half KK's eight are lanes 8 KK .. 8 KK + 7 of the row.
-template <int KK, int J>
-__device__ __forceinline__ bf16x8 widen_scaled(const int (&w)[8], float s) {
-  bf16x8 b;
-  b[0] = (__bf16)((float)(int8_t)(w[0] >> (8 * J)) * row_lane<8 * KK>(s));
-  b[1] = (__bf16)((float)(int8_t)(w[1] >> (8 * J)) * row_lane<8 * KK + 1>(s));
-  b[2] = (__bf16)((float)(int8_t)(w[2] >> (8 * J)) * row_lane<8 * KK + 2>(s));
-  b[3] = (__bf16)((float)(int8_t)(w[3] >> (8 * J)) * row_lane<8 * KK + 3>(s));
-  b[4] = (__bf16)((float)(int8_t)(w[4] >> (8 * J)) * row_lane<8 * KK + 4>(s));
-  b[5] = (__bf16)((float)(int8_t)(w[5] >> (8 * J)) * row_lane<8 * KK + 5>(s));
-  b[6] = (__bf16)((float)(int8_t)(w[6] >> (8 * J)) * row_lane<8 * KK + 6>(s));
-  b[7] = (__bf16)((float)(int8_t)(w[7] >> (8 * J)) * row_lane<8 * KK + 7>(s));
-  return b;
+// Two biased codes (bytes u = q + 128 of rows e and e + 1) -> float16 pair
+// q 2^-9, exactly: a byte alone is the subnormal u 2^-24, and one packed
+// multiply-add takes it to u 2^-9 - 128 2^-9.
+template <int J>
+__device__ __forceinline__ int widen_pair(int lo, int hi) {
+  const uint32_t u = __builtin_amdgcn_perm((uint32_t)hi, (uint32_t)lo,
+                                           0x0c000c00u | (uint32_t)J | ((uint32_t)(J + 4) << 16));
+  const f16x2 v = __builtin_bit_cast(f16x2, u);
+  const f16x2 r = __builtin_elementwise_fma(v, f16x2{(_Float16)32768.0f, (_Float16)32768.0f},
+                                            f16x2{(_Float16)-0.25f, (_Float16)-0.25f});
+  return __builtin_bit_cast(int, r);
 }
 
 // SPLIT: unit (tile, sp) takes the ks stages from sp * ks and writes its fp32
 // sums to part[sp][M][K]; k_w8a16_dgrad_reduce adds them.
 template <int TI, int SG, bool SPLIT, class LT>
 __global__ __launch_bounds__(64 * NWV, 2) void k_w8a16_dgrad(
-    const uint16_t *__restrict__ dy, const int8_t *__restrict__ q,
-    const float *__restrict__ scale, uint16_t *__restrict__ dx, int64_t M, int64_t N, int64_t K,
-    int tiles_m, int tiles_k, float *__restrict__ part, int ks, LT lt) {
+    const uint16_t *__restrict__ d, const int32_t *__restrict__ ex, const int8_t *__restrict__ q,
+    uint16_t *__restrict__ dx, int64_t M, int64_t N, int64_t NP, int64_t K, int tiles_m,
+    int tiles_k, float *__restrict__ part, int ks, LT lt) {
   using L = DgradLds<TI, SG>;
-  constexpr int BM = L::BM, BK = L::BK, NX = L::NX, NQ = L::NQ, NL = L::NL;
+  constexpr int BM = L::BM, BK = L::BK, NX = L::NX, NL = L::NL;
   extern __shared__ __attribute__((aligned(16))) char smem[];
 
   const int nt = tiles_m * tiles_k;
@@ -116,51 +192,44 @@ __global__ __launch_bounds__(64 * NWV, 2) void k_w8a16_dgrad(
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int64_t mval = M - m0 < BM ? M - m0 : BM;
-  const __amdgpu_buffer_rsrc_t rx = rsrc(dy + m0 * N, (uint32_t)(mval * N * 2));
-  const __amdgpu_buffer_rsrc_t rs = rsrc(scale, (uint32_t)(N * 4));
+  // rows past M lie past the descriptor's end: they read as zero
+  const __amdgpu_buffer_rsrc_t rx = rsrc(d + m0 * NP, (uint32_t)(mval * NP * 2));
 
-  uint32_t xoff[NX];
-  int xlim[NX];  // stages in which this lane's chunk lies before N
-#pragma unroll
-  for (int i = 0; i < NX; ++i) {
-    const int row = 8 * (i * NWV + wave) + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
-    xoff[i] = (uint32_t)row * (uint32_t)(2 * N) + 16u * c;
-    xlim[i] = row < mval ? (int)((N - 8 * c + BC - 1) / BC) : 0;
-  }
-  int qrow[NQ];
-  uint32_t qoff[NQ];
-#pragma unroll
-  for (int i = 0; i < NQ; ++i) {
-    qrow[i] = 4 * (i * NWV + wave) + (lane >> 4);
-    const int c = (lane & 15) ^ (4 * ((qrow[i] >> 3) & 3));
-    qoff[i] = (uint32_t)qrow[i] * (uint32_t)K + 16u * c;
-    if (k0 + 16 * c >= K) qrow[i] = OOB;  // a column past K: never loaded
-  }
-  const int soff = 32 * ((lane >> 3) & 1) + 8 * g + (lane & 7);  // the lane's channel of a stage
+  // load i of a wave covers d rows 32 i + 8 wave + lane / 8 and weight rows
+  // 16 i + 4 wave + lane / 16; the rows' 32 i and 16 i are scalar offsets (they
+  // leave d's swizzle alone and flip bit 3 of the weights' chunk for odd i)
+  const int xr = 8 * wave + (lane >> 3), qr = 4 * wave + (lane >> 4);
+  const int xoff = xr * (int)(2 * NP) + 16 * ((lane & 7) ^ ((xr >> 1) & 7));
+  const int qc = (lane & 15) ^ (4 * (qr >> 3));
+  const int qoff[2] = {qr * (int)K + 16 * qc, qr * (int)K + 16 * (qc ^ 8)};
+  const int nk_all = (int)(NP / BC);
+  const int kb = SPLIT ? sp * ks : 0;
+  const int nk = (SPLIT ? (kb + ks < nk_all ? kb + ks : nk_all) : nk_all) - kb;  // stages
+
   const uint32_t lds_base = (uint32_t)(uintptr_t)smem;
-  // stage kt into ring slot `slot`; past N everything reads as zero
-  auto issue = [&](int kt, int slot) {
+  // Load I of stage kb + t into ring slot `slot`; past the last stage the last
+  // one again (never computed; the counts of loads in flight stay exact).
+  auto issue = [&](int t, int slot, auto ii) {
+    constexpr int I = decltype(ii)::value;
+    const int kt = kb + (t < nk ? t : nk - 1);
     const uint32_t st = lds_base + (uint32_t)(slot * L::STAGE);
-#pragma unroll
-    for (int i = 0; i < NX; ++i)
-      to_lds<16>(rx, st + 1024u * (i * NWV + wave),
-                 kt < xlim[i] ? (int)(xoff[i] + 128u * (uint32_t)kt) : OOB);
-    const int64_t n0 = (int64_t)BC * kt;
-    const int64_t left = N - n0;
-    const int rows = left < BC ? (int)left : BC;  // not positive past the end: none
-    const __amdgpu_buffer_rsrc_t rq = rsrc(q + (left > 0 ? n0 : 0) * K + k0, 0x3fffffffu);
-#pragma unroll
-    for (int i = 0; i < NQ; ++i)
-      to_lds<16>(rq, st + L::XS + 1024u * (i * NWV + wave), qrow[i] < rows ? (int)qoff[i] : OOB);
-    to_lds<4>(rs, st + L::XS + L::QS + 256u * wave, soff < rows ? (int)(4 * (n0 + soff)) : OOB);
+    if constexpr (I < NX) {
+      to_lds(rx, st + 1024u * (I * NWV + wave), xoff, I * 64 * (int)NP + 128 * kt);
+    } else {
+      // columns past K read the next row (or, at the end of q, zero) into
+      // columns of the tile that are never stored
+      const int64_t base = (int64_t)BC * kt * K + k0, left = N * K - base;
+      to_lds(rsrc(q + base, left < 0x7fffffff ? (uint32_t)left : 0x7fffffffu),
+             st + L::XS + 1024u * ((I - NX) * NWV + wave), qoff[(I - NX) & 1],
+             (I - NX) * 16 * (int)K);
+    }
   };
 
-  // fragment offsets within a stage. dy: block i adds 2048 i, half kk flips bit
+  // fragment offsets within a stage. d: block i adds 2048 i, half kk flips bit
   // 6 (chunk 4 kk + g under the swizzle); weights: half kk adds 32 rows, channel
   // e of the lane's eight adds e rows
   const int fx = r * 128 + 16 * (g ^ ((r >> 1) & 7));
   const int fq = L::XS + 8 * g * BK + 16 * ((4 * wave + (r >> 2)) ^ (4 * g)) + 4 * (r & 3);
-  const int fs = L::XS + L::QS + 256 * wave + 4 * lane;
 
   f32x4 acc[TI][TJ];
 #pragma unroll
@@ -168,88 +237,110 @@ __global__ __launch_bounds__(64 * NWV, 2) void k_w8a16_dgrad(
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // Software pipeline over the 32-channel halves of the stages. While the matrix
-  // core works on one half, the next half's weights come from LDS and are
-  // widened between the matrix instructions, and each block of dy is replaced by
-  // the next half's as soon as its products are issued, so only the widened
-  // weights are held twice.
-  bf16x8 fa[TI], b0[TJ], b1[TJ];
+  // Software pipeline over the 32-channel halves of the stages, written in the
+  // order it issues in (one wave a SIMD has nobody to hide behind, so the
+  // instructions between two matrix instructions have to fit their 16 cycles).
+  // While the matrix core works on one half, the next half's weights come from
+  // LDS and are widened, a step after every second matrix instruction, and
+  // block i of d is replaced by the next half's once its products are issued, so
+  // only the widened weights are held twice.
+  f16x8 fa[TI];
+  i32x4 wb[2][TJ];
   int raw[8];
-  float sv;
   auto read_w = [&](const char *st, auto kk) {
-    constexpr int KK = decltype(kk)::value;
-    if constexpr (KK == 0) sv = *reinterpret_cast<const float *>(st + fs);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      raw[e] = *reinterpret_cast<const int *>(st + fq + (32 * KK + e) * BK);
+      raw[e] = *reinterpret_cast<const int *>(st + fq + (32 * decltype(kk)::value + e) * BK);
   };
   auto read_x = [&](const char *st, auto kk, int i) {
-    fa[i] = *reinterpret_cast<const bf16x8 *>(st + (fx ^ (64 * decltype(kk)::value)) + 2048 * i);
+    fa[i] = *reinterpret_cast<const f16x8 *>(st + (fx ^ (64 * decltype(kk)::value)) + 2048 * i);
   };
-  auto widen = [&](auto kk, bf16x8 (&b)[TJ]) {
-    constexpr int KK = decltype(kk)::value;
-    b[0] = widen_scaled<KK, 0>(raw, sv);
-    b[1] = widen_scaled<KK, 1>(raw, sv);
-    b[2] = widen_scaled<KK, 2>(raw, sv);
-    b[3] = widen_scaled<KK, 3>(raw, sv);
+  // step u of 16: channels 2 p, 2 p + 1 of column block j, u = 4 j + p
+  auto widen = [&](i32x4 (&b)[TJ], auto uu) {
+    constexpr int J = decltype(uu)::value / 4, P = decltype(uu)::value % 4;
+    if constexpr (J == 0) {
+      raw[2 * P] ^= 0x80808080;
+      raw[2 * P + 1] ^= 0x80808080;
+    }
+    b[J][P] = widen_pair<J>(raw[2 * P], raw[2 * P + 1]);
   };
-  // the products of the half in fa and b; st and kk: the next half
-  auto half = [&](const char *st, auto kk, const bf16x8 (&b)[TJ], bf16x8 (&next)[TJ]) {
-    read_w(st, kk);
-#pragma unroll
-    for (int i = 0; i < TI; ++i) {
-#pragma unroll
-      for (int j = 0; j < TJ; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], b[j], acc[i][j], 0, 0, 0);
-      read_x(st, kk, i);
-    }
-    widen(kk, next);
-    __builtin_amdgcn_sched_group_barrier(0x100, 9, 0);  // DS reads: the weights
-    __builtin_amdgcn_sched_group_barrier(0x008, TJ, 0);  // MFMA
-    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-#pragma unroll
-    for (int i = 1; i < TI; ++i) {
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, TI == 8 ? 4 : 8, 0);  // VALU
-      }
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
+  auto mma = [&](const i32x4 (&b)[TJ], int i, int j) {
+    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+        fa[i], __builtin_bit_cast(f16x8, b[j]), acc[i][j], 0, 0, 0);
   };
   std::integral_constant<int, 0> h0;
   std::integral_constant<int, 1> h1;
+  constexpr int SLOTS = 2 * TI;  // pairs of matrix instructions in a half
 
-  const int nk_all = (int)((N + BC - 1) / BC);
-  const int kb = SPLIT ? sp * ks : 0;
-  const int nk = (SPLIT ? (kb + ks < nk_all ? kb + ks : nk_all) : nk_all) - kb;  // stages
+  if (nk > 0) {
 #pragma unroll
-  for (int s = 0; s < SG; ++s) issue(s < nk ? kb + s : nk_all, s);
-  __builtin_amdgcn_s_waitcnt(vmcnt_imm(NL * (SG - 1)));
-  __builtin_amdgcn_s_barrier();  // stage 0 complete everywhere
-  const char *st = smem;
-  read_w(st, h0);
+    for (int s = 0; s < SG - 1; ++s) static_for<0, NL>([&](auto ii) { issue(s, s, ii); });
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(NL * (SG - 2)));
+    __builtin_amdgcn_s_barrier();  // stage 0 complete everywhere
+    read_w(smem, h0);
 #pragma unroll
-  for (int i = 0; i < TI; ++i) read_x(st, h0, i);
-  widen(h0, b0);
-  // Stage t: its second half is read under the first half's products; then its
-  // slot is free and takes stage t + SG (zeros past the last), stage t + 1 must
-  // have landed, and its first half is read under the second half's products.
+    for (int i = 0; i < TI; ++i) read_x(smem, h0, i);
+    static_for<0, 16>([&](auto uu) { widen(wb[0], uu); });
+  }
   int slot = 0;
   for (int t = 0; t < nk; ++t) {
-    half(st, h1, b0, b1);
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's reads of the slot are done
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(NL * (SG - 2)));
-    __builtin_amdgcn_s_barrier();
-    issue(t + SG < nk ? kb + t + SG : nk_all, slot);
+    const char *st = smem + slot * L::STAGE;
+    const int prev = slot == 0 ? SG - 1 : slot - 1;
+    // First half: its products, the second half's operands, and the loads of
+    // stage t - 1 + SG into the slot that stage t - 1 left at the last barrier.
+    read_w(st, h1);
+    static_for<0, SLOTS>([&](auto ss) {
+      constexpr int S = decltype(ss)::value, I = S / 2, JJ = 2 * (S % 2);
+      mma(wb[0], I, JJ);
+      mma(wb[0], I, JJ + 1);
+      // steps of the widening from the third pair on, NL loads over the slots
+      constexpr int U0 = S < 2 ? 0 : (S - 2) * 16 / (SLOTS - 2);
+      constexpr int U1 = S < 2 ? 0 : (S - 1) * 16 / (SLOTS - 2);
+      static_for<U0, U1>([&](auto uu) { widen(wb[1], uu); });
+      if constexpr (S % 2 == 1) read_x(st, h1, I);
+      constexpr int L0 = S * NL / SLOTS, L1 = (S + 1) * NL / SLOTS;
+      static_for<L0, L1>([&](auto ii) { issue(t - 1 + SG, prev, ii); });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    // Second half: after its first pairs this wave's reads of the slot are done;
+    // past the barrier the slot is free and stage t + 1 has landed everywhere.
     slot = slot + 1 == SG ? 0 : slot + 1;
     st = smem + slot * L::STAGE;
-    half(st, h0, b1, b0);
+    constexpr int SB = TI == 8 ? 4 : 2;  // pairs before the barrier
+    static_for<0, SLOTS>([&](auto ss) {
+      constexpr int S = decltype(ss)::value, I = S / 2, JJ = 2 * (S % 2);
+      if constexpr (S == SB) {
+        __builtin_amdgcn_s_waitcnt(0xC07F);
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(NL * (SG - 2)));
+        __builtin_amdgcn_s_barrier();
+        read_w(st, h0);
+#pragma unroll
+        for (int i = 0; i < SB / 2; ++i) read_x(st, h0, i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      mma(wb[1], I, JJ);
+      mma(wb[1], I, JJ + 1);
+      constexpr int D = SLOTS - SB - 2;
+      constexpr int U0 = S < SB + 2 ? 0 : (S - SB - 2) * 16 / D;
+      constexpr int U1 = S < SB + 2 ? 0 : (S - SB - 1) * 16 / D;
+      static_for<U0, U1>([&](auto uu) { widen(wb[0], uu); });
+      if constexpr (S >= SB && S % 2 == 1) read_x(st, h0, I);
+      __builtin_amdgcn_sched_barrier(0);
+    });
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);
   __syncthreads();
 
+  // acc[i][j] lane (r, g): rows 16 i + 4 g + v, column 64 wave + 4 r + j; the
+  // rows' exponents come off (ex is padded to whole tiles)
+#pragma unroll
+  for (int i = 0; i < TI; ++i) {
+    const i32x4 e4 = *reinterpret_cast<const i32x4 *>(ex + m0 + 16 * i + 4 * g);
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[i][j][v] = ldexpf(acc[i][j][v], kCode - e4[v]);
+  }
   if constexpr (SPLIT) {
     float *tf = reinterpret_cast<float *>(smem);
 #pragma unroll
@@ -269,15 +360,16 @@ __global__ __launch_bounds__(64 * NWV, 2) void k_w8a16_dgrad(
     }
     return;
   }
-  // acc[i][j] lane (r, g): rows 16 i + 4 g + v, column 64 wave + 4 r + j
   if constexpr (LT::on) lora_add_tile<true>(acc, lt, m0, M, k0 + 64 * wave);
   uint16_t *tl = reinterpret_cast<uint16_t *>(smem);
 #pragma unroll
   for (int i = 0; i < TI; ++i)
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const uint32_t lo = f32_to_bf16_rne(acc[i][0][v]) | ((uint32_t)f32_to_bf16_rne(acc[i][1][v]) << 16);
-      const uint32_t hi = f32_to_bf16_rne(acc[i][2][v]) | ((uint32_t)f32_to_bf16_rne(acc[i][3][v]) << 16);
+      const uint32_t lo =
+          f32_to_bf16_rne(acc[i][0][v]) | ((uint32_t)f32_to_bf16_rne(acc[i][1][v]) << 16);
+      const uint32_t hi =
+          f32_to_bf16_rne(acc[i][2][v]) | ((uint32_t)f32_to_bf16_rne(acc[i][3][v]) << 16);
       *reinterpret_cast<i32x2 *>(tl + (i * 16 + 4 * g + v) * L::TLD + 64 * wave + 4 * r) =
           i32x2{(int)lo, (int)hi};
     }
@@ -312,11 +404,11 @@ __global__ __launch_bounds__(256) void k_w8a16_dgrad_reduce(const float *__restr
       f32x4 t = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
       for (int j = 0; j < lt.R; ++j) {
-        const i32x2 d = *reinterpret_cast<const i32x2 *>(w + (int64_t)j * K);
-        t[0] = fmaf(u[j], __uint_as_float((uint32_t)d[0] << 16), t[0]);
-        t[1] = fmaf(u[j], __uint_as_float((uint32_t)d[0] & 0xffff0000u), t[1]);
-        t[2] = fmaf(u[j], __uint_as_float((uint32_t)d[1] << 16), t[2]);
-        t[3] = fmaf(u[j], __uint_as_float((uint32_t)d[1] & 0xffff0000u), t[3]);
+        const i32x2 p = *reinterpret_cast<const i32x2 *>(w + (int64_t)j * K);
+        t[0] = fmaf(u[j], __uint_as_float((uint32_t)p[0] << 16), t[0]);
+        t[1] = fmaf(u[j], __uint_as_float((uint32_t)p[0] & 0xffff0000u), t[1]);
+        t[2] = fmaf(u[j], __uint_as_float((uint32_t)p[1] << 16), t[2]);
+        t[3] = fmaf(u[j], __uint_as_float((uint32_t)p[1] & 0xffff0000u), t[3]);
       }
       acc += t;
     }
@@ -326,60 +418,52 @@ __global__ __launch_bounds__(256) void k_w8a16_dgrad_reduce(const float *__restr
   *reinterpret_cast<i32x2 *>(dx + m * K + k) = i32x2{(int)lo, (int)hi};
 }
 
+struct Call {
+  const uint16_t *d;
+  const int32_t *ex;
+  const int8_t *q;
+  uint16_t *dx;
+  int64_t M, N, NP, K;
+  float *part;
+  hipStream_t st;
+};
+
 template <int TI, int SG, class LT>
-hipError_t go(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q, const float *scale,
-              int64_t K, uint16_t *dx, hipStream_t st, const LT &lt) {
+hipError_t go(const Call &c, const LT &lt) {
   using L = DgradLds<TI, SG>;
-  void (*kern)(const uint16_t *, const int8_t *, const float *, uint16_t *, int64_t, int64_t, int64_t,
-               int, int, float *, int, LT) = k_w8a16_dgrad<TI, SG, false, LT>;
-  (void)hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize,
-                            L::BYTES);
+  (void)hipFuncSetAttribute((const void *)k_w8a16_dgrad<TI, SG, false, LT>,
+                            hipFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
   (void)hipGetLastError();
-  const int tm = (int)((M + L::BM - 1) / L::BM), tk = (int)((K + L::BK - 1) / L::BK);
-  hipLaunchKernelGGL(kern, dim3((unsigned)(tm * tk)), dim3(64 * NWV), L::BYTES, st, dy, q, scale,
-                     dx, M, N, K, tm, tk, (float *)nullptr, 0, lt);
+  const int tm = (int)((c.M + L::BM - 1) / L::BM), tk = (int)((c.K + L::BK - 1) / L::BK);
+  hipLaunchKernelGGL((k_w8a16_dgrad<TI, SG, false, LT>), dim3((unsigned)(tm * tk)), dim3(64 * NWV),
+                     L::BYTES, c.st, c.d, c.ex, c.q, c.dx, c.M, c.N, c.NP, c.K, tm, tk,
+                     (float *)nullptr, 0, lt);
   return hipGetLastError();
 }
 
 template <int TI, int SG, class LT>
-hipError_t go_split(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q, const float *scale,
-                    int64_t K, uint16_t *dx, float *part, int S, hipStream_t st, const LT &lt) {
+hipError_t go_split(const Call &c, int S, const LT &lt) {
   using L = DgradLds<TI, SG>;
-  void (*kern)(const uint16_t *, const int8_t *, const float *, uint16_t *, int64_t, int64_t, int64_t,
-               int, int, float *, int, NoLora) = k_w8a16_dgrad<TI, SG, true, NoLora>;
-  (void)hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize,
-                            L::BYTES_SPLIT);
+  (void)hipFuncSetAttribute((const void *)k_w8a16_dgrad<TI, SG, true, NoLora>,
+                            hipFuncAttributeMaxDynamicSharedMemorySize, L::BYTES_SPLIT);
   (void)hipGetLastError();
-  const int tm = (int)((M + L::BM - 1) / L::BM), tk = (int)((K + L::BK - 1) / L::BK);
-  const int nk = (int)((N + BC - 1) / BC);
+  const int tm = (int)((c.M + L::BM - 1) / L::BM), tk = (int)((c.K + L::BK - 1) / L::BK);
+  const int nk = (int)(c.NP / BC);
   const int ks = (nk + S - 1) / S, splits = (nk + ks - 1) / ks;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(tm * tk * splits)), dim3(64 * NWV), L::BYTES_SPLIT, st,
-                     dy, q, scale, dx, M, N, K, tm, tk, part, ks, NoLora{});
+  hipLaunchKernelGGL((k_w8a16_dgrad<TI, SG, true, NoLora>), dim3((unsigned)(tm * tk * splits)),
+                     dim3(64 * NWV), L::BYTES_SPLIT, c.st, c.d, c.ex, c.q, c.dx, c.M, c.N, c.NP,
+                     c.K, tm, tk, c.part, ks, NoLora{});
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t groups = M * (K / 4);
+  const int64_t groups = c.M * (c.K / 4);
   hipLaunchKernelGGL(k_w8a16_dgrad_reduce<LT>, dim3((unsigned)((groups + 255) / 256)), dim3(256),
-                     0, st, part, splits, M, K, dx, lt);
+                     0, c.st, c.part, splits, c.M, c.K, c.dx, lt);
   return hipGetLastError();
 }
-
-template <class LT>
-hipError_t launch(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q, const float *scale,
-                  int64_t K, uint16_t *dx, float *part, size_t part_bytes, hipStream_t st,
-                  const LT &lt) {
-  const int64_t twide = ((M + 127) / 128) * ((K + 255) / 256);
-  if (twide >= 160) return go<8, 4>(dy, M, N, q, scale, K, dx, st, lt);
-  const int S = w8a16_dgrad_splits(M, N, K);
-  if (S > 1 && part && part_bytes >= w8a16_dgrad_part_bytes(M, N, K))
-    return go_split<4, 4>(dy, M, N, q, scale, K, dx, part, S, st, lt);
-  return go<4, 4>(dy, M, N, q, scale, K, dx, st, lt);
-}
-
-}  // namespace
 
 // 64 x 256 tiles split while the units stay within two a CU and each keeps at
 // least 8 stages of 64 channels.
-int w8a16_dgrad_splits(int64_t M, int64_t N, int64_t K) {
+int splits_of(int64_t M, int64_t N, int64_t K) {
   const int64_t twide = ((M + 127) / 128) * ((K + 255) / 256);
   if (twide >= 160) return 1;
   const int64_t tiles = ((M + 63) / 64) * ((K + 255) / 256), nk = (N + BC - 1) / BC;
@@ -388,21 +472,67 @@ int w8a16_dgrad_splits(int64_t M, int64_t N, int64_t K) {
   return S;
 }
 
-size_t w8a16_dgrad_part_bytes(int64_t M, int64_t N, int64_t K) {
-  const int S = w8a16_dgrad_splits(M, N, K);
-  return S > 1 ? (size_t)S * (size_t)M * (size_t)K * 4 : 0;
+// d [M, NP], the rows' exponents, the partial sums.
+struct Layout {
+  int64_t NP;
+  size_t ex, part, total;
+};
+Layout layout(int64_t M, int64_t N, int64_t K) {
+  Layout l;
+  l.NP = (N + BC - 1) / BC * BC;
+  auto up = [](size_t b) { return (b + 255) / 256 * 256; };
+  l.ex = up((size_t)M * (size_t)l.NP * 2);
+  l.part = l.ex + up((size_t)(M + 127) / 128 * 128 * 4);
+  const int S = splits_of(M, N, K);
+  l.total = l.part + (S > 1 ? (size_t)S * (size_t)M * (size_t)K * 4 : 0);
+  return l;
+}
+
+template <int TPR, int NI>
+hipError_t scale(const uint16_t *dy, const float *s, const Call &c, uint16_t *d, int32_t *ex) {
+  const unsigned grid = (unsigned)((c.M + 256 / TPR - 1) / (256 / TPR));
+  hipLaunchKernelGGL((k_dgrad_scale<TPR, NI>), dim3(grid), dim3(256), 0, c.st, dy, s, c.M, c.N,
+                     c.NP, d, ex);
+  return hipGetLastError();
+}
+
+template <class LT>
+hipError_t launch(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q, const float *s,
+                  int64_t K, uint16_t *dx, void *ws, hipStream_t st, const LT &lt) {
+  const Layout l = layout(M, N, K);
+  char *base = static_cast<char *>(ws);
+  uint16_t *d = reinterpret_cast<uint16_t *>(base);
+  int32_t *ex = reinterpret_cast<int32_t *>(base + l.ex);
+  const Call c{d, ex, q, dx, M, N, l.NP, K, reinterpret_cast<float *>(base + l.part), st};
+  hipError_t e;
+  if (l.NP <= 1024) e = scale<64, 2>(dy, s, c, d, ex);
+  else if (l.NP <= 2048) e = scale<256, 1>(dy, s, c, d, ex);
+  else if (l.NP <= 4096) e = scale<256, 2>(dy, s, c, d, ex);
+  else if (l.NP <= 8192) e = scale<256, 4>(dy, s, c, d, ex);
+  else if (l.NP <= 16384) e = scale<256, 8>(dy, s, c, d, ex);
+  else e = scale<256, 0>(dy, s, c, d, ex);
+  if (e != hipSuccess) return e;
+  const int64_t twide = ((M + 127) / 128) * ((K + 255) / 256);
+  if (twide >= 160) return go<8, 4>(c, lt);
+  const int S = splits_of(M, N, K);
+  if (S > 1) return go_split<4, 4>(c, S, lt);
+  return go<4, 4>(c, lt);
+}
+
+}  // namespace
+
+size_t w8a16_dgrad_bytes(int64_t M, int64_t N, int64_t K) { return layout(M, N, K).total; }
+
+hipError_t launch_w8a16_dgrad(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q,
+                              const float *scale, int64_t K, uint16_t *dx, void *ws,
+                              hipStream_t st) {
+  return launch(dy, M, N, q, scale, K, dx, ws, st, NoLora{});
 }
 
 hipError_t launch_w8a16_dgrad(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q,
-                              const float *scale, int64_t K, uint16_t *dx, float *part,
-                              size_t part_bytes, hipStream_t st) {
-  return launch(dy, M, N, q, scale, K, dx, part, part_bytes, st, NoLora{});
-}
-
-hipError_t launch_w8a16_dgrad(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q,
-                              const float *scale, int64_t K, uint16_t *dx, float *part,
-                              size_t part_bytes, hipStream_t st, const LoraTerm &lt) {
-  return launch(dy, M, N, q, scale, K, dx, part, part_bytes, st, lt);
+                              const float *scale, int64_t K, uint16_t *dx, void *ws,
+                              hipStream_t st, const LoraTerm &lt) {
+  return launch(dy, M, N, q, scale, K, dx, ws, st, lt);
 }
 
 }  // namespace aql

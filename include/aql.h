@@ -72,7 +72,7 @@ extern "C" {
 #define AQL_OP_DQ8CA 2      /* workspace of aql_linear_dq8ca */
 #define AQL_OP_GPTQ_INT8 3  /* workspace of aql_gptq_int8 (M = the column block) */
 #define AQL_OP_W8A16 4      /* optional workspace of aql_linear_w8a16 (0: none used) */
-#define AQL_OP_W8A16_DGRAD 5 /* optional workspace of aql_linear_w8a16_dgrad (0: none used) */
+#define AQL_OP_W8A16_DGRAD 5 /* workspace of aql_linear_w8a16_dgrad */
 
 /* Bounds of the low-rank adapters: rank R a multiple of 8 up to
  * AQL_LORA_MAX_RANK, at most AQL_LORA_MAX_ADAPTERS stacked adapters. */
@@ -395,16 +395,17 @@ int aql_linear_w8a16_lora(const uint16_t *x, int64_t M, int64_t K, const int8_t 
 
 /*
  * Gradient of aql_linear_w8a16 to its input: dx[m, k] = sum_n dy[m, n] scale[n]
- * q[n, k], on the weights as they lie (no transposed copy). Each weight enters
- * as bf16(scale[n] q[n, k]), one rounding; sums are float32.
+ * q[n, k], on the weights as they lie (no transposed copy). Each dy[m, n]
+ * scale[n] is rounded once, to the 11 bits of float16 under an exponent of its
+ * row (products below 2^-28 of the row's largest keep fewer bits); the codes
+ * are exact and sums are float32.
  *
  *   dy  device, [M, N] bf16;  q, scale as aql_linear_w8a16
  *   dx  device, [M, K] bf16 (output)
- *   ws  optional device workspace of aql_workspace_bytes(AQL_OP_W8A16_DGRAD, M,
- *       N, K) bytes: shapes of few output tiles split the sum over N with it.
+ *   ws  device workspace of aql_workspace_bytes(AQL_OP_W8A16_DGRAD, M, N, K) bytes
  * Errors: M < 0 or > 1048560; K < 16, K % 16 != 0 or K > 2^24; N < 0,
- * N % 8 != 0 or N > 2^22; NULL (M, N > 0) or misaligned pointers. N == 0
- * writes zeros.
+ * N % 8 != 0 or N > 2^22; NULL (M, N > 0) or misaligned pointers; workspace
+ * too small. N == 0 writes zeros.
  */
 int aql_linear_w8a16_dgrad(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q,
                            const float *scale, int64_t K, uint16_t *dx, void *ws, size_t ws_bytes,

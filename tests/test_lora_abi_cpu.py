@@ -68,13 +68,13 @@ def test_forward_empty():
     assert call(L.aql_linear_w8a16_lora, FWD, N=0, q=None, scale=None, y=None, B=None) == OK
 
 
-DG = dict(dy=P, M=5, N=24, q=P, scale=P, K=64, dx=P, ws=None, ws_bytes=0, stream=None)
+DG = dict(dy=P, M=5, N=24, q=P, scale=P, K=64, dx=P, ws=P, ws_bytes=BIG, stream=None)
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(M=-1), SHAPE), (dict(M=1048561), SHAPE), (dict(N=-8), SHAPE), (dict(N=12), SHAPE),
     (dict(N=(1 << 22) + 8), SHAPE), (dict(K=0), SHAPE), (dict(K=24), SHAPE),
-    (dict(K=(1 << 24) + 16), SHAPE)]
+    (dict(K=(1 << 24) + 16), SHAPE), (dict(ws=None), WS), (dict(ws_bytes=5 * 64 * 2), WS)]
     + [({k: None}, NULL) for k in ("dy", "q", "scale", "dx")]
     + [({k: MIS}, ALIGN) for k in ("dy", "q", "scale", "dx", "ws")])
 def test_dgrad_refusals(kw, code):
@@ -84,9 +84,10 @@ def test_dgrad_refusals(kw, code):
 def test_dgrad_empty_and_workspace():
     assert call(L.aql_linear_w8a16_dgrad, DG, M=0, dy=None, dx=None) == OK
     wb = lambda M, N, K: L.aql_workspace_bytes(aql.AQL_OP_W8A16_DGRAD, M, N, K)
-    assert wb(2048, 11008, 4096) == 0                       # many tiles: no split
-    assert wb(64, 4096, 4096) > 0 and wb(64, 4096, 4096) % (64 * 4096 * 4) == 0
-    assert wb(-1, 16, 16) == 0 and wb(0, 16, 16) == 0
+    # the scaled dy in float16 and an exponent a row, nothing else where no sum is split
+    assert wb(2048, 11008, 4096) == 2048 * 11008 * 2 + 2048 * 4
+    assert wb(64, 4096, 4096) > 64 * 4096 * 2 + 64 * 4 + 64 * 4096 * 4
+    assert wb(-1, 16, 16) == 0 and wb(0, 16, 16) == 0 and wb(1 << 21, 16, 16) == 0
 
 
 BWD = dict(dy=P, M=5, N=24, q=P, scale=P, K=64, A=P, B=P, alpha=P, L=3, R=8, plan=P, h=P, xq=P,
@@ -107,7 +108,7 @@ def test_backward_refusals(kw, code):
 def test_backward_nothing_asked_for():
     assert call(L.aql_linear_w8a16_lora_backward, BWD, dx=None, dA=None, dB=None) == OK
     assert aql.aql_lora_backward_bytes(0, 24, 64, 8) == 0
-    assert aql.aql_lora_backward_bytes(5, 24, 64, 8) >= 5 * 8 * 4
+    assert aql.aql_lora_backward_bytes(5, 24, 64, 8) >= 5 * 8 * 4 + 5 * 64 * 2
 
 
 CK = dict(x=P, dtype=0, M=5, K=64, xq=P, xs=P, stream=None)
