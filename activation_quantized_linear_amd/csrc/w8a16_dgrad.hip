@@ -155,15 +155,19 @@ struct DgradLds {
   static_assert(NL * (SG - 2) < 64, "vmcnt");
 };
 
-// Two biased codes (bytes u = q + 128 of rows e and e + 1) -> float16 pair
-// q 2^-9, exactly: a byte alone is the subnormal u 2^-24, and one packed
-// multiply-add takes it to u 2^-9 - 128 2^-9.
+// Byte J of two dwords of biased codes u = q + 128 -> the low bytes of a pair of
+// 16-bit halves.
 template <int J>
-__device__ __forceinline__ int widen_pair(int lo, int hi) {
-  const uint32_t u = __builtin_amdgcn_perm((uint32_t)hi, (uint32_t)lo,
-                                           0x0c000c00u | (uint32_t)J | ((uint32_t)(J + 4) << 16));
-  const f16x2 v = __builtin_bit_cast(f16x2, u);
-  const f16x2 r = __builtin_elementwise_fma(v, f16x2{(_Float16)32768.0f, (_Float16)32768.0f},
+__device__ __forceinline__ int byte_pair(int lo, int hi) {
+  return (int)__builtin_amdgcn_perm((uint32_t)hi, (uint32_t)lo,
+                                    0x0c000c00u | (uint32_t)J | ((uint32_t)(J + 4) << 16));
+}
+
+// Such a pair -> float16 q 2^-9, exactly: a byte alone is the subnormal u 2^-24,
+// and one packed multiply-add takes it to u 2^-9 - 128 2^-9.
+__device__ __forceinline__ int unbias(int u) {
+  const f16x2 r = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, u),
+                                            f16x2{(_Float16)32768.0f, (_Float16)32768.0f},
                                             f16x2{(_Float16)-0.25f, (_Float16)-0.25f});
   return __builtin_bit_cast(int, r);
 }
@@ -176,7 +180,7 @@ __global__ __launch_bounds__(64 * NWV, 2) void k_w8a16_dgrad(
     uint16_t *__restrict__ dx, int64_t M, int64_t N, int64_t NP, int64_t K, int tiles_m,
     int tiles_k, float *__restrict__ part, int ks, LT lt) {
   using L = DgradLds<TI, SG>;
-  constexpr int BM = L::BM, BK = L::BK, NX = L::NX, NL = L::NL;
+  constexpr int BM = L::BM, BK = L::BK, NX = L::NX, NQ = L::NQ, NL = L::NL;
   extern __shared__ __attribute__((aligned(16))) char smem[];
 
   const int nt = tiles_m * tiles_k;
@@ -207,22 +211,37 @@ __global__ __launch_bounds__(64 * NWV, 2) void k_w8a16_dgrad(
   const int nk = (SPLIT ? (kb + ks < nk_all ? kb + ks : nk_all) : nk_all) - kb;  // stages
 
   const uint32_t lds_base = (uint32_t)(uintptr_t)smem;
-  // Load I of stage kb + t into ring slot `slot`; past the last stage the last
-  // one again (never computed; the counts of loads in flight stay exact).
-  auto issue = [&](int t, int slot, auto ii) {
+  // Where the next stage to load lies; past the last stage it stays on the last
+  // one (loaded again, never computed: the counts of loads in flight stay exact).
+  int xs = 128 * kb, left_x = nk - 1, left_w = nk - 1;
+  const int8_t *wp = q + (int64_t)BC * kb * K + k0;
+  uint64_t wleft = (uint64_t)(N * K - ((int64_t)BC * kb * K + k0));
+  auto next_x = [&]() {
+    xs += left_x > 0 ? 128 : 0;
+    --left_x;
+  };
+  auto next_w = [&]() {
+    const uint32_t step = left_w > 0 ? (uint32_t)BC * (uint32_t)K : 0u;
+    wp += step;
+    wleft -= step;
+    --left_w;
+  };
+  // columns past K read the next row (or, at the end of q, zero) into columns of
+  // the tile that are never stored
+  auto weights = [&]() {
+    const uint32_t hi = (uint32_t)(wleft >> 32), lo = (uint32_t)wleft;
+    return rsrc(wp, hi != 0 || lo > 0x7fffffffu ? 0x7fffffffu : lo);
+  };
+  // load I of d's NX, of the weights' NQ, into ring slot `slot`
+  auto load_x = [&](int slot, auto ii) {
     constexpr int I = decltype(ii)::value;
-    const int kt = kb + (t < nk ? t : nk - 1);
-    const uint32_t st = lds_base + (uint32_t)(slot * L::STAGE);
-    if constexpr (I < NX) {
-      to_lds(rx, st + 1024u * (I * NWV + wave), xoff, I * 64 * (int)NP + 128 * kt);
-    } else {
-      // columns past K read the next row (or, at the end of q, zero) into
-      // columns of the tile that are never stored
-      const int64_t base = (int64_t)BC * kt * K + k0, left = N * K - base;
-      to_lds(rsrc(q + base, left < 0x7fffffff ? (uint32_t)left : 0x7fffffffu),
-             st + L::XS + 1024u * ((I - NX) * NWV + wave), qoff[(I - NX) & 1],
-             (I - NX) * 16 * (int)K);
-    }
+    to_lds(rx, lds_base + (uint32_t)(slot * L::STAGE) + 1024u * (I * NWV + wave), xoff,
+           I * 64 * (int)NP + xs);
+  };
+  auto load_w = [&](__amdgpu_buffer_rsrc_t rq, int slot, auto ii) {
+    constexpr int I = decltype(ii)::value;
+    to_lds(rq, lds_base + (uint32_t)(slot * L::STAGE) + L::XS + 1024u * (I * NWV + wave),
+           qoff[I & 1], I * 16 * (int)K);
   };
 
   // fragment offsets within a stage. d: block i adds 2048 i, half kk flips bit
@@ -238,31 +257,33 @@ __global__ __launch_bounds__(64 * NWV, 2) void k_w8a16_dgrad(
     for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   // Software pipeline over the 32-channel halves of the stages, written in the
-  // order it issues in (one wave a SIMD has nobody to hide behind, so the
-  // instructions between two matrix instructions have to fit their 16 cycles).
-  // While the matrix core works on one half, the next half's weights come from
-  // LDS and are widened, a step after every second matrix instruction, and
-  // block i of d is replaced by the next half's once its products are issued, so
-  // only the widened weights are held twice.
+  // order it issues in: one wave a SIMD has nobody to hide behind, so what comes
+  // between two matrix instructions has to fit the 16 cycles of one (three other
+  // instructions). While the matrix core works on one half, the next half's
+  // weights come from LDS and are widened, and block i of d is replaced by the
+  // next half's once its products are issued, so only the widened weights are
+  // held twice.
   f16x8 fa[TI];
   i32x4 wb[2][TJ];
   int raw[8];
-  auto read_w = [&](const char *st, auto kk) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      raw[e] = *reinterpret_cast<const int *>(st + fq + (32 * decltype(kk)::value + e) * BK);
+  auto read_w = [&](const char *st, auto kk, int e) {  // rows e and e + 1
+    const char *w = st + fq + (32 * decltype(kk)::value + e) * BK;
+    raw[e] = *reinterpret_cast<const int *>(w);
+    raw[e + 1] = *reinterpret_cast<const int *>(w + BK);
   };
   auto read_x = [&](const char *st, auto kk, int i) {
     fa[i] = *reinterpret_cast<const f16x8 *>(st + (fx ^ (64 * decltype(kk)::value)) + 2048 * i);
   };
-  // step u of 16: channels 2 p, 2 p + 1 of column block j, u = 4 j + p
+  // The widening in 40 single instructions: per pair of rows P the bias of both
+  // dwords and block 0's pair (4), then the other blocks' pairs (2 each).
+  constexpr int STEPS = 40;
   auto widen = [&](i32x4 (&b)[TJ], auto uu) {
-    constexpr int J = decltype(uu)::value / 4, P = decltype(uu)::value % 4;
-    if constexpr (J == 0) {
-      raw[2 * P] ^= 0x80808080;
-      raw[2 * P + 1] ^= 0x80808080;
-    }
-    b[J][P] = widen_pair<J>(raw[2 * P], raw[2 * P + 1]);
+    constexpr int U = decltype(uu)::value;
+    constexpr int J = U < 16 ? 0 : 1 + (U - 16) / 8, P = U < 16 ? U / 4 : (U - 16) / 2 % 4;
+    constexpr int W = U < 16 ? U % 4 : 2 + U % 2;
+    if constexpr (W < 2) raw[2 * P + W] ^= 0x80808080;
+    if constexpr (W == 2) b[J][P] = byte_pair<J>(raw[2 * P], raw[2 * P + 1]);
+    if constexpr (W == 3) b[J][P] = unbias(b[J][P]);
   };
   auto mma = [&](const i32x4 (&b)[TJ], int i, int j) {
     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
@@ -270,61 +291,77 @@ __global__ __launch_bounds__(64 * NWV, 2) void k_w8a16_dgrad(
   };
   std::integral_constant<int, 0> h0;
   std::integral_constant<int, 1> h1;
-  constexpr int SLOTS = 2 * TI;  // pairs of matrix instructions in a half
+  constexpr int SLOTS = TI * TJ;  // matrix instructions in a half
 
   if (nk > 0) {
 #pragma unroll
-    for (int s = 0; s < SG - 1; ++s) static_for<0, NL>([&](auto ii) { issue(s, s, ii); });
+    for (int s = 0; s < SG - 1; ++s) {
+      static_for<0, NX>([&](auto ii) { load_x(s, ii); });
+      next_x();
+      const __amdgpu_buffer_rsrc_t rq = weights();
+      static_for<0, NQ>([&](auto ii) { load_w(rq, s, ii); });
+      next_w();
+    }
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(NL * (SG - 2)));
     __builtin_amdgcn_s_barrier();  // stage 0 complete everywhere
-    read_w(smem, h0);
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) read_w(smem, h0, e);
 #pragma unroll
     for (int i = 0; i < TI; ++i) read_x(smem, h0, i);
-    static_for<0, 16>([&](auto uu) { widen(wb[0], uu); });
+    static_for<0, STEPS>([&](auto uu) { widen(wb[0], uu); });
+    const __amdgpu_buffer_rsrc_t rq = weights();
+    static_for<0, NQ>([&](auto ii) { load_w(rq, SG - 1, ii); });
   }
   int slot = 0;
   for (int t = 0; t < nk; ++t) {
     const char *st = smem + slot * L::STAGE;
     const int prev = slot == 0 ? SG - 1 : slot - 1;
-    // First half: its products, the second half's operands, and the loads of
-    // stage t - 1 + SG into the slot that stage t - 1 left at the last barrier.
-    read_w(st, h1);
+    // First half: its products and the second half's operands.
     static_for<0, SLOTS>([&](auto ss) {
-      constexpr int S = decltype(ss)::value, I = S / 2, JJ = 2 * (S % 2);
-      mma(wb[0], I, JJ);
-      mma(wb[0], I, JJ + 1);
-      // steps of the widening from the third pair on, NL loads over the slots
-      constexpr int U0 = S < 2 ? 0 : (S - 2) * 16 / (SLOTS - 2);
-      constexpr int U1 = S < 2 ? 0 : (S - 1) * 16 / (SLOTS - 2);
+      constexpr int S = decltype(ss)::value, I = S / TJ;
+      mma(wb[0], I, S % TJ);
+      if constexpr (S < 4) read_w(st, h1, 2 * S);
+      constexpr int F = 4;  // first slot of the widening
+      constexpr int U0 = S < F ? 0 : (S - F) * STEPS / (SLOTS - F);
+      constexpr int U1 = S < F ? 0 : (S - F + 1) * STEPS / (SLOTS - F);
       static_for<U0, U1>([&](auto uu) { widen(wb[1], uu); });
-      if constexpr (S % 2 == 1) read_x(st, h1, I);
-      constexpr int L0 = S * NL / SLOTS, L1 = (S + 1) * NL / SLOTS;
-      static_for<L0, L1>([&](auto ii) { issue(t - 1 + SG, prev, ii); });
+      if constexpr (S % TJ == TJ - 1) read_x(st, h1, I);
+      if constexpr (S == 1) next_w();
       __builtin_amdgcn_sched_barrier(0);
     });
-    // Second half: after its first pairs this wave's reads of the slot are done;
-    // past the barrier the slot is free and stage t + 1 has landed everywhere.
+    // Second half. Under its first products d's loads of stage t - 1 + SG go into
+    // the slot that stage t - 1 left at the last barrier. Then this wave's reads
+    // of stage t are done; past the barrier its slot is free, its first loads are
+    // the weights of stage t + SG, and stage t + 1 has landed everywhere.
+    const int freed = slot;
     slot = slot + 1 == SG ? 0 : slot + 1;
     st = smem + slot * L::STAGE;
-    constexpr int SB = TI == 8 ? 4 : 2;  // pairs before the barrier
+    const __amdgpu_buffer_rsrc_t rq = weights();
+    constexpr int SB = TI;  // matrix instructions before the barrier: TI / 4 blocks
     static_for<0, SLOTS>([&](auto ss) {
-      constexpr int S = decltype(ss)::value, I = S / 2, JJ = 2 * (S % 2);
+      constexpr int S = decltype(ss)::value, I = S / TJ;
       if constexpr (S == SB) {
+        next_x();
         __builtin_amdgcn_s_waitcnt(0xC07F);
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(NL * (SG - 2)));
         __builtin_amdgcn_s_barrier();
-        read_w(st, h0);
-#pragma unroll
-        for (int i = 0; i < SB / 2; ++i) read_x(st, h0, i);
         __builtin_amdgcn_sched_barrier(0);
       }
-      mma(wb[1], I, JJ);
-      mma(wb[1], I, JJ + 1);
-      constexpr int D = SLOTS - SB - 2;
-      constexpr int U0 = S < SB + 2 ? 0 : (S - SB - 2) * 16 / D;
-      constexpr int U1 = S < SB + 2 ? 0 : (S - SB - 1) * 16 / D;
-      static_for<U0, U1>([&](auto uu) { widen(wb[0], uu); });
-      if constexpr (S >= SB && S % 2 == 1) read_x(st, h0, I);
+      mma(wb[1], I, S % TJ);
+      if constexpr (S < SB) {
+        constexpr int L0 = S * NX / SB, L1 = (S + 1) * NX / SB;
+        static_for<L0, L1>([&](auto ii) { load_x(prev, ii); });
+      } else {
+        if constexpr (S < SB + 4) read_w(st, h0, 2 * (S - SB));
+        if constexpr (S >= SB + 2 && S < SB + 2 + SB / TJ) read_x(st, h0, S - SB - 2);
+        if constexpr (S % TJ == TJ - 1) read_x(st, h0, I);
+        constexpr int F = SB + 4;
+        constexpr int U0 = S < F ? 0 : (S - F) * STEPS / (SLOTS - F);
+        constexpr int U1 = S < F ? 0 : (S - F + 1) * STEPS / (SLOTS - F);
+        static_for<U0, U1>([&](auto uu) { widen(wb[0], uu); });
+        constexpr int L0 = (S - SB) * NQ / (SLOTS - SB), L1 = (S - SB + 1) * NQ / (SLOTS - SB);
+        static_for<L0, L1>([&](auto ii) { load_w(rq, freed, ii); });
+      }
       __builtin_amdgcn_sched_barrier(0);
     });
   }
