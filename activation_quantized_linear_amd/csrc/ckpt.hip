@@ -25,6 +25,26 @@ __device__ __forceinline__ f32x4 load4(const void *x, int64_t i) {
   }
 }
 
+// rint(v / s) for |v| <= 127 s, s a normal float with a normal reciprocal r:
+// v r carries two roundings (2^-24 each) and lies within 2^-16 of the IEEE
+// quotient (at most 127), so unless it is within 2^-10 of a half integer both
+// round to the same code; those few take the division itself.
+__device__ __forceinline__ float code_of(float v, float s, float r) {
+  const float t = v * r;
+  float c = rintf(t);
+  if (fabsf(t - c) > 0.5f - 0x1p-10f) c = rintf(v / s);
+  return c;
+}
+
+// First element of group t's four of lane l, and whether they lie in the matrix:
+// (m, gi) is group t's row and place in it.
+__device__ __forceinline__ void next_group(int64_t &m, int64_t &gi, int64_t G) {
+  if (++gi == G) {
+    gi = 0;
+    ++m;
+  }
+}
+
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_act_checkpoint(const void *__restrict__ x, int64_t groups,
                                                         int64_t K, int64_t G,
@@ -32,16 +52,19 @@ __global__ __launch_bounds__(256) void k_act_checkpoint(const void *__restrict__
                                                         float *__restrict__ xs) {
   const int l = threadIdx.x & 31;
   const int64_t t0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kIlp;
+  int64_t m = t0 / G, gi = t0 - m * G;
   f32x4 v[kIlp];
   int64_t at[kIlp];
 #pragma unroll
   for (int u = 0; u < kIlp; ++u) {
-    const int64_t t = t0 + u, m = t / G, c = (t - m * G) * kCkptGroup + 4 * l;
-    const bool in = t < groups && c < K;  // whole fours: K is a multiple of 4
+    const int64_t c = gi * kCkptGroup + 4 * l;
+    const bool in = t0 + u < groups && c < K;  // whole fours: K is a multiple of 4
     at[u] = in ? m * K + c : -1;
     v[u] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (in) v[u] = load4<BF16>(x, at[u]);
+    next_group(m, gi, G);
   }
+  float mine = 1.0f;  // lane u keeps group t0 + u's scale
 #pragma unroll
   for (int u = 0; u < kIlp; ++u) {
     float mx = fmaxf(fmaxf(fabsf(v[u][0]), fabsf(v[u][1])), fmaxf(fabsf(v[u][2]), fabsf(v[u][3])));
@@ -49,17 +72,24 @@ __global__ __launch_bounds__(256) void k_act_checkpoint(const void *__restrict__
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
     float s = mx / 127.0f;
     s = s > 0.0f ? s : 1.0f;
+    if (l == u) mine = s;
     if (at[u] >= 0) {
       uint32_t w = 0;
+      // scales from 2^-100 to 2^100 have a normal reciprocal
+      if (s >= 0x1p-100f && s <= 0x1p100f) {
+        const float r = 1.0f / s;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int q = (int)clamp_code(rintf(v[u][e] / s), -127.0f, 127.0f);
-        w |= ((uint32_t)q & 255u) << (8 * e);
+        for (int e = 0; e < 4; ++e)
+          w |= ((uint32_t)(int)clamp_code(code_of(v[u][e], s, r), -127.0f, 127.0f) & 255u) << (8 * e);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w |= ((uint32_t)(int)clamp_code(rintf(v[u][e] / s), -127.0f, 127.0f) & 255u) << (8 * e);
       }
       *reinterpret_cast<uint32_t *>(xq + at[u]) = w;
     }
-    if (l == 0 && t0 + u < groups) xs[t0 + u] = s;
   }
+  if (l < kIlp && t0 + l < groups) xs[t0 + l] = mine;
 }
 
 template <bool BF16>
@@ -68,16 +98,18 @@ __global__ __launch_bounds__(256) void k_act_restore(const int8_t *__restrict__ 
                                                      int64_t K, int64_t G, void *__restrict__ x) {
   const int l = threadIdx.x & 31;
   const int64_t t0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kIlp;
+  int64_t m = t0 / G, gi = t0 - m * G;
   int w[kIlp];
   float s[kIlp];
   int64_t at[kIlp];
 #pragma unroll
   for (int u = 0; u < kIlp; ++u) {
-    const int64_t t = t0 + u, m = t / G, c = (t - m * G) * kCkptGroup + 4 * l;
-    const bool in = t < groups && c < K;
+    const int64_t c = gi * kCkptGroup + 4 * l;
+    const bool in = t0 + u < groups && c < K;
     at[u] = in ? m * K + c : -1;
     w[u] = in ? *reinterpret_cast<const int *>(xq + at[u]) : 0;
-    s[u] = in ? xs[t] : 0.0f;
+    s[u] = in ? xs[t0 + u] : 0.0f;
+    next_group(m, gi, G);
   }
 #pragma unroll
   for (int u = 0; u < kIlp; ++u) {

@@ -106,131 +106,140 @@ __device__ __forceinline__ void split_bf16(const float (&v)[8], bf16x8 &hi, bf16
   }
 }
 
-// The 16 x 32 contraction block of h that lane (r, g) holds for a matrix
-// instruction: row r of the block, ranks j0 .. j0 + 7, in two bf16 parts.
-__device__ __forceinline__ void lora_h_frag(const float *h, bool in, bf16x8 &hi, bf16x8 &lo) {
-  f32x4 h0 = {0.f, 0.f, 0.f, 0.f}, h1 = h0;
-  if (in) {
-    h0 = *reinterpret_cast<const f32x4 *>(h);
-    h1 = *reinterpret_cast<const f32x4 *>(h + 4);
-  }
-  const float v[8] = {h0[0], h0[1], h0[2], h0[3], h1[0], h1[1], h1[2], h1[3]};
-  split_bf16(v, hi, lo);
-}
+// The adapter terms of a workgroup's output tile, after its own sums: acc[i][j]
+// += h . W_a^T for the blocks of 16 x 16 that a wave holds (16x16x32 layout, lane
+// 16 g + r holding rows 4 g + v of one column). The tile's distinct adapters are
+// walked in ascending order (one, in a prefill or a training batch), 32 ranks at
+// a step: the rows' h goes to LDS split into two bf16 parts, once for all waves,
+// with the adapter's 32 ranks of the tile's columns beside it, and every block
+// takes two matrix instructions. Products are added through a select by row, so
+// no value of one adapter (an infinity or a NaN in it among them) reaches a row
+// of another.
+// KMAJOR: W is [L, R, N] (contraction rows) and block j's column is col0 + TJ r
+// + j; else W is [L, N, R] and the column is col0 + 16 j + r.
+template <int BM, int BN, bool KMAJOR>
+struct LoraLds {
+  static constexpr int H = BM * 128;                         // rows of 32 high, 32 low parts
+  static constexpr int W = KMAJOR ? 32 * BN * 2 : BN * 64;   // 32 ranks of BN columns
+  static constexpr int IDS = BM * 4;                         // the rows' adapters
+  static constexpr int BYTES = H + W + 2 * IDS + 16;         // the distinct ones, their number
+};
 
-// Its other operand, for a wave's TJ blocks of columns: ranks j0 .. j0 + 7 of
-// adapter a. W [L, N, R]: block j's column is n + 16 j, its ranks lie together.
-// KMAJOR, W [L, R, N] (contraction rows): block j's column is n + j, so the four
-// blocks' values of a rank are one 8-byte load, and pairs of ranks are packed.
-template <bool KMAJOR, int TJ>
-__device__ __forceinline__ void lora_w_frags(const LoraTerm &t, int a, int64_t n, int j0,
-                                             bf16x8 (&w)[TJ]) {
-  const bool jin = j0 < t.R;  // whole chunks of 8: R is a multiple of 8
-  if constexpr (KMAJOR) {
-    static_assert(TJ == 4, "four columns a lane");
-    i32x2 d[8];
-    const uint16_t *p = t.W + ((int64_t)a * t.R + j0) * t.N + n;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      d[e] = i32x2{0, 0};
-      if (jin && n < t.N) d[e] = *reinterpret_cast<const i32x2 *>(p + (int64_t)e * t.N);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      i32x4 v;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        v[e] = (int)__builtin_amdgcn_perm((uint32_t)d[2 * e + 1][j >> 1], (uint32_t)d[2 * e][j >> 1],
-                                          j & 1 ? 0x07060302u : 0x05040100u);
-      w[j] = __builtin_bit_cast(bf16x8, v);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < TJ; ++j) {
-      const int64_t nj = n + 16 * j;
-      i32x4 v = {0, 0, 0, 0};
-      if (jin && nj < t.N)
-        v = *reinterpret_cast<const i32x4 *>(t.W + ((int64_t)a * t.N + nj) * t.R + j0);
-      w[j] = __builtin_bit_cast(bf16x8, v);
-    }
-  }
-}
-
-// acc[i][j] += h . W_a^T over a wave's tile of MFMA blocks: 16 TI rows from m0
-// by 16 TJ columns from n0, accumulators in the 16x16x32 layout (lane 16 g + r
-// holds rows 4 g + v of one column: n0 + 16 j + r, or with KMAJOR n0 + TJ r + j).
-// All 64 lanes must be active.
-// Where all the tile's rows are of one adapter (a prefill, a training batch)
-// its operand is loaded once for the tile. Else each block of 16 rows walks its
-// distinct adapters in ascending order; in a block of several the products of
-// the other rows are computed and dropped by a select, so no value of one
-// adapter (an infinity or a NaN in it among them) reaches a row of another.
-template <bool KMAJOR, int TI, int TJ>
-__device__ __forceinline__ void lora_add_tile(f32x4 (&acc)[TI][TJ], const LoraTerm &t, int64_t m0,
-                                              int64_t M, int64_t n0) {
-  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-  const int64_t n = KMAJOR ? n0 + TJ * r : n0 + r;
-  int id[TI];
-  bool same = true;
-#pragma unroll
-  for (int i = 0; i < TI; ++i) {
-    const int64_t m = m0 + 16 * i + r;
-    id[i] = m < M ? t.idx[m] : -1;
-  }
-  const int a0 = __builtin_amdgcn_readfirstlane(id[0]);
-#pragma unroll
-  for (int i = 0; i < TI; ++i) same = same && (id[i] == a0 || m0 + 16 * i + r >= M);
-  if (__all(same)) {
-    if (a0 < 0) return;
-    for (int c = 0; c < t.R; c += 32) {
-      const int j0 = c + 8 * g;
-      bf16x8 w[TJ];
-      lora_w_frags<KMAJOR>(t, a0, n, j0, w);
-      const float *h = t.h + m0 * t.R;
-#pragma unroll
-      for (int i = 0; i < TI; ++i) {
-        const int row = 16 * i + r;
-        bf16x8 hi, lo;
-        lora_h_frag(h + row * t.R + j0, j0 < t.R && m0 + row < M, hi, lo);
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) {
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[j], acc[i][j], 0, 0, 0);
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[j], acc[i][j], 0, 0, 0);
-        }
+// smem: LoraLds<BM, BN, KMAJOR>::BYTES bytes that nothing uses once every wave
+// of the workgroup's NT threads has entered. The wave's blocks begin at row row0
+// and column col0 of the tile. The accumulators are touched in one counted loop
+// without branches around them: in loops that leave early or skip blocks the
+// compiler keeps a second copy of them, in scratch memory.
+template <int BM, int BN, int NT, bool KMAJOR, int TI, int TJ>
+__device__ __forceinline__ void lora_add_tile(char *smem, f32x4 (&acc)[TI][TJ], const LoraTerm &t,
+                                              int64_t m0, int64_t M, int64_t n0, int row0,
+                                              int col0) {
+  using S = LoraLds<BM, BN, KMAJOR>;
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  int *ids = reinterpret_cast<int *>(smem + S::H + S::W), *list = ids + BM, *count = list + BM;
+  auto hswz = [](int row) { return (row >> 1) & 7; };
+  auto wswz = [](int row) { return (row >> 2) & 3; };
+  __syncthreads();
+  for (int i = tid; i < BM; i += NT) ids[i] = m0 + i < M ? t.idx[m0 + i] : -1;
+  __syncthreads();
+  if (tid < 64) {
+    int n = 0;
+    for (int prev = -1;; ++n) {
+      int next = 0x7fffffff;
+      for (int i = lane; i < BM; i += 64) {
+        const int v = ids[i];
+        next = v > prev && v < next ? v : next;
       }
-    }
-    return;
-  }
 #pragma unroll
-  for (int i = 0; i < TI; ++i) {
-    int prev = -1;
-    for (;;) {
-      int next = id[i] > prev ? id[i] : 0x7fffffff;
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) {
+      for (int o = 1; o < 64; o <<= 1) {
         const int other = __shfl_xor(next, o);
         next = other < next ? other : next;
       }
-      const int a = __builtin_amdgcn_readfirstlane(next);
-      if (a == 0x7fffffff) break;
-      prev = a;
-      const uint32_t own = (uint32_t)(__ballot(id[i] == a) >> (4 * g));  // bit v: row 4 g + v
-      for (int c = 0; c < t.R; c += 32) {
-        const int j0 = c + 8 * g;
-        bf16x8 hi, lo;
-        lora_h_frag(t.h + (m0 + 16 * i + r) * t.R + j0, j0 < t.R && id[i] == a, hi, lo);
-        bf16x8 w[TJ];
-        lora_w_frags<KMAJOR>(t, a, n, j0, w);
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) {
-          f32x4 d = {0.f, 0.f, 0.f, 0.f};
-          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[j], d, 0, 0, 0);
-          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[j], d, 0, 0, 0);
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[i][j][v] += own & (1u << v) ? d[v] : 0.0f;
-        }
+      prev = __builtin_amdgcn_readfirstlane(next);
+      if (prev == 0x7fffffff) break;
+      if (lane == 0) list[n] = prev;
+    }
+    if (lane == 0) *count = n;
+  }
+  __syncthreads();
+  const int nc = (t.R + 31) / 32;
+  const int steps = __builtin_amdgcn_readfirstlane(*count) * nc;
+  __syncthreads();  // read by every wave: without an adapter the caller goes on at once
+  for (int q = 0; q < steps; ++q) {
+    const int a = __builtin_amdgcn_readfirstlane(list[q / nc]);
+    const int c = q % nc * 32;
+    for (int u = tid; u < BM * 4; u += NT) {  // a row's ranks c + 8 k .. + 7
+      const int row = u >> 2, k = u & 3;
+      f32x4 h0 = {0.f, 0.f, 0.f, 0.f}, h1 = h0;
+      if (ids[row] == a && c + 8 * k < t.R) {  // whole chunks: R is a multiple of 8
+        const float *h = t.h + (m0 + row) * t.R + c + 8 * k;
+        h0 = *reinterpret_cast<const f32x4 *>(h);
+        h1 = *reinterpret_cast<const f32x4 *>(h + 4);
+      }
+      const float v[8] = {h0[0], h0[1], h0[2], h0[3], h1[0], h1[1], h1[2], h1[3]};
+      bf16x8 hi, lo;
+      split_bf16(v, hi, lo);
+      *reinterpret_cast<bf16x8 *>(smem + row * 128 + 16 * (k ^ hswz(row))) = hi;
+      *reinterpret_cast<bf16x8 *>(smem + row * 128 + 16 * ((4 + k) ^ hswz(row))) = lo;
+    }
+    for (int u = tid; u < S::W / 16; u += NT) {
+      i32x4 w = {0, 0, 0, 0};
+      if constexpr (KMAJOR) {
+        const int j = u / (BN / 8), k = u % (BN / 8);  // rank c + j, columns 8 k .. + 7
+        if (c + j < t.R && n0 + 8 * k < t.N)  // whole chunks: N is a multiple of 8
+          w = *reinterpret_cast<const i32x4 *>(t.W + ((int64_t)a * t.R + c + j) * t.N + n0 + 8 * k);
+        *reinterpret_cast<i32x4 *>(smem + S::H + 16 * u) = w;
+      } else {
+        const int row = u >> 2, k = u & 3;  // column n0 + row, ranks c + 8 k .. + 7
+        if (c + 8 * k < t.R && n0 + row < t.N)
+          w = *reinterpret_cast<const i32x4 *>(t.W + ((int64_t)a * t.N + n0 + row) * t.R + c + 8 * k);
+        *reinterpret_cast<i32x4 *>(smem + S::H + row * 64 + 16 * (k ^ wswz(row))) = w;
       }
     }
+    __syncthreads();
+    bf16x8 w[TJ];
+    if constexpr (KMAJOR) {
+      static_assert(!KMAJOR || TJ == 4, "four columns a lane");
+      i32x2 d[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        d[e] = *reinterpret_cast<const i32x2 *>(smem + S::H + (8 * g + e) * BN * 2 +
+                                                2 * (col0 + 4 * r));
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        i32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[e] = (int)__builtin_amdgcn_perm((uint32_t)d[2 * e + 1][j >> 1],
+                                            (uint32_t)d[2 * e][j >> 1],
+                                            j & 1 ? 0x07060302u : 0x05040100u);
+        w[j] = __builtin_bit_cast(bf16x8, v);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        const int row = col0 + 16 * j + r;
+        w[j] = *reinterpret_cast<const bf16x8 *>(smem + S::H + row * 64 + 16 * (g ^ wswz(row)));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const i32x4 id = *reinterpret_cast<const i32x4 *>(ids + row0 + 16 * i + 4 * g);
+      const int row = row0 + 16 * i + r;
+      const bf16x8 hi = *reinterpret_cast<const bf16x8 *>(smem + row * 128 + 16 * (g ^ hswz(row)));
+      const bf16x8 lo =
+          *reinterpret_cast<const bf16x8 *>(smem + row * 128 + 16 * ((4 + g) ^ hswz(row)));
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        f32x4 d = {0.f, 0.f, 0.f, 0.f};
+        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[j], d, 0, 0, 0);
+        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[j], d, 0, 0, 0);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][j][v] += id[v] == a ? d[v] : 0.0f;
+      }
+      __builtin_amdgcn_sched_barrier(0);  // one block's operands at a time
+    }
+    __syncthreads();
   }
 }
 

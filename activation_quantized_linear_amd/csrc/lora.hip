@@ -185,18 +185,17 @@ __global__ __launch_bounds__(256) void k_lora_shrink_rows(
 // ------------------------------------------------------- shrink, tiled form
 
 // A workgroup of W waves takes one tile of the plan (16 rows of one adapter)
-// and all 16 RT ranks; the waves split the contraction in steps of 32 U and
-// meet in LDS. Operands go from memory to the MFMA registers as they lie: both
-// x and A have the contraction contiguous. KMAJOR: the adapter matrix is
-// [C, R] (dy onto B); each wave then copies its step's 32 x 16 blocks into LDS
-// with loads that write it directly and reads them back transposed.
-typedef __attribute__((address_space(3))) void lds_void;
+// and 16 RT ranks; the waves split the contraction in steps of 32 U and meet in
+// LDS. Operands go from memory to the MFMA registers as they lie: both x and A
+// have the contraction contiguous. KMAJOR: the adapter matrix is [C, R] (dy onto
+// B); each wave then passes its step's 32 x 16 blocks through its own LDS slot
+// and reads them back transposed.
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 template <int W, int RT, bool KMAJOR>
 struct ShrinkLds {
-  static constexpr int U = RT <= 2 ? 4 : (RT <= 4 ? 2 : 1);
+  static constexpr int U = RT == 1 ? 4 : 2;
   static constexpr int STEP = KMAJOR ? U * RT * 1024 : 0;  // bytes a wave stages per step
   static constexpr int RED = W * RT * 64 * 16;
   static constexpr int BYTES = W * STEP > RED ? W * STEP : RED;
@@ -211,14 +210,14 @@ __global__ __launch_bounds__(64 * W) void k_lora_shrink(
   constexpr int U = S::U;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const LoraPlanLayout p = lora_plan_layout(M, L);
-  const int tile = blockIdx.x;
+  const int tile = blockIdx.x, rb = blockIdx.y * 16 * RT;  // first rank
   const int a = plan[p.owner + tile];
   if (a == -2) return;
   const int32_t *perm = plan + p.perm + (int64_t)tile * kLoraTile;
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (a < 0) {
-    for (int i = threadIdx.x; i < kLoraTile * R; i += 64 * W) {
+    for (int i = rb == 0 ? (int)threadIdx.x : kLoraTile * R; i < kLoraTile * R; i += 64 * W) {
       const int m = perm[i / R];
       if (m >= 0) h[(int64_t)m * R + i % R] = 0.0f;
     }
@@ -242,15 +241,15 @@ __global__ __launch_bounds__(64 * W) void k_lora_shrink(
       if constexpr (!KMAJOR) {
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-          const int j = 16 * t + r < R ? 16 * t + r : R - 1;  // past R: dropped columns
+          const int jt = rb + 16 * t + r, j = jt < R ? jt : R - 1;  // past R: dropped columns
           av[u][t] = c < C ? *reinterpret_cast<const i32x4 *>(ab + (int64_t)j * C + c) : zero;
         }
       } else {
-        // lane l: row c0 + 32 u + l / 2 of A, ranks 16 t + 8 (l % 2) .. + 7
+        // lane l: row c0 + 32 u + l / 2 of A, ranks rb + 16 t + 8 (l % 2) .. + 7
         const int64_t cr = c0 + 32 * u + (lane >> 1);
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-          const int j = 16 * t + 8 * (lane & 1);
+          const int j = rb + 16 * t + 8 * (lane & 1);
           av[u][t] = cr < C && j < R ? *reinterpret_cast<const i32x4 *>(ab + cr * R + j) : zero;
         }
       }
@@ -296,7 +295,7 @@ __global__ __launch_bounds__(64 * W) void k_lora_shrink(
     f32x4 s = red[t * 64 + lane];
 #pragma unroll
     for (int w = 1; w < W; ++w) s += red[(w * RT + t) * 64 + lane];
-    const int j = 16 * t + r;
+    const int j = rb + 16 * t + r;
     if (j >= R) continue;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
@@ -308,14 +307,15 @@ __global__ __launch_bounds__(64 * W) void k_lora_shrink(
 
 // ----------------------------------------------------------- weight gradients
 
-// One workgroup of W waves: adapter a, 128 columns of dy (dB) or of the
-// checkpoint (dA; they share one scale per row) and 16 RT ranks. The
+// One workgroup of W waves: adapter a, 16 CW columns of dy (dB) or of the
+// checkpoint (dA, 128 columns: they share one scale per row) and 16 RT ranks. The
 // contraction runs over the adapter's rows in sorted order, 32 at a step, the
 // waves taking steps in turn and meeting in LDS at the end. Both operands have
-// the contraction as their slow axis: lane (r, g) reads 8 columns of the 8 rows
-// 8 g .. 8 g + 7 and turns the 8 x 8 block in registers into the operands of 8
-// MFMAs, MFMA c covering columns 8 r + c. The float32 operand (h, or u times
-// the row's scale) is split into three bf16 parts.
+// the contraction as their slow axis: lane (r, g) reads CW columns of the 8 rows
+// 8 g .. 8 g + 7 and turns the 8 x CW block in registers into the operands of CW
+// MFMAs, MFMA c covering columns CW r + c. The float32 operand (h, or u times
+// the row's scale) is split into three bf16 parts. The next step's loads are in
+// flight while one is multiplied.
 // a.lo16 | b.lo16 << 16 and the high halves
 __device__ __forceinline__ int pack_lo(int a, int b) {
   return (int)__builtin_amdgcn_perm((uint32_t)b, (uint32_t)a, 0x05040100u);
@@ -327,6 +327,7 @@ __device__ __forceinline__ int pack_hi(int a, int b) {
 template <int W, int RT, bool CODES>
 __device__ __forceinline__ void lora_wgrad(const LoraWgradArgs &p, const LoraPlanLayout &pl,
                                            int64_t a, int64_t c0, int j0, char *smem) {
+  constexpr int CW = CODES ? 8 : 4;
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t C = CODES ? p.K : p.N;
@@ -335,71 +336,89 @@ __device__ __forceinline__ void lora_wgrad(const LoraWgradArgs &p, const LoraPla
   const int32_t *perm = p.plan + pl.perm;
   const int first = p.plan[pl.first + a] * kLoraTile, last = p.plan[pl.first + a + 1] * kLoraTile;
   const float *left = CODES ? p.u : p.h;
-  const int64_t col = c0 + 8 * r;
-  const bool cin = col < C;  // whole chunks of 8: C is a multiple of 8
+  const int64_t col = c0 + CW * r;
+  const bool cin = col < C;  // whole chunks: C is a multiple of 8
 
-  f32x4 acc[RT][8];
+  f32x4 acc[RT][CW];
 #pragma unroll
   for (int t = 0; t < RT; ++t)
 #pragma unroll
-    for (int c = 0; c < 8; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < CW; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  for (int p0 = first + 32 * wave; p0 < last; p0 += 32 * W) {
-    int row[8];
+  // a step's operands: 8 rows x 8 bytes, their scales, 8 rows x RT ranks; rows
+  // of padding are zero on both sides
+  struct Step {
+    i32x2 d[8];
+    float s[CODES ? 8 : 1], v[RT][8];
+  };
+  auto rows_of = [&](int p0, int (&row)[8]) {
     const int q0 = p0 + 8 * g;
 #pragma unroll
     for (int e = 0; e < 8; ++e) row[e] = q0 + e < last ? perm[q0 + e] : -1;
-    // 8 rows x 8 columns; rows of padding are zero on both sides
-    i32x4 d[8];
-    float s[8];
+  };
+  auto load = [&](const int (&row)[8], Step &b) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      d[e] = i32x4{0, 0, 0, 0};
-      s[e] = 1.0f;
-      if (row[e] >= 0 && cin) {
-        if constexpr (CODES) {
-          const i32x2 v = *reinterpret_cast<const i32x2 *>(p.xq + (int64_t)row[e] * C + col);
-          d[e][0] = v[0];
-          d[e][1] = v[1];
-        } else {
-          d[e] = *reinterpret_cast<const i32x4 *>(p.dy + (int64_t)row[e] * C + col);
-        }
+      const bool in = row[e] >= 0;
+      b.d[e] = i32x2{0, 0};
+      if (in && cin) {
+        if constexpr (CODES)
+          b.d[e] = *reinterpret_cast<const i32x2 *>(p.xq + (int64_t)row[e] * C + col);
+        else
+          b.d[e] = *reinterpret_cast<const i32x2 *>(p.dy + (int64_t)row[e] * C + col);
       }
-      if constexpr (CODES) s[e] = row[e] >= 0 ? p.xs[(int64_t)row[e] * G + c0 / kGroup] : 0.0f;
+      if constexpr (CODES) b.s[e] = in ? p.xs[(int64_t)row[e] * G + c0 / kGroup] : 0.0f;
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        const int j = j0 + 16 * t + r;
+        b.v[t][e] = in && j < R ? left[(int64_t)row[e] * R + j] : 0.0f;
+      }
     }
+  };
+  auto multiply = [&](Step &b) {
     bf16x8 hi[RT], mid[RT], lo[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      float v[8];
-      const int j = j0 + 16 * t + r;
+      if constexpr (CODES)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[e] = row[e] >= 0 && j < R ? left[(int64_t)row[e] * R + j] : 0.0f;
-        if constexpr (CODES) v[e] *= s[e];
-      }
-      split_bf16(v, hi[t], mid[t], lo[t]);
+        for (int e = 0; e < 8; ++e) b.v[t][e] *= b.s[e];
+      split_bf16(b.v[t], hi[t], mid[t], lo[t]);
     }
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      i32x4 b;
+    for (int c = 0; c < CW; ++c) {
+      i32x4 o;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if constexpr (CODES) {
-          const float f0 = (float)(int8_t)(d[2 * e][c >> 2] >> (8 * (c & 3)));
-          const float f1 = (float)(int8_t)(d[2 * e + 1][c >> 2] >> (8 * (c & 3)));
-          b[e] = pack_hi((int)__float_as_uint(f0), (int)__float_as_uint(f1));  // exact
+          const float f0 = (float)(int8_t)(b.d[2 * e][c >> 2] >> (8 * (c & 3)));
+          const float f1 = (float)(int8_t)(b.d[2 * e + 1][c >> 2] >> (8 * (c & 3)));
+          o[e] = pack_hi((int)__float_as_uint(f0), (int)__float_as_uint(f1));  // exact
         } else {
-          b[e] = (c & 1) ? pack_hi(d[2 * e][c >> 1], d[2 * e + 1][c >> 1])
-                         : pack_lo(d[2 * e][c >> 1], d[2 * e + 1][c >> 1]);
+          o[e] = (c & 1) ? pack_hi(b.d[2 * e][c >> 1], b.d[2 * e + 1][c >> 1])
+                         : pack_lo(b.d[2 * e][c >> 1], b.d[2 * e + 1][c >> 1]);
         }
       }
-      const bf16x8 bv = __builtin_bit_cast(bf16x8, b);
+      const bf16x8 bv = __builtin_bit_cast(bf16x8, o);
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[t], bv, acc[t][c], 0, 0, 0);
         acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mid[t], bv, acc[t][c], 0, 0, 0);
         acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[t], bv, acc[t][c], 0, 0, 0);
       }
+    }
+  };
+  int row[8];
+  Step cur, nxt;
+  int p0 = first + 32 * wave;
+  if (p0 < last) {
+    rows_of(p0, row);
+    load(row, cur);
+    rows_of(p0 + 32 * W, row);
+    for (; p0 < last; p0 += 32 * W) {
+      load(row, nxt);
+      rows_of(p0 + 64 * W, row);
+      multiply(cur);
+      cur = nxt;
     }
   }
   // the waves' sums meet pairwise
@@ -411,14 +430,15 @@ __device__ __forceinline__ void lora_wgrad(const LoraWgradArgs &p, const LoraPla
 #pragma unroll
       for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int c = 0; c < 8; ++c) red[(((wave - half) * RT + t) * 8 + c) * 64 + lane] = acc[t][c];
+        for (int c = 0; c < CW; ++c)
+          red[(((wave - half) * RT + t) * CW + c) * 64 + lane] = acc[t][c];
     }
     __syncthreads();
     if (wave < half) {
 #pragma unroll
       for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int c = 0; c < 8; ++c) acc[t][c] += red[((wave * RT + t) * 8 + c) * 64 + lane];
+        for (int c = 0; c < CW; ++c) acc[t][c] += red[((wave * RT + t) * CW + c) * 64 + lane];
     }
   }
   if (wave != 0 || !cin) return;
@@ -442,7 +462,7 @@ __device__ __forceinline__ void lora_wgrad(const LoraWgradArgs &p, const LoraPla
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < CW; ++c) {
         float *dst = p.dB + ((int64_t)a * C + col + c) * R + j;
         f32x4 o = acc[t][c];
         if (p.accumulate) o += *reinterpret_cast<const f32x4 *>(dst);
@@ -460,7 +480,7 @@ __global__ __launch_bounds__(64 * W) void k_lora_wgrad(LoraWgradArgs p, int tile
   const int j0 = blockIdx.z * 16 * RT;
   const int tile = blockIdx.x;
   if (tile < tiles_b)
-    lora_wgrad<W, RT, false>(p, pl, a, (int64_t)tile * 128, j0, smem);
+    lora_wgrad<W, RT, false>(p, pl, a, (int64_t)tile * 64, j0, smem);
   else
     lora_wgrad<W, RT, true>(p, pl, a, (int64_t)(tile - tiles_b) * 128, j0, smem);
 }
@@ -475,7 +495,9 @@ hipError_t go_shrink(const uint16_t *x, int64_t M, int64_t C, const uint16_t *A,
                               hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     (void)hipGetLastError();
   }
-  hipLaunchKernelGGL((k_lora_shrink<W, RT, KMAJOR>), dim3((unsigned)lora_plan_layout(M, L).tiles),
+  hipLaunchKernelGGL((k_lora_shrink<W, RT, KMAJOR>), 
+                     dim3((unsigned)lora_plan_layout(M, L).tiles,
+                          (unsigned)((R + 16 * RT - 1) / (16 * RT))),
                      dim3(64 * W), bytes, st, x, C, A, alpha, (int)R, M, L, plan, h);
   return hipGetLastError();
 }
@@ -484,10 +506,13 @@ template <bool KMAJOR>
 hipError_t go_shrink_r(const uint16_t *x, int64_t M, int64_t C, const uint16_t *A,
                        const float *alpha, int64_t L, int64_t R, const int32_t *plan, float *h,
                        hipStream_t st) {
-  if (R <= 16) return go_shrink<8, 1, KMAJOR>(x, M, C, A, alpha, L, R, plan, h, st);
-  if (R <= 32) return go_shrink<8, 2, KMAJOR>(x, M, C, A, alpha, L, R, plan, h, st);
-  if (R <= 64) return go_shrink<8, 4, KMAJOR>(x, M, C, A, alpha, L, R, plan, h, st);
-  return go_shrink<8, 8, KMAJOR>(x, M, C, A, alpha, L, R, plan, h, st);
+  // One block of 16 ranks a workgroup: x is read once per block of ranks, from
+  // the caches, and the grid fills the chip (M = 500, K = 4096, R = 64: 21 us with
+  // all 64 ranks in each of 32 workgroups). Once there are more than four
+  // workgroups a CU, 64 ranks share a read of x.
+  if ((M / kLoraTile) * ((R + 15) / 16) > 1024)
+    return go_shrink<8, 4, KMAJOR>(x, M, C, A, alpha, L, R, plan, h, st);
+  return go_shrink<16, 1, KMAJOR>(x, M, C, A, alpha, L, R, plan, h, st);
 }
 
 template <int W, int RT>
@@ -498,7 +523,7 @@ hipError_t go_wgrad(const LoraWgradArgs &a, hipStream_t st) {
                               hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     (void)hipGetLastError();
   }
-  const int tb = a.dB ? (int)((a.N + 127) / 128) : 0, ta = a.dA ? (int)((a.K + 127) / 128) : 0;
+  const int tb = a.dB ? (int)((a.N + 63) / 64) : 0, ta = a.dA ? (int)((a.K + 127) / 128) : 0;
   const dim3 grid((unsigned)(tb + ta), (unsigned)a.L, (unsigned)((a.R + 16 * RT - 1) / (16 * RT)));
   hipLaunchKernelGGL((k_lora_wgrad<W, RT>), grid, dim3(64 * W), bytes, st, a, tb);
   return hipGetLastError();
@@ -533,9 +558,8 @@ hipError_t launch_lora_shrink_t(const uint16_t *dy, int64_t M, int64_t N, const 
 }
 
 hipError_t launch_lora_wgrad(const LoraWgradArgs &a, hipStream_t st) {
-  if (a.R <= 16) return go_wgrad<8, 1>(a, st);
-  if (a.R <= 32) return go_wgrad<8, 2>(a, st);
-  return go_wgrad<4, 4>(a, st);
+  if (a.R <= 16) return go_wgrad<16, 1>(a, st);
+  return go_wgrad<8, 2>(a, st);
 }
 
 }  // namespace aql

@@ -151,6 +151,7 @@ struct DgradLds {
   static constexpr int TILEF = BM * TLDF * 4;
   static constexpr int BYTES = RING > TILE ? RING : TILE;
   static constexpr int BYTES_SPLIT = RING > TILEF ? RING : TILEF;
+  static_assert(BYTES >= LoraLds<BM, BK, true>::BYTES, "the adapter terms stage in the ring");
   static_assert(NX * NWV * 8 == BM && NQ * NWV * 1024 == BC * BK, "loads split evenly");
   static_assert(NL * (SG - 2) < 64, "vmcnt");
 };
@@ -397,7 +398,9 @@ __global__ __launch_bounds__(64 * NWV, 2) void k_w8a16_dgrad(
     }
     return;
   }
-  if constexpr (LT::on) lora_add_tile<true>(acc, lt, m0, M, k0 + 64 * wave);
+  if constexpr (LT::on) {
+    lora_add_tile<BM, BK, 64 * NWV, true>(smem, acc, lt, m0, M, k0, 0, 64 * wave);
+  }
   uint16_t *tl = reinterpret_cast<uint16_t *>(smem);
 #pragma unroll
   for (int i = 0; i < TI; ++i)

@@ -98,6 +98,7 @@ struct GemmLds {
   static constexpr int TILE = BM * TLD * 2;
   static constexpr int BYTES = RING > XCH + TILE ? RING : XCH + TILE;
   static_assert(NXL * NG == BM / 8 && NWL * NG == 8, "load slots split evenly");
+  static_assert(BYTES >= LoraLds<BM, BN, false>::BYTES, "the adapter terms stage in the ring");
   static_assert(SG % KP == 0 && PS >= 3, "ring of whole steps, one read ahead");
 };
 
@@ -318,7 +319,10 @@ __global__ __launch_bounds__((64 * GemmLds<WM, TI, SG, KP>::NW)) void k_w8a16_ge
           for (int v = 0; v < 4; ++v) acc[i][j][v] = s * v4[v] + b;
         }
       }
-      lora_add_tile<false>(acc, lt, m0 + wm * 16 * TI, M, n0 + wn * 64);
+    }
+    // (the other partners' accumulators take part and are dropped)
+    lora_add_tile<BM, BN, 64 * NW, false>(smem, acc, lt, m0, M, n0, wm * 16 * TI, wn * 64);
+    if (part == 0) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -385,6 +389,7 @@ struct WideLds {
   static constexpr int TLD = BNW + 8;           // bf16 per staged output row
   static constexpr int TILE = BM * TLD * 2;
   static constexpr int BYTES = RING > TILE ? RING : TILE;
+  static_assert(BYTES >= LoraLds<BM, BNW, false>::BYTES, "the adapter terms stage in the ring");
   static constexpr int TLDF = BNW + 4;          // fp32 per staged partial-sum row (split K)
   static constexpr int TILEF = BM * TLDF * 4;
   static constexpr int BYTES_SPLIT = RING > TILEF ? RING : TILEF;
@@ -595,7 +600,7 @@ __global__ __launch_bounds__(512, SG == 2 ? 4 : 2) void k_w8a16_gemm_wide(const 
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[i][j][v] = s * acc[i][j][v] + b;
     }
-    lora_add_tile<false>(acc, lt, m0, M, n0 + wn * 32);
+    lora_add_tile<BM, BNW, 512, false>(smem, acc, lt, m0, M, n0, 0, wn * 32);
   }
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
