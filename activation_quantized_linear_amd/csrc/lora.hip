@@ -211,11 +211,13 @@ __global__ __launch_bounds__(64 * W) void k_lora_shrink(
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const LoraPlanLayout p = lora_plan_layout(M, L);
   const int tile = blockIdx.x, rb = blockIdx.y * 16 * RT;  // first rank
-  const int a = plan[p.owner + tile];
-  if (a == -2) return;
   const int32_t *perm = plan + p.perm + (int64_t)tile * kLoraTile;
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // the tile's adapter and rows at once, not one after the other
+  const int a = plan[p.owner + tile], mine = perm[r], head = perm[0];
+  const i32x4 out = *reinterpret_cast<const i32x4 *>(perm + 4 * g);
+  if (a == -2) return;
   if (a < 0) {
     for (int i = rb == 0 ? (int)threadIdx.x : kLoraTile * R; i < kLoraTile * R; i += 64 * W) {
       const int m = perm[i / R];
@@ -223,26 +225,28 @@ __global__ __launch_bounds__(64 * W) void k_lora_shrink(
     }
     return;
   }
+  const float al = alpha[a];
   // a padding position computes the tile's first row again; its results are dropped
-  const int mrow = perm[r] >= 0 ? perm[r] : perm[0];
-  const uint16_t *xr = x + (int64_t)mrow * C;
+  const uint16_t *xr = x + (int64_t)(mine >= 0 ? mine : head) * C;
   const uint16_t *ab = A + (int64_t)a * R * C;
   const i32x4 zero = {0, 0, 0, 0};
   f32x4 acc[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
   char *stage = smem + wave * S::STEP;
-  for (int64_t c0 = (int64_t)wave * (32 * U); c0 < C; c0 += (int64_t)W * 32 * U) {
-    i32x4 xv[U], av[U][RT];
+  struct Step {
+    i32x4 x[U], a[U][RT];
+  };
+  auto load = [&](int64_t c0, Step &s) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t c = c0 + 32 * u + 8 * g;
-      xv[u] = c < C ? *reinterpret_cast<const i32x4 *>(xr + c) : zero;
+      s.x[u] = c < C ? *reinterpret_cast<const i32x4 *>(xr + c) : zero;
       if constexpr (!KMAJOR) {
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
           const int jt = rb + 16 * t + r, j = jt < R ? jt : R - 1;  // past R: dropped columns
-          av[u][t] = c < C ? *reinterpret_cast<const i32x4 *>(ab + (int64_t)j * C + c) : zero;
+          s.a[u][t] = c < C ? *reinterpret_cast<const i32x4 *>(ab + (int64_t)j * C + c) : zero;
         }
       } else {
         // lane l: row c0 + 32 u + l / 2 of A, ranks rb + 16 t + 8 (l % 2) .. + 7
@@ -250,17 +254,19 @@ __global__ __launch_bounds__(64 * W) void k_lora_shrink(
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
           const int j = rb + 16 * t + 8 * (lane & 1);
-          av[u][t] = cr < C && j < R ? *reinterpret_cast<const i32x4 *>(ab + cr * R + j) : zero;
+          s.a[u][t] = cr < C && j < R ? *reinterpret_cast<const i32x4 *>(ab + cr * R + j) : zero;
         }
       }
     }
+  };
+  auto multiply = [&](Step &s) {
     if constexpr (KMAJOR) {
       // a wave's own LDS slot: its stores and loads complete in order
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int t = 0; t < RT; ++t)
-          *reinterpret_cast<i32x4 *>(stage + (u * RT + t) * 1024 + 16 * lane) = av[u][t];
+          *reinterpret_cast<i32x4 *>(stage + (u * RT + t) * 1024 + 16 * lane) = s.a[u][t];
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -273,7 +279,7 @@ __global__ __launch_bounds__(64 * W) void k_lora_shrink(
           const s16x4 hi =
               __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)(at + 128));
           const i32x2 l2 = __builtin_bit_cast(i32x2, lo), h2 = __builtin_bit_cast(i32x2, hi);
-          av[u][t] = i32x4{l2[0], l2[1], h2[0], h2[1]};
+          s.a[u][t] = i32x4{l2[0], l2[1], h2[0], h2[1]};
         }
       __builtin_amdgcn_wave_barrier();
     }
@@ -281,16 +287,27 @@ __global__ __launch_bounds__(64 * W) void k_lora_shrink(
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int t = 0; t < RT; ++t)
-        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv[u]),
-                                                         __builtin_bit_cast(bf16x8, av[u][t]),
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, s.x[u]),
+                                                         __builtin_bit_cast(bf16x8, s.a[u][t]),
                                                          acc[t], 0, 0, 0);
+  };
+  // the next step's loads are in flight while one is multiplied
+  constexpr int64_t STRIDE = (int64_t)W * 32 * U;
+  int64_t c0 = (int64_t)wave * (32 * U);
+  if (c0 < C) {
+    Step cur, nxt;
+    load(c0, cur);
+    for (; c0 < C; c0 += STRIDE) {
+      if (c0 + STRIDE < C) load(c0 + STRIDE, nxt);
+      multiply(cur);
+      cur = nxt;
+    }
   }
   __syncthreads();
   f32x4 *red = reinterpret_cast<f32x4 *>(smem);
 #pragma unroll
   for (int t = 0; t < RT; ++t) red[(wave * RT + t) * 64 + lane] = acc[t];
   __syncthreads();
-  const float al = alpha[a];
   for (int t = wave; t < RT; t += W) {
     f32x4 s = red[t * 64 + lane];
 #pragma unroll
@@ -299,7 +316,7 @@ __global__ __launch_bounds__(64 * W) void k_lora_shrink(
     if (j >= R) continue;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int m = perm[4 * g + v];
+      const int m = out[v];
       if (m >= 0) h[(int64_t)m * R + j] = al * s[v];
     }
   }
@@ -558,8 +575,12 @@ hipError_t launch_lora_shrink_t(const uint16_t *dy, int64_t M, int64_t N, const 
 }
 
 hipError_t launch_lora_wgrad(const LoraWgradArgs &a, hipStream_t st) {
-  if (a.R <= 16) return go_wgrad<16, 1>(a, st);
-  return go_wgrad<8, 2>(a, st);
+  // 16 ranks a workgroup; 4 waves where an adapter's rows are few (they would
+  // have no second step), 32 ranks where the data read again per block of ranks
+  // would come to more than the caches hold
+  if (a.R > 16 && a.M > 1024) return go_wgrad<8, 2>(a, st);
+  if (a.M / a.L > 512) return go_wgrad<16, 1>(a, st);
+  return go_wgrad<4, 1>(a, st);
 }
 
 }  // namespace aql
