@@ -91,7 +91,8 @@ _SIGS = {
     "aql_linear_w8a16_lora": ([_p, _i64, _i64, _p, _p, _p, _i64, _p, _p, _p, _i64, _i64, _p, _p,
                                _p, _p, _sz, _p], _int),
     "aql_linear_w8a16_dgrad": ([_p, _i64, _i64, _p, _p, _i64, _p, _p, _sz, _p], _int),
-    "aql_lora_backward_bytes": ([_i64, _i64, _i64, _i64], _sz),
+    "aql_lora_forward_bytes": ([_i64, _i64, _i64, _i64, _i64], _sz),
+    "aql_lora_backward_bytes": ([_i64, _i64, _i64, _i64, _i64], _sz),
     "aql_linear_w8a16_lora_backward": ([_p, _i64, _i64, _p, _p, _i64, _p, _p, _p, _i64, _i64, _p,
                                         _p, _p, _p, _int, _p, _p, _p, _p, _sz, _p], _int),
     "aql_act_checkpoint": ([_p, _int, _i64, _i64, _p, _p, _p], _int),
@@ -603,12 +604,17 @@ def _lora_args(A, B, alpha, N, K, dev):
     return L, R
 
 
+def aql_lora_forward_bytes(M, N, K, L, R):
+    return _lib.aql_lora_forward_bytes(M, N, K, L, R)
+
+
 def aql_linear_w8a16_lora(x, q, scale, A, B, alpha, plan, bias=None, y=None, h=None,
                           workspace=None):
     """W8A16 linear with every row's low-rank adapter. x bfloat16 [M, K], q int8 [N, K],
     scale float32 [N], A bfloat16 [L, R, K], B bfloat16 [L, N, R], alpha float32 [L],
     plan of aql_lora_plan, bias bfloat16 [N] -> (y bfloat16 [M, N], h float32 [M, R]),
-    h = alpha A x, which the backward pass takes. workspace: as aql_linear_w8a16."""
+    h = alpha A x, which the backward pass takes. workspace: uint8 device tensor of
+    aql_lora_forward_bytes; allocated here when one is needed and none is given."""
     _need(x, "x", torch.bfloat16, 2)
     dev = x.device
     M, K = x.shape
@@ -624,7 +630,7 @@ def aql_linear_w8a16_lora(x, q, scale, A, B, alpha, plan, bias=None, y=None, h=N
         _shape(bias, "bias", (N,))
     y = _out(y, "y", (M, N), torch.bfloat16, dev)
     h = _out(h, "h", (M, R), torch.float32, dev)
-    nbytes = aql_workspace_bytes(AQL_OP_W8A16, M, N, K)
+    nbytes = aql_lora_forward_bytes(M, N, K, L, R)
     ws = _workspace(workspace, nbytes, dev) if workspace is not None or nbytes > 0 else None
     _call("aql_linear_w8a16_lora", dev, _ptr(x), M, K, _ptr(q), _ptr(scale), _ptr(bias), N,
           _ptr(A), _ptr(B), _ptr(alpha), L, R, _ptr(plan.buffer), _ptr(y), _ptr(h), _ptr(ws), 0
@@ -650,8 +656,8 @@ def aql_linear_w8a16_dgrad(dy, q, scale, dx=None, workspace=None):
     return dx
 
 
-def aql_lora_backward_bytes(M, N, K, R):
-    return _lib.aql_lora_backward_bytes(M, N, K, R)
+def aql_lora_backward_bytes(M, N, K, L, R):
+    return _lib.aql_lora_backward_bytes(M, N, K, L, R)
 
 
 def aql_linear_w8a16_lora_backward(dy, q, scale, A, B, alpha, plan, h, xq, xs, dx=None, dA=None,
@@ -684,7 +690,7 @@ def aql_linear_w8a16_lora_backward(dy, q, scale, A, B, alpha, plan, h, xq, xs, d
     dx = _out(dx, "dx", (M, K), torch.bfloat16, dev) if need_dx else None
     dA = _out(dA, "dA", (L, R, K), torch.float32, dev)
     dB = _out(dB, "dB", (L, N, R), torch.float32, dev)
-    ws = _workspace(workspace, aql_lora_backward_bytes(M, N, K, R), dev)
+    ws = _workspace(workspace, aql_lora_backward_bytes(M, N, K, L, R), dev)
     _call("aql_linear_w8a16_lora_backward", dev, _ptr(dy), M, N, _ptr(q), _ptr(scale), K,
           _ptr(A), _ptr(B), _ptr(alpha), L, R, _ptr(plan.buffer), _ptr(h), _ptr(xq), _ptr(xs),
           int(bool(accumulate)), _ptr(dx), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel())

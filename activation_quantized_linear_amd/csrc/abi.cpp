@@ -184,8 +184,26 @@ static_assert(AQL_LORA_MAX_ADAPTERS == aql::kLoraMaxAdapters &&
                   AQL_LORA_MAX_RANK == aql::kLoraMaxRank && AQL_CKPT_GROUP == aql::kCkptGroup,
               "adapter bounds");
 
-// u [M, R], then the workspace of dx.
+// Workspace of the linear with adapters: the linear's own split-K partial sums,
+// and before them (the shrink is done first) the shrink's. One region serves both.
+size_t ws_lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+  const size_t lin = M >= kW8A16GemmMinM ? (K <= (1LL << 22) ? aql::w8a16_gemm_part_bytes(M, N, K) : 0)
+                                         : aql::w8a16_skinny_part_bytes(M, N, K);
+  const size_t shr = M >= aql::kLoraTiledMinM ? aql::lora_shrink_bytes(M, K, L, R) : 0;
+  return lin > shr ? lin : shr;
+}
+
+// Workspace of its backward pass: u [M, R], then one region for the shrink's
+// partial sums and, after them, dx's.
 size_t lora_bwd_u_bytes(int64_t M, int64_t R) { return align256((size_t)M * (size_t)R * 4); }
+size_t ws_lora_bwd(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+  const size_t shr = aql::lora_shrink_bytes(M, N, L, R), dx = aql::w8a16_dgrad_bytes(M, N, K);
+  return lora_bwd_u_bytes(M, R) + (shr > dx ? shr : dx);
+}
+bool lora_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+  return plan_sizes_ok(M, L) && M > 0 && N >= 0 && K >= 16 && K <= kMaxKW8A16 && R >= 8 &&
+         R <= AQL_LORA_MAX_RANK && R % 8 == 0;
+}
 
 // Validation shared by both static W8A8 entry points (all before any HIP call).
 int check_q8ta(const char *fn, const float *x, int64_t M, int64_t K, float s1, int32_t z1,
@@ -642,6 +660,10 @@ int aql_lora_plan(const int32_t *idx, int64_t M, int64_t L, void *plan, size_t p
                   fn);
 }
 
+size_t aql_lora_forward_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+  return lora_sizes_ok(M, N, K, L, R) ? ws_lora(M, N, K, L, R) : 0;
+}
+
 int aql_linear_w8a16_lora(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
                           const float *scale, const uint16_t *bias, int64_t N, const uint16_t *A,
                           const uint16_t *B, const float *alpha, int64_t L, int64_t R,
@@ -654,10 +676,14 @@ int aql_linear_w8a16_lora(const uint16_t *x, int64_t M, int64_t K, const int8_t 
   if (M == 0 || N == 0) return ok();
   REQUIRE(A && B && alpha && plan && h, AQL_ERR_NULL,
           "%s: A, B, alpha, plan and h must not be NULL", fn);
+  const size_t need = ws_lora(M, N, K, L, R);
+  REQUIRE(need == 0 || (ws && ws_bytes >= need), AQL_ERR_WORKSPACE,
+          "%s: workspace needs %zu bytes (got %zu)", fn, need, ws ? ws_bytes : (size_t)0);
   if (int e = check_device(fn)) return e;
   hipStream_t st = (hipStream_t)stream;
   const int32_t *p = static_cast<const int32_t *>(plan);
-  hipError_t e = aql::launch_lora_shrink(x, M, K, A, alpha, L, R, p, h, st);
+  hipError_t e =
+      aql::launch_lora_shrink(x, M, K, A, alpha, L, R, p, h, static_cast<float *>(ws), st);
   if (e != hipSuccess) return launched(e, fn);
   const aql::LoraTerm lt{h, B, p + aql::lora_plan_layout(M, L).idx, (int32_t)R, N};
   float *part = static_cast<float *>(ws);
@@ -685,11 +711,8 @@ int aql_linear_w8a16_dgrad(const uint16_t *dy, int64_t M, int64_t N, const int8_
       aql::launch_w8a16_dgrad(dy, M, N, q, scale, K, dx, ws, (hipStream_t)stream), fn);
 }
 
-size_t aql_lora_backward_bytes(int64_t M, int64_t N, int64_t K, int64_t R) {
-  if (M <= 0 || M > kMaxRows || N < 0 || N > (1LL << 22) || K < 16 || K > kMaxKW8A16 || R < 8 ||
-      R > AQL_LORA_MAX_RANK)
-    return 0;
-  return lora_bwd_u_bytes(M, R) + aql::w8a16_dgrad_bytes(M, N, K);
+size_t aql_lora_backward_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+  return lora_sizes_ok(M, N, K, L, R) && N <= (1LL << 22) ? ws_lora_bwd(M, N, K, L, R) : 0;
 }
 
 int aql_linear_w8a16_lora_backward(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q,
@@ -708,7 +731,7 @@ int aql_linear_w8a16_lora_backward(const uint16_t *dy, int64_t M, int64_t N, con
           "%s: A, alpha and h (xq and xs with dA) must not be NULL", fn);
   REQUIRE(M == 0 || N == 0 || (dy && q && scale && B), AQL_ERR_NULL,
           "%s: dy, q, scale and B must not be NULL", fn);
-  const size_t need = aql_lora_backward_bytes(M, N, K, R);
+  const size_t need = aql_lora_backward_bytes(M, N, K, L, R);
   REQUIRE(M == 0 || (ws && ws_bytes >= need), AQL_ERR_WORKSPACE,
           "%s: workspace needs %zu bytes (got %zu)", fn, need, ws ? ws_bytes : (size_t)0);
   if (!dx && !dA && !dB) return ok();
@@ -716,9 +739,10 @@ int aql_linear_w8a16_lora_backward(const uint16_t *dy, int64_t M, int64_t N, con
   hipStream_t st = (hipStream_t)stream;
   const int32_t *p = static_cast<const int32_t *>(plan);
   float *u = static_cast<float *>(ws);
+  void *rest = static_cast<char *>(ws) + lora_bwd_u_bytes(M, R);
   hipError_t e = hipSuccess;
   if (M > 0 && (dx || dA)) {
-    e = aql::launch_lora_shrink_t(dy, M, N, B, alpha, L, R, p, u, st);
+    e = aql::launch_lora_shrink_t(dy, M, N, B, alpha, L, R, p, u, static_cast<float *>(rest), st);
     if (e != hipSuccess) return launched(e, fn);
   }
   if (dA || (dB && N > 0)) {
@@ -742,8 +766,7 @@ int aql_linear_w8a16_lora_backward(const uint16_t *dy, int64_t M, int64_t N, con
   }
   if (dx && M > 0) {
     const aql::LoraTerm lt{u, A, p + aql::lora_plan_layout(M, L).idx, (int32_t)R, K};
-    e = aql::launch_w8a16_dgrad(dy, M, N, q, scale, K, dx,
-                                static_cast<char *>(ws) + lora_bwd_u_bytes(M, R), st, lt);
+    e = aql::launch_w8a16_dgrad(dy, M, N, q, scale, K, dx, rest, st, lt);
   }
   return launched(e, fn);
 }

@@ -245,17 +245,24 @@ __device__ __forceinline__ void lora_add_tile(char *smem, f32x4 (&acc)[TI][TJ], 
 
 // ---------------------------------------------------------------- launchers
 
+// Rows from which the shrink of x takes the tiled form, and the bytes of either
+// shrink's partial sums in the tiled form (C: the length of the contraction).
+constexpr int64_t kLoraTiledMinM = 64;
+size_t lora_shrink_bytes(int64_t M, int64_t C, int64_t L, int64_t R);
+
 // h[m, :] = alpha[a] A_a x[m] (float32 [M, R]); rows without an adapter get
-// zeros. x [M, K] bf16, A [L, R, K] bf16.
+// zeros. x [M, K] bf16, A [L, R, K] bf16. part: lora_shrink_bytes(M, K, L, R)
+// bytes from kLoraTiledMinM rows on.
 hipError_t launch_lora_shrink(const uint16_t *x, int64_t M, int64_t K, const uint16_t *A,
                               const float *alpha, int64_t L, int64_t R, const int32_t *plan,
-                              float *h, hipStream_t st);
+                              float *h, float *part, hipStream_t st);
 
 // u[m, :] = alpha[a] B_a^T dy[m] (float32 [M, R]); rows without an adapter get
-// zeros. dy [M, N] bf16, B [L, N, R] bf16, N % 8 == 0.
+// zeros. dy [M, N] bf16, B [L, N, R] bf16, N % 8 == 0. part:
+// lora_shrink_bytes(M, N, L, R) bytes.
 hipError_t launch_lora_shrink_t(const uint16_t *dy, int64_t M, int64_t N, const uint16_t *B,
                                 const float *alpha, int64_t L, int64_t R, const int32_t *plan,
-                                float *u, hipStream_t st);
+                                float *u, float *part, hipStream_t st);
 
 // dB[a][n, j] = sum_{m in a} dy[m, n] h[m, j] and
 // dA[a][j, k] = sum_{m in a} u[m, j] xq[m, k] xs[m, k / 128], both float32;

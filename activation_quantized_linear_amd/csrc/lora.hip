@@ -184,142 +184,193 @@ __global__ __launch_bounds__(256) void k_lora_shrink_rows(
 
 // ------------------------------------------------------- shrink, tiled form
 
-// A workgroup of W waves takes one tile of the plan (16 rows of one adapter)
-// and 16 RT ranks; the waves split the contraction in steps of 32 U and meet in
-// LDS. Operands go from memory to the MFMA registers as they lie: both x and A
-// have the contraction contiguous. KMAJOR: the adapter matrix is [C, R] (dy onto
-// B); each wave then passes its step's 32 x 16 blocks through its own LDS slot
-// and reads them back transposed.
+// A workgroup of 4 waves takes kNT tiles of the plan (64 rows, mostly of one
+// adapter), 16 ranks and one of gridDim.z ranges of the contraction; its waves
+// take steps of 64 in turn and meet in LDS. A CU draws little more than its 1/256
+// of the memory's rate, so what each workgroup reads decides: 64 rows share a
+// read of the 16 ranks (with one tile of 16 rows the adapter's bytes equal the
+// rows'), and the ranges spread few rows over the chip. Several ranges leave
+// float32 partial sums in sorted order, which k_lora_shrink_sum adds in order.
+// Operands go from memory to the MFMA registers as they lie: x and A have the
+// contraction contiguous. KMAJOR: the adapter matrix is [C, R] (dy onto B); each
+// wave then passes its step's 32 x 16 blocks through its own LDS slot and reads
+// them back transposed.
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-template <int W, int RT, bool KMAJOR>
-struct ShrinkLds {
-  static constexpr int U = RT == 1 ? 4 : 2;
-  static constexpr int STEP = KMAJOR ? U * RT * 1024 : 0;  // bytes a wave stages per step
-  static constexpr int RED = W * RT * 64 * 16;
-  static constexpr int BYTES = W * STEP > RED ? W * STEP : RED;
-};
+constexpr int kNT = 4, kWaves = 4, kU = 2;
+constexpr int kStep = 32 * kU;  // of the contraction, per wave and step
 
-template <int W, int RT, bool KMAJOR>
-__global__ __launch_bounds__(64 * W) void k_lora_shrink(
+template <bool KMAJOR>
+__global__ __launch_bounds__(64 * kWaves, 2) void k_lora_shrink(
     const uint16_t *__restrict__ x, int64_t C, const uint16_t *__restrict__ A,
     const float *__restrict__ alpha, int R, int64_t M, int64_t L,
-    const int32_t *__restrict__ plan, float *__restrict__ h) {
-  using S = ShrinkLds<W, RT, KMAJOR>;
-  constexpr int U = S::U;
-  extern __shared__ __attribute__((aligned(16))) char smem[];
+    const int32_t *__restrict__ plan, float *__restrict__ h, float *__restrict__ part,
+    int64_t range) {
+  __shared__ __attribute__((aligned(16))) char smem[kWaves * kNT * 64 * 16];
+  static_assert(kU * 1024 <= kNT * 64 * 16, "a wave's slot holds its step");
   const LoraPlanLayout p = lora_plan_layout(M, L);
-  const int tile = blockIdx.x, rb = blockIdx.y * 16 * RT;  // first rank
-  const int32_t *perm = plan + p.perm + (int64_t)tile * kLoraTile;
+  const int t0 = blockIdx.x * kNT, rb = blockIdx.y * 16;  // first tile, first rank
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // the tile's adapter and rows at once, not one after the other
-  const int a = plan[p.owner + tile], mine = perm[r], head = perm[0];
-  const i32x4 out = *reinterpret_cast<const i32x4 *>(perm + 4 * g);
-  if (a == -2) return;
-  if (a < 0) {
-    for (int i = rb == 0 ? (int)threadIdx.x : kLoraTile * R; i < kLoraTile * R; i += 64 * W) {
-      const int m = perm[i / R];
-      if (m >= 0) h[(int64_t)m * R + i % R] = 0.0f;
-    }
-    return;
+  const int64_t c_lo = blockIdx.z * range, c_hi = c_lo + range < C ? c_lo + range : C;
+  int owner[kNT], row[kNT];
+#pragma unroll
+  for (int t = 0; t < kNT; ++t) {
+    const bool in = t0 + t < p.tiles;
+    owner[t] = in ? plan[p.owner + t0 + t] : -2;
+    // a padding position computes the tile's first row again; its results are dropped
+    const int32_t *perm = plan + p.perm + (int64_t)(in ? t0 + t : t0) * kLoraTile;
+    row[t] = perm[r] >= 0 ? perm[r] : perm[0];
   }
-  const float al = alpha[a];
-  // a padding position computes the tile's first row again; its results are dropped
-  const uint16_t *xr = x + (int64_t)(mine >= 0 ? mine : head) * C;
-  const uint16_t *ab = A + (int64_t)a * R * C;
   const i32x4 zero = {0, 0, 0, 0};
-  f32x4 acc[RT];
+  char *stage = smem + wave * (kNT * 64 * 16);
+  f32x4 *red = reinterpret_cast<f32x4 *>(smem);
+  int done = -1;
+  for (;;) {
+    // the tiles' adapters in ascending order (-1 and -2: nothing to compute)
+    int a = 0x7fffffff;
 #pragma unroll
-  for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  char *stage = smem + wave * S::STEP;
-  struct Step {
-    i32x4 x[U], a[U][RT];
-  };
-  auto load = [&](int64_t c0, Step &s) {
+    for (int t = 0; t < kNT; ++t) a = owner[t] > done && owner[t] < a ? owner[t] : a;
+    if (a == 0x7fffffff) break;
+    done = a;
+    int any = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c = c0 + 32 * u + 8 * g;
-      s.x[u] = c < C ? *reinterpret_cast<const i32x4 *>(xr + c) : zero;
-      if constexpr (!KMAJOR) {
+    for (int t = kNT - 1; t >= 0; --t) any = owner[t] == a ? row[t] : any;
+    const uint16_t *xr[kNT];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          const int jt = rb + 16 * t + r, j = jt < R ? jt : R - 1;  // past R: dropped columns
-          s.a[u][t] = c < C ? *reinterpret_cast<const i32x4 *>(ab + (int64_t)j * C + c) : zero;
+    for (int t = 0; t < kNT; ++t)  // another adapter's tile reads one of this one's again
+      xr[t] = x + (int64_t)(owner[t] == a ? row[t] : any) * C;
+    const uint16_t *ab = A + (int64_t)a * R * C;
+    f32x4 acc[kNT];
+#pragma unroll
+    for (int t = 0; t < kNT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    struct Step {
+      i32x4 x[kU][kNT], a[kU];
+    };
+    auto load = [&](int64_t c0, Step &s) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int64_t c = c0 + 32 * u + 8 * g;
+        if constexpr (!KMAJOR) {
+          const int j = rb + r < R ? rb + r : R - 1;  // past R: dropped columns
+          s.a[u] = c < c_hi ? *reinterpret_cast<const i32x4 *>(ab + (int64_t)j * C + c) : zero;
+        } else {
+          // lane l: row c0 + 32 u + l / 2 of A, ranks rb + 8 (l % 2) .. + 7
+          const int64_t cr = c0 + 32 * u + (lane >> 1);
+          const int j = rb + 8 * (lane & 1);
+          s.a[u] = cr < c_hi && j < R ? *reinterpret_cast<const i32x4 *>(ab + cr * R + j) : zero;
         }
-      } else {
-        // lane l: row c0 + 32 u + l / 2 of A, ranks rb + 16 t + 8 (l % 2) .. + 7
-        const int64_t cr = c0 + 32 * u + (lane >> 1);
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          const int j = rb + 16 * t + 8 * (lane & 1);
-          s.a[u][t] = cr < C && j < R ? *reinterpret_cast<const i32x4 *>(ab + cr * R + j) : zero;
-        }
+        for (int t = 0; t < kNT; ++t)
+          s.x[u][t] = c < c_hi ? *reinterpret_cast<const i32x4 *>(xr[t] + c) : zero;
       }
-    }
-  };
-  auto multiply = [&](Step &s) {
-    if constexpr (KMAJOR) {
-      // a wave's own LDS slot: its stores and loads complete in order
+    };
+    auto multiply = [&](Step &s) {
+      if constexpr (KMAJOR) {
+        // a wave's own LDS slot: its stores and loads complete in order
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+        for (int u = 0; u < kU; ++u)
+          *reinterpret_cast<i32x4 *>(stage + u * 1024 + 16 * lane) = s.a[u];
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
-          *reinterpret_cast<i32x4 *>(stage + (u * RT + t) * 1024 + 16 * lane) = s.a[u][t];
-      __builtin_amdgcn_wave_barrier();
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
+        for (int u = 0; u < kU; ++u) {
           // 16 lanes read 4 rows x 16 ranks and get column r of them
-          const uint32_t at = (uint32_t)(uintptr_t)(stage + (u * RT + t) * 1024 +
-                                                    (8 * g + (r >> 2)) * 32 + 8 * (r & 3));
+          const uint32_t at = (uint32_t)(uintptr_t)(stage + u * 1024 + (8 * g + (r >> 2)) * 32 +
+                                                    8 * (r & 3));
           const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)at);
           const s16x4 hi =
               __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)(at + 128));
           const i32x2 l2 = __builtin_bit_cast(i32x2, lo), h2 = __builtin_bit_cast(i32x2, hi);
-          s.a[u][t] = i32x4{l2[0], l2[1], h2[0], h2[1]};
+          s.a[u] = i32x4{l2[0], l2[1], h2[0], h2[1]};
         }
-      __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_wave_barrier();
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int t = 0; t < kNT; ++t)
+          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, s.x[u][t]),
+                                                           __builtin_bit_cast(bf16x8, s.a[u]),
+                                                           acc[t], 0, 0, 0);
+    };
+    // the next step's loads are in flight while one is multiplied
+    int64_t c0 = c_lo + wave * kStep;
+    if (c0 < c_hi) {
+      Step cur, nxt;
+      load(c0, cur);
+      for (; c0 < c_hi; c0 += kWaves * kStep) {
+        load(c0 + kWaves * kStep, nxt);
+        multiply(cur);
+        cur = nxt;
+      }
     }
+    __syncthreads();
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int t = 0; t < kNT; ++t) red[(wave * kNT + t) * 64 + lane] = acc[t];
+    __syncthreads();
+    // wave t finishes tile t
+    const int t = wave;
+    static_assert(kWaves == kNT, "a tile a wave");
+    if (owner[0] == a || kNT > 1) {
+      int mine = owner[0];
 #pragma unroll
-      for (int t = 0; t < RT; ++t)
-        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, s.x[u]),
-                                                         __builtin_bit_cast(bf16x8, s.a[u][t]),
-                                                         acc[t], 0, 0, 0);
-  };
-  // the next step's loads are in flight while one is multiplied
-  constexpr int64_t STRIDE = (int64_t)W * 32 * U;
-  int64_t c0 = (int64_t)wave * (32 * U);
-  if (c0 < C) {
-    Step cur, nxt;
-    load(c0, cur);
-    for (; c0 < C; c0 += STRIDE) {
-      if (c0 + STRIDE < C) load(c0 + STRIDE, nxt);
-      multiply(cur);
-      cur = nxt;
+      for (int i = 1; i < kNT; ++i) mine = t == i ? owner[i] : mine;
+      const int j = rb + r;
+      if (mine == a && j < R) {
+        f32x4 s = red[t * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) s += red[(w * kNT + t) * 64 + lane];
+        const int64_t pos = (int64_t)(t0 + t) * kLoraTile + 4 * g;
+        if (part) {
+          float *dst = part + (blockIdx.z * p.tiles * kLoraTile + pos) * R + j;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) dst[(int64_t)v * R] = s[v];
+        } else {
+          const i32x4 out = *reinterpret_cast<const i32x4 *>(plan + p.perm + pos);
+          const float al = alpha[a];
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            if (out[v] >= 0) h[(int64_t)out[v] * R + j] = al * s[v];
+        }
+      }
+    }
+    __syncthreads();  // the sums are read before the next adapter's steps
+  }
+  if (part) return;
+  // rows without an adapter
+#pragma unroll
+  for (int t = 0; t < kNT; ++t) {
+    if (owner[t] != -1 || rb != 0) continue;
+    const int32_t *perm = plan + p.perm + (int64_t)(t0 + t) * kLoraTile;
+    for (int i = threadIdx.x; i < kLoraTile * R; i += 64 * kWaves) {
+      const int m = perm[i / R];
+      if (m >= 0) h[(int64_t)m * R + i % R] = 0.0f;
     }
   }
-  __syncthreads();
-  f32x4 *red = reinterpret_cast<f32x4 *>(smem);
-#pragma unroll
-  for (int t = 0; t < RT; ++t) red[(wave * RT + t) * 64 + lane] = acc[t];
-  __syncthreads();
-  for (int t = wave; t < RT; t += W) {
-    f32x4 s = red[t * 64 + lane];
-#pragma unroll
-    for (int w = 1; w < W; ++w) s += red[(w * RT + t) * 64 + lane];
-    const int j = rb + 16 * t + r;
-    if (j >= R) continue;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int m = out[v];
-      if (m >= 0) h[(int64_t)m * R + j] = al * s[v];
-    }
+}
+
+// h of the rows at each sorted position from Z partial sums; a thread takes 4 ranks.
+__global__ __launch_bounds__(256) void k_lora_shrink_sum(const float *__restrict__ part, int Z,
+                                                         const float *__restrict__ alpha, int R,
+                                                         int64_t M, int64_t L,
+                                                         const int32_t *__restrict__ plan,
+                                                         float *__restrict__ h) {
+  const LoraPlanLayout p = lora_plan_layout(M, L);
+  const int q = R / 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, pos = i / q;
+  const int j = (int)(i - pos * q) * 4;
+  const int64_t n = p.tiles * kLoraTile;
+  if (pos >= n) return;
+  const int m = plan[p.perm + pos], a = plan[p.owner + pos / kLoraTile];
+  if (m < 0) return;
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  if (a >= 0) {
+    for (int z = 0; z < Z; ++z)
+      s += *reinterpret_cast<const f32x4 *>(part + (z * n + pos) * R + j);
+    s *= alpha[a];
   }
+  *reinterpret_cast<f32x4 *>(h + (int64_t)m * R + j) = s;
 }
 
 // ----------------------------------------------------------- weight gradients
@@ -502,34 +553,36 @@ __global__ __launch_bounds__(64 * W) void k_lora_wgrad(LoraWgradArgs p, int tile
     lora_wgrad<W, RT, true>(p, pl, a, (int64_t)(tile - tiles_b) * 128, j0, smem);
 }
 
-template <int W, int RT, bool KMAJOR>
-hipError_t go_shrink(const uint16_t *x, int64_t M, int64_t C, const uint16_t *A,
-                     const float *alpha, int64_t L, int64_t R, const int32_t *plan, float *h,
-                     hipStream_t st) {
-  constexpr int bytes = ShrinkLds<W, RT, KMAJOR>::BYTES;
-  if constexpr (bytes > 65536) {
-    (void)hipFuncSetAttribute((const void *)k_lora_shrink<W, RT, KMAJOR>,
-                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    (void)hipGetLastError();
-  }
-  hipLaunchKernelGGL((k_lora_shrink<W, RT, KMAJOR>), 
-                     dim3((unsigned)lora_plan_layout(M, L).tiles,
-                          (unsigned)((R + 16 * RT - 1) / (16 * RT))),
-                     dim3(64 * W), bytes, st, x, C, A, alpha, (int)R, M, L, plan, h);
-  return hipGetLastError();
+// Ranges of the contraction: enough workgroups for two a CU, none with less than
+// two steps a wave.
+int shrink_ranges(int64_t M, int64_t C, int64_t L, int64_t R) {
+  const int64_t blocks = (lora_plan_layout(M, L).tiles + kNT - 1) / kNT * ((R + 15) / 16);
+  const int64_t most = C / (2 * kWaves * kStep);
+  int64_t z = 512 / (blocks > 0 ? blocks : 1);
+  z = z > 32 ? 32 : z;
+  z = z > most ? most : z;
+  return z < 1 ? 1 : (int)z;
 }
 
 template <bool KMAJOR>
-hipError_t go_shrink_r(const uint16_t *x, int64_t M, int64_t C, const uint16_t *A,
-                       const float *alpha, int64_t L, int64_t R, const int32_t *plan, float *h,
-                       hipStream_t st) {
-  // One block of 16 ranks a workgroup: x is read once per block of ranks, from
-  // the caches, and the grid fills the chip (M = 500, K = 4096, R = 64: 21 us with
-  // all 64 ranks in each of 32 workgroups). Once there are more than four
-  // workgroups a CU, 64 ranks share a read of x.
-  if ((M / kLoraTile) * ((R + 15) / 16) > 1024)
-    return go_shrink<8, 4, KMAJOR>(x, M, C, A, alpha, L, R, plan, h, st);
-  return go_shrink<16, 1, KMAJOR>(x, M, C, A, alpha, L, R, plan, h, st);
+hipError_t go_shrink(const uint16_t *x, int64_t M, int64_t C, const uint16_t *A,
+                     const float *alpha, int64_t L, int64_t R, const int32_t *plan, float *h,
+                     float *part, hipStream_t st) {
+  const LoraPlanLayout p = lora_plan_layout(M, L);
+  int z = shrink_ranges(M, C, L, R);
+  const int64_t range = (C + (int64_t)z * kStep - 1) / ((int64_t)z * kStep) * kStep;
+  if (z > 1) z = (int)((C + range - 1) / range);
+  hipLaunchKernelGGL(k_lora_shrink<KMAJOR>,
+                     dim3((unsigned)((p.tiles + kNT - 1) / kNT), (unsigned)((R + 15) / 16),
+                          (unsigned)z),
+                     dim3(64 * kWaves), 0, st, x, C, A, alpha, (int)R, M, L, plan, h,
+                     z > 1 ? part : nullptr, range);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || z <= 1) return e;
+  const int64_t n = p.tiles * kLoraTile * (R / 4);
+  hipLaunchKernelGGL(k_lora_shrink_sum, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, part,
+                     z, alpha, (int)R, M, L, plan, h);
+  return hipGetLastError();
 }
 
 template <int W, int RT>
@@ -554,10 +607,15 @@ hipError_t launch_lora_plan(const int32_t *idx, int64_t M, int64_t L, int32_t *p
   return hipGetLastError();
 }
 
+size_t lora_shrink_bytes(int64_t M, int64_t C, int64_t L, int64_t R) {
+  const int z = shrink_ranges(M, C, L, R);
+  return z > 1 ? (size_t)z * (size_t)lora_plan_layout(M, L).tiles * kLoraTile * (size_t)R * 4 : 0;
+}
+
 hipError_t launch_lora_shrink(const uint16_t *x, int64_t M, int64_t K, const uint16_t *A,
                               const float *alpha, int64_t L, int64_t R, const int32_t *plan,
-                              float *h, hipStream_t st) {
-  if (M >= 64) return go_shrink_r<false>(x, M, K, A, alpha, L, R, plan, h, st);
+                              float *h, float *part, hipStream_t st) {
+  if (M >= kLoraTiledMinM) return go_shrink<false>(x, M, K, A, alpha, L, R, plan, h, part, st);
   const int32_t *idx = plan + lora_plan_layout(M, L).idx;
   if (M * R < 2048)
     hipLaunchKernelGGL(k_lora_shrink_rows<1>, dim3((unsigned)R, (unsigned)M), dim3(256), 0, st, x,
@@ -570,8 +628,8 @@ hipError_t launch_lora_shrink(const uint16_t *x, int64_t M, int64_t K, const uin
 
 hipError_t launch_lora_shrink_t(const uint16_t *dy, int64_t M, int64_t N, const uint16_t *B,
                                 const float *alpha, int64_t L, int64_t R, const int32_t *plan,
-                                float *u, hipStream_t st) {
-  return go_shrink_r<true>(dy, M, N, B, alpha, L, R, plan, u, st);
+                                float *u, float *part, hipStream_t st) {
+  return go_shrink<true>(dy, M, N, B, alpha, L, R, plan, u, part, st);
 }
 
 hipError_t launch_lora_wgrad(const LoraWgradArgs &a, hipStream_t st) {

@@ -378,15 +378,18 @@ int aql_lora_plan(const int32_t *idx, int64_t M, int64_t L, void *plan, size_t p
  * The linear with adapters. The products with the adapters are float32 sums of
  * exact products; y is rounded to bf16 once, with everything in the sum.
  *
- *   x, q, scale, bias, y, M, N, K, ws   as aql_linear_w8a16 (the workspace is
- *           optional and sized by AQL_OP_W8A16)
+ *   x, q, scale, bias, y, M, N, K   as aql_linear_w8a16
  *   A, B, alpha, L, R   the stacked adapters
  *   plan    from aql_lora_plan for this batch (M, L)
  *   h       device, [M, R] float32 (output; the backward pass takes it)
+ *   ws      device workspace of aql_lora_forward_bytes(M, N, K, L, R) bytes (may be
+ *           NULL where that is 0)
  * Errors: as aql_linear_w8a16, plus R not a multiple of 8 in
  * 8..AQL_LORA_MAX_RANK, L outside 1..AQL_LORA_MAX_ADAPTERS, NULL or misaligned
- * A, B, alpha, plan or h. N == 0 launches nothing and leaves h as it was.
+ * A, B, alpha, plan or h, workspace too small. N == 0 launches nothing and
+ * leaves h as it was.
  */
+size_t aql_lora_forward_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
 int aql_linear_w8a16_lora(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
                           const float *scale, const uint16_t *bias, int64_t N, const uint16_t *A,
                           const uint16_t *B, const float *alpha, int64_t L, int64_t R,
@@ -423,12 +426,12 @@ int aql_linear_w8a16_dgrad(const uint16_t *dy, int64_t M, int64_t N, const int8_
  *   dx      device, [M, K] bf16 (output; may be NULL: not computed)
  *   dA, dB  device, [L, R, K] and [L, N, R] float32 (outputs; either may be
  *           NULL: not computed. xq and xs may be NULL without dA)
- *   ws      device workspace of aql_lora_backward_bytes(M, N, K, R) bytes
+ *   ws      device workspace of aql_lora_backward_bytes(M, N, K, L, R) bytes
  * Errors: as aql_linear_w8a16_dgrad and aql_linear_w8a16_lora;
  * AQL_ERR_WORKSPACE. M == 0 or N == 0 write what is left of the outputs
  * (zeros, unless they accumulate).
  */
-size_t aql_lora_backward_bytes(int64_t M, int64_t N, int64_t K, int64_t R);
+size_t aql_lora_backward_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
 int aql_linear_w8a16_lora_backward(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q,
                                    const float *scale, int64_t K, const uint16_t *A,
                                    const uint16_t *B, const float *alpha, int64_t L, int64_t R,

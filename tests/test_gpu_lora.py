@@ -517,7 +517,7 @@ def test_graph_replays_with_a_new_batch(M):
               h=torch.empty(M, R, device=DEV))
     out = dict(dx=torch.empty(M, 512, dtype=torch.bfloat16, device=DEV),
                dA=torch.empty(L, R, 512, device=DEV), dB=torch.empty(L, 264, R, device=DEV),
-               workspace=torch.empty(aql.aql_lora_backward_bytes(M, 264, 512, R), dtype=torch.uint8,
+               workspace=torch.empty(aql.aql_lora_backward_bytes(M, 264, 512, L, R), dtype=torch.uint8,
                                      device=DEV))
     xq, xs = aql.aql_act_checkpoint(d["x"])
 

@@ -62,6 +62,19 @@ def test_forward_refusals(kw, code):
     assert call(L.aql_linear_w8a16_lora, FWD, **kw) == code
 
 
+def test_forward_workspace():
+    wb = aql.aql_lora_forward_bytes
+    assert wb(1, 4096, 4096, 2, 16) == 0                      # one row: nothing to split
+    need = wb(100, 72, 8192, 3, 16)
+    assert need >= aql.aql_workspace_bytes(aql.AQL_OP_W8A16, 100, 72, 8192) > 0
+    big = dict(M=100, N=72, K=8192, R=16)
+    assert call(L.aql_linear_w8a16_lora, FWD, **big) == WS
+    assert call(L.aql_linear_w8a16_lora, FWD, ws=P, ws_bytes=need - 1, **big) == WS
+    for bad in ((0, 72, 64, 3, 16), (5, -1, 64, 3, 16), (5, 72, 8, 3, 16), (5, 72, 64, 0, 16),
+                (5, 72, 64, 3, 12)):
+        assert wb(*bad) == 0
+
+
 def test_forward_empty():
     none = {k: None for k in ("x", "y", "h")}
     assert call(L.aql_linear_w8a16_lora, FWD, M=0, **none) == OK
@@ -107,8 +120,8 @@ def test_backward_refusals(kw, code):
 
 def test_backward_nothing_asked_for():
     assert call(L.aql_linear_w8a16_lora_backward, BWD, dx=None, dA=None, dB=None) == OK
-    assert aql.aql_lora_backward_bytes(0, 24, 64, 8) == 0
-    assert aql.aql_lora_backward_bytes(5, 24, 64, 8) >= 5 * 8 * 4 + 5 * 64 * 2
+    assert aql.aql_lora_backward_bytes(0, 24, 64, 3, 8) == 0
+    assert aql.aql_lora_backward_bytes(5, 24, 64, 3, 8) >= 5 * 8 * 4 + 5 * 64 * 2
 
 
 CK = dict(x=P, dtype=0, M=5, K=64, xq=P, xs=P, stream=None)
