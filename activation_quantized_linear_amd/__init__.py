@@ -542,15 +542,64 @@ def aql_linear_w8a16_grouped(host_table, dev_table):
 # -------------------------------------------------------- low-rank adapters
 
 
-def _call(name, dev, *args):
-    """The C entry on the current stream of dev, with dev the current device."""
-    fn = getattr(_lib, name)
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, _stream(dev))
+# The calls below are made for every linear of a decode step, where the checks
+# cost as much as the kernels: each tensor is checked by one expression, and only
+# what fails it goes through the full checks for the error's text.
+
+
+def _dev_index(t, name, dtype, ndim):
+    """Device index of the tensor that the others have to be on."""
+    try:
+        if t.dtype is dtype and t.ndim == ndim and t.is_contiguous():
+            di = t.get_device()
+            if di >= 0:
+                return di
+    except AttributeError:
+        pass
+    _need(t, name, dtype, ndim)
+    return t.get_device()
+
+
+def _fit(t, name, dtype, shape, di):
+    """t's address, t being a contiguous tensor of this type and shape on device di."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == di and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, dtype, len(shape), torch.device("cuda", di))
+    _shape(t, name, shape)
+    return t.data_ptr()
+
+
+def _new(t, name, shape, dtype, dev):
+    """An output: t, or a new tensor."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _fit(t, name, dtype, shape, dev.index)
+    return t
+
+
+def _call(name, fn, di, *args):
+    """The C entry on the current stream of device di, with it the current device."""
+    if di == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(di))
     else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, _stream(dev))
-    _check(name, rc)
+        with torch.cuda.device(di):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(di))
+    if rc != AQL_OK:
+        _check(name, rc)
+
+
+def _scratch(workspace, nbytes, dev):
+    """(address, bytes, owner) of a workspace: the one given, or a new one where one is needed."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0, None
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return ws.data_ptr(), nbytes, ws
+    _need(workspace, "workspace", torch.uint8, device=dev)
+    return workspace.data_ptr(), workspace.numel(), workspace
 
 
 class LoraPlan:
@@ -572,36 +621,29 @@ def aql_lora_plan(idx, L, plan=None):
     """idx int32 [M]: each row's adapter in [0, L), any other value: none -> LoraPlan.
     plan: a LoraPlan of the same M and L on idx's device to write again (its
     buffer keeps its address, so a captured graph sees the new batch)."""
-    _need(idx, "idx", torch.int32, 1)
+    di = _dev_index(idx, "idx", torch.int32, 1)
     M, L = idx.shape[0], int(L)
     nbytes = aql_lora_plan_bytes(M, L)
     if plan is None:
         plan = LoraPlan(M, L, torch.empty(max(nbytes, 16), dtype=torch.uint8, device=idx.device))
-    else:
-        _lora_plan(plan, M, L, idx.device)
-    _call("aql_lora_plan", idx.device, _ptr(idx), M, L, _ptr(plan.buffer), plan.buffer.numel())
+    buf = _lora_plan(plan, M, L, di)
+    _call("aql_lora_plan", _lib.aql_lora_plan, di, idx.data_ptr(), M, L, buf,
+          plan.buffer.numel())
     return plan
 
 
-def _lora_plan(plan, M, L, dev):
+def _lora_plan(plan, M, L, di):
     if not isinstance(plan, LoraPlan):
         raise TypeError("plan must be a LoraPlan (aql_lora_plan)")
-    if (plan.M, plan.L) != (M, L):
+    if plan.M != M or plan.L != L:
         raise ValueError(f"plan is for M={plan.M}, L={plan.L}; the call has M={M}, L={L}")
-    _need(plan.buffer, "plan.buffer", torch.uint8, 1, dev)
-    if plan.buffer.numel() < aql_lora_plan_bytes(M, L):
-        raise ValueError("plan.buffer is too small")
+    return _fit(plan.buffer, "plan.buffer", torch.uint8, plan.buffer.shape, di)
 
 
-def _lora_args(A, B, alpha, N, K, dev):
-    _need(A, "A", torch.bfloat16, 3, dev)
-    L, R = A.shape[0], A.shape[1]
-    _shape(A, "A", (L, R, K))
-    _need(B, "B", torch.bfloat16, 3, dev)
-    _shape(B, "B", (L, N, R))
-    _need(alpha, "alpha", torch.float32, 1, dev)
-    _shape(alpha, "alpha", (L,))
-    return L, R
+def _lora_shape(A):
+    if not isinstance(A, torch.Tensor) or A.ndim != 3:
+        raise ValueError("A must be a [L, R, K] tensor")
+    return A.shape[0], A.shape[1]
 
 
 def aql_lora_forward_bytes(M, N, K, L, R):
@@ -615,44 +657,40 @@ def aql_linear_w8a16_lora(x, q, scale, A, B, alpha, plan, bias=None, y=None, h=N
     plan of aql_lora_plan, bias bfloat16 [N] -> (y bfloat16 [M, N], h float32 [M, R]),
     h = alpha A x, which the backward pass takes. workspace: uint8 device tensor of
     aql_lora_forward_bytes; allocated here when one is needed and none is given."""
-    _need(x, "x", torch.bfloat16, 2)
-    dev = x.device
+    di = _dev_index(x, "x", torch.bfloat16, 2)
     M, K = x.shape
-    _need(q, "q", torch.int8, 2, dev)
     N = q.shape[0]
-    _shape(q, "q", (N, K))
-    _need(scale, "scale", torch.float32, 1, dev)
-    _shape(scale, "scale", (N,))
-    L, R = _lora_args(A, B, alpha, N, K, dev)
-    _lora_plan(plan, M, L, dev)
-    if bias is not None:
-        _need(bias, "bias", torch.bfloat16, 1, dev)
-        _shape(bias, "bias", (N,))
-    y = _out(y, "y", (M, N), torch.bfloat16, dev)
-    h = _out(h, "h", (M, R), torch.float32, dev)
-    nbytes = aql_lora_forward_bytes(M, N, K, L, R)
-    ws = _workspace(workspace, nbytes, dev) if workspace is not None or nbytes > 0 else None
-    _call("aql_linear_w8a16_lora", dev, _ptr(x), M, K, _ptr(q), _ptr(scale), _ptr(bias), N,
-          _ptr(A), _ptr(B), _ptr(alpha), L, R, _ptr(plan.buffer), _ptr(y), _ptr(h), _ptr(ws), 0
-          if ws is None else ws.numel())
+    L, R = _lora_shape(A)
+    args = (x.data_ptr(), M, K, _fit(q, "q", torch.int8, (N, K), di),
+            _fit(scale, "scale", torch.float32, (N,), di),
+            None if bias is None else _fit(bias, "bias", torch.bfloat16, (N,), di), N,
+            _fit(A, "A", torch.bfloat16, (L, R, K), di),
+            _fit(B, "B", torch.bfloat16, (L, N, R), di),
+            _fit(alpha, "alpha", torch.float32, (L,), di), L, R, _lora_plan(plan, M, L, di))
+    dev = x.device
+    y = _new(y, "y", (M, N), torch.bfloat16, dev)
+    h = _new(h, "h", (M, R), torch.float32, dev)
+    ws, ws_bytes, _owner = _scratch(workspace, _lib.aql_lora_forward_bytes(M, N, K, L, R), dev)
+    _call("aql_linear_w8a16_lora", _lib.aql_linear_w8a16_lora, di, *args, y.data_ptr(),
+          h.data_ptr(), ws, ws_bytes)
     return y, h
 
 
 def aql_linear_w8a16_dgrad(dy, q, scale, dx=None, workspace=None):
     """Gradient of aql_linear_w8a16 to x: dy bfloat16 [M, N], q int8 [N, K], scale
-    float32 [N] -> dx bfloat16 [M, K] = (dy * scale) @ q."""
-    _need(dy, "dy", torch.bfloat16, 2)
-    dev = dy.device
+    float32 [N] -> dx bfloat16 [M, K] = (dy * scale) @ q. workspace: uint8 device tensor
+    of aql_workspace_bytes(AQL_OP_W8A16_DGRAD, M, N, K); allocated here when none is given."""
+    di = _dev_index(dy, "dy", torch.bfloat16, 2)
     M, N = dy.shape
-    _need(q, "q", torch.int8, 2, dev)
-    K = q.shape[1]
-    _shape(q, "q", (N, K))
-    _need(scale, "scale", torch.float32, 1, dev)
-    _shape(scale, "scale", (N,))
-    dx = _out(dx, "dx", (M, K), torch.bfloat16, dev)
-    ws = _workspace(workspace, aql_workspace_bytes(AQL_OP_W8A16_DGRAD, M, N, K), dev)
-    _call("aql_linear_w8a16_dgrad", dev, _ptr(dy), M, N, _ptr(q), _ptr(scale), K, _ptr(dx),
-          _ptr(ws), ws.numel())
+    K = q.shape[-1]
+    args = (dy.data_ptr(), M, N, _fit(q, "q", torch.int8, (N, K), di),
+            _fit(scale, "scale", torch.float32, (N,), di), K)
+    dev = dy.device
+    dx = _new(dx, "dx", (M, K), torch.bfloat16, dev)
+    ws, ws_bytes, _owner = _scratch(workspace,
+                                    _lib.aql_workspace_bytes(AQL_OP_W8A16_DGRAD, M, N, K), dev)
+    _call("aql_linear_w8a16_dgrad", _lib.aql_linear_w8a16_dgrad, di, *args, dx.data_ptr(), ws,
+          ws_bytes)
     return dx
 
 
@@ -666,34 +704,31 @@ def aql_linear_w8a16_lora_backward(dy, q, scale, A, B, alpha, plan, h, xq, xs, d
     forward pass; xq int8 [M, K], xs float32 [M, ceil(K / 128)]: the checkpoint of x
     (aql_act_checkpoint) -> (dx bfloat16 [M, K] or None, dA float32 [L, R, K],
     dB float32 [L, N, R]). accumulate=True adds to the given dA and dB.
-    need_dx=False leaves dx out."""
-    _need(dy, "dy", torch.bfloat16, 2)
-    dev = dy.device
+    need_dx=False leaves dx out. workspace: uint8 device tensor of
+    aql_lora_backward_bytes; allocated here when none is given."""
+    di = _dev_index(dy, "dy", torch.bfloat16, 2)
     M, N = dy.shape
-    _need(q, "q", torch.int8, 2, dev)
-    K = q.shape[1]
-    _shape(q, "q", (N, K))
-    _need(scale, "scale", torch.float32, 1, dev)
-    _shape(scale, "scale", (N,))
-    L, R = _lora_args(A, B, alpha, N, K, dev)
-    _lora_plan(plan, M, L, dev)
-    _need(h, "h", torch.float32, 2, dev)
-    _shape(h, "h", (M, R))
-    _need(xq, "xq", torch.int8, 2, dev)
-    _shape(xq, "xq", (M, K))
-    _need(xs, "xs", torch.float32, 2, dev)
-    _shape(xs, "xs", (M, (K + AQL_CKPT_GROUP - 1) // AQL_CKPT_GROUP))
+    K = q.shape[-1]
+    L, R = _lora_shape(A)
+    G = (K + AQL_CKPT_GROUP - 1) // AQL_CKPT_GROUP
+    args = (dy.data_ptr(), M, N, _fit(q, "q", torch.int8, (N, K), di),
+            _fit(scale, "scale", torch.float32, (N,), di), K,
+            _fit(A, "A", torch.bfloat16, (L, R, K), di),
+            _fit(B, "B", torch.bfloat16, (L, N, R), di),
+            _fit(alpha, "alpha", torch.float32, (L,), di), L, R, _lora_plan(plan, M, L, di),
+            _fit(h, "h", torch.float32, (M, R), di), _fit(xq, "xq", torch.int8, (M, K), di),
+            _fit(xs, "xs", torch.float32, (M, G), di), 1 if accumulate else 0)
     if accumulate and (dA is None or dB is None):
         raise ValueError("accumulate needs the dA and dB to add to")
     if dx is not None and not need_dx:
         raise ValueError("dx is given but need_dx is False")
-    dx = _out(dx, "dx", (M, K), torch.bfloat16, dev) if need_dx else None
-    dA = _out(dA, "dA", (L, R, K), torch.float32, dev)
-    dB = _out(dB, "dB", (L, N, R), torch.float32, dev)
-    ws = _workspace(workspace, aql_lora_backward_bytes(M, N, K, L, R), dev)
-    _call("aql_linear_w8a16_lora_backward", dev, _ptr(dy), M, N, _ptr(q), _ptr(scale), K,
-          _ptr(A), _ptr(B), _ptr(alpha), L, R, _ptr(plan.buffer), _ptr(h), _ptr(xq), _ptr(xs),
-          int(bool(accumulate)), _ptr(dx), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel())
+    dev = dy.device
+    dx = _new(dx, "dx", (M, K), torch.bfloat16, dev) if need_dx else None
+    dA = _new(dA, "dA", (L, R, K), torch.float32, dev)
+    dB = _new(dB, "dB", (L, N, R), torch.float32, dev)
+    ws, ws_bytes, _owner = _scratch(workspace, _lib.aql_lora_backward_bytes(M, N, K, L, R), dev)
+    _call("aql_linear_w8a16_lora_backward", _lib.aql_linear_w8a16_lora_backward, di, *args,
+          dx.data_ptr() if need_dx else None, dA.data_ptr(), dB.data_ptr(), ws, ws_bytes)
     return dx, dA, dB
 
 
@@ -710,23 +745,22 @@ def aql_act_checkpoint(x, xq=None, xs=None):
     """x float32 or bfloat16 [M, K] -> (xq int8 [M, K], xs float32 [M, ceil(K / 128)]):
     8-bit codes with one scale per 128 values of a row."""
     dt = _act_dtype(x.dtype, "x")
-    _need(x, "x", x.dtype, 2)
+    di = _dev_index(x, "x", x.dtype, 2)
     M, K = x.shape
     dev = x.device
-    xq = _out(xq, "xq", (M, K), torch.int8, dev)
-    xs = _out(xs, "xs", (M, (K + AQL_CKPT_GROUP - 1) // AQL_CKPT_GROUP), torch.float32, dev)
-    _call("aql_act_checkpoint", dev, _ptr(x), dt, M, K, _ptr(xq), _ptr(xs))
+    xq = _new(xq, "xq", (M, K), torch.int8, dev)
+    xs = _new(xs, "xs", (M, (K + AQL_CKPT_GROUP - 1) // AQL_CKPT_GROUP), torch.float32, dev)
+    _call("aql_act_checkpoint", _lib.aql_act_checkpoint, di, x.data_ptr(), dt, M, K,
+          xq.data_ptr(), xs.data_ptr())
     return xq, xs
 
 
 def aql_act_restore(xq, xs, dtype=torch.bfloat16, x=None):
     """xq int8 [M, K], xs float32 [M, ceil(K / 128)] -> x [M, K] of dtype: code * scale."""
     dt = _act_dtype(dtype, "dtype")
-    _need(xq, "xq", torch.int8, 2)
+    di = _dev_index(xq, "xq", torch.int8, 2)
     M, K = xq.shape
-    dev = xq.device
-    _need(xs, "xs", torch.float32, 2, dev)
-    _shape(xs, "xs", (M, (K + AQL_CKPT_GROUP - 1) // AQL_CKPT_GROUP))
-    x = _out(x, "x", (M, K), dtype, dev)
-    _call("aql_act_restore", dev, _ptr(xq), _ptr(xs), M, K, _ptr(x), dt)
+    sp = _fit(xs, "xs", torch.float32, (M, (K + AQL_CKPT_GROUP - 1) // AQL_CKPT_GROUP), di)
+    x = _new(x, "x", (M, K), dtype, xq.device)
+    _call("aql_act_restore", _lib.aql_act_restore, di, xq.data_ptr(), sp, M, K, x.data_ptr(), dt)
     return x

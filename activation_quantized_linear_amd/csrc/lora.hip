@@ -184,13 +184,16 @@ __global__ __launch_bounds__(256) void k_lora_shrink_rows(
 
 // ------------------------------------------------------- shrink, tiled form
 
-// A workgroup of 4 waves takes kNT tiles of the plan (64 rows, mostly of one
+// A workgroup of W waves takes NT tiles of the plan (16 rows each, mostly of one
 // adapter), 16 ranks and one of gridDim.z ranges of the contraction; its waves
-// take steps of 64 in turn and meet in LDS. A CU draws little more than its 1/256
-// of the memory's rate, so what each workgroup reads decides: 64 rows share a
-// read of the 16 ranks (with one tile of 16 rows the adapter's bytes equal the
-// rows'), and the ranges spread few rows over the chip. Several ranges leave
-// float32 partial sums in sorted order, which k_lora_shrink_sum adds in order.
+// take steps of 128 in turn and meet in LDS. What it costs is round trips to
+// memory (about 1.3 us each with the data in HBM), so all loads of a step are out
+// at once, and a CU draws little more than its 1/256 of the memory's rate, so
+// what each workgroup reads counts. Two forms:
+//  * NT = 4, W = 4, ranges of about one step a wave: 64 rows share a read of the
+//    16 ranks (with 16 rows the adapter's bytes equal the rows'), and float32
+//    partial sums in sorted order are added in order by k_lora_shrink_sum;
+//  * NT = 1, W = 16 over the whole of a short contraction: one launch.
 // Operands go from memory to the MFMA registers as they lie: x and A have the
 // contraction contiguous. KMAJOR: the adapter matrix is [C, R] (dy onto B); each
 // wave then passes its step's 32 x 16 blocks through its own LDS slot and reads
@@ -198,25 +201,25 @@ __global__ __launch_bounds__(256) void k_lora_shrink_rows(
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-constexpr int kNT = 4, kWaves = 4, kU = 2;
-constexpr int kStep = 32 * kU;  // of the contraction, per wave and step
+constexpr int kU = 4;           // matrix instructions of a step
+constexpr int kStep = 32 * kU;  // of the contraction, per wave
 
-template <bool KMAJOR>
-__global__ __launch_bounds__(64 * kWaves, 2) void k_lora_shrink(
+template <int NT, int W, bool KMAJOR>
+__global__ __launch_bounds__(64 * W) void k_lora_shrink(
     const uint16_t *__restrict__ x, int64_t C, const uint16_t *__restrict__ A,
     const float *__restrict__ alpha, int R, int64_t M, int64_t L,
     const int32_t *__restrict__ plan, float *__restrict__ h, float *__restrict__ part,
     int64_t range) {
-  __shared__ __attribute__((aligned(16))) char smem[kWaves * kNT * 64 * 16];
-  static_assert(kU * 1024 <= kNT * 64 * 16, "a wave's slot holds its step");
+  constexpr int SLOT = (KMAJOR && kU * 1024 > NT * 1024) ? kU * 1024 : NT * 1024;  // a wave's
+  __shared__ __attribute__((aligned(16))) char smem[W * SLOT];
   const LoraPlanLayout p = lora_plan_layout(M, L);
-  const int t0 = blockIdx.x * kNT, rb = blockIdx.y * 16;  // first tile, first rank
+  const int t0 = blockIdx.x * NT, rb = blockIdx.y * 16;  // first tile, first rank
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t c_lo = blockIdx.z * range, c_hi = c_lo + range < C ? c_lo + range : C;
-  int owner[kNT], row[kNT];
+  int owner[NT], row[NT];
 #pragma unroll
-  for (int t = 0; t < kNT; ++t) {
+  for (int t = 0; t < NT; ++t) {
     const bool in = t0 + t < p.tiles;
     owner[t] = in ? plan[p.owner + t0 + t] : -2;
     // a padding position computes the tile's first row again; its results are dropped
@@ -224,29 +227,30 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_lora_shrink(
     row[t] = perm[r] >= 0 ? perm[r] : perm[0];
   }
   const i32x4 zero = {0, 0, 0, 0};
-  char *stage = smem + wave * (kNT * 64 * 16);
+  char *stage = smem + wave * SLOT;
   f32x4 *red = reinterpret_cast<f32x4 *>(smem);
   int done = -1;
   for (;;) {
     // the tiles' adapters in ascending order (-1 and -2: nothing to compute)
     int a = 0x7fffffff;
 #pragma unroll
-    for (int t = 0; t < kNT; ++t) a = owner[t] > done && owner[t] < a ? owner[t] : a;
+    for (int t = 0; t < NT; ++t) a = owner[t] > done && owner[t] < a ? owner[t] : a;
     if (a == 0x7fffffff) break;
     done = a;
     int any = 0;
 #pragma unroll
-    for (int t = kNT - 1; t >= 0; --t) any = owner[t] == a ? row[t] : any;
-    const uint16_t *xr[kNT];
+    for (int t = NT - 1; t >= 0; --t) any = owner[t] == a ? row[t] : any;
+    const uint16_t *xr[NT];
 #pragma unroll
-    for (int t = 0; t < kNT; ++t)  // another adapter's tile reads one of this one's again
+    for (int t = 0; t < NT; ++t)  // another adapter's tile reads one of this one's again
       xr[t] = x + (int64_t)(owner[t] == a ? row[t] : any) * C;
     const uint16_t *ab = A + (int64_t)a * R * C;
-    f32x4 acc[kNT];
+    const float al = alpha[a];
+    f32x4 acc[NT];
 #pragma unroll
-    for (int t = 0; t < kNT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
     struct Step {
-      i32x4 x[kU][kNT], a[kU];
+      i32x4 x[kU][NT], a[kU];
     };
     auto load = [&](int64_t c0, Step &s) {
 #pragma unroll
@@ -262,7 +266,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_lora_shrink(
           s.a[u] = cr < c_hi && j < R ? *reinterpret_cast<const i32x4 *>(ab + cr * R + j) : zero;
         }
 #pragma unroll
-        for (int t = 0; t < kNT; ++t)
+        for (int t = 0; t < NT; ++t)
           s.x[u][t] = c < c_hi ? *reinterpret_cast<const i32x4 *>(xr[t] + c) : zero;
       }
     };
@@ -289,38 +293,30 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_lora_shrink(
 #pragma unroll
       for (int u = 0; u < kU; ++u)
 #pragma unroll
-        for (int t = 0; t < kNT; ++t)
+        for (int t = 0; t < NT; ++t)
           acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, s.x[u][t]),
                                                            __builtin_bit_cast(bf16x8, s.a[u]),
                                                            acc[t], 0, 0, 0);
     };
-    // the next step's loads are in flight while one is multiplied
-    int64_t c0 = c_lo + wave * kStep;
-    if (c0 < c_hi) {
-      Step cur, nxt;
-      load(c0, cur);
-      for (; c0 < c_hi; c0 += kWaves * kStep) {
-        load(c0 + kWaves * kStep, nxt);
-        multiply(cur);
-        cur = nxt;
-      }
+    for (int64_t c0 = c_lo + wave * kStep; c0 < c_hi; c0 += W * kStep) {
+      Step s;
+      load(c0, s);
+      multiply(s);
     }
-    __syncthreads();
+    __syncthreads();  // the waves' slots become the sums'
 #pragma unroll
-    for (int t = 0; t < kNT; ++t) red[(wave * kNT + t) * 64 + lane] = acc[t];
+    for (int t = 0; t < NT; ++t) red[(wave * NT + t) * 64 + lane] = acc[t];
     __syncthreads();
-    // wave t finishes tile t
-    const int t = wave;
-    static_assert(kWaves == kNT, "a tile a wave");
-    if (owner[0] == a || kNT > 1) {
+    if (wave < NT) {  // wave t finishes tile t
+      const int t = wave;
       int mine = owner[0];
 #pragma unroll
-      for (int i = 1; i < kNT; ++i) mine = t == i ? owner[i] : mine;
+      for (int i = 1; i < NT; ++i) mine = t == i ? owner[i] : mine;
       const int j = rb + r;
       if (mine == a && j < R) {
         f32x4 s = red[t * 64 + lane];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) s += red[(w * kNT + t) * 64 + lane];
+        for (int w = 1; w < W; ++w) s += red[(w * NT + t) * 64 + lane];
         const int64_t pos = (int64_t)(t0 + t) * kLoraTile + 4 * g;
         if (part) {
           float *dst = part + (blockIdx.z * p.tiles * kLoraTile + pos) * R + j;
@@ -328,7 +324,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_lora_shrink(
           for (int v = 0; v < 4; ++v) dst[(int64_t)v * R] = s[v];
         } else {
           const i32x4 out = *reinterpret_cast<const i32x4 *>(plan + p.perm + pos);
-          const float al = alpha[a];
 #pragma unroll
           for (int v = 0; v < 4; ++v)
             if (out[v] >= 0) h[(int64_t)out[v] * R + j] = al * s[v];
@@ -340,10 +335,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_lora_shrink(
   if (part) return;
   // rows without an adapter
 #pragma unroll
-  for (int t = 0; t < kNT; ++t) {
+  for (int t = 0; t < NT; ++t) {
     if (owner[t] != -1 || rb != 0) continue;
     const int32_t *perm = plan + p.perm + (int64_t)(t0 + t) * kLoraTile;
-    for (int i = threadIdx.x; i < kLoraTile * R; i += 64 * kWaves) {
+    for (int i = threadIdx.x; i < kLoraTile * R; i += 64 * W) {
       const int m = perm[i / R];
       if (m >= 0) h[(int64_t)m * R + i % R] = 0.0f;
     }
@@ -362,14 +357,22 @@ __global__ __launch_bounds__(256) void k_lora_shrink_sum(const float *__restrict
   const int j = (int)(i - pos * q) * 4;
   const int64_t n = p.tiles * kLoraTile;
   if (pos >= n) return;
+  // the sums, the row and its adapter at once (what lies at positions without a
+  // row was never written and is not used)
   const int m = plan[p.perm + pos], a = plan[p.owner + pos / kLoraTile];
-  if (m < 0) return;
   f32x4 s = {0.f, 0.f, 0.f, 0.f};
-  if (a >= 0) {
-    for (int z = 0; z < Z; ++z)
-      s += *reinterpret_cast<const f32x4 *>(part + (z * n + pos) * R + j);
-    s *= alpha[a];
+  int z = 0;
+  for (; z + 4 <= Z; z += 4) {
+    f32x4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = *reinterpret_cast<const f32x4 *>(part + ((z + i) * n + pos) * R + j);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s += v[i];
   }
+  for (; z < Z; ++z) s += *reinterpret_cast<const f32x4 *>(part + (z * n + pos) * R + j);
+  if (m < 0) return;
+  s = a >= 0 ? s * alpha[a] : f32x4{0.f, 0.f, 0.f, 0.f};
   *reinterpret_cast<f32x4 *>(h + (int64_t)m * R + j) = s;
 }
 
@@ -553,13 +556,19 @@ __global__ __launch_bounds__(64 * W) void k_lora_wgrad(LoraWgradArgs p, int tile
     lora_wgrad<W, RT, true>(p, pl, a, (int64_t)(tile - tiles_b) * 128, j0, smem);
 }
 
-// Ranges of the contraction: enough workgroups for two a CU, none with less than
-// two steps a wave.
+// One launch (NT = 1) for a contraction of at most two steps a wave on a grid of
+// at most one workgroup a CU (M = 500, K = 4096, R = 64: 9.9 us, 13.7 in ranges with
+// their second launch); else ranges of one step a wave while that keeps the grid
+// within two workgroups a CU (M = 2048, N = 14336, R = 16: 20.7 us, 26.6 whole).
+bool shrink_whole(int64_t M, int64_t C, int64_t L, int64_t R) {
+  return C <= 2 * 16 * kStep && lora_plan_layout(M, L).tiles * ((R + 15) / 16) <= 256;
+}
+
 int shrink_ranges(int64_t M, int64_t C, int64_t L, int64_t R) {
-  const int64_t blocks = (lora_plan_layout(M, L).tiles + kNT - 1) / kNT * ((R + 15) / 16);
-  const int64_t most = C / (2 * kWaves * kStep);
-  int64_t z = 512 / (blocks > 0 ? blocks : 1);
-  z = z > 32 ? 32 : z;
+  if (shrink_whole(M, C, L, R)) return 1;
+  const int64_t blocks = (lora_plan_layout(M, L).tiles + 3) / 4 * ((R + 15) / 16);
+  const int64_t most = (C + 4 * kStep - 1) / (4 * kStep);
+  int64_t z = 512 / blocks;
   z = z > most ? most : z;
   return z < 1 ? 1 : (int)z;
 }
@@ -569,14 +578,18 @@ hipError_t go_shrink(const uint16_t *x, int64_t M, int64_t C, const uint16_t *A,
                      const float *alpha, int64_t L, int64_t R, const int32_t *plan, float *h,
                      float *part, hipStream_t st) {
   const LoraPlanLayout p = lora_plan_layout(M, L);
+  const unsigned rb = (unsigned)((R + 15) / 16);
+  if (shrink_whole(M, C, L, R)) {
+    hipLaunchKernelGGL((k_lora_shrink<1, 16, KMAJOR>), dim3((unsigned)p.tiles, rb), dim3(1024), 0,
+                       st, x, C, A, alpha, (int)R, M, L, plan, h, (float *)nullptr, C);
+    return hipGetLastError();
+  }
   int z = shrink_ranges(M, C, L, R);
   const int64_t range = (C + (int64_t)z * kStep - 1) / ((int64_t)z * kStep) * kStep;
   if (z > 1) z = (int)((C + range - 1) / range);
-  hipLaunchKernelGGL(k_lora_shrink<KMAJOR>,
-                     dim3((unsigned)((p.tiles + kNT - 1) / kNT), (unsigned)((R + 15) / 16),
-                          (unsigned)z),
-                     dim3(64 * kWaves), 0, st, x, C, A, alpha, (int)R, M, L, plan, h,
-                     z > 1 ? part : nullptr, range);
+  hipLaunchKernelGGL((k_lora_shrink<4, 4, KMAJOR>),
+                     dim3((unsigned)((p.tiles + 3) / 4), rb, (unsigned)z), dim3(256), 0, st, x, C,
+                     A, alpha, (int)R, M, L, plan, h, z > 1 ? part : nullptr, range);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || z <= 1) return e;
   const int64_t n = p.tiles * kLoraTile * (R / 4);
@@ -588,10 +601,12 @@ hipError_t go_shrink(const uint16_t *x, int64_t M, int64_t C, const uint16_t *A,
 template <int W, int RT>
 hipError_t go_wgrad(const LoraWgradArgs &a, hipStream_t st) {
   constexpr int bytes = W / 2 * RT * 8 * 64 * 16;
-  if constexpr (bytes > 65536) {
+  static bool attr_set = false;
+  if (bytes > 65536 && !attr_set) {
     (void)hipFuncSetAttribute((const void *)k_lora_wgrad<W, RT>,
                               hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     (void)hipGetLastError();
+    attr_set = true;
   }
   const int tb = a.dB ? (int)((a.N + 63) / 64) : 0, ta = a.dA ? (int)((a.K + 127) / 128) : 0;
   const dim3 grid((unsigned)(tb + ta), (unsigned)a.L, (unsigned)((a.R + 16 * RT - 1) / (16 * RT)));

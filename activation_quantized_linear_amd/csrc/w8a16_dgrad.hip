@@ -471,9 +471,13 @@ struct Call {
 template <int TI, int SG, class LT>
 hipError_t go(const Call &c, const LT &lt) {
   using L = DgradLds<TI, SG>;
-  (void)hipFuncSetAttribute((const void *)k_w8a16_dgrad<TI, SG, false, LT>,
-                            hipFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
-  (void)hipGetLastError();
+  static bool attr_set = false;
+  if (!attr_set) {  // more than 64 KB of dynamic LDS; a launch the limit refuses reports itself
+    (void)hipFuncSetAttribute((const void *)k_w8a16_dgrad<TI, SG, false, LT>,
+                              hipFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+    (void)hipGetLastError();
+    attr_set = true;
+  }
   const int tm = (int)((c.M + L::BM - 1) / L::BM), tk = (int)((c.K + L::BK - 1) / L::BK);
   hipLaunchKernelGGL((k_w8a16_dgrad<TI, SG, false, LT>), dim3((unsigned)(tm * tk)), dim3(64 * NWV),
                      L::BYTES, c.st, c.d, c.ex, c.q, c.dx, c.M, c.N, c.NP, c.K, tm, tk,
@@ -484,9 +488,13 @@ hipError_t go(const Call &c, const LT &lt) {
 template <int TI, int SG, class LT>
 hipError_t go_split(const Call &c, int S, const LT &lt) {
   using L = DgradLds<TI, SG>;
-  (void)hipFuncSetAttribute((const void *)k_w8a16_dgrad<TI, SG, true, NoLora>,
-                            hipFuncAttributeMaxDynamicSharedMemorySize, L::BYTES_SPLIT);
-  (void)hipGetLastError();
+  static bool attr_set = false;
+  if (!attr_set) {
+    (void)hipFuncSetAttribute((const void *)k_w8a16_dgrad<TI, SG, true, NoLora>,
+                              hipFuncAttributeMaxDynamicSharedMemorySize, L::BYTES_SPLIT);
+    (void)hipGetLastError();
+    attr_set = true;
+  }
   const int tm = (int)((c.M + L::BM - 1) / L::BM), tk = (int)((c.K + L::BK - 1) / L::BK);
   const int nk = (int)(c.NP / BC);
   const int ks = (nk + S - 1) / S, splits = (nk + ks - 1) / ks;
