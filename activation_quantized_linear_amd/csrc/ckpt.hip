@@ -3,25 +3,62 @@
 // and back, x' = code * s. One pass over the data each way, bound by memory:
 // 3 bytes a value (bf16) plus 4 bytes a group.
 //
-// 32 lanes hold a group, 4 values a lane, so a group's maximum takes 5 lane
-// exchanges and no LDS, a wave works on two groups at a time, and a lane packs
-// its four codes into one dword store. Groups are numbered over the whole
-// matrix; a half wave takes kIlp of them at once to keep enough loads in flight.
+// 16 lanes hold a group, 8 values a lane (16 bytes of bf16), so a group's maximum
+// takes four DPP moves and no LDS, and a lane packs its codes into one 8-byte
+// store. Groups are numbered over the whole matrix; 16 lanes take kIlp of them at
+// once to keep enough loads in flight. Rows whose length is not a multiple of 8
+// move in fours.
 #include "ckpt.h"
 
 namespace aql {
 namespace {
 
-constexpr int kIlp = 4;
+constexpr int kIlp = 4;  // groups in flight for 16 lanes
 
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  const int i = (int)__float_as_uint(v);
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(i, i, CTRL, 0xf, 0xf, false));
+}
+
+// The maximum over a row of 16 lanes, in every lane.
+__device__ __forceinline__ float max16(float v) {
+  v = fmaxf(v, dpp<kDppXor1>(v));
+  v = fmaxf(v, dpp<kDppXor2>(v));
+  v = fmaxf(v, dpp<kDppHalfMirror>(v));
+  return fmaxf(v, dpp<kDppMirror>(v));
+}
+
+// n (8, 4 or 0) values from element i on; the others zero.
 template <bool BF16>
-__device__ __forceinline__ f32x4 load4(const void *x, int64_t i) {
+__device__ __forceinline__ void load8(const void *x, int64_t i, int n, float (&v)[8]) {
   if constexpr (BF16) {
-    const i32x2 d = *reinterpret_cast<const i32x2 *>(static_cast<const uint16_t *>(x) + i);
-    return f32x4{__uint_as_float((uint32_t)d[0] << 16), __uint_as_float((uint32_t)d[0] & 0xffff0000u),
-                 __uint_as_float((uint32_t)d[1] << 16), __uint_as_float((uint32_t)d[1] & 0xffff0000u)};
+    const uint16_t *p = static_cast<const uint16_t *>(x) + i;
+    i32x4 d = {0, 0, 0, 0};
+    if (n == 8) {
+      d = *reinterpret_cast<const i32x4 *>(p);
+    } else if (n) {
+      const i32x2 h = *reinterpret_cast<const i32x2 *>(p);
+      d[0] = h[0];
+      d[1] = h[1];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = __uint_as_float((uint32_t)d[e] << 16);
+      v[2 * e + 1] = __uint_as_float((uint32_t)d[e] & 0xffff0000u);
+    }
   } else {
-    return *reinterpret_cast<const f32x4 *>(static_cast<const float *>(x) + i);
+    const float *p = static_cast<const float *>(x) + i;
+    f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
+    if (n) a = *reinterpret_cast<const f32x4 *>(p);
+    if (n == 8) b = *reinterpret_cast<const f32x4 *>(p + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = a[e];
+      v[4 + e] = b[e];
+    }
   }
 }
 
@@ -36,8 +73,6 @@ __device__ __forceinline__ float code_of(float v, float s, float r) {
   return c;
 }
 
-// First element of group t's four of lane l, and whether they lie in the matrix:
-// (m, gi) is group t's row and place in it.
 __device__ __forceinline__ void next_group(int64_t &m, int64_t &gi, int64_t G) {
   if (++gi == G) {
     gi = 0;
@@ -45,49 +80,60 @@ __device__ __forceinline__ void next_group(int64_t &m, int64_t &gi, int64_t G) {
   }
 }
 
+// A lane's place in group (m, gi): its first element and how many of its eight
+// lie in the row (K is a multiple of 4).
+__device__ __forceinline__ int place(bool live, int64_t m, int64_t gi, int l, int64_t K,
+                                     int64_t &at) {
+  const int64_t c = gi * kCkptGroup + 8 * l;
+  at = m * K + c;
+  return !live || c >= K ? 0 : (c + 8 <= K ? 8 : 4);
+}
+
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_act_checkpoint(const void *__restrict__ x, int64_t groups,
                                                         int64_t K, int64_t G,
                                                         int8_t *__restrict__ xq,
                                                         float *__restrict__ xs) {
-  const int l = threadIdx.x & 31;
-  const int64_t t0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kIlp;
+  const int l = threadIdx.x & 15;
+  const int64_t t0 = ((int64_t)blockIdx.x * 16 + (threadIdx.x >> 4)) * kIlp;
   int64_t m = t0 / G, gi = t0 - m * G;
-  f32x4 v[kIlp];
+  float v[kIlp][8];
   int64_t at[kIlp];
+  int n[kIlp];
 #pragma unroll
   for (int u = 0; u < kIlp; ++u) {
-    const int64_t c = gi * kCkptGroup + 4 * l;
-    const bool in = t0 + u < groups && c < K;  // whole fours: K is a multiple of 4
-    at[u] = in ? m * K + c : -1;
-    v[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (in) v[u] = load4<BF16>(x, at[u]);
+    n[u] = place(t0 + u < groups, m, gi, l, K, at[u]);
+    load8<BF16>(x, at[u], n[u], v[u]);
     next_group(m, gi, G);
   }
   float mine = 1.0f;  // lane u keeps group t0 + u's scale
 #pragma unroll
   for (int u = 0; u < kIlp; ++u) {
-    float mx = fmaxf(fmaxf(fabsf(v[u][0]), fabsf(v[u][1])), fmaxf(fabsf(v[u][2]), fabsf(v[u][3])));
+    float mx = 0.0f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
+    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[u][e]));
+    mx = max16(mx);
     float s = mx / 127.0f;
     s = s > 0.0f ? s : 1.0f;
     if (l == u) mine = s;
-    if (at[u] >= 0) {
-      uint32_t w = 0;
-      // scales from 2^-100 to 2^100 have a normal reciprocal
-      if (s >= 0x1p-100f && s <= 0x1p100f) {
-        const float r = 1.0f / s;
+    uint32_t w[2] = {0, 0};
+    // scales from 2^-100 to 2^100 have a normal reciprocal
+    if (s >= 0x1p-100f && s <= 0x1p100f) {
+      const float r = 1.0f / s;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          w |= ((uint32_t)(int)clamp_code(code_of(v[u][e], s, r), -127.0f, 127.0f) & 255u) << (8 * e);
-      } else {
+      for (int e = 0; e < 8; ++e)
+        w[e >> 2] |= ((uint32_t)(int)clamp_code(code_of(v[u][e], s, r), -127.0f, 127.0f) & 255u)
+                     << (8 * (e & 3));
+    } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          w |= ((uint32_t)(int)clamp_code(rintf(v[u][e] / s), -127.0f, 127.0f) & 255u) << (8 * e);
-      }
-      *reinterpret_cast<uint32_t *>(xq + at[u]) = w;
+      for (int e = 0; e < 8; ++e)
+        w[e >> 2] |= ((uint32_t)(int)clamp_code(rintf(v[u][e] / s), -127.0f, 127.0f) & 255u)
+                     << (8 * (e & 3));
     }
+    if (n[u] == 8)
+      *reinterpret_cast<i32x2 *>(xq + at[u]) = i32x2{(int)w[0], (int)w[1]};
+    else if (n[u])
+      *reinterpret_cast<uint32_t *>(xq + at[u]) = w[0];
   }
   if (l < kIlp && t0 + l < groups) xs[t0 + l] = mine;
 }
@@ -96,33 +142,46 @@ template <bool BF16>
 __global__ __launch_bounds__(256) void k_act_restore(const int8_t *__restrict__ xq,
                                                      const float *__restrict__ xs, int64_t groups,
                                                      int64_t K, int64_t G, void *__restrict__ x) {
-  const int l = threadIdx.x & 31;
-  const int64_t t0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kIlp;
+  const int l = threadIdx.x & 15;
+  const int64_t t0 = ((int64_t)blockIdx.x * 16 + (threadIdx.x >> 4)) * kIlp;
   int64_t m = t0 / G, gi = t0 - m * G;
-  int w[kIlp];
+  int w[kIlp][2];
   float s[kIlp];
   int64_t at[kIlp];
+  int n[kIlp];
 #pragma unroll
   for (int u = 0; u < kIlp; ++u) {
-    const int64_t c = gi * kCkptGroup + 4 * l;
-    const bool in = t0 + u < groups && c < K;
-    at[u] = in ? m * K + c : -1;
-    w[u] = in ? *reinterpret_cast<const int *>(xq + at[u]) : 0;
-    s[u] = in ? xs[t0 + u] : 0.0f;
+    n[u] = place(t0 + u < groups, m, gi, l, K, at[u]);
+    w[u][0] = w[u][1] = 0;
+    if (n[u] == 8) {
+      const i32x2 d = *reinterpret_cast<const i32x2 *>(xq + at[u]);
+      w[u][0] = d[0];
+      w[u][1] = d[1];
+    } else if (n[u]) {
+      w[u][0] = *reinterpret_cast<const int *>(xq + at[u]);
+    }
+    s[u] = n[u] ? xs[t0 + u] : 0.0f;
     next_group(m, gi, G);
   }
 #pragma unroll
   for (int u = 0; u < kIlp; ++u) {
-    if (at[u] < 0) continue;
-    f32x4 v;
+    if (n[u] == 0) continue;
+    float v[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = (float)(int8_t)(w[u] >> (8 * e)) * s[u];
+    for (int e = 0; e < 8; ++e) v[e] = (float)(int8_t)(w[u][e >> 2] >> (8 * (e & 3))) * s[u];
     if constexpr (BF16) {
-      const uint32_t lo = f32_to_bf16_rne(v[0]) | ((uint32_t)f32_to_bf16_rne(v[1]) << 16);
-      const uint32_t hi = f32_to_bf16_rne(v[2]) | ((uint32_t)f32_to_bf16_rne(v[3]) << 16);
-      *reinterpret_cast<i32x2 *>(static_cast<uint16_t *>(x) + at[u]) = i32x2{(int)lo, (int)hi};
+      i32x4 d;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        d[e] = (int)((uint32_t)f32_to_bf16_rne(v[2 * e]) |
+                     ((uint32_t)f32_to_bf16_rne(v[2 * e + 1]) << 16));
+      uint16_t *p = static_cast<uint16_t *>(x) + at[u];
+      if (n[u] == 8) *reinterpret_cast<i32x4 *>(p) = d;
+      else *reinterpret_cast<i32x2 *>(p) = i32x2{d[0], d[1]};
     } else {
-      *reinterpret_cast<f32x4 *>(static_cast<float *>(x) + at[u]) = v;
+      float *p = static_cast<float *>(x) + at[u];
+      *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
+      if (n[u] == 8) *reinterpret_cast<f32x4 *>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
     }
   }
 }
@@ -132,7 +191,7 @@ __global__ __launch_bounds__(256) void k_act_restore(const int8_t *__restrict__ 
 hipError_t launch_act_checkpoint(const void *x, bool bf16, int64_t M, int64_t K, int8_t *xq,
                                  float *xs, hipStream_t st) {
   const int64_t G = (K + kCkptGroup - 1) / kCkptGroup, groups = M * G;
-  const dim3 grid((unsigned)((groups + 8 * kIlp - 1) / (8 * kIlp)));
+  const dim3 grid((unsigned)((groups + 16 * kIlp - 1) / (16 * kIlp)));
   if (bf16)
     hipLaunchKernelGGL(k_act_checkpoint<true>, grid, dim3(256), 0, st, x, groups, K, G, xq, xs);
   else
@@ -143,7 +202,7 @@ hipError_t launch_act_checkpoint(const void *x, bool bf16, int64_t M, int64_t K,
 hipError_t launch_act_restore(const int8_t *xq, const float *xs, int64_t M, int64_t K, void *x,
                               bool bf16, hipStream_t st) {
   const int64_t G = (K + kCkptGroup - 1) / kCkptGroup, groups = M * G;
-  const dim3 grid((unsigned)((groups + 8 * kIlp - 1) / (8 * kIlp)));
+  const dim3 grid((unsigned)((groups + 16 * kIlp - 1) / (16 * kIlp)));
   if (bf16)
     hipLaunchKernelGGL(k_act_restore<true>, grid, dim3(256), 0, st, xq, xs, groups, K, G, x);
   else

@@ -168,33 +168,54 @@ __device__ __forceinline__ void lora_add_tile(char *smem, f32x4 (&acc)[TI][TJ], 
   for (int q = 0; q < steps; ++q) {
     const int a = __builtin_amdgcn_readfirstlane(list[q / nc]);
     const int c = q % nc * 32;
-    for (int u = tid; u < BM * 4; u += NT) {  // a row's ranks c + 8 k .. + 7
-      const int row = u >> 2, k = u & 3;
-      f32x4 h0 = {0.f, 0.f, 0.f, 0.f}, h1 = h0;
-      if (ids[row] == a && c + 8 * k < t.R) {  // whole chunks: R is a multiple of 8
+    // both operands' loads are out before the first is used
+    constexpr int TH = BM * 4, NH = (TH + NT - 1) / NT, NW = S::W / 16 / NT;
+    static_assert((NH == 1 || NH * NT == TH) && NW * NT == S::W / 16, "staged evenly");
+    f32x4 hv[NH][2];
+    i32x4 wv[NW];
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {  // a row's ranks c + 8 k .. + 7
+      const int u = tid + NT * i, row = u >> 2, k = u & 3;
+      hv[i][0] = hv[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (u < TH && ids[row] == a && c + 8 * k < t.R) {  // whole chunks: R is a multiple of 8
         const float *h = t.h + (m0 + row) * t.R + c + 8 * k;
-        h0 = *reinterpret_cast<const f32x4 *>(h);
-        h1 = *reinterpret_cast<const f32x4 *>(h + 4);
+        hv[i][0] = *reinterpret_cast<const f32x4 *>(h);
+        hv[i][1] = *reinterpret_cast<const f32x4 *>(h + 4);
       }
-      const float v[8] = {h0[0], h0[1], h0[2], h0[3], h1[0], h1[1], h1[2], h1[3]};
-      bf16x8 hi, lo;
-      split_bf16(v, hi, lo);
-      *reinterpret_cast<bf16x8 *>(smem + row * 128 + 16 * (k ^ hswz(row))) = hi;
-      *reinterpret_cast<bf16x8 *>(smem + row * 128 + 16 * ((4 + k) ^ hswz(row))) = lo;
     }
-    for (int u = tid; u < S::W / 16; u += NT) {
-      i32x4 w = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const int u = tid + NT * i;
+      wv[i] = i32x4{0, 0, 0, 0};
       if constexpr (KMAJOR) {
         const int j = u / (BN / 8), k = u % (BN / 8);  // rank c + j, columns 8 k .. + 7
         if (c + j < t.R && n0 + 8 * k < t.N)  // whole chunks: N is a multiple of 8
-          w = *reinterpret_cast<const i32x4 *>(t.W + ((int64_t)a * t.R + c + j) * t.N + n0 + 8 * k);
-        *reinterpret_cast<i32x4 *>(smem + S::H + 16 * u) = w;
+          wv[i] = *reinterpret_cast<const i32x4 *>(t.W + ((int64_t)a * t.R + c + j) * t.N + n0 +
+                                                   8 * k);
       } else {
         const int row = u >> 2, k = u & 3;  // column n0 + row, ranks c + 8 k .. + 7
         if (c + 8 * k < t.R && n0 + row < t.N)
-          w = *reinterpret_cast<const i32x4 *>(t.W + ((int64_t)a * t.N + n0 + row) * t.R + c + 8 * k);
-        *reinterpret_cast<i32x4 *>(smem + S::H + row * 64 + 16 * (k ^ wswz(row))) = w;
+          wv[i] = *reinterpret_cast<const i32x4 *>(t.W + ((int64_t)a * t.N + n0 + row) * t.R + c +
+                                                   8 * k);
       }
+    }
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      const int u = tid + NT * i, row = u >> 2, k = u & 3;
+      const float v[8] = {hv[i][0][0], hv[i][0][1], hv[i][0][2], hv[i][0][3],
+                          hv[i][1][0], hv[i][1][1], hv[i][1][2], hv[i][1][3]};
+      bf16x8 hi, lo;
+      split_bf16(v, hi, lo);
+      if (u < TH) {
+        *reinterpret_cast<bf16x8 *>(smem + row * 128 + 16 * (k ^ hswz(row))) = hi;
+        *reinterpret_cast<bf16x8 *>(smem + row * 128 + 16 * ((4 + k) ^ hswz(row))) = lo;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const int u = tid + NT * i, row = u >> 2, k = u & 3;
+      *reinterpret_cast<i32x4 *>(smem + S::H +
+                                 (KMAJOR ? 16 * u : row * 64 + 16 * (k ^ wswz(row)))) = wv[i];
     }
     __syncthreads();
     bf16x8 w[TJ];
