@@ -682,12 +682,16 @@ int aql_linear_w8a16_lora(const uint16_t *x, int64_t M, int64_t K, const int8_t 
   if (int e = check_device(fn)) return e;
   hipStream_t st = (hipStream_t)stream;
   const int32_t *p = static_cast<const int32_t *>(plan);
-  hipError_t e =
-      aql::launch_lora_shrink(x, M, K, A, alpha, L, R, p, h, static_cast<float *>(ws), st);
-  if (e != hipSuccess) return launched(e, fn);
-  const aql::LoraTerm lt{h, B, p + aql::lora_plan_layout(M, L).idx, (int32_t)R, N};
   float *part = static_cast<float *>(ws);
   const size_t pb = ws ? ws_bytes : 0;
+  aql::LoraTerm lt{h, B, p + aql::lora_plan_layout(M, L).idx, (int32_t)R, N};
+  if (M < kW8A16GemmMinM && aql::w8a16_skinny_splits(M, N, K) > 1) {
+    lt.A = A;  // the launch of the splits computes h beside them
+    lt.alpha = alpha;
+  } else {
+    const hipError_t e = aql::launch_lora_shrink(x, M, K, A, alpha, L, R, p, h, part, st);
+    if (e != hipSuccess) return launched(e, fn);
+  }
   // the same M-dispatch as aql_linear_w8a16
   if (M >= kW8A16GemmMinM && K <= (1LL << 22))
     return launched(aql::launch_w8a16_gemm(x, M, K, q, scale, bias, N, y, part, pb, st, lt), fn);

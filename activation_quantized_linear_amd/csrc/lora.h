@@ -59,6 +59,10 @@ struct LoraTerm {
   const int32_t *idx;    // [M]
   int32_t R;             // a multiple of 8
   int64_t N;
+  // not NULL: h is not there yet, the launch that leaves the projection's partial
+  // sums computes it beside them (lora_shrink_rows; A [L, R, K], alpha [L])
+  const uint16_t *A = nullptr;
+  const float *alpha = nullptr;
   __device__ __forceinline__ float add(int64_t m, int64_t n, float v) const {
     const int a = idx[m];
     if (a < 0) return v;
@@ -81,6 +85,70 @@ struct LoraTerm {
     return v + (s0 + s1);
   }
 };
+
+__device__ __forceinline__ float bf16_lo(int d) { return __uint_as_float((uint32_t)d << 16); }
+__device__ __forceinline__ float bf16_hi(int d) {
+  return __uint_as_float((uint32_t)d & 0xffff0000u);
+}
+
+// h of few rows, by a workgroup of 4 waves: J ranks from j0 on of row m. J rows of
+// the adapter's A are read once, the waves taking 512-element steps of K in turn.
+// Bound by latency and, with many adapters, by reading them (2 R K bytes each).
+// red: 4 J floats of LDS.
+template <int J>
+__device__ __forceinline__ void lora_shrink_rows(const uint16_t *x, int64_t K, const uint16_t *A,
+                                                 const float *alpha, int R, const int32_t *idx,
+                                                 float *h, int64_t m, int j0, float *red) {
+  const int a = idx[m];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (a < 0) {  // uniform over the workgroup
+    if (threadIdx.x < J) h[m * R + j0 + threadIdx.x] = 0.0f;
+    return;
+  }
+  const uint16_t *xr = x + m * K, *ar = A + ((int64_t)a * R + j0) * K;
+  float acc[J][2];
+#pragma unroll
+  for (int j = 0; j < J; ++j) acc[j][0] = acc[j][1] = 0.0f;
+  constexpr int U = J == 1 ? 4 : 2;
+  for (int64_t k0 = 8 * (int64_t)threadIdx.x; k0 < K; k0 += 2048 * U) {
+    i32x4 xv[U], av[U][J];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t k = k0 + 2048 * u;
+      xv[u] = i32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < J; ++j) av[u][j] = i32x4{0, 0, 0, 0};
+      if (k < K) {
+        xv[u] = *reinterpret_cast<const i32x4 *>(xr + k);
+#pragma unroll
+        for (int j = 0; j < J; ++j) av[u][j] = *reinterpret_cast<const i32x4 *>(ar + j * K + k);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x0 = bf16_lo(xv[u][e]), x1 = bf16_hi(xv[u][e]);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          acc[j][0] = fmaf(x0, bf16_lo(av[u][j][e]), acc[j][0]);
+          acc[j][1] = fmaf(x1, bf16_hi(av[u][j][e]), acc[j][1]);
+        }
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    float s = acc[j][0] + acc[j][1];
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    if (lane == 0) red[wave * J + j] = s;
+  }
+  __syncthreads();
+  if (threadIdx.x < J) {
+    const int j = threadIdx.x;
+    h[m * R + j0 + j] = alpha[a] * ((red[j] + red[J + j]) + (red[2 * J + j] + red[3 * J + j]));
+  }
+}
 
 // Eight floats -> bf16 parts with v = hi + lo up to 2^-16 |v| (both rounded to
 // nearest, 2^-8 each): products with bf16 operands then cost two matrix instructions and

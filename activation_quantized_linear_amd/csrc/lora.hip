@@ -114,72 +114,13 @@ __global__ __launch_bounds__(1024) void k_lora_plan(const int32_t *__restrict__ 
 
 // --------------------------------------------------- shrink, streaming form
 
-__device__ __forceinline__ float bf16_lo(int d) { return __uint_as_float((uint32_t)d << 16); }
-__device__ __forceinline__ float bf16_hi(int d) {
-  return __uint_as_float((uint32_t)d & 0xffff0000u);
-}
-
-// Few rows: a workgroup of 4 waves takes J ranks of one row and reads J rows
-// of its adapter's A once, the waves taking 512-element steps of K in turn.
-// Bound by latency and, with many adapters, by reading them (2 R K bytes each).
 template <int J>
 __global__ __launch_bounds__(256) void k_lora_shrink_rows(
     const uint16_t *__restrict__ x, int64_t K, const uint16_t *__restrict__ A,
     const float *__restrict__ alpha, int R, const int32_t *__restrict__ idx,
     float *__restrict__ h) {
-  __shared__ float red[4][J];
-  const int64_t m = blockIdx.y;
-  const int j0 = blockIdx.x * J;
-  const int a = idx[m];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (a < 0) {  // uniform over the workgroup
-    if (threadIdx.x < J) h[m * R + j0 + threadIdx.x] = 0.0f;
-    return;
-  }
-  const uint16_t *xr = x + m * K, *ar = A + ((int64_t)a * R + j0) * K;
-  float acc[J][2];
-#pragma unroll
-  for (int j = 0; j < J; ++j) acc[j][0] = acc[j][1] = 0.0f;
-  constexpr int U = J == 1 ? 4 : 2;
-  for (int64_t k0 = 8 * (int64_t)threadIdx.x; k0 < K; k0 += 2048 * U) {
-    i32x4 xv[U], av[U][J];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t k = k0 + 2048 * u;
-      xv[u] = i32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int j = 0; j < J; ++j) av[u][j] = i32x4{0, 0, 0, 0};
-      if (k < K) {
-        xv[u] = *reinterpret_cast<const i32x4 *>(xr + k);
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-          av[u][j] = *reinterpret_cast<const i32x4 *>(ar + j * K + k);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float x0 = bf16_lo(xv[u][e]), x1 = bf16_hi(xv[u][e]);
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          acc[j][0] = fmaf(x0, bf16_lo(av[u][j][e]), acc[j][0]);
-          acc[j][1] = fmaf(x1, bf16_hi(av[u][j][e]), acc[j][1]);
-        }
-      }
-  }
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    float s = acc[j][0] + acc[j][1];
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-    if (lane == 0) red[wave][j] = s;
-  }
-  __syncthreads();
-  if (threadIdx.x < J) {
-    const int j = threadIdx.x;
-    h[m * R + j0 + j] = alpha[a] * ((red[0][j] + red[1][j]) + (red[2][j] + red[3][j]));
-  }
+  __shared__ float red[4 * J];
+  lora_shrink_rows<J>(x, K, A, alpha, R, idx, h, blockIdx.y, blockIdx.x * J, red);
 }
 
 // ------------------------------------------------------- shrink, tiled form

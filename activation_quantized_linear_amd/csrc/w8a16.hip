@@ -1036,7 +1036,9 @@ struct ShLds {
 };
 
 // part == nullptr: the whole K, y written. Else split blockIdx.z takes steps
-// [z spl, (z + 1) spl) and writes its unscaled sums to part[z][M][N] (fp32).
+// [z spl, (z + 1) spl) and writes its unscaled sums to part[z][M][N] (fp32). With
+// adapters the slices behind the splits compute the rows' h, which the sum of the
+// splits needs (M = 27, K = 14336, N = 4096, R = 16: 25.1 us in a launch of its own).
 template <int WC, int WK, class LT>
 __global__ __launch_bounds__(64 * WC * WK) void k_w8a16_sksh(const uint16_t *__restrict__ x, int64_t M,
                                                              int64_t K, const int8_t *__restrict__ q,
@@ -1046,6 +1048,19 @@ __global__ __launch_bounds__(64 * WC * WK) void k_w8a16_sksh(const uint16_t *__r
                                                              float *__restrict__ part, int spl, LT lt) {
   static_assert(8 % WC == 0, "x pieces split over a range's waves");
   __shared__ __attribute__((aligned(16))) ShLds<WC, WK> sm;
+  if constexpr (LT::on && WC * WK == 4) {
+    // the slices past the splits: h of row i / (R / 4), ranks 4 (i % (R / 4)) .. + 3
+    const int splits = ((int)((K + 255) >> 8) + spl - 1) / (spl > 0 ? spl : 1);
+    if (part && (int)blockIdx.z >= splits) {
+      const int64_t i = ((int64_t)(blockIdx.z - splits) * gridDim.y + blockIdx.y) * gridDim.x +
+                        blockIdx.x;
+      const int q = lt.R / 4;
+      if (i < M * q)
+        lora_shrink_rows<4>(x, K, lt.A, lt.alpha, lt.R, lt.idx, const_cast<float *>(lt.h), i / q,
+                            4 * (int)(i % q), reinterpret_cast<float *>(&sm));
+      return;
+    }
+  }
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wc = wave % WC, wk = wave / WC;
@@ -1510,7 +1525,9 @@ hipError_t launch_stream(const uint16_t *x, int64_t M, int64_t K, const int8_t *
     const int nst = (int)((K + 255) / 256);
     const int spl = (nst + S - 1) / S;
     const int splits = (nst + spl - 1) / spl;
-    const dim3 grid((unsigned)((N + 63) / 64), (unsigned)((M + 15) / 16), (unsigned)splits);
+    dim3 grid((unsigned)((N + 63) / 64), (unsigned)((M + 15) / 16), (unsigned)splits);
+    if constexpr (LT::on)  // the rows' h in slices of workgroups behind the splits'
+      if (lt.A) grid.z += (unsigned)((M * (lt.R / 4) + grid.x * grid.y - 1) / (grid.x * grid.y));
     hipLaunchKernelGGL((k_w8a16_sksh<4, 1, LT>), grid, dim3(256), 0, st, x, M, K, q, scale, bias, N, y,
                        part, spl, lt);
     const hipError_t e = hipGetLastError();

@@ -509,14 +509,16 @@ hipError_t go_split(const Call &c, int S, const LT &lt) {
   return hipGetLastError();
 }
 
-// 64 x 256 tiles split while the units stay within two a CU and each keeps at
-// least 8 stages of 64 channels.
+// 64 x 256 tiles split while the units stay within one a CU and each keeps at
+// least 8 stages of 64 channels (M = 500, N = K = 4096: 33 us; 39 with two units a
+// CU, whose partial sums cost more than the second unit hides, 41 with half a one;
+// M = 333, N = 2560, K = 960: 18.7, 19.9 with 5 stages a unit).
 int splits_of(int64_t M, int64_t N, int64_t K) {
   const int64_t twide = ((M + 127) / 128) * ((K + 255) / 256);
   if (twide >= 160) return 1;
   const int64_t tiles = ((M + 63) / 64) * ((K + 255) / 256), nk = (N + BC - 1) / BC;
   int S = 1;
-  while (S < 32 && tiles * 2 * S <= 512 && nk / (2 * S) >= 8) S *= 2;
+  while (tiles * 2 * S <= 256 && nk / (2 * S) >= 8) S *= 2;
   return S;
 }
 
