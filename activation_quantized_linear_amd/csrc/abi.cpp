@@ -193,12 +193,11 @@ size_t ws_lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
   return lin > shr ? lin : shr;
 }
 
-// Workspace of its backward pass: u [M, R], then one region for the shrink's
-// partial sums and, after them, dx's.
+// Workspace of its backward pass: u [M, R], dx's, the shrink's partial sums.
 size_t lora_bwd_u_bytes(int64_t M, int64_t R) { return align256((size_t)M * (size_t)R * 4); }
 size_t ws_lora_bwd(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
-  const size_t shr = aql::lora_shrink_bytes(M, N, L, R), dx = aql::w8a16_dgrad_bytes(M, N, K);
-  return lora_bwd_u_bytes(M, R) + (shr > dx ? shr : dx);
+  return lora_bwd_u_bytes(M, R) + align256(aql::w8a16_dgrad_bytes(M, N, K)) +
+         aql::lora_shrink_bytes(M, N, L, R);
 }
 bool lora_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
   return plan_sizes_ok(M, L) && M > 0 && N >= 0 && K >= 16 && K <= kMaxKW8A16 && R >= 8 &&
@@ -743,10 +742,15 @@ int aql_linear_w8a16_lora_backward(const uint16_t *dy, int64_t M, int64_t N, con
   hipStream_t st = (hipStream_t)stream;
   const int32_t *p = static_cast<const int32_t *>(plan);
   float *u = static_cast<float *>(ws);
-  void *rest = static_cast<char *>(ws) + lora_bwd_u_bytes(M, R);
   hipError_t e = hipSuccess;
+  aql::DgradScale sc{};
+  char *dws = static_cast<char *>(ws) + lora_bwd_u_bytes(M, R);
   if (M > 0 && (dx || dA)) {
-    e = aql::launch_lora_shrink_t(dy, M, N, B, alpha, L, R, p, u, static_cast<float *>(rest), st);
+    if (dx) sc = aql::w8a16_dgrad_scale_args(dy, scale, M, N, K, dws);
+    e = aql::launch_lora_shrink_t(
+        dy, M, N, B, alpha, L, R, p, u,
+        reinterpret_cast<float *>(dws + align256(aql::w8a16_dgrad_bytes(M, N, K))),
+        dx ? &sc : nullptr, st);
     if (e != hipSuccess) return launched(e, fn);
   }
   if (dA || (dB && N > 0)) {
@@ -770,7 +774,7 @@ int aql_linear_w8a16_lora_backward(const uint16_t *dy, int64_t M, int64_t N, con
   }
   if (dx && M > 0) {
     const aql::LoraTerm lt{u, A, p + aql::lora_plan_layout(M, L).idx, (int32_t)R, K};
-    e = aql::launch_w8a16_dgrad(dy, M, N, q, scale, K, dx, rest, st, lt);
+    e = aql::launch_w8a16_dgrad_scaled(sc, q, K, dx, dws, st, lt);
   }
   return launched(e, fn);
 }

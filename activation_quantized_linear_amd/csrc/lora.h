@@ -348,10 +348,12 @@ hipError_t launch_lora_shrink(const uint16_t *x, int64_t M, int64_t K, const uin
 
 // u[m, :] = alpha[a] B_a^T dy[m] (float32 [M, R]); rows without an adapter get
 // zeros. dy [M, N] bf16, B [L, N, R] bf16, N % 8 == 0. part:
-// lora_shrink_bytes(M, N, L, R) bytes.
+// lora_shrink_bytes(M, N, L, R) bytes. sc (may be NULL): dy's scaling for the
+// input's gradient, done by further workgroups of the same launch.
+struct DgradScale;
 hipError_t launch_lora_shrink_t(const uint16_t *dy, int64_t M, int64_t N, const uint16_t *B,
                                 const float *alpha, int64_t L, int64_t R, const int32_t *plan,
-                                float *u, float *part, hipStream_t st);
+                                float *u, float *part, const DgradScale *sc, hipStream_t st);
 
 // dB[a][n, j] = sum_{m in a} dy[m, n] h[m, j] and
 // dA[a][j, k] = sum_{m in a} u[m, j] xq[m, k] xs[m, k / 128], both float32;

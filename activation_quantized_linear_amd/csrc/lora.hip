@@ -14,6 +14,8 @@
 // Every sum has one order, so results repeat bit for bit.
 #include "lora.h"
 
+#include "w8a16_dgrad.h"
+
 namespace aql {
 namespace {
 
@@ -126,7 +128,7 @@ __global__ __launch_bounds__(256) void k_lora_shrink_rows(
 // ------------------------------------------------------- shrink, tiled form
 
 // A workgroup of W waves takes NT tiles of the plan (16 rows each, mostly of one
-// adapter), 16 ranks and one of gridDim.z ranges of the contraction; its waves
+// adapter), 16 ranks and one of several ranges of the contraction; its waves
 // take steps of 128 in turn and meet in LDS. What it costs is round trips to
 // memory (about 1.3 us each with the data in HBM), so all loads of a step are out
 // at once, and a CU draws little more than its 1/256 of the memory's rate, so
@@ -145,19 +147,42 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 constexpr int kU = 4;           // matrix instructions of a step
 constexpr int kStep = 32 * kU;  // of the contraction, per wave
 
-template <int NT, int W, bool KMAJOR>
+// The scaling's part of a launch: none, or dgrad_scale_row<NI> in the workgroups
+// behind the shrink's, W / 4 rows each.
+struct NoScale {
+  static constexpr bool on = false;
+  __device__ void row(int64_t, int, float *) const {}
+};
+template <int NI>
+struct WithScale {
+  static constexpr bool on = true;
+  DgradScale a;
+  __device__ void row(int64_t m, int t, float *red) const { dgrad_scale_row<NI>(a, m, t, red); }
+};
+
+template <int NT, int W, bool KMAJOR, class SC>
 __global__ __launch_bounds__(64 * W) void k_lora_shrink(
     const uint16_t *__restrict__ x, int64_t C, const uint16_t *__restrict__ A,
     const float *__restrict__ alpha, int R, int64_t M, int64_t L,
     const int32_t *__restrict__ plan, float *__restrict__ h, float *__restrict__ part,
-    int64_t range) {
+    int64_t range, int tiles, int ranks, int shrink_blocks, SC sc) {
   constexpr int SLOT = (KMAJOR && kU * 1024 > NT * 1024) ? kU * 1024 : NT * 1024;  // a wave's
   __shared__ __attribute__((aligned(16))) char smem[W * SLOT];
+  if constexpr (SC::on) {
+    if ((int)blockIdx.x >= shrink_blocks) {
+      const int64_t m = (int64_t)(blockIdx.x - shrink_blocks) * (W / 4) + threadIdx.x / 256;
+      sc.row(m, threadIdx.x % 256, reinterpret_cast<float *>(smem));
+      return;
+    }
+  }
   const LoraPlanLayout p = lora_plan_layout(M, L);
-  const int t0 = blockIdx.x * NT, rb = blockIdx.y * 16;  // first tile, first rank
+  // the workgroup's first tile, first rank and range
+  const int bx = blockIdx.x % tiles, by = blockIdx.x / tiles % ranks;
+  const int bz = blockIdx.x / (tiles * ranks);
+  const int t0 = bx * NT, rb = by * 16;
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t c_lo = blockIdx.z * range, c_hi = c_lo + range < C ? c_lo + range : C;
+  const int64_t c_lo = bz * range, c_hi = c_lo + range < C ? c_lo + range : C;
   int owner[NT], row[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -260,7 +285,7 @@ __global__ __launch_bounds__(64 * W) void k_lora_shrink(
         for (int w = 1; w < W; ++w) s += red[(w * NT + t) * 64 + lane];
         const int64_t pos = (int64_t)(t0 + t) * kLoraTile + 4 * g;
         if (part) {
-          float *dst = part + (blockIdx.z * p.tiles * kLoraTile + pos) * R + j;
+          float *dst = part + (bz * p.tiles * kLoraTile + pos) * R + j;
 #pragma unroll
           for (int v = 0; v < 4; ++v) dst[(int64_t)v * R] = s[v];
         } else {
@@ -514,23 +539,28 @@ int shrink_ranges(int64_t M, int64_t C, int64_t L, int64_t R) {
   return z < 1 ? 1 : (int)z;
 }
 
-template <bool KMAJOR>
+template <bool KMAJOR, class SC>
 hipError_t go_shrink(const uint16_t *x, int64_t M, int64_t C, const uint16_t *A,
                      const float *alpha, int64_t L, int64_t R, const int32_t *plan, float *h,
-                     float *part, hipStream_t st) {
+                     float *part, const SC &sc, hipStream_t st) {
   const LoraPlanLayout p = lora_plan_layout(M, L);
-  const unsigned rb = (unsigned)((R + 15) / 16);
+  const int ranks = (int)((R + 15) / 16);
   if (shrink_whole(M, C, L, R)) {
-    hipLaunchKernelGGL((k_lora_shrink<1, 16, KMAJOR>), dim3((unsigned)p.tiles, rb), dim3(1024), 0,
-                       st, x, C, A, alpha, (int)R, M, L, plan, h, (float *)nullptr, C);
+    const int tiles = (int)p.tiles, blocks = tiles * ranks;
+    hipLaunchKernelGGL((k_lora_shrink<1, 16, KMAJOR, SC>),
+                       dim3((unsigned)(blocks + (SC::on ? (M + 3) / 4 : 0))), dim3(1024), 0, st, x,
+                       C, A, alpha, (int)R, M, L, plan, h, (float *)nullptr, C, tiles, ranks,
+                       blocks, sc);
     return hipGetLastError();
   }
   int z = shrink_ranges(M, C, L, R);
   const int64_t range = (C + (int64_t)z * kStep - 1) / ((int64_t)z * kStep) * kStep;
   if (z > 1) z = (int)((C + range - 1) / range);
-  hipLaunchKernelGGL((k_lora_shrink<4, 4, KMAJOR>),
-                     dim3((unsigned)((p.tiles + 3) / 4), rb, (unsigned)z), dim3(256), 0, st, x, C,
-                     A, alpha, (int)R, M, L, plan, h, z > 1 ? part : nullptr, range);
+  const int tiles = (int)((p.tiles + 3) / 4), blocks = tiles * ranks * z;
+  hipLaunchKernelGGL((k_lora_shrink<4, 4, KMAJOR, SC>),
+                     dim3((unsigned)(blocks + (SC::on ? M : 0))), dim3(256), 0, st, x, C, A, alpha,
+                     (int)R, M, L, plan, h, z > 1 ? part : nullptr, range, tiles, ranks, blocks,
+                     sc);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || z <= 1) return e;
   const int64_t n = p.tiles * kLoraTile * (R / 4);
@@ -571,7 +601,7 @@ size_t lora_shrink_bytes(int64_t M, int64_t C, int64_t L, int64_t R) {
 hipError_t launch_lora_shrink(const uint16_t *x, int64_t M, int64_t K, const uint16_t *A,
                               const float *alpha, int64_t L, int64_t R, const int32_t *plan,
                               float *h, float *part, hipStream_t st) {
-  if (M >= kLoraTiledMinM) return go_shrink<false>(x, M, K, A, alpha, L, R, plan, h, part, st);
+  if (M >= kLoraTiledMinM) return go_shrink<false>(x, M, K, A, alpha, L, R, plan, h, part, NoScale{}, st);
   const int32_t *idx = plan + lora_plan_layout(M, L).idx;
   if (M * R < 2048)
     hipLaunchKernelGGL(k_lora_shrink_rows<1>, dim3((unsigned)R, (unsigned)M), dim3(256), 0, st, x,
@@ -584,8 +614,13 @@ hipError_t launch_lora_shrink(const uint16_t *x, int64_t M, int64_t K, const uin
 
 hipError_t launch_lora_shrink_t(const uint16_t *dy, int64_t M, int64_t N, const uint16_t *B,
                                 const float *alpha, int64_t L, int64_t R, const int32_t *plan,
-                                float *u, float *part, hipStream_t st) {
-  return go_shrink<true>(dy, M, N, B, alpha, L, R, plan, u, part, st);
+                                float *u, float *part, const DgradScale *sc, hipStream_t st) {
+  if (!sc) return go_shrink<true>(dy, M, N, B, alpha, L, R, plan, u, part, NoScale{}, st);
+  if (sc->NP <= 4096)
+    return go_shrink<true>(dy, M, N, B, alpha, L, R, plan, u, part, WithScale<2>{*sc}, st);
+  if (sc->NP <= 16384)
+    return go_shrink<true>(dy, M, N, B, alpha, L, R, plan, u, part, WithScale<8>{*sc}, st);
+  return go_shrink<true>(dy, M, N, B, alpha, L, R, plan, u, part, WithScale<0>{*sc}, st);
 }
 
 hipError_t launch_lora_wgrad(const LoraWgradArgs &a, hipStream_t st) {

@@ -31,10 +31,8 @@ namespace {
 
 typedef __attribute__((address_space(3))) void lds_void;
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int BC = 64;           // channels a stage
-constexpr int kTop = 14;         // exponent of a row's largest scaled product
+constexpr int BC = kDgradStage;  // channels a stage
 constexpr int kCode = 9;         // codes enter the matrix cores as q 2^-9
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *base, uint32_t bytes) {
@@ -44,76 +42,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *base, uint32_
 
 // ------------------------------------------------------------- scaling of dy
 
-// TPR threads a row, 8 values a thread and round; NI rounds are held in
-// registers between the maximum and the scaling, so dy is read once (NI = 0: any
-// N, read twice). Bound by memory: 4 bytes a value.
-template <int TPR, int NI>
-__global__ __launch_bounds__(256) void k_dgrad_scale(const uint16_t *__restrict__ dy,
-                                                     const float *__restrict__ scale, int64_t M,
-                                                     int64_t N, int64_t NP,
-                                                     uint16_t *__restrict__ d,
-                                                     int32_t *__restrict__ ex) {
-  __shared__ float red[8];
-  const int t = threadIdx.x % TPR;
-  const int64_t m = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
-  if (TPR == 64 && m >= M) return;  // whole waves (TPR 256: one row a workgroup)
-  const uint16_t *row = dy + m * N;
-  auto load = [&](int64_t n, float (&v)[8]) {
-    const i32x4 w = *reinterpret_cast<const i32x4 *>(row + n);
-    const f32x4 s0 = *reinterpret_cast<const f32x4 *>(scale + n);
-    const f32x4 s1 = *reinterpret_cast<const f32x4 *>(scale + n + 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t u = (uint32_t)w[i];
-      v[2 * i] = __uint_as_float(u << 16) * (i < 2 ? s0[2 * i] : s1[2 * i - 4]);
-      v[2 * i + 1] = __uint_as_float(u & 0xffff0000u) * (i < 2 ? s0[2 * i + 1] : s1[2 * i - 3]);
-    }
-  };
-  float mx = 0.0f;
-  constexpr int NR = NI > 0 ? NI : 1;
-  float v[NR][8];
-  if constexpr (NI > 0) {
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int64_t n = 8 * (int64_t)(t + TPR * i);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
-      if (n < N) load(n, v[i]);  // whole chunks: N is a multiple of 8
-    }
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[i][e]));
-  } else {
-    for (int64_t n = 8 * (int64_t)t; n < N; n += 8 * TPR) {
-      load(n, v[0]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[0][e]));
-    }
-  }
-  mx = group_reduce_max<TPR>(mx, red);
-  const int e2 = kTop - __builtin_amdgcn_frexp_expf(mx);
-  if (t == 0) ex[m] = e2;
-  auto store = [&](int64_t n, const float (&x)[8]) {
-    f16x8 o;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = (_Float16)ldexpf(x[e], e2);
-    *reinterpret_cast<f16x8 *>(d + m * NP + n) = o;
-  };
-  if constexpr (NI > 0) {
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int64_t n = 8 * (int64_t)(t + TPR * i);
-      if (n < NP) store(n, v[i]);
-    }
-  } else {
-    for (int64_t n = 8 * (int64_t)t; n < NP; n += 8 * TPR) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[0][e] = 0.0f;
-      if (n < N) load(n, v[0]);
-      store(n, v[0]);
-    }
-  }
+template <int NI>
+__global__ __launch_bounds__(256) void k_dgrad_scale(DgradScale a) {
+  __shared__ float red[4];
+  dgrad_scale_row<NI>(a, blockIdx.x, threadIdx.x, red);
 }
 
 // ------------------------------------------------------------------- product
@@ -538,33 +470,21 @@ Layout layout(int64_t M, int64_t N, int64_t K) {
   return l;
 }
 
-template <int TPR, int NI>
-hipError_t scale(const uint16_t *dy, const float *s, const Call &c, uint16_t *d, int32_t *ex) {
-  const unsigned grid = (unsigned)((c.M + 256 / TPR - 1) / (256 / TPR));
-  hipLaunchKernelGGL((k_dgrad_scale<TPR, NI>), dim3(grid), dim3(256), 0, c.st, dy, s, c.M, c.N,
-                     c.NP, d, ex);
+template <int NI>
+hipError_t scale(const DgradScale &a, hipStream_t st) {
+  hipLaunchKernelGGL(k_dgrad_scale<NI>, dim3((unsigned)a.M), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
 template <class LT>
-hipError_t launch(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q, const float *s,
-                  int64_t K, uint16_t *dx, void *ws, hipStream_t st, const LT &lt) {
-  const Layout l = layout(M, N, K);
-  char *base = static_cast<char *>(ws);
-  uint16_t *d = reinterpret_cast<uint16_t *>(base);
-  int32_t *ex = reinterpret_cast<int32_t *>(base + l.ex);
-  const Call c{d, ex, q, dx, M, N, l.NP, K, reinterpret_cast<float *>(base + l.part), st};
-  hipError_t e;
-  if (l.NP <= 1024) e = scale<64, 2>(dy, s, c, d, ex);
-  else if (l.NP <= 2048) e = scale<256, 1>(dy, s, c, d, ex);
-  else if (l.NP <= 4096) e = scale<256, 2>(dy, s, c, d, ex);
-  else if (l.NP <= 8192) e = scale<256, 4>(dy, s, c, d, ex);
-  else if (l.NP <= 16384) e = scale<256, 8>(dy, s, c, d, ex);
-  else e = scale<256, 0>(dy, s, c, d, ex);
-  if (e != hipSuccess) return e;
-  const int64_t twide = ((M + 127) / 128) * ((K + 255) / 256);
+hipError_t launch(const DgradScale &a, const int8_t *q, int64_t K, uint16_t *dx, void *ws,
+                  hipStream_t st, const LT &lt) {
+  const Layout l = layout(a.M, a.N, K);
+  const Call c{a.d, a.ex, q, dx, a.M, a.N, a.NP, K,
+               reinterpret_cast<float *>(static_cast<char *>(ws) + l.part), st};
+  const int64_t twide = ((a.M + 127) / 128) * ((K + 255) / 256);
   if (twide >= 160) return go<8, 4>(c, lt);
-  const int S = splits_of(M, N, K);
+  const int S = splits_of(a.M, a.N, K);
   if (S > 1) return go_split<4, 4>(c, S, lt);
   return go<4, 4>(c, lt);
 }
@@ -573,16 +493,30 @@ hipError_t launch(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q, con
 
 size_t w8a16_dgrad_bytes(int64_t M, int64_t N, int64_t K) { return layout(M, N, K).total; }
 
-hipError_t launch_w8a16_dgrad(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q,
-                              const float *scale, int64_t K, uint16_t *dx, void *ws,
-                              hipStream_t st) {
-  return launch(dy, M, N, q, scale, K, dx, ws, st, NoLora{});
+DgradScale w8a16_dgrad_scale_args(const uint16_t *dy, const float *scale, int64_t M, int64_t N,
+                                  int64_t K, void *ws) {
+  const Layout l = layout(M, N, K);
+  char *base = static_cast<char *>(ws);
+  return DgradScale{dy, scale, M, N, l.NP, reinterpret_cast<uint16_t *>(base),
+                    reinterpret_cast<int32_t *>(base + l.ex)};
 }
 
 hipError_t launch_w8a16_dgrad(const uint16_t *dy, int64_t M, int64_t N, const int8_t *q,
-                              const float *scale, int64_t K, uint16_t *dx, void *ws,
-                              hipStream_t st, const LoraTerm &lt) {
-  return launch(dy, M, N, q, scale, K, dx, ws, st, lt);
+                              const float *s, int64_t K, uint16_t *dx, void *ws, hipStream_t st) {
+  const DgradScale a = w8a16_dgrad_scale_args(dy, s, M, N, K, ws);
+  hipError_t e;
+  if (a.NP <= 2048) e = scale<1>(a, st);
+  else if (a.NP <= 4096) e = scale<2>(a, st);
+  else if (a.NP <= 8192) e = scale<4>(a, st);
+  else if (a.NP <= 16384) e = scale<8>(a, st);
+  else e = scale<0>(a, st);
+  if (e != hipSuccess) return e;
+  return launch(a, q, K, dx, ws, st, NoLora{});
+}
+
+hipError_t launch_w8a16_dgrad_scaled(const DgradScale &a, const int8_t *q, int64_t K, uint16_t *dx,
+                                     void *ws, hipStream_t st, const LoraTerm &lt) {
+  return launch(a, q, K, dx, ws, st, lt);
 }
 
 }  // namespace aql
