@@ -177,45 +177,35 @@ __device__ __forceinline__ void split_bf16(const float (&v)[8], bf16x8 &hi, bf16
 // The adapter terms of a workgroup's output tile, after its own sums: acc[i][j]
 // += h . W_a^T for the blocks of 16 x 16 that a wave holds (16x16x32 layout, lane
 // 16 g + r holding rows 4 g + v of one column). The tile's distinct adapters are
-// walked in ascending order (one, in a prefill or a training batch), 32 ranks at
+// walked in ascending order (one, in a prefill or a training batch), 32 NS ranks at
 // a step: the rows' h goes to LDS split into two bf16 parts, once for all waves,
-// with the adapter's 32 ranks of the tile's columns beside it, and every block
-// takes two matrix instructions. Products are added through a select by row, so
-// no value of one adapter (an infinity or a NaN in it among them) reaches a row
-// of another.
+// with the adapter's ranks of the tile's columns beside it, and every block takes
+// two matrix instructions for 32 ranks. Products are added through a select by
+// row, so no value of one adapter (an infinity or a NaN in it among them) reaches
+// a row of another.
 // KMAJOR: W is [L, R, N] (contraction rows) and block j's column is col0 + TJ r
 // + j; else W is [L, N, R] and the column is col0 + 16 j + r.
-template <int BM, int BN, bool KMAJOR>
-struct LoraLds {
-  static constexpr int H = BM * 128;                         // rows of 32 high, 32 low parts
-  static constexpr int W = KMAJOR ? 32 * BN * 2 : BN * 64;   // 32 ranks of BN columns
-  static constexpr int IDS = BM * 4;                         // the rows' adapters
-  static constexpr int BYTES = H + W + 2 * IDS + 16;         // the distinct ones, their number
+
+// The tile's adapters in LDS, found before the main loop, under its first loads.
+template <int BM>
+struct LoraRows {
+  int ids[BM];   // of the rows, -1: none
+  int list[BM];  // the distinct ones, ascending
+  int count;
 };
 
-// smem: LoraLds<BM, BN, KMAJOR>::BYTES bytes that nothing uses once every wave
-// of the workgroup's NT threads has entered. The wave's blocks begin at row row0
-// and column col0 of the tile. The accumulators are touched in one counted loop
-// without branches around them: in loops that leave early or skip blocks the
-// compiler keeps a second copy of them, in scratch memory.
-template <int BM, int BN, int NT, bool KMAJOR, int TI, int TJ>
-__device__ __forceinline__ void lora_add_tile(char *smem, f32x4 (&acc)[TI][TJ], const LoraTerm &t,
-                                              int64_t m0, int64_t M, int64_t n0, int row0,
-                                              int col0) {
-  using S = LoraLds<BM, BN, KMAJOR>;
-  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
-  int *ids = reinterpret_cast<int *>(smem + S::H + S::W), *list = ids + BM, *count = list + BM;
-  auto hswz = [](int row) { return (row >> 1) & 7; };
-  auto wswz = [](int row) { return (row >> 2) & 3; };
-  __syncthreads();
-  for (int i = tid; i < BM; i += NT) ids[i] = m0 + i < M ? t.idx[m0 + i] : -1;
+template <int BM, int NT>
+__device__ __forceinline__ void lora_rows(LoraRows<BM> &s, const LoraTerm &t, int64_t m0,
+                                          int64_t M) {
+  const int tid = threadIdx.x;
+  for (int i = tid; i < BM; i += NT) s.ids[i] = m0 + i < M ? t.idx[m0 + i] : -1;
   __syncthreads();
   if (tid < 64) {
     int n = 0;
     for (int prev = -1;; ++n) {
       int next = 0x7fffffff;
-      for (int i = lane; i < BM; i += 64) {
-        const int v = ids[i];
+      for (int i = tid; i < BM; i += 64) {
+        const int v = s.ids[i];
         next = v > prev && v < next ? v : next;
       }
 #pragma unroll
@@ -225,108 +215,141 @@ __device__ __forceinline__ void lora_add_tile(char *smem, f32x4 (&acc)[TI][TJ], 
       }
       prev = __builtin_amdgcn_readfirstlane(next);
       if (prev == 0x7fffffff) break;
-      if (lane == 0) list[n] = prev;
+      if (tid == 0) s.list[n] = prev;
     }
-    if (lane == 0) *count = n;
+    if (tid == 0) s.count = n;
   }
+}
+
+template <int BM, int BN, bool KMAJOR, int NS>
+struct LoraLds {
+  static constexpr int H = BM * 128;                        // rows of 32 high, 32 low parts
+  static constexpr int W = KMAJOR ? 32 * BN * 2 : BN * 64;  // 32 ranks of BN columns
+  static constexpr int BYTES = NS * (H + W);
+};
+
+// smem: LoraLds<BM, BN, KMAJOR, NS>::BYTES bytes that nothing uses once every
+// wave of the workgroup's NT threads has entered; lora_rows has filled s. The wave's
+// blocks begin at row row0 and column col0 of the tile. The accumulators are touched
+// in one counted loop without branches around them: in loops that leave early or
+// skip blocks the compiler keeps a second copy of them, in scratch memory.
+template <int BM, int BN, int NT, bool KMAJOR, int NS, int TI, int TJ>
+__device__ __forceinline__ void lora_add_tile(char *smem, const LoraRows<BM> &s,
+                                              f32x4 (&acc)[TI][TJ], const LoraTerm &t, int64_t m0,
+                                              int64_t n0, int row0, int col0) {
+  using S = LoraLds<BM, BN, KMAJOR, NS>;
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  auto hswz = [](int row) { return (row >> 1) & 7; };
+  auto wswz = [](int row) { return (row >> 2) & 3; };
   __syncthreads();
-  const int nc = (t.R + 31) / 32;
-  const int steps = __builtin_amdgcn_readfirstlane(*count) * nc;
-  __syncthreads();  // read by every wave: without an adapter the caller goes on at once
+  const int nc = (t.R + 32 * NS - 1) / (32 * NS);
+  const int steps = __builtin_amdgcn_readfirstlane(s.count) * nc;
   for (int q = 0; q < steps; ++q) {
-    const int a = __builtin_amdgcn_readfirstlane(list[q / nc]);
-    const int c = q % nc * 32;
+    const int a = __builtin_amdgcn_readfirstlane(s.list[q / nc]);
+    const int c0 = q % nc * (32 * NS);
     // both operands' loads are out before the first is used
     constexpr int TH = BM * 4, NH = (TH + NT - 1) / NT, NW = S::W / 16 / NT;
     static_assert((NH == 1 || NH * NT == TH) && NW * NT == S::W / 16, "staged evenly");
-    f32x4 hv[NH][2];
-    i32x4 wv[NW];
+    f32x4 hv[NS][NH][2];
+    i32x4 wv[NS][NW];
 #pragma unroll
-    for (int i = 0; i < NH; ++i) {  // a row's ranks c + 8 k .. + 7
-      const int u = tid + NT * i, row = u >> 2, k = u & 3;
-      hv[i][0] = hv[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (u < TH && ids[row] == a && c + 8 * k < t.R) {  // whole chunks: R is a multiple of 8
-        const float *h = t.h + (m0 + row) * t.R + c + 8 * k;
-        hv[i][0] = *reinterpret_cast<const f32x4 *>(h);
-        hv[i][1] = *reinterpret_cast<const f32x4 *>(h + 4);
+    for (int b = 0; b < NS; ++b) {
+      const int c = c0 + 32 * b;
+#pragma unroll
+      for (int i = 0; i < NH; ++i) {  // a row's ranks c + 8 k .. + 7
+        const int u = tid + NT * i, row = u >> 2, k = u & 3;
+        hv[b][i][0] = hv[b][i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (u < TH && s.ids[row] == a && c + 8 * k < t.R) {  // whole chunks of 8 ranks
+          const float *h = t.h + (m0 + row) * t.R + c + 8 * k;
+          hv[b][i][0] = *reinterpret_cast<const f32x4 *>(h);
+          hv[b][i][1] = *reinterpret_cast<const f32x4 *>(h + 4);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        const int u = tid + NT * i;
+        wv[b][i] = i32x4{0, 0, 0, 0};
+        if constexpr (KMAJOR) {
+          const int j = u / (BN / 8), k = u % (BN / 8);  // rank c + j, columns 8 k .. + 7
+          if (c + j < t.R && n0 + 8 * k < t.N)  // whole chunks: N is a multiple of 8
+            wv[b][i] = *reinterpret_cast<const i32x4 *>(
+                t.W + ((int64_t)a * t.R + c + j) * t.N + n0 + 8 * k);
+        } else {
+          const int row = u >> 2, k = u & 3;  // column n0 + row, ranks c + 8 k .. + 7
+          if (c + 8 * k < t.R && n0 + row < t.N)
+            wv[b][i] = *reinterpret_cast<const i32x4 *>(
+                t.W + ((int64_t)a * t.N + n0 + row) * t.R + c + 8 * k);
+        }
       }
     }
 #pragma unroll
-    for (int i = 0; i < NW; ++i) {
-      const int u = tid + NT * i;
-      wv[i] = i32x4{0, 0, 0, 0};
-      if constexpr (KMAJOR) {
-        const int j = u / (BN / 8), k = u % (BN / 8);  // rank c + j, columns 8 k .. + 7
-        if (c + j < t.R && n0 + 8 * k < t.N)  // whole chunks: N is a multiple of 8
-          wv[i] = *reinterpret_cast<const i32x4 *>(t.W + ((int64_t)a * t.R + c + j) * t.N + n0 +
-                                                   8 * k);
-      } else {
-        const int row = u >> 2, k = u & 3;  // column n0 + row, ranks c + 8 k .. + 7
-        if (c + 8 * k < t.R && n0 + row < t.N)
-          wv[i] = *reinterpret_cast<const i32x4 *>(t.W + ((int64_t)a * t.N + n0 + row) * t.R + c +
-                                                   8 * k);
-      }
-    }
+    for (int b = 0; b < NS; ++b) {
+      char *hs = smem + b * (S::H + S::W);
 #pragma unroll
-    for (int i = 0; i < NH; ++i) {
-      const int u = tid + NT * i, row = u >> 2, k = u & 3;
-      const float v[8] = {hv[i][0][0], hv[i][0][1], hv[i][0][2], hv[i][0][3],
-                          hv[i][1][0], hv[i][1][1], hv[i][1][2], hv[i][1][3]};
-      bf16x8 hi, lo;
-      split_bf16(v, hi, lo);
-      if (u < TH) {
-        *reinterpret_cast<bf16x8 *>(smem + row * 128 + 16 * (k ^ hswz(row))) = hi;
-        *reinterpret_cast<bf16x8 *>(smem + row * 128 + 16 * ((4 + k) ^ hswz(row))) = lo;
+      for (int i = 0; i < NH; ++i) {
+        const int u = tid + NT * i, row = u >> 2, k = u & 3;
+        const f32x4 v0 = hv[b][i][0], v1 = hv[b][i][1];
+        const float v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+        bf16x8 hi, lo;
+        split_bf16(v, hi, lo);
+        if (u < TH) {
+          *reinterpret_cast<bf16x8 *>(hs + row * 128 + 16 * (k ^ hswz(row))) = hi;
+          *reinterpret_cast<bf16x8 *>(hs + row * 128 + 16 * ((4 + k) ^ hswz(row))) = lo;
+        }
       }
-    }
 #pragma unroll
-    for (int i = 0; i < NW; ++i) {
-      const int u = tid + NT * i, row = u >> 2, k = u & 3;
-      *reinterpret_cast<i32x4 *>(smem + S::H +
-                                 (KMAJOR ? 16 * u : row * 64 + 16 * (k ^ wswz(row)))) = wv[i];
+      for (int i = 0; i < NW; ++i) {
+        const int u = tid + NT * i, row = u >> 2, k = u & 3;
+        *reinterpret_cast<i32x4 *>(hs + S::H + (KMAJOR ? 16 * u : row * 64 + 16 * (k ^ wswz(row)))) =
+            wv[b][i];
+      }
     }
     __syncthreads();
-    bf16x8 w[TJ];
-    if constexpr (KMAJOR) {
-      static_assert(!KMAJOR || TJ == 4, "four columns a lane");
-      i32x2 d[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        d[e] = *reinterpret_cast<const i32x2 *>(smem + S::H + (8 * g + e) * BN * 2 +
-                                                2 * (col0 + 4 * r));
+    for (int b = 0; b < NS; ++b) {
+      const char *hs = smem + b * (S::H + S::W);
+      bf16x8 w[TJ];
+      if constexpr (KMAJOR) {
+        static_assert(!KMAJOR || TJ == 4, "four columns a lane");
+        i32x2 d[8];
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        i32x4 v;
+        for (int e = 0; e < 8; ++e)
+          d[e] = *reinterpret_cast<const i32x2 *>(hs + S::H + (8 * g + e) * BN * 2 +
+                                                  2 * (col0 + 4 * r));
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          v[e] = (int)__builtin_amdgcn_perm((uint32_t)d[2 * e + 1][j >> 1],
-                                            (uint32_t)d[2 * e][j >> 1],
-                                            j & 1 ? 0x07060302u : 0x05040100u);
-        w[j] = __builtin_bit_cast(bf16x8, v);
+        for (int j = 0; j < TJ; ++j) {
+          i32x4 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] = (int)__builtin_amdgcn_perm((uint32_t)d[2 * e + 1][j >> 1],
+                                              (uint32_t)d[2 * e][j >> 1],
+                                              j & 1 ? 0x07060302u : 0x05040100u);
+          w[j] = __builtin_bit_cast(bf16x8, v);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+          const int row = col0 + 16 * j + r;
+          w[j] = *reinterpret_cast<const bf16x8 *>(hs + S::H + row * 64 + 16 * (g ^ wswz(row)));
+        }
       }
-    } else {
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        const int row = col0 + 16 * j + r;
-        w[j] = *reinterpret_cast<const bf16x8 *>(smem + S::H + row * 64 + 16 * (g ^ wswz(row)));
+      for (int i = 0; i < TI; ++i) {
+        const i32x4 id = *reinterpret_cast<const i32x4 *>(s.ids + row0 + 16 * i + 4 * g);
+        const int row = row0 + 16 * i + r;
+        const bf16x8 hi = *reinterpret_cast<const bf16x8 *>(hs + row * 128 + 16 * (g ^ hswz(row)));
+        const bf16x8 lo =
+            *reinterpret_cast<const bf16x8 *>(hs + row * 128 + 16 * ((4 + g) ^ hswz(row)));
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+          f32x4 d = {0.f, 0.f, 0.f, 0.f};
+          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[j], d, 0, 0, 0);
+          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[j], d, 0, 0, 0);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[i][j][v] += id[v] == a ? d[v] : 0.0f;
+        }
+        __builtin_amdgcn_sched_barrier(0);  // one block's operands at a time
       }
-    }
-#pragma unroll
-    for (int i = 0; i < TI; ++i) {
-      const i32x4 id = *reinterpret_cast<const i32x4 *>(ids + row0 + 16 * i + 4 * g);
-      const int row = row0 + 16 * i + r;
-      const bf16x8 hi = *reinterpret_cast<const bf16x8 *>(smem + row * 128 + 16 * (g ^ hswz(row)));
-      const bf16x8 lo =
-          *reinterpret_cast<const bf16x8 *>(smem + row * 128 + 16 * ((4 + g) ^ hswz(row)));
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        f32x4 d = {0.f, 0.f, 0.f, 0.f};
-        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[j], d, 0, 0, 0);
-        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[j], d, 0, 0, 0);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][j][v] += id[v] == a ? d[v] : 0.0f;
-      }
-      __builtin_amdgcn_sched_barrier(0);  // one block's operands at a time
     }
     __syncthreads();
   }

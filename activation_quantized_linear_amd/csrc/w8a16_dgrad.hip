@@ -83,7 +83,7 @@ struct DgradLds {
   static constexpr int TILEF = BM * TLDF * 4;
   static constexpr int BYTES = RING > TILE ? RING : TILE;
   static constexpr int BYTES_SPLIT = RING > TILEF ? RING : TILEF;
-  static_assert(BYTES >= LoraLds<BM, BK, true>::BYTES, "the adapter terms stage in the ring");
+  static_assert(BYTES >= LoraLds<BM, BK, true, 2>::BYTES, "the adapter terms stage in the ring");
   static_assert(NX * NWV * 8 == BM && NQ * NWV * 1024 == BC * BK, "loads split evenly");
   static_assert(NL * (SG - 2) < 64, "vmcnt");
 };
@@ -225,6 +225,7 @@ __global__ __launch_bounds__(64 * NWV, 2) void k_w8a16_dgrad(
   std::integral_constant<int, 0> h0;
   std::integral_constant<int, 1> h1;
   constexpr int SLOTS = TI * TJ;  // matrix instructions in a half
+  LoraRows<BM> &adapters = *reinterpret_cast<LoraRows<BM> *>(smem + L::BYTES);
 
   if (nk > 0) {
 #pragma unroll
@@ -235,6 +236,7 @@ __global__ __launch_bounds__(64 * NWV, 2) void k_w8a16_dgrad(
       static_for<0, NQ>([&](auto ii) { load_w(rq, s, ii); });
       next_w();
     }
+    if constexpr (LT::on) lora_rows<BM, 64 * NWV>(adapters, lt, m0, M);
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(NL * (SG - 2)));
     __builtin_amdgcn_s_barrier();  // stage 0 complete everywhere
 #pragma unroll
@@ -331,7 +333,8 @@ __global__ __launch_bounds__(64 * NWV, 2) void k_w8a16_dgrad(
     return;
   }
   if constexpr (LT::on) {
-    lora_add_tile<BM, BK, 64 * NWV, true>(smem, acc, lt, m0, M, k0, 0, 64 * wave);
+    if (nk == 0) lora_rows<BM, 64 * NWV>(adapters, lt, m0, M);
+    lora_add_tile<BM, BK, 64 * NWV, true, 2>(smem, adapters, acc, lt, m0, k0, 0, 64 * wave);
   }
   uint16_t *tl = reinterpret_cast<uint16_t *>(smem);
 #pragma unroll
@@ -403,16 +406,17 @@ struct Call {
 template <int TI, int SG, class LT>
 hipError_t go(const Call &c, const LT &lt) {
   using L = DgradLds<TI, SG>;
+  constexpr int bytes = L::BYTES + (LT::on ? sizeof(LoraRows<L::BM>) : 0);
   static bool attr_set = false;
   if (!attr_set) {  // more than 64 KB of dynamic LDS; a launch the limit refuses reports itself
     (void)hipFuncSetAttribute((const void *)k_w8a16_dgrad<TI, SG, false, LT>,
-                              hipFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     (void)hipGetLastError();
     attr_set = true;
   }
   const int tm = (int)((c.M + L::BM - 1) / L::BM), tk = (int)((c.K + L::BK - 1) / L::BK);
   hipLaunchKernelGGL((k_w8a16_dgrad<TI, SG, false, LT>), dim3((unsigned)(tm * tk)), dim3(64 * NWV),
-                     L::BYTES, c.st, c.d, c.ex, c.q, c.dx, c.M, c.N, c.NP, c.K, tm, tk,
+                     bytes, c.st, c.d, c.ex, c.q, c.dx, c.M, c.N, c.NP, c.K, tm, tk,
                      (float *)nullptr, 0, lt);
   return hipGetLastError();
 }

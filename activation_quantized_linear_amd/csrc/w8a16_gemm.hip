@@ -98,7 +98,7 @@ struct GemmLds {
   static constexpr int TILE = BM * TLD * 2;
   static constexpr int BYTES = RING > XCH + TILE ? RING : XCH + TILE;
   static_assert(NXL * NG == BM / 8 && NWL * NG == 8, "load slots split evenly");
-  static_assert(BYTES >= LoraLds<BM, BN, false>::BYTES, "the adapter terms stage in the ring");
+  static_assert(BYTES >= LoraLds<BM, BN, false, 2>::BYTES, "the adapter terms stage in the ring");
   static_assert(SG % KP == 0 && PS >= 3, "ring of whole steps, one read ahead");
 };
 
@@ -239,6 +239,8 @@ __global__ __launch_bounds__((64 * GemmLds<WM, TI, SG, KP>::NW)) void k_w8a16_ge
   const int ns = (int)((K + KP * BK - 1) / (KP * BK));
 #pragma unroll
   for (int t = 0; t < PS - 1; ++t) issue(t, t);
+  LoraRows<BM> &adapters = *reinterpret_cast<LoraRows<BM> *>(smem + L::BYTES);
+  if constexpr (LT::on) lora_rows<BM, 64 * NW>(adapters, lt, m0, M);
   Frag cur, nxt;
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(NL * (PS - 2)));
   __builtin_amdgcn_s_barrier();  // step 0 complete everywhere
@@ -321,7 +323,8 @@ __global__ __launch_bounds__((64 * GemmLds<WM, TI, SG, KP>::NW)) void k_w8a16_ge
       }
     }
     // (the other partners' accumulators take part and are dropped)
-    lora_add_tile<BM, BN, 64 * NW, false>(smem, acc, lt, m0, M, n0, wm * 16 * TI, wn * 64);
+    lora_add_tile<BM, BN, 64 * NW, false, 2>(smem, adapters, acc, lt, m0, n0, wm * 16 * TI,
+                                             wn * 64);
     if (part == 0) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -389,7 +392,8 @@ struct WideLds {
   static constexpr int TLD = BNW + 8;           // bf16 per staged output row
   static constexpr int TILE = BM * TLD * 2;
   static constexpr int BYTES = RING > TILE ? RING : TILE;
-  static_assert(BYTES >= LoraLds<BM, BNW, false>::BYTES, "the adapter terms stage in the ring");
+  static constexpr int NS = SG == 4 ? 2 : 1;    // 32-rank blocks of an adapter step
+  static_assert(BYTES >= LoraLds<BM, BNW, false, NS>::BYTES, "the adapter terms stage in the ring");
   static constexpr int TLDF = BNW + 4;          // fp32 per staged partial-sum row (split K)
   static constexpr int TILEF = BM * TLDF * 4;
   static constexpr int BYTES_SPLIT = RING > TILEF ? RING : TILEF;
@@ -523,6 +527,8 @@ __global__ __launch_bounds__(512, SG == 2 ? 4 : 2) void k_w8a16_gemm_wide(const 
   const int nk = SPLIT ? (k0 + ks < nk_all ? k0 + ks : nk_all) : nk_all;
 #pragma unroll
   for (int s = 0; s < SG - 1; ++s) issue(k0 + s);
+  LoraRows<BM> &adapters = *reinterpret_cast<LoraRows<BM> *>(smem + L::BYTES);
+  if constexpr (LT::on) lora_rows<BM, 512>(adapters, lt, m0, M);
   int kt = k0;
   auto step = [&](int k) {
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(NL * (SG - 2)));
@@ -600,7 +606,7 @@ __global__ __launch_bounds__(512, SG == 2 ? 4 : 2) void k_w8a16_gemm_wide(const 
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[i][j][v] = s * acc[i][j][v] + b;
     }
-    lora_add_tile<BM, BNW, 512, false>(smem, acc, lt, m0, M, n0, 0, wn * 32);
+    lora_add_tile<BM, BNW, 512, false, L::NS>(smem, adapters, acc, lt, m0, n0, 0, wn * 32);
   }
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -721,16 +727,17 @@ template <int SG, class LT>
 hipError_t launch_wide(const uint16_t *x, int64_t M, int64_t K, const int8_t *q, const float *scale,
                        const uint16_t *bias, int64_t N, uint16_t *y, hipStream_t st, const LT &lt) {
   using L = WideLds<SG>;
+  constexpr int bytes = L::BYTES + (LT::on ? sizeof(LoraRows<L::BM>) : 0);
   static bool attr_set = false;
   if (!attr_set) {  // more than 64 KB of dynamic LDS; a launch the limit refuses reports itself
     (void)hipFuncSetAttribute((const void *)k_w8a16_gemm_wide<SG, false, LT>,
-                              hipFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     (void)hipGetLastError();
     attr_set = true;
   }
   const int tiles_m = (int)((M + L::BM - 1) / L::BM), tiles_n = (int)((N + L::BNW - 1) / L::BNW);
   hipLaunchKernelGGL((k_w8a16_gemm_wide<SG, false, LT>), dim3((unsigned)(tiles_m * tiles_n)), dim3(512),
-                     L::BYTES, st, x, q, scale, bias, y, M, N, K, tiles_m, tiles_n, nullptr, 0, lt);
+                     bytes, st, x, q, scale, bias, y, M, N, K, tiles_m, tiles_n, nullptr, 0, lt);
   return hipGetLastError();
 }
 
@@ -763,16 +770,17 @@ template <int WM, int TI, int SG, int KP, bool RAG, class LT>
 hipError_t launch_wm_k(const uint16_t *x, int64_t M, int64_t K, const int8_t *q, const float *scale,
                        const uint16_t *bias, int64_t N, uint16_t *y, hipStream_t st, const LT &lt) {
   using L = GemmLds<WM, TI, SG, KP>;
+  constexpr int bytes = L::BYTES + (LT::on ? sizeof(LoraRows<L::BM>) : 0);
   static bool attr_set = false;
   if (!attr_set) {  // more than 64 KB of dynamic LDS; a launch the limit refuses reports itself
     (void)hipFuncSetAttribute((const void *)k_w8a16_gemm<WM, TI, SG, KP, RAG, LT>,
-                              hipFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     (void)hipGetLastError();
     attr_set = true;
   }
   const int tiles_m = (int)((M + L::BM - 1) / L::BM), tiles_n = (int)((N + BN - 1) / BN);
   hipLaunchKernelGGL((k_w8a16_gemm<WM, TI, SG, KP, RAG, LT>), dim3((unsigned)(tiles_m * tiles_n)),
-                     dim3(64 * L::NW), L::BYTES, st, x, q, scale, bias, y, M, N, K, tiles_m,
+                     dim3(64 * L::NW), bytes, st, x, q, scale, bias, y, M, N, K, tiles_m,
                      tiles_n, lt);
   return hipGetLastError();
 }
