@@ -640,10 +640,13 @@ def _lora_plan(plan, M, L, di):
     return _fit(plan.buffer, "plan.buffer", torch.uint8, plan.buffer.shape, di)
 
 
-def _lora_shape(A):
-    if not isinstance(A, torch.Tensor) or A.ndim != 3:
-        raise ValueError("A must be a [L, R, K] tensor")
-    return A.shape[0], A.shape[1]
+def _dims(t, name, ndim):
+    """t's sizes, before the check of the whole tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.ndim != ndim:
+        raise ValueError(f"{name} must be {ndim}-D, got shape {tuple(t.shape)}")
+    return t.shape
 
 
 def aql_lora_forward_bytes(M, N, K, L, R):
@@ -659,8 +662,8 @@ def aql_linear_w8a16_lora(x, q, scale, A, B, alpha, plan, bias=None, y=None, h=N
     aql_lora_forward_bytes; allocated here when one is needed and none is given."""
     di = _dev_index(x, "x", torch.bfloat16, 2)
     M, K = x.shape
-    N = q.shape[0]
-    L, R = _lora_shape(A)
+    N = _dims(q, "q", 2)[0]
+    L, R, _ = _dims(A, "A", 3)
     args = (x.data_ptr(), M, K, _fit(q, "q", torch.int8, (N, K), di),
             _fit(scale, "scale", torch.float32, (N,), di),
             None if bias is None else _fit(bias, "bias", torch.bfloat16, (N,), di), N,
@@ -682,7 +685,7 @@ def aql_linear_w8a16_dgrad(dy, q, scale, dx=None, workspace=None):
     of aql_workspace_bytes(AQL_OP_W8A16_DGRAD, M, N, K); allocated here when none is given."""
     di = _dev_index(dy, "dy", torch.bfloat16, 2)
     M, N = dy.shape
-    K = q.shape[-1]
+    K = _dims(q, "q", 2)[1]
     args = (dy.data_ptr(), M, N, _fit(q, "q", torch.int8, (N, K), di),
             _fit(scale, "scale", torch.float32, (N,), di), K)
     dev = dy.device
@@ -708,8 +711,8 @@ def aql_linear_w8a16_lora_backward(dy, q, scale, A, B, alpha, plan, h, xq, xs, d
     aql_lora_backward_bytes; allocated here when none is given."""
     di = _dev_index(dy, "dy", torch.bfloat16, 2)
     M, N = dy.shape
-    K = q.shape[-1]
-    L, R = _lora_shape(A)
+    K = _dims(q, "q", 2)[1]
+    L, R, _ = _dims(A, "A", 3)
     G = (K + AQL_CKPT_GROUP - 1) // AQL_CKPT_GROUP
     args = (dy.data_ptr(), M, N, _fit(q, "q", torch.int8, (N, K), di),
             _fit(scale, "scale", torch.float32, (N,), di), K,
@@ -744,6 +747,7 @@ def _act_dtype(dtype, name):
 def aql_act_checkpoint(x, xq=None, xs=None):
     """x float32 or bfloat16 [M, K] -> (xq int8 [M, K], xs float32 [M, ceil(K / 128)]):
     8-bit codes with one scale per 128 values of a row."""
+    _dims(x, "x", 2)
     dt = _act_dtype(x.dtype, "x")
     di = _dev_index(x, "x", x.dtype, 2)
     M, K = x.shape

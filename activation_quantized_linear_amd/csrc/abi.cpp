@@ -672,9 +672,9 @@ int aql_linear_w8a16_lora(const uint16_t *x, int64_t M, int64_t K, const int8_t 
   if (int e = check_w8a16(fn, x, M, K, q, scale, bias, N, y)) return e;
   if (int e = check_lora(fn, A, B, alpha, L, R, plan, h)) return e;
   REQUIRE(aligned16(ws), AQL_ERR_ALIGN, "%s: ws must be 16-byte aligned", fn);
-  if (M == 0 || N == 0) return ok();
-  REQUIRE(A && B && alpha && plan && h, AQL_ERR_NULL,
-          "%s: A, B, alpha, plan and h must not be NULL", fn);
+  if (M == 0) return ok();
+  REQUIRE(x && A && (B || N == 0) && alpha && plan && h, AQL_ERR_NULL,
+          "%s: x, A, B, alpha, plan and h must not be NULL", fn);
   const size_t need = ws_lora(M, N, K, L, R);
   REQUIRE(need == 0 || (ws && ws_bytes >= need), AQL_ERR_WORKSPACE,
           "%s: workspace needs %zu bytes (got %zu)", fn, need, ws ? ws_bytes : (size_t)0);
@@ -684,12 +684,12 @@ int aql_linear_w8a16_lora(const uint16_t *x, int64_t M, int64_t K, const int8_t 
   float *part = static_cast<float *>(ws);
   const size_t pb = ws ? ws_bytes : 0;
   aql::LoraTerm lt{h, B, p + aql::lora_plan_layout(M, L).idx, (int32_t)R, N};
-  if (M < kW8A16GemmMinM && aql::w8a16_skinny_splits(M, N, K) > 1) {
+  if (N > 0 && M < kW8A16GemmMinM && aql::w8a16_skinny_splits(M, N, K) > 1) {
     lt.A = A;  // the launch of the splits computes h beside them
     lt.alpha = alpha;
   } else {
     const hipError_t e = aql::launch_lora_shrink(x, M, K, A, alpha, L, R, p, h, part, st);
-    if (e != hipSuccess) return launched(e, fn);
+    if (e != hipSuccess || N == 0) return launched(e, fn);
   }
   // the same M-dispatch as aql_linear_w8a16
   if (M >= kW8A16GemmMinM && K <= (1LL << 22))

@@ -1,5 +1,5 @@
 // Activation checkpoints in 8 bits: per row and group of 128 columns
-//   s = max |x| / 127 (1 where that is not positive), code = clamp(rint(x / s), -127, 127)
+//   s = max |x| / 127 (1 where that is 0), code = clamp(rint(x / s), -127, 127)
 // and back, x' = code * s. One pass over the data each way, bound by memory:
 // 3 bytes a value (bf16) plus 4 bytes a group.
 //
@@ -18,17 +18,21 @@ constexpr int kIlp = 4;  // groups in flight for 16 lanes
 constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
 
 template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-  const int i = (int)__float_as_uint(v);
-  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(i, i, CTRL, 0xf, 0xf, false));
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xf, 0xf, false);
 }
 
-// The maximum over a row of 16 lanes, in every lane.
-__device__ __forceinline__ float max16(float v) {
-  v = fmaxf(v, dpp<kDppXor1>(v));
-  v = fmaxf(v, dpp<kDppXor2>(v));
-  v = fmaxf(v, dpp<kDppHalfMirror>(v));
-  return fmaxf(v, dpp<kDppMirror>(v));
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// The maximum over a row of 16 lanes, in every lane. Magnitudes are compared as
+// their bits, which order like the values and put a NaN above an infinity, so a
+// group with either gets a scale that is none and does not restore as if it held
+// numbers.
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  v = umax(v, dpp<kDppXor1>(v));
+  v = umax(v, dpp<kDppXor2>(v));
+  v = umax(v, dpp<kDppHalfMirror>(v));
+  return umax(v, dpp<kDppMirror>(v));
 }
 
 // n (8, 4 or 0) values from element i on; the others zero.
@@ -109,12 +113,11 @@ __global__ __launch_bounds__(256) void k_act_checkpoint(const void *__restrict__
   float mine = 1.0f;  // lane u keeps group t0 + u's scale
 #pragma unroll
   for (int u = 0; u < kIlp; ++u) {
-    float mx = 0.0f;
+    uint32_t mx = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[u][e]));
-    mx = max16(mx);
-    float s = mx / 127.0f;
-    s = s > 0.0f ? s : 1.0f;
+    for (int e = 0; e < 8; ++e) mx = umax(mx, __float_as_uint(v[u][e]) & 0x7fffffffu);
+    float s = __uint_as_float(max16(mx)) / 127.0f;
+    s = s == 0.0f ? 1.0f : s;
     if (l == u) mine = s;
     uint32_t w[2] = {0, 0};
     // scales from 2^-100 to 2^100 have a normal reciprocal

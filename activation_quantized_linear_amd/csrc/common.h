@@ -27,11 +27,11 @@ __device__ __forceinline__ float clamp_code(float v, float lo, float hi) {
   return fminf(fmaxf(v, lo), hi);
 }
 
-// float -> bf16 bit pattern, round to nearest even (finite inputs).
+// float -> bf16 bit pattern, round to nearest even, subnormals kept, any NaN a
+// NaN (the hardware's conversion; adding half a step to the bits would carry a
+// NaN whose payload is all ones over to zero).
 __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
-  uint32_t u = __float_as_uint(f);
-  u += 0x7fffu + ((u >> 16) & 1u);
-  return (uint16_t)(u >> 16);
+  return __builtin_bit_cast(uint16_t, (__bf16)f);
 }
 
 __device__ __forceinline__ float bf16_to_f32(uint16_t h) {

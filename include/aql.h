@@ -357,7 +357,9 @@ int aql_linear_w8a16_grouped(const void *table, const void *dev_table, void *str
  *   dA[a][j, k] = sum_{m: idx[m] = a} u[m, j] x'[m, k]
  * where x' is x as its 8-bit checkpoint holds it (below). alpha is not trained.
  * A value of one adapter, or a row of one request, never reaches the rows and
- * gradients of another, whatever it holds.
+ * gradients of another, whatever it holds. Where an infinity or a NaN enters a
+ * result, the result is not finite, but which of the two it is does not follow
+ * the formula (float32 factors enter as sums of parts).
  *
  * The plan. aql_lora_plan sorts a batch's rows by adapter into
  * aql_lora_plan_bytes(M, L) bytes of device memory. Every layer's linears and
@@ -386,8 +388,7 @@ int aql_lora_plan(const int32_t *idx, int64_t M, int64_t L, void *plan, size_t p
  *           NULL where that is 0)
  * Errors: as aql_linear_w8a16, plus R not a multiple of 8 in
  * 8..AQL_LORA_MAX_RANK, L outside 1..AQL_LORA_MAX_ADAPTERS, NULL or misaligned
- * A, B, alpha, plan or h, workspace too small. N == 0 launches nothing and
- * leaves h as it was.
+ * A, B, alpha, plan or h, workspace too small. N == 0 writes h alone.
  */
 size_t aql_lora_forward_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
 int aql_linear_w8a16_lora(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
@@ -444,9 +445,10 @@ int aql_linear_w8a16_lora_backward(const uint16_t *dy, int64_t M, int64_t N, con
 /*
  * Activations kept for a backward pass in 8 bits, with one scale for each 128
  * values of a row (a row's last group may be shorter): s = max |x| / 127 in
- * binary32, 1 where that is not positive; code = clamp(round(x / s), -127, 127),
- * the quotient in binary32. Restored values are code * s. A channel that runs
- * hot costs its own group precision, not the row.
+ * binary32, 1 where that is 0; code = clamp(round(x / s), -127, 127), the
+ * quotient in binary32. Restored values are code * s. A channel that runs
+ * hot costs its own group precision, not the row; a group that holds a NaN or an
+ * infinity restores without a finite value.
  *
  *   x   device, [M, K] float32 (dtype AQL_F32) or bf16 (AQL_BF16)
  *   xq  device, [M, K] int8;  xs  device, [M, ceil(K / 128)] float32

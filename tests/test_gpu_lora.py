@@ -352,6 +352,80 @@ def test_dgrad_of_rows_of_any_size():
     close(dx, ref, 2.0 ** -8 * ref.abs() + (N + 4) * U * T + off + tiny, "dx")
 
 
+def test_dgrad_keeps_what_is_not_finite():
+    """NaN of any payload and infinities in dy's rows, or in a scale, reach every dx
+    they enter, and no other row."""
+    for M, N, K in ((40, 264, 320), (600, 256, 16640)):
+        c = make(M, K, N, 1, 8, "0")
+        c["q"][c["q"] == 0] = 1
+        d = dev(c)
+        dx0 = aql.aql_linear_w8a16_dgrad(d["dy"], d["q"], d["scale"])
+        d["dy"][3, 7], d["dy"][17, 200], d["dy"][M - 1, N - 1] = float("nan"), float("inf"), 1e38
+        d["dy"].view(torch.int16)[5, 0] = 2 ** 15 - 1
+        d["dy"].view(torch.int16)[6, 1] = -1
+        d["dy"][20, :] = 0.0
+        dx1 = aql.aql_linear_w8a16_dgrad(d["dy"], d["q"], d["scale"])
+        bad = torch.zeros(M, dtype=torch.bool, device=DEV)
+        bad[torch.tensor([3, 5, 6, 17], device=DEV)] = True
+        assert not torch.isfinite(dx1[bad]).any()
+        assert torch.isfinite(dx1[~bad]).all() and not dx1[20].any()
+        same = ~bad
+        same[20] = same[M - 1] = False
+        assert torch.equal(dx0[same], dx1[same])
+        for payload in (0x7fffffff, -1, 0x7f800001):
+            d["scale"].view(torch.int32)[9] = payload
+            assert torch.isnan(aql.aql_linear_w8a16_dgrad(d["dy"], d["q"], d["scale"])).all()
+
+
+@pytest.mark.parametrize("M", [1, 5, 30, 100, 700])
+def test_forward_keeps_what_is_not_finite(M):
+    """A NaN of any payload in a row of x, in a scale or in alpha shows in every output."""
+    c = make(M, 1024, 520, 3, 16, "runs")
+    c["q"][c["q"] == 0] = 1
+    for name, dt, payloads in (("x", torch.int16, (0x7fff, -1, 0x7f81)),
+                               ("scale", torch.int32, (0x7fffffff, -1, 0x7f800001)),
+                               ("alpha", torch.int32, (0x7fffffff, -1, 0x7f800001))):
+        for p in payloads:
+            d = dev(c)
+            d[name].view(dt).view(-1)[0] = p
+            y, h, _ = forward(d)
+            torch.cuda.synchronize()
+            if name == "scale":
+                assert torch.isnan(y[:, 0]).all() and torch.isfinite(y[:, 1:]).all()
+            else:
+                rows = torch.zeros(M, dtype=torch.bool, device=DEV)
+                rows[0 if name == "x" else slice(None)] = True
+                if name == "alpha":
+                    rows = d["idx"] == 0
+                assert torch.isnan(y[rows]).all() and torch.isfinite(y[~rows]).all()
+                assert torch.isnan(h[rows]).all() and torch.isfinite(h[~rows]).all()
+
+
+def test_two_streams_share_a_plan():
+    """Forward and backward of two layers on two streams at once, one plan."""
+    c1, c2 = make(90, 2560, 960, 3, 16, "random", seed=1), make(90, 960, 2560, 3, 16, "random", seed=2)
+    c2["idx"] = c1["idx"]
+    ds = [dev(c1), dev(c2)]
+    plan = aql.aql_lora_plan(ds[0]["idx"], 3)
+
+    def step(d):
+        y, h, _ = forward(d, plan)
+        xq, xs = aql.aql_act_checkpoint(d["x"])
+        return (y, h, *backward(d, plan, h, xq, xs))
+
+    want = [step(d) for d in ds]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ds]
+    got = [None, None]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = step(ds[i])
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(a, b) for a, b in zip(w, g))
+
+
 def test_backward_accumulates_and_leaves_out():
     c = make(100, 256, 136, 4, 16, "runs")
     c["idx"][c["idx"] == 2] = 1  # adapter 2: no rows
@@ -448,6 +522,29 @@ def test_checkpoint_past_32_bits():
         q1, s1 = aql.aql_act_checkpoint(x[r:r + 3].clone())
         assert torch.equal(xq[r:r + 3], q1) and torch.equal(xs[r:r + 3], s1)
         assert torch.equal(back[r:r + 3], aql.aql_act_restore(q1, s1))
+
+
+def test_checkpoint_of_values_that_are_no_numbers():
+    """A group with a NaN (of any payload) or an infinity restores without a finite
+    value; every other group restores as without it."""
+    for dt in (torch.float32, torch.bfloat16):
+        x = workloads.randn(workloads.gen(4), 9, 400).to(dt)
+        q0, s0 = aql.aql_act_checkpoint(x.to(DEV))
+        b0, f0 = aql.aql_act_restore(q0, s0), aql.aql_act_restore(q0, s0, torch.float32)
+        x[1, 5], x[2, 200], x[3, 399] = float("nan"), float("inf"), float("-inf")
+        x[4, 128:256] = float("inf")
+        i = x.view(torch.int32 if dt == torch.float32 else torch.int16)
+        i[5, 0], i[6, 390] = (2 ** 31 - 1, -1) if dt == torch.float32 else (2 ** 15 - 1, -1)
+        q1, s1 = aql.aql_act_checkpoint(x.to(DEV))
+        b1, f1 = aql.aql_act_restore(q1, s1), aql.aql_act_restore(q1, s1, torch.float32)
+        torch.cuda.synchronize()
+        bad = torch.zeros(9, 512, dtype=torch.bool)
+        for m, g in ((1, 0), (2, 1), (3, 3), (4, 1), (5, 0), (6, 3)):
+            bad[m, 128 * g:128 * (g + 1)] = True
+        bad = bad[:, :400].to(DEV)
+        for v0, v1 in ((b0, b1), (f0, f1)):
+            assert not torch.isfinite(v1[bad]).any()
+            assert torch.equal(v0[~bad], v1[~bad])
 
 
 # ------------------------------------------------------------------- together
@@ -573,3 +670,10 @@ def test_empty_batches():
     xq, xs = aql.aql_act_checkpoint(d["x"])
     dx, dA, dB = backward(d, plan, torch.zeros(5, 8, device=DEV), xq, xs)
     assert not dx.any() and not dA.any() and dB.shape == (2, 0, 8)
+    for M, K in ((5, 64), (20, 8192), (100, 512), (100, 8192)):  # h has a value all the same
+        c = make(M, K, 0, 2, 8, "runs")
+        y, h, _ = forward(dev(c))
+        torch.cuda.synchronize()
+        _, _, hr, htol = ref_forward(c)
+        assert y.shape == (M, 0)
+        close(h, hr, htol, "h")

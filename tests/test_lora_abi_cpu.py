@@ -78,7 +78,11 @@ def test_forward_workspace():
 def test_forward_empty():
     none = {k: None for k in ("x", "y", "h")}
     assert call(L.aql_linear_w8a16_lora, FWD, M=0, **none) == OK
-    assert call(L.aql_linear_w8a16_lora, FWD, N=0, q=None, scale=None, y=None, B=None) == OK
+    # no output channels: h is still to be computed
+    assert call(L.aql_linear_w8a16_lora, FWD, N=0, q=None, scale=None, y=None, B=None,
+                x=None) == NULL
+    assert call(L.aql_linear_w8a16_lora, FWD, N=0, q=None, scale=None, y=None, B=None,
+                h=None) == NULL
 
 
 DG = dict(dy=P, M=5, N=24, q=P, scale=P, K=64, dx=P, ws=P, ws_bytes=BIG, stream=None)
@@ -150,3 +154,17 @@ def test_binding_refuses_host_tensors():
         aql.aql_act_checkpoint(torch.zeros(4, 16))
     with pytest.raises(TypeError):
         aql.aql_act_checkpoint(torch.zeros(4, 16, dtype=torch.float16))
+
+
+def test_arguments_that_are_no_tensors():
+    x = torch.zeros(2, 16, dtype=torch.bfloat16)
+    for f in (lambda: aql.aql_act_checkpoint(None), lambda: aql.aql_act_restore(None, None),
+              lambda: aql.aql_lora_plan([0, 1], 2),
+              lambda: aql.aql_linear_w8a16_dgrad(None, None, None),
+              lambda: aql.aql_linear_w8a16_lora(None, *[None] * 6)):
+        with pytest.raises(TypeError):
+            f()
+    for f in (lambda: aql.aql_act_checkpoint(x), lambda: aql.aql_lora_plan(x[0].int(), 2),
+              lambda: aql.aql_linear_w8a16_dgrad(x, x, x)):
+        with pytest.raises(ValueError, match="device tensor"):
+            f()
