@@ -351,8 +351,11 @@ __global__ __launch_bounds__(256) void k_lora_shrink_sum(const float *__restrict
 // the contraction as their slow axis: lane (r, g) reads CW columns of the 8 rows
 // 8 g .. 8 g + 7 and turns the 8 x CW block in registers into the operands of CW
 // MFMAs, MFMA c covering columns CW r + c. The float32 operand (h, or u times
-// the row's scale) is split into three bf16 parts. The next step's loads are in
-// flight while one is multiplied.
+// the row's scale) is split into three bf16 parts. Loads in flight come from the
+// waves of a CU rather than from a step ahead in each, whose registers cost as
+// many waves. Bound by those round trips: 17 us for the 25 MB of M = 500, N = 4096,
+// K = 14336, R = 64, 3 adapters; 22 us, 3.1 TB/s, for M = 2048, N = 14336, K = 4096, R = 16.
+
 // a.lo16 | b.lo16 << 16 and the high halves
 __device__ __forceinline__ int pack_lo(int a, int b) {
   return (int)__builtin_amdgcn_perm((uint32_t)b, (uint32_t)a, 0x05040100u);
@@ -445,18 +448,13 @@ __device__ __forceinline__ void lora_wgrad(const LoraWgradArgs &p, const LoraPla
     }
   };
   int row[8];
-  Step cur, nxt;
   int p0 = first + 32 * wave;
-  if (p0 < last) {
-    rows_of(p0, row);
-    load(row, cur);
+  if (p0 < last) rows_of(p0, row);
+  for (; p0 < last; p0 += 32 * W) {
+    Step s;
+    load(row, s);
     rows_of(p0 + 32 * W, row);
-    for (; p0 < last; p0 += 32 * W) {
-      load(row, nxt);
-      rows_of(p0 + 64 * W, row);
-      multiply(cur);
-      cur = nxt;
-    }
+    multiply(s);
   }
   // the waves' sums meet pairwise
   f32x4 *red = reinterpret_cast<f32x4 *>(smem);
@@ -569,6 +567,8 @@ hipError_t go_shrink(const uint16_t *x, int64_t M, int64_t C, const uint16_t *A,
   return hipGetLastError();
 }
 
+constexpr int kWgradWaves = 2800;
+
 template <int W, int RT>
 hipError_t go_wgrad(const LoraWgradArgs &a, hipStream_t st) {
   constexpr int bytes = W / 2 * RT * 8 * 64 * 16;
@@ -624,12 +624,19 @@ hipError_t launch_lora_shrink_t(const uint16_t *dy, int64_t M, int64_t N, const 
 }
 
 hipError_t launch_lora_wgrad(const LoraWgradArgs &a, hipStream_t st) {
-  // 16 ranks a workgroup; 4 waves where an adapter's rows are few (they would
-  // have no second step), 32 ranks where the data read again per block of ranks
-  // would come to more than the caches hold
-  if (a.R > 16 && a.M > 1024) return go_wgrad<8, 2>(a, st);
-  if (a.M / a.L > 512) return go_wgrad<16, 1>(a, st);
-  return go_wgrad<4, 1>(a, st);
+  // long segments and several blocks of ranks: two of them share a read (M = 8192,
+  // 4 adapters, R = 64, N = K = 4096: 141 us of backward without dx, 150 apart)
+  if (a.R > 16 && a.M / a.L >= 1024) return go_wgrad<8, 2>(a, st);
+  // else the fewest waves a workgroup that make about 3 a SIMD in all: more of
+  // them only meet (M = 512, 16 adapters, R = 16, N = K = 4096: 15.4 us with 2, 18.2
+  // with 4), fewer leave the memory idle (M = 2048, N = 14336, K = 4096, one adapter:
+  // 37 us with 16, 45 with 4)
+  const int64_t units = ((a.dB ? (a.N + 63) / 64 : 0) + (a.dA ? (a.K + 127) / 128 : 0)) * a.L *
+                        ((a.R + 15) / 16);
+  if (2 * units >= kWgradWaves) return go_wgrad<2, 1>(a, st);
+  if (4 * units >= kWgradWaves) return go_wgrad<4, 1>(a, st);
+  if (8 * units >= kWgradWaves) return go_wgrad<8, 1>(a, st);
+  return go_wgrad<16, 1>(a, st);
 }
 
 }  // namespace aql

@@ -302,6 +302,7 @@ BACKWARD = [
     (130, 4096, 72, 3, 16, "random"), (257, 304, 200, 5, 48, "runs"), (500, 1024, 520, 3, 64, "runs"),
     (300, 80, 1048, 1, 16, "none"), (1000, 512, 640, 7, 128, "random"),
     (2100, 2560, 192, 2, 16, "runs"), (1100, 16384, 64, 1, 8, "0"), (33, 12288, 1032, 33, 8, "runs"),
+    (200, 4096, 1024, 8, 16, "runs"), (1100, 320, 136, 1, 40, "0"), (2200, 144, 72, 2, 128, "runs"),
 ]
 
 
