@@ -237,6 +237,10 @@ FORWARD = [
     (129, 1024, 264, 2, 128, "random"), (2048, 64, 2048, 5, 24, "runs"),
     (70, 64, 40960, 3, 16, "random"), (1024, 80, 16384, 2, 40, "runs"),
     (100, 8192, 72, 3, 16, "random"), (257, 8192, 1024, 1, 64, "0"), (150, 96, 64, 2, 16, "none"),
+    # rows that begin at any even address, in every tile form
+    (70, 64, 40957, 3, 16, "random"), (1024, 80, 16381, 2, 40, "runs"), (2048, 64, 2043, 1, 8, "0"),
+    (500, 64, 11005, 3, 16, "runs"), (77, 128, 6, 2, 8, "random"), (65, 64, 3, 1, 8, "0"),
+    (129, 64, 1, 1, 8, "0"),
 ]
 
 
