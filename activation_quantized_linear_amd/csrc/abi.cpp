@@ -184,20 +184,50 @@ static_assert(AQL_LORA_MAX_ADAPTERS == aql::kLoraMaxAdapters &&
                   AQL_LORA_MAX_RANK == aql::kLoraMaxRank && AQL_CKPT_GROUP == aql::kCkptGroup,
               "adapter bounds");
 
-// Workspace of the linear with adapters: the linear's own split-K partial sums,
-// and before them (the shrink is done first) the shrink's. One region serves both.
+// Bytes of the adapters' products [M, C] that a tiled kernel is given: where it
+// splits its contraction, all of them once there is much to add; else those of
+// groups that many adapters share, if there are as many.
+size_t lora_products_bytes(bool split, bool kmajor, int64_t M, int64_t C, int64_t L, int64_t R) {
+  const bool on = split ? aql::lora_split_products(kmajor, M, C, R) : L > aql::kLoraFew;
+  return on ? (size_t)M * (size_t)C * 4 : 0;
+}
+
+// Workspace of the linear with adapters: the linear's own split-K partial sums
+// and the adapters' products, and before them (the shrink is done first) the
+// shrink's partial sums in the same place.
+size_t lora_fwd_part_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M < kW8A16GemmMinM) return align256(aql::w8a16_skinny_part_bytes(M, N, K));
+  return K <= (1LL << 22) ? align256(aql::w8a16_gemm_part_bytes(M, N, K)) : 0;
+}
+size_t lora_fwd_products_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+  if (M < kW8A16GemmMinM || K > (1LL << 22)) return 0;
+  return lora_products_bytes(aql::w8a16_gemm_part_bytes(M, N, K) > 0, false, M, N, L, R);
+}
 size_t ws_lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
-  const size_t lin = M >= kW8A16GemmMinM ? (K <= (1LL << 22) ? aql::w8a16_gemm_part_bytes(M, N, K) : 0)
-                                         : aql::w8a16_skinny_part_bytes(M, N, K);
+  const size_t lin = lora_fwd_part_bytes(M, N, K) + lora_fwd_products_bytes(M, N, K, L, R);
   const size_t shr = M >= aql::kLoraTiledMinM ? aql::lora_shrink_bytes(M, K, L, R) : 0;
   return lin > shr ? lin : shr;
 }
 
-// Workspace of its backward pass: u [M, R], dx's, the shrink's partial sums.
+// Workspace of its backward pass: u [M, R], dx's, then the shrink's partial sums
+// and, once they are added, the adapters' products.
 size_t lora_bwd_u_bytes(int64_t M, int64_t R) { return align256((size_t)M * (size_t)R * 4); }
+size_t lora_bwd_products_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+  return lora_products_bytes(aql::w8a16_dgrad_split(M, N, K), true, M, K, L, R);
+}
 size_t ws_lora_bwd(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+  const size_t prod = lora_bwd_products_bytes(M, N, K, L, R);
+  const size_t shr = aql::lora_shrink_bytes(M, N, L, R);
   return lora_bwd_u_bytes(M, R) + align256(aql::w8a16_dgrad_bytes(M, N, K)) +
-         aql::lora_shrink_bytes(M, N, L, R);
+         (prod > shr ? prod : shr);
+}
+
+// The products of a tiled kernel's term, in T where there are any to be computed.
+hipError_t lora_products(aql::LoraTerm &lt, bool split, bool kmajor, int64_t M, int64_t L,
+                         const int32_t *p, float *T, hipStream_t st) {
+  lt.T = T;
+  lt.mixed = split ? nullptr : p + aql::lora_plan_layout(M, L).mixed;
+  return aql::launch_lora_products(lt.h, lt.W, kmajor, M, lt.N, L, lt.R, p, lt.mixed, T, st);
 }
 bool lora_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
   return plan_sizes_ok(M, L) && M > 0 && N >= 0 && K >= 16 && K <= kMaxKW8A16 && R >= 8 &&
@@ -692,8 +722,15 @@ int aql_linear_w8a16_lora(const uint16_t *x, int64_t M, int64_t K, const int8_t 
     if (e != hipSuccess || N == 0) return launched(e, fn);
   }
   // the same M-dispatch as aql_linear_w8a16
-  if (M >= kW8A16GemmMinM && K <= (1LL << 22))
+  if (M >= kW8A16GemmMinM && K <= (1LL << 22)) {
+    if (lora_fwd_products_bytes(M, N, K, L, R)) {
+      const size_t at = lora_fwd_part_bytes(M, N, K);
+      const hipError_t e =
+          lora_products(lt, at > 0, false, M, L, p, part + at / sizeof(float), st);
+      if (e != hipSuccess) return launched(e, fn);
+    }
     return launched(aql::launch_w8a16_gemm(x, M, K, q, scale, bias, N, y, part, pb, st, lt), fn);
+  }
   return launched(aql::launch_w8a16(x, M, K, q, scale, bias, N, y, part, pb, st, lt), fn);
 }
 
@@ -745,12 +782,10 @@ int aql_linear_w8a16_lora_backward(const uint16_t *dy, int64_t M, int64_t N, con
   hipError_t e = hipSuccess;
   aql::DgradScale sc{};
   char *dws = static_cast<char *>(ws) + lora_bwd_u_bytes(M, R);
+  float *part = reinterpret_cast<float *>(dws + align256(aql::w8a16_dgrad_bytes(M, N, K)));
   if (M > 0 && (dx || dA)) {
     if (dx) sc = aql::w8a16_dgrad_scale_args(dy, scale, M, N, K, dws);
-    e = aql::launch_lora_shrink_t(
-        dy, M, N, B, alpha, L, R, p, u,
-        reinterpret_cast<float *>(dws + align256(aql::w8a16_dgrad_bytes(M, N, K))),
-        dx ? &sc : nullptr, st);
+    e = aql::launch_lora_shrink_t(dy, M, N, B, alpha, L, R, p, u, part, dx ? &sc : nullptr, st);
     if (e != hipSuccess) return launched(e, fn);
   }
   if (dA || (dB && N > 0)) {
@@ -773,7 +808,11 @@ int aql_linear_w8a16_lora_backward(const uint16_t *dy, int64_t M, int64_t N, con
     if (e != hipSuccess) return launched(e, fn);
   }
   if (dx && M > 0) {
-    const aql::LoraTerm lt{u, A, p + aql::lora_plan_layout(M, L).idx, (int32_t)R, K};
+    aql::LoraTerm lt{u, A, p + aql::lora_plan_layout(M, L).idx, (int32_t)R, K};
+    if (lora_bwd_products_bytes(M, N, K, L, R)) {
+      e = lora_products(lt, aql::w8a16_dgrad_split(M, N, K), true, M, L, p, part, st);
+      if (e != hipSuccess) return launched(e, fn);
+    }
     e = aql::launch_w8a16_dgrad_scaled(sc, q, K, dx, dws, st, lt);
   }
   return launched(e, fn);

@@ -13,10 +13,14 @@ namespace aql {
 // rows' adapters (-1: none), then tiles of 16 positions. A tile holds rows of
 // one adapter, adapters ascending, rows ascending within one; the rows without
 // an adapter come last as adapter -1. A segment's last tile is padded with -1.
+// Last, for each group of 128 rows as the batch has them: whether more than
+// kLoraFew adapters share it.
 constexpr int kLoraTile = 16;
 constexpr int kLoraMaxAdapters = 1024;
 constexpr int kLoraHeader = 16;  // [0] tiles in use
 constexpr int kLoraMaxRank = 128;
+constexpr int kLoraGroup = 128;  // rows of the largest tile of the tiled kernels
+constexpr int kLoraFew = 4;      // adapters of a group that they take in their epilogues
 
 struct LoraPlanLayout {
   int64_t tiles;     // tiles a batch of M rows over L adapters can need
@@ -24,6 +28,7 @@ struct LoraPlanLayout {
   int64_t perm;      // [16 tiles] row at each sorted position, -1: padding
   int64_t owner;     // [tiles] adapter of a tile, -1: rows without one, -2: unused
   int64_t first;     // [L + 1] first tile of adapter a; [L]: of the rows without one
+  int64_t mixed;     // [M / 128] 1: more than kLoraFew adapters in the group
   int64_t total;     // int32 elements in all
 };
 constexpr LoraPlanLayout lora_plan_layout(int64_t M, int64_t L) {
@@ -33,7 +38,8 @@ constexpr LoraPlanLayout lora_plan_layout(int64_t M, int64_t L) {
   p.perm = p.idx + (M + 15) / 16 * 16;
   p.owner = p.perm + p.tiles * kLoraTile;
   p.first = p.owner + (p.tiles + 15) / 16 * 16;
-  p.total = p.first + (L + 1 + 15) / 16 * 16;
+  p.mixed = p.first + (L + 1 + 15) / 16 * 16;
+  p.total = p.mixed + ((M + kLoraGroup - 1) / kLoraGroup + 15) / 16 * 16;
   return p;
 }
 
@@ -63,9 +69,17 @@ struct LoraTerm {
   // sums computes it beside them (lora_shrink_rows; A [L, R, K], alpha [L])
   const uint16_t *A = nullptr;
   const float *alpha = nullptr;
+  // not NULL: the products themselves [M, N], of the rows in the plan's mixed
+  // groups, or of all rows where mixed is NULL (launch_lora_products)
+  const float *T = nullptr;
+  const int32_t *mixed = nullptr;
+  __device__ __forceinline__ bool ready(int64_t m0) const {  // the group of m0's products
+    return T && (!mixed || mixed[m0 / kLoraGroup]);
+  }
   __device__ __forceinline__ float add(int64_t m, int64_t n, float v) const {
     const int a = idx[m];
     if (a < 0) return v;
+    if (T) return v + T[m * N + n];  // (where outputs come one at a time: all rows)
     const uint16_t *w = W + ((int64_t)a * N + n) * R;
     const float *hm = h + m * R;
     float s0 = 0.0f, s1 = 0.0f;
@@ -200,7 +214,9 @@ __device__ __forceinline__ void lora_rows(LoraRows<BM> &s, const LoraTerm &t, in
   const int tid = threadIdx.x;
   for (int i = tid; i < BM; i += NT) s.ids[i] = m0 + i < M ? t.idx[m0 + i] : -1;
   __syncthreads();
-  if (tid < 64) {
+  if (t.ready(m0)) {
+    if (tid == 0) s.count = 0;
+  } else if (tid < 64) {
     int n = 0;
     for (int prev = -1;; ++n) {
       int next = 0x7fffffff;
@@ -353,6 +369,29 @@ __device__ __forceinline__ void lora_add_tile(char *smem, const LoraRows<BM> &s,
     }
     __syncthreads();
   }
+  if (t.ready(m0)) {  // no steps: the products lie in memory
+    const int c0 = col0 + (KMAJOR ? 4 * r : r);
+    const float *p = t.T + (m0 + row0 + 4 * g) * t.N + n0 + c0;
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const i32x4 id = *reinterpret_cast<const i32x4 *>(s.ids + row0 + 16 * i + 4 * g);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        if constexpr (KMAJOR) {
+          f32x4 d = {0.f, 0.f, 0.f, 0.f};
+          if (id[v] >= 0 && n0 + c0 < t.N) d = *reinterpret_cast<const f32x4 *>(p);
+#pragma unroll
+          for (int j = 0; j < TJ; ++j) acc[i][j][v] += d[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < TJ; ++j)
+            acc[i][j][v] += id[v] >= 0 && n0 + c0 + 16 * j < t.N ? p[16 * j] : 0.0f;
+        }
+        p += v < 3 ? t.N : 13 * t.N;
+        asm volatile("" : "+v"(p));  // one row's address at a time
+      }
+    }
+  }
 }
 
 // ---------------------------------------------------------------- launchers
@@ -377,6 +416,23 @@ struct DgradScale;
 hipError_t launch_lora_shrink_t(const uint16_t *dy, int64_t M, int64_t N, const uint16_t *B,
                                 const float *alpha, int64_t L, int64_t R, const int32_t *plan,
                                 float *u, float *part, const DgradScale *sc, hipStream_t st);
+
+// Whether a split kernel's sum of M x C outputs is better given their products
+// than left to compute each, R multiply-adds with R ranks read for it (M = 500, C =
+// 4096, R = 64, K = 14336: 99 us of the whole call, 148; M = 300, R = 16: 81, 83, R = 8:
+// 77, 73). With the contraction as W's slow axis (kmajor) neighbouring outputs share
+// lines, so later (backward at M = 500, R = 128, N = K = 4096: 70 us, 96; M = 300, R =
+// 16: 46, 43).
+constexpr bool lora_split_products(bool kmajor, int64_t M, int64_t C, int64_t R) {
+  return M * C * R >= (kmajor ? 1 << 26 : 1 << 24);
+}
+
+// T[m, n] = sum_j h[m, j] W[a][n, j] (float32 [M, N]) for the rows with an adapter,
+// where mixed is given only those in its groups; other rows stay as they are.
+// kmajor: W is [L, R, N].
+hipError_t launch_lora_products(const float *h, const uint16_t *W, bool kmajor, int64_t M,
+                                int64_t N, int64_t L, int64_t R, const int32_t *plan,
+                                const int32_t *mixed, float *T, hipStream_t st);
 
 // dB[a][n, j] = sum_{m in a} dy[m, n] h[m, j] and
 // dA[a][j, k] = sum_{m in a} u[m, j] xq[m, k] xs[m, k / 128], both float32;

@@ -75,6 +75,23 @@ __global__ __launch_bounds__(1024) void k_lora_plan(const int32_t *__restrict__ 
     plan[p.first + tid] = before;
     next[tid] = before * kLoraTile;
   }
+  for (int64_t gr = wave; gr * kLoraGroup < M; gr += 16) {  // a wave a group
+    const int64_t m = gr * kLoraGroup + lane;
+    const int v0 = m < M ? bin_of(m) : (int)L, v1 = m + 64 < M ? bin_of(m + 64) : (int)L;
+    int n = 0;
+    for (int prev = -1; n <= kLoraFew; ++n) {
+      int least = v0 > prev ? v0 : (int)L;
+      least = v1 > prev && v1 < least ? v1 : least;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int other = __shfl_xor(least, o);
+        least = other < least ? other : least;
+      }
+      if (least == (int)L) break;
+      prev = least;
+    }
+    if (lane == 0) plan[p.mixed + gr] = n > kLoraFew;
+  }
   for (int64_t t = total + tid; t < p.tiles; t += 1024) plan[p.owner + t] = -2;
   for (int64_t i = tid; i < p.tiles * kLoraTile; i += 1024) plan[p.perm + i] = -1;
   if (tid == 0) plan[0] = total;
@@ -520,6 +537,96 @@ __global__ __launch_bounds__(64 * W) void k_lora_wgrad(LoraWgradArgs p, int tile
     lora_wgrad<W, RT, true>(p, pl, a, (int64_t)(tile - tiles_b) * 128, j0, smem);
 }
 
+// --------------------------------------------------------- products in memory
+
+// One workgroup: a tile of the plan (16 rows of one adapter) x 256 columns, a wave
+// 64 of them. Where many adapters share a tile of the projection's kernel, walking
+// them there costs 3 to 5 us each (all 64 or 128 rows take part in each step), so
+// their products are computed here, spread over the chip with each adapter read
+// once per 16 rows, and the epilogues add them. Bound by memory: the adapters in
+// use and the float32 products, written here and read there (whole calls, 64
+// adapters at random: M = 128, N = 14336, K = 4096, R = 16: 51 us, 152 walked; M = 2048,
+// N = K = 4096, 32 adapters: 90, 183).
+template <bool KMAJOR>
+__global__ __launch_bounds__(256) void k_lora_products(const float *__restrict__ h,
+                                                       const uint16_t *__restrict__ W, int64_t M,
+                                                       int64_t N, int64_t L, int R,
+                                                       const int32_t *__restrict__ plan,
+                                                       const int32_t *__restrict__ mixed,
+                                                       int blocks, float *__restrict__ T) {
+  const LoraPlanLayout p = lora_plan_layout(M, L);
+  const int tile = blockIdx.x / blocks;  // blocks of columns
+  const int a = plan[p.owner + tile];
+  if (a < 0) return;
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, wave = threadIdx.x >> 6;
+  const int32_t *perm = plan + p.perm + (int64_t)tile * kLoraTile;
+  const int row = perm[r];
+  if (mixed && !__any(row >= 0 && mixed[(row < 0 ? 0 : row) / kLoraGroup])) return;
+  const i32x4 out = *reinterpret_cast<const i32x4 *>(perm + 4 * g);
+  const int64_t n0 = (int64_t)(blockIdx.x % blocks) * 256 + 64 * wave;
+  f32x4 d[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) d[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int c = 0; c < R; c += 32) {
+    const bool in = c + 8 * g < R;  // whole chunks of 8 ranks
+    f32x4 h0 = {0.f, 0.f, 0.f, 0.f}, h1 = h0;
+    if (in && row >= 0) {
+      const float *hm = h + (int64_t)row * R + c + 8 * g;
+      h0 = *reinterpret_cast<const f32x4 *>(hm);
+      h1 = *reinterpret_cast<const f32x4 *>(hm + 4);
+    }
+    bf16x8 w[4];
+    if constexpr (KMAJOR) {  // column n0 + 4 r + j
+      i32x2 v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = i32x2{0, 0};
+        if (in && n0 + 4 * r < N)  // whole chunks: N is a multiple of 16
+          v[e] = *reinterpret_cast<const i32x2 *>(W + ((int64_t)a * R + c + 8 * g + e) * N + n0 +
+                                                  4 * r);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        i32x4 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o[e] = j & 1 ? pack_hi(v[2 * e][j >> 1], v[2 * e + 1][j >> 1])
+                       : pack_lo(v[2 * e][j >> 1], v[2 * e + 1][j >> 1]);
+        w[j] = __builtin_bit_cast(bf16x8, o);
+      }
+    } else {  // column n0 + 16 j + r
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t n = n0 + 16 * j + r;
+        i32x4 o = {0, 0, 0, 0};
+        if (in && n < N) o = *reinterpret_cast<const i32x4 *>(W + ((int64_t)a * N + n) * R + c + 8 * g);
+        w[j] = __builtin_bit_cast(bf16x8, o);
+      }
+    }
+    const float v[8] = {h0[0], h0[1], h0[2], h0[3], h1[0], h1[1], h1[2], h1[3]};
+    bf16x8 hi, lo;
+    split_bf16(v, hi, lo);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[j], d[j], 0, 0, 0);
+      d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[j], d[j], 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    if (out[v] < 0) continue;
+    float *t = T + (int64_t)out[v] * N + n0;
+    if constexpr (KMAJOR) {
+      if (n0 + 4 * r < N)
+        *reinterpret_cast<f32x4 *>(t + 4 * r) = f32x4{d[0][v], d[1][v], d[2][v], d[3][v]};
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n0 + 16 * j + r < N) t[16 * j + r] = d[j][v];
+    }
+  }
+}
+
 // One launch (NT = 1) for a contraction of at most two steps a wave on a grid of
 // at most one workgroup a CU (M = 500, K = 4096, R = 64: 9.9 us, 13.7 in ranges with
 // their second launch); else ranges of one step a wave while that keeps the grid
@@ -621,6 +728,20 @@ hipError_t launch_lora_shrink_t(const uint16_t *dy, int64_t M, int64_t N, const 
   if (sc->NP <= 16384)
     return go_shrink<true>(dy, M, N, B, alpha, L, R, plan, u, part, WithScale<8>{*sc}, st);
   return go_shrink<true>(dy, M, N, B, alpha, L, R, plan, u, part, WithScale<0>{*sc}, st);
+}
+
+hipError_t launch_lora_products(const float *h, const uint16_t *W, bool kmajor, int64_t M,
+                                int64_t N, int64_t L, int64_t R, const int32_t *plan,
+                                const int32_t *mixed, float *T, hipStream_t st) {
+  const int64_t blocks = (N + 255) / 256;
+  const dim3 grid((unsigned)(lora_plan_layout(M, L).tiles * blocks));
+  if (kmajor)
+    hipLaunchKernelGGL(k_lora_products<true>, grid, dim3(256), 0, st, h, W, M, N, L, (int)R, plan,
+                       mixed, (int)blocks, T);
+  else
+    hipLaunchKernelGGL(k_lora_products<false>, grid, dim3(256), 0, st, h, W, M, N, L, (int)R, plan,
+                       mixed, (int)blocks, T);
+  return hipGetLastError();
 }
 
 hipError_t launch_lora_wgrad(const LoraWgradArgs &a, hipStream_t st) {

@@ -93,6 +93,8 @@ __device__ __forceinline__ void dgrad_scale_row(const DgradScale &a, int64_t m, 
 // Bytes of the workspace: dy times the scales in float16 [M, N rounded up to 64],
 // an exponent a row, and the partial sums of shapes that split the contraction.
 size_t w8a16_dgrad_bytes(int64_t M, int64_t N, int64_t K);
+// Whether such a shape splits it.
+bool w8a16_dgrad_split(int64_t M, int64_t N, int64_t K);
 
 // The scaling's arguments for a call with this workspace.
 DgradScale w8a16_dgrad_scale_args(const uint16_t *dy, const float *scale, int64_t M, int64_t N,

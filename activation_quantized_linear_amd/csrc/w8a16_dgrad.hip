@@ -373,7 +373,9 @@ __global__ __launch_bounds__(256) void k_w8a16_dgrad_reduce(const float *__restr
     acc += *reinterpret_cast<const f32x4 *>(part + ((int64_t)s * M + m) * K + k);
   if constexpr (LT::on) {
     const int a = lt.idx[m];
-    if (a >= 0) {
+    if (a >= 0 && lt.T) {
+      acc += *reinterpret_cast<const f32x4 *>(lt.T + m * K + k);
+    } else if (a >= 0) {
       const uint16_t *w = lt.W + (int64_t)a * lt.R * K + k;
       const float *u = lt.h + m * lt.R;
       f32x4 t = {0.f, 0.f, 0.f, 0.f};
@@ -494,6 +496,8 @@ hipError_t launch(const DgradScale &a, const int8_t *q, int64_t K, uint16_t *dx,
 }
 
 }  // namespace
+
+bool w8a16_dgrad_split(int64_t M, int64_t N, int64_t K) { return splits_of(M, N, K) > 1; }
 
 size_t w8a16_dgrad_bytes(int64_t M, int64_t N, int64_t K) { return layout(M, N, K).total; }
 

@@ -216,6 +216,11 @@ def test_plan(M, L, mix):
         assert (own[t:t + n] == a).all()
         t += n
     assert int(b[0]) == t and (own[t:] == -2).all() and (perm[16 * t:] == -1).all()
+    # groups of 128 rows: more than 4 adapters or not
+    mixed = b[o_first + up(L + 1):]
+    for i in range((M + 127) // 128):
+        here = valid[128 * i:128 * (i + 1)]
+        assert int(mixed[i]) == (len(set(here[here >= 0].tolist())) > 4)
 
 
 # -------------------------------------------------------------------- forward
@@ -241,6 +246,11 @@ FORWARD = [
     (70, 64, 40957, 3, 16, "random"), (1024, 80, 16381, 2, 40, "runs"), (2048, 64, 2043, 1, 8, "0"),
     (500, 64, 11005, 3, 16, "runs"), (77, 128, 6, 2, 8, "random"), (65, 64, 3, 1, 8, "0"),
     (129, 64, 1, 1, 8, "0"),
+    # many adapters in a tile, in every tile form; products given to the sum of a split
+    (64, 4096, 1000, 64, 16, "random"), (300, 128, 515, 300, 8, "runs"),
+    (150, 64, 20480, 9, 40, "random"), (1024, 80, 16381, 12, 8, "random"),
+    (2048, 64, 2043, 20, 16, "random"), (300, 8192, 1000, 7, 64, "random"),
+    (513, 8192, 1001, 5, 128, "runs"),
 ]
 
 
@@ -297,6 +307,37 @@ def test_adapters_do_not_reach_each_other(M):
     assert torch.equal(dA0[::2], dA1[::2]) and torch.equal(dB0[::2], dB1[::2])
 
 
+@pytest.mark.parametrize("K,N", [(512, 320), (64, 20480), (2560, 264)])
+def test_groups_of_many_and_of_few_adapters(K, N):
+    """One batch with rows of nine adapters at random, of one, of two and of none; a
+    NaN in one adapter's matrices, and in its rows, stays in its rows."""
+    M, L, R = 700, 9, 24
+    c = make(M, K, N, L, R, "random")
+    c["idx"][128:256], c["idx"][256:400] = 3, -1
+    c["idx"][400:640] = torch.arange(240).to(torch.int32) // 130
+    say("groups", K, N)
+
+    def run():
+        d = dev(c)
+        y, h, plan = forward(d)
+        xq, xs = aql.aql_act_checkpoint(d["x"])
+        out = (y, h, *backward(d, plan, h, xq, xs))
+        torch.cuda.synchronize()
+        return out
+
+    y, h, dx, dA, dB = run()
+    yr, ytol, hr, htol = ref_forward(c)
+    close(h, hr, htol, "h")
+    close(y, yr, ytol, "y", norm=4e-3)
+    rows = c["idx"] == 3
+    c["A"][3], c["B"][3], c["x"][rows], c["dy"][rows] = (float("nan"),) * 4
+    y1, h1, dx1, dA1, dB1 = run()
+    ok, others = (~rows).to(DEV), [a for a in range(L) if a != 3]
+    for a, b in ((y, y1), (h, h1), (dx, dx1)):
+        assert torch.equal(a[ok], b[ok]) and torch.isnan(b[~ok]).all()
+    assert torch.equal(dA[others], dA1[others]) and torch.equal(dB[others], dB1[others])
+
+
 # ------------------------------------------------------------------- backward
 
 BACKWARD = [
@@ -307,6 +348,8 @@ BACKWARD = [
     (300, 80, 1048, 1, 16, "none"), (1000, 512, 640, 7, 128, "random"),
     (2100, 2560, 192, 2, 16, "runs"), (1100, 16384, 64, 1, 8, "0"), (33, 12288, 1032, 33, 8, "runs"),
     (200, 4096, 1024, 8, 16, "runs"), (1100, 320, 136, 1, 40, "0"), (2200, 144, 72, 2, 128, "runs"),
+    (1100, 16384, 64, 9, 24, "random"), (198, 5120, 80, 16, 32, "random"),
+    (300, 4096, 1040, 6, 64, "random"), (130, 272, 136, 130, 8, "runs"),
 ]
 
 
