@@ -28,6 +28,8 @@ constexpr int kGroup = 128;  // columns of a checkpoint scale
 // the adapters, then chunks of 1024 rows in order. Inside a chunk a row's rank
 // is the number of equal rows before it in its wave (ballots) plus the counts
 // of the waves before (a byte table), so rows keep their order in a segment.
+// One launch a batch, for all its layers: bound by its barriers and round trips
+// (M = 500: 5.9 us, M = 2048: 8.4), which one workgroup keeps few.
 __global__ __launch_bounds__(1024) void k_lora_plan(const int32_t *__restrict__ idx, int64_t M,
                                                     int64_t L, int32_t *__restrict__ plan) {
   constexpr int NB = kLoraMaxAdapters + 1;  // the last bin: rows without an adapter
@@ -154,6 +156,8 @@ __global__ __launch_bounds__(256) void k_lora_shrink_rows(
 //    16 ranks (with 16 rows the adapter's bytes equal the rows'), and float32
 //    partial sums in sorted order are added in order by k_lora_shrink_sum;
 //  * NT = 1, W = 16 over the whole of a short contraction: one launch.
+// (x onto A at M = 500, K = 4096, R = 64: 10.4 us; dy onto B at M = 2048, N = 14336, R = 16:
+// 18 + 5 us, 32 + 5 with dy's scaling beside it, 59 MB read and written.)
 // Operands go from memory to the MFMA registers as they lie: x and A have the
 // contraction contiguous. KMAJOR: the adapter matrix is [C, R] (dy onto B); each
 // wave then passes its step's 32 x 16 blocks through its own LDS slot and reads

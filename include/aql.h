@@ -12,14 +12,16 @@
  *   [out_features, in_features], as the pages store a linear's weight.
  * - Device base pointers must be 16-byte aligned (AQL_ERR_ALIGN otherwise).
  * - An empty problem (M == 0 or N == 0 where the function has them) is valid:
- *   it returns AQL_OK without any HIP call, and pointers to its zero-element
+ *   it returns AQL_OK without any HIP call (unless its entry names outputs that
+ *   are not empty: those are written), and pointers to its zero-element
  *   buffers may be NULL. K must always be at least its stated minimum.
  * - bf16 values travel as their 16-bit patterns (uint16_t).
  * - Every argument is validated before anything is launched; a rejected call
  *   launches nothing and returns a negative status. aql_last_error() then
  *   describes the first problem found (thread-local text). There is no silent
  *   fallback to another algorithm or to the host.
- * - Inputs must be finite; results for NaN/Inf inputs are unspecified.
+ * - Inputs must be finite; results for NaN/Inf inputs are unspecified, but for
+ *   what an entry says of them.
  * - Rounding: round-half-to-even everywhere a float becomes an integer code,
  *   IEEE binary32 division where the definition divides, no flush of
  *   subnormals. Integer results (codes, zero points, weight sums, int32
