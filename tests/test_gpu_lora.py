@@ -595,6 +595,96 @@ def test_checkpoint_of_values_that_are_no_numbers():
             assert torch.equal(v0[~bad], v1[~bad])
 
 
+# ------------------------------------------------------------ past 32 bits
+
+
+def cut(c, rows, cols=None, ks=None):
+    """The problem of some rows and of some output channels or inputs, on the CPU."""
+    r = {"bias": None, "alpha": c["alpha"].cpu()}
+    r["x"], r["dy"], r["idx"] = c["x"][rows].cpu(), c["dy"][rows].cpu(), c["idx"][rows].cpu()
+    n = slice(None) if cols is None else cols
+    k = slice(None) if ks is None else ks
+    r["q"], r["scale"] = c["q"][n][:, k].cpu(), c["scale"][n].cpu()
+    r["B"], r["A"] = c["B"][:, n].cpu(), c["A"][:, :, k].cpu()
+    return r
+
+
+def big(M, K, N, L, R):
+    g = torch.Generator(device=DEV).manual_seed(M + K + N)
+    rnd = lambda *s, std=1.0: (torch.randn(*s, generator=g, device=DEV) * std).to(torch.bfloat16)
+    return {"x": rnd(M, K), "dy": rnd(M, N, std=1e-2),
+            "q": torch.randint(-127, 128, (N, K), generator=g, device=DEV, dtype=torch.int8),
+            "scale": 1e-3 + 1e-3 * torch.rand(N, generator=g, device=DEV), "bias": None,
+            "A": rnd(L, R, K, std=K ** -0.5), "B": rnd(L, N, R, std=0.02),
+            "alpha": torch.ones(L, device=DEV),
+            "idx": torch.randint(-1, L, (M,), generator=g, device=DEV, dtype=torch.int32)}
+
+
+@pytest.mark.parametrize("L", [3, 6])  # walked in the tiles, and products given
+def test_outputs_past_32_bits(L):
+    M, K, N, R = 2100, 16, 1050001, 8  # y: 2.2e9 values
+    say("outputs", L)
+    d = big(M, K, N, L, R)
+    y, h, _ = forward(d)
+    torch.cuda.synchronize()
+    rows = torch.tensor([0, 1, 1022, 1023, 1024, 2047, M - 1], device=DEV)
+    cols = torch.cat([torch.arange(40), torch.arange(N - 300, N)]).to(DEV)
+    c = cut(d, rows, cols)
+    yr, ytol, hr, htol = ref_forward(c)
+    close(h[rows], hr, htol, "h")
+    close(y[rows][:, cols], yr, ytol, "y", norm=4e-3)
+
+
+def test_weights_past_32_bits():
+    M, K, N, L, R = 70, 65552, 65600, 2, 8  # q: 4.3e9 bytes
+    say("weights")
+    d = big(M, K, N, L, R)
+    _, h, plan = forward(d)
+    xq, xs = aql.aql_act_checkpoint(d["x"])
+    dx, dA, dB = backward(d, plan, h, xq, xs)
+    alone = aql.aql_linear_w8a16_dgrad(d["dy"], d["q"], d["scale"])
+    torch.cuda.synchronize()
+    rows = torch.tensor([0, 63, 64, M - 1], device=DEV)
+    ks = torch.cat([torch.arange(16), torch.arange(K - 128, K)]).to(DEV)
+    c = cut(d, rows, ks=ks)
+    ref, T, off = ref_dgrad(c)
+    close(alone[rows][:, ks], ref, 2.0 ** -8 * ref.abs() + (N + 4) * U * T + off, "dx", norm=4e-3)
+    tol = torch.zeros_like(ref)
+    for i, a in enumerate(c["idx"].tolist()):
+        if a < 0:
+            continue
+        A, B, dy = f64(c["A"][a]), f64(c["B"][a]), f64(c["dy"][i])
+        u, ue = dy @ B, (N + 3) * U * (dy.abs() @ B.abs())
+        ref[i] += u @ A
+        T[i] += u.abs() @ A.abs()
+        tol[i] += (ue + 2.0 ** -16 * u.abs()) @ A.abs()
+    tol += off + 2.0 ** -8 * ref.abs() + (N + R + 4) * U * T
+    close(dx[rows][:, ks], ref, tol, "dx with adapters", norm=4e-3)
+
+
+def test_most_rows():
+    M, K, N, L, R = 1048560, 16, 24, 1024, 8
+    say("rows")
+    d = big(M, K, N, L, R)
+    y, h, plan = forward(d)
+    xq, xs = aql.aql_act_checkpoint(d["x"])
+    dx, dA, dB = backward(d, plan, h, xq, xs)
+    torch.cuda.synchronize()
+    rows = torch.cat([torch.arange(200), torch.arange(M - 200, M)]).to(DEV)
+    c = cut(d, rows)
+    yr, ytol, hr, htol = ref_forward(c)
+    close(h[rows], hr, htol, "h")
+    close(y[rows], yr, ytol, "y", norm=4e-3)
+    (rx, tx), _, _ = ref_backward(c, h[rows].cpu(), xq[rows].cpu(), xs[rows].cpu())
+    close(dx[rows], rx, tx, "dx", norm=4e-3)
+    for a in (0, 511, 1023):  # every row of these adapters
+        one = (d["idx"] == a).nonzero()[:, 0]
+        c = cut(d, one)
+        _, (rA, tA), (rB, tB) = ref_backward(c, h[one].cpu(), xq[one].cpu(), xs[one].cpu())
+        close(dA[a], rA[a], tA[a], "dA")
+        close(dB[a], rB[a], tB[a], "dB")
+
+
 # ------------------------------------------------------------------- together
 
 
