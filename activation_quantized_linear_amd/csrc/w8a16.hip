@@ -1038,7 +1038,8 @@ struct ShLds {
 // part == nullptr: the whole K, y written. Else split blockIdx.z takes steps
 // [z spl, (z + 1) spl) and writes its unscaled sums to part[z][M][N] (fp32). With
 // adapters the slices behind the splits compute the rows' h, which the sum of the
-// splits needs (M = 27, K = 14336, N = 4096, R = 16: 25.1 us in a launch of its own).
+// splits needs (M = 27, K = 14336, N = 4096, R = 16: 23.7 us a call, 26.3 with a launch
+// of its own for them).
 template <int WC, int WK, class LT>
 __global__ __launch_bounds__(64 * WC * WK) void k_w8a16_sksh(const uint16_t *__restrict__ x, int64_t M,
                                                              int64_t K, const int8_t *__restrict__ q,
