@@ -788,8 +788,10 @@ int aql_linear_w8a16_lora_backward(const uint16_t *dy, int64_t M, int64_t N, con
     e = aql::launch_lora_shrink_t(dy, M, N, B, alpha, L, R, p, u, part, dx ? &sc : nullptr, st);
     if (e != hipSuccess) return launched(e, fn);
   }
-  if (dA || (dB && N > 0)) {
-    aql::LoraWgradArgs w{};
+  aql::LoraWgradArgs w{};
+  const bool wgrad = dA || (dB && N > 0), split = aql::w8a16_dgrad_split(M, N, K);
+  bool beside = false;  // the weight gradients and the input gradient's last sum, one launch
+  if (wgrad) {
     w.dy = dy;
     w.xq = xq;
     w.xs = xs;
@@ -804,16 +806,19 @@ int aql_linear_w8a16_lora_backward(const uint16_t *dy, int64_t M, int64_t N, con
     w.L = L;
     w.R = R;
     w.accumulate = accumulate != 0;
-    e = aql::launch_lora_wgrad(w, st);
+    beside = dx && M > 0 && split && aql::lora_wgrad_beside(w);
+    if (!beside) e = aql::launch_lora_wgrad(w, st);
     if (e != hipSuccess) return launched(e, fn);
   }
   if (dx && M > 0) {
     aql::LoraTerm lt{u, A, p + aql::lora_plan_layout(M, L).idx, (int32_t)R, K};
     if (lora_bwd_products_bytes(M, N, K, L, R)) {
-      e = lora_products(lt, aql::w8a16_dgrad_split(M, N, K), true, M, L, p, part, st);
+      e = lora_products(lt, split, true, M, L, p, part, st);
       if (e != hipSuccess) return launched(e, fn);
     }
-    e = aql::launch_w8a16_dgrad_scaled(sc, q, K, dx, dws, st, lt);
+    aql::DgradParts parts{};
+    e = aql::launch_w8a16_dgrad_scaled(sc, q, K, dx, dws, st, lt, beside ? &parts : nullptr);
+    if (e == hipSuccess && beside) e = aql::launch_lora_wgrad_reduce(w, parts, lt, st);
   }
   return launched(e, fn);
 }

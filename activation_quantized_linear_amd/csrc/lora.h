@@ -453,5 +453,11 @@ struct LoraWgradArgs {
   bool accumulate;
 };
 hipError_t launch_lora_wgrad(const LoraWgradArgs &a, hipStream_t st);
+// The same with the last sum of a split input gradient beside it, in workgroups of 4
+// waves: for segments of few rows and not too many workgroups (lora_wgrad_beside).
+struct DgradParts;
+bool lora_wgrad_beside(const LoraWgradArgs &a);
+hipError_t launch_lora_wgrad_reduce(const LoraWgradArgs &a, const DgradParts &parts,
+                                    const LoraTerm &lt, hipStream_t st);
 
 }  // namespace aql

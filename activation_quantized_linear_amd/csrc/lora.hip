@@ -541,6 +541,28 @@ __global__ __launch_bounds__(64 * W) void k_lora_wgrad(LoraWgradArgs p, int tile
     lora_wgrad<W, RT, true>(p, pl, a, (int64_t)(tile - tiles_b) * 128, j0, smem);
 }
 
+// The same with the last sum of a split input gradient in the workgroups behind
+// (blocks of the weight gradients): both are short, and neither waits for the other.
+__global__ __launch_bounds__(256) void k_lora_wgrad_reduce(LoraWgradArgs p, int tiles_b, int tiles,
+                                                           int blocks, DgradParts parts,
+                                                           LoraTerm lt) {
+  __shared__ __attribute__((aligned(16))) char smem[4 / 2 * 8 * 64 * 16];
+  int b = blockIdx.x;
+  if (b >= blocks) {
+    dgrad_reduce(parts, lt, (int64_t)(b - blocks) * 256 + threadIdx.x);
+    return;
+  }
+  const LoraPlanLayout pl = lora_plan_layout(p.M, p.L);
+  const int tile = b % tiles;
+  b /= tiles;
+  const int64_t a = b % (int)p.L;
+  const int j0 = b / (int)p.L * 16;
+  if (tile < tiles_b)
+    lora_wgrad<4, 1, false>(p, pl, a, (int64_t)tile * 64, j0, smem);
+  else
+    lora_wgrad<4, 1, true>(p, pl, a, (int64_t)(tile - tiles_b) * 128, j0, smem);
+}
+
 // --------------------------------------------------------- products in memory
 
 // One workgroup: a tile of the plan (16 rows of one adapter) x 256 columns, a wave
@@ -748,6 +770,29 @@ hipError_t launch_lora_products(const float *h, const uint16_t *W, bool kmajor, 
   return hipGetLastError();
 }
 
+// Workgroups of the weight gradients, each 64 channels or 128 inputs of an adapter and
+// 16 ranks.
+static int64_t wgrad_units(const LoraWgradArgs &a) {
+  return ((a.dB ? (a.N + 63) / 64 : 0) + (a.dA ? (a.K + 127) / 128 : 0)) * a.L *
+         ((a.R + 15) / 16);
+}
+
+// Backward in a graph, with the sum beside and in launches each: M = 63, N = 2560, K = 960
+// 19.8 us, 23.7; M = 500, N = K = 4096, R = 128 60.5, 64.4; M = 512, one adapter 46.0,
+// 51.5. 64 adapters, R = 16 (6144 workgroups, for which 2 waves are enough): 55.6, 49.1.
+bool lora_wgrad_beside(const LoraWgradArgs &a) {
+  return a.M / a.L <= 512 && wgrad_units(a) < 2048;
+}
+
+hipError_t launch_lora_wgrad_reduce(const LoraWgradArgs &a, const DgradParts &parts,
+                                    const LoraTerm &lt, hipStream_t st) {
+  const int tb = a.dB ? (int)((a.N + 63) / 64) : 0, ta = a.dA ? (int)((a.K + 127) / 128) : 0;
+  const int64_t blocks = (int64_t)(tb + ta) * a.L * ((a.R + 15) / 16);
+  hipLaunchKernelGGL(k_lora_wgrad_reduce, dim3((unsigned)(blocks + parts.blocks())), dim3(256), 0,
+                     st, a, tb, tb + ta, (int)blocks, parts, lt);
+  return hipGetLastError();
+}
+
 hipError_t launch_lora_wgrad(const LoraWgradArgs &a, hipStream_t st) {
   // long segments and several blocks of ranks: two of them share a read (M = 8192,
   // 4 adapters, R = 64, N = K = 4096: 141 us of backward without dx, 150 apart)
@@ -756,8 +801,7 @@ hipError_t launch_lora_wgrad(const LoraWgradArgs &a, hipStream_t st) {
   // them only meet (M = 512, 16 adapters, R = 16, N = K = 4096: 15.4 us with 2, 18.2
   // with 4), fewer leave the memory idle (M = 2048, N = 14336, K = 4096, one adapter:
   // 37 us with 16, 45 with 4)
-  const int64_t units = ((a.dB ? (a.N + 63) / 64 : 0) + (a.dA ? (a.K + 127) / 128 : 0)) * a.L *
-                        ((a.R + 15) / 16);
+  const int64_t units = wgrad_units(a);
   if (2 * units >= kWgradWaves) return go_wgrad<2, 1>(a, st);
   if (4 * units >= kWgradWaves) return go_wgrad<4, 1>(a, st);
   if (8 * units >= kWgradWaves) return go_wgrad<8, 1>(a, st);

@@ -90,6 +90,49 @@ __device__ __forceinline__ void dgrad_scale_row(const DgradScale &a, int64_t m, 
   }
 }
 
+// What a split product leaves: dx = bf16(part[0] + ... + part[S - 1] + u A).
+struct DgradParts {
+  const float *part;  // [S, M, K]
+  int S;
+  int64_t M, K;
+  uint16_t *dx;
+  int64_t blocks() const { return (M * (K / 4) + 255) / 256; }
+};
+
+// Its sums in split order by M K / 4 threads, of which i takes 4 consecutive
+// columns, so the rows of A are read as whole lines.
+template <class LT>
+__device__ __forceinline__ void dgrad_reduce(const DgradParts &p, const LT &lt, int64_t i) {
+  const int64_t M = p.M, K = p.K, ng = K / 4;
+  if (i >= M * ng) return;
+  const int64_t m = i / ng, k = (i - m * ng) * 4;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < p.S; ++s)
+    acc += *reinterpret_cast<const f32x4 *>(p.part + ((int64_t)s * M + m) * K + k);
+  if constexpr (LT::on) {
+    const int a = lt.idx[m];
+    if (a >= 0 && lt.T) {
+      acc += *reinterpret_cast<const f32x4 *>(lt.T + m * K + k);
+    } else if (a >= 0) {
+      const uint16_t *w = lt.W + (int64_t)a * lt.R * K + k;
+      const float *u = lt.h + m * lt.R;
+      f32x4 t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+      for (int j = 0; j < lt.R; ++j) {
+        const i32x2 d = *reinterpret_cast<const i32x2 *>(w + (int64_t)j * K);
+        t[0] = fmaf(u[j], __uint_as_float((uint32_t)d[0] << 16), t[0]);
+        t[1] = fmaf(u[j], __uint_as_float((uint32_t)d[0] & 0xffff0000u), t[1]);
+        t[2] = fmaf(u[j], __uint_as_float((uint32_t)d[1] << 16), t[2]);
+        t[3] = fmaf(u[j], __uint_as_float((uint32_t)d[1] & 0xffff0000u), t[3]);
+      }
+      acc += t;
+    }
+  }
+  const uint32_t lo = f32_to_bf16_rne(acc[0]) | ((uint32_t)f32_to_bf16_rne(acc[1]) << 16);
+  const uint32_t hi = f32_to_bf16_rne(acc[2]) | ((uint32_t)f32_to_bf16_rne(acc[3]) << 16);
+  *reinterpret_cast<i32x2 *>(p.dx + m * K + k) = i32x2{(int)lo, (int)hi};
+}
+
 // Bytes of the workspace: dy times the scales in float16 [M, N rounded up to 64],
 // an exponent a row, and the partial sums of shapes that split the contraction.
 size_t w8a16_dgrad_bytes(int64_t M, int64_t N, int64_t K);
@@ -106,8 +149,10 @@ hipError_t launch_w8a16_dgrad(const uint16_t *dy, int64_t M, int64_t N, const in
                               const float *scale, int64_t K, uint16_t *dx, void *ws,
                               hipStream_t st);
 // The same plus sum_j u[m, j] A[a][j, k] (lt: h = u [M, R], W = A [L, R, K], N = K),
-// the scaling done by an earlier launch.
+// the scaling done by an earlier launch. later (may be NULL): a shape that splits
+// the contraction leaves its last sum to the caller.
 hipError_t launch_w8a16_dgrad_scaled(const DgradScale &a, const int8_t *q, int64_t K, uint16_t *dx,
-                                     void *ws, hipStream_t st, const LoraTerm &lt);
+                                     void *ws, hipStream_t st, const LoraTerm &lt,
+                                     DgradParts *later);
 
 }  // namespace aql

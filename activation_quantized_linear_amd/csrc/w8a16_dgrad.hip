@@ -364,41 +364,9 @@ __global__ __launch_bounds__(64 * NWV, 2) void k_w8a16_dgrad(
   }
 }
 
-// dx = bf16(part[0] + ... + part[S - 1] + u A), in split order; a thread takes 4
-// consecutive columns, so the rows of A are read as whole lines.
 template <class LT>
-__global__ __launch_bounds__(256) void k_w8a16_dgrad_reduce(const float *__restrict__ part, int S,
-                                                            int64_t M, int64_t K,
-                                                            uint16_t *__restrict__ dx, LT lt) {
-  const int64_t ng = K / 4;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= M * ng) return;
-  const int64_t m = i / ng, k = (i - m * ng) * 4;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < S; ++s)
-    acc += *reinterpret_cast<const f32x4 *>(part + ((int64_t)s * M + m) * K + k);
-  if constexpr (LT::on) {
-    const int a = lt.idx[m];
-    if (a >= 0 && lt.T) {
-      acc += *reinterpret_cast<const f32x4 *>(lt.T + m * K + k);
-    } else if (a >= 0) {
-      const uint16_t *w = lt.W + (int64_t)a * lt.R * K + k;
-      const float *u = lt.h + m * lt.R;
-      f32x4 t = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-      for (int j = 0; j < lt.R; ++j) {
-        const i32x2 p = *reinterpret_cast<const i32x2 *>(w + (int64_t)j * K);
-        t[0] = fmaf(u[j], __uint_as_float((uint32_t)p[0] << 16), t[0]);
-        t[1] = fmaf(u[j], __uint_as_float((uint32_t)p[0] & 0xffff0000u), t[1]);
-        t[2] = fmaf(u[j], __uint_as_float((uint32_t)p[1] << 16), t[2]);
-        t[3] = fmaf(u[j], __uint_as_float((uint32_t)p[1] & 0xffff0000u), t[3]);
-      }
-      acc += t;
-    }
-  }
-  const uint32_t lo = f32_to_bf16_rne(acc[0]) | ((uint32_t)f32_to_bf16_rne(acc[1]) << 16);
-  const uint32_t hi = f32_to_bf16_rne(acc[2]) | ((uint32_t)f32_to_bf16_rne(acc[3]) << 16);
-  *reinterpret_cast<i32x2 *>(dx + m * K + k) = i32x2{(int)lo, (int)hi};
+__global__ __launch_bounds__(256) void k_w8a16_dgrad_reduce(DgradParts p, LT lt) {
+  dgrad_reduce(p, lt, (int64_t)blockIdx.x * 256 + threadIdx.x);
 }
 
 struct Call {
@@ -430,7 +398,7 @@ hipError_t go(const Call &c, const LT &lt) {
 }
 
 template <int TI, int SG, class LT>
-hipError_t go_split(const Call &c, int S, const LT &lt) {
+hipError_t go_split(const Call &c, int S, const LT &lt, DgradParts *later) {
   using L = DgradLds<TI, SG>;
   static bool attr_set = false;
   if (!attr_set) {
@@ -447,9 +415,13 @@ hipError_t go_split(const Call &c, int S, const LT &lt) {
                      c.K, tm, tk, c.part, ks, NoLora{});
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t groups = c.M * (c.K / 4);
-  hipLaunchKernelGGL(k_w8a16_dgrad_reduce<LT>, dim3((unsigned)((groups + 255) / 256)), dim3(256),
-                     0, c.st, c.part, splits, c.M, c.K, c.dx, lt);
+  const DgradParts p{c.part, splits, c.M, c.K, c.dx};
+  if (later) {
+    *later = p;
+    return e;
+  }
+  hipLaunchKernelGGL(k_w8a16_dgrad_reduce<LT>, dim3((unsigned)p.blocks()), dim3(256), 0, c.st, p,
+                     lt);
   return hipGetLastError();
 }
 
@@ -490,14 +462,14 @@ hipError_t scale(const DgradScale &a, hipStream_t st) {
 
 template <class LT>
 hipError_t launch(const DgradScale &a, const int8_t *q, int64_t K, uint16_t *dx, void *ws,
-                  hipStream_t st, const LT &lt) {
+                  hipStream_t st, const LT &lt, DgradParts *later) {
   const Layout l = layout(a.M, a.N, K);
   const Call c{a.d, a.ex, q, dx, a.M, a.N, a.NP, K,
                reinterpret_cast<float *>(static_cast<char *>(ws) + l.part), st};
   const int64_t twide = ((a.M + 127) / 128) * ((K + 255) / 256);
   if (twide >= 160) return go<8, 4>(c, lt);
   const int S = splits_of(a.M, a.N, K);
-  if (S > 1) return go_split<4, 4>(c, S, lt);
+  if (S > 1) return go_split<4, 4>(c, S, lt, later);
   return go<4, 4>(c, lt);
 }
 
@@ -525,12 +497,13 @@ hipError_t launch_w8a16_dgrad(const uint16_t *dy, int64_t M, int64_t N, const in
   else if (a.NP <= 16384) e = scale<8>(a, st);
   else e = scale<0>(a, st);
   if (e != hipSuccess) return e;
-  return launch(a, q, K, dx, ws, st, NoLora{});
+  return launch(a, q, K, dx, ws, st, NoLora{}, nullptr);
 }
 
 hipError_t launch_w8a16_dgrad_scaled(const DgradScale &a, const int8_t *q, int64_t K, uint16_t *dx,
-                                     void *ws, hipStream_t st, const LoraTerm &lt) {
-  return launch(a, q, K, dx, ws, st, lt);
+                                     void *ws, hipStream_t st, const LoraTerm &lt,
+                                     DgradParts *later) {
+  return launch(a, q, K, dx, ws, st, lt, later);
 }
 
 }  // namespace aql

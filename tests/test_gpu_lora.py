@@ -350,6 +350,7 @@ BACKWARD = [
     (200, 4096, 1024, 8, 16, "runs"), (1100, 320, 136, 1, 40, "0"), (2200, 144, 72, 2, 128, "runs"),
     (1100, 16384, 64, 9, 24, "random"), (198, 5120, 80, 16, 32, "random"),
     (300, 4096, 1040, 6, 64, "random"), (130, 272, 136, 130, 8, "runs"),
+    (1200, 256, 2048, 2, 16, "runs"), (90, 4096, 1024, 64, 32, "random"),
 ]
 
 
