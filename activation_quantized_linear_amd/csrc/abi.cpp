@@ -203,10 +203,33 @@ size_t lora_fwd_products_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64
   if (M < kW8A16GemmMinM || K > (1LL << 22)) return 0;
   return lora_products_bytes(aql::w8a16_gemm_part_bytes(M, N, K) > 0, false, M, N, L, R);
 }
-size_t ws_lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+// What one batch of M rows needs. shrink: the most that its partial sums take for
+// any number of rows up to M.
+size_t lora_fwd_need(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
   const size_t lin = lora_fwd_part_bytes(M, N, K) + lora_fwd_products_bytes(M, N, K, L, R);
-  const size_t shr = M >= aql::kLoraTiledMinM ? aql::lora_shrink_bytes(M, K, L, R) : 0;
-  return lin > shr ? lin : shr;
+  const size_t shrink = M >= aql::kLoraTiledMinM ? aql::lora_shrink_most_bytes(M, K, L, R) : 0;
+  return std::max(lin, shrink);
+}
+
+// Workspaces never shrink as M grows, so that one of the largest batch serves the
+// others: the most that any number of rows up to M needs. That falls only where a
+// split ends or takes fewer ranges, between blocks of rows (16 of the streaming
+// kernels, 128 of the tiled ones, 64 of the input gradient's), so the blocks' ends
+// while there are splits and M itself are all there is to ask.
+size_t ws_lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+  size_t most = lora_fwd_need(M, N, K, L, R);
+  for (int64_t m : {16, 32, 48, 63})
+    if (m < M) most = std::max(most, lora_fwd_need(m, N, K, L, R));
+  for (int64_t m = 128; m < M && K <= (1LL << 22) && aql::w8a16_gemm_splits(m, N, K) > 1; m += 128)
+    most = std::max(most, lora_fwd_need(m, N, K, L, R));
+  return most;
+}
+
+size_t ws_dgrad(int64_t M, int64_t N, int64_t K) {
+  size_t most = aql::w8a16_dgrad_bytes(M, N, K);
+  for (int64_t m = 64; m < M && aql::w8a16_dgrad_split(m, N, K); m += 64)
+    most = std::max(most, aql::w8a16_dgrad_bytes(m, N, K));
+  return most;
 }
 
 // Workspace of its backward pass: u [M, R], dx's, then the shrink's partial sums
@@ -215,11 +238,16 @@ size_t lora_bwd_u_bytes(int64_t M, int64_t R) { return align256((size_t)M * (siz
 size_t lora_bwd_products_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
   return lora_products_bytes(aql::w8a16_dgrad_split(M, N, K), true, M, K, L, R);
 }
-size_t ws_lora_bwd(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
-  const size_t prod = lora_bwd_products_bytes(M, N, K, L, R);
-  const size_t shr = aql::lora_shrink_bytes(M, N, L, R);
+size_t lora_bwd_need(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
   return lora_bwd_u_bytes(M, R) + align256(aql::w8a16_dgrad_bytes(M, N, K)) +
-         (prod > shr ? prod : shr);
+         std::max(lora_bwd_products_bytes(M, N, K, L, R),
+                  aql::lora_shrink_most_bytes(M, N, L, R));
+}
+size_t ws_lora_bwd(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+  size_t most = lora_bwd_need(M, N, K, L, R);
+  for (int64_t m = 64; m < M && aql::w8a16_dgrad_split(m, N, K); m += 64)
+    most = std::max(most, lora_bwd_need(m, N, K, L, R));
+  return most;
 }
 
 // The products of a tiled kernel's term, in T where there are any to be computed.
@@ -339,7 +367,7 @@ size_t aql_workspace_bytes(int op, int64_t M, int64_t N, int64_t K) {
   }
   if (op == AQL_OP_W8A16_DGRAD) {
     if (M == 0 || M > kMaxRows || K == 0 || K > kMaxKW8A16 || N > (1LL << 22)) return 0;
-    return aql::w8a16_dgrad_bytes(M, N, K);
+    return ws_dgrad(M, N, K);
   }
   return 0;
 }
@@ -743,7 +771,7 @@ int aql_linear_w8a16_dgrad(const uint16_t *dy, int64_t M, int64_t N, const int8_
   if (M == 0) return ok();
   REQUIRE(dx && (N == 0 || (dy && q && scale)), AQL_ERR_NULL,
           "%s: dy, q, scale and dx must not be NULL", fn);
-  const size_t need = aql::w8a16_dgrad_bytes(M, N, K);
+  const size_t need = ws_dgrad(M, N, K);
   REQUIRE(ws && ws_bytes >= need, AQL_ERR_WORKSPACE, "%s: workspace needs %zu bytes (got %zu)", fn,
           need, ws ? ws_bytes : (size_t)0);
   if (int e = check_device(fn)) return e;

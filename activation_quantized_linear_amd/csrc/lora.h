@@ -401,13 +401,14 @@ __device__ __forceinline__ void lora_add_tile(char *smem, const LoraRows<BM> &s,
 
 // ---------------------------------------------------------------- launchers
 
-// Rows from which the shrink of x takes the tiled form, and the bytes of either
-// shrink's partial sums in the tiled form (C: the length of the contraction).
+// Rows from which the shrink of x takes the tiled form, and the most bytes that
+// either shrink's partial sums take in the tiled form for up to M rows (C: the length
+// of the contraction).
 constexpr int64_t kLoraTiledMinM = 64;
-size_t lora_shrink_bytes(int64_t M, int64_t C, int64_t L, int64_t R);
+size_t lora_shrink_most_bytes(int64_t M, int64_t C, int64_t L, int64_t R);
 
 // h[m, :] = alpha[a] A_a x[m] (float32 [M, R]); rows without an adapter get
-// zeros. x [M, K] bf16, A [L, R, K] bf16. part: lora_shrink_bytes(M, K, L, R)
+// zeros. x [M, K] bf16, A [L, R, K] bf16. part: lora_shrink_most_bytes(M, K, L, R)
 // bytes from kLoraTiledMinM rows on.
 hipError_t launch_lora_shrink(const uint16_t *x, int64_t M, int64_t K, const uint16_t *A,
                               const float *alpha, int64_t L, int64_t R, const int32_t *plan,
@@ -415,7 +416,7 @@ hipError_t launch_lora_shrink(const uint16_t *x, int64_t M, int64_t K, const uin
 
 // u[m, :] = alpha[a] B_a^T dy[m] (float32 [M, R]); rows without an adapter get
 // zeros. dy [M, N] bf16, B [L, N, R] bf16, N % 8 == 0. part:
-// lora_shrink_bytes(M, N, L, R) bytes. sc (may be NULL): dy's scaling for the
+// lora_shrink_most_bytes(M, N, L, R) bytes. sc (may be NULL): dy's scaling for the
 // input's gradient, done by further workgroups of the same launch.
 struct DgradScale;
 hipError_t launch_lora_shrink_t(const uint16_t *dy, int64_t M, int64_t N, const uint16_t *B,

@@ -726,9 +726,15 @@ hipError_t launch_lora_plan(const int32_t *idx, int64_t M, int64_t L, int32_t *p
   return hipGetLastError();
 }
 
-size_t lora_shrink_bytes(int64_t M, int64_t C, int64_t L, int64_t R) {
-  const int z = shrink_ranges(M, C, L, R);
-  return z > 1 ? (size_t)z * (size_t)lora_plan_layout(M, L).tiles * kLoraTile * (size_t)R * 4 : 0;
+// Z ranges over T tiles take Z T 64 R bytes. Z is at most one range for each step of
+// the waves, and it is 512 / (ceil(T / 4) ranks) at most (else 1, without partial
+// sums), so Z T <= 2048 / ranks; both bounds grow with M where Z T itself does not.
+size_t lora_shrink_most_bytes(int64_t M, int64_t C, int64_t L, int64_t R) {
+  if (shrink_whole(M, C, L, R)) return 0;  // and so is every smaller batch
+  const int64_t ranks = (R + 15) / 16, most = (C + 4 * kStep - 1) / (4 * kStep);
+  const int64_t steps = most * lora_plan_layout(M, L).tiles, places = 2048 / ranks;
+  if (most <= 1) return 0;
+  return (size_t)(steps < places ? steps : places) * kLoraTile * (size_t)R * 4;
 }
 
 hipError_t launch_lora_shrink(const uint16_t *x, int64_t M, int64_t K, const uint16_t *A,

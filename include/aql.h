@@ -102,7 +102,9 @@ const char *aql_last_error(void);
 
 /* Bytes of device workspace an operation needs for the given sizes (op is
  * AQL_OP_*); 0 for an unknown op or negative sizes. Workspace contents need
- * no initialization and are scratch after the call. */
+ * no initialization and are scratch after the call. A workspace that a call
+ * requires never shrinks as M grows, so one of the largest batch serves every
+ * smaller one of the same linear (not so the optional one of AQL_OP_W8A16). */
 size_t aql_workspace_bytes(int op, int64_t M, int64_t N, int64_t K);
 
 /* ----------------------------------------------------------- quantizers */
@@ -387,7 +389,8 @@ int aql_lora_plan(const int32_t *idx, int64_t M, int64_t L, void *plan, size_t p
  *   plan    from aql_lora_plan for this batch (M, L)
  *   h       device, [M, R] float32 (output; the backward pass takes it)
  *   ws      device workspace of aql_lora_forward_bytes(M, N, K, L, R) bytes (may be
- *           NULL where that is 0)
+ *           NULL where that is 0). It never shrinks as M grows: one of the
+ *           largest batch serves the others.
  * Errors: as aql_linear_w8a16, plus R not a multiple of 8 in
  * 8..AQL_LORA_MAX_RANK, L outside 1..AQL_LORA_MAX_ADAPTERS, NULL or misaligned
  * A, B, alpha, plan or h, workspace too small. N == 0 writes h alone.
@@ -429,7 +432,8 @@ int aql_linear_w8a16_dgrad(const uint16_t *dy, int64_t M, int64_t N, const int8_
  *   dx      device, [M, K] bf16 (output; may be NULL: not computed)
  *   dA, dB  device, [L, R, K] and [L, N, R] float32 (outputs; either may be
  *           NULL: not computed. xq and xs may be NULL without dA)
- *   ws      device workspace of aql_lora_backward_bytes(M, N, K, L, R) bytes
+ *   ws      device workspace of aql_lora_backward_bytes(M, N, K, L, R) bytes, which
+ *           never shrink as M grows either
  * Errors: as aql_linear_w8a16_dgrad and aql_linear_w8a16_lora;
  * AQL_ERR_WORKSPACE. M == 0 or N == 0 write what is left of the outputs
  * (zeros, unless they accumulate).

@@ -816,3 +816,27 @@ def test_empty_batches():
         _, _, hr, htol = ref_forward(c)
         assert y.shape == (M, 0)
         close(h, hr, htol, "h")
+
+
+def test_one_workspace_serves_smaller_batches():
+    """Buffers sized for the largest batch, filled with what no sum may take in, under
+    batches on both sides of the forms' edges; K and N split at some of them."""
+    N, K, L, R, most = 4096, 8192, 5, 8, 2048
+    full = dev(make(most, K, N, L, R, "random"))
+    fw = torch.empty(aql.aql_lora_forward_bytes(most, N, K, L, R), dtype=torch.uint8, device=DEV)
+    bw = torch.empty(aql.aql_lora_backward_bytes(most, N, K, L, R), dtype=torch.uint8, device=DEV)
+    dw = torch.empty(aql.aql_workspace_bytes(aql.AQL_OP_W8A16_DGRAD, most, N, K), dtype=torch.uint8,
+                     device=DEV)
+    for M in (2048, 1100, 512, 300, 130, 64, 63, 20, 1):
+        say("M", M)
+        d = dict(full, **{k: full[k][:M].contiguous() for k in ("x", "dy", "idx")})
+        y, h, plan = forward(d)
+        xq, xs = aql.aql_act_checkpoint(d["x"])
+        want = (y, h, *backward(d, plan, h, xq, xs), aql.aql_linear_w8a16_dgrad(d["dy"], d["q"], d["scale"]))
+        for w in (fw, bw, dw):
+            w.fill_(0xff)
+        y, h, _ = forward(d, plan, workspace=fw)
+        got = (y, h, *backward(d, plan, h, xq, xs, workspace=bw),
+               aql.aql_linear_w8a16_dgrad(d["dy"], d["q"], d["scale"], workspace=dw))
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), M

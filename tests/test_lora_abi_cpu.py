@@ -168,3 +168,29 @@ def test_arguments_that_are_no_tensors():
               lambda: aql.aql_linear_w8a16_dgrad(x, x, x)):
         with pytest.raises(ValueError, match="device tensor"):
             f()
+
+
+# Rows at and around every change of tiles, splits and forms.
+EDGES = sorted({m + d for m in (1, 12, 16, 32, 48, 64, 128, 192, 256, 320, 384, 448, 512, 576, 640,
+                                768, 1024, 1280, 2048, 2560, 4096, 8192) for d in (-1, 0, 1)
+                if m + d > 0} | set(range(1, 300, 7)) | {5000, 20480, 1048560})
+SIZES = [(4096, 14336, 1, 16), (4096, 4096, 1, 16), (14336, 4096, 8, 16), (4096, 14336, 3, 64),
+         (2560, 960, 2, 8), (960, 2560, 5, 128), (16, 8192, 1, 8), (64, 65536, 64, 32),
+         (4096, 4096, 1024, 128), (4096, 16, 6, 8), (12288, 1 << 23, 5, 8)]
+
+
+@pytest.mark.parametrize("N,K,A,R", SIZES)
+def test_a_workspace_of_a_large_batch_serves_smaller_ones(N, K, A, R):
+    """Sized once, for the most rows: no smaller batch may need more."""
+    fwd = [aql.aql_lora_forward_bytes(M, N, K, A, R) for M in EDGES]
+    dg = [aql.aql_workspace_bytes(aql.AQL_OP_W8A16_DGRAD, M, N, K) for M in EDGES]
+    bwd = [aql.aql_lora_backward_bytes(M, N, K, A, R) for M in EDGES]
+    for need in (fwd, dg, bwd):
+        assert need == sorted(need)
+    for top in (len(EDGES) - 1, EDGES.index(2048)):
+        for i in range(top + 1):
+            kw = dict(M=EDGES[i], N=N, K=K)
+            assert call(L.aql_linear_w8a16_lora, FWD, L=A, R=R, ws=P, ws_bytes=fwd[top], **kw) != WS
+            assert call(L.aql_linear_w8a16_dgrad, DG, ws_bytes=dg[top], **kw) != WS
+            assert call(L.aql_linear_w8a16_lora_backward, BWD, L=A, R=R, ws_bytes=bwd[top],
+                        **kw) != WS
