@@ -16,6 +16,12 @@ namespace {
 
 constexpr int kIlp = 4;  // groups in flight for 16 lanes
 
+// Groups of one launch, 4 threads each. A grid holds fewer than 2^32 threads, and of
+// a larger one only what is left over past 2^32 runs, without an error (2^30 + 5
+// rows of 4 values: all but the first 64 groups were left as they were).
+constexpr int64_t kSlice = 1 << 28;
+static_assert(kSlice % (16 * kIlp) == 0 && kSlice / (16 * kIlp) * 256 < (1LL << 32), "one grid");
+
 constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
 
 template <int CTRL>
@@ -95,12 +101,12 @@ __device__ __forceinline__ int place(bool live, int64_t m, int64_t gi, int l, in
 }
 
 template <bool BF16>
-__global__ __launch_bounds__(256) void k_act_checkpoint(const void *__restrict__ x, int64_t groups,
-                                                        int64_t K, int64_t G,
+__global__ __launch_bounds__(256) void k_act_checkpoint(const void *__restrict__ x, int64_t first,
+                                                        int64_t groups, int64_t K, int64_t G,
                                                         int8_t *__restrict__ xq,
                                                         float *__restrict__ xs) {
   const int l = threadIdx.x & 15;
-  const int64_t t0 = ((int64_t)blockIdx.x * 16 + (threadIdx.x >> 4)) * kIlp;
+  const int64_t t0 = first + ((int64_t)blockIdx.x * 16 + (threadIdx.x >> 4)) * kIlp;
   int64_t m = t0 / G, gi = t0 - m * G;
   float v[kIlp][8];
   int64_t at[kIlp];
@@ -144,10 +150,11 @@ __global__ __launch_bounds__(256) void k_act_checkpoint(const void *__restrict__
 
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_act_restore(const int8_t *__restrict__ xq,
-                                                     const float *__restrict__ xs, int64_t groups,
-                                                     int64_t K, int64_t G, void *__restrict__ x) {
+                                                     const float *__restrict__ xs, int64_t first,
+                                                     int64_t groups, int64_t K, int64_t G,
+                                                     void *__restrict__ x) {
   const int l = threadIdx.x & 15;
-  const int64_t t0 = ((int64_t)blockIdx.x * 16 + (threadIdx.x >> 4)) * kIlp;
+  const int64_t t0 = first + ((int64_t)blockIdx.x * 16 + (threadIdx.x >> 4)) * kIlp;
   int64_t m = t0 / G, gi = t0 - m * G;
   int w[kIlp][2];
   float s[kIlp];
@@ -190,28 +197,36 @@ __global__ __launch_bounds__(256) void k_act_restore(const int8_t *__restrict__ 
   }
 }
 
+// launch(first, grid) for slices of kSlice groups.
+template <class F>
+hipError_t slices(int64_t groups, F &&launch) {
+  for (int64_t first = 0; first < groups; first += kSlice) {
+    const int64_t n = groups - first < kSlice ? groups - first : kSlice;
+    launch(first, dim3((unsigned)((n + 16 * kIlp - 1) / (16 * kIlp))));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 }  // namespace
 
 hipError_t launch_act_checkpoint(const void *x, bool bf16, int64_t M, int64_t K, int8_t *xq,
                                  float *xs, hipStream_t st) {
   const int64_t G = (K + kCkptGroup - 1) / kCkptGroup, groups = M * G;
-  const dim3 grid((unsigned)((groups + 16 * kIlp - 1) / (16 * kIlp)));
-  if (bf16)
-    hipLaunchKernelGGL(k_act_checkpoint<true>, grid, dim3(256), 0, st, x, groups, K, G, xq, xs);
-  else
-    hipLaunchKernelGGL(k_act_checkpoint<false>, grid, dim3(256), 0, st, x, groups, K, G, xq, xs);
-  return hipGetLastError();
+  const auto kern = bf16 ? k_act_checkpoint<true> : k_act_checkpoint<false>;
+  return slices(groups, [&](int64_t first, dim3 grid) {
+    hipLaunchKernelGGL(kern, grid, dim3(256), 0, st, x, first, groups, K, G, xq, xs);
+  });
 }
 
 hipError_t launch_act_restore(const int8_t *xq, const float *xs, int64_t M, int64_t K, void *x,
                               bool bf16, hipStream_t st) {
   const int64_t G = (K + kCkptGroup - 1) / kCkptGroup, groups = M * G;
-  const dim3 grid((unsigned)((groups + 16 * kIlp - 1) / (16 * kIlp)));
-  if (bf16)
-    hipLaunchKernelGGL(k_act_restore<true>, grid, dim3(256), 0, st, xq, xs, groups, K, G, x);
-  else
-    hipLaunchKernelGGL(k_act_restore<false>, grid, dim3(256), 0, st, xq, xs, groups, K, G, x);
-  return hipGetLastError();
+  const auto kern = bf16 ? k_act_restore<true> : k_act_restore<false>;
+  return slices(groups, [&](int64_t first, dim3 grid) {
+    hipLaunchKernelGGL(kern, grid, dim3(256), 0, st, xq, xs, first, groups, K, G, x);
+  });
 }
 
 }  // namespace aql

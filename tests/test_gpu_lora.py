@@ -840,3 +840,33 @@ def test_one_workspace_serves_smaller_batches():
                aql.aql_linear_w8a16_dgrad(d["dy"], d["q"], d["scale"], workspace=dw))
         for a, b in zip(got, want):
             assert torch.equal(a, b), M
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_checkpoint_of_more_groups_than_a_launch_takes(dt):
+    """2^30 + 5 rows of 4: more threads than a grid may have. Blocks of 2^20 rows hold
+    the same numbers times a power of two, so codes repeat and scales follow it."""
+    n, reps, tail = 1 << 20, 1 << 10, 5
+    M = n * reps + tail
+    g = torch.Generator(device=DEV).manual_seed(5)
+    block = torch.randn(n, 4, generator=g, device=DEV).to(dt)
+    bq, bs = aql.aql_act_checkpoint(block)
+    power = (2.0 ** (torch.arange(reps, device=DEV) % 16))
+    x = torch.empty(M, 4, dtype=dt, device=DEV)
+    for i in range(reps):
+        torch.mul(block, float(2 ** (i % 16)), out=x[i * n:(i + 1) * n])
+    x[n * reps:] = block[:tail]
+    xq, xs = aql.aql_act_checkpoint(x)
+    say("saved", M)
+    body = n * reps
+    assert (xq[:body].view(reps, -1) == bq.view(1, -1)).all() and torch.equal(xq[body:], bq[:tail])
+    assert (xs[:body].view(reps, n) == bs.view(1, n) * power[:, None]).all()
+    assert torch.equal(xs[body:], bs[:tail])
+    want = aql.aql_act_restore(bq, bs, dt)
+    x.zero_()
+    aql.aql_act_restore(xq, xs, dt, x)
+    say("restored")
+    for i in range(0, reps, 31):
+        assert torch.equal(x[i * n:(i + 1) * n], want * float(2 ** (i % 16))), i
+    assert torch.equal(x[(reps - 1) * n:body], want * float(2 ** ((reps - 1) % 16)))
+    assert torch.equal(x[body:], want[:tail])
