@@ -136,6 +136,10 @@ int check_w8a16(const char *fn, const uint16_t *x, int64_t M, int64_t K, const i
   return AQL_OK;
 }
 
+// Channels of the linear with adapters: the streaming kernels' grids (up to 32 threads
+// a channel) and those of the adapters' products stay below 2^32 threads.
+constexpr int64_t kMaxNLora = 1 << 26;
+
 // Rows a 16-row tile grid of the W8A16 kernels can index.
 constexpr int64_t kMaxRows = 0xffff * 16LL;
 
@@ -258,7 +262,7 @@ hipError_t lora_products(aql::LoraTerm &lt, bool split, bool kmajor, int64_t M, 
   return aql::launch_lora_products(lt.h, lt.W, kmajor, M, lt.N, L, lt.R, p, lt.mixed, T, st);
 }
 bool lora_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
-  return plan_sizes_ok(M, L) && M > 0 && N >= 0 && K >= 16 && K <= kMaxKW8A16 && R >= 8 &&
+  return plan_sizes_ok(M, L) && M > 0 && N >= 0 && N <= kMaxNLora && K >= 16 && K <= kMaxKW8A16 && R >= 8 &&
          R <= AQL_LORA_MAX_RANK && R % 8 == 0;
 }
 
@@ -728,6 +732,8 @@ int aql_linear_w8a16_lora(const uint16_t *x, int64_t M, int64_t K, const int8_t 
                           void *stream) {
   const char *fn = "aql_linear_w8a16_lora";
   if (int e = check_w8a16(fn, x, M, K, q, scale, bias, N, y)) return e;
+  REQUIRE(N <= kMaxNLora, AQL_ERR_SHAPE, "%s: need N <= %lld (N=%lld)", fn, (long long)kMaxNLora,
+          (long long)N);
   if (int e = check_lora(fn, A, B, alpha, L, R, plan, h)) return e;
   REQUIRE(aligned16(ws), AQL_ERR_ALIGN, "%s: ws must be 16-byte aligned", fn);
   if (M == 0) return ok();

@@ -435,7 +435,7 @@ constexpr bool lora_split_products(bool kmajor, int64_t M, int64_t C, int64_t R)
 
 // T[m, n] = sum_j h[m, j] W[a][n, j] (float32 [M, N]) for the rows with an adapter,
 // where mixed is given only those in its groups; other rows stay as they are.
-// kmajor: W is [L, R, N].
+// kmajor: W is [L, R, N]. 1 <= N <= 2^26.
 hipError_t launch_lora_products(const float *h, const uint16_t *W, bool kmajor, int64_t M,
                                 int64_t N, int64_t L, int64_t R, const int32_t *plan,
                                 const int32_t *mixed, float *T, hipStream_t st);

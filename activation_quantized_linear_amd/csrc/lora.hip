@@ -579,9 +579,10 @@ __global__ __launch_bounds__(256) void k_lora_products(const float *__restrict__
                                                        int64_t N, int64_t L, int R,
                                                        const int32_t *__restrict__ plan,
                                                        const int32_t *__restrict__ mixed,
-                                                       int blocks, float *__restrict__ T) {
+                                                       int first, int blocks,
+                                                       float *__restrict__ T) {
   const LoraPlanLayout p = lora_plan_layout(M, L);
-  const int tile = blockIdx.x / blocks;  // blocks of columns
+  const int tile = first + blockIdx.x / blocks;  // blocks of columns
   const int a = plan[p.owner + tile];
   if (a < 0) return;
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, wave = threadIdx.x >> 6;
@@ -765,15 +766,19 @@ hipError_t launch_lora_shrink_t(const uint16_t *dy, int64_t M, int64_t N, const 
 hipError_t launch_lora_products(const float *h, const uint16_t *W, bool kmajor, int64_t M,
                                 int64_t N, int64_t L, int64_t R, const int32_t *plan,
                                 const int32_t *mixed, float *T, hipStream_t st) {
-  const int64_t blocks = (N + 255) / 256;
-  const dim3 grid((unsigned)(lora_plan_layout(M, L).tiles * blocks));
-  if (kmajor)
-    hipLaunchKernelGGL(k_lora_products<true>, grid, dim3(256), 0, st, h, W, M, N, L, (int)R, plan,
-                       mixed, (int)blocks, T);
-  else
-    hipLaunchKernelGGL(k_lora_products<false>, grid, dim3(256), 0, st, h, W, M, N, L, (int)R, plan,
-                       mixed, (int)blocks, T);
-  return hipGetLastError();
+  const int64_t tiles = lora_plan_layout(M, L).tiles, blocks = (N + 255) / 256;
+  // grids of at most 2^31 threads (one of 2^32 or more would run in part): 1089 tiles of
+  // 2^22 channels take three, ordinary batches one
+  const int64_t slice = (1LL << 31) / 256 / blocks;
+  const auto kern = kmajor ? k_lora_products<true> : k_lora_products<false>;
+  for (int64_t first = 0; first < tiles; first += slice) {
+    const int64_t n = tiles - first < slice ? tiles - first : slice;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(n * blocks)), dim3(256), 0, st, h, W, M, N, L, (int)R,
+                       plan, mixed, (int)first, (int)blocks, T);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // Workgroups of the weight gradients, each 64 channels or 128 inputs of an adapter and

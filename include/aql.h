@@ -391,7 +391,7 @@ int aql_lora_plan(const int32_t *idx, int64_t M, int64_t L, void *plan, size_t p
  *   ws      device workspace of aql_lora_forward_bytes(M, N, K, L, R) bytes (may be
  *           NULL where that is 0). It never shrinks as M grows: one of the
  *           largest batch serves the others.
- * Errors: as aql_linear_w8a16, plus R not a multiple of 8 in
+ * Errors: as aql_linear_w8a16, plus N > 2^26, R not a multiple of 8 in
  * 8..AQL_LORA_MAX_RANK, L outside 1..AQL_LORA_MAX_ADAPTERS, NULL or misaligned
  * A, B, alpha, plan or h, workspace too small. N == 0 writes h alone.
  */

@@ -870,3 +870,28 @@ def test_checkpoint_of_more_groups_than_a_launch_takes(dt):
         assert torch.equal(x[i * n:(i + 1) * n], want * float(2 ** (i % 16))), i
     assert torch.equal(x[(reps - 1) * n:body], want * float(2 ** ((reps - 1) % 16)))
     assert torch.equal(x[body:], want[:tail])
+
+
+def test_products_of_more_tiles_than_a_launch_takes():
+    """1089 tiles of the plan by 15470 blocks of columns are more threads than one grid
+    may have (1024 adapters of 8 ranks, 3.96e6 channels: B holds 65 GB)."""
+    M, K, N, L, R = 1025, 16, 3960001, 1024, 8
+    g = torch.Generator(device=DEV).manual_seed(8)
+    B = torch.empty(L, N, R, dtype=torch.bfloat16, device=DEV).normal_(0, 0.02, generator=g)
+    c = make(M, K, 8, L, R, "random")
+    perm = torch.randperm(M, generator=workloads.gen(6))
+    c["idx"] = (perm - 1).to(torch.int32)  # an adapter for every row but one
+    d = dev(c)
+    d["q"] = torch.randint(-127, 128, (N, K), generator=g, device=DEV, dtype=torch.int8)
+    d["scale"] = torch.rand(N, generator=g, device=DEV) * 1e-3
+    d["B"] = B
+    say("start", M, N, L)
+    y, h, _ = forward(d)
+    torch.cuda.synchronize()
+    cols = torch.cat([torch.randint(0, N, (60,), generator=workloads.gen(7)),
+                      torch.tensor([0, 255, 256, N - 257, N - 2, N - 1])])
+    at = cols.to(DEV)
+    part = dict(c, q=d["q"][at].cpu(), scale=d["scale"][at].cpu(), B=B[:, at].cpu())
+    ry, tol, rh, htol = ref_forward(part)
+    close(h, rh, htol, "h")
+    close(y[:, at], ry, tol, "y", norm=4e-3)

@@ -194,3 +194,14 @@ def test_a_workspace_of_a_large_batch_serves_smaller_ones(N, K, A, R):
             assert call(L.aql_linear_w8a16_dgrad, DG, ws_bytes=dg[top], **kw) != WS
             assert call(L.aql_linear_w8a16_lora_backward, BWD, L=A, R=R, ws_bytes=bwd[top],
                         **kw) != WS
+
+
+def test_forward_channels():
+    """More channels than one grid of the streaming kernels holds are refused."""
+    wide = dict(N=(1 << 26) + 1)
+    assert aql.aql_lora_forward_bytes(5, 1 << 26, 64, 3, 8) == 0  # few rows need none
+    assert aql.aql_lora_forward_bytes(64, 1 << 26, 64, 5, 8) > 0
+    assert aql.aql_lora_forward_bytes(64, wide["N"], 64, 5, 8) == 0
+    assert call(L.aql_linear_w8a16_lora, FWD, **wide) == SHAPE
+    assert "N <= 67108864" in aql.aql_last_error()
+    assert call(L.aql_linear_w8a16_lora, FWD, N=1 << 26) != SHAPE
