@@ -21,6 +21,11 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+// Whether a grid of this many workgroups (of its first dimension) can be started:
+// below 2^32 threads. The runtime does not refuse a larger one, it starts only what is
+// left over past 2^32, so launchers whose sizes can get there ask first.
+inline bool grid_fits(int64_t groups, int64_t threads) { return groups * threads < (1LL << 32); }
+
 // ------------------------------------------------------------ device helpers
 
 __device__ __forceinline__ float clamp_code(float v, float lo, float hi) {

@@ -309,6 +309,7 @@ __global__ __launch_bounds__(512) void k_gemm_i8(GemmArgs p, int tiles_m, int ti
 
 template <int EPI, int MODE>
 hipError_t launch_one(const GemmArgs &a, int tiles_m, int tiles_n, hipStream_t st) {
+  if (!grid_fits((int64_t)tiles_m * tiles_n, 512)) return hipErrorInvalidConfiguration;
   // More than 64 KB of dynamic LDS: raise the function's limit once. Its status
   // is not needed: a launch the limit does not allow reports its own error.
   static bool attr_set = false;

@@ -138,6 +138,7 @@ hipError_t quant_w8_dispatch(const void *w, int64_t N, int64_t K, float den, flo
                              float *scale, int32_t *wsum, hipStream_t st) {
   const int64_t nvec = K / 4;
   if (nvec <= 64 * 4) {
+    if (!grid_fits((N + 3) / 4, 256)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)((N + 3) / 4));
     if (nvec <= 64)
       hipLaunchKernelGGL((k_quantize_weight_int8<BF16, 64, 1>), grid, dim3(256), 0, st, w, N, K,
@@ -149,6 +150,7 @@ hipError_t quant_w8_dispatch(const void *w, int64_t N, int64_t K, float den, flo
       hipLaunchKernelGGL((k_quantize_weight_int8<BF16, 64, 4>), grid, dim3(256), 0, st, w, N, K,
                          den, lo, q, scale, wsum);
   } else {
+    if (!grid_fits(N, 256)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)N);
     if (nvec <= 256 * 2)
       hipLaunchKernelGGL((k_quantize_weight_int8<BF16, 256, 2>), grid, dim3(256), 0, st, w, N, K,
@@ -386,6 +388,7 @@ hipError_t cq_dispatch(const float *x, int64_t M, int64_t K, float *scale, int32
                        void *xq, hipStream_t st) {
   const int64_t nvec = K / 4;
   if (nvec <= 64 * 4) {
+    if (!grid_fits((M + 3) / 4, 256)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)((M + 3) / 4));
     if (nvec <= 64)
       hipLaunchKernelGGL((k_choose_qparams_rows<64, 1, PERM>), grid, dim3(256), 0, st, x, M, K,
@@ -397,6 +400,7 @@ hipError_t cq_dispatch(const float *x, int64_t M, int64_t K, float *scale, int32
       hipLaunchKernelGGL((k_choose_qparams_rows<64, 4, PERM>), grid, dim3(256), 0, st, x, M, K,
                          scale, zp, xq);
   } else {
+    if (!grid_fits(M, 256)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)M);
     if (nvec <= 256 * 2)
       hipLaunchKernelGGL((k_choose_qparams_rows<256, 2, PERM>), grid, dim3(256), 0, st, x, M, K,

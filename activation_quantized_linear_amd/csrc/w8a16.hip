@@ -1374,6 +1374,8 @@ hipError_t launch_m1_or_sk(const W8A16Shape &sh, const uint16_t *x, int64_t M, i
   if (sh.mblocks == 0) {
     if (M != 1 || !m1_shape_ok(sh) || (sh.xlds && sh.xlds < 2 * K)) return hipErrorInvalidValue;
     const int64_t rows = 4 * M1_TG * sh.cgroups;
+    if (!grid_fits((N + rows - 1) / rows, 64 * sh.waves * sh.cgroups))
+      return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)((N + rows - 1) / rows)), block(64 * sh.waves * sh.cgroups);
     m1_dispatch(sh.waves, sh.cgroups, sh.xlds > 0, [&](auto w, auto c, auto xl) {
       hipLaunchKernelGGL(
@@ -1383,6 +1385,7 @@ hipError_t launch_m1_or_sk(const W8A16Shape &sh, const uint16_t *x, int64_t M, i
     return hipGetLastError();
   }
   const int64_t rows = 4 * sh.tgroups;
+  if (!grid_fits((N + rows - 1) / rows, 64 * sh.waves)) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)((N + rows - 1) / rows), (unsigned)((M + 15) / 16));
   if (sh.tgroups == 8) launch_sk_single<2>(sh.waves, grid, st, x, M, K, q, scale, bias, N, y, lt);
   else launch_sk_single<1>(sh.waves, grid, st, x, M, K, q, scale, bias, N, y, lt);
@@ -1397,6 +1400,7 @@ hipError_t launch_w8a16_shape(const W8A16Shape &sh, const uint16_t *x, int64_t M
   if (sh.mblocks == 0 || sh.mblocks == kW8A16Skinny)
     return launch_m1_or_sk(sh, x, M, K, q, scale, bias, N, y, st, NoLora{});
   const int64_t rows = 4 * sh.tgroups;
+  if (!grid_fits((N + rows - 1) / rows, 64 * sh.waves)) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)((N + rows - 1) / rows), (unsigned)((M + 15) / 16));
   switch (sh.tgroups) {
     case 1: launch_single_tg<1>(sh.mblocks, sh.waves, grid, st, x, M, K, q, scale, bias, N, y); break;
@@ -1412,6 +1416,7 @@ template <class LT>
 hipError_t launch_m1c(const uint16_t *x, int64_t K, const int8_t *q, const float *scale,
                       const uint16_t *bias, int64_t N, uint16_t *y, hipStream_t st, const LT &lt) {
   if (K < kW8A16ContigMinK || K > kW8A16ContigMaxK || K % 16) return hipErrorInvalidValue;
+  if (!grid_fits((N + 7) / 8, 256)) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)((N + 7) / 8));
   // 4 waves split K, each with one or two pieces of 1 KB per row; one piece
   // per row is consumed in batches of 2 loads (K = 4096, N = 14336: 10.66 us
@@ -1436,6 +1441,7 @@ hipError_t launch_w8a16_m1c(const uint16_t *x, int64_t K, const int8_t *q, const
 
 hipError_t launch_w8a16_m1p_grouped(const W8A16GroupEntry *dev_tab, const W8A16GroupEntry *host_tab,
                                     int count, int total_blocks, hipStream_t st) {
+  if (!grid_fits(total_blocks, 256)) return hipErrorInvalidConfiguration;
   if (host_tab && count >= 1 && count <= kW8A16InlineMax) {
     W8A16InlineGroup g = {};
     for (int i = 0; i < count; ++i) g.e[i] = host_tab[i];
@@ -1460,6 +1466,7 @@ hipError_t launch_mfew(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
                        const LT &lt) {
   if (M < 2 || M > kW8A16FewMaxM || K < kW8A16FewMinK || K > kW8A16FewMaxK || K % 16)
     return hipErrorInvalidValue;
+  if (!grid_fits((N + 7) / 8, 512)) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)((N + 7) / 8));
   auto go = [&](auto kern, int W) {
     hipLaunchKernelGGL(kern, grid, dim3(64 * W), 0, st, x, M, K, q, scale, bias, N, y, lt);
@@ -1511,6 +1518,7 @@ hipError_t launch_stream(const uint16_t *x, int64_t M, int64_t K, const int8_t *
     // are 192 workgroups a row block, else two (M = 16: K = 4096, N = 14336:
     // 14.2 us against 17.8 for the skinny tile; N = 11008: 13.0 vs 17.0;
     // K = N = 8192: 20.0 vs 22.4)
+    if (!grid_fits((N + 63) / 64, 512)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)((N + 63) / 64), (unsigned)((M + 15) / 16));
     if (N >= 12288 && K <= 4096)
       hipLaunchKernelGGL((k_w8a16_sksh<4, 1, LT>), grid, dim3(256), 0, st, x, M, K, q, scale, bias, N, y, nullptr, 0, lt);
@@ -1559,6 +1567,8 @@ hipError_t launch_w8a16(const uint16_t *x, int64_t M, int64_t K, const int8_t *q
 
 hipError_t launch_w8a16_grouped(const W8A16GroupEntry *dev_tab, int count, int total_blocks,
                                 const W8A16Shape &sh, hipStream_t st) {
+  if (!grid_fits(total_blocks, 64 * sh.waves * (sh.mblocks == 0 ? sh.cgroups : 1)))
+    return hipErrorInvalidConfiguration;
   if (sh.mblocks == 0) {
     if (!m1_shape_ok(sh)) return hipErrorInvalidValue;
     const dim3 grid((unsigned)total_blocks), block(64 * sh.waves * sh.cgroups);
