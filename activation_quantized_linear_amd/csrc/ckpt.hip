@@ -7,12 +7,16 @@
 // 16 lanes hold a group, 8 values a lane (16 bytes of bf16), so a group's maximum
 // takes four DPP moves and no LDS, and a lane packs its codes into one 8-byte
 // store. Groups are numbered over the whole matrix; 16 lanes take kIlp of them at
-// once to keep enough loads in flight. Rows whose length is not a multiple of 8
-// move in fours.
+// once to keep enough loads in flight. Where K is an odd multiple of 4, a row's last
+// lane moves 4 values, and odd rows begin at half of such an access's size, which
+// global memory takes as it is; the types below say so.
 #include "ckpt.h"
 
 namespace aql {
 namespace {
+
+typedef int i32x4_8 __attribute__((ext_vector_type(4), aligned(8)));  // 8 bf16 of such a row
+typedef int i32x2_4 __attribute__((ext_vector_type(2), aligned(4)));  // 8 codes of one
 
 constexpr int kIlp = 4;  // groups in flight for 16 lanes
 
@@ -49,7 +53,7 @@ __device__ __forceinline__ void load8(const void *x, int64_t i, int n, float (&v
     const uint16_t *p = static_cast<const uint16_t *>(x) + i;
     i32x4 d = {0, 0, 0, 0};
     if (n == 8) {
-      d = *reinterpret_cast<const i32x4 *>(p);
+      d = *reinterpret_cast<const i32x4_8 *>(p);
     } else if (n) {
       const i32x2 h = *reinterpret_cast<const i32x2 *>(p);
       d[0] = h[0];
@@ -141,7 +145,7 @@ __global__ __launch_bounds__(256) void k_act_checkpoint(const void *__restrict__
                      << (8 * (e & 3));
     }
     if (n[u] == 8)
-      *reinterpret_cast<i32x2 *>(xq + at[u]) = i32x2{(int)w[0], (int)w[1]};
+      *reinterpret_cast<i32x2_4 *>(xq + at[u]) = i32x2{(int)w[0], (int)w[1]};
     else if (n[u])
       *reinterpret_cast<uint32_t *>(xq + at[u]) = w[0];
   }
@@ -165,7 +169,7 @@ __global__ __launch_bounds__(256) void k_act_restore(const int8_t *__restrict__ 
     n[u] = place(t0 + u < groups, m, gi, l, K, at[u]);
     w[u][0] = w[u][1] = 0;
     if (n[u] == 8) {
-      const i32x2 d = *reinterpret_cast<const i32x2 *>(xq + at[u]);
+      const i32x2 d = *reinterpret_cast<const i32x2_4 *>(xq + at[u]);
       w[u][0] = d[0];
       w[u][1] = d[1];
     } else if (n[u]) {
@@ -187,7 +191,7 @@ __global__ __launch_bounds__(256) void k_act_restore(const int8_t *__restrict__ 
         d[e] = (int)((uint32_t)f32_to_bf16_rne(v[2 * e]) |
                      ((uint32_t)f32_to_bf16_rne(v[2 * e + 1]) << 16));
       uint16_t *p = static_cast<uint16_t *>(x) + at[u];
-      if (n[u] == 8) *reinterpret_cast<i32x4 *>(p) = d;
+      if (n[u] == 8) *reinterpret_cast<i32x4_8 *>(p) = d;
       else *reinterpret_cast<i32x2 *>(p) = i32x2{d[0], d[1]};
     } else {
       float *p = static_cast<float *>(x) + at[u];
