@@ -702,12 +702,14 @@ def aql_lora_backward_bytes(M, N, K, L, R):
 
 
 def aql_linear_w8a16_lora_backward(dy, q, scale, A, B, alpha, plan, h, xq, xs, dx=None, dA=None,
-                                   dB=None, accumulate=False, need_dx=True, workspace=None):
+                                   dB=None, accumulate=False, need_dx=True, workspace=None,
+                                   need_dA=True, need_dB=True):
     """Backward pass of aql_linear_w8a16_lora. dy bfloat16 [M, N]; h float32 [M, R] of the
     forward pass; xq int8 [M, K], xs float32 [M, ceil(K / 128)]: the checkpoint of x
-    (aql_act_checkpoint) -> (dx bfloat16 [M, K] or None, dA float32 [L, R, K],
+    (aql_act_checkpoint) -> (dx bfloat16 [M, K], dA float32 [L, R, K],
     dB float32 [L, N, R]). accumulate=True adds to the given dA and dB.
-    need_dx=False leaves dx out. workspace: uint8 device tensor of
+    need_dx, need_dA, need_dB = False leave an output out (None in its place); without
+    dA, xq and xs may be None. workspace: uint8 device tensor of
     aql_lora_backward_bytes; allocated here when none is given."""
     di = _dev_index(dy, "dy", torch.bfloat16, 2)
     M, N = dy.shape
@@ -719,19 +721,24 @@ def aql_linear_w8a16_lora_backward(dy, q, scale, A, B, alpha, plan, h, xq, xs, d
             _fit(A, "A", torch.bfloat16, (L, R, K), di),
             _fit(B, "B", torch.bfloat16, (L, N, R), di),
             _fit(alpha, "alpha", torch.float32, (L,), di), L, R, _lora_plan(plan, M, L, di),
-            _fit(h, "h", torch.float32, (M, R), di), _fit(xq, "xq", torch.int8, (M, K), di),
-            _fit(xs, "xs", torch.float32, (M, G), di), 1 if accumulate else 0)
-    if accumulate and (dA is None or dB is None):
+            _fit(h, "h", torch.float32, (M, R), di),
+            None if xq is None and not need_dA else _fit(xq, "xq", torch.int8, (M, K), di),
+            None if xs is None and not need_dA else _fit(xs, "xs", torch.float32, (M, G), di),
+            1 if accumulate else 0)
+    if accumulate and (need_dA and dA is None or need_dB and dB is None):
         raise ValueError("accumulate needs the dA and dB to add to")
     if dx is not None and not need_dx:
         raise ValueError("dx is given but need_dx is False")
+    if dA is not None and not need_dA or dB is not None and not need_dB:
+        raise ValueError("dA or dB is given but need_dA or need_dB is False")
     dev = dy.device
     dx = _new(dx, "dx", (M, K), torch.bfloat16, dev) if need_dx else None
-    dA = _new(dA, "dA", (L, R, K), torch.float32, dev)
-    dB = _new(dB, "dB", (L, N, R), torch.float32, dev)
+    dA = _new(dA, "dA", (L, R, K), torch.float32, dev) if need_dA else None
+    dB = _new(dB, "dB", (L, N, R), torch.float32, dev) if need_dB else None
     ws, ws_bytes, _owner = _scratch(workspace, _lib.aql_lora_backward_bytes(M, N, K, L, R), dev)
     _call("aql_linear_w8a16_lora_backward", _lib.aql_linear_w8a16_lora_backward, di, *args,
-          dx.data_ptr() if need_dx else None, dA.data_ptr(), dB.data_ptr(), ws, ws_bytes)
+          dx.data_ptr() if need_dx else None, dA.data_ptr() if need_dA else None,
+          dB.data_ptr() if need_dB else None, ws, ws_bytes)
     return dx, dA, dB
 
 

@@ -895,3 +895,68 @@ def test_products_of_more_tiles_than_a_launch_takes():
     ry, tol, rh, htol = ref_forward(part)
     close(h, rh, htol, "h")
     close(y[:, at], ry, tol, "y", norm=4e-3)
+
+
+# a sum of splits beside the weight gradients, alone and with the products given
+# ahead; no split
+SUBSETS = [(63, 960, 2560, 2, 8), (300, 4096, 1040, 6, 64), (100, 256, 136, 4, 16)]
+
+
+@pytest.mark.parametrize("M,K,N,L,R", SUBSETS)
+def test_backward_of_some_outputs(M, K, N, L, R):
+    """Each subset of dx, dA and dB. dx does not depend on the others to the bit; the
+    weight gradients' sums may take another order, so they go by their bounds."""
+    c = make(M, K, N, L, R, "random")
+    d = dev(c)
+    _, h, plan = forward(d)
+    xq, xs = aql.aql_act_checkpoint(d["x"])
+    dx, _, _ = backward(d, plan, h, xq, xs)
+    refs = ref_backward(c, h.cpu(), xq.cpu(), xs.cpu())
+    for bits in range(8):
+        need = dict(need_dx=bool(bits & 1), need_dA=bool(bits & 2), need_dB=bool(bits & 4))
+        say(M, K, N, L, R, need)
+        ck = (xq, xs) if need["need_dA"] else (None, None)
+        got = backward(d, plan, h, *ck, **need)
+        for name, g, (ref, tol) in zip(("dx", "dA", "dB"), got, refs):
+            assert (g is not None) == need["need_" + name]
+            if g is not None:
+                close(g, ref, tol, name)
+        assert got[0] is None or torch.equal(got[0], dx)
+    a = torch.empty(L, R, K, device=DEV)
+    for kw in (dict(need_dA=False, dA=a), dict(need_dB=False, dB=torch.empty(L, N, R, device=DEV)),
+               dict(accumulate=True, dA=a), dict(accumulate=True, need_dA=False)):
+        with pytest.raises(ValueError):
+            backward(d, plan, h, xq, xs, **kw)
+    with pytest.raises(TypeError):
+        backward(d, plan, h, None, None)
+
+
+@pytest.mark.parametrize("M,K,N,L,R", SUBSETS)
+def test_backward_accumulates_in_every_form(M, K, N, L, R):
+    c = make(M, K, N, L, R, "random")
+    c["idx"][c["idx"] == 1] = -1  # adapter 1: no rows
+    d = dev(c)
+    _, h, plan = forward(d)
+    xq, xs = aql.aql_act_checkpoint(d["x"])
+    dx, dA, dB = backward(d, plan, h, xq, xs)
+    assert not dA[1].any() and not dB[1].any()
+    a0, b0 = torch.randn_like(dA), torch.randn_like(dB)
+    for need_dx in (True, False):
+        _, sA, sB = backward(d, plan, h, xq, xs, need_dx=need_dx)
+        a, b = a0.clone(), b0.clone()
+        got = backward(d, plan, h, xq, xs, dA=a, dB=b, accumulate=True, need_dx=need_dx)
+        assert got[1] is a and got[2] is b
+        assert torch.equal(a, a0 + sA) and torch.equal(b, b0 + sB)
+        assert torch.equal(got[0], dx) if need_dx else got[0] is None
+    _, onlyA, _ = backward(d, plan, h, xq, xs, need_dx=False, need_dB=False)
+    a = a0.clone()
+    backward(d, plan, h, xq, xs, dA=a, accumulate=True, need_dx=False, need_dB=False)
+    assert torch.equal(a, a0 + onlyA)
+
+
+def test_empty_backward_of_some_outputs():
+    d = dev(make(0, 64, 32, 2, 8, "none"))
+    _, h, plan = forward(d)
+    dx, dA, dB = backward(d, plan, h, None, None, need_dA=False)
+    assert dx.shape == (0, 64) and dA is None and not dB.any()
+    assert backward(d, plan, h, None, None, need_dA=False, need_dB=False, need_dx=False) == (None,) * 3
