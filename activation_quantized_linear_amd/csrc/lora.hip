@@ -14,12 +14,11 @@
 // Every sum has one order, so results repeat bit for bit.
 #include "lora.h"
 
+#include "ckpt.h"
 #include "w8a16_dgrad.h"
 
 namespace aql {
 namespace {
-
-constexpr int kGroup = 128;  // columns of a checkpoint scale
 
 // ------------------------------------------------------------------ the plan
 
@@ -389,11 +388,12 @@ template <int W, int RT, bool CODES>
 __device__ __forceinline__ void lora_wgrad(const LoraWgradArgs &p, const LoraPlanLayout &pl,
                                            int64_t a, int64_t c0, int j0, char *smem) {
   constexpr int CW = CODES ? 8 : 4;
+  static_assert(!CODES || 16 * CW == kCkptGroup, "a workgroup's columns share a scale");
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t C = CODES ? p.K : p.N;
   const int R = (int)p.R;
-  const int64_t G = (p.K + kGroup - 1) / kGroup;
+  const int64_t G = (p.K + kCkptGroup - 1) / kCkptGroup;
   const int32_t *perm = p.plan + pl.perm;
   const int first = p.plan[pl.first + a] * kLoraTile, last = p.plan[pl.first + a + 1] * kLoraTile;
   const float *left = CODES ? p.u : p.h;
@@ -428,7 +428,7 @@ __device__ __forceinline__ void lora_wgrad(const LoraWgradArgs &p, const LoraPla
         else
           b.d[e] = *reinterpret_cast<const i32x2 *>(p.dy + (int64_t)row[e] * C + col);
       }
-      if constexpr (CODES) b.s[e] = in ? p.xs[(int64_t)row[e] * G + c0 / kGroup] : 0.0f;
+      if constexpr (CODES) b.s[e] = in ? p.xs[(int64_t)row[e] * G + c0 / kCkptGroup] : 0.0f;
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         const int j = j0 + 16 * t + r;
@@ -706,13 +706,7 @@ constexpr int kWgradWaves = 2800;
 template <int W, int RT>
 hipError_t go_wgrad(const LoraWgradArgs &a, hipStream_t st) {
   constexpr int bytes = W / 2 * RT * 8 * 64 * 16;
-  static bool attr_set = false;
-  if (bytes > 65536 && !attr_set) {
-    (void)hipFuncSetAttribute((const void *)k_lora_wgrad<W, RT>,
-                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    (void)hipGetLastError();
-    attr_set = true;
-  }
+  static_assert(bytes <= 65536, "what any launch may have of LDS");
   const int tb = a.dB ? (int)((a.N + 63) / 64) : 0, ta = a.dA ? (int)((a.K + 127) / 128) : 0;
   const dim3 grid((unsigned)(tb + ta), (unsigned)a.L, (unsigned)((a.R + 16 * RT - 1) / (16 * RT)));
   hipLaunchKernelGGL((k_lora_wgrad<W, RT>), grid, dim3(64 * W), bytes, st, a, tb);
