@@ -1,8 +1,10 @@
 // Activation checkpoints in 8 bits: per row and group of 128 columns
 //   s = max |x| / 127 (1 where that is 0), code = clamp(rint(x / s), -127, 127)
 // and back, x' = code * s. One pass over the data each way, bound by memory:
-// 3 bytes a value (bf16) plus 4 bytes a group (8192 x 14336 bf16: 67 us, 5.3 TB/s to
-// codes, 64 us, 5.6 TB/s back; a copy of such a size runs at 5.0).
+// 3 bytes a value (bf16) plus 4 bytes a group (8192 x 14336 bf16: 68 us, 5.2 TB/s to
+// codes, 64 us, 5.6 TB/s back, each in a run of its own; in turn 81 and 56, the save
+// behind the restore's writes and the restore on codes still in cache. 4096 x 14336
+// float32 in turn: 69 and 46. A copy of such a size runs at 5.0).
 //
 // 16 lanes hold a group, 8 values a lane (16 bytes of bf16), so a group's maximum
 // takes four DPP moves and no LDS, and a lane packs its codes into one 8-byte

@@ -20,7 +20,12 @@ constexpr int kLoraMaxAdapters = 1024;
 constexpr int kLoraHeader = 16;  // [0] tiles in use
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraGroup = 128;  // rows of the largest tile of the tiled kernels
-constexpr int kLoraFew = 4;      // adapters of a group that they take in their epilogues
+// Adapters of a group that they take in their epilogues; with more the products are
+// computed ahead. Both sides, walked and ahead, us a call in a graph, R = 16: M = 128,
+// N = 14336, K = 4096, 3 adapters 45.2, 47.4, 4 47.8, 47.3, 5 50.4, 47.5, 8 59.0, 47.5;
+// M = 2048, N = K = 4096, 3 84.8, 89.6, 4 88.5, 90.4, 6 96.1, 90.2, 8 102.6, 91.2; backward
+// there, 2 93.3, 101.9, 4 100.6, 101.4, 6 111.9, 105.1.
+constexpr int kLoraFew = 4;
 
 struct LoraPlanLayout {
   int64_t tiles;     // tiles a batch of M rows over L adapters can need
@@ -167,7 +172,9 @@ __device__ __forceinline__ void lora_shrink_rows(const uint16_t *x, int64_t K, c
 
 // Eight floats -> bf16 parts with v = hi + lo up to 2^-16 |v| (both rounded to
 // nearest, 2^-8 each): products with bf16 operands then cost two matrix instructions and
-// keep the float32 operand's precision well below the output's rounding.
+// keep the float32 operand's precision well below the output's rounding. (A finite
+// value past bfloat16's largest, 3.396e38 and more, rounds to an infinity and counts
+// as one.)
 __device__ __forceinline__ void split_bf16(const float (&v)[8], bf16x8 &hi, bf16x8 &lo) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -197,8 +204,9 @@ __device__ __forceinline__ void split_bf16(const float (&v)[8], bf16x8 &hi, bf16
 // with the adapter's ranks of the tile's columns beside it, and every block takes
 // two matrix instructions for 32 ranks. Products are added through a select by
 // row, so no value of one adapter (an infinity or a NaN in it among them) reaches
-// a row of another. A step costs 3 to 5 us (M = 500, N = 14336, K = 4096 backward: 56 us
-// without adapters, 62 with one of up to 64 ranks, 68 with two in a tile): its
+// a row of another. A step costs 4 to 5 us (input gradient's kernel at M = 500, N = 4096,
+// K = 14336: 55.9 us without adapters, 60.2 with one of 64 ranks, 65.0 with two in a
+// tile): its
 // loads, their split and the products follow each other, and neither loading a
 // step ahead nor interleaving the blocks by hand shortened the whole, the first
 // for want of registers beside the accumulators.
@@ -424,11 +432,13 @@ hipError_t launch_lora_shrink_t(const uint16_t *dy, int64_t M, int64_t N, const 
                                 float *u, float *part, const DgradScale *sc, hipStream_t st);
 
 // Whether a split kernel's sum of M x C outputs is better given their products
-// than left to compute each, R multiply-adds with R ranks read for it (M = 500, C =
-// 4096, R = 64, K = 14336: 99 us of the whole call, 148; M = 300, R = 16: 81, 83, R = 8:
-// 77, 73). With the contraction as W's slow axis (kmajor) neighbouring outputs share
-// lines, so later (backward at M = 500, R = 128, N = K = 4096: 70 us, 96; M = 300, R =
-// 16: 46, 43).
+// than left to compute each, R multiply-adds with R ranks read for it. Whole calls in
+// a graph, products given and left, C = 4096, K = 14336: M = 500, R = 64 101.7 us, 143.6;
+// M = 128, R = 32 (2^24) 53.2, 56.1; M = 256, R = 16 (2^24) 61.5, 62.5; M = 128, R = 16
+// 52.7, 51.9; M = 256, R = 8 61.1, 56.9. With the contraction as W's slow axis (kmajor)
+// neighbouring outputs share lines, so later (backward, C = K = 4096: M = 500, R = 128
+// 72.0, 98.2; R = 32 (2^26) 48.6, 49.7; M = 256, R = 64 (2^26) 43.3, 44.9; M = 256, R = 32
+// 37.2, 35.9; M = 500, R = 16 46.7, 44.1; M = 128, R = 64 (2^25) 37.4, 38.8).
 constexpr bool lora_split_products(bool kmajor, int64_t M, int64_t C, int64_t R) {
   return M * C * R >= (kmajor ? 1 << 26 : 1 << 24);
 }

@@ -28,7 +28,8 @@ namespace {
 // is the number of equal rows before it in its wave (ballots) plus the counts
 // of the waves before (a byte table), so rows keep their order in a segment.
 // One launch a batch, for all its layers: bound by its barriers and round trips
-// (M = 500: 5.9 us, M = 2048: 8.4), which one workgroup keeps few.
+// (M = 500: 6.6 us, M = 2048: 8.4, 17 with 64 adapters at random), which one workgroup
+// keeps few.
 __global__ __launch_bounds__(1024) void k_lora_plan(const int32_t *__restrict__ idx, int64_t M,
                                                     int64_t L, int32_t *__restrict__ plan) {
   constexpr int NB = kLoraMaxAdapters + 1;  // the last bin: rows without an adapter
@@ -156,7 +157,7 @@ __global__ __launch_bounds__(256) void k_lora_shrink_rows(
 //    partial sums in sorted order are added in order by k_lora_shrink_sum;
 //  * NT = 1, W = 16 over the whole of a short contraction: one launch.
 // (x onto A at M = 500, K = 4096, R = 64: 10.4 us; dy onto B at M = 2048, N = 14336, R = 16:
-// 18 + 5 us, 32 + 5 with dy's scaling beside it, 59 MB read and written.)
+// 15 + 4 us, 32 + 5 with dy's scaling beside it, 59 MB read and written.)
 // Operands go from memory to the MFMA registers as they lie: x and A have the
 // contraction contiguous. KMAJOR: the adapter matrix is [C, R] (dy onto B); each
 // wave then passes its step's 32 x 16 blocks through its own LDS slot and reads
@@ -374,7 +375,8 @@ __global__ __launch_bounds__(256) void k_lora_shrink_sum(const float *__restrict
 // the row's scale) is split into three bf16 parts. Loads in flight come from the
 // waves of a CU rather than from a step ahead in each, whose registers cost as
 // many waves. Bound by those round trips: 17 us for the 25 MB of M = 500, N = 4096,
-// K = 14336, R = 64, 3 adapters; 22 us, 3.1 TB/s, for M = 2048, N = 14336, K = 4096, R = 16.
+// K = 14336, R = 64, 3 adapters (14 without the input's gradient around it); 21 us, 3.2
+// TB/s, for M = 2048, N = 14336, K = 4096, R = 16 (19).
 
 // a.lo16 | b.lo16 << 16 and the high halves
 __device__ __forceinline__ int pack_lo(int a, int b) {
@@ -571,8 +573,10 @@ __global__ __launch_bounds__(256) void k_lora_wgrad_reduce(LoraWgradArgs p, int 
 // their products are computed here, spread over the chip with each adapter read
 // once per 16 rows, and the epilogues add them. Bound by memory: the adapters in
 // use and the float32 products, written here and read there (whole calls, 64
-// adapters at random: M = 128, N = 14336, K = 4096, R = 16: 51 us, 152 walked; M = 2048,
-// N = K = 4096, 32 adapters: 90, 183).
+// adapters at random: M = 128, N = 14336, K = 4096, R = 16: 54 us, 156 walked, of which
+// 9.6 are this kernel's; M = 2048, N = K = 4096, 32 adapters: 90, 182). A batch with more
+// than kLoraFew adapters stacked but none of its groups mixed pays a launch whose
+// workgroups return (M = 128: 3.9 us; M = 2048: 5.4).
 template <bool KMAJOR>
 __global__ __launch_bounds__(256) void k_lora_products(const float *__restrict__ h,
                                                        const uint16_t *__restrict__ W, int64_t M,
@@ -737,6 +741,9 @@ hipError_t launch_lora_shrink(const uint16_t *x, int64_t M, int64_t K, const uin
                               float *h, float *part, hipStream_t st) {
   if (M >= kLoraTiledMinM) return go_shrink<false>(x, M, K, A, alpha, L, R, plan, h, part, NoScale{}, st);
   const int32_t *idx = plan + lora_plan_layout(M, L).idx;
+  // a rank a workgroup while those are few; from 8 a CU on x is better read once for 4
+  // (calls with N = K = 4096: M = 1, R = 8 7.1 us, 7.7 with 4; M = 32, R = 32 17.3, 17.4;
+  // M = 16, R = 128 23.0, 22.9; M = 63, R = 64 31.7, 30.4)
   if (M * R < 2048)
     hipLaunchKernelGGL(k_lora_shrink_rows<1>, dim3((unsigned)R, (unsigned)M), dim3(256), 0, st, x,
                        K, A, alpha, (int)R, idx, h);
@@ -776,15 +783,19 @@ hipError_t launch_lora_products(const float *h, const uint16_t *W, bool kmajor, 
 }
 
 // Workgroups of the weight gradients, each 64 channels or 128 inputs of an adapter and
-// 16 ranks.
+// 16 ranks. The rules below go by M / L, the mean of an adapter's rows: how the rows
+// lie is known on the device only. A batch that stacks many adapters and names one
+// pays for it (M = 2048, N = K = 4096, R = 16, 32 adapters: 49 us with all rows on one of
+// them, 10 with 64 each; 17 where that adapter is stacked alone).
 static int64_t wgrad_units(const LoraWgradArgs &a) {
   return ((a.dB ? (a.N + 63) / 64 : 0) + (a.dA ? (a.K + 127) / 128 : 0)) * a.L *
          ((a.R + 15) / 16);
 }
 
-// Backward in a graph, with the sum beside and in launches each: M = 63, N = 2560, K = 960
-// 19.8 us, 23.7; M = 500, N = K = 4096, R = 128 60.5, 64.4; M = 512, one adapter 46.0,
-// 51.5. 64 adapters, R = 16 (6144 workgroups, for which 2 waves are enough): 55.6, 49.1.
+// For segments of few rows on average. Backward in a graph, with the sum beside and in
+// launches each: M = 63, N = 2560, K = 960 19.8 us, 23.7; M = 500, N = K = 4096, R = 128
+// 60.5, 64.4; M = 512, one adapter 43.8, 51.5. 64 adapters, R = 16 (6144 workgroups, for
+// which 2 waves are enough): 55.6, 49.1.
 bool lora_wgrad_beside(const LoraWgradArgs &a) {
   return a.M / a.L <= 512 && wgrad_units(a) < 2048;
 }
@@ -800,7 +811,7 @@ hipError_t launch_lora_wgrad_reduce(const LoraWgradArgs &a, const DgradParts &pa
 
 hipError_t launch_lora_wgrad(const LoraWgradArgs &a, hipStream_t st) {
   // long segments and several blocks of ranks: two of them share a read (M = 8192,
-  // 4 adapters, R = 64, N = K = 4096: 141 us of backward without dx, 150 apart)
+  // 4 adapters, R = 64, N = K = 4096: 139 us of backward without dx, 150 apart)
   if (a.R > 16 && a.M / a.L >= 1024) return go_wgrad<8, 2>(a, st);
   // else the fewest waves a workgroup that make about 3 a SIMD in all: more of
   // them only meet (M = 512, 16 adapters, R = 16, N = K = 4096: 15.4 us with 2, 18.2

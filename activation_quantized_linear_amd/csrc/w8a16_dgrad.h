@@ -24,7 +24,7 @@ struct DgradScale {
 // Row m by 256 threads (t of them; rows past M take part and write nothing), 8
 // values a thread and round. NI rounds are held in registers between the maximum
 // and the scaling, so dy is read once (NI = 0: any N, read twice). Bound by
-// memory: 4 bytes a value (M = 2048, N = 14336: 20 us, 5.9 TB/s).
+// memory: 4 bytes a value (M = 2048, N = 14336: 23 us, 5.1 TB/s).
 // red: a float for each wave of the workgroup.
 template <int NI>
 __device__ __forceinline__ void dgrad_scale_row(const DgradScale &a, int64_t m, int t,

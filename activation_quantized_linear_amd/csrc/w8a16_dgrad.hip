@@ -19,12 +19,13 @@
 // matrix instructions take the columns in strides of 4 and nothing is
 // transposed, in memory or in registers. d is padded with zeros to whole
 // stages, so what the last stage reads past N in q adds nothing.
-// Measured at M = 2048, K = 4096: N = 11008 in 152 us, 1215 TFLOP/s, and 20 us for the
-// scaling; N = 14336 in 200 to 220 us (a bf16 library product of that shape, on
-// weights of twice the bytes: 251). The matrix cores are busy for 1024 of a stage's
-// 1550 cycles, and what more they do the clock takes back (1.9 to 2.0 GHz under
-// this load): the same work on 32x32x16 instructions or with two workgroups a CU
-// took as long.
+// Measured at M = 2048, K = 4096, in a run of such calls: N = 11008 in 151 us, 1225
+// TFLOP/s, and 20 us for the scaling; N = 14336 in 195 us and 23 (a bf16 library
+// product of that shape, on weights of twice the bytes: 251). The first milliseconds of
+// a burst run 10 to 20% slower, until the clock has risen. The matrix cores are busy
+// for 1024 of a stage's 1550 cycles, and what more they do the clock takes back (1.9
+// to 2.0 GHz under this load): the same work on 32x32x16 instructions or with two
+// workgroups a CU took as long.
 // A ring of SG stages keeps loads in flight behind exact vmcnt waits. d rows
 // store their 16-byte chunks XOR-swizzled by (row / 2) mod 8, and weight rows
 // theirs by 4 (row / 8 mod 4), which spreads each read over all banks.

@@ -366,7 +366,8 @@ int aql_linear_w8a16_grouped(const void *table, const void *dev_table, void *str
  * A value of one adapter, or a row of one request, never reaches the rows and
  * gradients of another, whatever it holds. Where an infinity or a NaN enters a
  * result, the result is not finite, but which of the two it is does not follow
- * the formula (float32 factors enter as sums of parts).
+ * the formula (float32 factors enter as sums of bfloat16 parts; of h and u, values
+ * past bfloat16's range, 3.396e38 and more, may count as infinite).
  *
  * The plan. aql_lora_plan sorts a batch's rows by adapter into
  * aql_lora_plan_bytes(M, L) bytes of device memory. Every layer's linears and
@@ -393,7 +394,11 @@ int aql_lora_plan(const int32_t *idx, int64_t M, int64_t L, void *plan, size_t p
  *   h       device, [M, R] float32 (output; the backward pass takes it)
  *   ws      device workspace of aql_lora_forward_bytes(M, N, K, L, R) bytes (may be
  *           NULL where that is 0). It never shrinks as M grows: one of the
- *           largest batch serves the others.
+ *           largest batch serves the others. With L > 4 and M >= 64 it may hold
+ *           4 M N bytes of the adapters' products (twice y), whether or not
+ *           this batch's rows need them: that is known only to the plan, on
+ *           the device. Stack no more adapters than a batch uses where that
+ *           matters.
  * Errors: as aql_linear_w8a16, plus N > 2^26, R not a multiple of 8 in
  * 8..AQL_LORA_MAX_RANK, L outside 1..AQL_LORA_MAX_ADAPTERS, NULL or misaligned
  * A, B, alpha, plan or h, workspace too small. N == 0 writes h alone.
@@ -436,7 +441,8 @@ int aql_linear_w8a16_dgrad(const uint16_t *dy, int64_t M, int64_t N, const int8_
  *   dA, dB  device, [L, R, K] and [L, N, R] float32 (outputs; either may be
  *           NULL: not computed. xq and xs may be NULL without dA)
  *   ws      device workspace of aql_lora_backward_bytes(M, N, K, L, R) bytes, which
- *           never shrink as M grows either
+ *           never shrink as M grows either; with L > 4 they may hold 4 M K
+ *           bytes of the adapters' products
  * Errors: as aql_linear_w8a16_dgrad and aql_linear_w8a16_lora;
  * AQL_ERR_WORKSPACE. M == 0 or N == 0 write what is left of the outputs
  * (zeros, unless they accumulate).
