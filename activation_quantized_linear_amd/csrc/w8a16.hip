@@ -1466,20 +1466,21 @@ hipError_t launch_mfew(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
                        const LT &lt) {
   if (M < 2 || M > kW8A16FewMaxM || K < kW8A16FewMinK || K > kW8A16FewMaxK || K % 16)
     return hipErrorInvalidValue;
-  if (!grid_fits((N + 7) / 8, 512)) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)((N + 7) / 8));
-  auto go = [&](auto kern, int W) {
-    hipLaunchKernelGGL(kern, grid, dim3(64 * W), 0, st, x, M, K, q, scale, bias, N, y, lt);
+  const int waves = K <= 8192 ? 4 : 8;
+  if (!grid_fits((N + 7) / 8, 64 * waves)) return hipErrorInvalidConfiguration;
+  auto go = [&](auto kern) {
+    hipLaunchKernelGGL(kern, grid, dim3(64 * waves), 0, st, x, M, K, q, scale, bias, N, y, lt);
   };
   // waves split K so that each keeps one or two pieces of 1 KB per row
   if (M == 2) {
-    if (K <= 4096) go(k_w8a16_mfew<4, 1, 2, LT>, 4);
-    else if (K <= 8192) go(k_w8a16_mfew<4, 2, 2, LT>, 4);
-    else go(k_w8a16_mfew<8, 2, 2, LT>, 8);
+    if (K <= 4096) go(k_w8a16_mfew<4, 1, 2, LT>);
+    else if (K <= 8192) go(k_w8a16_mfew<4, 2, 2, LT>);
+    else go(k_w8a16_mfew<8, 2, 2, LT>);
   } else {
-    if (K <= 4096) go(k_w8a16_mfew<4, 1, 4, LT>, 4);
-    else if (K <= 8192) go(k_w8a16_mfew<4, 2, 4, LT>, 4);
-    else go(k_w8a16_mfew<8, 2, 4, LT>, 8);
+    if (K <= 4096) go(k_w8a16_mfew<4, 1, 4, LT>);
+    else if (K <= 8192) go(k_w8a16_mfew<4, 2, 4, LT>);
+    else go(k_w8a16_mfew<8, 2, 4, LT>);
   }
   return hipGetLastError();
 }
@@ -1518,9 +1519,10 @@ hipError_t launch_stream(const uint16_t *x, int64_t M, int64_t K, const int8_t *
     // are 192 workgroups a row block, else two (M = 16: K = 4096, N = 14336:
     // 14.2 us against 17.8 for the skinny tile; N = 11008: 13.0 vs 17.0;
     // K = N = 8192: 20.0 vs 22.4)
-    if (!grid_fits((N + 63) / 64, 512)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)((N + 63) / 64), (unsigned)((M + 15) / 16));
-    if (N >= 12288 && K <= 4096)
+    const bool one = N >= 12288 && K <= 4096;
+    if (!grid_fits((N + 63) / 64, one ? 256 : 512)) return hipErrorInvalidConfiguration;
+    if (one)
       hipLaunchKernelGGL((k_w8a16_sksh<4, 1, LT>), grid, dim3(256), 0, st, x, M, K, q, scale, bias, N, y, nullptr, 0, lt);
     else
       hipLaunchKernelGGL((k_w8a16_sksh<4, 2, LT>), grid, dim3(512), 0, st, x, M, K, q, scale, bias, N, y, nullptr, 0, lt);

@@ -20,7 +20,7 @@
  *   launches nothing and returns a negative status. aql_last_error() then
  *   describes the first problem found (thread-local text). There is no silent
  *   fallback to another algorithm or to the host.
- * - Sizes whose grid would hold 2^32 threads or more (W8A16 from 2^27 channels, row and
+ * - Sizes whose grid would hold 2^32 threads or more (W8A16 from 2^26 channels, row and
  *   weight quantizers from 2^24 rows, int8 products of 2^36 outputs and more, each
  *   at the earliest) are refused with AQL_ERR_HIP, nothing written.
  * - Inputs must be finite; results for NaN/Inf inputs are unspecified, but for

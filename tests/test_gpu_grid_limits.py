@@ -49,3 +49,14 @@ def test_quantizers_of_more_rows_than_a_grid_holds(K):
     refused(lambda: aql.aql_choose_qparams_rows(x, scale=s, zp=i, xq=q), q.view(-1), s, i)
     aql.aql_quantize_weight_int8(x[8:], q=q[8:], scale=s[8:], wsum=i[8:])
     assert (q[8:] == 127).all() and (i[8:] == 127 * K).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(2, (1 << 26) + 64, 2048), (4, (1 << 29) + 64, 16)])
+def test_w8a16_below_the_limit_of_its_own_grid(M, N, K):
+    """Grids of fewer threads a channel go further: 32 for two rows, 4 for four."""
+    print("w8a16", M, N, K, flush=True)
+    q = torch.ones(N, K, dtype=torch.int8, device=DEV)
+    scale = torch.ones(N, device=DEV)
+    x = torch.ones(M, K, dtype=torch.bfloat16, device=DEV)
+    y = aql.aql_linear_w8a16(x, q, scale)
+    assert (y == K).all()
