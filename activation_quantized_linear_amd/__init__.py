@@ -34,6 +34,11 @@ AQL_WQ_SYM127 = 0
 AQL_WQ_SYM127_5 = 1
 AQL_W_Q8CSW = 0
 AQL_W_Q4GSW = 1
+AQL_ACT_NONE = 0
+AQL_ACT_RELU = 1
+AQL_ACT_GELU = 2
+AQL_ACT_GELU_TANH = 3
+AQL_ACT_SILU = 4
 AQL_OP_Q8TA_Q8CSW = 1
 AQL_OP_DQ8CA = 2
 AQL_OP_GPTQ_INT8 = 3
@@ -42,6 +47,8 @@ AQL_OP_W8A16_DGRAD = 5
 AQL_LORA_MAX_RANK = 128
 AQL_LORA_MAX_ADAPTERS = 1024
 AQL_CKPT_GROUP = 128
+AQL_KV_BLOCK = 64
+AQL_KV_MAX_HEAD = 256
 AQL_MAX_K_INT8 = 65536
 AQL_NOALLOC_SCRATCH_BYTES = 8 << 20
 
@@ -96,6 +103,17 @@ _SIGS = {
     "aql_linear_w8a16_lora_backward": ([_p, _i64, _i64, _p, _p, _i64, _p, _p, _p, _i64, _i64, _p,
                                         _p, _p, _p, _int, _p, _p, _p, _p, _sz, _p], _int),
     "aql_act_checkpoint": ([_p, _int, _i64, _i64, _p, _p, _p], _int),
+    "aql_linear_w8a16_act": ([_p, _i64, _i64, _p, _p, _p, _i64, _int, _p, _p, _p, _p, _p, _sz, _p],
+                             _int),
+    "aql_act_mul_backward": ([_p, _p, _int, _p, _i64, _i64, _p, _p, _p], _int),
+    "aql_kv_plan_bytes": ([_i64] * 6, _sz),
+    "aql_kv_plan": ([_p, _p] + [_i64] * 7 + [_p, _sz, _p], _int),
+    "aql_kv_cache_write": ([_p, _i64, _p, _i64, _int] + [_i64] * 5 + [_p, _i64, _i64, _p, _p, _p,
+                                                                      _p, _p, _i64, _p], _int),
+    "aql_kv_cache_read": ([_p] * 4 + [_i64] * 6 + [_p, _i64, _i64, _p, _p, _p, _int, _p], _int),
+    "aql_attention_kv8_bytes": ([_i64] * 7, _sz),
+    "aql_attention_kv8": ([_p, _i64] + [_i64] * 5 + [_f32, _i64] + [_p] * 4 + [_i64, _p, _i64, _i64]
+                          + [_p] * 4 + [_sz, _p], _int),
     "aql_act_restore": ([_p, _p, _i64, _i64, _p, _int, _p], _int),
 }
 for _name, (_args, _res) in _SIGS.items():
@@ -775,3 +793,221 @@ def aql_act_restore(xq, xs, dtype=torch.bfloat16, x=None):
     x = _new(x, "x", (M, K), dtype, xq.device)
     _call("aql_act_restore", _lib.aql_act_restore, di, xq.data_ptr(), sp, M, K, x.data_ptr(), dt)
     return x
+
+
+# ----------------------------------- activation, product and residual
+
+
+def aql_linear_w8a16_act(x, q, scale, bias=None, act=AQL_ACT_NONE, mul=None, residual=None, y=None,
+                         pre=None, workspace=None):
+    """act(aql_linear_w8a16(x, q, scale, bias)) * mul + residual in one launch. x bfloat16
+    [M, K], q int8 [N, K], scale float32 [N], bias bfloat16 [N], act AQL_ACT_*, mul and
+    residual bfloat16 [M, N] -> y bfloat16 [M, N]. pre: a bfloat16 [M, N] tensor that
+    receives the value before act, which aql_act_mul_backward takes. y may be mul or
+    residual. workspace: as aql_linear_w8a16."""
+    di = _dev_index(x, "x", torch.bfloat16, 2)
+    M, K = x.shape
+    N = _dims(q, "q", 2)[0]
+    out = (M, N)
+    bf16 = torch.bfloat16
+    args = (x.data_ptr(), M, K, _fit(q, "q", torch.int8, (N, K), di),
+            _fit(scale, "scale", torch.float32, (N,), di),
+            None if bias is None else _fit(bias, "bias", bf16, (N,), di), N, int(act),
+            None if mul is None else _fit(mul, "mul", bf16, out, di),
+            None if residual is None else _fit(residual, "residual", bf16, out, di),
+            None if pre is None else _fit(pre, "pre", bf16, out, di))
+    dev = x.device
+    y = _new(y, "y", out, bf16, dev)
+    ws, ws_bytes, _owner = _scratch(workspace, _lib.aql_workspace_bytes(AQL_OP_W8A16, M, N, K), dev)
+    _call("aql_linear_w8a16_act", _lib.aql_linear_w8a16_act, di, *args, y.data_ptr(), ws, ws_bytes)
+    return y
+
+
+def aql_act_mul_backward(dy, pre, act, mul=None, dv=None, dmul=None, need_dmul=True):
+    """Gradients of aql_linear_w8a16_act's epilogue. dy, pre, mul bfloat16 [M, N] ->
+    (dv, dmul), bfloat16 [M, N]: dy * mul * act'(pre) and dy * act(pre). dmul is None
+    without mul or with need_dmul=False. An output may be an input."""
+    di = _dev_index(dy, "dy", torch.bfloat16, 2)
+    M, N = dy.shape
+    args = (dy.data_ptr(), _fit(pre, "pre", torch.bfloat16, (M, N), di), int(act),
+            None if mul is None else _fit(mul, "mul", torch.bfloat16, (M, N), di), M, N)
+    if dmul is not None and (mul is None or not need_dmul):
+        raise ValueError("dmul is given but mul is None or need_dmul is False")
+    dev = dy.device
+    dv = _new(dv, "dv", (M, N), torch.bfloat16, dev)
+    if mul is not None and need_dmul:
+        dmul = _new(dmul, "dmul", (M, N), torch.bfloat16, dev)
+    _call("aql_act_mul_backward", _lib.aql_act_mul_backward, di, *args, dv.data_ptr(),
+          None if dmul is None else dmul.data_ptr())
+    return dv, dmul
+
+
+# --------------------------------------------- paged 8-bit KV cache, attention
+
+
+class KvCache:
+    """A paged 8-bit KV cache: P pages of AQL_KV_BLOCK tokens for Hkv heads of D values
+    (DP: D rounded up to a multiple of 64). Tensors: kq int8 [P, Hkv, DP/64, 64, 64], vq int8
+    [P, Hkv, DP, 64], ks and vs float32 [P, Hkv]; a value is code * scale."""
+
+    __slots__ = ("P", "Hkv", "D", "kq", "vq", "ks", "vs")
+
+    def __init__(self, P, Hkv, D, kq, vq, ks, vs):
+        self.P, self.Hkv, self.D = P, Hkv, D
+        self.kq, self.vq, self.ks, self.vs = kq, vq, ks, vs
+
+
+def aql_kv_cache(P, Hkv, D, device="cuda"):
+    """A new KvCache of P pages for Hkv heads of D values (a multiple of 8 up to
+    AQL_KV_MAX_HEAD). Its contents are whatever the memory held: a page is begun by writing
+    its first token."""
+    P, Hkv, D = int(P), int(Hkv), int(D)
+    if not (1 <= P < 1 << 31 and 1 <= Hkv <= 1024 and 8 <= D <= AQL_KV_MAX_HEAD and D % 8 == 0):
+        raise ValueError(f"need 1 <= P < 2^31, 1 <= Hkv <= 1024 and D a multiple of 8 in "
+                         f"[8, {AQL_KV_MAX_HEAD}], got P={P}, Hkv={Hkv}, D={D}")
+    DP = (D + 63) // 64 * 64
+    new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=device)
+    return KvCache(P, Hkv, D, new((P, Hkv, DP // 64, AQL_KV_BLOCK, 64), torch.int8),
+                   new((P, Hkv, DP, AQL_KV_BLOCK), torch.int8), new((P, Hkv), torch.float32),
+                   new((P, Hkv), torch.float32))
+
+
+class KvPlan:
+    """A step's sequences divided into work (aql_kv_plan). Holds the sizes it was made
+    for and its device buffer; every layer of a step shares one. info: a device int32 [1], 0 or 1 +
+    the first sequence that cannot be served (see aql.h)."""
+
+    __slots__ = ("T", "S", "Hq", "Hkv", "W", "most", "window", "buffer")
+
+    def __init__(self, T, S, Hq, Hkv, W, most, window, buffer):
+        self.T, self.S, self.Hq, self.Hkv, self.W = T, S, Hq, Hkv, W
+        self.most, self.window, self.buffer = most, window, buffer
+
+    @property
+    def info(self):
+        return self.buffer[:4].view(torch.int32)
+
+
+def aql_kv_plan_bytes(T, S, Hq, Hkv, W, most):
+    return _lib.aql_kv_plan_bytes(T, S, Hq, Hkv, W, most)
+
+
+def aql_kv_plan(cu, pos, T, most, Hq, Hkv, W, window=0, plan=None):
+    """cu int32 [S + 1]: the rows of a step's T at which its S sequences begin; pos int32 [S]:
+    the position of each one's first new token -> KvPlan. most: the most new tokens of any sequence;
+    W: columns of the page table; window: tokens that a token sees (0: all before it).
+    plan: a KvPlan of the same sizes on cu's device to write again (its buffer keeps its
+    address, so a captured graph sees the new step)."""
+    di = _dev_index(pos, "pos", torch.int32, 1)
+    S = pos.shape[0]
+    cp = _fit(cu, "cu", torch.int32, (S + 1,), di)
+    sizes = tuple(int(v) for v in (T, S, Hq, Hkv, W, most, window))
+    nbytes = aql_kv_plan_bytes(*sizes[:6])
+    if plan is None:
+        plan = KvPlan(*sizes, torch.empty(max(nbytes, 16), dtype=torch.uint8, device=pos.device))
+    elif not isinstance(plan, KvPlan):
+        raise TypeError("plan must be a KvPlan (aql_kv_plan)")
+    elif (plan.T, plan.S, plan.Hq, plan.Hkv, plan.W, plan.most, plan.window) != sizes:
+        raise ValueError("plan was made for other sizes")
+    buf = _fit(plan.buffer, "plan.buffer", torch.uint8, plan.buffer.shape, di)
+    _call("aql_kv_plan", _lib.aql_kv_plan, di, cp, pos.data_ptr(), *sizes, buf,
+          plan.buffer.numel())
+    return plan
+
+
+def _kv_call(cache, table, plan, di):
+    """Addresses of a cache's tensors, of the page table and of the plan."""
+    if not isinstance(cache, KvCache):
+        raise TypeError("cache must be a KvCache (aql_kv_cache)")
+    if not isinstance(plan, KvPlan):
+        raise TypeError("plan must be a KvPlan (aql_kv_plan)")
+    P, Hkv, DP = cache.P, cache.Hkv, (cache.D + 63) // 64 * 64
+    if plan.Hkv != Hkv:
+        raise ValueError(f"plan is for Hkv={plan.Hkv}, the cache has {Hkv}")
+    return (_fit(cache.kq, "cache.kq", torch.int8, (P, Hkv, DP // 64, AQL_KV_BLOCK, 64), di),
+            _fit(cache.vq, "cache.vq", torch.int8, (P, Hkv, DP, AQL_KV_BLOCK), di),
+            _fit(cache.ks, "cache.ks", torch.float32, (P, Hkv), di),
+            _fit(cache.vs, "cache.vs", torch.float32, (P, Hkv), di),
+            _fit(table, "table", torch.int32, (plan.S, plan.W), di),
+            _fit(plan.buffer, "plan.buffer", torch.uint8, plan.buffer.shape, di))
+
+
+def _device_of(t, name):
+    """Device index of a 3-D tensor that may have rows any distance apart."""
+    _dims(t, name, 3)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    return t.get_device()
+
+
+def _kv_rows(t, name, dtype, shape, di):
+    """(address, elements between rows) of t [T, heads, D], whose rows lie any distance apart."""
+    T, heads, D = shape
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == di and t.stride(2) == 1
+                and (t.stride(1) == D or heads == 1)):
+            return t.data_ptr(), heads * D if T < 2 else t.stride(0)
+    except AttributeError:
+        pass
+    if isinstance(t, torch.Tensor) and t.ndim == 3 and t.is_cuda and t.dtype == dtype:
+        _shape(t, name, shape)
+        if t.get_device() == di:
+            if t.is_contiguous():  # an empty one
+                return t.data_ptr(), heads * D
+            raise ValueError(f"{name} must have contiguous heads within a row")
+    _need(t, name, dtype, 3, torch.device("cuda", di))
+    raise ValueError(f"{name} is not a tensor that this call takes")
+
+
+def aql_kv_cache_write(k, v, cache, table, plan):
+    """Quantise the new tokens of a step into the cache. k, v float32 or bfloat16 [T, Hkv, D], each
+    row's heads contiguous (slices of a fused projection's output are fine); table int32 [S, W]:
+    each sequence's pages. Writes cache in place."""
+    di = _device_of(k, "k")
+    dt = _act_dtype(k.dtype, "k")
+    kq, vq, ks, vs, tp, pp = _kv_call(cache, table, plan, di)
+    shape = (plan.T, cache.Hkv, cache.D)
+    kp, krow = _kv_rows(k, "k", k.dtype, shape, di)
+    vp, vrow = _kv_rows(v, "v", k.dtype, shape, di)
+    _call("aql_kv_cache_write", _lib.aql_kv_cache_write, di, kp, krow, vp, vrow, dt, plan.T, plan.S,
+          plan.Hq, plan.Hkv, cache.D, tp, plan.W, plan.most, pp, kq, vq, ks, vs, cache.P)
+
+
+def aql_kv_cache_read(cache, table, plan, dtype=torch.bfloat16, k=None, v=None):
+    """The rows that a plan names, read back: (k, v) [T, Hkv, D] of dtype float32 or bfloat16,
+    code * scale. Rows of no sequence are left as they are."""
+    dt = _act_dtype(dtype, "dtype")
+    di = _dev_index(table, "table", torch.int32, 2)
+    kq, vq, ks, vs, tp, pp = _kv_call(cache, table, plan, di)
+    shape = (plan.T, cache.Hkv, cache.D)
+    k = _new(k, "k", shape, dtype, table.device)
+    v = _new(v, "v", shape, dtype, table.device)
+    _call("aql_kv_cache_read", _lib.aql_kv_cache_read, di, kq, vq, ks, vs, cache.P, plan.T, plan.S,
+          plan.Hq, plan.Hkv, cache.D, tp, plan.W, plan.most, pp, k.data_ptr(), v.data_ptr(), dt)
+    return k, v
+
+
+def aql_attention_kv8_bytes(T, S, Hq, Hkv, D, W, most):
+    return _lib.aql_attention_kv8_bytes(T, S, Hq, Hkv, D, W, most)
+
+
+def aql_attention_kv8(q, cache, table, plan, sm_scale=None, y=None, lse=None, workspace=None):
+    """Attention of a step's tokens over the cache, which holds their own K and V already
+    (aql_kv_cache_write). q bfloat16 [T, Hq, D], each row's heads contiguous; table int32
+    [S, W] -> y bfloat16 [T, Hq, D]. sm_scale: D^-0.5 if not given. lse: a float32 [T, Hq] tensor
+    that receives the logarithms of the softmax's denominators. Rows of no sequence are
+    left as they are. workspace: uint8 device tensor of aql_attention_kv8_bytes; allocated
+    here when one is needed and none is given."""
+    di = _device_of(q, "q")
+    kq, vq, ks, vs, tp, pp = _kv_call(cache, table, plan, di)
+    T, Hq, D = plan.T, plan.Hq, cache.D
+    qp, qrow = _kv_rows(q, "q", torch.bfloat16, (T, Hq, D), di)
+    dev = q.device
+    lp = None if lse is None else _fit(lse, "lse", torch.float32, (T, Hq), di)
+    y = _new(y, "y", (T, Hq, D), torch.bfloat16, dev)
+    ws, ws_bytes, _owner = _scratch(
+        workspace, _lib.aql_attention_kv8_bytes(T, plan.S, Hq, plan.Hkv, D, plan.W, plan.most), dev)
+    _call("aql_attention_kv8", _lib.aql_attention_kv8, di, qp, qrow, T, plan.S, Hq, plan.Hkv, D,
+          D ** -0.5 if sm_scale is None else float(sm_scale), plan.window, kq, vq, ks, vs, cache.P,
+          tp, plan.W, plan.most, pp, y.data_ptr(), lp, ws, ws_bytes)
+    return y

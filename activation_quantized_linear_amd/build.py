@@ -17,7 +17,8 @@ OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libaql.so")
 
 SOURCES = ["abi.cpp", "quant.hip", "w8a16.hip", "gemm_i8.hip", "dq8ca_q4.hip", "measure.hip",
-           "w8a16_gemm.hip", "calib.hip", "gptq.hip", "lora.hip", "w8a16_dgrad.hip", "ckpt.hip"]
+           "w8a16_gemm.hip", "calib.hip", "gptq.hip", "lora.hip", "w8a16_dgrad.hip", "ckpt.hip",
+           "act.hip", "kv_cache.hip", "kv_attn.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -13,12 +13,14 @@
 #include <string>
 #include <vector>
 
+#include "act.h"
 #include "aql.h"
 #include "calib.h"
 #include "ckpt.h"
 #include "dq8ca_q4.h"
 #include "gemm_i8.h"
 #include "gptq.h"
+#include "kv.h"
 #include "lora.h"
 #include "quant.h"
 #include "w8a16.h"
@@ -187,6 +189,63 @@ bool plan_sizes_ok(int64_t M, int64_t L) {
 static_assert(AQL_LORA_MAX_ADAPTERS == aql::kLoraMaxAdapters &&
                   AQL_LORA_MAX_RANK == aql::kLoraMaxRank && AQL_CKPT_GROUP == aql::kCkptGroup,
               "adapter bounds");
+
+static_assert(AQL_ACT_NONE == aql::kActNone && AQL_ACT_RELU == aql::kActRelu &&
+                  AQL_ACT_GELU == aql::kActGelu && AQL_ACT_GELU_TANH == aql::kActGeluTanh &&
+                  AQL_ACT_SILU == aql::kActSilu,
+              "activations");
+
+static_assert(AQL_KV_BLOCK == aql::kKvBlock && AQL_KV_MAX_HEAD == aql::kKvMaxHead, "cache bounds");
+
+bool kv_sizes_ok(const aql::KvSizes &z) {
+  return z.T >= 0 && z.T <= aql::kKvMaxTokens && z.S >= 0 && z.S <= aql::kKvMaxSeqs && z.W >= 1 &&
+         z.W <= aql::kKvMaxBlocks && z.Hkv >= 1 && z.Hq >= 1 && z.Hq <= 1024 &&
+         z.Hq % z.Hkv == 0 && z.most >= 1 && z.most <= aql::kKvMaxTokens && z.window >= 0 &&
+         z.window <= (1 << 30);
+}
+aql::KvSizes kv_sizes(int64_t T, int64_t S, int64_t Hq, int64_t Hkv, int64_t W, int64_t most,
+                      int64_t window) {
+  const bool heads = Hq >= 1 && Hq <= 1024 && Hkv >= 1 && Hkv <= Hq;  // (they fit an int)
+  return aql::KvSizes{T, S, W, most, heads ? (int)Hq : 0, heads ? (int)Hkv : 0, window};
+}
+
+int check_kv(const char *fn, const aql::KvSizes &z) {
+  REQUIRE(kv_sizes_ok(z), AQL_ERR_SHAPE,
+          "%s: need T in [0, %lld], S in [0, %lld], W in [1, %lld], Hq <= 1024 a multiple of Hkv, "
+          "most in [1, %lld], window in [0, 2^30] (T=%lld S=%lld W=%lld Hq=%d Hkv=%d most=%lld "
+          "window=%lld)",
+          fn, (long long)aql::kKvMaxTokens, (long long)aql::kKvMaxSeqs,
+          (long long)aql::kKvMaxBlocks, (long long)aql::kKvMaxTokens, (long long)z.T,
+          (long long)z.S, (long long)z.W, z.Hq, z.Hkv, (long long)z.most, (long long)z.window);
+  return AQL_OK;
+}
+
+// What every call on the cache checks.
+int check_kv_cache(const char *fn, const aql::KvSizes &z, int64_t D, const int32_t *table,
+                   const void *plan, const void *kq, const void *vq, const void *ks,
+                   const void *vs, int64_t P) {
+  if (int e = check_kv(fn, z)) return e;
+  REQUIRE(D >= 8 && D <= AQL_KV_MAX_HEAD && D % 8 == 0 && P >= 1 && P <= 0x7fffffffLL,
+          AQL_ERR_SHAPE, "%s: need D a multiple of 8 in [8, %d] and P in [1, 2^31 - 1] (D=%lld P=%lld)",
+          fn, AQL_KV_MAX_HEAD, (long long)D, (long long)P);
+  REQUIRE(aligned16(table) && aligned16(plan) && aligned16(kq) && aligned16(vq) && aligned16(ks) &&
+              aligned16(vs),
+          AQL_ERR_ALIGN, "%s: pointers must be 16-byte aligned", fn);
+  if (z.T == 0 || z.S == 0) return AQL_OK;
+  REQUIRE(table && plan && kq && vq && ks && vs, AQL_ERR_NULL,
+          "%s: table, plan, kq, vq, ks and vs must not be NULL", fn);
+  return AQL_OK;
+}
+
+bool kv_row_ok(int64_t row, int64_t least, int64_t esize) {
+  return row >= least && row <= (1LL << 40) && row * esize % 16 == 0;
+}
+
+aql::KvCache kv_cache(const int8_t *kq, const int8_t *vq, const float *ks, const float *vs,
+                      int64_t P, int Hkv, int64_t D) {
+  return aql::KvCache{const_cast<int8_t *>(kq), const_cast<int8_t *>(vq), const_cast<float *>(ks),
+                      const_cast<float *>(vs), P, Hkv, (int)D, aql::kv_padded(D)};
+}
 
 // Bytes of the adapters' products [M, C] that a tiled kernel is given: where it
 // splits its contraction, all of them once there is much to add; else those of
@@ -469,6 +528,47 @@ int aql_linear_w8a16(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
   return launched(aql::launch_w8a16(x, M, K, q, scale, bias, N, y, static_cast<float *>(ws),
                                     ws ? ws_bytes : 0, (hipStream_t)stream),
                   fn);
+}
+
+int aql_linear_w8a16_act(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
+                         const float *scale, const uint16_t *bias, int64_t N, int act,
+                         const uint16_t *mul, const uint16_t *residual, uint16_t *pre, uint16_t *y,
+                         void *ws, size_t ws_bytes, void *stream) {
+  const char *fn = "aql_linear_w8a16_act";
+  if (int e = check_w8a16(fn, x, M, K, q, scale, bias, N, y)) return e;
+  REQUIRE(act >= 0 && act < aql::kActKinds, AQL_ERR_PARAM, "%s: unknown act %d", fn, act);
+  REQUIRE(aligned16(mul) && aligned16(residual) && aligned16(pre) && aligned16(ws), AQL_ERR_ALIGN,
+          "%s: pointers must be 16-byte aligned", fn);
+  if (M == 0 || N == 0) return ok();
+  REQUIRE(y != pre, AQL_ERR_PARAM, "%s: y and pre must not share memory", fn);
+  if (int e = check_device(fn)) return e;
+  const aql::ActTerm at{act, mul, residual, pre, N};
+  float *part = static_cast<float *>(ws);
+  const size_t pb = ws ? ws_bytes : 0;
+  // the same M-dispatch as aql_linear_w8a16
+  if (M >= kW8A16GemmMinM && K <= (1LL << 22))
+    return launched(aql::launch_w8a16_gemm(x, M, K, q, scale, bias, N, y, part, pb,
+                                           (hipStream_t)stream, at),
+                    fn);
+  return launched(
+      aql::launch_w8a16(x, M, K, q, scale, bias, N, y, part, pb, (hipStream_t)stream, at), fn);
+}
+
+int aql_act_mul_backward(const uint16_t *dy, const uint16_t *pre, int act, const uint16_t *mul,
+                         int64_t M, int64_t N, uint16_t *dv, uint16_t *dmul, void *stream) {
+  const char *fn = "aql_act_mul_backward";
+  REQUIRE(act >= 0 && act < aql::kActKinds, AQL_ERR_PARAM, "%s: unknown act %d", fn, act);
+  REQUIRE(M >= 0 && N >= 0 && (M == 0 || N <= (1LL << 40) / M), AQL_ERR_SHAPE,
+          "%s: need M, N >= 0 and M N <= 2^40 (M=%lld N=%lld)", fn, (long long)M, (long long)N);
+  REQUIRE(aligned16(dy) && aligned16(pre) && aligned16(mul) && aligned16(dv) && aligned16(dmul),
+          AQL_ERR_ALIGN, "%s: pointers must be 16-byte aligned", fn);
+  if (M == 0 || N == 0) return ok();
+  REQUIRE(dy && pre && dv, AQL_ERR_NULL, "%s: dy, pre and dv must not be NULL", fn);
+  REQUIRE(!dmul || (mul && dmul != dv), AQL_ERR_PARAM,
+          "%s: dmul needs mul, and memory other than dv's", fn);
+  if (int e = check_device(fn)) return e;
+  return launched(
+      aql::launch_act_mul_backward(dy, pre, act, mul, M * N, dv, dmul, (hipStream_t)stream), fn);
 }
 
 size_t aql_w8a16_group_table_bytes(int count) {
@@ -879,6 +979,103 @@ int aql_act_restore(const int8_t *xq, const float *xs, int64_t M, int64_t K, voi
   REQUIRE(x && xq && xs, AQL_ERR_NULL, "%s: x, xq and xs must not be NULL", fn);
   if (int e = check_device(fn)) return e;
   return launched(aql::launch_act_restore(xq, xs, M, K, x, dtype == AQL_BF16, (hipStream_t)stream),
+                  fn);
+}
+
+size_t aql_kv_plan_bytes(int64_t T, int64_t S, int64_t Hq, int64_t Hkv, int64_t W, int64_t most) {
+  const aql::KvSizes z = kv_sizes(T, S, Hq, Hkv, W, most, 0);
+  return kv_sizes_ok(z) ? (size_t)aql::kv_plan_layout(z).total * 4 : 0;
+}
+
+int aql_kv_plan(const int32_t *cu, const int32_t *pos, int64_t T, int64_t S, int64_t Hq,
+                int64_t Hkv, int64_t W, int64_t most, int64_t window, void *plan,
+                size_t plan_bytes, void *stream) {
+  const char *fn = "aql_kv_plan";
+  const aql::KvSizes z = kv_sizes(T, S, Hq, Hkv, W, most, window);
+  if (int e = check_kv(fn, z)) return e;
+  REQUIRE(aligned16(cu) && aligned16(pos) && aligned16(plan), AQL_ERR_ALIGN,
+          "%s: pointers must be 16-byte aligned", fn);
+  REQUIRE(plan && (S == 0 || (cu && pos)), AQL_ERR_NULL, "%s: cu, pos and plan must not be NULL",
+          fn);
+  const size_t need = aql_kv_plan_bytes(T, S, Hq, Hkv, W, most);
+  REQUIRE(plan_bytes >= need, AQL_ERR_WORKSPACE, "%s: plan needs %zu bytes (got %zu)", fn, need,
+          plan_bytes);
+  if (int e = check_device(fn)) return e;
+  return launched(
+      aql::launch_kv_plan(cu, pos, z, static_cast<int32_t *>(plan), (hipStream_t)stream), fn);
+}
+
+int aql_kv_cache_write(const void *k, int64_t krow, const void *v, int64_t vrow, int dtype,
+                       int64_t T, int64_t S, int64_t Hq, int64_t Hkv, int64_t D,
+                       const int32_t *table, int64_t W, int64_t most, const void *plan, int8_t *kq,
+                       int8_t *vq, float *ks, float *vs, int64_t P, void *stream) {
+  const char *fn = "aql_kv_cache_write";
+  const aql::KvSizes z = kv_sizes(T, S, Hq, Hkv, W, most, 0);
+  REQUIRE(dtype == AQL_F32 || dtype == AQL_BF16, AQL_ERR_PARAM, "%s: unknown dtype %d", fn, dtype);
+  if (int e = check_kv_cache(fn, z, D, table, plan, kq, vq, ks, vs, P)) return e;
+  const int64_t es = dtype == AQL_BF16 ? 2 : 4;
+  REQUIRE(kv_row_ok(krow, Hkv * D, es) && kv_row_ok(vrow, Hkv * D, es), AQL_ERR_SHAPE,
+          "%s: rows must be at least Hkv D elements apart, and whole 16 bytes (krow=%lld vrow=%lld)",
+          fn, (long long)krow, (long long)vrow);
+  REQUIRE(aligned16(k) && aligned16(v), AQL_ERR_ALIGN, "%s: pointers must be 16-byte aligned", fn);
+  if (T == 0 || S == 0) return ok();
+  REQUIRE(k && v, AQL_ERR_NULL, "%s: k and v must not be NULL", fn);
+  if (int e = check_device(fn)) return e;
+  return launched(aql::launch_kv_write(k, krow, v, vrow, dtype == AQL_BF16,
+                                       kv_cache(kq, vq, ks, vs, P, z.Hkv, D), table, z,
+                                       static_cast<const int32_t *>(plan), (hipStream_t)stream),
+                  fn);
+}
+
+int aql_kv_cache_read(const int8_t *kq, const int8_t *vq, const float *ks, const float *vs,
+                      int64_t P, int64_t T, int64_t S, int64_t Hq, int64_t Hkv, int64_t D,
+                      const int32_t *table, int64_t W, int64_t most, const void *plan, void *k,
+                      void *v, int dtype, void *stream) {
+  const char *fn = "aql_kv_cache_read";
+  const aql::KvSizes z = kv_sizes(T, S, Hq, Hkv, W, most, 0);
+  REQUIRE(dtype == AQL_F32 || dtype == AQL_BF16, AQL_ERR_PARAM, "%s: unknown dtype %d", fn, dtype);
+  if (int e = check_kv_cache(fn, z, D, table, plan, kq, vq, ks, vs, P)) return e;
+  REQUIRE(aligned16(k) && aligned16(v), AQL_ERR_ALIGN, "%s: pointers must be 16-byte aligned", fn);
+  if (T == 0 || S == 0) return ok();
+  REQUIRE(k && v, AQL_ERR_NULL, "%s: k and v must not be NULL", fn);
+  if (int e = check_device(fn)) return e;
+  return launched(aql::launch_kv_read(kv_cache(kq, vq, ks, vs, P, z.Hkv, D), table, z,
+                                      static_cast<const int32_t *>(plan), k, v, dtype == AQL_BF16,
+                                      (hipStream_t)stream),
+                  fn);
+}
+
+size_t aql_attention_kv8_bytes(int64_t T, int64_t S, int64_t Hq, int64_t Hkv, int64_t D, int64_t W,
+                               int64_t most) {
+  const aql::KvSizes z = kv_sizes(T, S, Hq, Hkv, W, most, 0);
+  if (!kv_sizes_ok(z) || D < 8 || D > AQL_KV_MAX_HEAD || D % 8) return 0;
+  return aql::kv_attention_bytes(z, aql::kv_padded(D));
+}
+
+int aql_attention_kv8(const uint16_t *q, int64_t qrow, int64_t T, int64_t S, int64_t Hq,
+                      int64_t Hkv, int64_t D, float sm_scale, int64_t window, const int8_t *kq,
+                      const int8_t *vq, const float *ks, const float *vs, int64_t P,
+                      const int32_t *table, int64_t W, int64_t most, const void *plan,
+                      uint16_t *y, float *lse, void *ws, size_t ws_bytes, void *stream) {
+  const char *fn = "aql_attention_kv8";
+  const aql::KvSizes z = kv_sizes(T, S, Hq, Hkv, W, most, window);
+  REQUIRE(finite_pos(sm_scale), AQL_ERR_PARAM, "%s: sm_scale must be finite and > 0", fn);
+  if (int e = check_kv_cache(fn, z, D, table, plan, kq, vq, ks, vs, P)) return e;
+  REQUIRE(kv_row_ok(qrow, Hq * D, 2), AQL_ERR_SHAPE,
+          "%s: rows of q must be at least Hq D elements apart, and whole 16 bytes (qrow=%lld)", fn,
+          (long long)qrow);
+  REQUIRE(aligned16(q) && aligned16(y) && aligned16(lse) && aligned16(ws), AQL_ERR_ALIGN,
+          "%s: pointers must be 16-byte aligned", fn);
+  if (T == 0 || S == 0) return ok();
+  REQUIRE(q && y, AQL_ERR_NULL, "%s: q and y must not be NULL", fn);
+  const size_t need = aql_attention_kv8_bytes(T, S, Hq, Hkv, D, W, most);
+  REQUIRE(need == 0 || (ws && ws_bytes >= need), AQL_ERR_WORKSPACE,
+          "%s: workspace needs %zu bytes (got %zu)", fn, need, ws ? ws_bytes : (size_t)0);
+  if (int e = check_device(fn)) return e;
+  return launched(aql::launch_kv_attention(q, qrow, sm_scale,
+                                           kv_cache(kq, vq, ks, vs, P, z.Hkv, D), table, z,
+                                           static_cast<const int32_t *>(plan), y, lse, ws,
+                                           (hipStream_t)stream),
                   fn);
 }
 

@@ -1,0 +1,383 @@
+// Attention over the paged 8-bit KV cache. For a query at position p of a sequence, over
+// the tokens t that it sees (max(0, p - window + 1) .. p):
+//   y = sum_t e^(a (q . k_t)) v_t / sum_t e^(a (q . k_t)),  k_t = ks code_k, v_t = vs code_v,
+// with one ks and vs for each page of 64 tokens and kv head.
+//
+// The scales never touch the codes. Scores are computed in powers of two and with log2 vs in them,
+//   z_t = a log2(e) ks (q . code_k) + log2 vs,   w_t = 2^(z_t - M),
+// M the running maximum of z, so that outputs are sums of w_t code_v and w_t is at most 1
+// where it weighs most, whatever the pages' scales; the denominator adds a page's
+// w_t times 1 / vs. Codes widen exactly: k to bf16 beside q's own bf16, v to float16
+// beside w, which is rounded to float16 (by 2^-11 of its value, or below 2^-14 by 2^-25 of
+// the largest: a bf16 output itself is rounded by 2^-8). Sums, M and the denominator are float32.
+//
+// Scores are computed transposed (tokens as rows), so that a lane ends with 16
+// consecutive tokens of one query, which is the operand layout of the second product:
+// nothing passes through LDS or other lanes between the two. Of the 16 x 16 x 32
+// instructions' lanes 16 g + r, tile tau of a page's 4 takes tokens 16 (r / 4) + 4 tau + r % 4
+// as rows, so lane (r, g) holds tokens 16 g + 4 tau + v of query r. The contractions
+// over dims and over tokens take 16 consecutive bytes of the cache a lane, in the cache's order.
+#include "kv.h"
+
+namespace aql {
+namespace {
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ uint32_t bf16x2_from_i8(int lo, int hi) {
+  return __builtin_amdgcn_perm(__float_as_uint((float)hi), __float_as_uint((float)lo),
+                               0x07060302u);
+}
+
+// Eight codes (two dwords) -> eight bf16, exactly.
+__device__ __forceinline__ bf16x8 widen_bf16(uint32_t w0, uint32_t w1) {
+  const uint32_t a = bf16x2_from_i8((int)(int8_t)w0, (int)(int8_t)(w0 >> 8));
+  const uint32_t b = bf16x2_from_i8((int)(int8_t)(w0 >> 16), (int)w0 >> 24);
+  const uint32_t c = bf16x2_from_i8((int)(int8_t)w1, (int)(int8_t)(w1 >> 8));
+  const uint32_t d = bf16x2_from_i8((int)(int8_t)(w1 >> 16), (int)w1 >> 24);
+  return __builtin_bit_cast(bf16x8, u32x4{a, b, c, d});
+}
+
+// Two codes, already offset by 128, as the low mantissa bits of float16 1024, less 1152.
+__device__ __forceinline__ uint32_t f16x2_from_u8(uint32_t w, uint32_t sel) {
+  const f16x2 v = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, w, sel));
+  return __builtin_bit_cast(uint32_t, v - f16x2{(_Float16)1152.0f, (_Float16)1152.0f});
+}
+
+// Eight codes -> eight float16, exactly.
+__device__ __forceinline__ f16x8 widen_f16(uint32_t w0, uint32_t w1) {
+  const uint32_t x0 = w0 ^ 0x80808080u, x1 = w1 ^ 0x80808080u;
+  return __builtin_bit_cast(f16x8, u32x4{f16x2_from_u8(x0, 0x04010400u), f16x2_from_u8(x0, 0x04030402u),
+                                         f16x2_from_u8(x1, 0x04010400u), f16x2_from_u8(x1, 0x04030402u)});
+}
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// f over the four lanes that hold a query, in each.
+template <class F>
+__device__ __forceinline__ float across(float v, F &&f) {
+  v = f(v, __shfl_xor(v, 16));
+  return f(v, __shfl_xor(v, 32));
+}
+
+struct AttnArgs {
+  const uint16_t *q;
+  int64_t qrow;
+  float sm;  // sm_scale log2(e)
+  KvCache c;
+  const int32_t *table;
+  int64_t W;
+  const int32_t *plan;
+  int64_t at_units, at_joins, window;
+  int G, Hq;
+  uint16_t *y;
+  float *lse;
+  float *pm, *po;  // partial results: (M, denominator) and sums of each part, head and row
+};
+
+constexpr float kLn2 = 0.693147181f;
+
+// Outputs of row `row` of a unit's sequence: 4 dims from d on.
+__device__ __forceinline__ void store_out(const AttnArgs &a, int tok, int h, int row, int d,
+                                          const f32x4 &o) {
+  const int64_t at = ((int64_t)(tok + row / a.G) * a.Hq + h * a.G + row % a.G) * a.c.D + d;
+  const uint32_t lo = (uint32_t)f32_to_bf16_rne(o[0]) | ((uint32_t)f32_to_bf16_rne(o[1]) << 16);
+  const uint32_t hi = (uint32_t)f32_to_bf16_rne(o[2]) | ((uint32_t)f32_to_bf16_rne(o[3]) << 16);
+  *reinterpret_cast<uint2 *>(a.y + at) = uint2{lo, hi};
+}
+__device__ __forceinline__ void store_lse(const AttnArgs &a, int tok, int h, int row, float M,
+                                          float l) {
+  if (a.lse)
+    a.lse[(int64_t)(tok + row / a.G) * a.Hq + h * a.G + row % a.G] =
+        l == 0.0f ? -__builtin_inff() : (M + __log2f(l)) * kLn2;
+}
+
+// Few rows (decode): 16 NB rows of one kv head against a range of blocks, streamed from
+// memory once. Bound by memory. The four waves take blocks in turn, each with a
+// maximum and sums of its own, and join in LDS at the end. The next block's K is in
+// flight from when the present one is used up, V from the same moment one block earlier.
+template <int NB, int C>
+__global__ __launch_bounds__(256) void k_kv_attn_stream(AttnArgs a) {
+  constexpr int DP = 64 * C, ND = DP / 16, HD = C > 2 ? 128 : DP;  // HD: dims joined at a time
+  __shared__ __attribute__((aligned(16))) float ob[4][16][HD + 4];
+  __shared__ float om[4][16 * NB], ol[4][16 * NB];
+  const int i = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
+  if (i >= a.plan[kKvUnits]) return;
+  const KvUnit u = reinterpret_cast<const KvUnit *>(a.plan + a.at_units)[i];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int rows = min(16 * NB, u.len * a.G - u.row0);  // of the unit
+
+  bf16x8 qf[NB][2 * C];
+  int qpos[NB];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int row = u.row0 + 16 * nb + r;
+    const bool live = 16 * nb + r < rows;
+    qpos[nb] = u.pos + (live ? row / a.G : u.row0 / a.G);
+    const uint16_t *p = a.q + (int64_t)(u.tok + row / a.G) * a.qrow + (h * a.G + row % a.G) * a.c.D;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int d = 64 * c + 16 * g + 8 * s;
+        i32x4 v = {0, 0, 0, 0};
+        if (live && d < a.c.D) v = *reinterpret_cast<const i32x4 *>(p + d);
+        qf[nb][2 * c + s] = __builtin_bit_cast(bf16x8, v);
+      }
+  }
+  const int pmin = u.pos + u.row0 / a.G, pmax = u.pos + (u.row0 + rows - 1) / a.G;
+
+  f32x4 acc[NB][ND];
+  float M[NB], l[NB];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    M[nb] = -__builtin_inff();
+    l[nb] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) acc[nb][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  const int32_t *row_table = a.table + u.seq * a.W;
+  const int ktok = 16 * (r >> 2) + (r & 3);
+  const int64_t kofs = ktok * 64 + 16 * g, vofs = r * 64 + 16 * g;
+  i32x4 kb[4][C], vb[ND];
+  // a page that is none reads page 0 and counts for nothing
+  auto page_at = [&](int b) { return __builtin_amdgcn_readfirstlane(row_table[b]); };
+  auto base = [&](int page) {
+    return ((int64_t)(page >= 0 && page < a.c.pages ? page : 0) * a.c.Hkv + h) * (64 * DP);
+  };
+  auto load_k = [&](int page) {
+    const int8_t *p = a.c.kq + base(page) + kofs;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        kb[t][c] = *reinterpret_cast<const i32x4 *>(p + c * 4096 + t * 256);
+  };
+  int b = u.b0 + wave;
+  int page = b < u.b1 ? page_at(b) : 0;
+  if (b < u.b1) load_k(page);
+  while (b < u.b1) {
+    const bool more = b + 4 < u.b1;
+    const int next = more ? page_at(b + 4) : page;
+    {
+      const int8_t *p = a.c.vq + base(page) + vofs;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) vb[d] = *reinterpret_cast<const i32x4 *>(p + d * 1024);
+    }
+    const bool live = page >= 0 && page < a.c.pages;
+    const int64_t at = (live ? (int64_t)page : 0) * a.c.Hkv + h;
+    const float c1 = a.c.ks[at] * a.sm, vs = a.c.vs[at];
+    const float c2 = __builtin_amdgcn_logf(vs), iv = __builtin_amdgcn_rcpf(vs);
+
+    f32x4 s[NB][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) s[nb][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const bf16x8 k0 = widen_bf16((uint32_t)kb[t][c][0], (uint32_t)kb[t][c][1]);
+        const bf16x8 k1 = widen_bf16((uint32_t)kb[t][c][2], (uint32_t)kb[t][c][3]);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          s[nb][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, qf[nb][2 * c], s[nb][t], 0, 0, 0);
+          s[nb][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, qf[nb][2 * c + 1], s[nb][t], 0, 0, 0);
+        }
+      }
+    }
+    if (more) load_k(next);
+
+    // tokens past a query or before its window, and those of a page that is none
+    const int t0 = b * 64;
+    const bool whole = live && t0 + 63 <= pmin && (a.window == 0 || t0 > pmax - a.window);
+    f16x8 pf[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      float mx = -__builtin_inff();
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          float z = fmaf(s[nb][t][v], c1, c2);
+          if (!whole) {
+            const int tok = t0 + 16 * g + 4 * t + v;
+            const bool see = live && tok <= qpos[nb] && (a.window == 0 || tok > qpos[nb] - a.window);
+            z = see ? z : -__builtin_inff();
+          }
+          s[nb][t][v] = z;
+          mx = fmaxf(mx, z);
+        }
+      mx = across(mx, [](float x, float y) { return fmaxf(x, y); });
+      const float Mn = fmaxf(M[nb], mx);
+      const float off = Mn == -__builtin_inff() ? 0.0f : Mn;
+      const float alpha = exp2_hw(M[nb] - off);
+      M[nb] = Mn;
+      float sum = 0.0f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float w = exp2_hw(s[nb][t][v] - off);
+          sum += w;
+          pf[nb][t >> 1][4 * (t & 1) + v] = (_Float16)w;
+        }
+      // (a page without a visible token may hold any scale)
+      l[nb] = fmaf(l[nb], alpha, sum == 0.0f ? 0.0f : sum * iv);
+#pragma unroll
+      for (int d = 0; d < ND; ++d) acc[nb][d] *= alpha;
+    }
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+      const f16x8 v0 = widen_f16((uint32_t)vb[d][0], (uint32_t)vb[d][1]);
+      const f16x8 v1 = widen_f16((uint32_t)vb[d][2], (uint32_t)vb[d][3]);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        acc[nb][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[nb][0], acc[nb][d], 0, 0, 0);
+        acc[nb][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[nb][1], acc[nb][d], 0, 0, 0);
+      }
+    }
+    page = next;
+    b += 4;
+  }
+
+  // ---- the waves' results join
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const float sum = across(l[nb], [](float x, float y) { return x + y; });
+    if (g == 0) {
+      om[wave][16 * nb + r] = M[nb];
+      ol[wave][16 * nb + r] = sum;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int row = 16 * nb + r;
+    float top = om[0][row];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) top = fmaxf(top, om[w][row]);
+    const float off = top == -__builtin_inff() ? 0.0f : top;
+    const float f = exp2_hw(M[nb] - off);
+#pragma unroll
+    for (int half = 0; half < DP; half += HD) {
+#pragma unroll
+      for (int d = 0; d < HD / 16; ++d)
+        if (half / 16 + d < ND)
+          *reinterpret_cast<f32x4 *>(&ob[wave][r][16 * d + 4 * g]) = acc[nb][half / 16 + d] * f;
+      __syncthreads();
+      // thread (row orow, piece oc): 4 dims at a time
+      const int orow = threadIdx.x >> 4, oc = threadIdx.x & 15, lrow = 16 * nb + orow;
+      if (lrow < rows) {
+        float t2 = om[0][lrow], L = 0.0f;
+#pragma unroll
+        for (int w = 1; w < 4; ++w) t2 = fmaxf(t2, om[w][lrow]);
+        const float o2 = t2 == -__builtin_inff() ? 0.0f : t2;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) L = fmaf(ol[w][lrow], exp2_hw(om[w][lrow] - o2), L);
+        const int64_t at = ((int64_t)u.part * a.c.Hkv + h) * (16 * NB) + lrow;
+        if (half == 0 && oc == 0) {
+          if (u.part < 0) {
+            store_lse(a, u.tok, h, u.row0 + lrow, t2, L);
+          } else {
+            a.pm[2 * at] = t2;
+            a.pm[2 * at + 1] = L;
+          }
+        }
+#pragma unroll
+        for (int p = 0; p < HD / 64; ++p) {
+          const int d = 4 * (oc + 16 * p);
+          if (half + d >= a.c.D) continue;
+          f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) o += *reinterpret_cast<const f32x4 *>(&ob[w][orow][d]);
+          if (u.part < 0) store_out(a, u.tok, h, u.row0 + lrow, half + d, L == 0.0f ? f32x4{0.f, 0.f, 0.f, 0.f} : o * (1.0f / L));
+          else *reinterpret_cast<f32x4 *>(a.po + at * DP + half + d) = o;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// The partial results of rows whose blocks were spread over several units, in the order
+// of the parts.
+__global__ __launch_bounds__(256) void k_kv_attn_join(AttnArgs a, int tile) {
+  const int i = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
+  if (i >= a.plan[kKvJoins]) return;
+  const KvJoin u = reinterpret_cast<const KvJoin *>(a.plan + a.at_joins)[i];
+  const int rows = min(tile, u.len * a.G - u.row0), per = a.c.D / 4;
+  for (int e = threadIdx.x; e < rows * per; e += 256) {
+    const int row = e / per, d = 4 * (e % per);
+    const int64_t step = (int64_t)a.c.Hkv * tile;
+    const int64_t at = ((int64_t)u.part * a.c.Hkv + h) * tile + row;
+    float top = -__builtin_inff();
+    for (int p = 0; p < u.parts; ++p) top = fmaxf(top, a.pm[2 * (at + p * step)]);
+    const float off = top == -__builtin_inff() ? 0.0f : top;
+    float L = 0.0f;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    for (int p = 0; p < u.parts; ++p) {
+      const float f = exp2_hw(a.pm[2 * (at + p * step)] - off);
+      L = fmaf(a.pm[2 * (at + p * step) + 1], f, L);
+      o += *reinterpret_cast<const f32x4 *>(a.po + (at + p * step) * a.c.DP + d) * f;
+    }
+    if (d == 0) store_lse(a, u.tok, h, u.row0 + row, top, L);
+    store_out(a, u.tok, h, u.row0 + row, d, L == 0.0f ? f32x4{0.f, 0.f, 0.f, 0.f} : o * (1.0f / L));
+  }
+}
+
+template <int NB>
+void launch_stream(const AttnArgs &a, unsigned grid, hipStream_t st) {
+  switch (a.c.DP / 64) {
+    case 1: hipLaunchKernelGGL((k_kv_attn_stream<NB, 1>), dim3(grid), dim3(256), 0, st, a); break;
+    case 2: hipLaunchKernelGGL((k_kv_attn_stream<NB, 2>), dim3(grid), dim3(256), 0, st, a); break;
+    case 3: hipLaunchKernelGGL((k_kv_attn_stream<NB, 3>), dim3(grid), dim3(256), 0, st, a); break;
+    default: hipLaunchKernelGGL((k_kv_attn_stream<NB, 4>), dim3(grid), dim3(256), 0, st, a); break;
+  }
+}
+
+}  // namespace
+
+size_t kv_attention_bytes(const KvSizes &z, int DP) {
+  const int64_t rows = kv_plan_layout(z).parts * z.Hkv * kv_tile_rows(z);
+  return (size_t)rows * (8 + 4 * (size_t)DP);
+}
+
+hipError_t launch_kv_attention(const uint16_t *q, int64_t qrow, float sm_scale, const KvCache &c,
+                               const int32_t *table, const KvSizes &z, const int32_t *plan,
+                               uint16_t *y, float *lse, void *ws, hipStream_t st) {
+  const KvPlanLayout lay = kv_plan_layout(z);
+  const int tile = kv_tile_rows(z);
+  AttnArgs a{};
+  a.q = q;
+  a.qrow = qrow;
+  a.sm = sm_scale * 1.44269504f;
+  a.c = c;
+  a.table = table;
+  a.W = z.W;
+  a.plan = plan;
+  a.at_units = lay.at_units;
+  a.at_joins = lay.at_joins;
+  a.window = z.window;
+  a.G = z.Hq / z.Hkv;
+  a.Hq = z.Hq;
+  a.y = y;
+  a.lse = lse;
+  // sums first: rows of 4 DP bytes keep every access aligned
+  a.po = static_cast<float *>(ws);
+  a.pm = a.po + lay.parts * z.Hkv * tile * c.DP;
+  if (!grid_fits(lay.units * z.Hkv, 256)) return hipErrorInvalidConfiguration;
+  const unsigned grid = (unsigned)(lay.units * z.Hkv);
+  if (tile == 16) launch_stream<1>(a, grid, st);
+  else if (tile == 32) launch_stream<2>(a, grid, st);
+  else launch_stream<4>(a, grid, st);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || lay.joins == 0) return e;
+  hipLaunchKernelGGL(k_kv_attn_join, dim3((unsigned)(lay.joins * z.Hkv)), dim3(256), 0, st, a, tile);
+  return hipGetLastError();
+}
+
+}  // namespace aql

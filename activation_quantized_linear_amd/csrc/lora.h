@@ -55,7 +55,7 @@ hipError_t launch_lora_plan(const int32_t *idx, int64_t M, int64_t L, int32_t *p
 
 // No adapters: the epilogues compile to what they are without this parameter.
 struct NoLora {
-  static constexpr bool on = false;
+  static constexpr bool on = false, act = false;
   __device__ __forceinline__ float add(int64_t, int64_t, float v) const { return v; }
 };
 
@@ -64,7 +64,7 @@ struct NoLora {
 // bf16 once, with the projection's sum in it. Rows without an adapter read
 // neither h nor W.
 struct LoraTerm {
-  static constexpr bool on = true;
+  static constexpr bool on = true, act = false;
   const float *h;        // [M, R]
   const uint16_t *W;     // [L, N, R] bf16
   const int32_t *idx;    // [M]

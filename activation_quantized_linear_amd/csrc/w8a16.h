@@ -3,6 +3,7 @@
 // validated by the C ABI layer.
 #pragma once
 
+#include "act.h"
 #include "common.h"
 #include "lora.h"
 
@@ -17,6 +18,10 @@ hipError_t launch_w8a16(const uint16_t *x, int64_t M, int64_t K, const int8_t *q
 hipError_t launch_w8a16(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
                         const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
                         float *part, size_t part_bytes, hipStream_t st, const LoraTerm &lt);
+// The same with an activation, a product and a residual applied to each sum.
+hipError_t launch_w8a16(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
+                        const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
+                        float *part, size_t part_bytes, hipStream_t st, const ActTerm &at);
 
 // K splits of the shared-x skinny tile below kW8A16ShareMinN channels (1: the
 // shape does not split): 12 <= M < 64, K >= 8192, 4 splits up to 128 tiles of

@@ -1366,7 +1366,7 @@ int w8a16_xlds_bytes(int64_t K) {
 
 namespace {
 
-// The single-row tile and the skinny tile, with or without adapters.
+// The single-row tile and the skinny tile, with or without a term of adapters or an activation.
 template <class LT>
 hipError_t launch_m1_or_sk(const W8A16Shape &sh, const uint16_t *x, int64_t M, int64_t K,
                            const int8_t *q, const float *scale, const uint16_t *bias, int64_t N,
@@ -1545,8 +1545,8 @@ hipError_t launch_stream(const uint16_t *x, int64_t M, int64_t K, const int8_t *
     if (e != hipSuccess) return e;
     return launch_w8a16_splitk_reduce(part, splits, M, N, scale, bias, y, st, lt);
   }
-  if constexpr (LT::on)
-    // two or three rows take the skinny tile too (the 4-row tile has no adapter form)
+  if constexpr (LT::on || LT::act)
+    // two or three rows take the skinny tile too (the 4-row tile has neither form)
     return launch_m1_or_sk(w8a16_shape(M > 1 && M < kW8A16SkinnyMinM ? kW8A16SkinnyMinM : M, N, K),
                            x, M, K, q, scale, bias, N, y, st, lt);
   else
@@ -1565,6 +1565,12 @@ hipError_t launch_w8a16(const uint16_t *x, int64_t M, int64_t K, const int8_t *q
                         const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
                         float *part, size_t part_bytes, hipStream_t st, const LoraTerm &lt) {
   return launch_stream(x, M, K, q, scale, bias, N, y, part, part_bytes, st, lt);
+}
+
+hipError_t launch_w8a16(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
+                        const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
+                        float *part, size_t part_bytes, hipStream_t st, const ActTerm &at) {
+  return launch_stream(x, M, K, q, scale, bias, N, y, part, part_bytes, st, at);
 }
 
 hipError_t launch_w8a16_grouped(const W8A16GroupEntry *dev_tab, int count, int total_blocks,

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "act.h"
 #include "lora.h"
 
 namespace aql {
@@ -24,6 +25,9 @@ hipError_t launch_w8a16_splitk_reduce(const float *part, int S, int64_t M, int64
 hipError_t launch_w8a16_splitk_reduce(const float *part, int S, int64_t M, int64_t N,
                                       const float *scale, const uint16_t *bias, uint16_t *y,
                                       hipStream_t st, const LoraTerm &lt);
+hipError_t launch_w8a16_splitk_reduce(const float *part, int S, int64_t M, int64_t N,
+                                      const float *scale, const uint16_t *bias, uint16_t *y,
+                                      hipStream_t st, const ActTerm &at);
 
 // y[M, N] bf16 = scale[n] * x[M, K] bf16 . q[N, K]^T int8 (+ bias[n] bf16);
 // K <= 2^22 (32-bit buffer offsets of a 128-row tile of x). part (may be
@@ -36,5 +40,9 @@ hipError_t launch_w8a16_gemm(const uint16_t *x, int64_t M, int64_t K, const int8
 hipError_t launch_w8a16_gemm(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
                              const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
                              float *part, size_t part_bytes, hipStream_t st, const LoraTerm &lt);
+// The same with an activation, a product and a residual applied to each sum.
+hipError_t launch_w8a16_gemm(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
+                             const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
+                             float *part, size_t part_bytes, hipStream_t st, const ActTerm &at);
 
 }  // namespace aql

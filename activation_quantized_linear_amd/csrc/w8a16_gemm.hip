@@ -118,6 +118,88 @@ __device__ __forceinline__ void store_tile(const uint16_t *tl, uint16_t *y, int6
   }
 }
 
+// The tile's part of an [M, N] bf16 matrix into LDS rows, as store_tile writes them:
+// whole chunks from each row's first aligned element, the ends one by one. Places
+// past the matrix keep what they hold.
+template <int BM, int BN_, int NT, int TLD>
+__device__ __forceinline__ void load_tile(uint16_t *tl, const uint16_t *src, int64_t m0, int64_t M,
+                                          int64_t n0, int64_t N) {
+  const int tid = threadIdx.x;
+  constexpr int CH = BN_ / 8;
+  if ((N & 7) == 0) {
+    for (int u = tid; u < BM * CH; u += NT) {
+      const int row = u / CH, c = u % CH;
+      const int64_t m = m0 + row, n = n0 + 8 * c;
+      if (m >= M || n >= N) continue;
+      *reinterpret_cast<i32x4 *>(tl + row * TLD + 8 * c) =
+          *reinterpret_cast<const i32x4 *>(src + m * N + n);
+    }
+    return;
+  }
+  const int lim = N - n0 < BN_ ? (int)(N - n0) : BN_;
+  auto head = [&](int row) { return (int)(-((m0 + row) * N + n0) & 7); };
+  for (int u = tid; u < BM * CH; u += NT) {
+    const int row = u / CH, e0 = head(row) + 8 * (u % CH);
+    if (m0 + row >= M || e0 + 8 > lim) continue;
+    const i32x4 v = *reinterpret_cast<const i32x4 *>(src + (m0 + row) * N + n0 + e0);
+    uint16_t *d = tl + row * TLD + e0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d[e] = (uint16_t)((uint32_t)v[e >> 1] >> (16 * (e & 1)));
+  }
+  for (int u = tid; u < BM * 16; u += NT) {  // 8 lanes an end
+    const int row = u / 16, h = head(row);
+    if (m0 + row >= M) continue;
+    const int tail = h < lim ? h + (lim - h) / 8 * 8 : lim;
+    const int e = u % 16 < 8 ? u % 8 : tail + u % 8;
+    if (e < (u % 16 < 8 ? (h < lim ? h : lim) : lim))
+      tl[row * TLD + e] = src[(m0 + row) * N + n0 + e];
+  }
+}
+
+// The epilogue's activation, product and residual on a workgroup's tile, whose scaled
+// sums the waves with `mine` hold in acc (16x16 layout, block (i, j) at row row0 + 16 i, column
+// col0 + 16 j). mul and residual come through the LDS tile as whole rows, and a lane
+// reads from it just the places that it writes, so the last of them turns into y in
+// place. Everything stays float32 until y is rounded. tl: nothing uses it on entry.
+template <int BM, int BN_, int NT, int TLD, int TI, int TJ>
+__device__ __forceinline__ void act_tile(uint16_t *tl, f32x4 (&acc)[TI][TJ], const ActTerm &at,
+                                         bool mine, int64_t m0, int64_t M, int64_t n0, int row0,
+                                         int col0) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  uint16_t *own = tl + (row0 + 4 * g) * TLD + col0 + r;
+  auto each = [&](auto &&f) {
+    if (mine) {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[i][j][v] = f(acc[i][j][v], own[(16 * i + v) * TLD + 16 * j]);
+    }
+  };
+  if (at.pre) {
+    each([](float a, uint16_t &t) { t = f32_to_bf16_rne(a); return a; });
+    __syncthreads();
+    store_tile<BM, BN_, NT, TLD>(tl, at.pre, m0, M, n0, at.N);
+    __syncthreads();
+  }
+  if (at.mul) load_tile<BM, BN_, NT, TLD>(tl, at.mul, m0, M, n0, at.N);
+  act_dispatch(at.kind, [&](auto k) {
+    each([](float a, uint16_t &) { return act_value<decltype(k)::value>(a); });
+  });
+  if (at.mul) {
+    __syncthreads();
+    each([](float a, uint16_t &t) { return a * bf16_to_f32(t); });
+  }
+  if (at.res) {
+    __syncthreads();
+    load_tile<BM, BN_, NT, TLD>(tl, at.res, m0, M, n0, at.N);
+    __syncthreads();
+    each([](float a, uint16_t &t) { return a + bf16_to_f32(t); });
+  }
+  each([](float a, uint16_t &t) { t = f32_to_bf16_rne(a); return a; });
+}
+
 __device__ __forceinline__ int swz_x(int row) { return (row >> 1) & 7; }
 __device__ __forceinline__ int swz_w(int row) { return (row >> 2) & 3; }
 
@@ -352,8 +434,8 @@ __global__ __launch_bounds__((64 * GemmLds<WM, TI, SG, KP>::NW)) void k_w8a16_ge
   }
   __syncthreads();
   uint16_t *tl = reinterpret_cast<uint16_t *>(smem + L::XCH);
-  if constexpr (LT::on) {
-    if (part == 0) {  // the same sums in place, then the adapter terms
+  if constexpr (LT::on || LT::act) {
+    if (part == 0) {  // the same sums in place, then the adapter terms or the activation
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int64_t n = n0 + wn * 64 + j * 16 + r;
@@ -371,9 +453,12 @@ __global__ __launch_bounds__((64 * GemmLds<WM, TI, SG, KP>::NW)) void k_w8a16_ge
       }
     }
     // (the other partners' accumulators take part and are dropped)
-    lora_add_tile<BM, BN, 64 * NW, false, 2>(smem, adapters, acc, lt, m0, n0, wm * 16 * TI,
-                                             wn * 64);
-    if (part == 0) {
+    if constexpr (LT::on)
+      lora_add_tile<BM, BN, 64 * NW, false, 2>(smem, adapters, acc, lt, m0, n0, wm * 16 * TI,
+                                               wn * 64);
+    else
+      act_tile<BM, BN, 64 * NW, L::TLD>(tl, acc, lt, part == 0, m0, M, n0, wm * 16 * TI, wn * 64);
+    if (LT::on && part == 0) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -627,7 +712,7 @@ __global__ __launch_bounds__(512, SG == 2 ? 4 : 2) void k_w8a16_gemm_wide(const 
   // scale + bias + bf16 into the LDS output tile; acc[i][j] lane holds
   // D[4g + v][r] of MFMA tile (i, j): row m, column n.
   uint16_t *tl = reinterpret_cast<uint16_t *>(smem);
-  if constexpr (LT::on) {
+  if constexpr (LT::on || LT::act) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int64_t n = n0 + wn * 32 + j * 16 + r;
@@ -638,10 +723,13 @@ __global__ __launch_bounds__(512, SG == 2 ? 4 : 2) void k_w8a16_gemm_wide(const 
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[i][j][v] = s * acc[i][j][v] + b;
     }
-    lora_add_tile<BM, BNW, 512, false, L::NS>(smem, adapters, acc, lt, m0, n0, 0, wn * 32);
+    if constexpr (LT::on)
+      lora_add_tile<BM, BNW, 512, false, L::NS>(smem, adapters, acc, lt, m0, n0, 0, wn * 32);
+    else
+      act_tile<BM, BNW, 512, L::TLD>(tl, acc, lt, true, m0, M, n0, 0, wn * 32);
   }
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < (LT::act ? 0 : 2); ++j) {
     const int col = wn * 32 + j * 16 + r;
     const int64_t n = n0 + col;
     const float s = LT::on ? 1.0f : n < N ? scale[n] : 0.0f;
@@ -735,6 +823,12 @@ hipError_t launch_w8a16_splitk_reduce(const float *part, int S, int64_t M, int64
                                       const float *scale, const uint16_t *bias, uint16_t *y,
                                       hipStream_t st, const LoraTerm &lt) {
   return launch_reduce(part, S, M, N, scale, bias, y, st, lt);
+}
+
+hipError_t launch_w8a16_splitk_reduce(const float *part, int S, int64_t M, int64_t N,
+                                      const float *scale, const uint16_t *bias, uint16_t *y,
+                                      hipStream_t st, const ActTerm &at) {
+  return launch_reduce(part, S, M, N, scale, bias, y, st, at);
 }
 
 namespace {
@@ -861,6 +955,12 @@ hipError_t launch_w8a16_gemm(const uint16_t *x, int64_t M, int64_t K, const int8
                              const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
                              float *part, size_t part_bytes, hipStream_t st, const LoraTerm &lt) {
   return launch_gemm(x, M, K, q, scale, bias, N, y, part, part_bytes, st, lt);
+}
+
+hipError_t launch_w8a16_gemm(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
+                             const float *scale, const uint16_t *bias, int64_t N, uint16_t *y,
+                             float *part, size_t part_bytes, hipStream_t st, const ActTerm &at) {
+  return launch_gemm(x, M, K, q, scale, bias, N, y, part, part_bytes, st, at);
 }
 
 }  // namespace aql

@@ -73,6 +73,12 @@ extern "C" {
 #define AQL_W_Q8CSW 0 /* int8 weights [N, K], one fp32 scale per output channel */
 #define AQL_W_Q4GSW 1 /* 4-bit group-symmetric weights, packed [N, K/2], fp32 scales [N, K/group] */
 
+#define AQL_ACT_NONE 0      /* act(v) = v */
+#define AQL_ACT_RELU 1      /* max(v, 0) */
+#define AQL_ACT_GELU 2      /* v Phi(v), Phi the normal distribution (the erf form) */
+#define AQL_ACT_GELU_TANH 3 /* 0.5 v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) */
+#define AQL_ACT_SILU 4      /* v / (1 + e^-v) */
+
 #define AQL_OP_Q8TA_Q8CSW 1 /* workspace of aql_linear_q8ta_q8csw */
 #define AQL_OP_DQ8CA 2      /* workspace of aql_linear_dq8ca */
 #define AQL_OP_GPTQ_INT8 3  /* workspace of aql_gptq_int8 (M = the column block) */
@@ -86,6 +92,10 @@ extern "C" {
 
 /* Values of a row that share one scale in an 8-bit activation checkpoint. */
 #define AQL_CKPT_GROUP 128
+
+/* Tokens of a page of the 8-bit KV cache, and the largest head. */
+#define AQL_KV_BLOCK 64
+#define AQL_KV_MAX_HEAD 256
 
 /* Largest K accepted by the int8 paths: keeps |sum_k (xq - z) q| below 2^31. */
 #define AQL_MAX_K_INT8 65536
@@ -298,6 +308,50 @@ int aql_linear_dq8ca(const float *x, int64_t M, int64_t K, int wfmt, const void 
                      int64_t N, float *y, float *x_scale_out, int32_t *x_zp_out, void *ws,
                      size_t ws_bytes, void *stream);
 
+/* ---------------------------------- activation, product and residual */
+
+/*
+ * The W8A16 linear with what a decoder layer does to its output in the same launch:
+ *   v[m, n] = scale[n] sum_k x[m, k] q[n, k] + bias[n]
+ *   y[m, n] = act(v[m, n]) mul[m, n] + residual[m, n]
+ * without mul: act(v) + residual, without residual: act(v) mul. A gated MLP is
+ * up = linear(x), h = linear_act(x; gate weights, silu, mul = up), then
+ * out = linear_act(h; down weights, none, residual). All of it is float32 and y is
+ * rounded to bf16 once.
+ *
+ *   x, q, scale, bias, M, N, K, ws   as aql_linear_w8a16
+ *   act       AQL_ACT_*
+ *   mul       device, [M, N] bf16 (may be NULL)
+ *   residual  device, [M, N] bf16 (may be NULL)
+ *   pre       device, [M, N] bf16: v, which the gradients take (output; may be NULL)
+ *   y         device, [M, N] bf16 (output). It may be mul's or residual's own
+ *             memory; outputs overlap nothing else.
+ * Errors: as aql_linear_w8a16, plus an unknown act, misaligned mul, residual or pre,
+ * y == pre.
+ */
+int aql_linear_w8a16_act(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
+                         const float *scale, const uint16_t *bias, int64_t N, int act,
+                         const uint16_t *mul, const uint16_t *residual, uint16_t *pre, uint16_t *y,
+                         void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Gradients of that epilogue, for a gradient dy of y:
+ *   dv[m, n]   = dy[m, n] mul[m, n] act'(pre[m, n])
+ *   dmul[m, n] = dy[m, n] act(pre[m, n])
+ * (the residual's is dy itself); dv is the dy of aql_linear_w8a16_dgrad. act' of relu
+ * at 0 is 0. Float32 inside, each output rounded once.
+ *
+ *   dy, pre   device, [M, N] bf16
+ *   mul       device, [M, N] bf16 (may be NULL: 1)
+ *   dv        device, [M, N] bf16 (output)
+ *   dmul      device, [M, N] bf16 (output; may be NULL). Only with mul.
+ * An output may be an input's own memory. Errors: unknown act; M, N < 0 or
+ * M N > 2^40; dmul without mul (AQL_ERR_PARAM); dv == dmul (AQL_ERR_PARAM); NULL dy, pre
+ * or dv (M, N > 0); misaligned pointers.
+ */
+int aql_act_mul_backward(const uint16_t *dy, const uint16_t *pre, int act, const uint16_t *mul,
+                         int64_t M, int64_t N, uint16_t *dv, uint16_t *dmul, void *stream);
+
 /* ----------------------------------------------------------- grouped W8A16 */
 
 /*
@@ -474,6 +528,104 @@ int aql_act_checkpoint(const void *x, int dtype, int64_t M, int64_t K, int8_t *x
                        void *stream);
 int aql_act_restore(const int8_t *xq, const float *xs, int64_t M, int64_t K, void *x, int dtype,
                     void *stream);
+
+/* ------------------------------------------- paged 8-bit KV cache, attention */
+
+/*
+ * K and V of served sequences in 8 bits, in pages of AQL_KV_BLOCK tokens, and attention
+ * of new tokens over them.
+ *
+ * The cache is four arrays of P pages for Hkv kv heads of D values (DP: D rounded up
+ * to a multiple of 64, the rest zero codes):
+ *   kq  int8 [P, Hkv, DP / 64, AQL_KV_BLOCK, 64]   codes of K, in slices of 64 dims
+ *   vq  int8 [P, Hkv, DP, AQL_KV_BLOCK]            codes of V, transposed
+ *   ks, vs  float32 [P, Hkv]                       a scale for each page and head
+ * A value is code * scale. Nothing needs initialization: places that were not
+ * written are never used.
+ *
+ * A step serves S sequences: sequence s has the rows cu[s] .. cu[s + 1] - 1 of the
+ * step's T rows, new tokens at positions pos[s], pos[s] + 1, ...; the tokens before them
+ * are in the cache. table [S, W] holds each sequence's page numbers: position t lies in
+ * page table[s][t / AQL_KV_BLOCK] at place t % AQL_KV_BLOCK; entries past a
+ * sequence's last page are not read. Rows past cu[S] belong to no sequence.
+ *
+ * The plan. aql_kv_plan divides a step into work for the device; every layer's write
+ * and attention use the same plan while cu and pos stand (it copies what it needs).
+ *   cu      device, [S + 1] int32;  pos  device, [S] int32
+ *   most    most new tokens of any sequence (may be more than that)
+ *   window  tokens that a token sees, itself the last of them; 0: all before it
+ *   plan    device, aql_kv_plan_bytes(...) bytes (output). Its first int32 is 0, or 1 +
+ *           the first sequence that cannot be served (its rows of cu are not
+ *           ascending inside 0 .. T, it has more than `most` tokens, pos < 0, or positions past the
+ *           table): such a sequence is left out, its rows stay as they are; 1 + S
+ *           where sequences overlap to more rows than T: nothing is done.
+ * T, S, Hq, Hkv, W, most and window must be those of the plan in every call that takes it.
+ * Errors: T outside 0..2^20, S outside 0..4096, W outside 1..2^20, Hkv < 1, Hq not a
+ * multiple of Hkv in 1..1024, most outside 1..2^20, window outside 0..2^30 (AQL_ERR_SHAPE);
+ * NULL or misaligned pointers; plan_bytes too small (AQL_ERR_WORKSPACE).
+ */
+size_t aql_kv_plan_bytes(int64_t T, int64_t S, int64_t Hq, int64_t Hkv, int64_t W, int64_t most);
+int aql_kv_plan(const int32_t *cu, const int32_t *pos, int64_t T, int64_t S, int64_t Hq,
+                int64_t Hkv, int64_t W, int64_t most, int64_t window, void *plan,
+                size_t plan_bytes, void *stream);
+
+/*
+ * Quantise the step's new tokens into their pages. For K and V each, a page and head has
+ * s = max(max |x| / 127, 2^-64) over the tokens written since its first place was;
+ * code = clamp(round(x / s), -127, 127), the quotient in binary32. A write behind
+ * live tokens of a page raises s where its tokens need it, and codes that were there become
+ * clamp(round((code * s_old) / s), -127, 127), the product and the quotient each rounded to
+ * binary32. Tokens of a page behind the written ones are lost (a sequence may
+ * be taken back to an earlier position). Sequences must not write one page at once. A
+ * NaN or an infinity leaves its page and head without finite values until it is begun
+ * anew. Page numbers outside 0 .. P - 1 are not written.
+ *
+ *   k, v   device, [T, Hkv, D] float32 (AQL_F32) or bf16 (AQL_BF16), rows of T krow and
+ *          vrow elements apart (slices of a fused projection's output)
+ *   table  device, [S, W] int32
+ * Errors: unknown dtype; D not a multiple of 8 in 8..AQL_KV_MAX_HEAD; P outside 1..2^31 - 1;
+ * krow or vrow below Hkv D, or not whole 16 bytes; the plan's errors; NULL (T, S > 0) or
+ * misaligned pointers.
+ */
+int aql_kv_cache_write(const void *k, int64_t krow, const void *v, int64_t vrow, int dtype,
+                       int64_t T, int64_t S, int64_t Hq, int64_t Hkv, int64_t D,
+                       const int32_t *table, int64_t W, int64_t most, const void *plan, int8_t *kq,
+                       int8_t *vq, float *ks, float *vs, int64_t P, void *stream);
+
+/*
+ * Read the rows that a plan names back: k, v [T, Hkv, D] (outputs), code * scale rounded
+ * to dtype. Rows of a page number outside 0 .. P - 1 become zeros, rows of no sequence
+ * stay. Arguments and errors as aql_kv_cache_write.
+ */
+int aql_kv_cache_read(const int8_t *kq, const int8_t *vq, const float *ks, const float *vs,
+                      int64_t P, int64_t T, int64_t S, int64_t Hq, int64_t Hkv, int64_t D,
+                      const int32_t *table, int64_t W, int64_t most, const void *plan, void *k,
+                      void *v, int dtype, void *stream);
+
+/*
+ * Attention of the step's tokens over the cache, which holds their own K and V already.
+ * The token at position p of a sequence sees positions max(0, p - window + 1) .. p; head i
+ * of Hq reads kv head i / (Hq / Hkv):
+ *   y = sum_t softmax_t(sm_scale q . k_t) v_t,   lse = log sum_t e^(sm_scale q . k_t)
+ * Codes and q enter exactly; a weight (at most 1 where weight times scale is largest) is
+ * rounded to float16 before it meets V; sums, maxima and denominators are float32 and y is
+ * rounded once. Tokens of page numbers outside 0 .. P - 1 are not seen; a row that
+ * sees nothing gets y = 0 and lse = -inf. What a page without finite values does to
+ * rows that see none of its tokens: nothing.
+ *
+ *   q    device, [T, Hq, D] bf16, rows of T qrow elements apart
+ *   y    device, [T, Hq, D] bf16 (output);  lse  device, [T, Hq] float32 (output; may be NULL)
+ *   ws   device workspace of aql_attention_kv8_bytes(...) bytes (may be NULL where that is 0)
+ * Errors: as aql_kv_cache_write; qrow likewise; sm_scale not finite and positive
+ * (AQL_ERR_PARAM); workspace too small.
+ */
+size_t aql_attention_kv8_bytes(int64_t T, int64_t S, int64_t Hq, int64_t Hkv, int64_t D, int64_t W,
+                               int64_t most);
+int aql_attention_kv8(const uint16_t *q, int64_t qrow, int64_t T, int64_t S, int64_t Hq,
+                      int64_t Hkv, int64_t D, float sm_scale, int64_t window, const int8_t *kq,
+                      const int8_t *vq, const float *ks, const float *vs, int64_t P,
+                      const int32_t *table, int64_t W, int64_t most, const void *plan,
+                      uint16_t *y, float *lse, void *ws, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------ stage entry */
 
