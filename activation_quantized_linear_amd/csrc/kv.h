@@ -63,13 +63,17 @@ struct KvSizes {
 };
 
 // Rows of a unit, by the most that any sequence can have.
+constexpr int kKvTileRows = 256;
 constexpr int kv_tile_rows(const KvSizes &z) {
   const int64_t rows = z.most * (z.Hq / z.Hkv);
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kKvTileRows;
 }
 // Units that a step is divided into where there is enough to divide (over all kv heads),
 // and the fewest blocks of one.
-constexpr int64_t kKvTarget = 1024;
+constexpr int64_t kv_target(const KvSizes &z) {
+  const int64_t t = (kv_tile_rows(z) == kKvTileRows ? 512 : 1024) / z.Hkv;
+  return t > 1 ? t : 1;
+}
 constexpr int64_t kKvMinBlocks = 4;
 
 struct KvPlanLayout {
@@ -81,7 +85,7 @@ constexpr KvPlanLayout kv_plan_layout(const KvSizes &z) {
   const int64_t live = z.S < z.T ? z.S : z.T;  // sequences with tokens
   const int64_t G = z.Hq / z.Hkv;
   const int64_t tiles = z.T * G / kv_tile_rows(z) + live;
-  const int64_t target = kKvTarget / z.Hkv > 1 ? kKvTarget / z.Hkv : 1;
+  const int64_t target = kv_target(z);
   const int64_t most = (z.W + kKvMinBlocks - 1) / kKvMinBlocks;  // parts of one tile
   KvPlanLayout p{};
   p.pieces = z.T / kKvBlock + 2 * live;

@@ -17,6 +17,9 @@
 // instructions' lanes 16 g + r, tile tau of a page's 4 takes tokens 16 (r / 4) + 4 tau + r % 4
 // as rows, so lane (r, g) holds tokens 16 g + 4 tau + v of query r. The contractions
 // over dims and over tokens take 16 consecutive bytes of the cache a lane, in the cache's order.
+#include <atomic>
+#include <type_traits>
+
 #include "kv.h"
 
 namespace aql {
@@ -55,11 +58,15 @@ __device__ __forceinline__ f16x8 widen_f16(uint32_t w0, uint32_t w1) {
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// f over the four lanes that hold a query, in each.
+// f over the four lanes that hold a query, without LDS.
 template <class F>
 __device__ __forceinline__ float across(float v, F &&f) {
-  v = f(v, __shfl_xor(v, 16));
-  return f(v, __shfl_xor(v, 32));
+  const uint32_t a = __float_as_uint(v);
+  const auto p = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+  const float w = f(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  const uint32_t b = __float_as_uint(w);
+  const auto q = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  return f(__uint_as_float(q[0]), __uint_as_float(q[1]));
 }
 
 struct AttnArgs {
@@ -129,6 +136,7 @@ __global__ __launch_bounds__(256) void k_kv_attn_stream(AttnArgs a) {
       }
   }
   const int pmin = u.pos + u.row0 / a.G, pmax = u.pos + (u.row0 + rows - 1) / a.G;
+  const uint32_t oldest = a.window > 0 ? (uint32_t)a.window - 1 : 0x7fffffffu;
 
   f32x4 acc[NB][ND];
   float M[NB], l[NB];
@@ -191,23 +199,21 @@ __global__ __launch_bounds__(256) void k_kv_attn_stream(AttnArgs a) {
     }
     if (more) load_k(next);
 
-    // tokens past a query or before its window, and those of a page that is none
+    // tokens past a query or before its window, and those of a page that is none: of the
+    // lane's tokens, how far each lies behind its query, as an unsigned number
     const int t0 = b * 64;
-    const bool whole = live && t0 + 63 <= pmin && (a.window == 0 || t0 > pmax - a.window);
+    const bool whole = live && t0 + 63 <= pmin && (uint32_t)(pmax - t0) <= oldest;
     f16x8 pf[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
+      const int age = live ? qpos[nb] - t0 - 16 * g : -1 - 64;
       float mx = -__builtin_inff();
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           float z = fmaf(s[nb][t][v], c1, c2);
-          if (!whole) {
-            const int tok = t0 + 16 * g + 4 * t + v;
-            const bool see = live && tok <= qpos[nb] && (a.window == 0 || tok > qpos[nb] - a.window);
-            z = see ? z : -__builtin_inff();
-          }
+          if (!whole) z = (uint32_t)(age - 4 * t - v) <= oldest ? z : -__builtin_inff();
           s[nb][t][v] = z;
           mx = fmaxf(mx, z);
         }
@@ -303,6 +309,262 @@ __global__ __launch_bounds__(256) void k_kv_attn_stream(AttnArgs a) {
   }
 }
 
+// LDS writes done and every wave here; loads from memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Many rows (prefill): 4 waves of 16 NB rows of one kv head against a range of blocks. A
+// block's codes are widened once for all waves, on the way from memory into LDS, where
+// they lie as the matrix instructions' operands: fragment by fragment, 16 bytes
+// a lane, lane (r, g) at 256 g + 16 (r ^ 4 g), which neither the reads nor the
+// writes (lanes 4 r + g, 16 bytes of a token or dim each) conflict on. One barrier a block: while
+// block i meets V, block i + 1 meets K, and K of block i + 2 and V of block i + 1
+// go to the halves of LDS that the last block has left.
+template <int C>
+struct TileLds {
+  static constexpr int HALF = 8192 * C;       // one block's K, or V
+  static constexpr int BYTES = 4 * HALF;      // K, K, V, V
+};
+
+template <int NB, int C>
+__global__ __launch_bounds__(256, C == 1 ? 2 : 1) void k_kv_attn_tile(AttnArgs a) {
+  constexpr int DP = 64 * C, ND = DP / 16, HALF = TileLds<C>::HALF;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int i = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
+  if (i >= a.plan[kKvUnits]) return;
+  const KvUnit u = reinterpret_cast<const KvUnit *>(a.plan + a.at_units)[i];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int total = u.len * a.G;                             // rows of the sequence
+  const int wg0 = u.row0 + (int)blockIdx.y * (64 * NB);      // the workgroup's first
+  if (wg0 >= total) return;
+  const int w0 = wg0 + wave * (16 * NB);                     // the wave's first
+  const int rows = min(16 * NB, total - w0);                 // (none: the wave only loads)
+
+  bf16x8 qf[NB][2 * C];
+  int qpos[NB];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int row = w0 + 16 * nb + r;
+    const bool live = row < total;
+    qpos[nb] = u.pos + (live ? row : total - 1) / a.G;
+    const uint16_t *p = a.q + (int64_t)(u.tok + row / a.G) * a.qrow + (h * a.G + row % a.G) * a.c.D;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int d = 64 * c + 16 * g + 8 * s;
+        i32x4 v = {0, 0, 0, 0};
+        if (live && d < a.c.D) v = *reinterpret_cast<const i32x4 *>(p + d);
+        qf[nb][2 * c + s] = __builtin_bit_cast(bf16x8, v);
+      }
+  }
+  const int pmin = u.pos + min(w0, total - 1) / a.G, pmax = u.pos + (min(w0 + 16 * NB, total) - 1) / a.G;
+  const uint32_t oldest = a.window > 0 ? (uint32_t)a.window - 1 : 0x7fffffffu;
+
+  // ---- blocks from memory into LDS
+  const int32_t *row_table = a.table + u.seq * a.W;
+  const int n = u.b1 - u.b0;
+  auto page_at = [&](int k) { return row_table[u.b0 + min(k, n - 1)]; };
+  auto base = [&](int page) {
+    return ((int64_t)(page >= 0 && page < a.c.pages ? page : 0) * a.c.Hkv + h) * (64 * DP);
+  };
+  i32x4 kreg[C], vreg[C];
+  auto load_k = [&](int k) {
+    const int8_t *p = a.c.kq + base(page_at(k)) + wave * 1024 + lane * 16;
+#pragma unroll
+    for (int c = 0; c < C; ++c) kreg[c] = *reinterpret_cast<const i32x4 *>(p + c * 4096);
+  };
+  auto load_v = [&](int k) {
+    const int8_t *p = a.c.vq + base(page_at(k)) + wave * 1024 + lane * 16;
+#pragma unroll
+    for (int c = 0; c < C; ++c) vreg[c] = *reinterpret_cast<const i32x4 *>(p + c * 4096);
+  };
+  // lane 4 x + lg of a load: K: token 16 wave + x, dims 16 lg ..; V: dim 16 (wave + 4 c) + x, tokens 16 lg ..
+  const int lg = lane & 3, lx = lane >> 2;
+  const int kto = (lx >> 2) * (C * 2048) + lg * 256 + (((4 * wave + (lx & 3)) ^ (4 * lg)) * 16);
+  const int vto = wave * 2048 + lg * 256 + ((lx ^ (4 * lg)) * 16);
+  auto put_k = [&](int k) {
+    char *p = smem + (k & 1) * HALF + kto;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      *reinterpret_cast<bf16x8 *>(p + c * 2048) = widen_bf16((uint32_t)kreg[c][0], (uint32_t)kreg[c][1]);
+      *reinterpret_cast<bf16x8 *>(p + c * 2048 + 1024) = widen_bf16((uint32_t)kreg[c][2], (uint32_t)kreg[c][3]);
+    }
+  };
+  auto put_v = [&](int k) {
+    char *p = smem + (2 + (k & 1)) * HALF + vto;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      *reinterpret_cast<f16x8 *>(p + c * 8192) = widen_f16((uint32_t)vreg[c][0], (uint32_t)vreg[c][1]);
+      *reinterpret_cast<f16x8 *>(p + c * 8192 + 1024) = widen_f16((uint32_t)vreg[c][2], (uint32_t)vreg[c][3]);
+    }
+  };
+  const int fo = g * 256 + ((r ^ (4 * g)) * 16);
+
+  f32x4 acc[NB][ND], s[NB][4];
+  float M[NB], off[NB], l[NB];  // off: M, or 0 where no token was seen yet
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    M[nb] = -__builtin_inff();
+    off[nb] = l[nb] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) acc[nb][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  auto scores = [&](int k) {
+    const char *p = smem + (k & 1) * HALF + fo;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) s[nb][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int cs = 0; cs < 2 * C; ++cs) {
+        const bf16x8 kf = *reinterpret_cast<const bf16x8 *>(p + (t * 2 * C + cs) * 1024);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+          s[nb][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[nb][cs], s[nb][t], 0, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // Scores of block k in s become weights and meet V; with `more`, those of block k + 1
+  // take their place. The reference M of a row moves only when a score passes it by 2^8:
+  // weights up to 2^8 lose nothing in float16, and moving it costs every sum a product.
+  auto step = [&](auto more, int k) {
+    const int t0 = 64 * (u.b0 + k), page = page_at(k);
+    const bool live = page >= 0 && page < a.c.pages;
+    const int64_t at = (live ? (int64_t)page : 0) * a.c.Hkv + h;
+    const float vs = a.c.vs[at], iv = __builtin_amdgcn_rcpf(vs);
+    float c1 = a.c.ks[at] * a.sm, c2 = __builtin_amdgcn_logf(vs);
+    if (!(live && t0 + 63 <= pmin && (uint32_t)(pmax - t0) <= oldest)) {
+      // tokens past a query or before its window, and those of a page that is none: of the
+      // lane's tokens, how far each lies behind its query, as an unsigned number
+      int age[NB];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) age[nb] = live ? qpos[nb] - t0 - 16 * g : -1 - 64;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const bool see = (uint32_t)(age[nb] - 4 * t - v) <= oldest;
+            s[nb][t][v] = see ? fmaf(s[nb][t][v], c1, c2) : -__builtin_inff();
+          }
+      c1 = 1.0f;  // (done, so that a scale that is no number stays with its tokens)
+      c2 = 0.0f;
+    }
+    float top[NB];
+    bool grow = false;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      float mx = s[nb][0][0];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) mx = fmaxf(mx, s[nb][t][v]);
+      top[nb] = across(fmaf(mx, c1, c2), [](float x, float y) { return fmaxf(x, y); });
+      grow = grow || top[nb] > M[nb] + 8.0f;
+    }
+    if (__any(grow)) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        M[nb] = fmaxf(M[nb], top[nb]);
+        const float to = M[nb] == -__builtin_inff() ? 0.0f : M[nb];
+        const float alpha = exp2_hw(off[nb] - to);
+        off[nb] = to;
+        l[nb] *= alpha;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) acc[nb][d] *= alpha;
+      }
+    }
+    f16x8 pf[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const float c3 = c2 - off[nb];
+      float sum = 0.0f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float w = exp2_hw(fmaf(s[nb][t][v], c1, c3));
+          sum += w;
+          pf[nb][t >> 1][4 * (t & 1) + v] = (_Float16)w;
+        }
+      l[nb] += sum == 0.0f ? 0.0f : sum * iv;  // (a page that is not seen may have any scale)
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (decltype(more)::value) scores(k + 1);
+    const char *p = smem + (2 + (k & 1)) * HALF + fo;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const f16x8 vf = *reinterpret_cast<const f16x8 *>(p + (2 * d + ks) * 1024);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+          acc[nb][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[nb][ks], acc[nb][d], 0, 0, 0);
+      }
+      if (d & 1) __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto fetch = [&](int k) {
+    put_v(k + 1);
+    load_v(k + 2);
+    put_k(k + 2);
+    load_k(k + 3);
+    lds_barrier();
+  };
+
+  load_k(0);
+  load_v(0);
+  put_k(0);
+  load_k(1);
+  lds_barrier();
+  put_v(0);
+  load_v(1);
+  put_k(1);
+  load_k(2);
+  if (rows <= 0) {  // a wave without rows only brings blocks in
+    lds_barrier();
+    for (int k = 0; k < n - 1; ++k) fetch(k);
+    return;
+  }
+  scores(0);
+  lds_barrier();
+  for (int k = 0; k < n - 1; ++k) {
+    step(std::true_type{}, k);
+    fetch(k);
+  }
+  step(std::false_type{}, n - 1);
+
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int lrow = 16 * nb + r;
+    l[nb] = across(l[nb], [](float x, float y) { return x + y; });  // the lanes' own tokens
+    if (lrow >= rows) continue;
+    const int row = w0 + lrow;
+    const float inv = l[nb] == 0.0f ? 0.0f : 1.0f / l[nb];
+    if (u.part < 0) {
+      if (g == 0) store_lse(a, u.tok, h, row, M[nb], l[nb]);
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+        if (16 * d + 4 * g < a.c.D) store_out(a, u.tok, h, row, 16 * d + 4 * g, acc[nb][d] * inv);
+    } else {
+      const int64_t at = ((int64_t)u.part * a.c.Hkv + h) * kKvTileRows + (row - u.row0);
+      if (g == 0) {
+        a.pm[2 * at] = M[nb];
+        a.pm[2 * at + 1] = l[nb];
+      }
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+        if (16 * d + 4 * g < a.c.D)
+          *reinterpret_cast<f32x4 *>(a.po + at * DP + 16 * d + 4 * g) = acc[nb][d];
+    }
+  }
+}
+
 // The partial results of rows whose blocks were spread over several units, in the order
 // of the parts.
 __global__ __launch_bounds__(256) void k_kv_attn_join(AttnArgs a, int tile) {
@@ -339,6 +601,24 @@ void launch_stream(const AttnArgs &a, unsigned grid, hipStream_t st) {
   }
 }
 
+template <int NB, int C>
+hipError_t launch_tile(const AttnArgs &a, unsigned grid, hipStream_t st) {
+  const auto kern = k_kv_attn_tile<NB, C>;
+  constexpr int bytes = TileLds<C>::BYTES;
+  if constexpr (bytes > 65536) {  // once a device; a launch that the limit refuses reports itself
+    static std::atomic<uint64_t> set{0};
+    int dev = 0;
+    (void)hipGetDevice(&dev);
+    if (!(set.load(std::memory_order_relaxed) >> (dev & 63) & 1)) {
+      (void)hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      (void)hipGetLastError();
+      set.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
+    }
+  }
+  hipLaunchKernelGGL(kern, dim3(grid, kKvTileRows / (64 * NB)), dim3(256), bytes, st, a);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 size_t kv_attention_bytes(const KvSizes &z, int DP) {
@@ -371,10 +651,20 @@ hipError_t launch_kv_attention(const uint16_t *q, int64_t qrow, float sm_scale, 
   a.pm = a.po + lay.parts * z.Hkv * tile * c.DP;
   if (!grid_fits(lay.units * z.Hkv, 256)) return hipErrorInvalidConfiguration;
   const unsigned grid = (unsigned)(lay.units * z.Hkv);
-  if (tile == 16) launch_stream<1>(a, grid, st);
-  else if (tile == 32) launch_stream<2>(a, grid, st);
-  else launch_stream<4>(a, grid, st);
-  const hipError_t e = hipGetLastError();
+  hipError_t e = hipSuccess;
+  if (tile == kKvTileRows) {
+    switch (c.DP / 64) {
+      case 1: e = launch_tile<4, 1>(a, grid, st); break;
+      case 2: e = launch_tile<4, 2>(a, grid, st); break;
+      case 3: e = launch_tile<2, 3>(a, grid, st); break;
+      default: e = launch_tile<2, 4>(a, grid, st); break;
+    }
+  } else {
+    if (tile == 16) launch_stream<1>(a, grid, st);
+    else if (tile == 32) launch_stream<2>(a, grid, st);
+    else launch_stream<4>(a, grid, st);
+    e = hipGetLastError();
+  }
   if (e != hipSuccess || lay.joins == 0) return e;
   hipLaunchKernelGGL(k_kv_attn_join, dim3((unsigned)(lay.joins * z.Hkv)), dim3(256), 0, st, a, tile);
   return hipGetLastError();

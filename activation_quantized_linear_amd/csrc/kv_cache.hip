@@ -416,9 +416,8 @@ __global__ __launch_bounds__(512) void k_kv_read(KvCache c, const int32_t *__res
 
 hipError_t launch_kv_plan(const int32_t *cu, const int32_t *pos, const KvSizes &z, int32_t *plan,
                           hipStream_t st) {
-  const int64_t target = kKvTarget / z.Hkv > 1 ? kKvTarget / z.Hkv : 1;
   hipLaunchKernelGGL(k_kv_plan, dim3(1), dim3(kPlanThreads), 0, st, cu, pos, z, kv_tile_rows(z),
-                     kv_plan_layout(z), target, plan);
+                     kv_plan_layout(z), kv_target(z), plan);
   return hipGetLastError();
 }
 

@@ -125,7 +125,8 @@ class Step:
             assert (lse[n:] == 77).all()
             none = torch.isinf(wl[:n])
             assert torch.equal(none, torch.isinf(lse[:n]))
-            assert (none | ((lse[:n] - wl[:n]).abs() <= ltol[:n])).all()
+            bad = ~(none | ((lse[:n] - wl[:n]).abs() <= ltol[:n]))
+            assert not bad.any(), ((lse[:n] - wl[:n]).abs() / ltol[:n])[bad].max().item()
 
 
 DECODE = [(0, 1), (62, 1), (63, 1), (64, 1), (65, 1), (333, 1), (1000, 1)]
@@ -149,6 +150,10 @@ CASES = [
     ([(4000, 1), (1, 1)], 4, 2, 128, 0),   # one long sequence: spread over several units
     ([(2100, 20)], 2, 1, 64, 0),
     ([(1500, 70)], 2, 1, 128, 900),
+    ([(0, 150), (100, 33), (5, 1)], 3, 1, 192, 0),
+    ([(0, 90), (700, 1), (0, 0), (63, 1), (2000, 64)], 12, 4, 128, 0),   # a chunk among decoding sequences
+    ([(0, 260), (40, 100)], 2, 2, 256, 0),
+    ([(3000, 300)], 2, 2, 64, 0),
 ]
 
 
