@@ -314,7 +314,7 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// Many rows (prefill): 4 waves of 16 NB rows of one kv head against a range of blocks. A
+// Many rows (prefill): 8 waves of 16 NB rows of one kv head against a range of blocks. A
 // block's codes are widened once for all waves, on the way from memory into LDS, where
 // they lie as the matrix instructions' operands: fragment by fragment, 16 bytes
 // a lane, lane (r, g) at 256 g + 16 (r ^ 4 g), which neither the reads nor the
@@ -328,7 +328,7 @@ struct TileLds {
 };
 
 template <int NB, int C>
-__global__ __launch_bounds__(256, C == 1 ? 2 : 1) void k_kv_attn_tile(AttnArgs a) {
+__global__ __launch_bounds__(512, 2) void k_kv_attn_tile(AttnArgs a) {
   constexpr int DP = 64 * C, ND = DP / 16, HALF = TileLds<C>::HALF;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int i = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
@@ -337,7 +337,7 @@ __global__ __launch_bounds__(256, C == 1 ? 2 : 1) void k_kv_attn_tile(AttnArgs a
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int total = u.len * a.G;                             // rows of the sequence
-  const int wg0 = u.row0 + (int)blockIdx.y * (64 * NB);      // the workgroup's first
+  const int wg0 = u.row0 + (int)blockIdx.y * (128 * NB);     // the workgroup's first
   if (wg0 >= total) return;
   const int w0 = wg0 + wave * (16 * NB);                     // the wave's first
   const int rows = min(16 * NB, total - w0);                 // (none: the wave only loads)
@@ -370,35 +370,30 @@ __global__ __launch_bounds__(256, C == 1 ? 2 : 1) void k_kv_attn_tile(AttnArgs a
   auto base = [&](int page) {
     return ((int64_t)(page >= 0 && page < a.c.pages ? page : 0) * a.c.Hkv + h) * (64 * DP);
   };
-  i32x4 kreg[C], vreg[C];
-  auto load_k = [&](int k) {
-    const int8_t *p = a.c.kq + base(page_at(k)) + wave * 1024 + lane * 16;
+  // waves 0 .. 3 bring K, waves 4 .. 7 V, a load of C KiB each. Lane 4 x + lg of a load: of K,
+  // token 16 part + x, dims 16 lg ..; of V, dim 16 (part + 4 c) + x, tokens 16 lg ..
+  const bool isv = wave >= 4;
+  const int part = wave & 3, lg = lane & 3, lx = lane >> 2;
+  const int8_t *src = (isv ? a.c.vq : a.c.kq) + part * 1024 + lane * 16;
+  const int to = isv ? 2 * HALF + part * 2048 + lg * 256 + ((lx ^ (4 * lg)) * 16)
+                     : (lx >> 2) * (C * 2048) + lg * 256 + (((4 * part + (lx & 3)) ^ (4 * lg)) * 16);
+  i32x4 reg[C];
+  auto load = [&](int k) {
+    const int8_t *p = src + base(page_at(k));
 #pragma unroll
-    for (int c = 0; c < C; ++c) kreg[c] = *reinterpret_cast<const i32x4 *>(p + c * 4096);
+    for (int c = 0; c < C; ++c) reg[c] = *reinterpret_cast<const i32x4 *>(p + c * 4096);
   };
-  auto load_v = [&](int k) {
-    const int8_t *p = a.c.vq + base(page_at(k)) + wave * 1024 + lane * 16;
-#pragma unroll
-    for (int c = 0; c < C; ++c) vreg[c] = *reinterpret_cast<const i32x4 *>(p + c * 4096);
-  };
-  // lane 4 x + lg of a load: K: token 16 wave + x, dims 16 lg ..; V: dim 16 (wave + 4 c) + x, tokens 16 lg ..
-  const int lg = lane & 3, lx = lane >> 2;
-  const int kto = (lx >> 2) * (C * 2048) + lg * 256 + (((4 * wave + (lx & 3)) ^ (4 * lg)) * 16);
-  const int vto = wave * 2048 + lg * 256 + ((lx ^ (4 * lg)) * 16);
-  auto put_k = [&](int k) {
-    char *p = smem + (k & 1) * HALF + kto;
+  auto put = [&](int k) {
+    char *p = smem + (k & 1) * HALF + to;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      *reinterpret_cast<bf16x8 *>(p + c * 2048) = widen_bf16((uint32_t)kreg[c][0], (uint32_t)kreg[c][1]);
-      *reinterpret_cast<bf16x8 *>(p + c * 2048 + 1024) = widen_bf16((uint32_t)kreg[c][2], (uint32_t)kreg[c][3]);
-    }
-  };
-  auto put_v = [&](int k) {
-    char *p = smem + (2 + (k & 1)) * HALF + vto;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      *reinterpret_cast<f16x8 *>(p + c * 8192) = widen_f16((uint32_t)vreg[c][0], (uint32_t)vreg[c][1]);
-      *reinterpret_cast<f16x8 *>(p + c * 8192 + 1024) = widen_f16((uint32_t)vreg[c][2], (uint32_t)vreg[c][3]);
+      if (isv) {
+        *reinterpret_cast<f16x8 *>(p + c * 8192) = widen_f16((uint32_t)reg[c][0], (uint32_t)reg[c][1]);
+        *reinterpret_cast<f16x8 *>(p + c * 8192 + 1024) = widen_f16((uint32_t)reg[c][2], (uint32_t)reg[c][3]);
+      } else {
+        *reinterpret_cast<bf16x8 *>(p + c * 2048) = widen_bf16((uint32_t)reg[c][0], (uint32_t)reg[c][1]);
+        *reinterpret_cast<bf16x8 *>(p + c * 2048 + 1024) = widen_bf16((uint32_t)reg[c][2], (uint32_t)reg[c][3]);
+      }
     }
   };
   const int fo = g * 256 + ((r ^ (4 * g)) * 16);
@@ -425,7 +420,6 @@ __global__ __launch_bounds__(256, C == 1 ? 2 : 1) void k_kv_attn_tile(AttnArgs a
         for (int nb = 0; nb < NB; ++nb)
           s[nb][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[nb][cs], s[nb][t], 0, 0, 0);
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
   };
   // Scores of block k in s become weights and meet V; with `more`, those of block k + 1
@@ -493,7 +487,6 @@ __global__ __launch_bounds__(256, C == 1 ? 2 : 1) void k_kv_attn_tile(AttnArgs a
           pf[nb][t >> 1][4 * (t & 1) + v] = (_Float16)w;
         }
       l[nb] += sum == 0.0f ? 0.0f : sum * iv;  // (a page that is not seen may have any scale)
-      __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (decltype(more)::value) scores(k + 1);
     const char *p = smem + (2 + (k & 1)) * HALF + fo;
@@ -506,26 +499,22 @@ __global__ __launch_bounds__(256, C == 1 ? 2 : 1) void k_kv_attn_tile(AttnArgs a
         for (int nb = 0; nb < NB; ++nb)
           acc[nb][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[nb][ks], acc[nb][d], 0, 0, 0);
       }
-      if (d & 1) __builtin_amdgcn_sched_barrier(0);
     }
   };
+  // V is a block behind K
+  const int ahead = isv ? 1 : 2;
   auto fetch = [&](int k) {
-    put_v(k + 1);
-    load_v(k + 2);
-    put_k(k + 2);
-    load_k(k + 3);
+    put(k + ahead);
+    load(k + ahead + 1);
     lds_barrier();
   };
 
-  load_k(0);
-  load_v(0);
-  put_k(0);
-  load_k(1);
+  load(0);
+  if (!isv) put(0);
+  if (!isv) load(1);
   lds_barrier();
-  put_v(0);
-  load_v(1);
-  put_k(1);
-  load_k(2);
+  put(isv ? 0 : 1);
+  load(ahead);
   if (rows <= 0) {  // a wave without rows only brings blocks in
     lds_barrier();
     for (int k = 0; k < n - 1; ++k) fetch(k);
@@ -615,7 +604,7 @@ hipError_t launch_tile(const AttnArgs &a, unsigned grid, hipStream_t st) {
       set.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
     }
   }
-  hipLaunchKernelGGL(kern, dim3(grid, kKvTileRows / (64 * NB)), dim3(256), bytes, st, a);
+  hipLaunchKernelGGL(kern, dim3(grid, kKvTileRows / (128 * NB)), dim3(512), bytes, st, a);
   return hipGetLastError();
 }
 
@@ -649,15 +638,15 @@ hipError_t launch_kv_attention(const uint16_t *q, int64_t qrow, float sm_scale, 
   // sums first: rows of 4 DP bytes keep every access aligned
   a.po = static_cast<float *>(ws);
   a.pm = a.po + lay.parts * z.Hkv * tile * c.DP;
-  if (!grid_fits(lay.units * z.Hkv, 256)) return hipErrorInvalidConfiguration;
+  if (!grid_fits(lay.units * z.Hkv, 512)) return hipErrorInvalidConfiguration;
   const unsigned grid = (unsigned)(lay.units * z.Hkv);
   hipError_t e = hipSuccess;
   if (tile == kKvTileRows) {
     switch (c.DP / 64) {
-      case 1: e = launch_tile<4, 1>(a, grid, st); break;
-      case 2: e = launch_tile<4, 2>(a, grid, st); break;
-      case 3: e = launch_tile<2, 3>(a, grid, st); break;
-      default: e = launch_tile<2, 4>(a, grid, st); break;
+      case 1: e = launch_tile<2, 1>(a, grid, st); break;
+      case 2: e = launch_tile<2, 2>(a, grid, st); break;
+      case 3: e = launch_tile<1, 3>(a, grid, st); break;
+      default: e = launch_tile<1, 4>(a, grid, st); break;
     }
   } else {
     if (tile == 16) launch_stream<1>(a, grid, st);
