@@ -56,6 +56,14 @@ __device__ __forceinline__ f16x8 widen_f16(uint32_t w0, uint32_t w1) {
                                          f16x2_from_u8(x1, 0x04010400u), f16x2_from_u8(x1, 0x04030402u)});
 }
 
+// The power of two below a row's largest magnitude, and its inverse: a row of q times
+// that is below 2, and float16 holds its bf16 values exactly, or to 2^-25 of the largest.
+__device__ __forceinline__ float row_exponent(float largest, float &inv) {
+  const uint32_t e = min(max(__float_as_uint(largest) & 0x7f800000u, 1u << 23), 253u << 23);
+  inv = __uint_as_float((254u << 23) - e);
+  return __uint_as_float(e);
+}
+
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // f over the four lanes that hold a query, without LDS.
@@ -342,22 +350,36 @@ __global__ __launch_bounds__(512, 2) void k_kv_attn_tile(AttnArgs a) {
   const int w0 = wg0 + wave * (16 * NB);                     // the wave's first
   const int rows = min(16 * NB, total - w0);                 // (none: the wave only loads)
 
-  bf16x8 qf[NB][2 * C];
+  f16x8 qf[NB][2 * C];
   int qpos[NB];
+  float qs[NB];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     const int row = w0 + 16 * nb + r;
     const bool live = row < total;
     qpos[nb] = u.pos + (live ? row : total - 1) / a.G;
     const uint16_t *p = a.q + (int64_t)(u.tok + row / a.G) * a.qrow + (h * a.G + row % a.G) * a.c.D;
+    i32x4 v[2 * C];
+    uint32_t mx = 0;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int cs = 0; cs < 2 * C; ++cs) {
+      const int d = 32 * (cs & ~1) + 16 * g + 8 * (cs & 1);
+      v[cs] = i32x4{0, 0, 0, 0};
+      if (live && d < a.c.D) v[cs] = *reinterpret_cast<const i32x4 *>(p + d);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int d = 64 * c + 16 * g + 8 * s;
-        i32x4 v = {0, 0, 0, 0};
-        if (live && d < a.c.D) v = *reinterpret_cast<const i32x4 *>(p + d);
-        qf[nb][2 * c + s] = __builtin_bit_cast(bf16x8, v);
+      for (int e = 0; e < 4; ++e)
+        mx = max(mx, max((uint32_t)v[cs][e] << 16 & 0x7fffffffu, (uint32_t)v[cs][e] & 0x7fff0000u));
+    }
+    float inv;
+    qs[nb] = a.sm * row_exponent(across(__uint_as_float(mx), [](float x, float y) {
+      return __uint_as_float(max(__float_as_uint(x), __float_as_uint(y)));
+    }), inv);
+#pragma unroll
+    for (int cs = 0; cs < 2 * C; ++cs)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        qf[nb][cs][2 * e] = (_Float16)(__uint_as_float((uint32_t)v[cs][e] << 16) * inv);
+        qf[nb][cs][2 * e + 1] = (_Float16)(__uint_as_float((uint32_t)v[cs][e] & 0xffff0000u) * inv);
       }
   }
   const int pmin = u.pos + min(w0, total - 1) / a.G, pmax = u.pos + (min(w0 + 16 * NB, total) - 1) / a.G;
@@ -367,8 +389,9 @@ __global__ __launch_bounds__(512, 2) void k_kv_attn_tile(AttnArgs a) {
   const int32_t *row_table = a.table + u.seq * a.W;
   const int n = u.b1 - u.b0;
   auto page_at = [&](int k) { return row_table[u.b0 + min(k, n - 1)]; };
-  auto base = [&](int page) {
-    return ((int64_t)(page >= 0 && page < a.c.pages ? page : 0) * a.c.Hkv + h) * (64 * DP);
+  // a page that is none reads page 0 and counts for nothing
+  auto head_at = [&](int page) {
+    return (int64_t)(page >= 0 && page < a.c.pages ? page : 0) * a.c.Hkv + h;
   };
   // waves 0 .. 3 bring K, waves 4 .. 7 V, a load of C KiB each. Lane 4 x + lg of a load: of K,
   // token 16 part + x, dims 16 lg ..; of V, dim 16 (part + 4 c) + x, tokens 16 lg ..
@@ -377,27 +400,25 @@ __global__ __launch_bounds__(512, 2) void k_kv_attn_tile(AttnArgs a) {
   const int8_t *src = (isv ? a.c.vq : a.c.kq) + part * 1024 + lane * 16;
   const int to = isv ? 2 * HALF + part * 2048 + lg * 256 + ((lx ^ (4 * lg)) * 16)
                      : (lx >> 2) * (C * 2048) + lg * 256 + (((4 * part + (lx & 3)) ^ (4 * lg)) * 16);
+  const int per = isv ? 8192 : 2048;  // between a load's pieces in LDS
   i32x4 reg[C];
-  auto load = [&](int k) {
-    const int8_t *p = src + base(page_at(k));
+  auto load = [&](int page) {
+    const int8_t *p = src + head_at(page) * (64 * DP);
 #pragma unroll
     for (int c = 0; c < C; ++c) reg[c] = *reinterpret_cast<const i32x4 *>(p + c * 4096);
   };
-  auto put = [&](int k) {
-    char *p = smem + (k & 1) * HALF + to;
+  // piece i of the 2 C that a wave widens: into block k's half of LDS
+  auto put = [&](int k, int i) {
+    *reinterpret_cast<f16x8 *>(smem + (k & 1) * HALF + to + (i >> 1) * per + (i & 1) * 1024) =
+        widen_f16((uint32_t)reg[i >> 1][2 * (i & 1)], (uint32_t)reg[i >> 1][2 * (i & 1) + 1]);
+  };
+  auto put_all = [&](int k) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      if (isv) {
-        *reinterpret_cast<f16x8 *>(p + c * 8192) = widen_f16((uint32_t)reg[c][0], (uint32_t)reg[c][1]);
-        *reinterpret_cast<f16x8 *>(p + c * 8192 + 1024) = widen_f16((uint32_t)reg[c][2], (uint32_t)reg[c][3]);
-      } else {
-        *reinterpret_cast<bf16x8 *>(p + c * 2048) = widen_bf16((uint32_t)reg[c][0], (uint32_t)reg[c][1]);
-        *reinterpret_cast<bf16x8 *>(p + c * 2048 + 1024) = widen_bf16((uint32_t)reg[c][2], (uint32_t)reg[c][3]);
-      }
-    }
+    for (int i = 0; i < 2 * C; ++i) put(k, i);
   };
   const int fo = g * 256 + ((r ^ (4 * g)) * 16);
 
+  const int ahead = isv ? 1 : 2;  // V is a block behind K
   f32x4 acc[NB][ND], s[NB][4];
   float M[NB], off[NB], l[NB];  // off: M, or 0 where no token was seen yet
 #pragma unroll
@@ -407,30 +428,52 @@ __global__ __launch_bounds__(512, 2) void k_kv_attn_tile(AttnArgs a) {
 #pragma unroll
     for (int d = 0; d < ND; ++d) acc[nb][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  auto scores = [&](int k) {
-    const char *p = smem + (k & 1) * HALF + fo;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) s[nb][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int cs = 0; cs < 2 * C; ++cs) {
-        const bf16x8 kf = *reinterpret_cast<const bf16x8 *>(p + (t * 2 * C + cs) * 1024);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-          s[nb][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[nb][cs], s[nb][t], 0, 0, 0);
-      }
-    }
+  constexpr int F = 8 * C;  // fragments of a block's K, and of its V
+  auto read = [&](int k, bool v, int f) {
+    return *reinterpret_cast<const f16x8 *>(smem + (2 * v + (k & 1)) * HALF + fo + f * 1024);
+  };
+  // Before block k: the pages of k .. k + 3 and the scales of k and k + 1 are here, and one of each
+  // is asked for, so that no load waits for another's result.
+  int page0, page1, page2, page3, page4;
+  float ks0, vs0, ks1, vs1, ks2, vs2;
+  auto ask = [&](int k) {
+    page4 = page_at(k + 4);
+    ks2 = a.c.ks[head_at(page2)];
+    vs2 = a.c.vs[head_at(page2)];
+  };
+  auto move = [&]() {
+    page0 = page1;
+    page1 = page2;
+    page2 = page3;
+    page3 = __builtin_amdgcn_readfirstlane(page4);
+    ks0 = ks1;
+    vs0 = vs1;
+    ks1 = ks2;
+    vs1 = vs2;
   };
   // Scores of block k in s become weights and meet V; with `more`, those of block k + 1
   // take their place. The reference M of a row moves only when a score passes it by 2^8:
   // weights up to 2^8 lose nothing in float16, and moving it costs every sum a product.
+  //
+  // Written in the order of issue. Every fragment is read four ahead of its products; the weights'
+  // arithmetic goes between the products of the next scores, the widening of the codes
+  // to come between those with V. (Left to the compiler, the reads wait for each other: the
+  // prefill of 11490 tokens, 32 heads of 128 over 8, takes 474 us.)
   auto step = [&](auto more, int k) {
-    const int t0 = 64 * (u.b0 + k), page = page_at(k);
-    const bool live = page >= 0 && page < a.c.pages;
-    const int64_t at = (live ? (int64_t)page : 0) * a.c.Hkv + h;
-    const float vs = a.c.vs[at], iv = __builtin_amdgcn_rcpf(vs);
-    float c1 = a.c.ks[at] * a.sm, c2 = __builtin_amdgcn_logf(vs);
+    const int t0 = 64 * (u.b0 + k);
+    const bool live = page0 >= 0 && page0 < a.c.pages;
+    const float iv = __builtin_amdgcn_rcpf(vs0);
+    constexpr bool MORE = decltype(more)::value;
+    f16x8 kf[4], vf[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      if constexpr (MORE) kf[f] = read(k + 1, false, f);
+      else vf[f] = read(k, true, f);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    float c1[NB], c2 = __builtin_amdgcn_logf(vs0);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) c1[nb] = ks0 * qs[nb];
     if (!(live && t0 + 63 <= pmin && (uint32_t)(pmax - t0) <= oldest)) {
       // tokens past a query or before its window, and those of a page that is none: of the
       // lane's tokens, how far each lies behind its query, as an unsigned number
@@ -444,10 +487,11 @@ __global__ __launch_bounds__(512, 2) void k_kv_attn_tile(AttnArgs a) {
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             const bool see = (uint32_t)(age[nb] - 4 * t - v) <= oldest;
-            s[nb][t][v] = see ? fmaf(s[nb][t][v], c1, c2) : -__builtin_inff();
+            s[nb][t][v] = see ? fmaf(s[nb][t][v], c1[nb], c2) : -__builtin_inff();
           }
-      c1 = 1.0f;  // (done, so that a scale that is no number stays with its tokens)
-      c2 = 0.0f;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) c1[nb] = 1.0f;  // (done, so that a scale that is no number
+      c2 = 0.0f;                                       // stays with its tokens)
     }
     float top[NB];
     bool grow = false;
@@ -458,7 +502,7 @@ __global__ __launch_bounds__(512, 2) void k_kv_attn_tile(AttnArgs a) {
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int v = 0; v < 4; ++v) mx = fmaxf(mx, s[nb][t][v]);
-      top[nb] = across(fmaf(mx, c1, c2), [](float x, float y) { return fmaxf(x, y); });
+      top[nb] = across(fmaf(mx, c1[nb], c2), [](float x, float y) { return fmaxf(x, y); });
       grow = grow || top[nb] > M[nb] + 8.0f;
     }
     if (__any(grow)) {
@@ -474,57 +518,101 @@ __global__ __launch_bounds__(512, 2) void k_kv_attn_tile(AttnArgs a) {
       }
     }
     f16x8 pf[NB][2];
+    float c3[NB], sum[NB];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const float c3 = c2 - off[nb];
-      float sum = 0.0f;
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float w = exp2_hw(fmaf(s[nb][t][v], c1, c3));
-          sum += w;
-          pf[nb][t >> 1][4 * (t & 1) + v] = (_Float16)w;
-        }
-      l[nb] += sum == 0.0f ? 0.0f : sum * iv;  // (a page that is not seen may have any scale)
+      c3[nb] = c2 - off[nb];
+      sum[nb] = 0.0f;
     }
-    if constexpr (decltype(more)::value) scores(k + 1);
-    const char *p = smem + (2 + (k & 1)) * HALF + fo;
+    f32x4 sn[NB][4];
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int d = 0; d < ND; ++d) {
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const f16x8 vf = *reinterpret_cast<const f16x8 *>(p + (2 * d + ks) * 1024);
+    for (int f = 0; f < F; ++f) {
+      if constexpr (MORE) {
+        const int t = f / (2 * C), cs = f % (2 * C);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
-          acc[nb][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[nb][ks], acc[nb][d], 0, 0, 0);
+          sn[nb][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+              kf[f & 3], qf[nb][cs], cs == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sn[nb][t], 0, 0, 0);
+        if (f + 4 < F) kf[f & 3] = read(k + 1, false, f + 4);
+        else vf[f & 3] = read(k, true, f + 4 - F);
       }
+#pragma unroll
+      for (int e = 16 * NB * f / F; e < 16 * NB * (f + 1) / F; ++e) {
+        const int nb = e >> 4, t = e >> 2 & 3, v = e & 3;
+        const float w = exp2_hw(fmaf(s[nb][t][v], c1[nb], c3[nb]));
+        sum[nb] += w;
+        pf[nb][t >> 1][4 * (t & 1) + v] = (_Float16)w;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)  // (a page that is not seen may have any scale)
+      l[nb] += sum[nb] == 0.0f ? 0.0f : sum[nb] * iv;
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+        acc[nb][f >> 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[f & 3], pf[nb][f & 1],
+                                                                 acc[nb][f >> 1], 0, 0, 0);
+      if (f + 4 < F) vf[f & 3] = read(k, true, f + 4);
+      if constexpr (MORE)
+        if (f % 4 == 1) put(k + ahead, f / 4);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (MORE) {
+      load(isv ? page2 : page3);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) s[nb][t] = sn[nb][t];
     }
   };
-  // V is a block behind K
-  const int ahead = isv ? 1 : 2;
-  auto fetch = [&](int k) {
-    put(k + ahead);
-    load(k + ahead + 1);
-    lds_barrier();
-  };
-
-  load(0);
-  if (!isv) put(0);
-  if (!isv) load(1);
+  page0 = __builtin_amdgcn_readfirstlane(page_at(0));
+  page1 = __builtin_amdgcn_readfirstlane(page_at(1));
+  page2 = __builtin_amdgcn_readfirstlane(page_at(2));
+  page3 = __builtin_amdgcn_readfirstlane(page_at(3));
+  ks0 = a.c.ks[head_at(page0)];
+  vs0 = a.c.vs[head_at(page0)];
+  ks1 = a.c.ks[head_at(page1)];
+  vs1 = a.c.vs[head_at(page1)];
+  load(page0);
+  if (!isv) {
+    put_all(0);
+    load(page1);
+  }
   lds_barrier();
-  put(isv ? 0 : 1);
-  load(ahead);
+  put_all(ahead - 1);
+  load(isv ? page1 : page2);
   if (rows <= 0) {  // a wave without rows only brings blocks in
     lds_barrier();
-    for (int k = 0; k < n - 1; ++k) fetch(k);
+    for (int k = 0; k < n - 1; ++k) {
+      ask(k);
+      put_all(k + ahead);
+      load(isv ? page2 : page3);
+      lds_barrier();
+      move();
+    }
     return;
   }
-  scores(0);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) s[nb][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int cs = 0; cs < 2 * C; ++cs) {
+      const f16x8 kf = read(0, false, t * 2 * C + cs);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+        s[nb][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[nb][cs], s[nb][t], 0, 0, 0);
+    }
+  }
   lds_barrier();
   for (int k = 0; k < n - 1; ++k) {
+    ask(k);
     step(std::true_type{}, k);
-    fetch(k);
+    lds_barrier();
+    move();
   }
   step(std::false_type{}, n - 1);
 
