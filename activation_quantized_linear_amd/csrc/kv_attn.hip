@@ -324,9 +324,8 @@ __device__ __forceinline__ void lds_barrier() {
 
 // Many rows (prefill): 8 waves of 16 NB rows of one kv head against a range of blocks. A
 // block's codes are widened once for all waves, on the way from memory into LDS, where
-// they lie as the matrix instructions' operands: fragment by fragment, 16 bytes
-// a lane, lane (r, g) at 256 g + 16 (r ^ 4 g), which neither the reads nor the
-// writes (lanes 4 r + g, 16 bytes of a token or dim each) conflict on. One barrier a block: while
+// they lie as the matrix instructions' operands, fragment by fragment, 16 bytes a lane in the
+// order of lanes (the one order that neither reads nor writes conflict on). One barrier a block: while
 // block i meets V, block i + 1 meets K, and K of block i + 2 and V of block i + 1
 // go to the halves of LDS that the last block has left.
 template <int C>
@@ -393,13 +392,13 @@ __global__ __launch_bounds__(512, 2) void k_kv_attn_tile(AttnArgs a) {
   auto head_at = [&](int page) {
     return (int64_t)(page >= 0 && page < a.c.pages ? page : 0) * a.c.Hkv + h;
   };
-  // waves 0 .. 3 bring K, waves 4 .. 7 V, a load of C KiB each. Lane 4 x + lg of a load: of K,
-  // token 16 part + x, dims 16 lg ..; of V, dim 16 (part + 4 c) + x, tokens 16 lg ..
+  // waves 0 .. 3 bring K, waves 4 .. 7 V, in loads of a KiB whose lanes hold what the lanes of
+  // two fragments will: of K, tile `part`, slice c of the dims; of V, dims 16 (part + 4 c) ..
   const bool isv = wave >= 4;
-  const int part = wave & 3, lg = lane & 3, lx = lane >> 2;
-  const int8_t *src = (isv ? a.c.vq : a.c.kq) + part * 1024 + lane * 16;
-  const int to = isv ? 2 * HALF + part * 2048 + lg * 256 + ((lx ^ (4 * lg)) * 16)
-                     : (lx >> 2) * (C * 2048) + lg * 256 + (((4 * part + (lx & 3)) ^ (4 * lg)) * 16);
+  const int part = wave & 3;
+  const int8_t *src = isv ? a.c.vq + part * 1024 + r * 64 + 16 * g
+                          : a.c.kq + (16 * (r >> 2) + 4 * part + (r & 3)) * 64 + 16 * g;
+  const int to = isv ? 2 * HALF + part * 2048 + lane * 16 : part * (C * 2048) + lane * 16;
   const int per = isv ? 8192 : 2048;  // between a load's pieces in LDS
   i32x4 reg[C];
   auto load = [&](int page) {
@@ -416,7 +415,7 @@ __global__ __launch_bounds__(512, 2) void k_kv_attn_tile(AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < 2 * C; ++i) put(k, i);
   };
-  const int fo = g * 256 + ((r ^ (4 * g)) * 16);
+  const int fo = lane * 16;
 
   const int ahead = isv ? 1 : 2;  // V is a block behind K
   f32x4 acc[NB][ND], s[NB][4];
