@@ -641,30 +641,94 @@ __global__ __launch_bounds__(512, 2) void k_kv_attn_tile(AttnArgs a) {
   }
 }
 
-// The partial results of rows whose blocks were spread over several units, in the order
-// of the parts.
+// The partial results of rows whose blocks were spread over several units. 16 C threads
+// take a row's dims; with SPREAD (few rows, up to hundreds of parts) the workgroup's groups of
+// threads share a row's parts and add up in LDS, else (many rows, few parts) each takes a
+// row. Sums are in one order for a given number of parts.
+template <int C, bool SPREAD>
 __global__ __launch_bounds__(256) void k_kv_attn_join(AttnArgs a, int tile) {
+  constexpr int TPR = 16 * C, GROUPS = 256 / TPR, U = 4;  // U: parts in flight
+  __shared__ float red[2][GROUPS];
+  __shared__ f32x4 sums[SPREAD ? GROUPS : 1][TPR];
   const int i = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
   if (i >= a.plan[kKvJoins]) return;
   const KvJoin u = reinterpret_cast<const KvJoin *>(a.plan + a.at_joins)[i];
-  const int rows = min(tile, u.len * a.G - u.row0), per = a.c.D / 4;
-  for (int e = threadIdx.x; e < rows * per; e += 256) {
-    const int row = e / per, d = 4 * (e % per);
-    const int64_t step = (int64_t)a.c.Hkv * tile;
-    const int64_t at = ((int64_t)u.part * a.c.Hkv + h) * tile + row;
-    float top = -__builtin_inff();
-    for (int p = 0; p < u.parts; ++p) top = fmaxf(top, a.pm[2 * (at + p * step)]);
-    const float off = top == -__builtin_inff() ? 0.0f : top;
-    float L = 0.0f;
-    f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    for (int p = 0; p < u.parts; ++p) {
-      const float f = exp2_hw(a.pm[2 * (at + p * step)] - off);
-      L = fmaf(a.pm[2 * (at + p * step) + 1], f, L);
-      o += *reinterpret_cast<const f32x4 *>(a.po + (at + p * step) * a.c.DP + d) * f;
+  const int rows = min(tile, u.len * a.G - u.row0);
+  const int gi = threadIdx.x / TPR, d = 4 * (threadIdx.x % TPR);
+  const int row = SPREAD ? (int)blockIdx.y : (int)blockIdx.y * GROUPS + gi;
+  if (SPREAD ? row >= rows : (int)blockIdx.y * GROUPS >= rows) return;
+  const bool live = gi < GROUPS && row < rows && d < a.c.D;
+  const int64_t step = (int64_t)a.c.Hkv * tile;
+  const int64_t at = ((int64_t)u.part * a.c.Hkv + h) * tile + row;
+  const int p0 = SPREAD ? gi : 0, by = SPREAD ? GROUPS : 1;
+  float top = -__builtin_inff(), L = 0.0f;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  if (live)
+    for (int p = p0; p < u.parts; p += U * by) {
+      float m[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) m[k] = a.pm[2 * (at + min(p + k * by, u.parts - 1) * step)];
+#pragma unroll
+      for (int k = 0; k < U; ++k) top = fmaxf(top, m[k]);
     }
-    if (d == 0) store_lse(a, u.tok, h, u.row0 + row, top, L);
-    store_out(a, u.tok, h, u.row0 + row, d, L == 0.0f ? f32x4{0.f, 0.f, 0.f, 0.f} : o * (1.0f / L));
+  if constexpr (SPREAD) {
+    if (gi < GROUPS && d == 0) red[0][gi] = top;
+    __syncthreads();
+    for (int k = 0; k < GROUPS; ++k) top = fmaxf(top, red[0][k]);
   }
+  const float off = top == -__builtin_inff() ? 0.0f : top;
+  if (live)
+    for (int p = p0; p < u.parts; p += U * by) {
+      float m[U], l[U];
+      f32x4 v[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int64_t r = at + min(p + k * by, u.parts - 1) * step;
+        m[k] = a.pm[2 * r];
+        l[k] = a.pm[2 * r + 1];
+        v[k] = *reinterpret_cast<const f32x4 *>(a.po + r * a.c.DP + d);
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const float f = exp2_hw(m[k] - off);
+        if (p + k * by < u.parts) {  // (a part that is none may hold anything)
+          L = fmaf(l[k], f, L);
+          o += v[k] * f;
+        }
+      }
+    }
+  if constexpr (SPREAD) {
+    if (live) {
+      sums[gi][threadIdx.x % TPR] = o;
+      if (d == 0) red[1][gi] = L;
+    }
+    __syncthreads();
+    if (gi != 0 || !live) return;
+    L = 0.0f;
+    o = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < GROUPS; ++k) {
+      L += red[1][k];
+      o += sums[k][threadIdx.x];
+    }
+  }
+  if (!live) return;
+  if (d == 0) store_lse(a, u.tok, h, u.row0 + row, top, L);
+  store_out(a, u.tok, h, u.row0 + row, d, o * (L == 0.0f ? 0.0f : 1.0f / L));
+}
+
+template <bool SPREAD>
+hipError_t launch_join(const AttnArgs &a, int64_t joins, int tile, hipStream_t st) {
+  const auto go = [&](auto kern, int groups) {
+    hipLaunchKernelGGL(kern, dim3((unsigned)(joins * a.c.Hkv), SPREAD ? tile : (tile + groups - 1) / groups),
+                       dim3(256), 0, st, a, tile);
+  };
+  switch (a.c.DP / 64) {
+    case 1: go(k_kv_attn_join<1, SPREAD>, 16); break;
+    case 2: go(k_kv_attn_join<2, SPREAD>, 8); break;
+    case 3: go(k_kv_attn_join<3, SPREAD>, 5); break;
+    default: go(k_kv_attn_join<4, SPREAD>, 4); break;
+  }
+  return hipGetLastError();
 }
 
 template <int NB>
@@ -742,8 +806,8 @@ hipError_t launch_kv_attention(const uint16_t *q, int64_t qrow, float sm_scale, 
     e = hipGetLastError();
   }
   if (e != hipSuccess || lay.joins == 0) return e;
-  hipLaunchKernelGGL(k_kv_attn_join, dim3((unsigned)(lay.joins * z.Hkv)), dim3(256), 0, st, a, tile);
-  return hipGetLastError();
+  return tile == kKvTileRows ? launch_join<false>(a, lay.joins, tile, st)
+                             : launch_join<true>(a, lay.joins, tile, st);
 }
 
 }  // namespace aql
