@@ -322,7 +322,7 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// Many rows (prefill): 8 waves of 16 NB rows of one kv head against a range of blocks. A
+// Many rows (prefill): 4 waves of 16 NB rows of one kv head against a range of blocks. A
 // block's codes are widened once for all waves, on the way from memory into LDS, where
 // they lie as the matrix instructions' operands, fragment by fragment, 16 bytes a lane in the
 // order of lanes (the one order that neither reads nor writes conflict on). One barrier a block: while
@@ -335,7 +335,7 @@ struct TileLds {
 };
 
 template <int NB, int C>
-__global__ __launch_bounds__(512, 2) void k_kv_attn_tile(AttnArgs a) {
+__global__ __launch_bounds__(256, 2) void k_kv_attn_tile(AttnArgs a) {
   constexpr int DP = 64 * C, ND = DP / 16, HALF = TileLds<C>::HALF;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int i = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
@@ -344,7 +344,7 @@ __global__ __launch_bounds__(512, 2) void k_kv_attn_tile(AttnArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int total = u.len * a.G;                             // rows of the sequence
-  const int wg0 = u.row0 + (int)blockIdx.y * (128 * NB);     // the workgroup's first
+  const int wg0 = u.row0 + (int)blockIdx.y * (64 * NB);     // the workgroup's first
   if (wg0 >= total) return;
   const int w0 = wg0 + wave * (16 * NB);                     // the wave's first
   const int rows = min(16 * NB, total - w0);                 // (none: the wave only loads)
@@ -392,32 +392,40 @@ __global__ __launch_bounds__(512, 2) void k_kv_attn_tile(AttnArgs a) {
   auto head_at = [&](int page) {
     return (int64_t)(page >= 0 && page < a.c.pages ? page : 0) * a.c.Hkv + h;
   };
-  // waves 0 .. 3 bring K, waves 4 .. 7 V, in loads of a KiB whose lanes hold what the lanes of
-  // two fragments will: of K, tile `part`, slice c of the dims; of V, dims 16 (part + 4 c) ..
-  const bool isv = wave >= 4;
-  const int part = wave & 3;
-  const int8_t *src = isv ? a.c.vq + part * 1024 + r * 64 + 16 * g
-                          : a.c.kq + (16 * (r >> 2) + 4 * part + (r & 3)) * 64 + 16 * g;
-  const int to = isv ? 2 * HALF + part * 2048 + lane * 16 : part * (C * 2048) + lane * 16;
-  const int per = isv ? 8192 : 2048;  // between a load's pieces in LDS
-  i32x4 reg[C];
-  auto load = [&](int page) {
-    const int8_t *p = src + head_at(page) * (64 * DP);
+  // every wave brings C KiB of K and of V, in loads whose lanes hold what the lanes of two
+  // fragments will: of K, tile `wave`, slice c of the dims; of V, dims 16 (wave + 4 c) ..
+  const int8_t *ksrc = a.c.kq + (16 * (r >> 2) + 4 * wave + (r & 3)) * 64 + 16 * g;
+  const int8_t *vsrc = a.c.vq + wave * 1024 + r * 64 + 16 * g;
+  i32x4 kr[C], vr[C];
+  auto load_k = [&](int page) {
+    const int8_t *p = ksrc + head_at(page) * (64 * DP);
 #pragma unroll
-    for (int c = 0; c < C; ++c) reg[c] = *reinterpret_cast<const i32x4 *>(p + c * 4096);
+    for (int c = 0; c < C; ++c) kr[c] = *reinterpret_cast<const i32x4 *>(p + c * 4096);
   };
-  // piece i of the 2 C that a wave widens: into block k's half of LDS
-  auto put = [&](int k, int i) {
-    *reinterpret_cast<f16x8 *>(smem + (k & 1) * HALF + to + (i >> 1) * per + (i & 1) * 1024) =
-        widen_f16((uint32_t)reg[i >> 1][2 * (i & 1)], (uint32_t)reg[i >> 1][2 * (i & 1) + 1]);
-  };
-  auto put_all = [&](int k) {
+  auto load_v = [&](int page) {
+    const int8_t *p = vsrc + head_at(page) * (64 * DP);
 #pragma unroll
-    for (int i = 0; i < 2 * C; ++i) put(k, i);
+    for (int c = 0; c < C; ++c) vr[c] = *reinterpret_cast<const i32x4 *>(p + c * 4096);
+  };
+  // piece i of the 2 C that a wave widens of either, into block k's half of LDS
+  auto put_k = [&](int k, int i) {
+    *reinterpret_cast<f16x8 *>(smem + (k & 1) * HALF + wave * (C * 2048) + lane * 16 + i * 1024) =
+        widen_f16((uint32_t)kr[i >> 1][2 * (i & 1)], (uint32_t)kr[i >> 1][2 * (i & 1) + 1]);
+  };
+  auto put_v = [&](int k, int i) {
+    *reinterpret_cast<f16x8 *>(smem + (2 + (k & 1)) * HALF + wave * 2048 + lane * 16 +
+                               (i >> 1) * 8192 + (i & 1) * 1024) =
+        widen_f16((uint32_t)vr[i >> 1][2 * (i & 1)], (uint32_t)vr[i >> 1][2 * (i & 1) + 1]);
+  };
+  auto put_all = [&](int k) {  // V is a block behind K
+#pragma unroll
+    for (int i = 0; i < 2 * C; ++i) {
+      put_v(k + 1, i);
+      put_k(k + 2, i);
+    }
   };
   const int fo = lane * 16;
 
-  const int ahead = isv ? 1 : 2;  // V is a block behind K
   f32x4 acc[NB][ND], s[NB][4];
   float M[NB], off[NB], l[NB];  // off: M, or 0 where no token was seen yet
 #pragma unroll
@@ -556,11 +564,15 @@ __global__ __launch_bounds__(512, 2) void k_kv_attn_tile(AttnArgs a) {
                                                                  acc[nb][f >> 1], 0, 0, 0);
       if (f + 4 < F) vf[f & 3] = read(k, true, f + 4);
       if constexpr (MORE)
-        if (f % 4 == 1) put(k + ahead, f / 4);
+        if (f & 1) {
+          if (f < F / 2) put_v(k + 1, f / 2);
+          else put_k(k + 2, f / 2 - 2 * C);
+        }
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (MORE) {
-      load(isv ? page2 : page3);
+      load_v(page2);
+      load_k(page3);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -575,20 +587,22 @@ __global__ __launch_bounds__(512, 2) void k_kv_attn_tile(AttnArgs a) {
   vs0 = a.c.vs[head_at(page0)];
   ks1 = a.c.ks[head_at(page1)];
   vs1 = a.c.vs[head_at(page1)];
-  load(page0);
-  if (!isv) {
-    put_all(0);
-    load(page1);
-  }
+  load_k(page0);
+  load_v(page0);
+#pragma unroll
+  for (int i = 0; i < 2 * C; ++i) put_k(0, i);
+  load_k(page1);
   lds_barrier();
-  put_all(ahead - 1);
-  load(isv ? page1 : page2);
+  put_all(-1);
+  load_v(page1);
+  load_k(page2);
   if (rows <= 0) {  // a wave without rows only brings blocks in
     lds_barrier();
     for (int k = 0; k < n - 1; ++k) {
       ask(k);
-      put_all(k + ahead);
-      load(isv ? page2 : page3);
+      put_all(k);
+      load_v(page2);
+      load_k(page3);
       lds_barrier();
       move();
     }
@@ -755,7 +769,7 @@ hipError_t launch_tile(const AttnArgs &a, unsigned grid, hipStream_t st) {
       set.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
     }
   }
-  hipLaunchKernelGGL(kern, dim3(grid, kKvTileRows / (128 * NB)), dim3(512), bytes, st, a);
+  hipLaunchKernelGGL(kern, dim3(grid, kKvTileRows / (64 * NB)), dim3(256), bytes, st, a);
   return hipGetLastError();
 }
 
@@ -789,7 +803,7 @@ hipError_t launch_kv_attention(const uint16_t *q, int64_t qrow, float sm_scale, 
   // sums first: rows of 4 DP bytes keep every access aligned
   a.po = static_cast<float *>(ws);
   a.pm = a.po + lay.parts * z.Hkv * tile * c.DP;
-  if (!grid_fits(lay.units * z.Hkv, 512)) return hipErrorInvalidConfiguration;
+  if (!grid_fits(lay.units * z.Hkv, 256)) return hipErrorInvalidConfiguration;
   const unsigned grid = (unsigned)(lay.units * z.Hkv);
   hipError_t e = hipSuccess;
   if (tile == kKvTileRows) {
