@@ -71,8 +71,8 @@ __device__ __forceinline__ int owner(const int *first, int S, int i) {
 
 // One workgroup. Sequences' pieces and tiles are counted and summed up; every piece and
 // tile then finds its sequence by bisection, three times over the tiles: their blocks,
-// their units' lengths, the units. A tile's blocks are divided into units of
-// at most `chunk` = total / target blocks, and units are laid out longest
+// their units' lengths, the units. A tile's blocks are divided into units of about
+// `chunk` = total / target blocks, at most a quarter more, and units are laid out longest
 // first (by classes of length: atomics in LDS give the places inside a class, which no
 // result depends on), so that the last ones to start are short.
 __global__ __launch_bounds__(kPlanThreads) void k_kv_plan(const int32_t *__restrict__ cu,
@@ -140,7 +140,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_kv_plan(const int32_t *__restr
   int64_t chunk = (blocks + target - 1) / target;
   chunk = chunk < kKvMinBlocks ? kKvMinBlocks : chunk;
   if (lay.parts == 0) chunk = z.W;
-  const int longest = (int)min(chunk, (int64_t)s_longest);
+  const int longest = (int)min(chunk + chunk / 4, (int64_t)s_longest);
   auto bin_of = [&](int len) {  // long units first
     return kBins - 1 - (int)((int64_t)len * (kBins - 1) / (longest > 0 ? longest : 1));
   };
@@ -167,7 +167,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_kv_plan(const int32_t *__restr
       const int row0 = (i - first_tile[s]) * tile;
       int b0, b1;
       tile_blocks(q, G, z.window, row0, tile, b0, b1);
-      const int n = b1 - b0, parts = (int)((n + chunk - 1) / chunk);
+      const int n = b1 - b0, parts = max(1, (int)((n + chunk - 1 - chunk / 4) / chunk));
       const int each = (n + parts - 1) / parts, bin = bin_of(each);
       if (pass == 0) {
         atomicAdd(&count[bin], parts);
