@@ -71,10 +71,14 @@ constexpr int kv_tile_rows(const KvSizes &z) {
 // Units that a step is divided into where there is enough to divide (over all kv heads),
 // and the fewest blocks of one.
 constexpr int64_t kv_target(const KvSizes &z) {
-  const int64_t t = (kv_tile_rows(z) == kKvTileRows ? 512 : 1024) / z.Hkv;
+  const int64_t t = (kv_tile_rows(z) == kKvTileRows ? 512 : 768) / z.Hkv;
   return t > 1 ? t : 1;
 }
 constexpr int64_t kKvMinBlocks = 4;
+// Tables of at most so many blocks leave nothing to divide: a second launch that joins the parts
+// costs what 4 waves take for two more blocks each (one request of 334 tokens, 15 heads
+// of 64 over 5: 5.1 us in one unit, 7.0 divided; of 1024 tokens 8.1, 7.1).
+constexpr int64_t kKvWhole = 8;
 
 struct KvPlanLayout {
   int64_t pieces, units, joins;        // most of each
@@ -86,7 +90,7 @@ constexpr KvPlanLayout kv_plan_layout(const KvSizes &z) {
   const int64_t G = z.Hq / z.Hkv;
   const int64_t tiles = z.T * G / kv_tile_rows(z) + live;
   const int64_t target = kv_target(z);
-  const int64_t most = (z.W + kKvMinBlocks - 1) / kKvMinBlocks;  // parts of one tile
+  const int64_t most = z.W <= kKvWhole ? 1 : (z.W + kKvMinBlocks - 1) / kKvMinBlocks;  // of a tile
   KvPlanLayout p{};
   p.pieces = z.T / kKvBlock + 2 * live;
   // a unit has at least total / target blocks, but for the last one of a tile

@@ -7,9 +7,9 @@
 //   z_t = a log2(e) ks (q . code_k) + log2 vs,   w_t = 2^(z_t - M),
 // M the running maximum of z, so that outputs are sums of w_t code_v and w_t is at most 1
 // where it weighs most, whatever the pages' scales; the denominator adds a page's
-// w_t times 1 / vs. Codes widen exactly: k to bf16 beside q's own bf16, v to float16
-// beside w, which is rounded to float16 (by 2^-11 of its value, or below 2^-14 by 2^-25 of
-// the largest: a bf16 output itself is rounded by 2^-8). Sums, M and the denominator are float32.
+// w_t times 1 / vs. Codes widen to float16 exactly, and so does q under an exponent of its row
+// (values below 2^-14 of the row's largest by 2^-25 of that). w is rounded to float16 (by 2^-11
+// of its value, or below 2^-14 by 2^-25 of the largest: a bf16 output itself is rounded by 2^-8). Sums, M and the denominator are float32.
 //
 // Scores are computed transposed (tokens as rows), so that a lane ends with 16
 // consecutive tokens of one query, which is the operand layout of the second product:
@@ -29,20 +29,6 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ uint32_t bf16x2_from_i8(int lo, int hi) {
-  return __builtin_amdgcn_perm(__float_as_uint((float)hi), __float_as_uint((float)lo),
-                               0x07060302u);
-}
-
-// Eight codes (two dwords) -> eight bf16, exactly.
-__device__ __forceinline__ bf16x8 widen_bf16(uint32_t w0, uint32_t w1) {
-  const uint32_t a = bf16x2_from_i8((int)(int8_t)w0, (int)(int8_t)(w0 >> 8));
-  const uint32_t b = bf16x2_from_i8((int)(int8_t)(w0 >> 16), (int)w0 >> 24);
-  const uint32_t c = bf16x2_from_i8((int)(int8_t)w1, (int)(int8_t)(w1 >> 8));
-  const uint32_t d = bf16x2_from_i8((int)(int8_t)(w1 >> 16), (int)w1 >> 24);
-  return __builtin_bit_cast(bf16x8, u32x4{a, b, c, d});
-}
-
 // Two codes, already offset by 128, as the low mantissa bits of float16 1024, less 1152.
 __device__ __forceinline__ uint32_t f16x2_from_u8(uint32_t w, uint32_t sel) {
   const f16x2 v = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, w, sel));
@@ -57,7 +43,7 @@ __device__ __forceinline__ f16x8 widen_f16(uint32_t w0, uint32_t w1) {
 }
 
 // The power of two below a row's largest magnitude, and its inverse: a row of q times
-// that is below 2, and float16 holds its bf16 values exactly, or to 2^-25 of the largest.
+// that is below 2.
 __device__ __forceinline__ float row_exponent(float largest, float &inv) {
   const uint32_t e = min(max(__float_as_uint(largest) & 0x7f800000u, 1u << 23), 253u << 23);
   inv = __uint_as_float((254u << 23) - e);
@@ -75,6 +61,36 @@ __device__ __forceinline__ float across(float v, F &&f) {
   const uint32_t b = __float_as_uint(w);
   const auto q = __builtin_amdgcn_permlane16_swap(b, b, false, false);
   return f(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+
+// A lane's operands of one row of q, dims 64 c + 16 g + 8 s .. + 7 in q[2 c + s], in float16
+// under the row's exponent, which goes into the scores' scale. Dims from D on, and rows that
+// are none, are zero.
+template <int C>
+__device__ __forceinline__ void load_query(const uint16_t *p, bool live, int D, int g, float sm,
+                                           f16x8 (&q)[2 * C], float &scale) {
+  i32x4 v[2 * C];
+  uint32_t mx = 0;
+#pragma unroll
+  for (int cs = 0; cs < 2 * C; ++cs) {
+    const int d = 32 * (cs & ~1) + 16 * g + 8 * (cs & 1);
+    v[cs] = i32x4{0, 0, 0, 0};
+    if (live && d < D) v[cs] = *reinterpret_cast<const i32x4 *>(p + d);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      mx = max(mx, max((uint32_t)v[cs][e] << 16 & 0x7fffffffu, (uint32_t)v[cs][e] & 0x7fff0000u));
+  }
+  float inv;
+  scale = sm * row_exponent(across(__uint_as_float(mx), [](float x, float y) {
+            return __uint_as_float(max(__float_as_uint(x), __float_as_uint(y)));
+          }), inv);
+#pragma unroll
+  for (int cs = 0; cs < 2 * C; ++cs)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      q[cs][2 * e] = (_Float16)(__uint_as_float((uint32_t)v[cs][e] << 16) * inv);
+      q[cs][2 * e + 1] = (_Float16)(__uint_as_float((uint32_t)v[cs][e] & 0xffff0000u) * inv);
+    }
 }
 
 struct AttnArgs {
@@ -110,7 +126,8 @@ __device__ __forceinline__ void store_lse(const AttnArgs &a, int tok, int h, int
 }
 
 // Few rows (decode): 16 NB rows of one kv head against a range of blocks, streamed from
-// memory once. Bound by memory. The four waves take blocks in turn, each with a
+// memory once (loads that leave no copy in the caches: 64 requests of up to 8192 tokens 88 us,
+// 103 with them). Bound by memory. The four waves take blocks in turn, each with a
 // maximum and sums of its own, and join in LDS at the end. The next block's K is in
 // flight from when the present one is used up, V from the same moment one block earlier.
 template <int NB, int C>
@@ -125,23 +142,16 @@ __global__ __launch_bounds__(256) void k_kv_attn_stream(AttnArgs a) {
   const int r = lane & 15, g = lane >> 4;
   const int rows = min(16 * NB, u.len * a.G - u.row0);  // of the unit
 
-  bf16x8 qf[NB][2 * C];
+  f16x8 qf[NB][2 * C];
   int qpos[NB];
+  float qs[NB];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     const int row = u.row0 + 16 * nb + r;
     const bool live = 16 * nb + r < rows;
     qpos[nb] = u.pos + (live ? row / a.G : u.row0 / a.G);
     const uint16_t *p = a.q + (int64_t)(u.tok + row / a.G) * a.qrow + (h * a.G + row % a.G) * a.c.D;
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int d = 64 * c + 16 * g + 8 * s;
-        i32x4 v = {0, 0, 0, 0};
-        if (live && d < a.c.D) v = *reinterpret_cast<const i32x4 *>(p + d);
-        qf[nb][2 * c + s] = __builtin_bit_cast(bf16x8, v);
-      }
+    load_query<C>(p, live, a.c.D, g, a.sm, qf[nb], qs[nb]);
   }
   const int pmin = u.pos + u.row0 / a.G, pmax = u.pos + (u.row0 + rows - 1) / a.G;
   const uint32_t oldest = a.window > 0 ? (uint32_t)a.window - 1 : 0x7fffffffu;
@@ -171,7 +181,7 @@ __global__ __launch_bounds__(256) void k_kv_attn_stream(AttnArgs a) {
     for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int t = 0; t < 4; ++t)
-        kb[t][c] = *reinterpret_cast<const i32x4 *>(p + c * 4096 + t * 256);
+        kb[t][c] = __builtin_nontemporal_load(reinterpret_cast<const i32x4 *>(p + c * 4096 + t * 256));
   };
   int b = u.b0 + wave;
   int page = b < u.b1 ? page_at(b) : 0;
@@ -182,11 +192,11 @@ __global__ __launch_bounds__(256) void k_kv_attn_stream(AttnArgs a) {
     {
       const int8_t *p = a.c.vq + base(page) + vofs;
 #pragma unroll
-      for (int d = 0; d < ND; ++d) vb[d] = *reinterpret_cast<const i32x4 *>(p + d * 1024);
+      for (int d = 0; d < ND; ++d) vb[d] = __builtin_nontemporal_load(reinterpret_cast<const i32x4 *>(p + d * 1024));
     }
     const bool live = page >= 0 && page < a.c.pages;
     const int64_t at = (live ? (int64_t)page : 0) * a.c.Hkv + h;
-    const float c1 = a.c.ks[at] * a.sm, vs = a.c.vs[at];
+    const float ks = a.c.ks[at], vs = a.c.vs[at];
     const float c2 = __builtin_amdgcn_logf(vs), iv = __builtin_amdgcn_rcpf(vs);
 
     f32x4 s[NB][4];
@@ -196,12 +206,12 @@ __global__ __launch_bounds__(256) void k_kv_attn_stream(AttnArgs a) {
       for (int nb = 0; nb < NB; ++nb) s[nb][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const bf16x8 k0 = widen_bf16((uint32_t)kb[t][c][0], (uint32_t)kb[t][c][1]);
-        const bf16x8 k1 = widen_bf16((uint32_t)kb[t][c][2], (uint32_t)kb[t][c][3]);
+        const f16x8 k0 = widen_f16((uint32_t)kb[t][c][0], (uint32_t)kb[t][c][1]);
+        const f16x8 k1 = widen_f16((uint32_t)kb[t][c][2], (uint32_t)kb[t][c][3]);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          s[nb][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, qf[nb][2 * c], s[nb][t], 0, 0, 0);
-          s[nb][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, qf[nb][2 * c + 1], s[nb][t], 0, 0, 0);
+          s[nb][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[nb][2 * c], s[nb][t], 0, 0, 0);
+          s[nb][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[nb][2 * c + 1], s[nb][t], 0, 0, 0);
         }
       }
     }
@@ -215,6 +225,7 @@ __global__ __launch_bounds__(256) void k_kv_attn_stream(AttnArgs a) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int age = live ? qpos[nb] - t0 - 16 * g : -1 - 64;
+      const float c1 = ks * qs[nb];
       float mx = -__builtin_inff();
 #pragma unroll
       for (int t = 0; t < 4; ++t)
@@ -358,28 +369,7 @@ __global__ __launch_bounds__(256, 2) void k_kv_attn_tile(AttnArgs a) {
     const bool live = row < total;
     qpos[nb] = u.pos + (live ? row : total - 1) / a.G;
     const uint16_t *p = a.q + (int64_t)(u.tok + row / a.G) * a.qrow + (h * a.G + row % a.G) * a.c.D;
-    i32x4 v[2 * C];
-    uint32_t mx = 0;
-#pragma unroll
-    for (int cs = 0; cs < 2 * C; ++cs) {
-      const int d = 32 * (cs & ~1) + 16 * g + 8 * (cs & 1);
-      v[cs] = i32x4{0, 0, 0, 0};
-      if (live && d < a.c.D) v[cs] = *reinterpret_cast<const i32x4 *>(p + d);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        mx = max(mx, max((uint32_t)v[cs][e] << 16 & 0x7fffffffu, (uint32_t)v[cs][e] & 0x7fff0000u));
-    }
-    float inv;
-    qs[nb] = a.sm * row_exponent(across(__uint_as_float(mx), [](float x, float y) {
-      return __uint_as_float(max(__float_as_uint(x), __float_as_uint(y)));
-    }), inv);
-#pragma unroll
-    for (int cs = 0; cs < 2 * C; ++cs)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        qf[nb][cs][2 * e] = (_Float16)(__uint_as_float((uint32_t)v[cs][e] << 16) * inv);
-        qf[nb][cs][2 * e + 1] = (_Float16)(__uint_as_float((uint32_t)v[cs][e] & 0xffff0000u) * inv);
-      }
+    load_query<C>(p, live, a.c.D, g, a.sm, qf[nb], qs[nb]);
   }
   const int pmin = u.pos + min(w0, total - 1) / a.G, pmax = u.pos + (min(w0 + 16 * NB, total) - 1) / a.G;
   const uint32_t oldest = a.window > 0 ? (uint32_t)a.window - 1 : 0x7fffffffu;
