@@ -64,6 +64,10 @@ struct KvSizes {
 
 // Rows of a unit, by the most that any sequence can have.
 constexpr int kKvTileRows = 128;
+// Units of at most so many rows stream also in a step of tiles; there a block of theirs
+// costs about a quarter of a tile's.
+constexpr int kKvFewRows = 16;
+constexpr int kKvTileCost = 4;
 constexpr int kv_tile_rows(const KvSizes &z) {
   const int64_t rows = z.most * (z.Hq / z.Hkv);
   return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kKvTileRows;
@@ -71,7 +75,7 @@ constexpr int kv_tile_rows(const KvSizes &z) {
 // Units that a step is divided into where there is enough to divide (over all kv heads),
 // and the fewest blocks of one.
 constexpr int64_t kv_target(const KvSizes &z) {
-  const int64_t t = (kv_tile_rows(z) == kKvTileRows ? 512 : 768) / z.Hkv;
+  const int64_t t = (kv_tile_rows(z) == kKvTileRows ? 384 : 768) / z.Hkv;
   return t > 1 ? t : 1;
 }
 constexpr int64_t kKvMinBlocks = 4;

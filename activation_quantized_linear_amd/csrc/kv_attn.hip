@@ -102,7 +102,7 @@ struct AttnArgs {
   int64_t W;
   const int32_t *plan;
   int64_t at_units, at_joins, window;
-  int G, Hq;
+  int G, Hq, tile;  // tile: rows of a partial result
   uint16_t *y;
   float *lse;
   float *pm, *po;  // partial results: (M, denominator) and sums of each part, head and row
@@ -131,29 +131,36 @@ __device__ __forceinline__ void store_lse(const AttnArgs &a, int tok, int h, int
 // maximum and sums of its own, and join in LDS at the end. The next block's K is in
 // flight from when the present one is used up, V from the same moment one block earlier.
 template <int NB, int C>
-__global__ __launch_bounds__(256) void k_kv_attn_stream(AttnArgs a) {
-  constexpr int DP = 64 * C, ND = DP / 16, HD = C > 2 ? 128 : DP;  // HD: dims joined at a time
-  __shared__ __attribute__((aligned(16))) float ob[4][16][HD + 4];
-  __shared__ float om[4][16 * NB], ol[4][16 * NB];
-  const int i = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
-  if (i >= a.plan[kKvUnits]) return;
-  const KvUnit u = reinterpret_cast<const KvUnit *>(a.plan + a.at_units)[i];
+struct StreamLds {
+  static constexpr int DIMS = C > 2 ? 128 : 64 * C;  // joined at a time
+  float o[4][16][DIMS + 4];
+  float m[4][16 * NB], l[4][16 * NB];
+};
+
+// Rows row0 .. row0 + 16 NB - 1 of u's sequence.
+template <int NB, int C>
+__device__ __forceinline__ void stream_rows(const AttnArgs &a, const KvUnit &u, int h, int row0,
+                                            StreamLds<NB, C> &lds) {
+  constexpr int DP = 64 * C, ND = DP / 16, HD = StreamLds<NB, C>::DIMS;
+  auto &ob = lds.o;
+  auto &om = lds.m;
+  auto &ol = lds.l;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int rows = min(16 * NB, u.len * a.G - u.row0);  // of the unit
+  const int rows = min(16 * NB, u.len * a.G - row0);
 
   f16x8 qf[NB][2 * C];
   int qpos[NB];
   float qs[NB];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    const int row = u.row0 + 16 * nb + r;
+    const int row = row0 + 16 * nb + r;
     const bool live = 16 * nb + r < rows;
-    qpos[nb] = u.pos + (live ? row / a.G : u.row0 / a.G);
+    qpos[nb] = u.pos + (live ? row : row0) / a.G;
     const uint16_t *p = a.q + (int64_t)(u.tok + row / a.G) * a.qrow + (h * a.G + row % a.G) * a.c.D;
     load_query<C>(p, live, a.c.D, g, a.sm, qf[nb], qs[nb]);
   }
-  const int pmin = u.pos + u.row0 / a.G, pmax = u.pos + (u.row0 + rows - 1) / a.G;
+  const int pmin = u.pos + row0 / a.G, pmax = u.pos + (row0 + rows - 1) / a.G;
   const uint32_t oldest = a.window > 0 ? (uint32_t)a.window - 1 : 0x7fffffffu;
 
   f32x4 acc[NB][ND];
@@ -303,10 +310,10 @@ __global__ __launch_bounds__(256) void k_kv_attn_stream(AttnArgs a) {
         const float o2 = t2 == -__builtin_inff() ? 0.0f : t2;
 #pragma unroll
         for (int w = 0; w < 4; ++w) L = fmaf(ol[w][lrow], exp2_hw(om[w][lrow] - o2), L);
-        const int64_t at = ((int64_t)u.part * a.c.Hkv + h) * (16 * NB) + lrow;
+        const int64_t at = ((int64_t)u.part * a.c.Hkv + h) * a.tile + row0 - row0 + lrow;
         if (half == 0 && oc == 0) {
           if (u.part < 0) {
-            store_lse(a, u.tok, h, u.row0 + lrow, t2, L);
+            store_lse(a, u.tok, h, row0 + lrow, t2, L);
           } else {
             a.pm[2 * at] = t2;
             a.pm[2 * at + 1] = L;
@@ -319,13 +326,23 @@ __global__ __launch_bounds__(256) void k_kv_attn_stream(AttnArgs a) {
           f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int w = 0; w < 4; ++w) o += *reinterpret_cast<const f32x4 *>(&ob[w][orow][d]);
-          if (u.part < 0) store_out(a, u.tok, h, u.row0 + lrow, half + d, L == 0.0f ? f32x4{0.f, 0.f, 0.f, 0.f} : o * (1.0f / L));
+          if (u.part < 0) store_out(a, u.tok, h, row0 + lrow, half + d, L == 0.0f ? f32x4{0.f, 0.f, 0.f, 0.f} : o * (1.0f / L));
           else *reinterpret_cast<f32x4 *>(a.po + at * DP + half + d) = o;
         }
       }
       __syncthreads();
     }
   }
+}
+
+template <int NB, int C>
+__global__ __launch_bounds__(256) void k_kv_attn_stream(AttnArgs a) {
+  __shared__ __attribute__((aligned(16))) StreamLds<NB, C> lds;
+  const int i = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
+  if (i >= a.plan[kKvUnits]) return;
+  const KvUnit u = reinterpret_cast<const KvUnit *>(a.plan + a.at_units)[i];
+  const int row0 = u.row0 + (int)blockIdx.y * (16 * NB);
+  if (row0 < u.len * a.G) stream_rows<NB, C>(a, u, h, row0, lds);
 }
 
 // LDS writes done and every wave here; loads from memory stay in flight.
@@ -346,19 +363,13 @@ struct TileLds {
 };
 
 template <int NB, int C>
-__global__ __launch_bounds__(256, 2) void k_kv_attn_tile(AttnArgs a) {
+__device__ __forceinline__ void tile_rows(const AttnArgs &a, const KvUnit &u, int h, char *smem) {
   constexpr int DP = 64 * C, ND = DP / 16, HALF = TileLds<C>::HALF;
-  extern __shared__ __attribute__((aligned(16))) char smem[];
-  const int i = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
-  if (i >= a.plan[kKvUnits]) return;
-  const KvUnit u = reinterpret_cast<const KvUnit *>(a.plan + a.at_units)[i];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int total = u.len * a.G;                             // rows of the sequence
-  const int wg0 = u.row0 + (int)blockIdx.y * (64 * NB);     // the workgroup's first
-  if (wg0 >= total) return;
-  const int w0 = wg0 + wave * (16 * NB);                     // the wave's first
-  const int rows = min(16 * NB, total - w0);                 // (none: the wave only loads)
+  const int total = u.len * a.G;                  // rows of the sequence
+  const int w0 = u.row0 + wave * (16 * NB);       // the wave's first
+  const int rows = min(16 * NB, total - w0);      // (none: the wave only loads)
 
   f16x8 qf[NB][2 * C];
   int qpos[NB];
@@ -645,12 +656,29 @@ __global__ __launch_bounds__(256, 2) void k_kv_attn_tile(AttnArgs a) {
   }
 }
 
+// Units of few rows among them (decoding sequences in a step with a prefill, a
+// sequence's last rows) stream instead: a block that 128 rows meet in 2.2 us is read by one of
+// their 4 waves in little more than 1.
+template <int C>
+__global__ __launch_bounds__(256, C > 2 ? 1 : 2) void k_kv_attn_tile(AttnArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  static_assert(sizeof(StreamLds<1, C>) <= TileLds<C>::BYTES, "either's LDS");
+  const int i = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
+  if (i >= a.plan[kKvUnits]) return;
+  const KvUnit u = reinterpret_cast<const KvUnit *>(a.plan + a.at_units)[i];
+  if (u.len * a.G - u.row0 <= kKvFewRows)
+    stream_rows<1, C>(a, u, h, u.row0, *reinterpret_cast<StreamLds<1, C> *>(smem));
+  else
+    tile_rows<kKvTileRows / 64, C>(a, u, h, smem);
+}
+
 // The partial results of rows whose blocks were spread over several units. 16 C threads
 // take a row's dims; with SPREAD (few rows, up to hundreds of parts) the workgroup's groups of
 // threads share a row's parts and add up in LDS, else (many rows, few parts) each takes a
 // row. Sums are in one order for a given number of parts.
 template <int C, bool SPREAD>
-__global__ __launch_bounds__(256) void k_kv_attn_join(AttnArgs a, int tile) {
+__global__ __launch_bounds__(256) void k_kv_attn_join(AttnArgs a) {
+  const int tile = a.tile;
   constexpr int TPR = 16 * C, GROUPS = 256 / TPR, U = 4;  // U: parts in flight
   __shared__ float red[2][GROUPS];
   __shared__ f32x4 sums[SPREAD ? GROUPS : 1][TPR];
@@ -721,10 +749,10 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(AttnArgs a, int tile) {
 }
 
 template <bool SPREAD>
-hipError_t launch_join(const AttnArgs &a, int64_t joins, int tile, hipStream_t st) {
+hipError_t launch_join(const AttnArgs &a, int64_t joins, hipStream_t st) {
   const auto go = [&](auto kern, int groups) {
-    hipLaunchKernelGGL(kern, dim3((unsigned)(joins * a.c.Hkv), SPREAD ? tile : (tile + groups - 1) / groups),
-                       dim3(256), 0, st, a, tile);
+    hipLaunchKernelGGL(kern, dim3((unsigned)(joins * a.c.Hkv), SPREAD ? a.tile : (a.tile + groups - 1) / groups),
+                       dim3(256), 0, st, a);
   };
   switch (a.c.DP / 64) {
     case 1: go(k_kv_attn_join<1, SPREAD>, 16); break;
@@ -735,19 +763,21 @@ hipError_t launch_join(const AttnArgs &a, int64_t joins, int tile, hipStream_t s
   return hipGetLastError();
 }
 
+// (a unit of 64 rows with a head past 128 in two workgroups of 32: its sums need the registers)
 template <int NB>
 void launch_stream(const AttnArgs &a, unsigned grid, hipStream_t st) {
+  constexpr int WIDE = NB > 2 ? 2 : NB;
   switch (a.c.DP / 64) {
     case 1: hipLaunchKernelGGL((k_kv_attn_stream<NB, 1>), dim3(grid), dim3(256), 0, st, a); break;
     case 2: hipLaunchKernelGGL((k_kv_attn_stream<NB, 2>), dim3(grid), dim3(256), 0, st, a); break;
-    case 3: hipLaunchKernelGGL((k_kv_attn_stream<NB, 3>), dim3(grid), dim3(256), 0, st, a); break;
-    default: hipLaunchKernelGGL((k_kv_attn_stream<NB, 4>), dim3(grid), dim3(256), 0, st, a); break;
+    case 3: hipLaunchKernelGGL((k_kv_attn_stream<WIDE, 3>), dim3(grid, NB / WIDE), dim3(256), 0, st, a); break;
+    default: hipLaunchKernelGGL((k_kv_attn_stream<WIDE, 4>), dim3(grid, NB / WIDE), dim3(256), 0, st, a); break;
   }
 }
 
-template <int NB, int C>
+template <int C>
 hipError_t launch_tile(const AttnArgs &a, unsigned grid, hipStream_t st) {
-  const auto kern = k_kv_attn_tile<NB, C>;
+  const auto kern = k_kv_attn_tile<C>;
   constexpr int bytes = TileLds<C>::BYTES;
   if constexpr (bytes > 65536) {  // once a device; a launch that the limit refuses reports itself
     static std::atomic<uint64_t> set{0};
@@ -759,7 +789,7 @@ hipError_t launch_tile(const AttnArgs &a, unsigned grid, hipStream_t st) {
       set.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
     }
   }
-  hipLaunchKernelGGL(kern, dim3(grid, kKvTileRows / (64 * NB)), dim3(256), bytes, st, a);
+  hipLaunchKernelGGL(kern, dim3(grid), dim3(256), bytes, st, a);
   return hipGetLastError();
 }
 
@@ -787,6 +817,7 @@ hipError_t launch_kv_attention(const uint16_t *q, int64_t qrow, float sm_scale, 
   a.at_joins = lay.at_joins;
   a.window = z.window;
   a.G = z.Hq / z.Hkv;
+  a.tile = tile;
   a.Hq = z.Hq;
   a.y = y;
   a.lse = lse;
@@ -798,10 +829,10 @@ hipError_t launch_kv_attention(const uint16_t *q, int64_t qrow, float sm_scale, 
   hipError_t e = hipSuccess;
   if (tile == kKvTileRows) {
     switch (c.DP / 64) {
-      case 1: e = launch_tile<2, 1>(a, grid, st); break;
-      case 2: e = launch_tile<2, 2>(a, grid, st); break;
-      case 3: e = launch_tile<1, 3>(a, grid, st); break;
-      default: e = launch_tile<1, 4>(a, grid, st); break;
+      case 1: e = launch_tile<1>(a, grid, st); break;
+      case 2: e = launch_tile<2>(a, grid, st); break;
+      case 3: e = launch_tile<3>(a, grid, st); break;
+      default: e = launch_tile<4>(a, grid, st); break;
     }
   } else {
     if (tile == 16) launch_stream<1>(a, grid, st);
@@ -810,8 +841,8 @@ hipError_t launch_kv_attention(const uint16_t *q, int64_t qrow, float sm_scale, 
     e = hipGetLastError();
   }
   if (e != hipSuccess || lay.joins == 0) return e;
-  return tile == kKvTileRows ? launch_join<false>(a, lay.joins, tile, st)
-                             : launch_join<true>(a, lay.joins, tile, st);
+  return tile == kKvTileRows ? launch_join<false>(a, lay.joins, st)
+                             : launch_join<true>(a, lay.joins, st);
 }
 
 }  // namespace aql

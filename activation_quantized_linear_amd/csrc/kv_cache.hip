@@ -37,6 +37,11 @@ __device__ __forceinline__ void tile_blocks(const Seq &q, int G, int64_t window,
   b1 = (q.pos + last / G) / kKvBlock + 1;
 }
 
+// What one block of these rows costs, in blocks of few rows.
+__device__ __forceinline__ int block_cost(const Seq &q, int G, int tile, int row0) {
+  return tile < kKvTileRows || q.len * G - row0 <= kKvFewRows ? 1 : kKvTileCost;
+}
+
 // Exclusive sum over the workgroup's threads; total to all.
 __device__ __forceinline__ int64_t scan(int64_t v, int64_t *lds, int64_t &total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -72,7 +77,7 @@ __device__ __forceinline__ int owner(const int *first, int S, int i) {
 // One workgroup. Sequences' pieces and tiles are counted and summed up; every piece and
 // tile then finds its sequence by bisection, three times over the tiles: their blocks,
 // their units' lengths, the units. A tile's blocks are divided into units of about
-// `chunk` = total / target blocks, at most a quarter more, and units are laid out longest
+// `chunk` = total / target blocks' cost, at most a quarter more, and units are laid out longest
 // first (by classes of length: atomics in LDS give the places inside a class, which no
 // result depends on), so that the last ones to start are short.
 __global__ __launch_bounds__(kPlanThreads) void k_kv_plan(const int32_t *__restrict__ cu,
@@ -131,17 +136,21 @@ __global__ __launch_bounds__(kPlanThreads) void k_kv_plan(const int32_t *__restr
     bool bad;
     const Seq q = sequence(cu, pos, z, s, bad);
     int b0, b1;
-    tile_blocks(q, G, z.window, (i - first_tile[s]) * tile, tile, b0, b1);
-    mine += b1 - b0;
-    most = max(most, b1 - b0);
+    const int row0 = (i - first_tile[s]) * tile;
+    tile_blocks(q, G, z.window, row0, tile, b0, b1);
+    const int cost = (b1 - b0) * block_cost(q, G, tile, row0);
+    mine += cost;
+    most = max(most, cost);
   }
   atomicMax(&s_longest, most);
   scan(mine, tmp, blocks);
   int64_t chunk = (blocks + target - 1) / target;
-  chunk = chunk < kKvMinBlocks ? kKvMinBlocks : chunk;
-  if (lay.parts == 0) chunk = z.W;
+  const int64_t least = kKvMinBlocks * (tile < kKvTileRows ? 1 : kKvTileCost);
+  chunk = chunk < least ? least : chunk;
+  if (lay.parts == 0) chunk = kKvTileCost * z.W;
   const int longest = (int)min(chunk + chunk / 4, (int64_t)s_longest);
-  auto bin_of = [&](int len) {  // long units first
+  auto bin_of = [&](int len) {  // long units first (a part that may not be smaller is the longest)
+    len = min(len, longest);
     return kBins - 1 - (int)((int64_t)len * (kBins - 1) / (longest > 0 ? longest : 1));
   };
 
@@ -167,8 +176,12 @@ __global__ __launch_bounds__(kPlanThreads) void k_kv_plan(const int32_t *__restr
       const int row0 = (i - first_tile[s]) * tile;
       int b0, b1;
       tile_blocks(q, G, z.window, row0, tile, b0, b1);
-      const int n = b1 - b0, parts = max(1, (int)((n + chunk - 1 - chunk / 4) / chunk));
-      const int each = (n + parts - 1) / parts, bin = bin_of(each);
+      const int n = b1 - b0;
+      const int64_t cost = (int64_t)n * block_cost(q, G, tile, row0);
+      // (no more parts than the plan has room for: at least kKvMinBlocks blocks each)
+      const int parts = (int)max((int64_t)1, min((cost + chunk - 1 - chunk / 4) / chunk,
+                                                 (int64_t)(n + kKvMinBlocks - 1) / kKvMinBlocks));
+      const int bin = bin_of((int)((cost + parts - 1) / parts));
       if (pass == 0) {
         atomicAdd(&count[bin], parts);
         continue;
