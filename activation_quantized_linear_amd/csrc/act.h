@@ -28,12 +28,37 @@ __device__ __forceinline__ float gelu_tanh_arg(float z) {
   return 1.59576912f * c * fmaf(0.044715f * c, c, 1.0f);
 }
 
+// Phi(z) of the normal distribution, and e^(-z^2 / 2). Phi(-|z|) = P(t) e^(-z^2 / 2) with
+// t = 1 / (1 + 0.3182 |z|), P fitted for this file: a weighted least-squares fit of degree 8 to
+// erfcx(x) / 2, x = |z| / sqrt 2 in [0, 20], its relative error held below 4e-7 over
+// the whole tail (the exponent's own rounding adds up to 8e-6 at |z| = 13). A third of
+// erfcf's instructions: the linear of M = 2048, N = 14336, K = 4096 with gelu took 256 us with that,
+// 224 without an activation.
+__device__ __forceinline__ float normal_cdf(float z, float &e) {
+  const float a = fabsf(z);
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.318198055f, a, 1.0f));
+  float p = 0.0347404033f;
+  p = fmaf(p, t, -0.125645936f);
+  p = fmaf(p, t, 0.114017196f);
+  p = fmaf(p, t, 0.0112389755f);
+  p = fmaf(p, t, 0.0990576223f);
+  p = fmaf(p, t, 0.112606712f);
+  p = fmaf(p, t, 0.127045199f);
+  p = fmaf(p, t, 0.126940012f);
+  e = __builtin_amdgcn_exp2f(-0.72134752f * z * z);
+  const float left = p * t * e;
+  return z < 0.0f ? left : 1.0f - left;
+}
+
 // act(z). The tanh form is z times a sigmoid, 0.5 (1 + tanh u) = 1 / (1 + e^-2u), and the
-// erf form takes erfc: neither loses its left tail in a difference from 1.
+// erf form computes its left tail as such: neither loses it in a difference from 1.
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == kActRelu) return z < 0.0f ? 0.0f : z;  // (NaN stays NaN)
-  if constexpr (ACT == kActGelu) return 0.5f * z * erfcf(-0.707106781f * z);
+  if constexpr (ACT == kActGelu) {
+    float e;
+    return z * normal_cdf(z, e);
+  }
   if constexpr (ACT == kActGeluTanh) return z * sigmoid(gelu_tanh_arg(z));
   if constexpr (ACT == kActSilu) return z * sigmoid(z);
   return z;
@@ -46,9 +71,10 @@ __device__ __forceinline__ void act_value_grad(float z, float &a, float &d) {
     a = act_value<ACT>(z);
     d = z > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == kActGelu) {
-    const float c = 0.5f * erfcf(-0.707106781f * z);
+    float e;
+    const float c = normal_cdf(z, e);
     a = z * c;
-    d = fmaf(z * 0.398942280f, __builtin_amdgcn_exp2f(-0.72134752f * z * z), c);
+    d = fmaf(z * 0.398942280f, e, c);
   } else if constexpr (ACT == kActGeluTanh) {
     const float g = sigmoid(gelu_tanh_arg(z)), c = fminf(fmaxf(z, -64.0f), 64.0f);
     a = z * g;

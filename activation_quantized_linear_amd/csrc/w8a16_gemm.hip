@@ -161,6 +161,9 @@ __device__ __forceinline__ void load_tile(uint16_t *tl, const uint16_t *src, int
 // col0 + 16 j). mul and residual come through the LDS tile as whole rows, and a lane
 // reads from it just the places that it writes, so the last of them turns into y in
 // place. Everything stays float32 until y is rounded. tl: nothing uses it on entry.
+// Bound by the tiles' rows through memory once the products are done: mul or residual
+// cost 5 us at M = 500, N = 11007 (11 MB, one round of tiles: 57 -> 62), 14 at M = 2048, N =
+// 14336 (59 MB: 224 -> 238); with the tile's loads out in fours 64 and 252 (registers).
 template <int BM, int BN_, int NT, int TLD, int TI, int TJ>
 __device__ __forceinline__ void act_tile(uint16_t *tl, f32x4 (&acc)[TI][TJ], const ActTerm &at,
                                          bool mine, int64_t m0, int64_t M, int64_t n0, int row0,
