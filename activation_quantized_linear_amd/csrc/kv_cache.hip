@@ -6,6 +6,8 @@
 // its scale from the new tokens; behind live tokens the scale only grows, and where
 // it does their codes become clamp(rint((code s) / s')), each product and quotient
 // rounded once to binary32.
+#include <type_traits>
+
 #include "kv.h"
 
 namespace aql {
@@ -248,18 +250,49 @@ __device__ __forceinline__ void load8(const void *x, int64_t i, float (&v)[8]) {
   }
 }
 
-// A thread's share of a page and head: tokens 4 jq .. 4 jq + 3, dims 8 c .. 8 c + 7.
-// Codes lie as one dword (4 tokens) for each dim of V, 8 bytes (dims) for each token of K.
+// A thread's share of a page and head: tokens 4 jq .. 4 jq + 3, dims 8 c .. 8 c + 7. Consecutive
+// lanes take consecutive dims, so that rows of K and V pass as whole runs (with
+// consecutive tokens, 64 bytes of 16 rows a wave, writing and reading 8881 tokens of 8 heads of 128
+// back took 32.6 us, 28.5 with runs). Codes: 8 bytes of each token of K; V's page is transposed, its tokens
+// contiguous, so its codes change sides in LDS and pass in 16-byte pieces.
+template <int C>
 struct Share {
+  static constexpr int NC = 8 * C, THREADS = 16 * NC;
+  static constexpr int ROW = 17;  // dwords of a dim's 64 codes in LDS
   int jq, c;
-  __device__ Share() : jq(threadIdx.x & 15), c(threadIdx.x >> 4) {}
-  __device__ int64_t k(int t) const { return (c >> 3) * 4096 + (4 * jq + t) * 64 + (c & 7) * 8; }
-  __device__ int64_t v(int e) const { return (8 * c + e) * 64 + 4 * jq; }
+  __device__ Share() : jq(threadIdx.x / NC), c(threadIdx.x % NC) {}
+  __device__ int k(int t) const { return (c >> 3) * 4096 + (4 * jq + t) * 64 + (c & 7) * 8; }
+  __device__ int lds(int e) const { return (8 * c + e) * ROW + jq; }
 };
 
-// code[t] = the 8 codes of token t, one a byte of the two dwords, from either layout.
-__device__ __forceinline__ void load_codes(const int8_t *p, bool isv, const Share &sh,
-                                           uint32_t (&code)[4][2]) {
+// w[e] = the codes of dim e, one token a byte, of code[t] = those of token t, one dim a byte.
+__device__ __forceinline__ void transpose(const uint32_t (&code)[4][2], uint32_t (&w)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    w[e] = 0;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) w[e] |= (code[t][e >> 2] >> (8 * (e & 3)) & 255u) << (8 * t);
+  }
+}
+__device__ __forceinline__ void transpose(const uint32_t (&w)[8], uint32_t (&code)[4][2]) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      code[t][h] = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) code[t][h] |= (w[4 * h + e] >> (8 * t) & 255u) << (8 * e);
+    }
+}
+
+__device__ __forceinline__ int code_at(const uint32_t (&code)[2], int e) {
+  return (int)(int8_t)(code[e >> 2] >> (8 * (e & 3)));
+}
+
+// Codes of a page and head as they lie, code[t] those of token 4 jq + t.
+template <int C>
+__device__ __forceinline__ void load_codes(const int8_t *p, bool isv, const Share<C> &sh,
+                                           uint32_t *lds, uint32_t (&code)[4][2]) {
   if (!isv) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -269,47 +302,44 @@ __device__ __forceinline__ void load_codes(const int8_t *p, bool isv, const Shar
     }
     return;
   }
-  uint32_t d[8];
+  i32x4 d[2];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) d[e] = *reinterpret_cast<const uint32_t *>(p + sh.v(e));
+  for (int i = 0; i < 2; ++i)
+    d[i] = *reinterpret_cast<const i32x4 *>(p + 16 * (threadIdx.x + Share<C>::THREADS * i));
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
+  for (int i = 0; i < 2; ++i) {
+    const int piece = threadIdx.x + Share<C>::THREADS * i;
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      uint32_t r = 0;
+    for (int e = 0; e < 4; ++e)
+      lds[(piece >> 2) * Share<C>::ROW + 4 * (piece & 3) + e] = (uint32_t)d[i][e];
+  }
+  __syncthreads();
+  uint32_t w[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) r |= ((d[4 * w + e] >> (8 * t)) & 255u) << (8 * e);
-      code[t][w] = r;
-    }
+  for (int e = 0; e < 8; ++e) w[e] = lds[sh.lds(e)];
+  transpose(w, code);
 }
 
-__device__ __forceinline__ int code_at(const uint32_t (&code)[2], int e) {
-  return (int)(int8_t)(code[e >> 2] >> (8 * (e & 3)));
-}
-
-// One workgroup of 2 DP threads a piece, kv head and array (blockIdx.y: K, V). The
-// page is read only where codes have to be rounded anew, or to complete V's dwords.
-// Bound by memory for whole pages (3 bytes a value), by its chain of loads (the piece, the
-// page's number, its scale) for single tokens.
-template <bool BF16>
-__global__ __launch_bounds__(512) void k_kv_write(const void *__restrict__ k, int64_t krow,
-                                                  const void *__restrict__ v, int64_t vrow,
-                                                  KvCache c, const int32_t *__restrict__ table,
-                                                  int64_t W, const int32_t *__restrict__ plan,
-                                                  int64_t at_pieces) {
+// One workgroup a piece, kv head and array (blockIdx.y: K, V). The page is read only where
+// codes have to be rounded anew, or to complete V's 16-byte pieces. Bound by memory for
+// whole pages (3 bytes a value), by its chain of loads (the piece, the page's number, its
+// scale) for single tokens.
+template <bool BF16, int C>
+__global__ __launch_bounds__(Share<C>::THREADS) void k_kv_write(
+    const void *__restrict__ k, int64_t krow, const void *__restrict__ v, int64_t vrow, KvCache c,
+    const int32_t *__restrict__ table, int64_t W, const int32_t *__restrict__ plan,
+    int64_t at_pieces) {
+  __shared__ uint32_t lds[64 * C * Share<C>::ROW];
+  __shared__ uint32_t part[8];
   const int i = blockIdx.x / c.Hkv, h = blockIdx.x % c.Hkv;
   if (i >= plan[kKvPieces]) return;
   const KvPiece u = reinterpret_cast<const KvPiece *>(plan + at_pieces)[i];
   const int64_t page = table[u.seq * W + u.blk];
-  if (page < 0 || page >= c.pages) return;
   const bool isv = blockIdx.y == 1;
   const void *x = isv ? v : k;
   const int64_t row = isv ? vrow : krow;
-  float *scale = (isv ? c.vs : c.ks) + page * c.Hkv + h;
-  int8_t *codes = (isv ? c.vq : c.kq) + (page * c.Hkv + h) * (kKvBlock * (int64_t)c.DP);
-  const Share sh;
+  const Share<C> sh;
   const int end = u.off + u.n;
-  const float old = u.off > 0 ? *scale : 0.0f;
 
   float f[4][8];
   uint32_t mx = 0;
@@ -319,20 +349,24 @@ __global__ __launch_bounds__(512) void k_kv_write(const void *__restrict__ k, in
     const int j = 4 * sh.jq + t;
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[t][e] = 0.0f;
-    if (dims && j >= u.off && j < end) {
+    if (dims && j >= u.off && j < end)
       load8<BF16>(x, (u.tok + j - u.off) * row + (int64_t)h * c.D + 8 * sh.c, f[t]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) mx = umax(mx, __float_as_uint(f[t][e]) & 0x7fffffffu);
-    }
   }
+  if (page < 0 || page >= c.pages) return;  // (the tokens' loads are on their way meanwhile)
+  float *scale = (isv ? c.vs : c.ks) + page * c.Hkv + h;
+  int8_t *codes = (isv ? c.vq : c.kq) + (page * c.Hkv + h) * (kKvBlock * 64 * C);
+  const float old = u.off > 0 ? *scale : 0.0f;
   // the largest magnitude: bits order like magnitudes, a NaN above an infinity, so a page that
   // is given either gets a scale that is no number and restores none
-  __shared__ uint32_t part[8];
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mx = umax(mx, __float_as_uint(f[t][e]) & 0x7fffffffu);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) mx = umax(mx, (uint32_t)__shfl_xor((int)mx, o));
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = mx;
   __syncthreads();
-  for (int w = 0; w < (int)blockDim.x >> 6; ++w) mx = umax(mx, part[w]);
+  for (int w = 0; w < Share<C>::THREADS / 64; ++w) mx = umax(mx, part[w]);
   const uint32_t top = umax(__float_as_uint(__uint_as_float(mx) / 127.0f),
                             __float_as_uint(kKvMinScale));
   const float s = __uint_as_float(umax(__float_as_uint(old), top));
@@ -340,51 +374,65 @@ __global__ __launch_bounds__(512) void k_kv_write(const void *__restrict__ k, in
   if (threadIdx.x == 0 && (u.off == 0 || anew)) *scale = s;
 
   const int from = anew ? 0 : u.off;  // tokens from .. end - 1 are written
-  if (4 * sh.jq + 3 < from || 4 * sh.jq >= end) return;
   uint32_t code[4][2] = {};
-  if (u.off > 0 && 4 * sh.jq < u.off && (anew || isv)) load_codes(codes, isv, sh, code);
-  const bool near = s <= 0x1p100f;  // scales up to 2^100 have a normal reciprocal
-  const float r = 1.0f / s;
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const int j = 4 * sh.jq + t;
-    if (j >= end) {
-      code[t][0] = code[t][1] = 0;
-      continue;
-    }
-    if (j < from) continue;
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x1 = j < u.off ? (float)code_at(code[t], e) * old : f[t][e];
-      w[e >> 2] |= ((uint32_t)(near ? code_of(x1, s, r) : code_far(x1, s)) & 255u) << (8 * (e & 3));
-    }
-    code[t][0] = w[0];
-    code[t][1] = w[1];
+  if (anew) {  // (uniform over the workgroup)
+    load_codes(codes, isv, sh, lds, code);
+    if (isv) __syncthreads();
   }
-  if (!isv) {
+  const auto codes_of = [&](auto &&one) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int j = 4 * sh.jq + t;
-      if (j >= from && j < end)
-        *reinterpret_cast<i32x2 *>(codes + sh.k(t)) = i32x2{(int)code[t][0], (int)code[t][1]};
+      uint32_t w[2] = {0, 0};
+      if (j >= from && j < end) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x1 = j < u.off ? (float)code_at(code[t], e) * old : f[t][e];
+          w[e >> 2] |= ((uint32_t)one(x1) & 255u) << (8 * (e & 3));
+        }
+        if (!isv) *reinterpret_cast<i32x2 *>(codes + sh.k(t)) = i32x2{(int)w[0], (int)w[1]};
+      }
+      code[t][0] = w[0];
+      code[t][1] = w[1];
     }
-    return;
+  };
+  if (s <= 0x1p100f) {  // scales up to 2^100 have a normal reciprocal
+    const float r = 1.0f / s;
+    codes_of([&](float x1) { return code_of(x1, s, r); });
+  } else {
+    codes_of([&](float x1) { return code_far(x1, s); });
   }
+  if (!isv) return;
+  uint32_t w[8];
+  transpose(code, w);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    uint32_t d = 0;
+  for (int e = 0; e < 8; ++e) lds[sh.lds(e)] = w[e];
+  __syncthreads();
 #pragma unroll
-    for (int t = 0; t < 4; ++t) d |= ((uint32_t)code_at(code[t], e) & 255u) << (8 * t);
-    *reinterpret_cast<uint32_t *>(codes + sh.v(e)) = d;
+  for (int q = 0; q < 2; ++q) {  // 16 tokens of a dim; those before `from` stay
+    const int piece = threadIdx.x + Share<C>::THREADS * q, t0 = 16 * (piece & 3);
+    if (t0 + 16 <= from || t0 >= end) continue;
+    i32x4 d, *to = reinterpret_cast<i32x4 *>(codes + 16 * piece);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] = (int)lds[(piece >> 2) * Share<C>::ROW + (piece & 3) * 4 + e];
+    if (t0 < from) {
+      const i32x4 was = *to;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int keep = min(max(from - t0 - 4 * e, 0), 4);  // bytes
+        const uint32_t mask = keep == 4 ? 0xffffffffu : (1u << (8 * keep)) - 1u;
+        d[e] = (int)(((uint32_t)was[e] & mask) | ((uint32_t)d[e] & ~mask));
+      }
+    }
+    *to = d;
   }
 }
 
-template <bool BF16>
-__global__ __launch_bounds__(512) void k_kv_read(KvCache c, const int32_t *__restrict__ table,
-                                                 int64_t W, const int32_t *__restrict__ plan,
-                                                 int64_t at_pieces, void *__restrict__ k,
-                                                 void *__restrict__ v) {
+template <bool BF16, int C>
+__global__ __launch_bounds__(Share<C>::THREADS) void k_kv_read(
+    KvCache c, const int32_t *__restrict__ table, int64_t W, const int32_t *__restrict__ plan,
+    int64_t at_pieces, void *__restrict__ k, void *__restrict__ v) {
+  __shared__ uint32_t lds[64 * C * Share<C>::ROW];
   const int i = blockIdx.x / c.Hkv, h = blockIdx.x % c.Hkv;
   if (i >= plan[kKvPieces]) return;
   const KvPiece u = reinterpret_cast<const KvPiece *>(plan + at_pieces)[i];
@@ -392,16 +440,15 @@ __global__ __launch_bounds__(512) void k_kv_read(KvCache c, const int32_t *__res
   const bool live = page >= 0 && page < c.pages;
   const bool isv = blockIdx.y == 1;
   const int64_t at = live ? page * c.Hkv + h : 0;
-  const int8_t *codes = (isv ? c.vq : c.kq) + at * (kKvBlock * (int64_t)c.DP);
-  const Share sh;
+  const Share<C> sh;
   const int end = u.off + u.n;
-  if (8 * sh.c >= c.D || 4 * sh.jq + 3 < u.off || 4 * sh.jq >= end) return;
   uint32_t code[4][2] = {};
   float s = 0.0f;
-  if (live) {
+  if (live) {  // (uniform over the workgroup)
     s = (isv ? c.vs : c.ks)[at];
-    load_codes(codes, isv, sh, code);
+    load_codes((isv ? c.vq : c.kq) + at * (kKvBlock * 64 * C), isv, sh, lds, code);
   }
+  if (8 * sh.c >= c.D) return;
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     const int j = 4 * sh.jq + t;
@@ -425,6 +472,35 @@ __global__ __launch_bounds__(512) void k_kv_read(KvCache c, const int32_t *__res
   }
 }
 
+template <bool BF16, int C>
+void launch_write(unsigned grid, hipStream_t st, const void *k, int64_t krow, const void *v,
+                  int64_t vrow, const KvCache &c, const int32_t *table, int64_t W,
+                  const int32_t *plan, int64_t at) {
+  hipLaunchKernelGGL((k_kv_write<BF16, C>), dim3(grid, 2), dim3(Share<C>::THREADS), 0, st, k, krow,
+                     v, vrow, c, table, W, plan, at);
+}
+template <bool BF16, int C>
+void launch_read(unsigned grid, hipStream_t st, const KvCache &c, const int32_t *table, int64_t W,
+                 const int32_t *plan, int64_t at, void *k, void *v) {
+  hipLaunchKernelGGL((k_kv_read<BF16, C>), dim3(grid, 2), dim3(Share<C>::THREADS), 0, st, c, table,
+                     W, plan, at, k, v);
+}
+
+// f(bool constant, int constant) for the type and the head's slices of 64.
+template <class F>
+void dispatch(bool bf16, int slices, F &&f) {
+  const auto by_type = [&](auto c) {
+    if (bf16) f(std::true_type{}, c);
+    else f(std::false_type{}, c);
+  };
+  switch (slices) {
+    case 1: by_type(std::integral_constant<int, 1>{}); break;
+    case 2: by_type(std::integral_constant<int, 2>{}); break;
+    case 3: by_type(std::integral_constant<int, 3>{}); break;
+    default: by_type(std::integral_constant<int, 4>{}); break;
+  }
+}
+
 }  // namespace
 
 hipError_t launch_kv_plan(const int32_t *cu, const int32_t *pos, const KvSizes &z, int32_t *plan,
@@ -439,9 +515,10 @@ hipError_t launch_kv_write(const void *k, int64_t krow, const void *v, int64_t v
                            const int32_t *plan, hipStream_t st) {
   const KvPlanLayout lay = kv_plan_layout(z);
   if (!grid_fits(lay.pieces * c.Hkv, 2 * c.DP)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(bf16 ? k_kv_write<true> : k_kv_write<false>,
-                     dim3((unsigned)(lay.pieces * c.Hkv), 2), dim3(2 * c.DP), 0, st, k, krow, v,
-                     vrow, c, table, z.W, plan, lay.at_pieces);
+  dispatch(bf16, c.DP / 64, [&](auto t, auto n) {
+    launch_write<decltype(t)::value, decltype(n)::value>((unsigned)(lay.pieces * c.Hkv), st, k, krow,
+                                                         v, vrow, c, table, z.W, plan, lay.at_pieces);
+  });
   return hipGetLastError();
 }
 
@@ -449,9 +526,10 @@ hipError_t launch_kv_read(const KvCache &c, const int32_t *table, const KvSizes 
                           const int32_t *plan, void *k, void *v, bool bf16, hipStream_t st) {
   const KvPlanLayout lay = kv_plan_layout(z);
   if (!grid_fits(lay.pieces * c.Hkv, 2 * c.DP)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(bf16 ? k_kv_read<true> : k_kv_read<false>,
-                     dim3((unsigned)(lay.pieces * c.Hkv), 2), dim3(2 * c.DP), 0, st, c, table, z.W,
-                     plan, lay.at_pieces, k, v);
+  dispatch(bf16, c.DP / 64, [&](auto t, auto n) {
+    launch_read<decltype(t)::value, decltype(n)::value>((unsigned)(lay.pieces * c.Hkv), st, c, table,
+                                                        z.W, plan, lay.at_pieces, k, v);
+  });
   return hipGetLastError();
 }
 
