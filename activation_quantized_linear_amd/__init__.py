@@ -848,13 +848,27 @@ def aql_act_mul_backward(dy, pre, act, mul=None, dv=None, dmul=None, need_dmul=T
 class KvCache:
     """A paged 8-bit KV cache: P pages of AQL_KV_BLOCK tokens for Hkv heads of D values
     (DP: D rounded up to a multiple of 64). Tensors: kq int8 [P, Hkv, DP/64, 64, 64], vq int8
-    [P, Hkv, DP, 64], ks and vs float32 [P, Hkv]; a value is code * scale."""
+    [P, Hkv, DP, 64], ks and vs float32 [P, Hkv]; a value is code * scale. They are checked here once
+    and stay the cache's own."""
 
-    __slots__ = ("P", "Hkv", "D", "kq", "vq", "ks", "vs")
+    __slots__ = ("_sizes", "_tensors", "_at", "_device")
 
     def __init__(self, P, Hkv, D, kq, vq, ks, vs):
-        self.P, self.Hkv, self.D = P, Hkv, D
-        self.kq, self.vq, self.ks, self.vs = kq, vq, ks, vs
+        di = _dev_index(kq, "kq", torch.int8, 5) if isinstance(kq, torch.Tensor) and kq.is_cuda else -1
+        DP = (D + 63) // 64 * 64
+        self._sizes, self._tensors, self._device = (P, Hkv, D), (kq, vq, ks, vs), di
+        self._at = None if di < 0 else (
+            _fit(kq, "kq", torch.int8, (P, Hkv, DP // 64, AQL_KV_BLOCK, 64), di),
+            _fit(vq, "vq", torch.int8, (P, Hkv, DP, AQL_KV_BLOCK), di),
+            _fit(ks, "ks", torch.float32, (P, Hkv), di), _fit(vs, "vs", torch.float32, (P, Hkv), di))
+
+    P = property(lambda self: self._sizes[0])
+    Hkv = property(lambda self: self._sizes[1])
+    D = property(lambda self: self._sizes[2])
+    kq = property(lambda self: self._tensors[0])
+    vq = property(lambda self: self._tensors[1])
+    ks = property(lambda self: self._tensors[2])
+    vs = property(lambda self: self._tensors[3])
 
 
 def aql_kv_cache(P, Hkv, D, device="cuda"):
@@ -877,15 +891,26 @@ class KvPlan:
     for and its device buffer; every layer of a step shares one. info: a device int32 [1], 0 or 1 +
     the first sequence that cannot be served (see aql.h)."""
 
-    __slots__ = ("T", "S", "Hq", "Hkv", "W", "most", "window", "buffer")
+    __slots__ = ("_sizes", "_buffer", "_at", "_device", "_scratch")
 
     def __init__(self, T, S, Hq, Hkv, W, most, window, buffer):
-        self.T, self.S, self.Hq, self.Hkv, self.W = T, S, Hq, Hkv, W
-        self.most, self.window, self.buffer = most, window, buffer
+        self._sizes, self._buffer = (T, S, Hq, Hkv, W, most, window), buffer
+        self._device = buffer.get_device()
+        self._at = buffer.data_ptr()
+        self._scratch = {}  # workspace bytes of an attention call by head size
+
+    T = property(lambda self: self._sizes[0])
+    S = property(lambda self: self._sizes[1])
+    Hq = property(lambda self: self._sizes[2])
+    Hkv = property(lambda self: self._sizes[3])
+    W = property(lambda self: self._sizes[4])
+    most = property(lambda self: self._sizes[5])
+    window = property(lambda self: self._sizes[6])
+    buffer = property(lambda self: self._buffer)
 
     @property
     def info(self):
-        return self.buffer[:4].view(torch.int32)
+        return self._buffer[:4].view(torch.int32)
 
 
 def aql_kv_plan_bytes(T, S, Hq, Hkv, W, most):
@@ -907,29 +932,25 @@ def aql_kv_plan(cu, pos, T, most, Hq, Hkv, W, window=0, plan=None):
         plan = KvPlan(*sizes, torch.empty(max(nbytes, 16), dtype=torch.uint8, device=pos.device))
     elif not isinstance(plan, KvPlan):
         raise TypeError("plan must be a KvPlan (aql_kv_plan)")
-    elif (plan.T, plan.S, plan.Hq, plan.Hkv, plan.W, plan.most, plan.window) != sizes:
-        raise ValueError("plan was made for other sizes")
-    buf = _fit(plan.buffer, "plan.buffer", torch.uint8, plan.buffer.shape, di)
-    _call("aql_kv_plan", _lib.aql_kv_plan, di, cp, pos.data_ptr(), *sizes, buf,
-          plan.buffer.numel())
+    elif plan._sizes != sizes or plan._device != di:
+        raise ValueError("plan was made for other sizes, or on another device")
+    _call("aql_kv_plan", _lib.aql_kv_plan, di, cp, pos.data_ptr(), *sizes, plan._at,
+          plan._buffer.numel())
     return plan
 
 
 def _kv_call(cache, table, plan, di):
-    """Addresses of a cache's tensors, of the page table and of the plan."""
+    """Addresses of a cache's tensors and of the page table, having seen that all belong together."""
     if not isinstance(cache, KvCache):
         raise TypeError("cache must be a KvCache (aql_kv_cache)")
     if not isinstance(plan, KvPlan):
         raise TypeError("plan must be a KvPlan (aql_kv_plan)")
-    P, Hkv, DP = cache.P, cache.Hkv, (cache.D + 63) // 64 * 64
-    if plan.Hkv != Hkv:
-        raise ValueError(f"plan is for Hkv={plan.Hkv}, the cache has {Hkv}")
-    return (_fit(cache.kq, "cache.kq", torch.int8, (P, Hkv, DP // 64, AQL_KV_BLOCK, 64), di),
-            _fit(cache.vq, "cache.vq", torch.int8, (P, Hkv, DP, AQL_KV_BLOCK), di),
-            _fit(cache.ks, "cache.ks", torch.float32, (P, Hkv), di),
-            _fit(cache.vs, "cache.vs", torch.float32, (P, Hkv), di),
-            _fit(table, "table", torch.int32, (plan.S, plan.W), di),
-            _fit(plan.buffer, "plan.buffer", torch.uint8, plan.buffer.shape, di))
+    _, S, _, Hkv, W, _, _ = plan._sizes
+    if Hkv != cache._sizes[1]:
+        raise ValueError(f"plan is for Hkv={Hkv}, the cache has {cache._sizes[1]}")
+    if cache._device != di or plan._device != di:
+        raise ValueError(f"cache and plan must be on cuda:{di}")
+    return cache._at, _fit(table, "table", torch.int32, (S, W), di)
 
 
 def _device_of(t, name):
@@ -965,12 +986,13 @@ def aql_kv_cache_write(k, v, cache, table, plan):
     each sequence's pages. Writes cache in place."""
     di = _device_of(k, "k")
     dt = _act_dtype(k.dtype, "k")
-    kq, vq, ks, vs, tp, pp = _kv_call(cache, table, plan, di)
-    shape = (plan.T, cache.Hkv, cache.D)
-    kp, krow = _kv_rows(k, "k", k.dtype, shape, di)
-    vp, vrow = _kv_rows(v, "v", k.dtype, shape, di)
-    _call("aql_kv_cache_write", _lib.aql_kv_cache_write, di, kp, krow, vp, vrow, dt, plan.T, plan.S,
-          plan.Hq, plan.Hkv, cache.D, tp, plan.W, plan.most, pp, kq, vq, ks, vs, cache.P)
+    at, tp = _kv_call(cache, table, plan, di)
+    T, S, Hq, Hkv, W, most, _ = plan._sizes
+    P, _, D = cache._sizes
+    kp, krow = _kv_rows(k, "k", k.dtype, (T, Hkv, D), di)
+    vp, vrow = _kv_rows(v, "v", k.dtype, (T, Hkv, D), di)
+    _call("aql_kv_cache_write", _lib.aql_kv_cache_write, di, kp, krow, vp, vrow, dt, T, S, Hq, Hkv,
+          D, tp, W, most, plan._at, *at, P)
 
 
 def aql_kv_cache_read(cache, table, plan, dtype=torch.bfloat16, k=None, v=None):
@@ -978,12 +1000,14 @@ def aql_kv_cache_read(cache, table, plan, dtype=torch.bfloat16, k=None, v=None):
     code * scale. Rows of no sequence are left as they are."""
     dt = _act_dtype(dtype, "dtype")
     di = _dev_index(table, "table", torch.int32, 2)
-    kq, vq, ks, vs, tp, pp = _kv_call(cache, table, plan, di)
-    shape = (plan.T, cache.Hkv, cache.D)
-    k = _new(k, "k", shape, dtype, table.device)
-    v = _new(v, "v", shape, dtype, table.device)
-    _call("aql_kv_cache_read", _lib.aql_kv_cache_read, di, kq, vq, ks, vs, cache.P, plan.T, plan.S,
-          plan.Hq, plan.Hkv, cache.D, tp, plan.W, plan.most, pp, k.data_ptr(), v.data_ptr(), dt)
+    at, tp = _kv_call(cache, table, plan, di)
+    T, S, Hq, Hkv, W, most, _ = plan._sizes
+    P, _, D = cache._sizes
+    dev = table.device
+    k = _new(k, "k", (T, Hkv, D), dtype, dev)
+    v = _new(v, "v", (T, Hkv, D), dtype, dev)
+    _call("aql_kv_cache_read", _lib.aql_kv_cache_read, di, *at, P, T, S, Hq, Hkv, D, tp, W, most,
+          plan._at, k.data_ptr(), v.data_ptr(), dt)
     return k, v
 
 
@@ -999,15 +1023,19 @@ def aql_attention_kv8(q, cache, table, plan, sm_scale=None, y=None, lse=None, wo
     left as they are. workspace: uint8 device tensor of aql_attention_kv8_bytes; allocated
     here when one is needed and none is given."""
     di = _device_of(q, "q")
-    kq, vq, ks, vs, tp, pp = _kv_call(cache, table, plan, di)
-    T, Hq, D = plan.T, plan.Hq, cache.D
-    qp, qrow = _kv_rows(q, "q", torch.bfloat16, (T, Hq, D), di)
+    at, tp = _kv_call(cache, table, plan, di)
+    T, S, Hq, Hkv, W, most, window = plan._sizes
+    P, _, D = cache._sizes
+    shape = (T, Hq, D)
+    qp, qrow = _kv_rows(q, "q", torch.bfloat16, shape, di)
     dev = q.device
     lp = None if lse is None else _fit(lse, "lse", torch.float32, (T, Hq), di)
-    y = _new(y, "y", (T, Hq, D), torch.bfloat16, dev)
-    ws, ws_bytes, _owner = _scratch(
-        workspace, _lib.aql_attention_kv8_bytes(T, plan.S, Hq, plan.Hkv, D, plan.W, plan.most), dev)
-    _call("aql_attention_kv8", _lib.aql_attention_kv8, di, qp, qrow, T, plan.S, Hq, plan.Hkv, D,
-          D ** -0.5 if sm_scale is None else float(sm_scale), plan.window, kq, vq, ks, vs, cache.P,
-          tp, plan.W, plan.most, pp, y.data_ptr(), lp, ws, ws_bytes)
+    y = _new(y, "y", shape, torch.bfloat16, dev)
+    need = plan._scratch.get(D)
+    if need is None:
+        need = plan._scratch[D] = _lib.aql_attention_kv8_bytes(T, S, Hq, Hkv, D, W, most)
+    ws, ws_bytes, _owner = _scratch(workspace, need, dev)
+    _call("aql_attention_kv8", _lib.aql_attention_kv8, di, qp, qrow, T, S, Hq, Hkv, D,
+          D ** -0.5 if sm_scale is None else float(sm_scale), window, *at, P, tp, W, most, plan._at,
+          y.data_ptr(), lp, ws, ws_bytes)
     return y

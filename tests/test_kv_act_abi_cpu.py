@@ -45,8 +45,8 @@ def test_plan_refusals(kw, code):
 def test_bytes():
     b, w = aql.aql_kv_plan_bytes, aql.aql_attention_kv8_bytes
     assert b(0, 0, 8, 2, 5, 4) > 0
-    # a piece of 32 bytes for each page that new tokens touch, a unit for each 64 rows
-    assert b(1 << 16, 7, 8, 2, 5000, 1 << 14) >= 32 * ((1 << 16) // 64 + 2 * 7) + 32 * (1 << 16) * 4 // 64
+    # a piece of 32 bytes for each page that new tokens touch, a unit for each 128 rows
+    assert b(1 << 16, 7, 8, 2, 5000, 1 << 14) >= 32 * ((1 << 16) // 64 + 2 * 7) + 32 * (1 << 16) * 4 // 128
     for bad in SIZES:
         z = dict(T=9, S=3, Hq=8, Hkv=2, W=5, most=4)
         z.update(bad)
