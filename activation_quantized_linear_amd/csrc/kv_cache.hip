@@ -77,8 +77,8 @@ __device__ __forceinline__ int owner(const int *first, int S, int i) {
 }
 
 // One workgroup. Sequences' pieces and tiles are counted and summed up; every piece and
-// tile then finds its sequence by bisection, three times over the tiles: their blocks,
-// their units' lengths, the units. A tile's blocks are divided into units of about
+// tile then finds its sequence by bisection, with three passes over the tiles: their blocks,
+// their units' lengths, the units. Bound by latency (PLANFIG). A tile's blocks are divided into units of about
 // `chunk` = total / target blocks' cost, at most a quarter more, and units are laid out longest
 // first (by classes of length: atomics in LDS give the places inside a class, which no
 // result depends on), so that the last ones to start are short.
@@ -90,36 +90,36 @@ __global__ __launch_bounds__(kPlanThreads) void k_kv_plan(const int32_t *__restr
   __shared__ int first_piece[kKvMaxSeqs + 1], first_tile[kKvMaxSeqs + 1];
   __shared__ int64_t tmp[kPlanThreads / 64];
   __shared__ int count[kBins], cursor[kBins], s_bad, s_parts, s_joins, s_longest;
+  __shared__ unsigned long long s_blocks;
   const int tid = threadIdx.x, G = z.Hq / z.Hkv, S = (int)z.S;
   if (tid == 0) {
     s_bad = 0x7fffffff;
     s_parts = s_joins = s_longest = 0;
+    s_blocks = 0;
   }
   if (tid < kBins) count[tid] = 0;
   __syncthreads();
 
-  // ---- pieces and tiles of every sequence
-  int64_t npieces = 0, ntiles = 0, total;
+  // ---- pieces and tiles of every sequence, summed up as the halves of one number
+  int64_t npieces = 0, ntiles = 0;
   for (int s0 = 0; s0 < S; s0 += kPlanThreads) {
     const int s = s0 + tid;
-    int64_t p = 0, t = 0;
+    int64_t both = 0, total;
     if (s < S) {
       bool bad;
       const Seq q = sequence(cu, pos, z, s, bad);
       if (bad) atomicMin(&s_bad, s);
-      if (q.len > 0) {
-        p = (q.pos + q.len - 1) / kKvBlock - q.pos / kKvBlock + 1;
-        t = ((int64_t)q.len * G + tile - 1) / tile;
-      }
+      if (q.len > 0)
+        both = (int64_t)((q.pos + q.len - 1) / kKvBlock - q.pos / kKvBlock + 1) << 32 |
+               ((int64_t)q.len * G + tile - 1) / tile;
     }
-    const int64_t fp = scan(p, tmp, total) + npieces;
-    npieces += total;
-    const int64_t ft = scan(t, tmp, total) + ntiles;
-    ntiles += total;
+    const int64_t at = scan(both, tmp, total);
     if (s < S) {
-      first_piece[s] = (int)fp;
-      first_tile[s] = (int)ft;
+      first_piece[s] = (int)(npieces + (at >> 32));
+      first_tile[s] = (int)(ntiles + (at & 0xffffffff));
     }
+    npieces += total >> 32;
+    ntiles += total & 0xffffffff;
   }
   // sequences that overlap in the step would have more than the plan holds
   const bool fits = npieces <= lay.pieces && ntiles <= lay.units - lay.parts;
@@ -130,22 +130,36 @@ __global__ __launch_bounds__(kPlanThreads) void k_kv_plan(const int32_t *__restr
   }
   __syncthreads();
 
-  // ---- blocks of every tile
-  int64_t mine = 0, blocks;
-  int most = 0;
-  for (int i = tid; i < ntiles; i += kPlanThreads) {
-    const int s = owner(first_tile, S, i);
+  // ---- blocks of every tile; a thread keeps its first one's numbers
+  struct Tile {
+    Seq q;
+    int s, row0, b0, b1, cost;
+  };
+  auto tile_of = [&](int i) {
+    Tile t;
+    t.s = owner(first_tile, S, i);
     bool bad;
-    const Seq q = sequence(cu, pos, z, s, bad);
-    int b0, b1;
-    const int row0 = (i - first_tile[s]) * tile;
-    tile_blocks(q, G, z.window, row0, tile, b0, b1);
-    const int cost = (b1 - b0) * block_cost(q, G, tile, row0);
-    mine += cost;
-    most = max(most, cost);
+    t.q = sequence(cu, pos, z, t.s, bad);
+    t.row0 = (i - first_tile[t.s]) * tile;
+    tile_blocks(t.q, G, z.window, t.row0, tile, t.b0, t.b1);
+    t.cost = (t.b1 - t.b0) * block_cost(t.q, G, tile, t.row0);
+    return t;
+  };
+  Tile own{};
+  if (tid < ntiles) own = tile_of(tid);
+  int64_t mine = own.cost;
+  int most = own.cost;
+  for (int i = tid + kPlanThreads; i < ntiles; i += kPlanThreads) {
+    const Tile t = tile_of(i);
+    mine += t.cost;
+    most = max(most, t.cost);
   }
-  atomicMax(&s_longest, most);
-  scan(mine, tmp, blocks);
+  if (most > 0) {
+    atomicMax(&s_longest, most);
+    atomicAdd(&s_blocks, (unsigned long long)mine);
+  }
+  __syncthreads();
+  const int64_t blocks = (int64_t)s_blocks;
   int64_t chunk = (blocks + target - 1) / target;
   const int64_t least = kKvMinBlocks * (tile < kKvTileRows ? 1 : kKvTileCost);
   chunk = chunk < least ? least : chunk;
@@ -172,14 +186,10 @@ __global__ __launch_bounds__(kPlanThreads) void k_kv_plan(const int32_t *__restr
   KvJoin *joins = reinterpret_cast<KvJoin *>(plan + lay.at_joins);
   for (int pass = 0; pass < 2; ++pass) {
     for (int i = tid; i < ntiles; i += kPlanThreads) {
-      const int s = owner(first_tile, S, i);
-      bool bad;
-      const Seq q = sequence(cu, pos, z, s, bad);
-      const int row0 = (i - first_tile[s]) * tile;
-      int b0, b1;
-      tile_blocks(q, G, z.window, row0, tile, b0, b1);
-      const int n = b1 - b0;
-      const int64_t cost = (int64_t)n * block_cost(q, G, tile, row0);
+      const Tile t = i == tid ? own : tile_of(i);
+      const Seq &q = t.q;
+      const int s = t.s, row0 = t.row0, b0 = t.b0, n = t.b1 - t.b0;
+      const int64_t cost = t.cost;
       // (no more parts than the plan has room for: at least kKvMinBlocks blocks each)
       const int parts = (int)max((int64_t)1, min((cost + chunk - 1 - chunk / 4) / chunk,
                                                  (int64_t)(n + kKvMinBlocks - 1) / kKvMinBlocks));
@@ -200,6 +210,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_kv_plan(const int32_t *__restr
     }
     __syncthreads();
     if (pass == 0) {
+      int64_t total;
       const int64_t at = scan(tid < kBins ? count[tid] : 0, tmp, total);
       if (tid < kBins) cursor[tid] = (int)at;
       if (tid == 0) plan[kKvUnits] = (int)total;

@@ -71,7 +71,8 @@ def parse():
     ap.add_argument("--only", default=None,
                     help="run just one workload (sweep|chain|llm7b|q8ta|dq8ca|quant|calib|gptq|copy), or a "
                          "measurement outside the default run (wsweep: working-set sweep; oracle: "
-                         "the CPU oracle at full size beside the GPU)")
+                         "the CPU oracle at full size beside the GPU; decoder: a decode step of "
+                         "whole layers, attention over the 8-bit cache among them)")
     ap.add_argument("--no-settle", action="store_true",
                     help="profile helper: skip the settle phase (counter runs serialize every "
                          "dispatch, so settling there only costs time)")
@@ -320,6 +321,58 @@ def sec_decode_chain(torch, aql, workloads, dev, copies=3):
                                  f"up+gate sharing x, then down on up's output), 64 launches",
                      "us": ms * 1e3, "GB/s": gbs, "frac_hbm": gbs / HBM_PEAK_GBS,
                      "us_per_launch": ms * 1e3 / 64})
+        say(rows[-1])
+    return rows
+
+
+def sec_decoder(torch, aql, workloads, dev):
+    """A decode step of SmolVLM-500M's 32 text layers with everything that has weights or a cache:
+    the fused q, k, v projection, the cache write, attention (15 heads of 64 over 5 kv heads), the output
+    projection onto the residual stream, up, silu(gate) * up and down onto the residual
+    stream; the norms and rotations between them are left out. One plan a step. Captured in a
+    HIP graph; requests with contexts of 1023 tokens each; random weights."""
+    layers, H, F, Hq, Hkv, D = workloads.SMOLVLM_LAYERS, workloads.SMOLVLM_HIDDEN, workloads.SMOLVLM_FFN, 15, 5, 64
+    g = torch.Generator(device=dev).manual_seed(0)
+
+    def weight(n, k):
+        w = torch.randn(n, k, generator=g, device=dev) * 0.02
+        return aql.aql_quantize_weight_int8(w, aql.AQL_WQ_SYM127)[:2]
+
+    weights = [[weight(n, k) for n, k in (((Hq + 2 * Hkv) * D, H), (H, Hq * D), (F, H), (F, H), (H, F))]
+               for _ in range(layers)]
+    rows = []
+    for M, past in ((1, 1023), (16, 1023), (64, 1023)):
+        W = (past + 64) // 64
+        table = torch.randperm(M * W, generator=g, device=dev).view(M, W).to(torch.int32)
+        one = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)
+        plan = aql.aql_kv_plan(one(range(M + 1)), one([past] * M), M, 1, Hq, Hkv, W)
+        before = aql.aql_kv_plan(one([i * past for i in range(M + 1)]), one([0] * M), M * past, past, Hq, Hkv, W)
+        caches = []
+        for _ in range(layers):
+            cache = aql.aql_kv_cache(M * W, Hkv, D, dev)
+            k, v = torch.randn(2, M * past, Hkv, D, generator=g, device=dev).to(torch.bfloat16)
+            aql.aql_kv_cache_write(k, v, cache, table, before)
+            caches.append(cache)
+        x0 = torch.randn(M, H, generator=g, device=dev).to(torch.bfloat16)
+
+        def step(_):
+            x = x0
+            for (wqkv, wo, wu, wg, wd), cache in zip(weights, caches):
+                qkv = aql.aql_linear_w8a16(x, *wqkv)
+                q, k, v = (t.unflatten(1, (-1, D)) for t in qkv.split([Hq * D, Hkv * D, Hkv * D], 1))
+                aql.aql_kv_cache_write(k, v, cache, table, plan)
+                y = aql.aql_attention_kv8(q, cache, table, plan)
+                x = aql.aql_linear_w8a16_act(y.view(M, Hq * D), *wo, residual=x)
+                up = aql.aql_linear_w8a16(x, *wu)
+                h = aql.aql_linear_w8a16_act(x, *wg, act=aql.AQL_ACT_SILU, mul=up)
+                x = aql.aql_linear_w8a16_act(h, *wd, residual=x)
+
+        step(0)
+        med, _ = event_time_ms(torch, step, 3, 1, graph=True)
+        nbytes = layers * (sum(q.numel() for q, _ in weights[0]) + M * (past + 1) * Hkv * 2 * D)
+        rows.append({"workload": f"smolvlm500m decode step, {M} requests of {past + 1} tokens, HIP graph: 32 layers x "
+                                 "(qkv, cache write, attention, out + residual, up, silu(gate) * up, down + residual)",
+                     "us": med * 1e3, "GB/s": nbytes / (med * 1e-3) / 1e9, "us_per_layer": med * 1e3 / layers})
         say(rows[-1])
     return rows
 
@@ -791,7 +844,7 @@ def main():
         fn = {"llm7b": sec_llm7b, "q8ta": sec_q8ta, "dq8ca": sec_dq8ca, "quant": sec_quant,
               "chain": sec_decode_chain,
               "calib": sec_calib, "copy": sec_copy, "gptq": sec_gptq, "wsweep": sec_wsweep,
-              "oracle": sec_oracle}[args.only]
+              "oracle": sec_oracle, "decoder": sec_decoder}[args.only]
         print(json.dumps({"only": args.only, "rows": fn(torch, aql, workloads, dev)}), flush=True)
         return
     calls, step_bytes, nbytes, layers = sweep_workload(torch, aql, workloads, dev)
