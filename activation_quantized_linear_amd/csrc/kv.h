@@ -75,7 +75,7 @@ constexpr int kv_tile_rows(const KvSizes &z) {
 // Units that a step is divided into where there is enough to divide (over all kv heads),
 // and the fewest blocks of one.
 constexpr int64_t kv_target(const KvSizes &z) {
-  const int64_t t = (kv_tile_rows(z) == kKvTileRows ? 384 : 768) / z.Hkv;
+  const int64_t t = (kv_tile_rows(z) == kKvTileRows ? 448 : 768) / z.Hkv;
   return t > 1 ? t : 1;
 }
 constexpr int64_t kKvMinBlocks = 4;
