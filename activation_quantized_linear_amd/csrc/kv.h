@@ -48,7 +48,8 @@ struct KvUnit {
   int32_t seq, tok, len, pos, row0, b0, b1, part;
 };
 
-// Rows whose blocks are spread over `parts` units, from partial result `part` on.
+// Rows whose blocks are spread over `parts` units, from partial result `part` on. (pad: the
+// plan's own.)
 struct KvJoin {
   int32_t tok, len, row0, part, parts, pad[3];
 };

@@ -78,7 +78,7 @@ __device__ __forceinline__ int owner(const int *first, int S, int i) {
 
 // One workgroup. Sequences' pieces and tiles are counted and summed up; every piece and
 // tile then finds its sequence by bisection, with three passes over the tiles: their blocks,
-// their units' lengths, the units. Bound by latency (PLANFIG). A tile's blocks are divided into units of about
+// their units' lengths, the units. Bound by latency (one request 7 us, 27 of them 11, 64 divided ones 16). A tile's blocks are divided into units of about
 // `chunk` = total / target blocks' cost, at most a quarter more, and units are laid out longest
 // first (by classes of length: atomics in LDS give the places inside a class, which no
 // result depends on), so that the last ones to start are short.
@@ -198,15 +198,13 @@ __global__ __launch_bounds__(kPlanThreads) void k_kv_plan(const int32_t *__restr
         atomicAdd(&count[bin], parts);
         continue;
       }
-      int at = atomicAdd(&cursor[bin], parts), part = -1;
-      if (parts > 1) {
-        part = atomicAdd(&s_parts, parts);
-        joins[atomicAdd(&s_joins, 1)] = KvJoin{q.tok, q.len, row0, part, parts, {0, 0, 0}};
+      const int at = atomicAdd(&cursor[bin], parts);
+      if (parts > 1) {  // (its units below; the join keeps their place and the tile meanwhile)
+        const int part = atomicAdd(&s_parts, parts);
+        joins[atomicAdd(&s_joins, 1)] = KvJoin{q.tok, q.len, row0, part, parts, {at, i, 0}};
+      } else {
+        units[at] = KvUnit{s, q.tok, q.len, q.pos, row0, b0, b0 + n, -1};
       }
-      for (int u = 0; u < parts; ++u)  // as even as whole blocks are
-        units[at + u] = KvUnit{s, q.tok, q.len, q.pos, row0, b0 + (int)((int64_t)n * u / parts),
-                               b0 + (int)((int64_t)n * (u + 1) / parts),
-                               part < 0 ? -1 : part + u};
     }
     __syncthreads();
     if (pass == 0) {
@@ -216,6 +214,16 @@ __global__ __launch_bounds__(kPlanThreads) void k_kv_plan(const int32_t *__restr
       if (tid == 0) plan[kKvUnits] = (int)total;
       __syncthreads();
     }
+  }
+  // a wave a divided tile, a lane a part: as even as whole blocks are
+  for (int j = tid >> 6; j < s_joins; j += kPlanThreads / 64) {
+    const KvJoin w = joins[j];
+    const Tile t = tile_of(w.pad[1]);
+    const uint32_t n = (uint32_t)(t.b1 - t.b0), parts = (uint32_t)w.parts;  // n parts < 2^31
+    for (uint32_t u = tid & 63; u < parts; u += 64)
+      units[w.pad[0] + u] = KvUnit{t.s, t.q.tok, t.q.len, t.q.pos, t.row0,
+                                   t.b0 + (int)(n * u / parts), t.b0 + (int)(n * (u + 1) / parts),
+                                   w.part + (int)u};
   }
   if (tid == 0) {
     plan[kKvInfo] = s_bad != 0x7fffffff ? s_bad + 1 : fits ? 0 : S + 1;
