@@ -310,7 +310,7 @@ __device__ __forceinline__ void stream_rows(const AttnArgs &a, const KvUnit &u, 
         const float o2 = t2 == -__builtin_inff() ? 0.0f : t2;
 #pragma unroll
         for (int w = 0; w < 4; ++w) L = fmaf(ol[w][lrow], exp2_hw(om[w][lrow] - o2), L);
-        const int64_t at = ((int64_t)u.part * a.c.Hkv + h) * a.tile + row0 - row0 + lrow;
+        const int64_t at = ((int64_t)u.part * a.c.Hkv + h) * a.tile + row0 - u.row0 + lrow;
         if (half == 0 && oc == 0) {
           if (u.part < 0) {
             store_lse(a, u.tok, h, row0 + lrow, t2, L);

@@ -170,6 +170,29 @@ def test_write_and_attention(seqs, Hq, Hkv, D, window):
     s.check_attention(y, lse)
 
 
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+@pytest.mark.parametrize("new", [6, 12, 25, 70])  # units of 16, 32, 64 and 128 rows
+@pytest.mark.parametrize("window", [0, 1200])
+def test_divided_units(D, new, window):
+    """Long sequences whose blocks are divided over units, of every number of rows and head size."""
+    s = Step([(1900, new), (900, max(1, new // 3)), (0, 2)], 4, 2, D, seed=D + new, window=window, pad=1)
+    s.write_past()
+    plan = s.write()
+    y, lse = s.attend(plan)
+    s.check_attention(y, lse)
+
+
+@pytest.mark.parametrize("Hq,D", [(129, 64), (200, 128), (1024, 8)])
+@pytest.mark.parametrize("window", [0, 100])
+def test_many_heads_of_one_kv_head(Hq, D, window):
+    """A token's heads fill more than one unit."""
+    s = Step([(700, 1), (63, 2), (0, 1)], Hq, 1, D, seed=Hq, window=window)
+    s.write_past()
+    plan = s.write()
+    y, lse = s.attend(plan)
+    s.check_attention(y, lse)
+
+
 def test_scale_of_softmax_and_no_lse():
     s = Step([(70, 3), (0, 70), (200, 1)], 4, 2, 64, seed=3)
     s.write_past()
