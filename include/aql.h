@@ -547,7 +547,8 @@ int aql_act_restore(const int8_t *xq, const float *xs, int64_t M, int64_t K, voi
  * step's T rows, new tokens at positions pos[s], pos[s] + 1, ...; the tokens before them
  * are in the cache. table [S, W] holds each sequence's page numbers: position t lies in
  * page table[s][t / AQL_KV_BLOCK] at place t % AQL_KV_BLOCK; entries past a
- * sequence's last page are not read. Rows past cu[S] belong to no sequence.
+ * sequence's last page are not read, nor, by attention, those of pages wholly before every
+ * window. Rows past cu[S] belong to no sequence.
  *
  * The plan. aql_kv_plan divides a step into work for the device; every layer's write
  * and attention use the same plan while cu and pos stand (it copies what it needs).
@@ -585,7 +586,8 @@ int aql_kv_plan(const int32_t *cu, const int32_t *pos, int64_t T, int64_t S, int
  *   table  device, [S, W] int32
  * Errors: unknown dtype; D not a multiple of 8 in 8..AQL_KV_MAX_HEAD; P outside 1..2^31 - 1;
  * krow or vrow below Hkv D, or not whole 16 bytes; the plan's errors; NULL (T, S > 0) or
- * misaligned pointers.
+ * misaligned pointers; more pages and heads than one grid holds, (T / 64 + 2 min(S, T)) Hkv
+ * times 2 DP past 2^32 (AQL_ERR_HIP).
  */
 int aql_kv_cache_write(const void *k, int64_t krow, const void *v, int64_t vrow, int dtype,
                        int64_t T, int64_t S, int64_t Hq, int64_t Hkv, int64_t D,
@@ -617,7 +619,8 @@ int aql_kv_cache_read(const int8_t *kq, const int8_t *vq, const float *ks, const
  *   y    device, [T, Hq, D] bf16 (output);  lse  device, [T, Hq] float32 (output; may be NULL)
  *   ws   device workspace of aql_attention_kv8_bytes(...) bytes (may be NULL where that is 0)
  * Errors: as aql_kv_cache_write; qrow likewise; sm_scale not finite and positive
- * (AQL_ERR_PARAM); workspace too small.
+ * (AQL_ERR_PARAM); workspace too small; units of work past one grid (AQL_ERR_HIP; at most
+ * T Hq / 16 + S Hkv + 2048 of them, fewer than 2^24 fit).
  */
 size_t aql_attention_kv8_bytes(int64_t T, int64_t S, int64_t Hq, int64_t Hkv, int64_t D, int64_t W,
                                int64_t most);
