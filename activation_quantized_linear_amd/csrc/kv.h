@@ -63,10 +63,11 @@ struct KvSizes {
   int64_t window;     // 0: none
 };
 
-// Rows of a unit, by the most that any sequence can have. Up to 64 a block's codes go
-// straight to registers and are bound by memory; past that every block serves so many rows
-// that widening it once, into LDS, pays (prefill of 11490 tokens, 32 heads of 128 over 8:
-// 907 us in units of 64 rows, 400 in tiles of 128).
+// Rows of a unit, by the most that any sequence can have. Up to 32 a block's codes go
+// straight to registers and are bound by memory; past that a block serves so many rows
+// that widening it once, into LDS, pays (one sequence of 64 rows for 8 kv heads of 128, 20, 300, 30000
+// tokens, us: streamed in units of 64 rows 13.6, 17.6, 71.7; tiles 7.2, 12.8, 47.7; of 32 rows, 300 and
+// 1500 tokens: streamed 10.5, 11.2; tiles 12.5, 13.0).
 constexpr int kKvTileRows = 128;
 // Units of at most so many rows stream also in a step of tiles; there a block of theirs
 // costs about a quarter of a tile's.
@@ -74,7 +75,7 @@ constexpr int kKvFewRows = 16;
 constexpr int kKvTileCost = 4;
 constexpr int kv_tile_rows(const KvSizes &z) {
   const int64_t rows = z.most * (z.Hq / z.Hkv);
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kKvTileRows;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : kKvTileRows;
 }
 // Units that a step is divided into where there is enough to divide (over all kv heads),
 // and the fewest blocks of one. Streams: three workgroups a CU (64 requests of up to 8192
@@ -95,6 +96,7 @@ constexpr int64_t kKvWhole = 8;
 struct KvPlanLayout {
   int64_t pieces, units, joins;        // most of each
   int64_t parts;                       // most partial results (of each kv head)
+  int64_t tiles;                       // most tiles
   int64_t at_pieces, at_units, at_joins, total;  // in words
 };
 constexpr KvPlanLayout kv_plan_layout(const KvSizes &z) {
@@ -107,8 +109,9 @@ constexpr KvPlanLayout kv_plan_layout(const KvSizes &z) {
   p.pieces = z.T / kKvBlock + 2 * live;
   // a unit has at least total / target blocks, but for the last one of a tile
   p.parts = most < 2 ? 0 : 2 * target < tiles * most ? 2 * target : tiles * most;
+  p.tiles = tiles;
   p.units = tiles + p.parts;
-  p.joins = p.parts / 2;
+  p.joins = p.parts / 2 < tiles ? p.parts / 2 : tiles;
   p.at_pieces = kKvHeader;
   p.at_units = p.at_pieces + 8 * p.pieces;
   p.at_joins = p.at_units + 8 * p.units;

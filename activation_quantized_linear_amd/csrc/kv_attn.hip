@@ -763,15 +763,14 @@ hipError_t launch_join(const AttnArgs &a, int64_t joins, hipStream_t st) {
   return hipGetLastError();
 }
 
-// (a unit of 64 rows with a head past 128 in two workgroups of 32: its sums need the registers)
+// In units of 16 NB rows, `per` workgroups of them a unit of the plan.
 template <int NB>
-void launch_stream(const AttnArgs &a, unsigned grid, hipStream_t st) {
-  constexpr int WIDE = NB > 2 ? 2 : NB;
+void launch_stream(const AttnArgs &a, unsigned grid, unsigned per, hipStream_t st) {
   switch (a.c.DP / 64) {
-    case 1: hipLaunchKernelGGL((k_kv_attn_stream<NB, 1>), dim3(grid), dim3(256), 0, st, a); break;
-    case 2: hipLaunchKernelGGL((k_kv_attn_stream<NB, 2>), dim3(grid), dim3(256), 0, st, a); break;
-    case 3: hipLaunchKernelGGL((k_kv_attn_stream<WIDE, 3>), dim3(grid, NB / WIDE), dim3(256), 0, st, a); break;
-    default: hipLaunchKernelGGL((k_kv_attn_stream<WIDE, 4>), dim3(grid, NB / WIDE), dim3(256), 0, st, a); break;
+    case 1: hipLaunchKernelGGL((k_kv_attn_stream<NB, 1>), dim3(grid, per), dim3(256), 0, st, a); break;
+    case 2: hipLaunchKernelGGL((k_kv_attn_stream<NB, 2>), dim3(grid, per), dim3(256), 0, st, a); break;
+    case 3: hipLaunchKernelGGL((k_kv_attn_stream<NB, 3>), dim3(grid, per), dim3(256), 0, st, a); break;
+    default: hipLaunchKernelGGL((k_kv_attn_stream<NB, 4>), dim3(grid, per), dim3(256), 0, st, a); break;
   }
 }
 
@@ -827,7 +826,7 @@ hipError_t launch_kv_attention(const uint16_t *q, int64_t qrow, float sm_scale, 
   if (!grid_fits(lay.units * z.Hkv, 256)) return hipErrorInvalidConfiguration;
   const unsigned grid = (unsigned)(lay.units * z.Hkv);
   hipError_t e = hipSuccess;
-  if (tile == kKvTileRows) {
+  if (tile == kKvTileRows && (c.DP <= 128 || z.most * a.G > 64)) {
     switch (c.DP / 64) {
       case 1: e = launch_tile<1>(a, grid, st); break;
       case 2: e = launch_tile<2>(a, grid, st); break;
@@ -835,14 +834,20 @@ hipError_t launch_kv_attention(const uint16_t *q, int64_t qrow, float sm_scale, 
       default: e = launch_tile<4>(a, grid, st); break;
     }
   } else {
-    if (tile == 16) launch_stream<1>(a, grid, st);
-    else if (tile == 32) launch_stream<2>(a, grid, st);
-    else launch_stream<4>(a, grid, st);
+    // (33 to 64 rows of a head past 128, whose tiles leave one workgroup a CU, in two streams of
+    // 32: one sequence, one kv head of 256, 300 and 1500 tokens 16.7, 17.0 us, as tiles 21.9, 22.2.
+    // The two of a unit lie on one XCD and its L2.)
+    if (tile == 16) launch_stream<1>(a, grid, 1, st);
+    else if (tile == 32) launch_stream<2>(a, grid, 1, st);
+    else launch_stream<2>(a, (grid + 7) / 8 * 8, 2, st);
     e = hipGetLastError();
   }
   if (e != hipSuccess || lay.joins == 0) return e;
-  return tile == kKvTileRows ? launch_join<false>(a, lay.joins, st)
-                             : launch_join<true>(a, lay.joins, st);
+  // few tiles may be in many parts each (one sequence of 64 rows for one kv head of 128, 30000
+  // tokens: 45.5 us with a row a group of threads, 19.9 spread), many are in few (16 requests and a
+  // chunk of 509 tokens, 264 joins at most: 90, 105 spread; 256 tokens behind 16000, 72: 94, 99)
+  return tile == kKvTileRows && lay.joins * z.Hkv > 64 ? launch_join<false>(a, lay.joins, st)
+                                                       : launch_join<true>(a, lay.joins, st);
 }
 
 }  // namespace aql

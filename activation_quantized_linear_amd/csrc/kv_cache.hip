@@ -78,10 +78,11 @@ __device__ __forceinline__ int owner(const int *first, int S, int i) {
 
 // One workgroup. Sequences' pieces and tiles are counted and summed up; every piece and
 // tile then finds its sequence by bisection, with three passes over the tiles: their blocks,
-// their units' lengths, the units. Bound by latency (one request 7 us, 27 of them 11, 64 divided ones 16). A tile's blocks are divided into units of about
-// `chunk` = total / target blocks' cost, at most a quarter more, and units are laid out longest
-// first (by classes of length: atomics in LDS give the places inside a class, which no
-// result depends on), so that the last ones to start are short.
+// their units' lengths, the units. Bound by latency (one request 7 us, 27 of them 11, 64 divided
+// ones 16). A tile's blocks are divided into units of about `chunk` = total / target blocks'
+// cost (and kKvMinBlocks blocks), at most a quarter more, and units are laid out longest
+// first (by classes of length: atomics in LDS give the places inside a class, which no result
+// depends on), so that the last ones to start are short.
 __global__ __launch_bounds__(kPlanThreads) void k_kv_plan(const int32_t *__restrict__ cu,
                                                           const int32_t *__restrict__ pos,
                                                           KvSizes z, int tile, KvPlanLayout lay,
@@ -160,11 +161,13 @@ __global__ __launch_bounds__(kPlanThreads) void k_kv_plan(const int32_t *__restr
   }
   __syncthreads();
   const int64_t blocks = (int64_t)s_blocks;
-  int64_t chunk = (blocks + target - 1) / target;
-  const int64_t least = kKvMinBlocks * (tile < kKvTileRows ? 1 : kKvTileCost);
-  chunk = chunk < least ? least : chunk;
-  if (lay.parts == 0) chunk = kKvTileCost * z.W;
-  const int longest = (int)min(chunk + chunk / 4, (int64_t)s_longest);
+  const int64_t share = (blocks + target - 1) / target;
+  auto chunk_of = [&](int cost) -> int64_t {  // of a tile whose blocks cost so much each
+    if (lay.parts == 0) return kKvTileCost * z.W;
+    return share < kKvMinBlocks * cost ? kKvMinBlocks * cost : share;
+  };
+  const int64_t widest = chunk_of(tile < kKvTileRows ? 1 : kKvTileCost);
+  const int longest = (int)min(widest + widest / 4, (int64_t)s_longest);
   auto bin_of = [&](int len) {  // long units first (a part that may not be smaller is the longest)
     len = min(len, longest);
     return kBins - 1 - (int)((int64_t)len * (kBins - 1) / (longest > 0 ? longest : 1));
@@ -189,7 +192,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_kv_plan(const int32_t *__restr
       const Tile t = i == tid ? own : tile_of(i);
       const Seq &q = t.q;
       const int s = t.s, row0 = t.row0, b0 = t.b0, n = t.b1 - t.b0;
-      const int64_t cost = t.cost;
+      const int64_t cost = t.cost, chunk = chunk_of(block_cost(q, G, tile, row0));
       // (no more parts than the plan has room for: at least kKvMinBlocks blocks each)
       const int parts = (int)max((int64_t)1, min((cost + chunk - 1 - chunk / 4) / chunk,
                                                  (int64_t)(n + kKvMinBlocks - 1) / kKvMinBlocks));
