@@ -130,18 +130,21 @@ __device__ __forceinline__ void store_lse(const AttnArgs &a, int tok, int h, int
 // 103 with them). Bound by memory. The four waves take blocks in turn, each with a
 // maximum and sums of its own, and join in LDS at the end. The next block's K is in
 // flight from when the present one is used up, V from the same moment one block earlier.
-template <int NB, int C>
+// (With 8 waves on two a SIMD's registers, a block's V is loaded once its K is used up and
+// the next K after that: the other waves' loads fill the time.)
+template <int NB, int C, int NW>
 struct StreamLds {
   static constexpr int DIMS = C > 2 ? 128 : 64 * C;  // joined at a time
-  float o[4][16][DIMS + 4];
-  float m[4][16 * NB], l[4][16 * NB];
+  float o[NW][16][DIMS + 4];
+  float m[NW][16 * NB], l[NW][16 * NB];
 };
 
 // Rows row0 .. row0 + 16 NB - 1 of u's sequence.
-template <int NB, int C>
+template <int NB, int C, int NW>
 __device__ __forceinline__ void stream_rows(const AttnArgs &a, const KvUnit &u, int h, int row0,
-                                            StreamLds<NB, C> &lds) {
-  constexpr int DP = 64 * C, ND = DP / 16, HD = StreamLds<NB, C>::DIMS;
+                                            StreamLds<NB, C, NW> &lds) {
+  constexpr int DP = 64 * C, ND = DP / 16, HD = StreamLds<NB, C, NW>::DIMS;
+  constexpr bool AHEAD = NW == 4;
   auto &ob = lds.o;
   auto &om = lds.m;
   auto &ol = lds.l;
@@ -194,13 +197,14 @@ __device__ __forceinline__ void stream_rows(const AttnArgs &a, const KvUnit &u, 
   int page = b < u.b1 ? page_at(b) : 0;
   if (b < u.b1) load_k(page);
   while (b < u.b1) {
-    const bool more = b + 4 < u.b1;
-    const int next = more ? page_at(b + 4) : page;
-    {
+    const bool more = b + NW < u.b1;
+    const int next = more ? page_at(b + NW) : page;
+    auto load_v = [&]() {
       const int8_t *p = a.c.vq + base(page) + vofs;
 #pragma unroll
       for (int d = 0; d < ND; ++d) vb[d] = __builtin_nontemporal_load(reinterpret_cast<const i32x4 *>(p + d * 1024));
-    }
+    };
+    if constexpr (AHEAD) load_v();
     const bool live = page >= 0 && page < a.c.pages;
     const int64_t at = (live ? (int64_t)page : 0) * a.c.Hkv + h;
     const float ks = a.c.ks[at], vs = a.c.vs[at];
@@ -222,7 +226,12 @@ __device__ __forceinline__ void stream_rows(const AttnArgs &a, const KvUnit &u, 
         }
       }
     }
-    if (more) load_k(next);
+    if constexpr (!AHEAD) {
+      __builtin_amdgcn_sched_barrier(0);
+      load_v();
+    } else if (more) {
+      load_k(next);
+    }
 
     // tokens past a query or before its window, and those of a page that is none: of the
     // lane's tokens, how far each lies behind its query, as an unsigned number
@@ -272,8 +281,12 @@ __device__ __forceinline__ void stream_rows(const AttnArgs &a, const KvUnit &u, 
         acc[nb][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[nb][1], acc[nb][d], 0, 0, 0);
       }
     }
+    if constexpr (!AHEAD) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (more) load_k(next);
+    }
     page = next;
-    b += 4;
+    b += NW;
   }
 
   // ---- the waves' results join
@@ -291,7 +304,7 @@ __device__ __forceinline__ void stream_rows(const AttnArgs &a, const KvUnit &u, 
     const int row = 16 * nb + r;
     float top = om[0][row];
 #pragma unroll
-    for (int w = 1; w < 4; ++w) top = fmaxf(top, om[w][row]);
+    for (int w = 1; w < NW; ++w) top = fmaxf(top, om[w][row]);
     const float off = top == -__builtin_inff() ? 0.0f : top;
     const float f = exp2_hw(M[nb] - off);
 #pragma unroll
@@ -303,13 +316,13 @@ __device__ __forceinline__ void stream_rows(const AttnArgs &a, const KvUnit &u, 
       __syncthreads();
       // thread (row orow, piece oc): 4 dims at a time
       const int orow = threadIdx.x >> 4, oc = threadIdx.x & 15, lrow = 16 * nb + orow;
-      if (lrow < rows) {
+      if (orow < 16 && lrow < rows) {
         float t2 = om[0][lrow], L = 0.0f;
 #pragma unroll
-        for (int w = 1; w < 4; ++w) t2 = fmaxf(t2, om[w][lrow]);
+        for (int w = 1; w < NW; ++w) t2 = fmaxf(t2, om[w][lrow]);
         const float o2 = t2 == -__builtin_inff() ? 0.0f : t2;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) L = fmaf(ol[w][lrow], exp2_hw(om[w][lrow] - o2), L);
+        for (int w = 0; w < NW; ++w) L = fmaf(ol[w][lrow], exp2_hw(om[w][lrow] - o2), L);
         const int64_t at = ((int64_t)u.part * a.c.Hkv + h) * a.tile + row0 - u.row0 + lrow;
         if (half == 0 && oc == 0) {
           if (u.part < 0) {
@@ -325,7 +338,7 @@ __device__ __forceinline__ void stream_rows(const AttnArgs &a, const KvUnit &u, 
           if (half + d >= a.c.D) continue;
           f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int w = 0; w < 4; ++w) o += *reinterpret_cast<const f32x4 *>(&ob[w][orow][d]);
+          for (int w = 0; w < NW; ++w) o += *reinterpret_cast<const f32x4 *>(&ob[w][orow][d]);
           if (u.part < 0) store_out(a, u.tok, h, row0 + lrow, half + d, L == 0.0f ? f32x4{0.f, 0.f, 0.f, 0.f} : o * (1.0f / L));
           else *reinterpret_cast<f32x4 *>(a.po + at * DP + half + d) = o;
         }
@@ -337,12 +350,12 @@ __device__ __forceinline__ void stream_rows(const AttnArgs &a, const KvUnit &u, 
 
 template <int NB, int C>
 __global__ __launch_bounds__(256) void k_kv_attn_stream(AttnArgs a) {
-  __shared__ __attribute__((aligned(16))) StreamLds<NB, C> lds;
+  __shared__ __attribute__((aligned(16))) StreamLds<NB, C, 4> lds;
   const int i = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
   if (i >= a.plan[kKvUnits]) return;
   const KvUnit u = reinterpret_cast<const KvUnit *>(a.plan + a.at_units)[i];
   const int row0 = u.row0 + (int)blockIdx.y * (16 * NB);
-  if (row0 < u.len * a.G) stream_rows<NB, C>(a, u, h, row0, lds);
+  if (row0 < u.len * a.G) stream_rows<NB, C, 4>(a, u, h, row0, lds);
 }
 
 // LDS writes done and every wave here; loads from memory stay in flight.
@@ -365,7 +378,9 @@ struct TileLds {
 template <int NB, int C>
 __device__ __forceinline__ void tile_rows(const AttnArgs &a, const KvUnit &u, int h, char *smem) {
   constexpr int DP = 64 * C, ND = DP / 16, HALF = TileLds<C>::HALF;
+  constexpr int P = kKvTileRows / (64 * NB), SL = (C + P - 1) / P;  // fours of waves, slices of each
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int four = wave >> 2, kw = wave & 3;
   const int r = lane & 15, g = lane >> 4;
   const int total = u.len * a.G;                  // rows of the sequence
   const int w0 = u.row0 + wave * (16 * NB);       // the wave's first
@@ -393,34 +408,41 @@ __device__ __forceinline__ void tile_rows(const AttnArgs &a, const KvUnit &u, in
   auto head_at = [&](int page) {
     return (int64_t)(page >= 0 && page < a.c.pages ? page : 0) * a.c.Hkv + h;
   };
-  // every wave brings C KiB of K and of V, in loads whose lanes hold what the lanes of two
-  // fragments will: of K, tile `wave`, slice c of the dims; of V, dims 16 (wave + 4 c) ..
-  const int8_t *ksrc = a.c.kq + (16 * (r >> 2) + 4 * wave + (r & 3)) * 64 + 16 * g;
-  const int8_t *vsrc = a.c.vq + wave * 1024 + r * 64 + 16 * g;
-  i32x4 kr[C], vr[C];
+  // every wave brings SL KiB of K and of V, in loads whose lanes hold what the lanes of two
+  // fragments will: slices c = four, four + P, .. of the dims, of K tile kw, of V dims
+  // 16 (kw + 4 c) ..
+  const int8_t *ksrc = a.c.kq + (16 * (r >> 2) + 4 * kw + (r & 3)) * 64 + 16 * g;
+  const int8_t *vsrc = a.c.vq + kw * 1024 + r * 64 + 16 * g;
+  auto slice = [&](int i) { return four + P * i; };
+  i32x4 kr[SL], vr[SL];
   auto load_k = [&](int page) {
     const int8_t *p = ksrc + head_at(page) * (64 * DP);
 #pragma unroll
-    for (int c = 0; c < C; ++c) kr[c] = *reinterpret_cast<const i32x4 *>(p + c * 4096);
+    for (int i = 0; i < SL; ++i)
+      if (C % P == 0 || slice(i) < C) kr[i] = *reinterpret_cast<const i32x4 *>(p + slice(i) * 4096);
   };
   auto load_v = [&](int page) {
     const int8_t *p = vsrc + head_at(page) * (64 * DP);
 #pragma unroll
-    for (int c = 0; c < C; ++c) vr[c] = *reinterpret_cast<const i32x4 *>(p + c * 4096);
+    for (int i = 0; i < SL; ++i)
+      if (C % P == 0 || slice(i) < C) vr[i] = *reinterpret_cast<const i32x4 *>(p + slice(i) * 4096);
   };
-  // piece i of the 2 C that a wave widens of either, into block k's half of LDS
+  // piece i of the 2 SL that a wave widens of either, into block k's half of LDS
   auto put_k = [&](int k, int i) {
-    *reinterpret_cast<f16x8 *>(smem + (k & 1) * HALF + wave * (C * 2048) + lane * 16 + i * 1024) =
-        widen_f16((uint32_t)kr[i >> 1][2 * (i & 1)], (uint32_t)kr[i >> 1][2 * (i & 1) + 1]);
+    if (C % P == 0 || slice(i >> 1) < C)
+      *reinterpret_cast<f16x8 *>(smem + (k & 1) * HALF + kw * (C * 2048) + lane * 16 +
+                                 slice(i >> 1) * 2048 + (i & 1) * 1024) =
+          widen_f16((uint32_t)kr[i >> 1][2 * (i & 1)], (uint32_t)kr[i >> 1][2 * (i & 1) + 1]);
   };
   auto put_v = [&](int k, int i) {
-    *reinterpret_cast<f16x8 *>(smem + (2 + (k & 1)) * HALF + wave * 2048 + lane * 16 +
-                               (i >> 1) * 8192 + (i & 1) * 1024) =
-        widen_f16((uint32_t)vr[i >> 1][2 * (i & 1)], (uint32_t)vr[i >> 1][2 * (i & 1) + 1]);
+    if (C % P == 0 || slice(i >> 1) < C)
+      *reinterpret_cast<f16x8 *>(smem + (2 + (k & 1)) * HALF + kw * 2048 + lane * 16 +
+                                 slice(i >> 1) * 8192 + (i & 1) * 1024) =
+          widen_f16((uint32_t)vr[i >> 1][2 * (i & 1)], (uint32_t)vr[i >> 1][2 * (i & 1) + 1]);
   };
   auto put_all = [&](int k) {  // V is a block behind K
 #pragma unroll
-    for (int i = 0; i < 2 * C; ++i) {
+    for (int i = 0; i < 2 * SL; ++i) {
       put_v(k + 1, i);
       put_k(k + 2, i);
     }
@@ -566,8 +588,8 @@ __device__ __forceinline__ void tile_rows(const AttnArgs &a, const KvUnit &u, in
       if (f + 4 < F) vf[f & 3] = read(k, true, f + 4);
       if constexpr (MORE)
         if (f & 1) {
-          if (f < F / 2) put_v(k + 1, f / 2);
-          else put_k(k + 2, f / 2 - 2 * C);
+          if (f < F / 2 && f / 2 < 2 * SL) put_v(k + 1, f / 2);
+          if (f >= F / 2 && f / 2 - 2 * C < 2 * SL) put_k(k + 2, f / 2 - 2 * C);
         }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -591,7 +613,7 @@ __device__ __forceinline__ void tile_rows(const AttnArgs &a, const KvUnit &u, in
   load_k(page0);
   load_v(page0);
 #pragma unroll
-  for (int i = 0; i < 2 * C; ++i) put_k(0, i);
+  for (int i = 0; i < 2 * SL; ++i) put_k(0, i);
   load_k(page1);
   lds_barrier();
   put_all(-1);
@@ -659,17 +681,24 @@ __device__ __forceinline__ void tile_rows(const AttnArgs &a, const KvUnit &u, in
 // Units of few rows among them (decoding sequences in a step with a prefill, a
 // sequence's last rows) stream instead: a block that 128 rows meet in 2.2 us is read by one of
 // their 4 waves in little more than 1.
+//
+// Heads past 128 leave room for one workgroup's LDS a CU: it has 8 waves of 16 rows, so that
+// every SIMD still has two.
 template <int C>
-__global__ __launch_bounds__(256, C > 2 ? 1 : 2) void k_kv_attn_tile(AttnArgs a) {
+constexpr int kTileWaves = C > 2 ? 8 : 4;
+
+template <int C>
+__global__ __launch_bounds__(64 * kTileWaves<C>, 2) void k_kv_attn_tile(AttnArgs a) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  static_assert(sizeof(StreamLds<1, C>) <= TileLds<C>::BYTES, "either's LDS");
+  using Stream = StreamLds<1, C, kTileWaves<C>>;
+  static_assert(sizeof(Stream) <= TileLds<C>::BYTES, "either's LDS");
   const int i = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
   if (i >= a.plan[kKvUnits]) return;
   const KvUnit u = reinterpret_cast<const KvUnit *>(a.plan + a.at_units)[i];
   if (u.len * a.G - u.row0 <= kKvFewRows)
-    stream_rows<1, C>(a, u, h, u.row0, *reinterpret_cast<StreamLds<1, C> *>(smem));
+    stream_rows<1, C, kTileWaves<C>>(a, u, h, u.row0, *reinterpret_cast<Stream *>(smem));
   else
-    tile_rows<kKvTileRows / 64, C>(a, u, h, smem);
+    tile_rows<kKvTileRows / (16 * kTileWaves<C>), C>(a, u, h, smem);
 }
 
 // The partial results of rows whose blocks were spread over several units. 16 C threads
@@ -788,7 +817,7 @@ hipError_t launch_tile(const AttnArgs &a, unsigned grid, hipStream_t st) {
       set.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
     }
   }
-  hipLaunchKernelGGL(kern, dim3(grid), dim3(256), bytes, st, a);
+  hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * kTileWaves<C>), bytes, st, a);
   return hipGetLastError();
 }
 
