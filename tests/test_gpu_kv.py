@@ -171,11 +171,23 @@ def test_write_and_attention(seqs, Hq, Hkv, D, window):
 
 
 @pytest.mark.parametrize("D", [64, 128, 192, 256])
-@pytest.mark.parametrize("new", [6, 12, 25, 70])  # units of 16, 32, 64 and 128 rows
+@pytest.mark.parametrize("new", [6, 12, 25, 70])  # 12, 24, 50 and 140 rows
 @pytest.mark.parametrize("window", [0, 1200])
 def test_divided_units(D, new, window):
     """Long sequences whose blocks are divided over units, of every number of rows and head size."""
     s = Step([(1900, new), (900, max(1, new // 3)), (0, 2)], 4, 2, D, seed=D + new, window=window, pad=1)
+    s.write_past()
+    plan = s.write()
+    y, lse = s.attend(plan)
+    s.check_attention(y, lse)
+
+
+@pytest.mark.parametrize("D", [64, 128, 184, 256])
+@pytest.mark.parametrize("Hq,Hkv,window", [(4, 2, 0), (16, 1, 0), (3, 3, 500)])
+def test_few_rows_among_many(D, Hq, Hkv, window):
+    """Decoding sequences, divided and whole, beside a prefill and a short chunk."""
+    s = Step([(3000, 1), (0, 200), (700, 1), (130, 1), (63, 3), (0, 1), (1000, 17)], Hq, Hkv, D, seed=D + Hq,
+             window=window, pad=2)
     s.write_past()
     plan = s.write()
     y, lse = s.attend(plan)
