@@ -793,7 +793,9 @@ __global__ __launch_bounds__(256) void k_w8a16_splitk_reduce(const float *__rest
   for (int e = 0; e < 4; ++e) {
     const int64_t nn = n + (e < cnt ? e : 0);
     const float b = bias ? bf16_to_f32(bias[nn]) : 0.0f;
-    out[e] = f32_to_bf16_rne(lt.add(m, nn, scale[nn] * acc[e] + b));
+    const float v = scale[nn] * acc[e] + b;
+    // (ActTerm's add() stores pre: only for outputs that are there)
+    out[e] = f32_to_bf16_rne(!LT::act || e < cnt ? lt.add(m, nn, v) : v);
   }
   uint16_t *dst = y + m * N + n;
   if (vec) {
