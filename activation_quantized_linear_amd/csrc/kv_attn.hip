@@ -538,10 +538,11 @@ __device__ __forceinline__ void tile_rows(const AttnArgs &a, const KvUnit &u, in
     if (__any(grow)) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        M[nb] = fmaxf(M[nb], top[nb]);
-        const float to = M[nb] == -__builtin_inff() ? 0.0f : M[nb];
-        const float alpha = exp2_hw(off[nb] - to);
-        off[nb] = to;
+        // (from M, not off: 0 where nothing was seen yet, however far below 0 the new maximum lies)
+        const float before = M[nb];
+        M[nb] = fmaxf(before, top[nb]);
+        off[nb] = M[nb] == -__builtin_inff() ? 0.0f : M[nb];
+        const float alpha = exp2_hw(before - off[nb]);
         l[nb] *= alpha;
 #pragma unroll
         for (int d = 0; d < ND; ++d) acc[nb][d] *= alpha;
