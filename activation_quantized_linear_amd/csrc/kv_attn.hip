@@ -5,11 +5,13 @@
 //
 // The scales never touch the codes. Scores are computed in powers of two and with log2 vs in them,
 //   z_t = a log2(e) ks (q . code_k) + log2 vs,   w_t = 2^(z_t - M),
-// M the running maximum of z, so that outputs are sums of w_t code_v and w_t is at most 1
-// where it weighs most, whatever the pages' scales; the denominator adds a page's
-// w_t times 1 / vs. Codes widen to float16 exactly, and so does q under an exponent of its row
-// (values below 2^-14 of the row's largest by 2^-25 of that). w is rounded to float16 (by 2^-11
-// of its value, or below 2^-14 by 2^-25 of the largest: a bf16 output itself is rounded by 2^-8). Sums, M and the denominator are float32.
+// M a little below the running maximum of z (kTop), so that outputs are sums of w_t code_v and w_t is
+// at most 2^15 where it weighs most, whatever the pages' scales; the denominator adds a
+// page's w_t times 1 / vs. Codes widen to float16 exactly, and so does q under an exponent of its row
+// (values below 2^-14 of the row's largest by 2^-25 of that). w is rounded to float16: by 2^-11
+// of its value, or where it is subnormal there by 2^-25, 2^-40 of the largest weight in streams and 2^-32 in
+// tiles, so that what 2^20 small weights lose together stays far below a bf16 output's
+// 2^-8. Sums, M and the denominator are float32.
 //
 // Scores are computed transposed (tokens as rows), so that a lane ends with 16
 // consecutive tokens of one query, which is the operand layout of the second product:
@@ -109,6 +111,11 @@ struct AttnArgs {
 };
 
 constexpr float kLn2 = 0.693147181f;
+
+// Weights use float16's range: their reference M is the largest score less 15 in the streaming kernel,
+// so that the largest weight is 2^15. The tile kernel moves M only when a score passes it by 15, and
+// then to 7 below that score.
+constexpr float kTop = 15.0f, kTopMoved = 7.0f;
 
 // Outputs of row `row` of a unit's sequence: 4 dims from d on.
 __device__ __forceinline__ void store_out(const AttnArgs &a, int tok, int h, int row, int d,
@@ -253,7 +260,7 @@ __device__ __forceinline__ void stream_rows(const AttnArgs &a, const KvUnit &u, 
           mx = fmaxf(mx, z);
         }
       mx = across(mx, [](float x, float y) { return fmaxf(x, y); });
-      const float Mn = fmaxf(M[nb], mx);
+      const float Mn = fmaxf(M[nb], mx - kTop);
       const float off = Mn == -__builtin_inff() ? 0.0f : Mn;
       const float alpha = exp2_hw(M[nb] - off);
       M[nb] = Mn;
@@ -482,8 +489,8 @@ __device__ __forceinline__ void tile_rows(const AttnArgs &a, const KvUnit &u, in
     vs1 = vs2;
   };
   // Scores of block k in s become weights and meet V; with `more`, those of block k + 1
-  // take their place. The reference M of a row moves only when a score passes it by 2^8:
-  // weights up to 2^8 lose nothing in float16, and moving it costs every sum a product.
+  // take their place. The reference M of a row moves only when a score passes it by kTop:
+  // weights up to 2^15 lose nothing in float16, and moving it costs every sum a product.
   //
   // Written in the order of issue. Every fragment is read four ahead of its products; the weights'
   // arithmetic goes between the products of the next scores, the widening of the codes
@@ -533,14 +540,14 @@ __device__ __forceinline__ void tile_rows(const AttnArgs &a, const KvUnit &u, in
 #pragma unroll
         for (int v = 0; v < 4; ++v) mx = fmaxf(mx, s[nb][t][v]);
       top[nb] = across(fmaf(mx, c1[nb], c2), [](float x, float y) { return fmaxf(x, y); });
-      grow = grow || top[nb] > M[nb] + 8.0f;
+      grow = grow || top[nb] > M[nb] + kTop;
     }
     if (__any(grow)) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         // (from M, not off: 0 where nothing was seen yet, however far below 0 the new maximum lies)
         const float before = M[nb];
-        M[nb] = fmaxf(before, top[nb]);
+        M[nb] = fmaxf(before, top[nb] - kTopMoved);
         off[nb] = M[nb] == -__builtin_inff() ? 0.0f : M[nb];
         const float alpha = exp2_hw(before - off[nb]);
         l[nb] *= alpha;

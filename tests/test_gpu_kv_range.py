@@ -133,3 +133,36 @@ def test_common_offset(D, new, past, offset):
 def test_common_offset_in_a_window(D, new):
     c, q, sm = offset_case([(1000, new), (0, new)], D, -150, window=100, seed=D)
     c.check(q, sm)
+
+
+@pytest.mark.parametrize("new", [1, 6, 70])  # streams of 16 and 32 rows, tiles
+@pytest.mark.parametrize("past", [300, 2100])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_most_of_the_weight_without_values(new, past, D):
+    """In every page one token has nearly all of the weight and a V of zero; the others, 14.5 2^-24
+    of its weight each, are all that the outputs are made of."""
+    g = torch.Generator(device=DEV).manual_seed(D + new)
+    c = Filled([(past, new), (past // 2, 1)], 4, 1, D)
+    k = torch.zeros(c.P, 1, BLOCK, D, dtype=torch.int8, device=DEV)
+    v = torch.randint(30, 128, (c.P, 1, BLOCK, D), generator=g, device=DEV, dtype=torch.int8)
+    k[:, :, 0, 0] = 127
+    v[:, :, 0] = 0
+    c.fill(k, torch.full((c.P, 1), 1 / 127, device=DEV), v, torch.full((c.P, 1), 0.03, device=DEV))
+    q = torch.randn(c.T, 4, D, generator=g, device=DEV)
+    q[..., 0] = 1.0
+    c.check(q.to(torch.bfloat16), -math.log(14.5 * 2.0 ** -24))
+
+
+@pytest.mark.parametrize("new,Hkv", [(1, 1), (6, 1), (70, 1), (1, 256), (40, 256)])
+def test_one_token_with_most_of_the_weight(new, Hkv, D=64):
+    """The first of 131072 tokens has 90% of every row's weight and a V of zero; divided and whole."""
+    g = torch.Generator(device=DEV).manual_seed(D + new)
+    c = Filled([(131072 - new, new)], 4 * Hkv, Hkv, D)
+    k = torch.zeros(c.P, Hkv, BLOCK, D, dtype=torch.int8, device=DEV)
+    v = torch.randint(30, 128, (c.P, Hkv, BLOCK, D), generator=g, device=DEV, dtype=torch.int8)
+    k[c.pages[0][0], :, 0, 0] = 127
+    v[c.pages[0][0], :, 0] = 0
+    c.fill(k, torch.full((c.P, Hkv), 1 / 127, device=DEV), v, torch.full((c.P, Hkv), 0.03, device=DEV))
+    q = torch.randn(c.T, 4 * Hkv, D, generator=g, device=DEV)
+    q[..., 0] = 1.0
+    c.check(q.to(torch.bfloat16), -math.log(14.5 * 2.0 ** -24))
