@@ -8,7 +8,8 @@
 // M a little below the running maximum of z (kTop), so that outputs are sums of w_t code_v and w_t is
 // at most 2^15 where it weighs most, whatever the pages' scales; the denominator adds a
 // page's w_t times 1 / vs. Codes widen to float16 exactly, and so does q under an exponent of its row
-// (values below 2^-14 of the row's largest by 2^-25 of that). w is rounded to float16: by 2^-11
+// that brings the largest value to 2^15 .. 2^16 (values down to 2^-32 of the largest keep all of their
+// bits, smaller ones are rounded by 2^-40 of it). w is rounded to float16: by 2^-11
 // of its value, or where it is subnormal there by 2^-25, 2^-40 of the largest weight in streams and 2^-32 in
 // tiles, so that what 2^20 small weights lose together stays far below a bf16 output's
 // 2^-8. Sums, M and the denominator are float32.
@@ -44,12 +45,13 @@ __device__ __forceinline__ f16x8 widen_f16(uint32_t w0, uint32_t w1) {
                                          f16x2_from_u8(x1, 0x04010400u), f16x2_from_u8(x1, 0x04030402u)});
 }
 
-// The power of two below a row's largest magnitude, and its inverse: a row of q times
-// that is below 2.
+// The power of two that brings a row's largest magnitude to 2^15 .. 2^16, as inv, and its inverse.
+// The largest bfloat16 there, 65280, is below float16's 65504. Rows whose largest is below
+// 2^-111 take 2^126, the largest power that has an inverse.
 __device__ __forceinline__ float row_exponent(float largest, float &inv) {
-  const uint32_t e = min(max(__float_as_uint(largest) & 0x7f800000u, 1u << 23), 253u << 23);
-  inv = __uint_as_float((254u << 23) - e);
-  return __uint_as_float(e);
+  const uint32_t e = min(max(__float_as_uint(largest) & 0x7f800000u, 16u << 23), 254u << 23);
+  inv = __uint_as_float((269u << 23) - e);
+  return __uint_as_float(e - (15u << 23));
 }
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }

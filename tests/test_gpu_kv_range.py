@@ -166,3 +166,22 @@ def test_one_token_with_most_of_the_weight(new, Hkv, D=64):
     q = torch.randn(c.T, 4 * Hkv, D, generator=g, device=DEV)
     q[..., 0] = 1.0
     c.check(q.to(torch.bfloat16), -math.log(14.5 * 2.0 ** -24))
+
+
+@pytest.mark.parametrize("new", [1, 6, 70])
+@pytest.mark.parametrize("D", [64, 128, 200])
+def test_small_elements_of_a_query(new, D):
+    """A query whose largest element meets a channel without K, and whose other elements, down to 2^-32
+    of it, meet channels that run as hot: each counts with all of its bits."""
+    g = torch.Generator(device=DEV).manual_seed(D + new)
+    c = Filled([(700, new), (40, 1)], 4, 2, D)
+    k = torch.randint(-127, 128, (c.P, 2, BLOCK, D), generator=g, device=DEV, dtype=torch.int8)
+    v = torch.randint(-127, 128, (c.P, 2, BLOCK, D), generator=g, device=DEV, dtype=torch.int8)
+    k[..., 0] = 0
+    down = torch.tensor([22.0, 24.0, 28.0, 30.0], device=DEV)  # of each head
+    ks = torch.tensor([2.0 ** 16, 2.0 ** 22], device=DEV).expand(c.P, 2).contiguous()
+    c.fill(k, ks, v, torch.rand(c.P, 2, generator=g, device=DEV) + 0.5)
+    q = torch.rand(c.T, 4, D, generator=g, device=DEV) * 2 + 0.25
+    q = torch.where(torch.rand(c.T, 4, D, generator=g, device=DEV) < 0.5, q, -q) * (2.0 ** -down)[None, :, None]
+    q[..., 0] = 1.0
+    c.check(q.to(torch.bfloat16), 0.25)
