@@ -229,7 +229,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_kv_plan(const int32_t *__restr
                                    w.part + (int)u};
   }
   if (tid == 0) {
-    plan[kKvInfo] = s_bad != 0x7fffffff ? s_bad + 1 : fits ? 0 : S + 1;
+    // (overlapping sequences come with one whose rows are not ascending: nothing being done goes first)
+    plan[kKvInfo] = !fits ? S + 1 : s_bad != 0x7fffffff ? s_bad + 1 : 0;
     plan[kKvPieces] = (int)npieces;
     plan[kKvJoins] = s_joins;
   }

@@ -558,8 +558,10 @@ int aql_act_restore(const int8_t *xq, const float *xs, int64_t M, int64_t K, voi
  *   plan    device, aql_kv_plan_bytes(...) bytes (output). Its first int32 is 0, or 1 +
  *           the first sequence that cannot be served (its rows of cu are not
  *           ascending inside 0 .. T, it has more than `most` tokens, pos < 0, or positions past the
- *           table): such a sequence is left out, its rows stay as they are; 1 + S
- *           where sequences overlap to more rows than T: nothing is done.
+ *           table): such a sequence is left out, its rows stay as they are, but for those
+ *           that another sequence takes too (the outputs of a row of two sequences are undefined);
+ *           1 + S where sequences overlap to more pages or rows than the plan holds for T:
+ *           nothing is done.
  * T, S, Hq, Hkv, W, most and window must be those of the plan in every call that takes it.
  * Errors: T outside 0..2^20, S outside 0..4096, W outside 1..2^20, Hkv < 1, Hq not a
  * multiple of Hkv in 1..1024, most outside 1..2^20, window outside 0..2^30 (AQL_ERR_SHAPE);

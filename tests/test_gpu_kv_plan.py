@@ -1,0 +1,35 @@
+"""The plan of a step on the 8-bit cache: sequences that overlap, and plans of two streams at once."""
+import pytest
+import torch
+
+import activation_quantized_linear_amd as aql
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("cu,T,most", [([0, 600, 0, 600, 0, 600, 0, 600], 600, 600), ([0, 300, 0, 300, 0, 300, 0, 300], 300, 300)])
+def test_sequences_that_overlap_to_more_rows(cu, T, most):
+    """1 + S, whatever else is wrong with a sequence; nothing is written or attended."""
+    S, Hq, Hkv, D, W, P = len(cu) - 1, 4, 2, 64, 16, 200
+    plan = aql.aql_kv_plan(i32(cu), i32([0] * S), T, most, Hq, Hkv, W)
+    assert plan.info.item() == 1 + S
+    cache = aql.aql_kv_cache(P, Hkv, D, DEV)
+    for t in (cache.kq, cache.vq, cache.ks, cache.vs):
+        t.fill_(77)
+    table = torch.arange(S * W, dtype=torch.int32, device=DEV).view(S, W)
+    k = torch.ones(T, Hkv, D, dtype=torch.bfloat16, device=DEV)
+    aql.aql_kv_cache_write(k, k, cache, table, plan)
+    y = torch.full((T, Hq, D), 77.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((T, Hq), 77.0, device=DEV)
+    aql.aql_attention_kv8(torch.ones_like(y), cache, table, plan, y=y, lse=lse)
+    a, b = aql.aql_kv_cache_read(cache, table, plan, k=torch.full_like(k, 77.0), v=torch.full_like(k, 77.0))
+    for t in (cache.kq, cache.vq, cache.ks, cache.vs, y, lse, a, b):
+        assert (t == 77).all()
+    # the same buffer serves the next step
+    aql.aql_kv_plan(i32([0] + [T] * S), i32([0] * S), T, most, Hq, Hkv, W, plan=plan)
+    assert plan.info.item() == 0
