@@ -697,6 +697,7 @@ __device__ __forceinline__ void tile_rows(const AttnArgs &a, const KvUnit &u, in
 // 16 requests and a chunk of 100 tokens behind 8000: 117, 104).
 template <int C>
 constexpr int kTileWaves = C > 2 ? 8 : 4;
+static_assert(kTileWaves<3> == kTileWaves<4> && kTileWaves<1> == 4 && kTileWaves<2> == 4, "the launcher's check");
 
 template <int C>
 __global__ __launch_bounds__(64 * kTileWaves<C>, 2) void k_kv_attn_tile(AttnArgs a) {
@@ -863,10 +864,14 @@ hipError_t launch_kv_attention(const uint16_t *q, int64_t qrow, float sm_scale, 
   // sums first: rows of 4 DP bytes keep every access aligned
   a.po = static_cast<float *>(ws);
   a.pm = a.po + lay.parts * z.Hkv * tile * c.DP;
-  if (!grid_fits(lay.units * z.Hkv, 256)) return hipErrorInvalidConfiguration;
-  const unsigned grid = (unsigned)(lay.units * z.Hkv);
+  const bool tiles = tile == kKvTileRows && (c.DP <= 128 || z.most * a.G > 64);
+  const int64_t groups = lay.units * z.Hkv;
+  // (the rounded grid of two streams a unit below is the largest of 256 threads)
+  if (!grid_fits((groups + 7) / 8 * 8, tiles && c.DP > 128 ? 64 * kTileWaves<4> : 256))
+    return hipErrorInvalidConfiguration;
+  const unsigned grid = (unsigned)groups;
   hipError_t e = hipSuccess;
-  if (tile == kKvTileRows && (c.DP <= 128 || z.most * a.G > 64)) {
+  if (tiles) {
     switch (c.DP / 64) {
       case 1: e = launch_tile<1>(a, grid, st); break;
       case 2: e = launch_tile<2>(a, grid, st); break;

@@ -623,7 +623,8 @@ int aql_kv_cache_read(const int8_t *kq, const int8_t *vq, const float *ks, const
  *   ws   device workspace of aql_attention_kv8_bytes(...) bytes (may be NULL where that is 0)
  * Errors: as aql_kv_cache_write; qrow likewise; sm_scale not finite and positive
  * (AQL_ERR_PARAM); workspace too small; units of work past one grid (AQL_ERR_HIP; at most
- * T Hq / 16 + S Hkv + 2048 of them, fewer than 2^24 fit).
+ * T Hq / 16 + S Hkv + 2048 of them; at most 2^24 - 8 fit, 2^23 - 8 for heads past 128 where
+ * most Hq / Hkv > 64).
  */
 size_t aql_attention_kv8_bytes(int64_t T, int64_t S, int64_t Hq, int64_t Hkv, int64_t D, int64_t W,
                                int64_t most);

@@ -33,3 +33,20 @@ def test_sequences_that_overlap_to_more_rows(cu, T, most):
     # the same buffer serves the next step
     aql.aql_kv_plan(i32([0] + [T] * S), i32([0] * S), T, most, Hq, Hkv, W, plan=plan)
     assert plan.info.item() == 0
+
+
+@pytest.mark.parametrize("T,D,fits", [(1 << 20, 256, False), (1 << 20, 136, False), (1 << 19, 256, True), (1 << 20, 128, True)])
+def test_units_past_one_grid(T, D, fits):
+    """Heads past 128 run in workgroups of 512 threads, of which a grid holds half as many. The plan
+    has room for as many units as a step of these sizes could have and holds none."""
+    Hq, Hkv, W = 1024, 1, 8
+    print("attention", T, D, flush=True)
+    room = torch.zeros(aql.aql_kv_plan_bytes(T, 1, Hq, Hkv, W, T), dtype=torch.uint8, device=DEV)
+    assert aql.aql_attention_kv8_bytes(T, 1, Hq, Hkv, D, W, T) == 0
+    any16 = torch.zeros(1 << 16, dtype=torch.uint8, device=DEV)
+    p = any16.data_ptr()
+    rc = aql._lib.aql_attention_kv8(p, Hq * D, T, 1, Hq, Hkv, D, 0.1, 0, p, p, p, p, 1, p, W, T, room.data_ptr(), p, None,
+                                    None, 0, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == (aql.AQL_OK if fits else aql.AQL_ERR_HIP), aql.aql_last_error()
+    assert not any16.any()
