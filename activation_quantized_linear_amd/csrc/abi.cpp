@@ -195,6 +195,17 @@ static_assert(AQL_ACT_NONE == aql::kActNone && AQL_ACT_RELU == aql::kActRelu &&
                   AQL_ACT_SILU == aql::kActSilu,
               "activations");
 
+// Whether two [M, N] bf16 matrices (16-byte aligned; M, N > 0) share memory, and whether they do
+// without being the same one.
+bool share(const uint16_t *a, const uint16_t *b, int64_t M, int64_t N) {
+  if (!a || !b) return false;
+  const uintptr_t p = (uintptr_t)a, q = (uintptr_t)b;
+  return (p > q ? p - q : q - p) / 2 / (uint64_t)N < (uint64_t)M;
+}
+bool cross(const uint16_t *a, const uint16_t *b, int64_t M, int64_t N) {
+  return a != b && share(a, b, M, N);
+}
+
 static_assert(AQL_KV_BLOCK == aql::kKvBlock && AQL_KV_MAX_HEAD == aql::kKvMaxHead, "cache bounds");
 
 bool kv_sizes_ok(const aql::KvSizes &z) {
@@ -540,7 +551,10 @@ int aql_linear_w8a16_act(const uint16_t *x, int64_t M, int64_t K, const int8_t *
   REQUIRE(aligned16(mul) && aligned16(residual) && aligned16(pre) && aligned16(ws), AQL_ERR_ALIGN,
           "%s: pointers must be 16-byte aligned", fn);
   if (M == 0 || N == 0) return ok();
-  REQUIRE(y != pre, AQL_ERR_PARAM, "%s: y and pre must not share memory", fn);
+  REQUIRE(!share(pre, y, M, N) && !share(pre, mul, M, N) && !share(pre, residual, M, N),
+          AQL_ERR_PARAM, "%s: pre must not share memory with y, mul or residual", fn);
+  REQUIRE(!cross(y, mul, M, N) && !cross(y, residual, M, N), AQL_ERR_PARAM,
+          "%s: y may be mul or residual itself, but not share a part of their memory", fn);
   if (int e = check_device(fn)) return e;
   const aql::ActTerm at{act, mul, residual, pre, N};
   float *part = static_cast<float *>(ws);

@@ -326,8 +326,8 @@ int aql_linear_dq8ca(const float *x, int64_t M, int64_t K, int wfmt, const void 
  *   pre       device, [M, N] bf16: v, which the gradients take (output; may be NULL)
  *   y         device, [M, N] bf16 (output). It may be mul's or residual's own
  *             memory; outputs overlap nothing else.
- * Errors: as aql_linear_w8a16, plus an unknown act, misaligned mul, residual or pre,
- * y == pre.
+ * Errors: as aql_linear_w8a16, plus an unknown act, misaligned mul, residual or pre, pre
+ * in memory of y, mul or residual, y in a part of mul's or residual's (AQL_ERR_PARAM).
  */
 int aql_linear_w8a16_act(const uint16_t *x, int64_t M, int64_t K, const int8_t *q,
                          const float *scale, const uint16_t *bias, int64_t N, int act,
