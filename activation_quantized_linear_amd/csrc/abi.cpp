@@ -578,8 +578,11 @@ int aql_act_mul_backward(const uint16_t *dy, const uint16_t *pre, int act, const
           AQL_ERR_ALIGN, "%s: pointers must be 16-byte aligned", fn);
   if (M == 0 || N == 0) return ok();
   REQUIRE(dy && pre && dv, AQL_ERR_NULL, "%s: dy, pre and dv must not be NULL", fn);
-  REQUIRE(!dmul || (mul && dmul != dv), AQL_ERR_PARAM,
+  REQUIRE(!dmul || (mul && !share(dmul, dv, M, N)), AQL_ERR_PARAM,
           "%s: dmul needs mul, and memory other than dv's", fn);
+  for (const uint16_t *in : {dy, pre, mul})
+    REQUIRE(!cross(dv, in, M, N) && !cross(dmul, in, M, N), AQL_ERR_PARAM,
+            "%s: an output may be an input itself, but not share a part of its memory", fn);
   if (int e = check_device(fn)) return e;
   return launched(
       aql::launch_act_mul_backward(dy, pre, act, mul, M * N, dv, dmul, (hipStream_t)stream), fn);

@@ -346,8 +346,8 @@ int aql_linear_w8a16_act(const uint16_t *x, int64_t M, int64_t K, const int8_t *
  *   dv        device, [M, N] bf16 (output)
  *   dmul      device, [M, N] bf16 (output; may be NULL). Only with mul.
  * An output may be an input's own memory. Errors: unknown act; M, N < 0 or
- * M N > 2^40; dmul without mul (AQL_ERR_PARAM); dv == dmul (AQL_ERR_PARAM); NULL dy, pre
- * or dv (M, N > 0); misaligned pointers.
+ * M N > 2^40; dmul without mul, dmul in dv's memory, either in a part of an input's
+ * (AQL_ERR_PARAM); NULL dy, pre or dv (M, N > 0); misaligned pointers.
  */
 int aql_act_mul_backward(const uint16_t *dy, const uint16_t *pre, int act, const uint16_t *mul,
                          int64_t M, int64_t N, uint16_t *dv, uint16_t *dmul, void *stream);

@@ -33,3 +33,24 @@ def test_separate_memory_is_not(kw):
     if torch.cuda.is_available():
         pytest.skip("the addresses are no device's")
     assert call(**kw) not in (aql.AQL_ERR_PARAM, aql.AQL_OK)
+
+
+def gradients(dy=A, pre=B, mul=Y, dv=PRE, dmul=0x5000000):
+    ptr = [C.c_void_p(v) if v else None for v in (dy, pre, mul, dv, dmul)]
+    return aql._lib.aql_act_mul_backward(ptr[0], ptr[1], aql.AQL_ACT_SILU, ptr[2], M, N, ptr[3], ptr[4], None)
+
+
+@pytest.mark.parametrize("kw", [dict(dv=A + 16), dict(dv=B - 16), dict(dv=Y + SIZE - 16), dict(dmul=A - 16),
+                                dict(dmul=B + 16), dict(dmul=Y - SIZE + 16), dict(dmul=PRE), dict(dmul=PRE + 16)])
+def test_gradients_across_memory_are_refused(kw):
+    assert gradients(**kw) == aql.AQL_ERR_PARAM
+    assert "memory" in aql.aql_last_error()
+
+
+@pytest.mark.parametrize("kw", [{}, dict(dv=A), dict(dv=B, dmul=Y), dict(dv=Y, dmul=A), dict(dmul=B), dict(dv=A + SIZE),
+                                dict(mul=None, dmul=None, dv=A), dict(dmul=PRE - SIZE)])
+def test_gradients_in_memory_of_their_own_or_an_input(kw):
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are no device's")
+    assert gradients(**kw) not in (aql.AQL_ERR_PARAM, aql.AQL_OK)
