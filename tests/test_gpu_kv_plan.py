@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import activation_quantized_linear_amd as aql
+from test_gpu_kv import Step
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -50,3 +51,31 @@ def test_units_past_one_grid(T, D, fits):
     torch.cuda.synchronize()
     assert rc == (aql.AQL_OK if fits else aql.AQL_ERR_HIP), aql.aql_last_error()
     assert not any16.any()
+
+
+def test_two_streams_with_work_in_flight():
+    """Writes and attention of two batches queued on two streams, everything made before: divided
+    units, so that both keep partial results, of decoding sequences and of a chunk."""
+    batches = [Step([(3000, 1), (2500, 1), (700, 1)], 8, 2, 64, seed=41), Step([(2600, 40), (900, 1)], 4, 2, 128, seed=43)]
+    work = []
+    for s in batches:
+        s.write_past()
+        plan = s.write()
+        assert aql.aql_attention_kv8_bytes(s.T, len(s.seqs), s.Hq, s.Hkv, s.D, s.W, max(s.news)) > 0
+        want = s.attend(plan)
+        s.check_attention(*want)
+        work.append((s, plan, want, s.q.to(DEV), s.k.to(DEV), s.v.to(DEV)))
+    turns = 60
+    outs = [[(torch.full_like(w[2][0], 77.0), torch.full_like(w[2][1], 77.0)) for _ in range(turns)] for w in work]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for t in range(turns):
+        for (s, plan, _, q, k, v), out, st in zip(work, outs, streams):
+            with torch.cuda.stream(st):
+                aql.aql_kv_cache_write(k, v, s.cache, s.dev_table, plan)  # (the same tokens: the same codes)
+                aql.aql_attention_kv8(q, s.cache, s.dev_table, plan, y=out[t][0], lse=out[t][1])
+    torch.cuda.synchronize()
+    for (s, _, want, *_), out in zip(work, outs):
+        s.check_cache()
+        for y, lse in out:
+            assert torch.equal(y, want[0]) and torch.equal(lse, want[1])
