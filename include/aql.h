@@ -611,10 +611,11 @@ int aql_kv_cache_read(const int8_t *kq, const int8_t *vq, const float *ks, const
  * The token at position p of a sequence sees positions max(0, p - window + 1) .. p; head i
  * of Hq reads kv head i / (Hq / Hkv):
  *   y = sum_t softmax_t(sm_scale q . k_t) v_t,   lse = log sum_t e^(sm_scale q . k_t)
- * Codes enter exactly, and so does q but for elements below 2^-32 of the largest of their token and
- * head (rounded by 2^-40 of that); a weight is rounded to float16 before it meets V, by 2^-11 of it or
- * 2^-32 of the largest weight times V's scale; sums, maxima and denominators are float32 and y is
- * rounded once. Tokens of page numbers outside 0 .. P - 1 are not seen; a row that
+ * Codes enter exactly, and so does q but for elements below 2^-32 of the largest of their token
+ * and head (rounded by 2^-40 of that); a weight is rounded to float16 before it meets V, by
+ * 2^-11 of it or 2^-32 of the largest weight times V's scale; sums, maxima and denominators
+ * are float32 and y is rounded once. Scales of V that a row sees may lie up to 2^110 apart (the
+ * least is 2^-64). Tokens of page numbers outside 0 .. P - 1 are not seen; a row that
  * sees nothing gets y = 0 and lse = -inf. What a page without finite values does to
  * rows that see none of its tokens: nothing.
  *

@@ -185,3 +185,20 @@ def test_small_elements_of_a_query(new, D):
     q = torch.where(torch.rand(c.T, 4, D, generator=g, device=DEV) < 0.5, q, -q) * (2.0 ** -down)[None, :, None]
     q[..., 0] = 1.0
     c.check(q.to(torch.bfloat16), 0.25)
+
+
+@pytest.mark.parametrize("new", [1, 6, 70])
+@pytest.mark.parametrize("D", [64, 192])
+@pytest.mark.parametrize("up", [0, 46])
+def test_scales_of_v_far_apart(new, D, up):
+    """Every other page has V of zero under the smallest scale, 2^-64, the rest V of 2^up: the tokens
+    of both count alike in the denominator."""
+    g = torch.Generator(device=DEV).manual_seed(D + new)
+    c = Filled([(700, new), (100, 1)], 4, 2, D)
+    k = torch.randint(-32, 33, (c.P, 2, BLOCK, D), generator=g, device=DEV, dtype=torch.int8)
+    v = torch.randint(-127, 128, (c.P, 2, BLOCK, D), generator=g, device=DEV, dtype=torch.int8)
+    vs = torch.full((c.P, 2), 2.0 ** up, device=DEV)
+    for p in (p for s in c.pages for p in s[::2]):
+        v[p], vs[p] = 0, 2.0 ** -64
+    c.fill(k, torch.full((c.P, 2), 2.0 ** -5, device=DEV), v, vs)
+    c.check(torch.randn(c.T, 4, D, generator=g, device=DEV).to(torch.bfloat16), D ** -0.5)
