@@ -79,3 +79,64 @@ def test_two_streams_with_work_in_flight():
         s.check_cache()
         for y, lse in out:
             assert torch.equal(y, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("D", [64, 200, 256])
+def test_captured_chunks(D):
+    """Plan, write, attention and read of a chunk beside decoding sequences in one graph: its positions move on
+    the device, replays alternate with eager work, and each equals the eager step and the plain form."""
+    Hq, Hkv, new, turns = 4, 2, 48, 3
+    s = Step([(900, new), (700, 1), (60, 1)], Hq, Hkv, D, seed=D)
+    s.write_past()
+    free = [p for p in range(s.P) if all(p not in r for r in s.table)]
+    need = [(p + turns * n + 63) // 64 for p, n in zip(s.pasts, s.news)]
+    W = max(need) + 2
+    P = s.P + sum(need)
+    wide = aql.aql_kv_cache(P, Hkv, D, DEV)  # room for the pages to come
+    for a, b in ((wide.kq, s.cache.kq), (wide.vq, s.cache.vq), (wide.ks, s.cache.ks), (wide.vs, s.cache.vs)):
+        a[:s.P] = b
+    s.cache, fresh = wide, iter(free + list(range(s.P, P)))
+    have = [(p + n + 63) // 64 for p, n in zip(s.pasts, s.news)]
+    s.table = [[r[b] if b < h else next(fresh) if b < m else -1 for b in range(W)] for r, h, m in zip(s.table, have, need)]
+    s.dev_table, s.W = i32(s.table), W
+    ref = s.ref
+    s.ref = type(ref)(P, Hkv, D)
+    for name in "kv":
+        s.ref.codes[name][:s.P], s.ref.scale[name][:s.P] = ref.codes[name], ref.scale[name]
+    s.P = P
+    cu, pos, grow = i32(s.cu), i32(s.pasts), i32(s.news)
+    q, k, v = [torch.zeros(s.T, h, D, dtype=torch.bfloat16, device=DEV) for h in (Hq, Hkv, Hkv)]
+    plan = aql.aql_kv_plan(cu, pos, s.T, new, Hq, Hkv, W)
+    y, kb, vb = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    lse = torch.empty(s.T, Hq, device=DEV)
+    keep = [t.clone() for t in (wide.kq, wide.vq, wide.ks, wide.vs)]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        aql.aql_kv_plan(cu, pos, s.T, new, Hq, Hkv, W, plan=plan)
+        aql.aql_kv_cache_write(k, v, wide, s.dev_table, plan)
+        aql.aql_attention_kv8(q, wide, s.dev_table, plan, y=y, lse=lse)
+        aql.aql_kv_cache_read(wide, s.dev_table, plan, k=kb, v=vb)
+        pos.add_(grow)
+    for a, b in zip((wide.kq, wide.vq, wide.ks, wide.vs), keep):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))  # (nothing ran in the capture)
+    g = torch.Generator().manual_seed(D)
+    for t in range(turns):
+        s.q, s.k, s.v = [torch.randn(s.T, h, D, generator=g).to(torch.bfloat16) for h in (Hq, Hkv, Hkv)]
+        for a, b in ((q, s.q), (k, s.k), (v, s.v)):
+            a.copy_(b)
+        graph.replay()
+        s.seqs = [(c, p, n) for c, p, n in zip(s.cu, s.pasts, s.news)]
+        s.ref_write(s.k, s.v, s.seqs)
+        torch.cuda.synchronize()
+        assert plan.info.item() == 0
+        s.check_cache()
+        s.check_attention(y, lse)
+        eager = aql.aql_attention_kv8(q, wide, s.dev_table, plan)
+        assert torch.equal(eager, y)
+        a, b = aql.aql_kv_cache_read(wide, s.dev_table, plan)
+        assert torch.equal(a, kb) and torch.equal(b, vb)
+        other = Step([(70, 40)], 2, 1, 64, seed=t)
+        other.write_past()
+        other.attend(other.write())
+        s.pasts = [p + n for p, n in zip(s.pasts, s.news)]
