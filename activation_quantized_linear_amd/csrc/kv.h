@@ -80,9 +80,9 @@ constexpr int kv_tile_rows(const KvSizes &z) {
 // Units that a step is divided into where there is enough to divide (over all kv heads),
 // and the fewest blocks of one. Streams: three workgroups a CU (64 requests of up to 8192
 // tokens, one of 131071, us: 512 units 93.9, 50.2; 768 88.2, 50.8; 1024 90.2, 52.1). Tiles:
-// under the two a CU that run at once, so that uneven ones need no second round (16 requests
+// fewer than the two a CU that run at once, as each tile's parts are rounded up (16 requests
 // and a chunk of 509 tokens behind 6007; 256 behind 16000: 384 units 91, 105; 448 91, 94; 512 107,
-// 89).
+// 89; the first comes to 528 units all the same, the longest 1.29 of their mean cost).
 constexpr int64_t kv_target(const KvSizes &z) {
   const int64_t t = (kv_tile_rows(z) == kKvTileRows ? 448 : 768) / z.Hkv;
   return t > 1 ? t : 1;
@@ -90,7 +90,9 @@ constexpr int64_t kv_target(const KvSizes &z) {
 constexpr int64_t kKvMinBlocks = 4;
 // Tables of at most so many blocks leave nothing to divide: a second launch that joins the parts
 // costs what 4 waves take for two more blocks each (one request of 334 tokens, 15 heads
-// of 64 over 5: 5.1 us in one unit, 7.0 divided; of 1024 tokens 8.1, 7.1).
+// of 64 over 5: 5.1 us in one unit, 7.0 divided; of 1024 tokens 8.1, 7.1). It is the table's
+// width that counts, which the host knows: with wider tables the same request is divided, and
+// one of 31 tokens, which is not, has the second launch all the same (5.8 us against 4.3).
 constexpr int64_t kKvWhole = 8;
 
 struct KvPlanLayout {

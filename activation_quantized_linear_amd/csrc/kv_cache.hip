@@ -241,7 +241,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_kv_plan(const int32_t *__restr
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 // rint(v / s) for |v| <= 127 s: v times the reciprocal r is within 2^-16 of the
-// quotient, so only values that near a half integer take the division.
+// quotient, so only values near a half integer take the division. (From 2^-10 on, which
+// one value in 512 is, and so some value of one wave in eight.)
 __device__ __forceinline__ int code_of(float v, float s, float r) {
   const float t = v * r;
   float c = rintf(t);
