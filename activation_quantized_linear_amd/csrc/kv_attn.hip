@@ -7,13 +7,14 @@
 //   z_t = a log2(e) ks (q . code_k) + log2 vs,   w_t = 2^(z_t - M),
 // M a little below the running maximum of z (kTop), so that outputs are sums of w_t code_v and w_t is
 // at most 2^15 where it weighs most, whatever the pages' scales; the denominator adds a
-// page's w_t times 1 / vs, in which a weight of up to 2^-20 of the largest counts while the scales of
-// V that a row sees lie within 2^110 of each other (w_t is at least 2^-126, float32's least). Codes widen to float16 exactly, and so does q under an exponent of its row
-// that brings the largest value to 2^15 .. 2^16 (values down to 2^-32 of the largest keep all of their
-// bits, smaller ones are rounded by 2^-40 of it). w is rounded to float16: by 2^-11
-// of its value, or where it is subnormal there by 2^-25, 2^-40 of the largest weight in streams and 2^-32 in
-// tiles, so that what 2^20 small weights lose together stays far below a bf16 output's
-// 2^-8. Sums, M and the denominator are float32.
+// page's w_t times 1 / vs, in which weights down to 2^-20 of the largest count while the scales of V
+// that a row sees lie within 2^110 of each other (below 2^-126 w_t is 0). Codes widen to float16
+// exactly, and so does q under an exponent of its row that brings the largest value to
+// 2^15 .. 2^16 (values down to 2^-32 of the largest keep all of their bits, smaller ones are
+// rounded by 2^-40 of it). w is rounded to float16: by 2^-11 of its value, or where it is
+// subnormal there by 2^-25, which is 2^-40 of the largest weight in streams and 2^-32 in tiles,
+// so that what 2^20 small weights lose together stays far below a bf16 output's 2^-8. Sums,
+// M and the denominator are float32.
 //
 // Scores are computed transposed (tokens as rows), so that a lane ends with 16
 // consecutive tokens of one query, which is the operand layout of the second product:
